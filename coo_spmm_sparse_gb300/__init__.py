@@ -16,6 +16,15 @@ Tensors are fp32, contiguous, on the handle's device; results are written to
 the given output tensors (or new ones) on the current torch CUDA stream unless
 `stream` is given.  A C-ABI error raises SnackError.  ``SnackLinear`` is a thin
 nn.Module / autograd wrapper for training loops.
+
+Around the layers (fp32, bfloat16 and float16; no handle):
+
+    r, h, stats = snack_residual_norm_forward(x, y, ...)   # residual_norm.py
+    grads = snack_residual_norm_backward(dr, dh, x, y, stats, ...)
+    Y, H = snack_adapter_forward(X, A, B, offsets, adapter, scale, Y)   # adapters.py
+    dX, dA, dB = snack_adapter_backward(X, dY, A, B, offsets, adapter, scale, H)
+    norm = snack_grad_norm(grads)                           # grad_clip.py
+    norm = snack_clip_grad_norm(grads, max_norm)
 """
 
 from __future__ import annotations
@@ -34,6 +43,9 @@ __all__ = [
     "snack_backward_input", "snack_backward_weight", "snack_backward", "snack_prune_regrow",
     "snack_values", "snack_values_changed", "snack_sgd_step", "snack_adam_step", "snack_optimizer_state", "snack_export", "snack_export_segments", "snack_plan", "snack_nnz",
     "snack_device_bytes", "snack_destroy", "snack_launch_count", "snack_debug_fail_alloc", "snack_forward_csr_static", "snack_device_error", "snack_selftest_wait", "SnackLinear", "library_path",
+    "snack_residual_norm_forward", "snack_residual_norm_backward", "snack_residual_norm", "SnackResidualNorm",
+    "snack_adapter_forward", "snack_adapter_backward", "SnackAdapters",
+    "SnackTensorList", "snack_tensor_list", "snack_grad_norm", "snack_clip_grad_norm",
 ]
 
 
@@ -207,6 +219,56 @@ def snack_prune_regrow(h: SnackHandle, frac: float, seed: int, stream=None):
     _check(_lib.snack_prune_regrow(h.ptr, ctypes.c_float(frac), seed & (2**64 - 1),
                                    _stream(stream), ctypes.byref(p), ctypes.byref(t)), h)
     return int(p.value), int(t.value)
+
+
+_DTYPES = {torch.float32: _abi.F32, torch.bfloat16: _abi.BF16, torch.float16: _abi.F16}
+
+
+def _dense_type(t: torch.Tensor, name: str) -> int:
+    """snack_dtype of a CUDA tensor of the current device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a CUDA float32, bfloat16 or float16 tensor")
+    return _DTYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, row stride) of t seen as [rows][last dimension]: its leading
+    dimensions must lie one regular step apart, its last one contiguous."""
+    if t.is_contiguous():
+        return (t.numel() // t.shape[-1] if t.shape[-1] else 0), t.shape[-1]
+    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    rows, step = 1, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = st
+        elif st != step * rows:
+            raise ValueError(f"{name}: the rows of its leading dimensions are not evenly spaced")
+        rows *= n
+    step = t.shape[-1] if step is None else step
+    if step < t.shape[-1]:
+        raise ValueError(f"{name}: its rows overlap")
+    return rows, step
+
+
+def _same_device(*tensors):
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    if dev is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"{dev} is not the current CUDA device")
+    return dev
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 class _CudaArray:
@@ -460,3 +522,10 @@ class SnackLinear(torch.nn.Module):
     def export(self):
         """(row, col, val) numpy arrays of the stored entries in canonical order."""
         return snack_export(self.handle)
+
+
+from .adapters import SnackAdapters, snack_adapter_backward, snack_adapter_forward  # noqa: E402
+from .grad_clip import (SnackTensorList, snack_clip_grad_norm, snack_grad_norm,  # noqa: E402
+                        snack_tensor_list)
+from .residual_norm import (SnackResidualNorm, snack_residual_norm,  # noqa: E402
+                            snack_residual_norm_backward, snack_residual_norm_forward)

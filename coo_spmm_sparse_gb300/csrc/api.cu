@@ -511,6 +511,7 @@ cudaError_t device_malloc(void **p, size_t bytes) {
 // Failures of entry points that have no handle report through
 // snack_last_error(NULL), like snack_create.
 void record_thread_error(const std::string &msg) { g_create_error = msg; }
+void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 }  // namespace snack
 
 extern "C" {

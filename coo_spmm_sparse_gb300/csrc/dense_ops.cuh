@@ -1,0 +1,117 @@
+// What the kernels on dense activations share (residual_norm.cu, adapter.cu,
+// grad_clip.cu): element types, block sums, launches, argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "../../include/snack.h"
+
+namespace snack {
+
+void record_thread_error(const std::string &msg);  // api.cu
+void count_launches(int n);                        // api.cu
+int device_sms();                                  // SM count of the current device
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
+
+// Rounds to nearest even: the one rounding of a stored result.
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+// Element i of an array whose type is only known at run time.
+__device__ __forceinline__ float load_as_float(const void *p, int type, int64_t i) {
+  if (type == SNACK_F32) return static_cast<const float *>(p)[i];
+  if (type == SNACK_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+  return __half2float(static_cast<const __half *>(p)[i]);
+}
+
+__device__ __forceinline__ void store_from_float(void *p, int type, int64_t i, float v) {
+  if (type == SNACK_F32)
+    static_cast<float *>(p)[i] = v;
+  else if (type == SNACK_BF16)
+    static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half *>(p)[i] = __float2half_rn(v);
+}
+
+// Programmatic dependent launches: a kernel launched with pdl waits for the
+// whole of its predecessor here, before it touches any memory.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependency_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sums of N values over the block, the same in every thread; `red` holds
+// N * 32 floats and may be reused after the call.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+  if (nw == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[k * 32 + w] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < nw ? red[k * 32 + lane] : 0.f);
+  __syncthreads();
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, bool pdl,
+                                 cudaStream_t s, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+inline snack_status refuse(snack_status st, const std::string &msg) {
+  record_thread_error(msg);
+  return st;
+}
+
+inline snack_status cuda_status(cudaError_t e, const char *what) {
+  return refuse(e == cudaErrorMemoryAllocation ? SNACK_ERR_ALLOC : SNACK_ERR_CUDA,
+                std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+inline int64_t type_bytes(int type) { return type == SNACK_F32 ? 4 : 2; }
+inline bool known_type(int type) { return type == SNACK_F32 || type == SNACK_BF16 || type == SNACK_F16; }
+inline bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace snack

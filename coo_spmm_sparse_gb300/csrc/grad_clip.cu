@@ -1,0 +1,365 @@
+// The global gradient norm over many tensors, and clipping.
+//
+//   norm = sqrt(sum_i sum_j g_ij^2)  or  max |g_ij|;   out = g * min(1, max_norm / (norm + eps))
+//
+// Memory bound: n elements are read once for the norm and once more, after
+// the norm is known, to be scaled and written.  The tensors' addresses travel
+// as kernel parameters (no table is copied to the device beforehand), cut
+// into chunks of equal length that the blocks of a persistent grid take in
+// turn.  Every block leaves one partial sum; whoever needs the norm adds the
+// partials in their order, so that no atomic decides a result's bits.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "dense_ops.cuh"
+
+namespace snack {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 4;
+constexpr int kMostTable = 1024;  // tensors of one launch: 30 KB of the 32 KB that parameters may take
+
+template <int K>
+struct TensorTable {
+  int count;
+  int chunk_elems;
+  int64_t chunks;
+  const void *src[K];
+  void *dst[K];
+  int64_t n[K];
+  uint32_t first[K];  // first chunk of the tensor
+  uint8_t stype[K], dtype[K];
+};
+
+// The tensor that holds chunk c.
+template <int K>
+__device__ __forceinline__ int tensor_of(const TensorTable<K> &t, uint32_t c) {
+  int lo = 0, hi = t.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= c)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// max() that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+
+template <bool MAX>
+__device__ __forceinline__ void take(float &acc, float v) {
+  if (MAX)
+    acc = max_nan(fabsf(v), acc);
+  else
+    acc = fmaf(v, v, acc);
+}
+
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float *red) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const auto join = [](float a, float b) { return MAX ? max_nan(a, b) : a + b; };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (lane == 0) red[w] = v;
+  __syncthreads();
+  v = lane < kThreads / 32 ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  return v;
+}
+
+__device__ __forceinline__ bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename T>
+struct Vec {  // 16 bytes
+  static constexpr int N = 16 / sizeof(T);
+  uint4 raw;
+  __device__ __forceinline__ void load(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = raw; }
+  __device__ __forceinline__ float get(int i) const { return to_float(reinterpret_cast<const T *>(&raw)[i]); }
+  __device__ __forceinline__ void set(int i, float v) { reinterpret_cast<T *>(&raw)[i] = from_float<T>(v); }
+};
+
+template <typename T, bool MAX>
+__device__ __forceinline__ void norm_chunk(const T *p, int n, float (&acc)[4]) {
+  constexpr int V = Vec<T>::N;
+  const int tid = threadIdx.x;
+  int done = 0;
+  if (aligned(p)) {
+    const int nv = n / V;
+    int i = tid;
+    for (; i + 3 * kThreads < nv; i += 4 * kThreads) {
+      Vec<T> v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k].load(p + (int64_t)(i + k * kThreads) * V);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) take<MAX>(acc[k], v[k].get(j));
+    }
+    for (; i < nv; i += kThreads) {
+      Vec<T> v;
+      v.load(p + (int64_t)i * V);
+#pragma unroll
+      for (int j = 0; j < V; ++j) take<MAX>(acc[j & 3], v.get(j));
+    }
+    done = nv * V;
+  }
+  for (int i = done + tid; i < n; i += kThreads) take<MAX>(acc[0], to_float(p[i]));
+}
+
+template <int K, bool MAX>
+__global__ void __launch_bounds__(kThreads) norm_partials(const __grid_constant__ TensorTable<K> t,
+                                                          float *partial) {
+  __shared__ float red[32];
+  dependency_wait();
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int k = tensor_of(t, (uint32_t)c);
+    const int64_t at = (c - t.first[k]) * (int64_t)t.chunk_elems;
+    const int64_t left = t.n[k] - at;
+    const int n = left < t.chunk_elems ? (int)left : t.chunk_elems;
+    if (t.stype[k] == SNACK_F32)
+      norm_chunk<float, MAX>(static_cast<const float *>(t.src[k]) + at, n, acc);
+    else if (t.stype[k] == SNACK_BF16)
+      norm_chunk<__nv_bfloat16, MAX>(static_cast<const __nv_bfloat16 *>(t.src[k]) + at, n, acc);
+    else
+      norm_chunk<__half, MAX>(static_cast<const __half *>(t.src[k]) + at, n, acc);
+  }
+  const float v = MAX ? max_nan(max_nan(acc[0], acc[1]), max_nan(acc[2], acc[3]))
+                      : (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  const float s = block_reduce<MAX>(v, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// The norm from all partials, the same in every thread of every block.
+template <bool MAX>
+__device__ __forceinline__ float whole_norm(const float *partial, int parts, float *red) {
+  float v = 0.f;
+  for (int i = threadIdx.x; i < parts; i += kThreads) v = MAX ? max_nan(partial[i], v) : v + partial[i];
+  v = block_reduce<MAX>(v, red);
+  return MAX ? v : sqrtf(v);
+}
+
+template <bool MAX>
+__global__ void __launch_bounds__(kThreads) norm_finish(const float *partial, int parts, float *norm) {
+  __shared__ float red[32];
+  dependency_wait();
+  const float v = whole_norm<MAX>(partial, parts, red);
+  if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename S, typename D>
+__device__ __forceinline__ void scale_chunk(const S *p, D *q, int n, float coef) {
+  constexpr int V = Vec<S>::N;
+  const int tid = threadIdx.x;
+  int done = 0;
+  if (aligned(p) && aligned(q)) {
+    const int nv = n / V;
+    for (int i = tid; i < nv; i += kThreads) {
+      Vec<S> v;
+      v.load(p + (int64_t)i * V);
+      D out[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) out[j] = from_float<D>(v.get(j) * coef);
+      D *at = q + (int64_t)i * V;
+#pragma unroll
+      for (int j = 0; j < V; j += 16 / (int)sizeof(D)) {
+        if constexpr (V * sizeof(D) >= 16)
+          *reinterpret_cast<uint4 *>(at + j) = *reinterpret_cast<const uint4 *>(out + j);
+        else
+          *reinterpret_cast<uint2 *>(at + j) = *reinterpret_cast<const uint2 *>(out + j);
+      }
+    }
+    done = nv * V;
+  }
+  for (int i = done + tid; i < n; i += kThreads) q[i] = from_float<D>(to_float(p[i]) * coef);
+}
+
+template <typename S>
+__device__ __forceinline__ void scale_chunk_to(const S *p, void *q, int dtype, int64_t at, int n, float coef) {
+  if (dtype == SNACK_F32)
+    scale_chunk(p, static_cast<float *>(q) + at, n, coef);
+  else if (dtype == SNACK_BF16)
+    scale_chunk(p, static_cast<__nv_bfloat16 *>(q) + at, n, coef);
+  else
+    scale_chunk(p, static_cast<__half *>(q) + at, n, coef);
+}
+
+template <int K, bool MAX>
+__global__ void __launch_bounds__(kThreads) scale_tensors(const __grid_constant__ TensorTable<K> t,
+                                                          const float *partial, int parts, float max_norm,
+                                                          float eps, float *norm) {
+  __shared__ float red[32];
+  dependency_wait();
+  const float total = whole_norm<MAX>(partial, parts, red);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  const float ratio = max_norm / (total + eps);
+  const float coef = ratio >= 1.f ? 1.f : ratio;  // a NaN stays
+  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int k = tensor_of(t, (uint32_t)c);
+    // in place and nothing to clip: what would be written is there already
+    if (coef == 1.f && t.dst[k] == t.src[k]) continue;
+    const int64_t at = (c - t.first[k]) * (int64_t)t.chunk_elems;
+    const int64_t left = t.n[k] - at;
+    const int n = left < t.chunk_elems ? (int)left : t.chunk_elems;
+    if (t.stype[k] == SNACK_F32)
+      scale_chunk_to(static_cast<const float *>(t.src[k]) + at, t.dst[k], t.dtype[k], at, n, coef);
+    else if (t.stype[k] == SNACK_BF16)
+      scale_chunk_to(static_cast<const __nv_bfloat16 *>(t.src[k]) + at, t.dst[k], t.dtype[k], at, n, coef);
+    else
+      scale_chunk_to(static_cast<const __half *>(t.src[k]) + at, t.dst[k], t.dtype[k], at, n, coef);
+  }
+}
+
+struct Request {
+  int64_t count;
+  const void *const *grads;
+  void *const *outs;
+  const int64_t *sizes;
+  const int32_t *types, *out_types;
+  float max_norm, eps;
+  float *norm;
+  float *partial;
+  cudaStream_t s;
+};
+
+int grid_blocks() { return device_sms() * kBlocksPerSm; }
+
+// Chunk length: about four chunks for every resident block, so that none
+// waits long for the last, between 2048 elements (a sweep of the block in
+// 16-byte vectors) and 32768 (beyond it the search for the tensor no longer
+// shows).
+int chunk_length(int64_t total) {
+  int c = 2048;
+  while (c < 32768 && total > (int64_t)c * 4 * grid_blocks()) c *= 2;
+  return c;
+}
+
+// Tensors [i, end) of one launch.
+template <int K>
+int64_t fill(TensorTable<K> &t, const Request &q, int64_t i, int chunk) {
+  t.count = 0;
+  t.chunks = 0;
+  t.chunk_elems = chunk;
+  for (; i < q.count && t.count < K; ++i) {
+    if (q.sizes[i] == 0) continue;
+    const int64_t c = (q.sizes[i] + chunk - 1) / chunk;
+    if (t.chunks + c > 0xffffffffLL) break;
+    const int k = t.count++;
+    t.src[k] = q.grads[i];
+    t.dst[k] = q.outs ? q.outs[i] : const_cast<void *>(q.grads[i]);
+    t.n[k] = q.sizes[i];
+    t.stype[k] = (uint8_t)q.types[i];
+    t.dtype[k] = (uint8_t)(q.outs ? q.out_types[i] : q.types[i]);
+    t.first[k] = (uint32_t)t.chunks;
+    t.chunks += c;
+  }
+  return i;
+}
+
+template <int K, bool MAX>
+cudaError_t run(const Request &q, bool clip) {
+  int64_t total = 0;
+  for (int64_t i = 0; i < q.count; ++i) total += q.sizes[i];
+  const int chunk = chunk_length(total);
+  static thread_local TensorTable<K> t;
+  int parts = 0;
+  cudaError_t e;
+  int64_t next = 0;
+  while (next < q.count) {
+    next = fill(t, q, next, chunk);
+    if (t.count == 0) break;
+    const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
+    e = launch_kernel(norm_partials<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, q.partial + parts);
+    if (e != cudaSuccess) return e;
+    parts += g;
+  }
+  if (!clip || parts == 0)
+    return launch_kernel(norm_finish<MAX>, dim3(1), kThreads, 0, true, q.s, (const float *)q.partial, parts,
+                         q.norm);
+  bool first = true;
+  for (next = 0; next < q.count;) {
+    next = fill(t, q, next, chunk);
+    if (t.count == 0) break;
+    const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
+    e = launch_kernel(scale_tensors<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, (const float *)q.partial,
+                      parts, q.max_norm, q.eps, first ? q.norm : nullptr);
+    if (e != cudaSuccess) return e;
+    first = false;
+  }
+  return cudaSuccess;
+}
+
+snack_status check(const Request &q, int norm_kind, const void *workspace, bool clip) {
+  if (q.count < 0) return refuse(SNACK_ERR_INVALID_ARG, "count must be >= 0");
+  if (norm_kind != 0 && norm_kind != 1) return refuse(SNACK_ERR_INVALID_ARG, "norm_kind must be 0 or 1");
+  if (!q.norm || !workspace || (q.count > 0 && (!q.grads || !q.sizes || !q.types)))
+    return refuse(SNACK_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned_to(workspace, 16) || !aligned_to(q.norm, 4))
+    return refuse(SNACK_ERR_INVALID_ARG, "workspace must be 16-byte aligned, norm 4-byte aligned");
+  if (q.outs && !q.out_types) return refuse(SNACK_ERR_INVALID_ARG, "outs without out_types");
+  if (clip && !(q.max_norm >= 0.f)) return refuse(SNACK_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if (clip && !(q.eps >= 0.f)) return refuse(SNACK_ERR_INVALID_ARG, "eps must be >= 0");
+  for (int64_t i = 0; i < q.count; ++i) {
+    if (q.sizes[i] < 0) return refuse(SNACK_ERR_INVALID_ARG, "a tensor's size is negative");
+    if (!known_type(q.types[i]) || (q.outs && !known_type(q.out_types[i])))
+      return refuse(SNACK_ERR_INVALID_ARG, "a tensor's type is not one of snack_dtype");
+    if (q.sizes[i] == 0) continue;
+    if (!q.grads[i] || (q.outs && !q.outs[i])) return refuse(SNACK_ERR_INVALID_ARG, "a tensor is NULL");
+    if (!aligned_to(q.grads[i], type_bytes(q.types[i])) ||
+        (q.outs && !aligned_to(q.outs[i], type_bytes(q.out_types[i]))))
+      return refuse(SNACK_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+    if (q.outs && q.outs[i] == q.grads[i] && q.out_types[i] != q.types[i])
+      return refuse(SNACK_ERR_INVALID_ARG, "an output in place must keep its gradient's type");
+  }
+  return SNACK_OK;
+}
+
+snack_status dispatch(const Request &q, int norm_kind, bool clip) {
+  cudaError_t e;
+  // a short list takes a short parameter block: 30 KB of parameters cost every launch
+#define SNACK_CLIP(K) e = norm_kind ? run<K, true>(q, clip) : run<K, false>(q, clip)
+  if (q.count <= 32)
+    SNACK_CLIP(32);
+  else if (q.count <= 192)
+    SNACK_CLIP(192);
+  else
+    SNACK_CLIP(kMostTable);
+#undef SNACK_CLIP
+  return e == cudaSuccess ? SNACK_OK : cuda_status(e, clip ? "gradient clipping launch" : "gradient norm launch");
+}
+
+}  // namespace
+}  // namespace snack
+
+extern "C" size_t snack_grad_norm_workspace(int64_t count) {
+  // one float per block and launch
+  const int64_t launches = (count < 0 ? 0 : count) / snack::kMostTable + 2;
+  return (size_t)launches * snack::grid_blocks() * sizeof(float);
+}
+
+extern "C" snack_status snack_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes,
+                                        const int32_t *types, int norm_kind, float *norm, void *workspace,
+                                        void *stream) {
+  const snack::Request q = {count, grads, nullptr, sizes, types, nullptr, 0.f, 0.f, norm,
+                            static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)};
+  const snack_status st = snack::check(q, norm_kind, workspace, false);
+  return st == SNACK_OK ? snack::dispatch(q, norm_kind, false) : st;
+}
+
+extern "C" snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void *const *outs,
+                                             const int64_t *sizes, const int32_t *types,
+                                             const int32_t *out_types, int norm_kind, float max_norm,
+                                             float eps, float *norm, void *workspace, void *stream) {
+  const snack::Request q = {count,    grads, outs, sizes, types, out_types,
+                            max_norm, eps,   norm, static_cast<float *>(workspace),
+                            static_cast<cudaStream_t>(stream)};
+  const snack_status st = snack::check(q, norm_kind, workspace, true);
+  return st == SNACK_OK ? snack::dispatch(q, norm_kind, true) : st;
+}

@@ -301,6 +301,160 @@ snack_status snack_forward_csr_static(int64_t out_features, int64_t in_features,
                                       int64_t batch, void *stream);
 
 /*
+ * ---- Around the sparse layers: dense operators of a decoder block ----------
+ *
+ * The calls below need no handle.  They take device pointers of the element
+ * types listed here, compute in 32-bit floats and round once, when a result
+ * is stored.  They allocate nothing: where a call needs scratch, the caller
+ * passes a `workspace` of the size that the matching *_workspace() call gives
+ * (16-byte aligned device memory, in use until the call's work on `stream` is
+ * done; its contents need not be set).  Results do not depend on the order in
+ * which blocks run: the same inputs give the same bits.  Errors are reported
+ * through snack_last_error(NULL).  All are asynchronous on `stream`, do not
+ * synchronise and can be captured into a CUDA graph.  The paper has no
+ * counterpart to them.
+ */
+typedef enum { SNACK_F32 = 0, SNACK_BF16 = 1, SNACK_F16 = 2 } snack_dtype;
+
+typedef enum { SNACK_NORM_LAYER = 0, SNACK_NORM_RMS = 1 } snack_norm_kind;
+
+typedef enum {
+  SNACK_GATE_NONE = 0,     /* no gate                                          */
+  SNACK_GATE_CHANNEL = 1,  /* [width]: one factor per channel                  */
+  SNACK_GATE_TOKEN = 2,    /* [rows]: one factor per row                       */
+  SNACK_GATE_SEQUENCE = 3, /* [rows / group_rows][width]: rows of a group share */
+  SNACK_GATE_FULL = 4      /* [rows][width], row stride gate_stride            */
+} snack_gate_kind;
+
+/*
+ * The norms before and after a block with its gate and residual scales:
+ *
+ *   u = P(y)             post_norm != 0; else u = y
+ *   r = residual_scale * x + branch_scale * gate * u
+ *   h = N(r)             next_norm != 0
+ *
+ * P and N normalise each row of `width` elements with weight and bias
+ * (either may be NULL): SNACK_NORM_LAYER subtracts the row's mean and divides
+ * by sqrt(variance + eps) (biased variance), SNACK_NORM_RMS divides by
+ * sqrt(mean of squares + eps).  N sees r before r is rounded to stream_type.
+ * y == NULL leaves the branch out (r = residual_scale * x): a plain norm.
+ *
+ * x, r, dr and dx are of stream_type; y, h, gate, dy, dh and dgate of
+ * branch_type; weights, biases and their gradients of param_type.
+ * (stream_type, branch_type) is one type twice, or SNACK_F32 and a 16-bit
+ * type; param_type is SNACK_F32 or branch_type.  Rows of x, y, a full gate,
+ * dr and dh lie *_stride elements apart, at least width unless there is one
+ * row; outputs are contiguous.  1 <= width < 2^31, rows * width < 2^62.
+ */
+typedef struct {
+  int64_t rows, width;
+  int64_t group_rows; /* rows that share one gate row (SNACK_GATE_SEQUENCE) */
+  int32_t norm_kind, post_norm, next_norm, gate_kind;
+  int32_t stream_type, branch_type, param_type, reserved;
+  float residual_scale, branch_scale, eps, reserved_f;
+  const void *x, *y, *gate;
+  int64_t x_stride, y_stride, gate_stride;
+  const void *post_weight, *post_bias, *next_weight, *next_bias;
+  float *stats; /* [rows][4]: mean, 1/deviation of y; the same of r (16-byte aligned) */
+} snack_norm_args;
+
+/*
+ * Writes r (may be NULL), h (NULL without next_norm) and, if args->stats is
+ * not NULL, the rows' statistics that the backward call reads.
+ */
+snack_status snack_residual_norm_forward(const snack_norm_args *args, void *r, void *h,
+                                         void *stream);
+
+/*
+ * Gradients of a residual norm; dr / dh are those of r / h (either may be
+ * NULL: zero).  Outputs that are NULL are skipped; the others are
+ * overwritten.  dgate has the gate's shape (contiguous), summed over what
+ * the gate was shared by.
+ */
+typedef struct {
+  const void *dr, *dh;
+  int64_t dr_stride, dh_stride;
+  void *dx, *dy, *dgate;
+  void *dpost_weight, *dpost_bias, *dnext_weight, *dnext_bias;
+} snack_norm_grads;
+
+size_t snack_residual_norm_workspace(const snack_norm_args *args);
+
+/* args as for the forward call that filled args->stats. */
+snack_status snack_residual_norm_backward(const snack_norm_args *args,
+                                          const snack_norm_grads *grads, void *workspace,
+                                          void *stream);
+
+/*
+ * Low-rank adapters of many requests beside one projection.  Request i owns
+ * the tokens offsets[i] .. offsets[i+1]-1 and names adapter n = adapter[i];
+ * for each of its tokens
+ *
+ *   H[t] = A[n] X[t],   Y[t] += s[n] * B[n] H[t]
+ *
+ * with A [adapters][rank][in], B [adapters][out][rank], s[n] = scale[n] (or
+ * `uniform_scale` where scale is NULL).  Tokens of a request whose adapter
+ * is outside [0, adapters), and tokens outside every request, keep their Y
+ * (H is zero there).  offsets [requests + 1] (non-decreasing, in [0, tokens])
+ * and adapter [requests] are int32 device arrays and never read by the host;
+ * values that break this are clamped, never followed out of bounds.
+ * X and Y rows lie x_stride / y_stride elements apart.  X, Y, A and B are of
+ * `type`; scale and H [tokens][rank] are fp32.  H is what the backward call
+ * reads.  Limits: 1 <= rank <= 512, tokens, requests, in, out < 2^31,
+ * adapters <= 65536.  X and Y must not overlap.
+ */
+typedef struct {
+  int64_t tokens, requests, adapters, in, out, rank;
+  int32_t type;
+  float uniform_scale;
+  const void *X, *A, *B;
+  int64_t x_stride;
+  const int32_t *offsets, *adapter;
+  const float *scale;
+} snack_adapter_args;
+
+size_t snack_adapter_forward_workspace(const snack_adapter_args *args);
+snack_status snack_adapter_forward(const snack_adapter_args *args, void *Y, int64_t y_stride,
+                                   float *H, void *workspace, void *stream);
+
+/*
+ * Gradients of the adapters' part of Y from dY [tokens][out]:
+ *   dH[t] = s[n] * B[n]^T dY[t],   dX[t] += A[n]^T dH[t],
+ *   dA[n] = sum_t dH[t] X[t]^T,    dB[n] = s[n] * sum_t dY[t] H[t]^T.
+ * dX is added to (it holds the projection's own input gradient), dA and dB
+ * are overwritten (zeros for adapters without tokens).  dX, dA or dB may be
+ * NULL; dX must not overlap X or dY.
+ */
+size_t snack_adapter_backward_workspace(const snack_adapter_args *args);
+snack_status snack_adapter_backward(const snack_adapter_args *args, const void *dY,
+                                    int64_t dy_stride, const float *H, void *dX,
+                                    int64_t dx_stride, void *dA, void *dB, void *workspace,
+                                    void *stream);
+
+/*
+ * The global norm over `count` gradient tensors: norm_kind 0: sqrt of the sum
+ * of all squares; 1: the largest magnitude.  grads[i] points to sizes[i]
+ * contiguous elements of types[i]; the arrays of pointers, sizes and types
+ * are host memory, read before the call returns.  *norm (device) receives
+ * the norm; NaN or infinities in a gradient make it NaN or infinite, and no
+ * gradient at all makes it 0.
+ */
+size_t snack_grad_norm_workspace(int64_t count);
+snack_status snack_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes,
+                             const int32_t *types, int norm_kind, float *norm, void *workspace,
+                             void *stream);
+
+/*
+ * The norm, and the gradients times min(1, max_norm / (norm + eps)), rounded
+ * to out_types[i] into outs[i] (outs == NULL, or outs[i] == grads[i] of the
+ * same type: in place; no other overlap).  A NaN norm makes every result NaN.
+ */
+snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void *const *outs,
+                                  const int64_t *sizes, const int32_t *types,
+                                  const int32_t *out_types, int norm_kind, float max_norm,
+                                  float eps, float *norm, void *workspace, void *stream);
+
+/*
  * Read and clear the handle's device error flag: *flag = 1 if, since the
  * last read, a kernel of this handle gave up a bounded wait on one of its
  * own shared-memory copies (its outputs for that call are then not to be

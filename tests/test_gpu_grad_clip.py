@@ -1,0 +1,196 @@
+"""The gradient norm over many tensors and clipping, against 64-bit sums.
+
+The norm of n squares is a tree of 32-bit sums of positive terms: held to
+1e-5 of its value, and so is the factor; results carry one rounding more."""
+
+import math
+
+import pytest
+import torch
+
+from dense_ref import assert_within
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+def tensors(sizes, types, seed=0, std=0.1, offset=0):
+    """One tensor per size; offset: elements by which each starts off a 16-byte boundary."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    out = []
+    for i, n in enumerate(sizes):
+        k = offset * (i % 5)
+        t = (torch.randn(n + k, generator=g, device="cuda") * std).to(types[i % len(types)])
+        out.append(t[k:])
+    return out
+
+
+def norm64(ts, kind):
+    v = [t.double() for t in ts if t.numel()]
+    if not v:
+        return 0.0
+    if kind == math.inf:
+        return float(torch.stack([t.abs().max() for t in v]).max())
+    return float(torch.stack([t.square().sum() for t in v]).sum().sqrt())
+
+
+LISTS = [
+    ([1], [F32], 0),
+    ([5, 1, 0, 33, 4096, 70001], [F32], 0),
+    ([5, 1, 0, 33, 4096, 70001], [F32, BF16, F16], 1),
+    ([1000] * 148 + [3_000_001], [F32], 0),
+    ([777] * 300, [BF16, F32], 3),
+    ([17 + (i * 37) % 900 for i in range(2500)], [F32, F16], 1),
+    ([5_000_003, 9_000_000], [BF16], 1),
+]
+
+
+@pytest.mark.parametrize("sizes,types,offset", LISTS)
+@pytest.mark.parametrize("kind", [2.0, math.inf])
+def test_norm(sizes, types, offset, kind):
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors(sizes, types, 1, offset=offset)
+    want = norm64(ts, kind)
+    for g in (ts, sn.snack_tensor_list(ts)):
+        got = float(sn.snack_grad_norm(g, kind))
+        assert abs(got - want) <= 1e-5 * want
+
+
+@pytest.mark.parametrize("sizes,types,offset", LISTS)
+@pytest.mark.parametrize("kind", [2.0, math.inf])
+@pytest.mark.parametrize("share", [0.3, 1.7])
+def test_clip_in_place(sizes, types, offset, kind, share):
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors(sizes, types, 2, offset=offset)
+    before = [t.clone() for t in ts]
+    want = norm64(ts, kind)
+    got = float(sn.snack_clip_grad_norm(ts, share * want, kind))
+    assert abs(got - want) <= 1e-5 * want
+    coef = min(1.0, share * want / (want + 1e-6))
+    for t, b in zip(ts, before):
+        if coef == 1.0:
+            assert torch.equal(t, b)
+        else:
+            v = b.double() * coef
+            assert_within("clipped", t, v, 2 * v.abs())
+
+
+@pytest.mark.parametrize("sizes,types,offset", LISTS)
+@pytest.mark.parametrize("dst,shift", [(F32, 0), (F32, 1), (BF16, 0), (BF16, 3), (F16, 1)])
+@pytest.mark.parametrize("share", [0.3, 1.7])
+def test_clip_into_other_tensors(sizes, types, offset, dst, shift, share):
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors(sizes, types, 3, offset=offset)
+    # packed end to end, `shift` elements off a 16-byte boundary, between guards
+    flat = torch.full((sum(sizes) + 64 + shift,), 7.0, dtype=dst, device="cuda")
+    out, at = [], 32 + shift
+    for n in sizes:
+        out.append(flat[at: at + n])
+        at += n
+    want = norm64(ts, 2.0)
+    before = [t.clone() for t in ts]
+    got = float(sn.snack_clip_grad_norm(ts, share * want, out=out))
+    assert abs(got - want) <= 1e-5 * want
+    coef = min(1.0, share * want / (want + 1e-6))
+    for t, b, o in zip(ts, before, out):
+        assert torch.equal(t, b)
+        v = b.double() * coef
+        assert_within("clipped", o, v, 2 * v.abs())
+    assert (flat[: 32 + shift] == 7).all() and (flat[at:] == 7).all()
+
+
+def test_nothing_and_zeros():
+    import coo_spmm_sparse_gb300 as sn
+    assert float(sn.snack_grad_norm([])) == 0.0
+    assert float(sn.snack_clip_grad_norm([], 1.0)) == 0.0
+    z = [torch.zeros(10, device="cuda"), torch.zeros(0, device="cuda")]
+    for kind in (2.0, math.inf):
+        assert float(sn.snack_grad_norm(z, kind)) == 0.0
+    assert float(sn.snack_clip_grad_norm(z, 0.0)) == 0.0
+    assert torch.equal(z[0], torch.zeros(10, device="cuda"))
+    e = [torch.zeros(0, device="cuda")]
+    assert float(sn.snack_clip_grad_norm(e, 1.0)) == 0.0
+
+
+@pytest.mark.parametrize("kind", [2.0, math.inf])
+@pytest.mark.parametrize("where", [0, 100_002])
+def test_nan_and_infinity(kind, where):
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([100_003, 50], [F32, BF16], 4)
+    ts[0][where] = float("inf")
+    assert float(sn.snack_grad_norm(ts, kind)) == math.inf
+    sn.snack_clip_grad_norm(ts, 1.0, kind)  # inf * 0 is NaN, what is finite becomes 0
+    assert torch.isnan(ts[0][where]) and float(ts[0].nan_to_num(0.0).abs().sum()) == 0.0
+    ts = tensors([100_003, 50], [F32, BF16], 4)
+    ts[0][where] = float("nan")
+    assert math.isnan(float(sn.snack_grad_norm(ts, kind)))
+    sn.snack_clip_grad_norm(ts, 1.0, kind)
+    assert torch.isnan(ts[0]).all() and torch.isnan(ts[1]).all()
+
+
+def test_matches_torch_on_a_model_and_keeps_bits():
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([768 * 50, 768, 3, 100_001] * 9, [F32], 5)
+    ps = [torch.nn.Parameter(torch.zeros_like(t)) for t in ts]
+    for p, t in zip(ps, ts):
+        p.grad = t.clone()
+    want = torch.nn.utils.clip_grad_norm_(ps, 1.0)
+    runs = []
+    for _ in range(3):
+        mine = [t.clone() for t in ts]
+        runs.append((float(sn.snack_clip_grad_norm(mine, 1.0)), mine))
+    assert abs(runs[0][0] - float(want)) <= 1e-5 * float(want)
+    for p, m in zip(ps, runs[0][1]):
+        assert torch.allclose(p.grad, m, rtol=2e-5, atol=0)
+    for n, m in runs[1:]:
+        assert n == runs[0][0] and all(torch.equal(a, b) for a, b in zip(m, runs[0][1]))
+
+
+def test_other_stream_and_graph():
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([100_000, 7, 4096], [F32], 6)
+    want = norm64(ts, 2.0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    n1 = sn.snack_grad_norm(ts, stream=s)
+    s.synchronize()
+    assert abs(float(n1) - want) <= 1e-5 * want
+    lst, out = sn.snack_tensor_list(ts), [torch.empty_like(t) for t in ts]
+    norm = torch.zeros((), device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sn.snack_clip_grad_norm(lst, 1.0, out=out, norm=norm)
+    for t in ts:
+        t.mul_(2.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert abs(float(norm) - 2 * want) <= 2e-5 * want
+    for t, o in zip(ts, out):
+        v = t.double() / (2 * want + 1e-6)
+        assert_within("clipped", o, v, 2 * v.abs())
+
+
+def test_refusals():
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([10, 20], [F32])
+    with pytest.raises(TypeError):
+        sn.snack_grad_norm([ts[0].cpu()])
+    with pytest.raises(TypeError):
+        sn.snack_grad_norm([ts[0].double()])
+    with pytest.raises(ValueError):
+        sn.snack_grad_norm([torch.zeros(4, 6, device="cuda").t()])
+    with pytest.raises(ValueError):
+        sn.snack_grad_norm(ts, 1.0)
+    for bad in (-1.0, float("nan")):
+        with pytest.raises(ValueError):
+            sn.snack_clip_grad_norm(ts, bad)
+    with pytest.raises(ValueError):
+        sn.snack_clip_grad_norm(ts, 1.0, out=[ts[0]])
+    with pytest.raises(ValueError):
+        sn.snack_clip_grad_norm(ts, 1.0, out=[ts[1], ts[0]])
+    with pytest.raises(ValueError):
+        sn.snack_grad_norm(ts, norm=torch.zeros(2, device="cuda"))
+    with pytest.raises(sn.SnackError) as e:
+        sn.snack_clip_grad_norm(ts, 1.0, eps=-1.0)
+    assert e.value.status == 1
