@@ -3,6 +3,27 @@
 //   H[t] = A_n X[t],  Y[t] += s_n B_n H[t]        n: the adapter of token t's request
 //   dH[t] = s_n B_n^T dY[t],  dX[t] += A_n^T dH[t],
 //   dA_n = sum_t dH[t] X[t]^T,  dB_n = s_n sum_t dY[t] H[t]^T
+//
+// Memory bound for ranks up to about 64: every element of X, Y, dY and dX
+// takes 2 * rank multiply-adds.  Few tokens (decoding): a block for each
+// token, the weights are the work.  Many tokens: they are first grouped by
+// adapter (`plan`), so that requests that share one fill tiles together,
+// and each product then runs over tiles of 32 tokens on the matrix
+// instructions:
+//
+//   down   [tokens x K] x [K x rank]   K split over the block's warps, one sum through shared memory
+//   up     [tokens x rank] x [rank x K], added to the rows in place
+//   outer  [rank x tokens] x [tokens x K], tokens split over blocks, parts added in order
+//
+// Operands go from memory straight into the registers that the matrix
+// instruction wants them in.  The order in which the summed index is fed to
+// it is free as long as both operands keep it, so a lane takes 16 contiguous
+// bytes of a row and the four lanes of a row take 64: no shared memory and
+// no barrier stands between a load and its product.  fp32 operands are split
+// into two tf32 parts, x = hi + lo, and hi*hi + hi*lo + lo*hi is summed:
+// what is left out is below 2^-22 of a product.  Running sums leave the
+// matrix unit's accumulator every few steps for a 32-bit sum that rounds to
+// nearest.
 #include <algorithm>
 
 #include "dense_ops.cuh"
@@ -11,145 +32,961 @@ namespace snack {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 32;            // tokens of a tile
+constexpr int kPlanThreads = 1024;
+constexpr int kRankPass = 64;        // ranks that one pass of `down` sums
+
+// Ranks that one pass of `outer` sums.
+__host__ __device__ constexpr int outer_ranks(int64_t rank) { return rank <= 16 ? 16 : 32; }
+
+// Tokens grouped by adapter.
+struct Plan {
+  int32_t *head;   // [0] tiles, [1] used adapters, [2] tokens with an adapter
+  int32_t *perm;   // [tokens] token at each place
+  int4 *tiles;     // {adapter, first place, tokens, index among the used}
+  int4 *used;      // {adapter, first place, tokens, 0}
+  int32_t *index;  // [adapters] index among the used, or -1
+  int32_t *soff, *place, *base;  // many requests: offsets kept in order, first places, running places
+  int64_t max_tiles, max_used;
+};
 
 struct AdapterArgs {
   snack_adapter_args a;
-  void *Y;
-  int64_t y_stride;
-  const void *dY;
-  int64_t dy_stride;
-  void *dX;
-  int64_t dx_stride;
-  float *H;         // [tokens][rank]
-  const float *Hin;
-  float *dH;        // [tokens][rank]
-  void *dA, *dB;
+  Plan p;
+  float *H;  // [tokens][rank], zeroed by the plan where a token has no adapter (or null)
 };
-
-// The adapter of token t, or -1.
-__device__ __forceinline__ int adapter_of(const snack_adapter_args &a, int64_t t) {
-  // the last request that begins at or before t; requests that hold nothing
-  // begin where the next one does
-  int lo = 0, hi = (int)a.requests;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.offsets[mid] <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  if (lo == 0 || t >= a.offsets[lo]) return -1;
-  const int n = a.adapter[lo - 1];
-  return n >= 0 && n < a.adapters ? n : -1;
-}
 
 __device__ __forceinline__ float scale_of(const snack_adapter_args &a, int n) {
   return a.scale ? a.scale[n] : a.uniform_scale;
 }
 
-// A warp for each (token, rank index): the product over `in`.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) adapter_down(const __grid_constant__ AdapterArgs q) {
+// ------------------------------------------------------------------ plan
+
+__device__ __forceinline__ int32_t clamp_offset(int32_t v, int64_t tokens) {
+  return v < 0 ? 0 : (v > tokens ? (int32_t)tokens : v);
+}
+
+// Inclusive maximum over the block's values, `carry` included; `red` holds 32 ints.
+__device__ __forceinline__ int32_t block_scan_max(int32_t v, int32_t carry, int32_t *red) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = max(v, u);
+  }
+  if (lane == 31) red[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    int32_t s = lane < (int)blockDim.x / 32 ? red[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s = max(s, u);
+    }
+    red[lane] = s;
+  }
+  __syncthreads();
+  if (w > 0) v = max(v, red[w - 1]);
+  v = max(v, carry);
+  __syncthreads();
+  return v;
+}
+
+// The request of token t by the ordered offsets (o[0..n]): the last that
+// begins at or before t, or -1.
+__device__ __forceinline__ int request_of(const int32_t *o, int n, int32_t t) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (o[mid] <= t)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo == 0 || t >= o[lo] ? -1 : lo - 1;
+}
+
+__device__ __forceinline__ void zero_row(const AdapterArgs &q, int64_t t) {
+  if (q.H)
+    for (int64_t j = 0; j < q.a.rank; ++j) q.H[t * q.a.rank + j] = 0.f;
+}
+
+// Up to 1024 requests: every block works all of them out in shared memory
+// (each request compares itself with all others) and places its own share
+// of the tokens; block 0 writes the tables.
+__global__ void __launch_bounds__(kPlanThreads) plan_small(const __grid_constant__ AdapterArgs q) {
+  __shared__ int32_t off[kPlanThreads + 1], key[kPlanThreads], len[kPlanThreads], place[kPlanThreads],
+      tiles_of[kPlanThreads], red[32];
   dependency_wait();
+  dependency_launch();
   const snack_adapter_args &a = q.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < a.tokens * a.rank; w += warps) {
-    const int64_t t = w / a.rank, j = w % a.rank;
-    const int n = adapter_of(a, t);
+  const int R = (int)a.requests, r = threadIdx.x;
+  {
+    const int32_t v = r < R ? clamp_offset(a.offsets[r], a.tokens) : 0;
+    const int32_t m = block_scan_max(v, 0, red);
+    if (r < R) off[r] = m;
+    if (r == R - 1) off[R] = max(m, clamp_offset(a.offsets[R], a.tokens));
+  }
+  __syncthreads();
+  int n = -1;
+  if (r < R) {
+    n = a.adapter[r];
+    len[r] = off[r + 1] - off[r];
+    if (n < 0 || n >= a.adapters || len[r] == 0) n = -1;
+    key[r] = n;
+  }
+  __syncthreads();
+  int first = 0, total = 0, all = 0;
+  bool leader = n >= 0;
+  if (r < R)
+    for (int j = 0; j < R; ++j) {
+      const int k = key[j];
+      if (k < 0) continue;
+      const int l = len[j];
+      all += l;
+      if (k < n || (k == n && j < r)) first += l;
+      if (k == n) {
+        total += l;
+        if (j < r) leader = false;
+      }
+    }
+  if (r < R) {
+    place[r] = first;
+    tiles_of[r] = leader ? (total + kTile - 1) / kTile : 0;
+  }
+  if (blockIdx.x == 0) {
+    for (int64_t i = r; i < a.adapters; i += kPlanThreads) q.p.index[i] = -1;
+    __syncthreads();
+    int t0 = 0, u = 0, tn = 0, un = 0;
+    if (r < R)
+      for (int j = 0; j < R; ++j) {
+        const int c = tiles_of[j];
+        if (c == 0) continue;
+        tn += c;
+        ++un;
+        if (key[j] < n) {
+          t0 += c;
+          ++u;
+        }
+      }
+    if (r < R && leader) {
+      q.p.index[n] = u;
+      q.p.used[u] = make_int4(n, first, total, 0);
+      for (int k = 0; k * kTile < total; ++k)
+        q.p.tiles[t0 + k] = make_int4(n, first + k * kTile, min(kTile, total - k * kTile), u);
+    }
+    if (r == 0) {
+      q.p.head[0] = tn;
+      q.p.head[1] = un;
+      q.p.head[2] = all;
+    }
+  }
+  __syncthreads();
+  for (int64_t t = (int64_t)blockIdx.x * kPlanThreads + r; t < a.tokens; t += (int64_t)gridDim.x * kPlanThreads) {
+    const int i = request_of(off, R, (int32_t)t);
+    if (i >= 0 && key[i] >= 0)
+      q.p.perm[place[i] + ((int32_t)t - off[i])] = (int32_t)t;
+    else
+      zero_row(q, t);
+  }
+}
+
+// Any number of requests: one block counts the tokens of every adapter,
+// places adapters and then requests, 1024 at a time.
+__global__ void __launch_bounds__(kPlanThreads) plan_requests(const __grid_constant__ AdapterArgs q) {
+  __shared__ int32_t key[kPlanThreads], len[kPlanThreads], red[32], carry[3];
+  dependency_wait();
+  dependency_launch();
+  const snack_adapter_args &a = q.a;
+  const Plan &p = q.p;
+  const int tid = threadIdx.x;
+  for (int64_t i = tid; i < a.adapters; i += kPlanThreads) p.base[i] = 0;
+  int32_t top = 0;
+  for (int64_t c = 0; c <= a.requests; c += kPlanThreads) {
+    const int64_t i = c + tid;
+    const int32_t v = i <= a.requests ? clamp_offset(a.offsets[i], a.tokens) : 0;
+    const int32_t m = block_scan_max(v, top, red);
+    if (i <= a.requests) p.soff[i] = m;
+    if (tid == kPlanThreads - 1) carry[0] = m;
+    __syncthreads();
+    top = carry[0];
+    __syncthreads();
+  }
+  for (int64_t i = tid; i < a.requests; i += kPlanThreads) {
+    const int n = a.adapter[i], l = p.soff[i + 1] - p.soff[i];
+    if (n >= 0 && n < a.adapters && l > 0) atomicAdd(&p.base[n], l);
+  }
+  if (tid < 3) carry[tid] = 0;
+  __syncthreads();
+  // exclusive sums over the adapters of tokens, used ones and tiles
+  for (int64_t c = 0; c < a.adapters; c += kPlanThreads) {
+    const int64_t n = c + tid;
+    const int32_t total = n < a.adapters ? p.base[n] : 0;
+    int32_t sum[3] = {total, total > 0, (total + kTile - 1) / kTile}, mine[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int lane = tid & 31, w = tid >> 5;
+      int32_t v = sum[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (lane == 31) red[w] = v;
+      __syncthreads();
+      if (w == 0) {
+        int32_t s = red[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t u = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += u;
+        }
+        red[lane] = s;
+      }
+      __syncthreads();
+      v += (w > 0 ? red[w - 1] : 0) + carry[k];
+      mine[k] = v - sum[k];
+      __syncthreads();
+      if (tid == kPlanThreads - 1) carry[k] = v;
+      __syncthreads();
+    }
+    if (n < a.adapters) {
+      p.base[n] = mine[0];
+      p.index[n] = total > 0 ? mine[1] : -1;
+      if (total > 0) {
+        p.used[mine[1]] = make_int4((int)n, mine[0], total, 0);
+        for (int k = 0; k * kTile < total; ++k)
+          p.tiles[mine[2] + k] = make_int4((int)n, mine[0] + k * kTile, min(kTile, total - k * kTile), mine[1]);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.head[0] = carry[2];
+    p.head[1] = carry[1];
+    p.head[2] = carry[0];
+  }
+  for (int64_t c = 0; c < a.requests; c += kPlanThreads) {
+    const int64_t i = c + tid;
+    int n = -1, l = 0;
+    if (i < a.requests) {
+      n = a.adapter[i];
+      l = p.soff[i + 1] - p.soff[i];
+      if (n < 0 || n >= a.adapters || l == 0) n = -1;
+    }
+    key[tid] = n;
+    len[tid] = l;
+    __syncthreads();
+    int before = 0;
+    if (n >= 0)
+      for (int j = 0; j < tid; ++j) before += key[j] == n ? len[j] : 0;
+    if (i < a.requests) p.place[i] = n >= 0 ? p.base[n] + before : -1;
+    __syncthreads();
+    if (n >= 0) atomicAdd(&p.base[n], l);
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) plan_tokens(const __grid_constant__ AdapterArgs q) {
+  dependency_wait();
+  dependency_launch();
+  const snack_adapter_args &a = q.a;
+  for (int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x; t < a.tokens; t += (int64_t)gridDim.x * kThreads) {
+    const int i = request_of(q.p.soff, (int)a.requests, (int32_t)t);
+    if (i >= 0 && q.p.place[i] >= 0)
+      q.p.perm[q.p.place[i] + ((int32_t)t - q.p.soff[i])] = (int32_t)t;
+    else
+      zero_row(q, t);
+  }
+}
+
+// ------------------------------------------------------------------ matrix instructions
+
+__device__ __forceinline__ float tf32_of(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return __uint_as_float(r);
+}
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+        "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                       uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_16<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma_16<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two values as one register of T pairs, and what that rounding left out as another.
+template <typename T>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo) {
+  alignas(4) T h[2] = {from_float<T>(x), from_float<T>(y)};
+  alignas(4) T l[2] = {from_float<T>(x - to_float(h[0])), from_float<T>(y - to_float(h[1]))};
+  hi = *reinterpret_cast<const uint32_t *>(h);
+  lo = *reinterpret_cast<const uint32_t *>(l);
+}
+
+// 16 bytes of a row from element k on; elements from `limit` on read as 0.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 load16(const T *row, int64_t k, int64_t limit, bool valid) {
+  constexpr int E = 16 / sizeof(T);
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (ALIGNED) {
+    if (valid && k < limit) v = *reinterpret_cast<const uint4 *>(row + k);
+  } else if (valid) {
+    T *e = reinterpret_cast<T *>(&v);
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (k + i < limit) e[i] = row[k + i];
+  }
+  return v;
+}
+
+// One group of the summed index (64 bytes of a row: 16 fp32 or 32 16-bit
+// elements) of a 16 x 8 product: rows g and g + 8 in v0 and v1, the other
+// operand's row g in w.
+template <typename T>
+struct Group {
+  static constexpr int E = 16 / sizeof(T);
+  static constexpr int K = 4 * E;
+};
+
+__device__ __forceinline__ void split4(const uint4 &v, float (&hi)[4], float (&lo)[4]) {
+  const float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = tf32_of(x[i]);
+    lo[i] = x[i] - hi[i];
+  }
+}
+
+// ------------------------------------------------------------------ down: H = X W^T
+
+struct DownArgs {
+  const void *X;      // rows of K elements, x_stride apart
+  const void *W;      // [adapter or used index][rank][K]
+  int64_t x_stride, K, rank;
+  bool by_used;       // W is indexed by the tile's index among the used adapters
+  bool scaled;        // times the adapter's scale
+  float *H;           // [tokens][rank]
+};
+
+// Block: one tile of kTile tokens, ranks [64 z, 64 z + 64).  Its warps take
+// every eighth run of U groups of K and meet in shared memory.
+template <typename T, int NT, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) adapter_down(const __grid_constant__ AdapterArgs q,
+                                                         const __grid_constant__ DownArgs d) {
+  constexpr int MT = kTile / 16, E = Group<T>::E, KG = Group<T>::K;
+  constexpr int U = NT <= 2 ? 4 : 2;
+  constexpr int kCols = NT * 8;
+  extern __shared__ float part[];  // [kWarps][kTile][kCols + 4]
+  dependency_wait();
+  dependency_launch();
+  if ((int)blockIdx.x >= q.p.head[0]) return;
+  const int4 tile = q.p.tiles[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int64_t j0 = (int64_t)blockIdx.y * kRankPass;
+  const T *rows[2 * MT];
+  bool ok[2 * MT];
+#pragma unroll
+  for (int m = 0; m < 2 * MT; ++m) {
+    const int i = m * 8 + g;
+    ok[m] = i < tile.z;
+    rows[m] = static_cast<const T *>(d.X) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.x_stride : 0);
+  }
+  const T *wrow[NT];
+  bool wok[NT];
+  const int64_t wbase = (int64_t)(d.by_used ? tile.w : tile.x) * d.rank;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int64_t j = j0 + n * 8 + g;
+    wok[n] = j < d.rank;
+    wrow[n] = static_cast<const T *>(d.W) + (wok[n] ? (wbase + j) * d.K : 0);
+  }
+  float sum[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
+
+  for (int64_t k0 = (int64_t)warp * U * KG; k0 < d.K; k0 += (int64_t)kWarps * U * KG) {
+    uint4 x[U][2 * MT], w[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = k0 + u * KG + t * E;
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m) x[u][m] = load16<T, ALIGNED>(rows[m], k, d.K, ok[m]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) w[u][n] = load16<T, ALIGNED>(wrow[n], k, d.K, wok[n]);
+    }
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (sizeof(T) == 4) {
+        float xh[2 * MT][4], xl[2 * MT][4];
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) split4(x[u][m], xh[m], xl[m]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float wh[4], wl[4];
+          split4(w[u][n], wh, wl);
+#pragma unroll
+          for (int s = 0; s < 4; s += 2)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_tf32(acc[m][n], xl[2 * m][s], xl[2 * m + 1][s], xl[2 * m][s + 1], xl[2 * m + 1][s + 1], wh[s], wh[s + 1]);
+              mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wl[s], wl[s + 1]);
+              mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wh[s], wh[s + 1]);
+            }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma_16<T>(acc[m][n], x[u][2 * m].x, x[u][2 * m + 1].x, x[u][2 * m].y, x[u][2 * m + 1].y, w[u][n].x, w[u][n].y);
+            mma_16<T>(acc[m][n], x[u][2 * m].z, x[u][2 * m + 1].z, x[u][2 * m].w, x[u][2 * m + 1].w, w[u][n].z, w[u][n].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[m][n][i] += acc[m][n][i];
+  }
+  constexpr int LD = kCols + 4;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float *at = part + ((int64_t)warp * kTile + m * 16 + g) * LD + n * 8 + 2 * t;
+      at[0] = sum[m][n][0];
+      at[1] = sum[m][n][1];
+      at[8 * LD] = sum[m][n][2];
+      at[8 * LD + 1] = sum[m][n][3];
+    }
+  __syncthreads();
+  const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
+  for (int e = threadIdx.x; e < kTile * kCols; e += kThreads) {
+    const int i = e / kCols, j = e % kCols;
+    if (i >= tile.z || j0 + j >= d.rank) continue;
     float s = 0.f;
-    if (n >= 0) {
-      const T *x = static_cast<const T *>(a.X) + t * a.x_stride;
-      const T *m = static_cast<const T *>(a.A) + ((int64_t)n * a.rank + j) * a.in;
-      for (int64_t i = lane; i < a.in; i += 32) s = fmaf(to_float(x[i]), to_float(m[i]), s);
-      s = warp_sum(s);
-    }
-    if (lane == 0) q.H[w] = s;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += part[((int64_t)w * kTile + i) * LD + j];
+    d.H[(int64_t)q.p.perm[tile.y + i] * d.rank + j0 + j] = s * scale;
   }
 }
 
+// ------------------------------------------------------------------ up: Y += H W^T
+
+struct UpArgs {
+  const float *H;     // [tokens][rank]
+  const void *W;      // [adapter or used index][K][rank]
+  void *Y;            // rows of K elements, y_stride apart, added to
+  int64_t y_stride, K, rank;
+  bool by_used, scaled;
+  int64_t blocks;     // blocks side by side over K
+};
+
+// Columns that a warp takes at once: 64 bytes of each row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ AdapterArgs q) {
-  dependency_wait();
-  const snack_adapter_args &a = q.a;
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const int n = adapter_of(a, t);
-    if (n < 0) continue;
-    const float scale = scale_of(a, n);
-    for (int64_t o = threadIdx.x; o < a.out; o += kThreads) {
-      const T *m = static_cast<const T *>(a.B) + ((int64_t)n * a.out + o) * a.rank;
-      float s = 0.f;
-      for (int64_t j = 0; j < a.rank; ++j) s = fmaf(q.H[t * a.rank + j], to_float(m[j]), s);
-      T *y = static_cast<T *>(q.Y) + t * q.y_stride + o;
-      *y = from_float<T>(fmaf(scale, s, to_float(*y)));
-    }
-  }
-}
+struct UpShape {
+  static constexpr int E = 16 / sizeof(T);
+  static constexpr int NT = E / 2;       // 8-column products side by side
+  static constexpr int COLS = 4 * E;     // 16 or 32
+  static constexpr int GROUPS = 4;       // column groups of a warp
+};
 
-// A warp for each (token, rank index): dH.
+// Four ranks of a weight row as the B operand of one or two instructions.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) adapter_back_rank(const __grid_constant__ AdapterArgs q) {
-  dependency_wait();
-  const snack_adapter_args &a = q.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; w < a.tokens * a.rank; w += warps) {
-    const int64_t t = w / a.rank, j = w % a.rank;
-    const int n = adapter_of(a, t);
-    float s = 0.f;
-    if (n >= 0) {
-      const T *dy = static_cast<const T *>(q.dY) + t * q.dy_stride;
-      const T *m = static_cast<const T *>(a.B) + (int64_t)n * a.out * a.rank + j;
-      for (int64_t o = lane; o < a.out; o += 32) s = fmaf(to_float(dy[o]), to_float(m[o * a.rank]), s);
-      s = warp_sum(s) * scale_of(a, n);
+__device__ __forceinline__ void load_ranks(const T *row, int64_t j, int64_t rank, bool vec, bool valid, T (&out)[4]) {
+  if (vec) {
+    if (sizeof(T) == 4) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (valid && j < rank) v = *reinterpret_cast<const uint4 *>(row + j);
+      *reinterpret_cast<uint4 *>(out) = v;
+    } else {
+      uint2 v = make_uint2(0, 0);
+      if (valid && j < rank) v = *reinterpret_cast<const uint2 *>(row + j);
+      *reinterpret_cast<uint2 *>(out) = v;
     }
-    if (lane == 0) q.dH[w] = s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = valid && j + i < rank ? row[j + i] : from_float<T>(0.f);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) adapter_back_input(const __grid_constant__ AdapterArgs q) {
+// Block: one tile of kTile tokens, kWarps * GROUPS column groups.  The
+// tile's H is kept in shared memory, split in two parts, in the order in
+// which the lanes want it.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ AdapterArgs q,
+                                                       const __grid_constant__ UpArgs d) {
+  using S = UpShape<T>;
+  constexpr int MT = kTile / 16, E = S::E, NT = S::NT;
+  extern __shared__ uint4 frag[];  // [16-rank groups][MT][2 (high and low)][16-bit: 1, fp32: 2][32 lanes]
+  constexpr int PER = sizeof(T) == 4 ? 2 : 1;
   dependency_wait();
-  const snack_adapter_args &a = q.a;
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const int n = adapter_of(a, t);
-    if (n < 0) continue;
-    for (int64_t i = threadIdx.x; i < a.in; i += kThreads) {
-      const T *m = static_cast<const T *>(a.A) + (int64_t)n * a.rank * a.in + i;
-      float s = 0.f;
-      for (int64_t j = 0; j < a.rank; ++j) s = fmaf(q.dH[t * a.rank + j], to_float(m[j * a.in]), s);
-      T *dx = static_cast<T *>(q.dX) + t * q.dx_stride + i;
-      *dx = from_float<T>(to_float(*dx) + s);
+  dependency_launch();
+  const int64_t which = blockIdx.x / d.blocks, cblock = blockIdx.x % d.blocks;
+  if (which >= q.p.head[0]) return;
+  const int4 tile = q.p.tiles[which];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int rg = (int)((d.rank + 15) / 16);
+  const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
+  for (int i = warp; i < rg * MT; i += kWarps) {
+    const int m = i % MT, k = i / MT;
+    float h[2][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = m * 16 + half * 8 + g;
+      const float *at = d.H + (row < tile.z ? (int64_t)q.p.perm[tile.y + row] * d.rank : 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t j = k * 16 + 4 * t + e;
+        h[half][e] = row < tile.z && j < d.rank ? at[j] * scale : 0.f;
+      }
     }
+    uint4 *to = frag + (int64_t)(k * MT + m) * 2 * PER * 32 + lane;
+    if constexpr (sizeof(T) == 4) {
+      float hi[2][4], lo[2][4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hi[half][e] = tf32_of(h[half][e]);
+          lo[half][e] = h[half][e] - hi[half][e];
+        }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        to[(0 * PER + s) * 32] = make_uint4(__float_as_uint(hi[0][2 * s]), __float_as_uint(hi[1][2 * s]),
+                                            __float_as_uint(hi[0][2 * s + 1]), __float_as_uint(hi[1][2 * s + 1]));
+        to[(1 * PER + s) * 32] = make_uint4(__float_as_uint(lo[0][2 * s]), __float_as_uint(lo[1][2 * s]),
+                                            __float_as_uint(lo[0][2 * s + 1]), __float_as_uint(lo[1][2 * s + 1]));
+      }
+    } else {
+      uint4 hi, lo;
+      split_pair<T>(h[0][0], h[0][1], hi.x, lo.x);
+      split_pair<T>(h[1][0], h[1][1], hi.y, lo.y);
+      split_pair<T>(h[0][2], h[0][3], hi.z, lo.z);
+      split_pair<T>(h[1][2], h[1][3], hi.w, lo.w);
+      to[0] = hi;
+      to[32] = lo;
+    }
+  }
+  T *rows[2 * MT];
+  bool ok[2 * MT];
+#pragma unroll
+  for (int m = 0; m < 2 * MT; ++m) {
+    const int i = m * 8 + g;
+    ok[m] = i < tile.z;
+    rows[m] = static_cast<T *>(d.Y) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.y_stride : 0);
+  }
+  __syncthreads();
+  const T *W = static_cast<const T *>(d.W) + (int64_t)(d.by_used ? tile.w : tile.x) * d.K * d.rank;
+  const bool wvec = d.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(d.W) & (4 * sizeof(T) - 1)) == 0;
+#pragma unroll 2
+  for (int c = 0; c < S::GROUPS; ++c) {
+    const int64_t c0 = ((cblock * S::GROUPS + c) * kWarps + warp) * S::COLS;
+    if (c0 >= d.K) break;
+    uint4 y[2 * MT];
+#pragma unroll
+    for (int m = 0; m < 2 * MT; ++m) y[m] = load16<T, ALIGNED>(rows[m], c0 + t * E, d.K, ok[m]);
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    for (int k = 0; k < rg; ++k) {
+      const uint4 *from = frag + (int64_t)k * MT * 2 * PER * 32 + lane;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        // column of the product's index g: the lane that ends up with columns
+        // 2t and 2t + 1 of every n holds E columns in a row
+        const int64_t col = c0 + (g >> 1) * E + 2 * n + (g & 1);
+        alignas(16) T w[4];
+        load_ranks(W + (col < d.K ? col * d.rank : 0), (int64_t)k * 16 + 4 * t, d.rank, wvec, col < d.K, w);
+        if constexpr (sizeof(T) == 4) {
+          float wh[4], wl[4];
+          split4(*reinterpret_cast<const uint4 *>(w), wh, wl);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const uint4 h = from[((m * 2 + 0) * PER + s) * 32], l = from[((m * 2 + 1) * PER + s) * 32];
+              const auto f = [](uint32_t v) { return __uint_as_float(v); };
+              mma_tf32(acc[m][n], f(l.x), f(l.y), f(l.z), f(l.w), wh[2 * s], wh[2 * s + 1]);
+              mma_tf32(acc[m][n], f(h.x), f(h.y), f(h.z), f(h.w), wl[2 * s], wl[2 * s + 1]);
+              mma_tf32(acc[m][n], f(h.x), f(h.y), f(h.z), f(h.w), wh[2 * s], wh[2 * s + 1]);
+            }
+        } else {
+          const uint2 b = *reinterpret_cast<const uint2 *>(w);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint4 h = from[(m * 2 + 0) * 32], l = from[(m * 2 + 1) * 32];
+            mma_16<T>(acc[m][n], l.x, l.y, l.z, l.w, b.x, b.y);
+            mma_16<T>(acc[m][n], h.x, h.y, h.z, h.w, b.x, b.y);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!ok[2 * m + half]) continue;
+        T *e = reinterpret_cast<T *>(&y[2 * m + half]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            e[2 * n + i] = from_float<T>(to_float(e[2 * n + i]) + acc[m][n][2 * half + i]);
+        T *to = rows[2 * m + half] + c0 + t * E;
+        if (ALIGNED) {
+          if (c0 + t * E < d.K) *reinterpret_cast<uint4 *>(to) = y[2 * m + half];
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (c0 + t * E + i < d.K) to[i] = e[i];
+        }
+      }
   }
 }
 
-// One thread for each element of dA (or dB): the sum over the tokens of the
-// adapter's requests.
-template <typename T, bool DB>
-__global__ void __launch_bounds__(kThreads) adapter_back_weights(const __grid_constant__ AdapterArgs q) {
+// ------------------------------------------------------------------ outer: sum_t h[t] x[t]^T
+
+struct OuterArgs {
+  const float *H;   // [tokens][rank]
+  const void *X;    // rows of K elements
+  int64_t x_stride, K, rank;
+  int64_t chunk;    // places of one block
+  int64_t blocks;   // blocks side by side over K
+  float *parts;     // [chunk index + used index][rank][K]
+};
+
+// Block: kWarps * (128 bytes of columns), one chunk of places, 16 * RM
+// ranks.  A chunk may hold the end of one adapter and the beginning of
+// others: each leaves a part of its own, in the slot chunk + index among
+// the used.  The chunk's H lies in shared memory, a token every LD floats:
+// lane (g, t) reads rank g of token t, bank 8 t + g.
+template <typename T, int RM, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) adapter_outer(const __grid_constant__ AdapterArgs q,
+                                                          const __grid_constant__ OuterArgs d) {
+  constexpr int E = 16 / sizeof(T), NT = E, COLS = 8 * E, LD = 16 * RM + 8;
+  constexpr int TS = sizeof(T) == 4 ? 8 : 16;  // tokens of a step
+  constexpr int U = sizeof(T) == 4 ? 4 : 2;    // steps whose rows are loaded together
+  constexpr int NR = TS / 4;
+  extern __shared__ float hs[];  // [chunk][LD], then the chunk's tokens
+  int32_t *tok = reinterpret_cast<int32_t *>(hs + d.chunk * LD);
   dependency_wait();
-  const snack_adapter_args &a = q.a;
-  const int64_t len = DB ? a.out : a.in, total = a.adapters * a.rank * len;
-  const T *big = static_cast<const T *>(DB ? q.dY : a.X);
-  const int64_t stride = DB ? q.dy_stride : a.x_stride;
-  const float *small = DB ? q.Hin : q.dH;
+  dependency_launch();
+  const int64_t slice = blockIdx.x / d.blocks, cblock = blockIdx.x % d.blocks;
+  const int64_t p0 = slice * d.chunk;
+  const int places = (int)(min((int64_t)q.p.head[2], p0 + d.chunk) - p0);
+  if (places <= 0) return;
+  const int64_t j0 = (int64_t)blockIdx.y * 16 * RM;
+  for (int i = threadIdx.x; i < places * 16 * RM; i += kThreads) {
+    const int k = i / (16 * RM), j = i % (16 * RM);
+    const int32_t t = q.p.perm[p0 + k];
+    if (j == 0) tok[k] = t;
+    hs[k * LD + j] = j0 + j < d.rank ? d.H[t * d.rank + j0 + j] : 0.f;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int64_t c0 = (cblock * kWarps + warp) * COLS, col = c0 + g * E;
+  if (c0 >= d.K) return;
+  const T *X = static_cast<const T *>(d.X);
+  // the first adapter of the chunk: the last used one that begins at or before p0
+  int u = 0;
+  {
+    int lo = 0, hi = q.p.head[1];
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (q.p.used[mid].y <= p0)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    u = lo - 1;
+  }
+  for (int p = 0; p < places; ++u) {
+    const int4 use = q.p.used[u];
+    const int end = (int)min((int64_t)places, (int64_t)use.y + use.z - p0);
+    float sum[RM][NT][4];
+#pragma unroll
+    for (int m = 0; m < RM; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
+    for (; p < end; p += U * TS) {
+      uint4 x[U][NR];
+#pragma unroll
+      for (int s = 0; s < U; ++s)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          // rows of a step: fp32 t and t + 4; 16-bit 2t, 2t + 1, 2t + 8, 2t + 9
+          const int k = p + s * TS + (sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1));
+          x[s][i] = load16<T, ALIGNED>(X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K, k < end);
+        }
+      float acc[RM][NT][4];
+#pragma unroll
+      for (int m = 0; m < RM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        float h[NR][2 * RM];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int k = p + s * TS + (sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1));
+#pragma unroll
+          for (int m = 0; m < 2 * RM; ++m) h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
+        }
+        if constexpr (sizeof(T) == 4) {
+          float xh[2][4], xl[2][4];
+          split4(x[s][0], xh[0], xl[0]);
+          split4(x[s][1], xh[1], xl[1]);
+#pragma unroll
+          for (int m = 0; m < RM; ++m) {
+            float hh[4], hl[4];
+            const float v[4] = {h[0][2 * m], h[0][2 * m + 1], h[1][2 * m], h[1][2 * m + 1]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hh[i] = tf32_of(v[i]);
+              hl[i] = v[i] - hh[i];
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_tf32(acc[m][n], hl[0], hl[1], hl[2], hl[3], xh[0][n], xh[1][n]);
+              mma_tf32(acc[m][n], hh[0], hh[1], hh[2], hh[3], xl[0][n], xl[1][n]);
+              mma_tf32(acc[m][n], hh[0], hh[1], hh[2], hh[3], xh[0][n], xh[1][n]);
+            }
+          }
+        } else {
+          uint32_t b[2][NT];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t lo[4] = {x[s][2 * e].x, x[s][2 * e].y, x[s][2 * e].z, x[s][2 * e].w};
+            const uint32_t hi[4] = {x[s][2 * e + 1].x, x[s][2 * e + 1].y, x[s][2 * e + 1].z, x[s][2 * e + 1].w};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[e][n] = __byte_perm(lo[n / 2], hi[n / 2], n % 2 ? 0x7632 : 0x5410);
+          }
+#pragma unroll
+          for (int m = 0; m < RM; ++m) {
+            uint32_t hh[4], hl[4];
+            split_pair<T>(h[0][2 * m], h[1][2 * m], hh[0], hl[0]);
+            split_pair<T>(h[0][2 * m + 1], h[1][2 * m + 1], hh[1], hl[1]);
+            split_pair<T>(h[2][2 * m], h[3][2 * m], hh[2], hl[2]);
+            split_pair<T>(h[2][2 * m + 1], h[3][2 * m + 1], hh[3], hl[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_16<T>(acc[m][n], hl[0], hl[1], hl[2], hl[3], b[0][n], b[1][n]);
+              mma_16<T>(acc[m][n], hh[0], hh[1], hh[2], hh[3], b[0][n], b[1][n]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < RM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[m][n][i] += acc[m][n][i];
+    }
+    p = end;
+    float *out = d.parts + (slice + u) * d.rank * d.K;
+#pragma unroll
+    for (int m = 0; m < RM; ++m)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int64_t j = j0 + m * 16 + half * 8 + g;
+        if (j >= d.rank) continue;
+        // index 2t, 2t + 1 of product n is column c0 + (2t or 2t + 1) * E + n
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int64_t c = c0 + (2 * t + i) * E + n;
+            if (c < d.K) out[j * d.K + c] = sum[m][n][2 * half + i];
+          }
+      }
+  }
+}
+
+// The parts of each adapter, added in order, rounded once.  TRANSPOSE: the
+// output is [adapter][K][rank].
+template <typename T, bool TRANSPOSE>
+__global__ void __launch_bounds__(kThreads) adapter_outer_finish(const __grid_constant__ AdapterArgs q,
+                                                                 const __grid_constant__ OuterArgs d, T *out,
+                                                                 bool scaled) {
+  dependency_wait();
+  dependency_launch();
+  const int64_t per = d.rank * d.K, total = q.a.adapters * per;
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kThreads) {
-    const int64_t n = e / (a.rank * len), rest = e % (a.rank * len);
-    const int64_t j = DB ? rest % a.rank : rest / len, i = DB ? rest / a.rank : rest % len;
+    const int64_t n = e / per, i = e % per;
+    const int u = q.p.index[n];
     float s = 0.f;
-    bool used = false;
-    for (int64_t r = 0; r < a.requests; ++r) {
-      if (a.adapter[r] != n) continue;
-      used = true;
-      const int64_t t0 = max(0, a.offsets[r]), t1 = min((int64_t)a.offsets[r + 1], a.tokens);
-      float part = 0.f;
-      for (int64_t t = t0; t < t1; ++t) part = fmaf(small[t * a.rank + j], to_float(big[t * stride + i]), part);
-      s += part;
+    if (u >= 0) {
+      const int4 use = q.p.used[u];
+      const int64_t s0 = use.y / d.chunk + u, s1 = (use.y + use.z - 1) / d.chunk + u;
+      const int64_t at = TRANSPOSE ? (i % d.rank) * d.K + i / d.rank : i;
+      for (int64_t k = s0; k <= s1; ++k) s += d.parts[k * per + at];
+      if (scaled) s *= scale_of(q.a, (int)n);
     }
-    static_cast<T *>(DB ? q.dB : q.dA)[e] = from_float<T>(DB && used ? s * scale_of(a, (int)n) : s);
+    out[e] = from_float<T>(s);
   }
 }
+
+// Weights of the used adapters, each [rows][cols] turned to [cols][rows].
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adapter_turn(const __grid_constant__ AdapterArgs q, const T *in, T *out,
+                                                         int64_t rows, int64_t cols) {
+  __shared__ T tile[32][33];
+  dependency_wait();
+  dependency_launch();
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t across = (cols + 31) / 32, r0 = blockIdx.x / across * 32, c0 = blockIdx.x % across * 32;
+  for (int u = blockIdx.y; u < q.p.head[1]; u += gridDim.y) {
+    const T *from = in + (int64_t)q.p.used[u].x * rows * cols;
+    T *to = out + (int64_t)u * rows * cols;
+#pragma unroll
+    for (int i = ty; i < 32; i += 8)
+      if (r0 + i < rows && c0 + tx < cols) tile[i][tx] = from[(r0 + i) * cols + c0 + tx];
+    __syncthreads();
+#pragma unroll
+    for (int i = ty; i < 32; i += 8)
+      if (c0 + i < cols && r0 + tx < rows) to[(c0 + i) * rows + r0 + tx] = tile[tx][i];
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ few tokens
+
+// The adapter of token t by the caller's offsets, or -1.
+__device__ __forceinline__ int adapter_of(const snack_adapter_args &a, int64_t t) {
+  const int i = request_of(a.offsets, (int)a.requests, (int32_t)t);
+  if (i < 0) return -1;
+  const int n = a.adapter[i];
+  return n >= 0 && n < a.adapters ? n : -1;
+}
+
+constexpr int kFewRanks = 16;  // ranks that a block of `few_down` sums
+
+// Block (token, 16 ranks): its warps split the row of X and of the weights.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) adapter_few_down(const __grid_constant__ AdapterArgs q) {
+  constexpr int E = 16 / sizeof(T);
+  __shared__ float part[kWarps][kFewRanks];
+  dependency_wait();
+  dependency_launch();
+  const snack_adapter_args &a = q.a;
+  const int64_t tkn = blockIdx.x, j0 = (int64_t)blockIdx.y * kFewRanks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = adapter_of(a, tkn);
+  const int ranks = (int)min((int64_t)kFewRanks, a.rank - j0);
+  float s[kFewRanks];
+#pragma unroll
+  for (int j = 0; j < kFewRanks; ++j) s[j] = 0.f;
+  if (n >= 0) {
+    const T *x = static_cast<const T *>(a.X) + tkn * a.x_stride;
+    const T *w = static_cast<const T *>(a.A) + ((int64_t)n * a.rank + j0) * a.in;
+    for (int64_t k = (int64_t)threadIdx.x * E; k < a.in; k += kThreads * E) {
+      const uint4 xv = load16<T, ALIGNED>(x, k, a.in, true);
+      uint4 wv[kFewRanks];
+#pragma unroll
+      for (int j = 0; j < kFewRanks; ++j) wv[j] = load16<T, ALIGNED>(w + (j < ranks ? j : 0) * a.in, k, a.in, j < ranks);
+#pragma unroll
+      for (int j = 0; j < kFewRanks; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          s[j] = fmaf(to_float(reinterpret_cast<const T *>(&xv)[e]), to_float(reinterpret_cast<const T *>(&wv[j])[e]), s[j]);
+    }
+  }
+  // sixteen sums over the warp: each step halves the ranks that a lane still holds
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const bool up = lane & o;
+      const float send = up ? s[j] : s[j + o], keep = up ? s[j + o] : s[j];
+      s[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
+  if (lane < kFewRanks) part[warp][lane] = s[0];
+  __syncthreads();
+  if (threadIdx.x < ranks) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
+    q.H[tkn * a.rank + j0 + threadIdx.x] = v;
+  }
+}
+
+// Block (256 columns, token): one thread for each column.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adapter_few_up(const __grid_constant__ AdapterArgs q, T *Y,
+                                                           int64_t y_stride) {
+  extern __shared__ float h[];
+  const snack_adapter_args &a = q.a;
+  dependency_wait();
+  dependency_launch();
+  const int64_t tkn = blockIdx.y, o = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int n = adapter_of(a, tkn);
+  if (n < 0) return;
+  const float scale = scale_of(a, n);
+  for (int64_t j = threadIdx.x; j < a.rank; j += kThreads) h[j] = q.H[tkn * a.rank + j] * scale;
+  __syncthreads();
+  if (o >= a.out) return;
+  T *y = Y + tkn * y_stride + o;
+  const T *w = static_cast<const T *>(a.B) + ((int64_t)n * a.out + o) * a.rank;
+  constexpr int E = 16 / sizeof(T);
+  const float y0 = to_float(*y);
+  float s = 0.f;
+  if (a.rank % E == 0 && (reinterpret_cast<uintptr_t>(a.B) & 15) == 0) {
+    for (int64_t j = 0; j < a.rank; j += E) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(w + j);
+#pragma unroll
+      for (int e = 0; e < E; ++e) s = fmaf(h[j + e], to_float(reinterpret_cast<const T *>(&v)[e]), s);
+    }
+  } else {
+    for (int64_t j = 0; j < a.rank; ++j) s = fmaf(h[j], to_float(w[j]), s);
+  }
+  *y = from_float<T>(y0 + s);
+}
+
+// ------------------------------------------------------------------ host
 
 const char *bad_args(const snack_adapter_args *a) {
   if (!a) return "args is NULL";
@@ -179,40 +1016,213 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width, int type) {
   return rows < 1 ? 0 : ((rows - 1) * stride + width) * type_bytes(type);
 }
 
+int64_t align16(int64_t b) { return (b + 15) / 16 * 16; }
+
+// Up to this many tokens are taken one by one: the weights of each are read
+// for it alone, and no plan is made.
+constexpr int64_t kFewTokens = 128;
+
+// Lays the plan out in `ws` (null: only its size).
+int64_t lay_plan(const snack_adapter_args &a, Plan *p, char *ws) {
+  p->max_used = std::min(a.adapters, std::min(a.requests, a.tokens));
+  p->max_tiles = a.tokens / kTile + p->max_used;
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    char *r = ws ? ws + at : nullptr;
+    at += align16(bytes);
+    return r;
+  };
+  p->head = reinterpret_cast<int32_t *>(take(16));
+  p->tiles = reinterpret_cast<int4 *>(take(p->max_tiles * 16));
+  p->used = reinterpret_cast<int4 *>(take(p->max_used * 16));
+  p->perm = reinterpret_cast<int32_t *>(take(a.tokens * 4));
+  p->index = reinterpret_cast<int32_t *>(take(a.adapters * 4));
+  const bool many = a.requests > kPlanThreads;
+  p->soff = reinterpret_cast<int32_t *>(take(many ? (a.requests + 1) * 4 : 0));
+  p->place = reinterpret_cast<int32_t *>(take(many ? a.requests * 4 : 0));
+  p->base = reinterpret_cast<int32_t *>(take(many ? a.adapters * 4 : 0));
+  return at;
+}
+
+cudaError_t launch_plan(const AdapterArgs &q, cudaStream_t s) {
+  const snack_adapter_args &a = q.a;
+  if (a.requests <= kPlanThreads) {
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(32, (a.tokens + kPlanThreads - 1) / kPlanThreads));
+    return launch_kernel(plan_small, dim3((unsigned)blocks), kPlanThreads, 0, true, s, q);
+  }
+  cudaError_t e = launch_kernel(plan_requests, dim3(1), kPlanThreads, 0, true, s, q);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = std::min<int64_t>((a.tokens + kThreads - 1) / kThreads, device_sms() * 8);
+  return launch_kernel(plan_tokens, dim3((unsigned)blocks), kThreads, 0, true, s, q);
+}
+
+// Raises the kernel's limit of dynamic shared memory where it is above the default.
 template <typename K>
-cudaError_t go(K kern, int64_t blocks, const AdapterArgs &q, cudaStream_t s) {
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)device_sms() * 8));
-  return launch_kernel(kern, dim3((unsigned)grid), kThreads, 0, true, s, q);
+cudaError_t allow_smem(K kern, size_t bytes) {
+  return bytes <= 48 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+bool vector_rows(const void *p, int64_t stride, int64_t width, int type) {
+  const int64_t e = 16 / type_bytes(type);
+  return aligned_to(p, 16) && width % e == 0 && stride % e == 0;
+}
+
+template <typename T, int NT>
+cudaError_t launch_down_nt(const AdapterArgs &q, const DownArgs &d, bool vec, cudaStream_t s) {
+  const dim3 grid((unsigned)q.p.max_tiles, (unsigned)((d.rank + kRankPass - 1) / kRankPass));
+  const size_t smem = sizeof(float) * kWarps * kTile * (NT * 8 + 4);
+  auto k = vec ? adapter_down<T, NT, true> : adapter_down<T, NT, false>;
+  const cudaError_t e = allow_smem(k, smem);
+  return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
 }
 
 template <typename T>
-cudaError_t forward(const AdapterArgs &q, cudaStream_t s) {
-  cudaError_t e = go(adapter_down<T>, (q.a.tokens * q.a.rank + 7) / 8, q, s);
-  return e != cudaSuccess ? e : go(adapter_up<T>, q.a.tokens, q, s);
+cudaError_t launch_down(const AdapterArgs &q, const DownArgs &d, cudaStream_t s) {
+  if (q.p.max_tiles == 0) return cudaSuccess;
+  const bool vec = vector_rows(d.X, d.x_stride, d.K, q.a.type) && aligned_to(d.W, 16);
+  if (d.rank <= 8) return launch_down_nt<T, 1>(q, d, vec, s);
+  if (d.rank <= 16) return launch_down_nt<T, 2>(q, d, vec, s);
+  if (d.rank <= 32) return launch_down_nt<T, 4>(q, d, vec, s);
+  return launch_down_nt<T, 8>(q, d, vec, s);
 }
 
 template <typename T>
-cudaError_t backward(const AdapterArgs &q, cudaStream_t s) {
+cudaError_t launch_up(const AdapterArgs &q, UpArgs d, cudaStream_t s) {
+  if (q.p.max_tiles == 0) return cudaSuccess;
+  using S = UpShape<T>;
+  const int64_t cols = (int64_t)kWarps * S::GROUPS * S::COLS;
+  d.blocks = (d.K + cols - 1) / cols;
+  if (q.p.max_tiles * d.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(q.p.max_tiles * d.blocks));
+  const size_t smem = (size_t)((d.rank + 15) / 16) * (kTile / 16) * 2 * (sizeof(T) == 4 ? 2 : 1) * 32 * 16;
+  auto k = vector_rows(d.Y, d.y_stride, d.K, q.a.type) ? adapter_up<T, true> : adapter_up<T, false>;
+  const cudaError_t e = allow_smem(k, smem);
+  return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
+}
+
+// Places of one block of `outer`: blocks enough to fill the GPU three times,
+// at least 64 places (below it the parts cost more than the split gains),
+// at most 512 (their H lies in shared memory: 80 KB at 32 ranks).
+int64_t outer_chunk(const snack_adapter_args &a, int64_t K) {
+  const int64_t cols = kWarps * 8 * (16 / type_bytes(a.type)), ranks = outer_ranks(a.rank);
+  const int64_t blocks = (K + cols - 1) / cols * ((a.rank + ranks - 1) / ranks);
+  const int64_t split = std::max<int64_t>(1, (int64_t)device_sms() * 3 / blocks);
+  const int64_t c = (a.tokens + split - 1) / split;
+  return std::max<int64_t>(64, std::min<int64_t>(512, (c + 31) / 32 * 32));
+}
+
+int64_t outer_bytes(const snack_adapter_args &a, int64_t K) {
+  const int64_t chunk = outer_chunk(a, K), used = std::min(a.adapters, std::min(a.requests, a.tokens));
+  return align16(((a.tokens + chunk - 1) / chunk + used) * a.rank * K * 4);
+}
+
+template <typename T, bool TRANSPOSE>
+cudaError_t launch_outer(const AdapterArgs &q, OuterArgs d, T *out, bool scaled, cudaStream_t s) {
+  const snack_adapter_args &a = q.a;
+  d.chunk = outer_chunk(a, d.K);
+  const int64_t cols = kWarps * 8 * (16 / (int64_t)sizeof(T)), ranks = outer_ranks(a.rank);
+  d.blocks = (d.K + cols - 1) / cols;
+  const int64_t slices = (a.tokens + d.chunk - 1) / d.chunk;
+  if (slices * d.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(slices * d.blocks), (unsigned)((a.rank + ranks - 1) / ranks));
   cudaError_t e = cudaSuccess;
-  if (q.a.tokens > 0) e = go(adapter_back_rank<T>, (q.a.tokens * q.a.rank + 7) / 8, q, s);
-  if (e == cudaSuccess && q.dX && q.a.tokens > 0) e = go(adapter_back_input<T>, q.a.tokens, q, s);
-  const int64_t per = q.a.adapters * q.a.rank;
-  if (e == cudaSuccess && q.dA && per > 0)
-    e = go(adapter_back_weights<T, false>, (per * q.a.in + kThreads - 1) / kThreads, q, s);
-  if (e == cudaSuccess && q.dB && per > 0)
-    e = go(adapter_back_weights<T, true>, (per * q.a.out + kThreads - 1) / kThreads, q, s);
-  return e;
+  if (q.p.max_used > 0) {
+    const bool vec = vector_rows(d.X, d.x_stride, d.K, a.type);
+    auto k = ranks == 16 ? (vec ? adapter_outer<T, 1, true> : adapter_outer<T, 1, false>)
+                         : (vec ? adapter_outer<T, 2, true> : adapter_outer<T, 2, false>);
+    const size_t smem = (size_t)d.chunk * (ranks + 8 + 1) * 4;
+    if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
+    if ((e = launch_kernel(k, grid, kThreads, smem, true, s, q, d)) != cudaSuccess) return e;
+  }
+  const int64_t total = a.adapters * a.rank * d.K;
+  const int64_t blocks = std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)device_sms() * 8);
+  return launch_kernel(adapter_outer_finish<T, TRANSPOSE>, dim3((unsigned)blocks), kThreads, 0, true, s, q, d, out,
+                       scaled);
 }
 
-#define SNACK_TYPES(type, F)                       \
-  ((type) == SNACK_F32 ? F<float>(q, s) : (type) == SNACK_BF16 ? F<__nv_bfloat16>(q, s) : F<__half>(q, s))
+template <typename T>
+cudaError_t launch_turn(const AdapterArgs &q, const void *in, void *out, int64_t rows, int64_t cols, cudaStream_t s) {
+  if (q.p.max_used == 0) return cudaSuccess;
+  const int64_t blocks = (rows + 31) / 32 * ((cols + 31) / 32);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(q.p.max_used, 65535));
+  return launch_kernel(adapter_turn<T>, grid, kThreads, 0, true, s, q, static_cast<const T *>(in),
+                       static_cast<T *>(out), rows, cols);
+}
+
+template <typename T>
+cudaError_t forward(const AdapterArgs &q, void *Y, int64_t y_stride, cudaStream_t s) {
+  const snack_adapter_args &a = q.a;
+  if (a.tokens <= kFewTokens) {
+    const dim3 grid((unsigned)a.tokens, (unsigned)((a.rank + kFewRanks - 1) / kFewRanks));
+    auto k = vector_rows(a.X, a.x_stride, a.in, a.type) && aligned_to(a.A, 16) ? adapter_few_down<T, true>
+                                                                                : adapter_few_down<T, false>;
+    cudaError_t e = launch_kernel(k, grid, kThreads, 0, true, s, q);
+    if (e != cudaSuccess) return e;
+    const dim3 up((unsigned)((a.out + kThreads - 1) / kThreads), (unsigned)a.tokens);
+    return launch_kernel(adapter_few_up<T>, up, kThreads, (size_t)a.rank * 4, true, s, q, static_cast<T *>(Y),
+                         y_stride);
+  }
+  cudaError_t e = launch_plan(q, s);
+  if (e != cudaSuccess) return e;
+  const DownArgs d = {a.X, a.A, a.x_stride, a.in, a.rank, false, false, q.H};
+  if ((e = launch_down<T>(q, d, s)) != cudaSuccess) return e;
+  const UpArgs u = {q.H, a.B, Y, y_stride, a.out, a.rank, false, true, 0};
+  return launch_up<T>(q, u, s);
+}
+
+struct Back {
+  const void *dY;
+  int64_t dy_stride;
+  const float *H;
+  void *dX;
+  int64_t dx_stride;
+  void *dA, *dB;
+  float *dH;      // [tokens][rank]
+  void *At, *Bt;  // [used][in][rank], [used][rank][out]
+  float *parts;
+};
+
+template <typename T>
+cudaError_t backward(const AdapterArgs &q, const Back &b, cudaStream_t s) {
+  const snack_adapter_args &a = q.a;
+  cudaError_t e = launch_plan(q, s);
+  if (e != cudaSuccess) return e;
+  if (b.dX || b.dA) {
+    if ((e = launch_turn<T>(q, a.B, b.Bt, a.out, a.rank, s)) != cudaSuccess) return e;
+    const DownArgs d = {b.dY, b.Bt, b.dy_stride, a.out, a.rank, true, true, b.dH};
+    if ((e = launch_down<T>(q, d, s)) != cudaSuccess) return e;
+  }
+  if (b.dB) {
+    const OuterArgs o = {b.H, b.dY, b.dy_stride, a.out, a.rank, 0, 0, b.parts};
+    if ((e = launch_outer<T, true>(q, o, static_cast<T *>(b.dB), true, s)) != cudaSuccess) return e;
+  }
+  if (b.dX) {
+    if ((e = launch_turn<T>(q, a.A, b.At, a.rank, a.in, s)) != cudaSuccess) return e;
+    const UpArgs u = {b.dH, b.At, b.dX, b.dx_stride, a.in, a.rank, true, false, 0};
+    if ((e = launch_up<T>(q, u, s)) != cudaSuccess) return e;
+  }
+  if (b.dA) {
+    const OuterArgs o = {b.dH, a.X, a.x_stride, a.in, a.rank, 0, 0, b.parts};
+    if ((e = launch_outer<T, false>(q, o, static_cast<T *>(b.dA), false, s)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+#define SNACK_TYPES(type, F, ...)                                                     \
+  ((type) == SNACK_F32 ? F<float>(__VA_ARGS__) : (type) == SNACK_BF16 ? F<__nv_bfloat16>(__VA_ARGS__) \
+                                                                      : F<__half>(__VA_ARGS__))
 
 }  // namespace
 }  // namespace snack
 
 extern "C" size_t snack_adapter_forward_workspace(const snack_adapter_args *args) {
-  (void)args;
-  return 16;
+  using namespace snack;
+  if (bad_args(args) || args->tokens <= kFewTokens) return 16;
+  Plan p;
+  return (size_t)lay_plan(*args, &p, nullptr);
 }
 
 extern "C" snack_status snack_adapter_forward(const snack_adapter_args *args, void *Y, int64_t y_stride,
@@ -229,18 +1239,44 @@ extern "C" snack_status snack_adapter_forward(const snack_adapter_args *args, vo
     return refuse(SNACK_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
   if (overlap(a.X, rows_bytes(a.tokens, a.x_stride, a.in, a.type), Y, rows_bytes(a.tokens, y_stride, a.out, a.type)))
     return refuse(SNACK_ERR_INVALID_ARG, "Y overlaps X");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   AdapterArgs q = {};
   q.a = a;
-  q.Y = Y;
-  q.y_stride = y_stride;
   q.H = H;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = SNACK_TYPES(a.type, forward);
+  lay_plan(a, &q.p, static_cast<char *>(workspace));
+  const cudaError_t e = SNACK_TYPES(a.type, forward, q, Y, y_stride, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "adapter launch");
 }
 
+namespace snack {
+namespace {
+
+// The backward's scratch: the plan, dH, turned weights of the used adapters,
+// parts of dA or dB (one after the other).
+int64_t lay_back(const snack_adapter_args &a, Plan *p, Back *b, char *ws) {
+  int64_t at = lay_plan(a, p, ws);
+  const auto take = [&](int64_t bytes) {
+    char *r = ws ? ws + at : nullptr;
+    at += align16(bytes);
+    return r;
+  };
+  const int64_t e = type_bytes(a.type);
+  b->dH = reinterpret_cast<float *>(take(a.tokens * a.rank * 4));
+  b->At = take(p->max_used * a.in * a.rank * e);
+  b->Bt = take(p->max_used * a.out * a.rank * e);
+  b->parts = reinterpret_cast<float *>(take(std::max(outer_bytes(a, a.in), outer_bytes(a, a.out))));
+  return at;
+}
+
+}  // namespace
+}  // namespace snack
+
 extern "C" size_t snack_adapter_backward_workspace(const snack_adapter_args *args) {
-  return snack::bad_args(args) ? 16 : (size_t)(args->tokens * args->rank * 4 + 16);
+  using namespace snack;
+  if (bad_args(args)) return 16;
+  Plan p;
+  Back b;
+  return (size_t)lay_back(*args, &p, &b, nullptr);
 }
 
 extern "C" snack_status snack_adapter_backward(const snack_adapter_args *args, const void *dY,
@@ -261,17 +1297,25 @@ extern "C" snack_status snack_adapter_backward(const snack_adapter_args *args, c
   if (overlap(a.X, rows_bytes(a.tokens, a.x_stride, a.in, a.type), dX, dxb) ||
       overlap(dY, rows_bytes(a.tokens, dy_stride, a.out, a.type), dX, dxb))
     return refuse(SNACK_ERR_INVALID_ARG, "dX overlaps X or dY");
-  AdapterArgs q = {};
-  q.a = a;
-  q.dY = dY;
-  q.dy_stride = dy_stride;
-  q.dX = dX;
-  q.dx_stride = dx_stride;
-  q.Hin = H;
-  q.dA = dA;
-  q.dB = dB;
-  q.dH = static_cast<float *>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = SNACK_TYPES(a.type, backward);
+  if (a.adapters == 0) return SNACK_OK;
+  if (a.tokens == 0 || a.requests == 0) {
+    cudaError_t e = cudaSuccess;
+    if (dA) e = cudaMemsetAsync(dA, 0, (size_t)(a.adapters * a.rank * a.in * e0), s);
+    if (dB && e == cudaSuccess) e = cudaMemsetAsync(dB, 0, (size_t)(a.adapters * a.rank * a.out * e0), s);
+    return e == cudaSuccess ? SNACK_OK : cuda_status(e, "adapter gradients");
+  }
+  AdapterArgs q = {};
+  Back b = {};
+  q.a = a;
+  lay_back(a, &q.p, &b, static_cast<char *>(workspace));
+  b.dY = dY;
+  b.dy_stride = dy_stride;
+  b.H = H;
+  b.dX = dX;
+  b.dx_stride = dx_stride;
+  b.dA = dA;
+  b.dB = dB;
+  const cudaError_t e = SNACK_TYPES(a.type, backward, q, b, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "adapter backward launch");
 }

@@ -164,7 +164,7 @@ __device__ __forceinline__ void scale_chunk(const S *p, D *q, int n, float coef)
     for (int i = tid; i < nv; i += kThreads) {
       Vec<S> v;
       v.load(p + (int64_t)i * V);
-      D out[V];
+      alignas(16) D out[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) out[j] = from_float<D>(v.get(j) * coef);
       D *at = q + (int64_t)i * V;
