@@ -18,8 +18,12 @@
 // Operands go from memory straight into the registers that the matrix
 // instruction wants them in.  The order in which the summed index is fed to
 // it is free as long as both operands keep it, so a lane takes 16 contiguous
-// bytes of a row and the four lanes of a row take 64: no shared memory and
-// no barrier stands between a load and its product.  fp32 operands are split
+// bytes of a row and the four lanes of a row take 64.  A lane's rows come by
+// asynchronous copies into slots of shared memory that it alone reads: they
+// are registers that can wait for memory, several steps ahead, and need no
+// barrier.  (Loads into registers left 64 bytes in flight per lane at one
+// block per SM: 47 us for `down` and 80 us for `outer` over 134 MB.)
+// fp32 operands are split
 // into two tf32 parts, x = hi + lo, and hi*hi + hi*lo + lo*hi is summed:
 // what is left out is below 2^-22 of a product.  Running sums leave the
 // matrix unit's accumulator every few steps for a 32-bit sum that rounds to
@@ -359,6 +363,28 @@ __device__ __forceinline__ uint4 load16(const T *row, int64_t k, int64_t limit, 
   return v;
 }
 
+// The same copied asynchronously into a slot of shared memory (16-byte
+// aligned rows); what is not there arrives as 0.
+template <typename T>
+__device__ __forceinline__ void copy16(uint4 *slot, const T *row, int64_t k, int64_t limit, bool valid) {
+  const bool in = valid && k < limit;
+  const T *from = in ? row + k : row;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(slot)),
+               "l"(from), "r"(in ? 16 : 0)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy8(uint2 *slot, const T *row, int64_t k, int64_t limit, bool valid) {
+  const bool in = valid && k < limit;
+  const T *from = in ? row + k : row;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(slot)),
+               "l"(from), "r"(in ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // One group of the summed index (64 bytes of a row: 16 fp32 or 32 16-bit
 // elements) of a 16 x 8 product: rows g and g + 8 in v0 and v1, the other
 // operand's row g in w.
@@ -388,15 +414,28 @@ struct DownArgs {
   float *H;           // [tokens][rank]
 };
 
-// Block: one tile of kTile tokens, ranks [64 z, 64 z + 64).  Its warps take
-// every eighth run of U groups of K and meet in shared memory.
+// Steps that a lane's copies run ahead: about 96 KB a block, two blocks an SM.
+template <int NT>
+struct DownShape {
+  static constexpr int SLOTS = 2 * (kTile / 16) + NT;  // 16-byte slots of a lane and step
+  static constexpr int STAGES = NT <= 2 ? 4 : (NT == 4 ? 3 : 2);
+  static constexpr int LD = NT * 8 + 4;
+  static constexpr size_t RING = (size_t)kWarps * STAGES * SLOTS * 32 * 16;
+  static constexpr size_t PART = sizeof(float) * kWarps * kTile * LD;
+  static constexpr size_t SMEM = RING > PART ? RING : PART;
+};
+
+// Block: one tile of kTile tokens, ranks [64 y, 64 y + 64).  Its warps take
+// pairs of groups of K (128 bytes of each row) in turn and meet in shared
+// memory at the end.
 template <typename T, int NT, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) adapter_down(const __grid_constant__ AdapterArgs q,
-                                                         const __grid_constant__ DownArgs d) {
+__global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const __grid_constant__ AdapterArgs q,
+                                                                         const __grid_constant__ DownArgs d) {
+  using S = DownShape<NT>;
   constexpr int MT = kTile / 16, E = Group<T>::E, KG = Group<T>::K;
-  constexpr int U = NT <= 2 ? 4 : 2;
-  constexpr int kCols = NT * 8;
-  extern __shared__ float part[];  // [kWarps][kTile][kCols + 4]
+  constexpr int kCols = NT * 8, STAGES = S::STAGES, SLOTS = S::SLOTS;
+  extern __shared__ uint4 smem4[];
+  float *part = reinterpret_cast<float *>(smem4);  // [kWarps][kTile][LD], over the ring
   dependency_wait();
   dependency_launch();
   if ((int)blockIdx.x >= q.p.head[0]) return;
@@ -411,77 +450,101 @@ __global__ void __launch_bounds__(kThreads) adapter_down(const __grid_constant__
     ok[m] = i < tile.z;
     rows[m] = static_cast<const T *>(d.X) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.x_stride : 0);
   }
-  const T *wrow[NT];
-  bool wok[NT];
   const int64_t wbase = (int64_t)(d.by_used ? tile.w : tile.x) * d.rank;
+  const T *wrow = static_cast<const T *>(d.W) + (wbase + min(j0 + g, d.rank - 1)) * d.K;
+  const int ranks_left = (int)min((int64_t)kRankPass, d.rank - j0) - g;  // row n * 8 + g is there: n * 8 < ranks_left
+  uint4 *ring = smem4 + (int64_t)warp * STAGES * SLOTS * 32 + lane;
+
+  // step i of this warp: group ((i / 2) * kWarps + warp) * 2 + i % 2
+  const int groups = (int)((d.K + KG - 1) / KG);
+  const auto group_of = [&](int i) { return ((i >> 1) * kWarps + warp) * 2 + (i & 1); };
+  const int steps = [&] {  // steps whose group is there
+    const int whole = groups / (2 * kWarps) * 2, rest = groups % (2 * kWarps) - 2 * warp;
+    return whole + (rest <= 0 ? 0 : (rest >= 2 ? 2 : rest));
+  }();
+  const auto fetch = [&](int i) {
+    if (ALIGNED && i < steps) {
+      const int64_t k = (int64_t)group_of(i) * KG + t * E;
+      uint4 *slot = ring + (i % STAGES) * SLOTS * 32;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int64_t j = j0 + n * 8 + g;
-    wok[n] = j < d.rank;
-    wrow[n] = static_cast<const T *>(d.W) + (wok[n] ? (wbase + j) * d.K : 0);
-  }
-  float sum[MT][NT][4];
+      for (int m = 0; m < 2 * MT; ++m) copy16(slot + m * 32, rows[m], k, d.K, ok[m]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        copy16(slot + (2 * MT + n) * 32, wrow + (n * 8 < ranks_left ? (int64_t)n * 8 * d.K : 0), k, d.K, n * 8 < ranks_left);
+    }
+    if (ALIGNED) copies_commit();
+  };
+  float sum[MT][NT][4], acc[MT][NT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
-
-  for (int64_t k0 = (int64_t)warp * U * KG; k0 < d.K; k0 += (int64_t)kWarps * U * KG) {
-    uint4 x[U][2 * MT], w[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = k0 + u * KG + t * E;
-#pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) x[u][m] = load16<T, ALIGNED>(rows[m], k, d.K, ok[m]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) w[u][n] = load16<T, ALIGNED>(wrow[n], k, d.K, wok[n]);
-    }
-    float acc[MT][NT][4];
+      for (int i = 0; i < 4; ++i) sum[m][n][i] = acc[m][n][i] = 0.f;
+  const auto flush = [&] {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if constexpr (sizeof(T) == 4) {
-        float xh[2 * MT][4], xl[2 * MT][4];
-#pragma unroll
-        for (int m = 0; m < 2 * MT; ++m) split4(x[u][m], xh[m], xl[m]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float wh[4], wl[4];
-          split4(w[u][n], wh, wl);
-#pragma unroll
-          for (int s = 0; s < 4; s += 2)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma_tf32(acc[m][n], xl[2 * m][s], xl[2 * m + 1][s], xl[2 * m][s + 1], xl[2 * m + 1][s + 1], wh[s], wh[s + 1]);
-              mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wl[s], wl[s + 1]);
-              mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wh[s], wh[s + 1]);
-            }
+        for (int i = 0; i < 4; ++i) {
+          sum[m][n][i] += acc[m][n][i];
+          acc[m][n][i] = 0.f;
         }
-      } else {
+  };
+
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  for (int i = 0; i < steps; ++i) {
+    uint4 x[2 * MT], w[NT];
+    if (ALIGNED) {
+      copies_wait<STAGES - 2>();
+      const uint4 *slot = ring + (i % STAGES) * SLOTS * 32;
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m) x[m] = slot[m * 32];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) w[n] = slot[(2 * MT + n) * 32];
+      fetch(i + STAGES - 1);  // into the slots that step i - 1 has read
+    } else {
+      const int64_t k = (int64_t)group_of(i) * KG + t * E;
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m) x[m] = load16<T, false>(rows[m], k, d.K, ok[m]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        w[n] = load16<T, false>(wrow + (n * 8 < ranks_left ? (int64_t)n * 8 * d.K : 0), k, d.K, n * 8 < ranks_left);
+    }
+    if constexpr (sizeof(T) == 4) {
+      float xh[2 * MT][4], xl[2 * MT][4];
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m) split4(x[m], xh[m], xl[m]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float wh[4], wl[4];
+        split4(w[n], wh, wl);
+#pragma unroll
+        for (int s = 0; s < 4; s += 2)
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            mma_16<T>(acc[m][n], x[u][2 * m].x, x[u][2 * m + 1].x, x[u][2 * m].y, x[u][2 * m + 1].y, w[u][n].x, w[u][n].y);
-            mma_16<T>(acc[m][n], x[u][2 * m].z, x[u][2 * m + 1].z, x[u][2 * m].w, x[u][2 * m + 1].w, w[u][n].z, w[u][n].w);
+            mma_tf32(acc[m][n], xl[2 * m][s], xl[2 * m + 1][s], xl[2 * m][s + 1], xl[2 * m + 1][s + 1], wh[s], wh[s + 1]);
+            mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wl[s], wl[s + 1]);
+            mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wh[s], wh[s + 1]);
           }
       }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
+    } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[m][n][i] += acc[m][n][i];
+        for (int m = 0; m < MT; ++m) {
+          mma_16<T>(acc[m][n], x[2 * m].x, x[2 * m + 1].x, x[2 * m].y, x[2 * m + 1].y, w[n].x, w[n].y);
+          mma_16<T>(acc[m][n], x[2 * m].z, x[2 * m + 1].z, x[2 * m].w, x[2 * m + 1].w, w[n].z, w[n].w);
+        }
+    }
+    if ((i & 3) == 3) flush();
   }
-  constexpr int LD = kCols + 4;
+  flush();
+  copies_wait<0>();
+  __syncthreads();
+  constexpr int LD = S::LD;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -519,9 +582,18 @@ struct UpArgs {
 template <typename T>
 struct UpShape {
   static constexpr int E = 16 / sizeof(T);
-  static constexpr int NT = E / 2;       // 8-column products side by side
-  static constexpr int COLS = 4 * E;     // 16 or 32
-  static constexpr int GROUPS = 4;       // column groups of a warp
+  static constexpr int NT = E / 2;                          // 8-column products side by side
+  static constexpr int COLS = 4 * E;                        // 16 or 32
+  static constexpr int GROUPS = 8;                          // column groups of a warp
+  static constexpr int PER = sizeof(T) == 4 ? 2 : 1;        // instructions for 16 ranks
+  static constexpr int WBYTES = 4 * sizeof(T);              // four ranks of a weight row
+  // bytes of a warp's step: its rows of Y, and the weights of RG times 16 ranks
+  __host__ __device__ static constexpr int step_bytes(int rg) { return 2 * (kTile / 16) * 512 + NT * rg * 32 * WBYTES; }
+  __host__ __device__ static constexpr int stages(int rg) { return rg == 2 ? 3 : 4; }
+  __host__ __device__ static constexpr size_t frag_bytes(int64_t rank) { return (size_t)((rank + 15) / 16) * (kTile / 16) * 2 * PER * 512; }
+  __host__ __device__ static constexpr size_t smem(int rg, int64_t rank) {
+    return frag_bytes(rank) + (size_t)kWarps * stages(rg) * step_bytes(rg);
+  }
 };
 
 // Four ranks of a weight row as the B operand of one or two instructions.
@@ -545,21 +617,66 @@ __device__ __forceinline__ void load_ranks(const T *row, int64_t j, int64_t rank
 
 // Block: one tile of kTile tokens, kWarps * GROUPS column groups.  The
 // tile's H is kept in shared memory, split in two parts, in the order in
-// which the lanes want it.
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ AdapterArgs q,
-                                                       const __grid_constant__ UpArgs d) {
+// which the lanes want it.  RG: 16-rank groups (1 or 2, weights copied ahead
+// with the rows; 0: any number, weights loaded when they are needed).
+template <typename T, int RG, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant__ AdapterArgs q,
+                                                          const __grid_constant__ UpArgs d) {
   using S = UpShape<T>;
-  constexpr int MT = kTile / 16, E = S::E, NT = S::NT;
-  extern __shared__ uint4 frag[];  // [16-rank groups][MT][2 (high and low)][16-bit: 1, fp32: 2][32 lanes]
-  constexpr int PER = sizeof(T) == 4 ? 2 : 1;
+  constexpr int MT = kTile / 16, E = S::E, NT = S::NT, PER = S::PER, STAGES = S::stages(RG);
+  constexpr bool AHEAD = ALIGNED && RG > 0;  // rows and weights both in vectors
+  extern __shared__ uint4 frag[];            // [16-rank groups][MT][2 (high and low)][PER][32 lanes], then the rings
   dependency_wait();
   dependency_launch();
   const int64_t which = blockIdx.x / d.blocks, cblock = blockIdx.x % d.blocks;
   if (which >= q.p.head[0]) return;
   const int4 tile = q.p.tiles[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int rg = (int)((d.rank + 15) / 16);
+  const int rg = RG > 0 ? RG : (int)((d.rank + 15) / 16);
+  T *rows[2 * MT];
+  bool ok[2 * MT];
+#pragma unroll
+  for (int m = 0; m < 2 * MT; ++m) {
+    const int i = m * 8 + g;
+    ok[m] = i < tile.z;
+    rows[m] = static_cast<T *>(d.Y) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.y_stride : 0);
+  }
+  const T *W = static_cast<const T *>(d.W) + (int64_t)(d.by_used ? tile.w : tile.x) * d.K * d.rank;
+  const int64_t first = (cblock * S::GROUPS * kWarps + warp) * S::COLS;
+  const auto column = [&](int c) { return first + (int64_t)c * kWarps * S::COLS; };
+  // column of product n's index g: the lane that ends up with columns 2t and
+  // 2t + 1 of every n holds E columns in a row
+  const int gcol = (g >> 1) * E + (g & 1);
+  char *ring = reinterpret_cast<char *>(frag) + S::frag_bytes(d.rank) + (size_t)warp * STAGES * S::step_bytes(RG);
+  const auto fetch = [&](int c) {
+    if (!ALIGNED) return;
+    const int64_t c0 = column(c);
+    if (c < S::GROUPS && c0 < d.K) {
+      char *at = ring + (c % STAGES) * S::step_bytes(RG);
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m)
+        copy16(reinterpret_cast<uint4 *>(at) + m * 32 + lane, rows[m], c0 + t * E, d.K, ok[m]);
+      if (AHEAD) {
+        at += 2 * MT * 512;
+#pragma unroll
+        for (int k = 0; k < RG; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int64_t col = c0 + gcol + 2 * n;
+            const T *row = W + (col < d.K ? col * d.rank : 0);
+            char *slot = at + ((k * NT + n) * 32 + lane) * S::WBYTES;
+            if constexpr (sizeof(T) == 4)
+              copy16(reinterpret_cast<uint4 *>(slot), row, k * 16 + 4 * t, d.rank, col < d.K);
+            else
+              copy8(reinterpret_cast<uint2 *>(slot), row, k * 16 + 4 * t, d.rank, col < d.K);
+          }
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int c = 0; c < STAGES - 1; ++c) fetch(c);
+
   const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
   for (int i = warp; i < rg * MT; i += kWarps) {
     const int m = i % MT, k = i / MT;
@@ -601,24 +718,21 @@ __global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ A
       to[32] = lo;
     }
   }
-  T *rows[2 * MT];
-  bool ok[2 * MT];
-#pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) {
-    const int i = m * 8 + g;
-    ok[m] = i < tile.z;
-    rows[m] = static_cast<T *>(d.Y) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.y_stride : 0);
-  }
   __syncthreads();
-  const T *W = static_cast<const T *>(d.W) + (int64_t)(d.by_used ? tile.w : tile.x) * d.K * d.rank;
   const bool wvec = d.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(d.W) & (4 * sizeof(T) - 1)) == 0;
-#pragma unroll 2
   for (int c = 0; c < S::GROUPS; ++c) {
-    const int64_t c0 = ((cblock * S::GROUPS + c) * kWarps + warp) * S::COLS;
+    const int64_t c0 = column(c);
     if (c0 >= d.K) break;
     uint4 y[2 * MT];
+    const char *at = ring + (c % STAGES) * S::step_bytes(RG);
+    if (ALIGNED) {
+      copies_wait<STAGES - 2>();
 #pragma unroll
-    for (int m = 0; m < 2 * MT; ++m) y[m] = load16<T, ALIGNED>(rows[m], c0 + t * E, d.K, ok[m]);
+      for (int m = 0; m < 2 * MT; ++m) y[m] = reinterpret_cast<const uint4 *>(at)[m * 32 + lane];
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2 * MT; ++m) y[m] = load16<T, false>(rows[m], c0 + t * E, d.K, ok[m]);
+    }
     float acc[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -626,15 +740,22 @@ __global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ A
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll(RG > 0 ? RG : 1)
     for (int k = 0; k < rg; ++k) {
       const uint4 *from = frag + (int64_t)k * MT * 2 * PER * 32 + lane;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        // column of the product's index g: the lane that ends up with columns
-        // 2t and 2t + 1 of every n holds E columns in a row
-        const int64_t col = c0 + (g >> 1) * E + 2 * n + (g & 1);
         alignas(16) T w[4];
-        load_ranks(W + (col < d.K ? col * d.rank : 0), (int64_t)k * 16 + 4 * t, d.rank, wvec, col < d.K, w);
+        if (AHEAD) {
+          const char *slot = at + 2 * MT * 512 + ((k * NT + n) * 32 + lane) * S::WBYTES;
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(slot);
+          else
+            *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(slot);
+        } else {
+          const int64_t col = c0 + gcol + 2 * n;
+          load_ranks(W + (col < d.K ? col * d.rank : 0), (int64_t)k * 16 + 4 * t, d.rank, wvec, col < d.K, w);
+        }
         if constexpr (sizeof(T) == 4) {
           float wh[4], wl[4];
           split4(*reinterpret_cast<const uint4 *>(w), wh, wl);
@@ -659,6 +780,7 @@ __global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ A
         }
       }
     }
+    fetch(c + STAGES - 1);  // into the slots that step c - 1 has read
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -680,6 +802,7 @@ __global__ void __launch_bounds__(kThreads) adapter_up(const __grid_constant__ A
         }
       }
   }
+  copies_wait<0>();
 }
 
 // ------------------------------------------------------------------ outer: sum_t h[t] x[t]^T
@@ -693,19 +816,27 @@ struct OuterArgs {
   float *parts;     // [chunk index + used index][rank][K]
 };
 
+// A lane's copies: 8 KB of rows for a warp.
+template <typename T>
+struct OuterShape {
+  static constexpr int STAGES = sizeof(T) == 4 ? 8 : 4;
+  static constexpr int RING = kWarps * 512;  // 16-byte slots of all warps
+};
+
 // Block: kWarps * (128 bytes of columns), one chunk of places, 16 * RM
 // ranks.  A chunk may hold the end of one adapter and the beginning of
 // others: each leaves a part of its own, in the slot chunk + index among
 // the used.  The chunk's H lies in shared memory, a token every LD floats:
 // lane (g, t) reads rank g of token t, bank 8 t + g.
 template <typename T, int RM, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) adapter_outer(const __grid_constant__ AdapterArgs q,
+__global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_constant__ AdapterArgs q,
                                                           const __grid_constant__ OuterArgs d) {
   constexpr int E = 16 / sizeof(T), NT = E, COLS = 8 * E, LD = 16 * RM + 8;
   constexpr int TS = sizeof(T) == 4 ? 8 : 16;  // tokens of a step
-  constexpr int U = sizeof(T) == 4 ? 4 : 2;    // steps whose rows are loaded together
-  constexpr int NR = TS / 4;
-  extern __shared__ float hs[];  // [chunk][LD], then the chunk's tokens
+  constexpr int NR = TS / 4, STAGES = OuterShape<T>::STAGES;
+  constexpr int FLUSH = 32 / TS;               // steps between two sums outside the matrix unit
+  extern __shared__ uint4 smem4[];             // the warps' rings, [chunk][LD] floats of H, the chunk's tokens
+  float *hs = reinterpret_cast<float *>(smem4 + OuterShape<T>::RING);
   int32_t *tok = reinterpret_cast<int32_t *>(hs + d.chunk * LD);
   dependency_wait();
   dependency_launch();
@@ -725,6 +856,7 @@ __global__ void __launch_bounds__(kThreads) adapter_outer(const __grid_constant_
   const int64_t c0 = (cblock * kWarps + warp) * COLS, col = c0 + g * E;
   if (c0 >= d.K) return;
   const T *X = static_cast<const T *>(d.X);
+  uint4 *ring = smem4 + warp * STAGES * NR * 32 + lane;
   // the first adapter of the chunk: the last used one that begins at or before p0
   int u = 0;
   {
@@ -748,83 +880,104 @@ __global__ void __launch_bounds__(kThreads) adapter_outer(const __grid_constant_
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
-    for (; p < end; p += U * TS) {
-      uint4 x[U][NR];
+    float acc[RM][NT][4];
 #pragma unroll
-      for (int s = 0; s < U; ++s)
+    for (int m = 0; m < RM; ++m)
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          // rows of a step: fp32 t and t + 4; 16-bit 2t, 2t + 1, 2t + 8, 2t + 9
-          const int k = p + s * TS + (sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1));
-          x[s][i] = load16<T, ALIGNED>(X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K, k < end);
-        }
-      float acc[RM][NT][4];
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    const auto flush = [&] {
 #pragma unroll
       for (int m = 0; m < RM; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-#pragma unroll
-      for (int s = 0; s < U; ++s) {
-        float h[NR][2 * RM];
+          for (int i = 0; i < 4; ++i) {
+            sum[m][n][i] += acc[m][n][i];
+            acc[m][n][i] = 0.f;
+          }
+    };
+    // rows of a step: fp32 t and t + 4; 16-bit 2t, 2t + 1, 2t + 8, 2t + 9
+    const auto place = [&](int step, int i) {
+      return p + step * TS + (sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1));
+    };
+    const int steps = (end - p + TS - 1) / TS;
+    const auto fetch = [&](int step) {
+      if (!ALIGNED) return;
+      if (step < steps)
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          const int k = p + s * TS + (sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1));
-#pragma unroll
-          for (int m = 0; m < 2 * RM; ++m) h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
+          const int k = place(step, i);
+          copy16(ring + ((step % STAGES) * NR + i) * 32, X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K,
+                 k < end);
         }
-        if constexpr (sizeof(T) == 4) {
-          float xh[2][4], xl[2][4];
-          split4(x[s][0], xh[0], xl[0]);
-          split4(x[s][1], xh[1], xl[1]);
+      copies_commit();
+    };
 #pragma unroll
-          for (int m = 0; m < RM; ++m) {
-            float hh[4], hl[4];
-            const float v[4] = {h[0][2 * m], h[0][2 * m + 1], h[1][2 * m], h[1][2 * m + 1]};
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+    for (int step = 0; step < steps; ++step) {
+      uint4 x[NR];
+      float h[NR][2 * RM];
+      if (ALIGNED) copies_wait<STAGES - 2>();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              hh[i] = tf32_of(v[i]);
-              hl[i] = v[i] - hh[i];
-            }
+      for (int i = 0; i < NR; ++i) {
+        const int k = place(step, i);
+        if (ALIGNED)
+          x[i] = ring[((step % STAGES) * NR + i) * 32];
+        else
+          x[i] = load16<T, false>(X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K, k < end);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_tf32(acc[m][n], hl[0], hl[1], hl[2], hl[3], xh[0][n], xh[1][n]);
-              mma_tf32(acc[m][n], hh[0], hh[1], hh[2], hh[3], xl[0][n], xl[1][n]);
-              mma_tf32(acc[m][n], hh[0], hh[1], hh[2], hh[3], xh[0][n], xh[1][n]);
-            }
+        for (int m = 0; m < 2 * RM; ++m) h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
+      }
+      fetch(step + STAGES - 1);  // into the slots that the step before has read
+      if constexpr (sizeof(T) == 4) {
+        float xh[2][4], xl[2][4];
+        split4(x[0], xh[0], xl[0]);
+        split4(x[1], xh[1], xl[1]);
+#pragma unroll
+        for (int m = 0; m < RM; ++m) {
+          float hh[4], hl[4];
+          const float v[4] = {h[0][2 * m], h[0][2 * m + 1], h[1][2 * m], h[1][2 * m + 1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            hh[i] = tf32_of(v[i]);
+            hl[i] = v[i] - hh[i];
           }
-        } else {
-          uint32_t b[2][NT];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t lo[4] = {x[s][2 * e].x, x[s][2 * e].y, x[s][2 * e].z, x[s][2 * e].w};
-            const uint32_t hi[4] = {x[s][2 * e + 1].x, x[s][2 * e + 1].y, x[s][2 * e + 1].z, x[s][2 * e + 1].w};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[e][n] = __byte_perm(lo[n / 2], hi[n / 2], n % 2 ? 0x7632 : 0x5410);
+          for (int n = 0; n < NT; ++n) {
+            mma_tf32(acc[m][n], hl[0], hl[1], hl[2], hl[3], xh[0][n], xh[1][n]);
+            mma_tf32(acc[m][n], hh[0], hh[1], hh[2], hh[3], xl[0][n], xl[1][n]);
+            mma_tf32(acc[m][n], hh[0], hh[1], hh[2], hh[3], xh[0][n], xh[1][n]);
           }
+        }
+      } else {
+        uint32_t b[2][NT];
 #pragma unroll
-          for (int m = 0; m < RM; ++m) {
-            uint32_t hh[4], hl[4];
-            split_pair<T>(h[0][2 * m], h[1][2 * m], hh[0], hl[0]);
-            split_pair<T>(h[0][2 * m + 1], h[1][2 * m + 1], hh[1], hl[1]);
-            split_pair<T>(h[2][2 * m], h[3][2 * m], hh[2], hl[2]);
-            split_pair<T>(h[2][2 * m + 1], h[3][2 * m + 1], hh[3], hl[3]);
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t lo[4] = {x[2 * e].x, x[2 * e].y, x[2 * e].z, x[2 * e].w};
+          const uint32_t hi[4] = {x[2 * e + 1].x, x[2 * e + 1].y, x[2 * e + 1].z, x[2 * e + 1].w};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_16<T>(acc[m][n], hl[0], hl[1], hl[2], hl[3], b[0][n], b[1][n]);
-              mma_16<T>(acc[m][n], hh[0], hh[1], hh[2], hh[3], b[0][n], b[1][n]);
-            }
+          for (int n = 0; n < NT; ++n) b[e][n] = __byte_perm(lo[n / 2], hi[n / 2], n % 2 ? 0x7632 : 0x5410);
+        }
+#pragma unroll
+        for (int m = 0; m < RM; ++m) {
+          uint32_t hh[4], hl[4];
+          split_pair<T>(h[0][2 * m], h[1][2 * m], hh[0], hl[0]);
+          split_pair<T>(h[0][2 * m + 1], h[1][2 * m + 1], hh[1], hl[1]);
+          split_pair<T>(h[2][2 * m], h[3][2 * m], hh[2], hl[2]);
+          split_pair<T>(h[2][2 * m + 1], h[3][2 * m + 1], hh[3], hl[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16<T>(acc[m][n], hl[0], hl[1], hl[2], hl[3], b[0][n], b[1][n]);
+            mma_16<T>(acc[m][n], hh[0], hh[1], hh[2], hh[3], b[0][n], b[1][n]);
           }
         }
       }
-#pragma unroll
-      for (int m = 0; m < RM; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[m][n][i] += acc[m][n][i];
+      if (step % FLUSH == FLUSH - 1) flush();
     }
+    flush();
+    copies_wait<0>();
     p = end;
     float *out = d.parts + (slice + u) * d.rank * d.K;
 #pragma unroll
@@ -902,56 +1055,38 @@ __device__ __forceinline__ int adapter_of(const snack_adapter_args &a, int64_t t
   return n >= 0 && n < a.adapters ? n : -1;
 }
 
-constexpr int kFewRanks = 16;  // ranks that a block of `few_down` sums
-
-// Block (token, 16 ranks): its warps split the row of X and of the weights.
+// A warp for each (token, rank).
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) adapter_few_down(const __grid_constant__ AdapterArgs q) {
-  constexpr int E = 16 / sizeof(T);
-  __shared__ float part[kWarps][kFewRanks];
+  constexpr int E = 16 / sizeof(T), U = 4;
   dependency_wait();
   dependency_launch();
   const snack_adapter_args &a = q.a;
-  const int64_t tkn = blockIdx.x, j0 = (int64_t)blockIdx.y * kFewRanks;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (at >= a.tokens * a.rank) return;
+  const int64_t tkn = at / a.rank, j = at % a.rank;
+  const int lane = threadIdx.x & 31;
   const int n = adapter_of(a, tkn);
-  const int ranks = (int)min((int64_t)kFewRanks, a.rank - j0);
-  float s[kFewRanks];
-#pragma unroll
-  for (int j = 0; j < kFewRanks; ++j) s[j] = 0.f;
+  float s = 0.f;
   if (n >= 0) {
     const T *x = static_cast<const T *>(a.X) + tkn * a.x_stride;
-    const T *w = static_cast<const T *>(a.A) + ((int64_t)n * a.rank + j0) * a.in;
-    for (int64_t k = (int64_t)threadIdx.x * E; k < a.in; k += kThreads * E) {
-      const uint4 xv = load16<T, ALIGNED>(x, k, a.in, true);
-      uint4 wv[kFewRanks];
+    const T *w = static_cast<const T *>(a.A) + ((int64_t)n * a.rank + j) * a.in;
+    for (int64_t k0 = lane * E; k0 < a.in; k0 += U * 32 * E) {
+      uint4 xv[U], wv[U];
 #pragma unroll
-      for (int j = 0; j < kFewRanks; ++j) wv[j] = load16<T, ALIGNED>(w + (j < ranks ? j : 0) * a.in, k, a.in, j < ranks);
+      for (int u = 0; u < U; ++u) {
+        xv[u] = load16<T, ALIGNED>(x, k0 + u * 32 * E, a.in, true);
+        wv[u] = load16<T, ALIGNED>(w, k0 + u * 32 * E, a.in, true);
+      }
 #pragma unroll
-      for (int j = 0; j < kFewRanks; ++j)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          s[j] = fmaf(to_float(reinterpret_cast<const T *>(&xv)[e]), to_float(reinterpret_cast<const T *>(&wv[j])[e]), s[j]);
+          s = fmaf(to_float(reinterpret_cast<const T *>(&xv[u])[e]), to_float(reinterpret_cast<const T *>(&wv[u])[e]), s);
     }
+    s = warp_sum(s);
   }
-  // sixteen sums over the warp: each step halves the ranks that a lane still holds
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1)
-#pragma unroll
-    for (int j = 0; j < o; ++j) {
-      const bool up = lane & o;
-      const float send = up ? s[j] : s[j + o], keep = up ? s[j + o] : s[j];
-      s[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
-  if (lane < kFewRanks) part[warp][lane] = s[0];
-  __syncthreads();
-  if (threadIdx.x < ranks) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
-    q.H[tkn * a.rank + j0 + threadIdx.x] = v;
-  }
+  if (lane == 0) q.H[at] = s;
 }
 
 // Block (256 columns, token): one thread for each column.
@@ -1072,7 +1207,7 @@ bool vector_rows(const void *p, int64_t stride, int64_t width, int type) {
 template <typename T, int NT>
 cudaError_t launch_down_nt(const AdapterArgs &q, const DownArgs &d, bool vec, cudaStream_t s) {
   const dim3 grid((unsigned)q.p.max_tiles, (unsigned)((d.rank + kRankPass - 1) / kRankPass));
-  const size_t smem = sizeof(float) * kWarps * kTile * (NT * 8 + 4);
+  const size_t smem = DownShape<NT>::SMEM;
   auto k = vec ? adapter_down<T, NT, true> : adapter_down<T, NT, false>;
   const cudaError_t e = allow_smem(k, smem);
   return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
@@ -1096,21 +1231,25 @@ cudaError_t launch_up(const AdapterArgs &q, UpArgs d, cudaStream_t s) {
   d.blocks = (d.K + cols - 1) / cols;
   if (q.p.max_tiles * d.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(q.p.max_tiles * d.blocks));
-  const size_t smem = (size_t)((d.rank + 15) / 16) * (kTile / 16) * 2 * (sizeof(T) == 4 ? 2 : 1) * 32 * 16;
-  auto k = vector_rows(d.Y, d.y_stride, d.K, q.a.type) ? adapter_up<T, true> : adapter_up<T, false>;
+  const bool wvec = d.rank % 4 == 0 && aligned_to(d.W, 4 * sizeof(T));
+  const bool vec = vector_rows(d.Y, d.y_stride, d.K, q.a.type);
+  const int rg = !wvec || d.rank > 32 ? 0 : (d.rank > 16 ? 2 : 1);
+  auto k = !vec ? adapter_up<T, 0, false>
+                : (rg == 0 ? adapter_up<T, 0, true> : (rg == 1 ? adapter_up<T, 1, true> : adapter_up<T, 2, true>));
+  const size_t smem = S::smem(vec ? rg : 0, d.rank);
   const cudaError_t e = allow_smem(k, smem);
   return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
 }
 
-// Places of one block of `outer`: blocks enough to fill the GPU three times,
-// at least 64 places (below it the parts cost more than the split gains),
-// at most 512 (their H lies in shared memory: 80 KB at 32 ranks).
+// Places of one block of `outer`: one round of blocks, two on each SM; at
+// least 64 places (below it the parts cost more than the split gains), at
+// most 448 at 16 ranks and 256 at 32 (two blocks' rings and H fit an SM).
 int64_t outer_chunk(const snack_adapter_args &a, int64_t K) {
   const int64_t cols = kWarps * 8 * (16 / type_bytes(a.type)), ranks = outer_ranks(a.rank);
   const int64_t blocks = (K + cols - 1) / cols * ((a.rank + ranks - 1) / ranks);
-  const int64_t split = std::max<int64_t>(1, (int64_t)device_sms() * 3 / blocks);
+  const int64_t split = std::max<int64_t>(1, (int64_t)device_sms() * 2 / blocks);
   const int64_t c = (a.tokens + split - 1) / split;
-  return std::max<int64_t>(64, std::min<int64_t>(512, (c + 31) / 32 * 32));
+  return std::max<int64_t>(64, std::min<int64_t>(ranks == 16 ? 448 : 256, (c + 15) / 16 * 16));
 }
 
 int64_t outer_bytes(const snack_adapter_args &a, int64_t K) {
@@ -1132,7 +1271,7 @@ cudaError_t launch_outer(const AdapterArgs &q, OuterArgs d, T *out, bool scaled,
     const bool vec = vector_rows(d.X, d.x_stride, d.K, a.type);
     auto k = ranks == 16 ? (vec ? adapter_outer<T, 1, true> : adapter_outer<T, 1, false>)
                          : (vec ? adapter_outer<T, 2, true> : adapter_outer<T, 2, false>);
-    const size_t smem = (size_t)d.chunk * (ranks + 8 + 1) * 4;
+    const size_t smem = (size_t)OuterShape<T>::RING * 16 + (size_t)d.chunk * (ranks + 8 + 1) * 4;
     if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
     if ((e = launch_kernel(k, grid, kThreads, smem, true, s, q, d)) != cudaSuccess) return e;
   }
@@ -1156,7 +1295,7 @@ template <typename T>
 cudaError_t forward(const AdapterArgs &q, void *Y, int64_t y_stride, cudaStream_t s) {
   const snack_adapter_args &a = q.a;
   if (a.tokens <= kFewTokens) {
-    const dim3 grid((unsigned)a.tokens, (unsigned)((a.rank + kFewRanks - 1) / kFewRanks));
+    const dim3 grid((unsigned)((a.tokens * a.rank + kWarps - 1) / kWarps));
     auto k = vector_rows(a.X, a.x_stride, a.in, a.type) && aligned_to(a.A, 16) ? adapter_few_down<T, true>
                                                                                 : adapter_few_down<T, false>;
     cudaError_t e = launch_kernel(k, grid, kThreads, 0, true, s, q);
