@@ -307,10 +307,10 @@ __global__ void __launch_bounds__(kThreads) plan_tokens(const __grid_constant__ 
 
 // ------------------------------------------------------------------ matrix instructions
 
+// x rounded to the 11 significant bits of tf32, halves away from zero (a
+// magnitude above 2^128 - 2^116 overflows; what x - hi then is, is not a number).
 __device__ __forceinline__ float tf32_of(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return __uint_as_float(r);
+  return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
@@ -845,18 +845,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_consta
   const int places = (int)(min((int64_t)q.p.head[2], p0 + d.chunk) - p0);
   if (places <= 0) return;
   const int64_t j0 = (int64_t)blockIdx.y * 16 * RM;
-  for (int i = threadIdx.x; i < places * 16 * RM; i += kThreads) {
-    const int k = i / (16 * RM), j = i % (16 * RM);
-    const int32_t t = q.p.perm[p0 + k];
-    if (j == 0) tok[k] = t;
-    hs[k * LD + j] = j0 + j < d.rank ? d.H[t * d.rank + j0 + j] : 0.f;
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int64_t c0 = (cblock * kWarps + warp) * COLS, col = c0 + g * E;
-  if (c0 >= d.K) return;
-  const T *X = static_cast<const T *>(d.X);
-  uint4 *ring = smem4 + warp * STAGES * NR * 32 + lane;
+  // the chunk's tokens, then their H: two rounds of loads, each all at once,
+  // the second one over while the first rows of X are on their way
+  for (int i = threadIdx.x; i < places; i += kThreads) tok[i] = q.p.perm[p0 + i];
   // the first adapter of the chunk: the last used one that begins at or before p0
   int u = 0;
   {
@@ -870,6 +861,28 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_consta
     }
     u = lo - 1;
   }
+  __syncthreads();
+  const bool hvec = d.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(d.H) & 15) == 0;
+  if (hvec) {
+    for (int i = threadIdx.x; i < places * 4 * RM; i += kThreads) {
+      const int k = i / (4 * RM), j = i % (4 * RM) * 4;
+      copy16(reinterpret_cast<uint4 *>(hs + k * LD + j), d.H + tok[k] * d.rank, j0 + j, d.rank, true);
+    }
+  } else {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < places * 16 * RM; i += kThreads) {
+      const int k = i / (16 * RM), j = i % (16 * RM);
+      hs[k * LD + j] = j0 + j < d.rank ? d.H[tok[k] * d.rank + j0 + j] : 0.f;
+    }
+  }
+  copies_commit();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int64_t c0 = (cblock * kWarps + warp) * COLS, col = c0 + g * E;
+  const T *X = static_cast<const T *>(d.X);
+  const bool copy_ok = c0 + (lane & 7) * E < d.K;
+  const T *copy_from = X + (copy_ok ? c0 + (lane & 7) * E : 0);
+  uint4 *ring = smem4 + warp * STAGES * NR * 32;
+  bool first = true;
   for (int p = 0; p < places; ++u) {
     const int4 use = q.p.used[u];
     const int end = (int)min((int64_t)places, (int64_t)use.y + use.z - p0);
@@ -898,39 +911,53 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_consta
             acc[m][n][i] = 0.f;
           }
     };
-    // rows of a step: fp32 t and t + 4; 16-bit 2t, 2t + 1, 2t + 8, 2t + 9
-    const auto place = [&](int step, int i) {
-      return p + step * TS + (sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1));
-    };
     const int steps = (end - p + TS - 1) / TS;
+    // Eight lanes copy a row's 128 bytes (one line for each request: by the
+    // product's own layout, a quarter of a warp would ask for four lines, 32
+    // bytes of each); chunk c of a row lies at c ^ turn(row), so that the
+    // eight lanes that read together find it in eight different bank groups.
+    const auto turn = [](int row) { return sizeof(T) == 4 ? 2 * (row & 3) : row & 6; };
     const auto fetch = [&](int step) {
       if (!ALIGNED) return;
       if (step < steps)
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          const int k = place(step, i);
-          copy16(ring + ((step % STAGES) * NR + i) * 32, X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K,
-                 k < end);
+          const int row = 4 * i + (lane >> 3), k = p + step * TS + row;
+          const bool in = copy_ok && k < end;
+          copy16(ring + (step % STAGES) * NR * 32 + row * 8 + ((lane & 7) ^ turn(row)),
+                 copy_from + (in ? tok[k] * d.x_stride : 0), 0, 1, in);
         }
       copies_commit();
     };
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+    if (first) {  // H is there when only the rows' copies are outstanding
+      if (ALIGNED)
+        copies_wait<STAGES - 1>();
+      else
+        copies_wait<0>();
+      __syncthreads();
+      first = false;
+    }
     for (int step = 0; step < steps; ++step) {
       uint4 x[NR];
       float h[NR][2 * RM];
-      if (ALIGNED) copies_wait<STAGES - 2>();
+      if (ALIGNED) {
+        copies_wait<STAGES - 2>();
+        __syncwarp();
+      }
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        const int k = place(step, i);
+        // rows of a lane: fp32 t and t + 4; 16-bit 2t, 2t + 1, 2t + 8, 2t + 9
+        const int row = sizeof(T) == 4 ? t + 4 * i : 2 * t + (i & 1) + 8 * (i >> 1), k = p + step * TS + row;
         if (ALIGNED)
-          x[i] = ring[((step % STAGES) * NR + i) * 32];
+          x[i] = ring[(step % STAGES) * NR * 32 + row * 8 + (g ^ turn(row))];
         else
           x[i] = load16<T, false>(X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K, k < end);
 #pragma unroll
         for (int m = 0; m < 2 * RM; ++m) h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
       }
-      fetch(step + STAGES - 1);  // into the slots that the step before has read
+      fetch(step + STAGES - 1);  // into the slots that every lane read before this step's barrier
       if constexpr (sizeof(T) == 4) {
         float xh[2][4], xl[2][4];
         split4(x[0], xh[0], xl[0]);
@@ -978,6 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_consta
     }
     flush();
     copies_wait<0>();
+    __syncwarp();
     p = end;
     float *out = d.parts + (slice + u) * d.rank * d.K;
 #pragma unroll
