@@ -381,10 +381,6 @@ __device__ __forceinline__ void copy8(uint2 *slot, const T *row, int64_t k, int6
                "l"(from), "r"(in ? 8 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // One group of the summed index (64 bytes of a row: 16 fp32 or 32 16-bit
 // elements) of a 16 x 8 product: rows g and g + 8 in v0 and v1, the other
 // operand's row g in w.
@@ -1217,14 +1213,6 @@ cudaError_t launch_plan(const AdapterArgs &q, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t blocks = std::min<int64_t>((a.tokens + kThreads - 1) / kThreads, device_sms() * 8);
   return launch_kernel(plan_tokens, dim3((unsigned)blocks), kThreads, 0, true, s, q);
-}
-
-// Raises the kernel's limit of dynamic shared memory where it is above the default.
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 bool vector_rows(const void *p, int64_t stride, int64_t width, int type) {

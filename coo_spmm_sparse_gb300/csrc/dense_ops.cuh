@@ -82,6 +82,26 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *red) {
   __syncthreads();
 }
 
+// Asynchronous copies into shared memory (16-byte aligned global addresses);
+// `bytes` below the size fills the rest with zeros.
+__device__ __forceinline__ void copy_async16(void *slot, const void *from, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(slot)),
+               "l"(from), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Raises the kernel's limit of dynamic shared memory where it may be above
+// the default (48 KB with the kernel's static part, at most 8 KB here).
+template <typename K>
+inline cudaError_t allow_smem(K kern, size_t bytes) {
+  return bytes <= 40 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, bool pdl,
                                  cudaStream_t s, Args &&...args) {
@@ -106,6 +126,7 @@ inline snack_status refuse(snack_status st, const std::string &msg) {
 }
 
 inline snack_status cuda_status(cudaError_t e, const char *what) {
+  cudaGetLastError();  // reported here: not left for the caller's next CUDA call
   return refuse(e == cudaErrorMemoryAllocation ? SNACK_ERR_ALLOC : SNACK_ERR_CUDA,
                 std::string(what) + ": " + cudaGetErrorString(e));
 }

@@ -15,22 +15,12 @@
 // not carry the rounding of r to 16 bits.
 #include <algorithm>
 
-#include "dense_ops.cuh"
+#include "residual_norm.cuh"
 
 namespace snack {
 namespace {
 
 constexpr int kThreads = 256;
-
-struct NormArgs {
-  snack_norm_args a;
-  snack_norm_grads g;
-  void *r, *h;
-  float *row_scalars;  // [rows][2]: mean(t), mean(t rhat)
-  float *parts;        // [slabs][kCols][width]
-  int64_t groups, group_len;  // rows that share a gate row lie in one group of group_len rows
-  int64_t slabs, slab_rows, slabs_per_group;
-};
 
 // Column sums of the backward: the gradients of weights, biases and of a
 // gate that rows share.
@@ -293,15 +283,20 @@ bool wants_columns(const snack_norm_args &a, const snack_norm_grads &g) {
          (g.dgate && (a.gate_kind == SNACK_GATE_CHANNEL || a.gate_kind == SNACK_GATE_SEQUENCE));
 }
 
-// Rows are summed in slabs, each within one group: enough of them for two
-// rounds of blocks over the GPU, at least 32 rows in each.
-void plan_slabs(const snack_norm_args &a, NormArgs *n) {
+// Rows are summed in slabs, each within one group: as many in all as there
+// are teams to take them (or two rounds of the any-shape kernel's blocks).
+void plan_slabs(NormArgs *n, int64_t teams) {
+  const snack_norm_args &a = n->a;
   const bool seq = a.gate_kind == SNACK_GATE_SEQUENCE;
   n->groups = seq ? a.rows / a.group_rows : 1;
   n->group_len = seq ? a.group_rows : a.rows;
-  const int64_t tiles = (a.width + kColThreads - 1) / kColThreads;
-  int64_t want = (int64_t)device_sms() * 16 / std::max<int64_t>(1, tiles * n->groups);
-  want = std::max<int64_t>(1, std::min<int64_t>(want, (n->group_len + 31) / 32));
+  int64_t want = teams / std::max<int64_t>(1, n->groups);
+  if (teams == 0) {
+    const int64_t tiles = (a.width + kColThreads - 1) / kColThreads;
+    want = (int64_t)device_sms() * 16 / std::max<int64_t>(1, tiles * n->groups);
+    want = std::min<int64_t>(want, (n->group_len + 31) / 32);
+  }
+  want = std::max<int64_t>(1, want);
   n->slab_rows = std::max<int64_t>(1, (n->group_len + want - 1) / want);
   n->slabs_per_group = (n->group_len + n->slab_rows - 1) / n->slab_rows;  // 0 without rows
   n->slabs = n->slabs_per_group * n->groups;
@@ -339,14 +334,6 @@ const char *bad_args(const snack_norm_args *a) {
   if (a->stats && !aligned_to(a->stats, 16)) return "stats must be 16-byte aligned";
   return nullptr;
 }
-
-// F(TS, TB) for the types of a.
-#define SNACK_NORM_TYPES(F)                                                             \
-  if (a.stream_type == SNACK_F32 && a.branch_type == SNACK_F32) F(float, float)         \
-  else if (a.stream_type == SNACK_F32 && a.branch_type == SNACK_BF16) F(float, __nv_bfloat16) \
-  else if (a.stream_type == SNACK_F32) F(float, __half)                                 \
-  else if (a.stream_type == SNACK_BF16) F(__nv_bfloat16, __nv_bfloat16)                 \
-  else F(__half, __half)
 
 cudaError_t launch_forward(const NormArgs &n, cudaStream_t s) {
   const snack_norm_args &a = n.a;
@@ -393,16 +380,26 @@ extern "C" snack_status snack_residual_norm_forward(const snack_norm_args *args,
   n.a = *args;
   n.r = r;
   n.h = h;
-  const cudaError_t e = launch_forward(n, static_cast<cudaStream_t>(stream));
+  const TeamPlan p = team_forward(n);
+  const cudaError_t e = p.threads ? launch_team_forward(n, p, static_cast<cudaStream_t>(stream))
+                                  : launch_forward(n, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "residual norm launch");
 }
 
 extern "C" size_t snack_residual_norm_workspace(const snack_norm_args *args) {
   using namespace snack;
   if (bad_args(args)) return 16;
+  // enough for either way of summing the columns, whatever the gradients' alignment
   NormArgs n = {};
-  plan_slabs(*args, &n);
-  return (size_t)(align16(args->rows * 8) + n.slabs * kCols * args->width * 4 + 16);
+  n.a = *args;
+  plan_slabs(&n, 0);
+  int64_t floats = n.slabs * kCols;
+  const TeamPlan p = team_backward(n);
+  if (p.threads) {
+    plan_slabs(&n, p.teams);
+    floats = std::max(floats, 2 * (p.teams + n.slabs));
+  }
+  return (size_t)(align16(args->rows * 8) + floats * args->width * 4 + 16);
 }
 
 extern "C" snack_status snack_residual_norm_backward(const snack_norm_args *args,
@@ -426,11 +423,16 @@ extern "C" snack_status snack_residual_norm_backward(const snack_norm_args *args
   NormArgs n = {};
   n.a = a;
   n.g = g;
-  plan_slabs(a, &n);
+  const TeamPlan p = team_backward(n);
+  plan_slabs(&n, p.teams);
   n.row_scalars = static_cast<float *>(workspace);
   n.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + align16(a.rows * 8));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  if (p.threads && a.rows > 0) {
+    e = launch_team_backward(n, p, s);
+    return e == cudaSuccess ? SNACK_OK : cuda_status(e, "residual norm backward launch");
+  }
   if (a.rows > 0 && (e = launch_backward_rows(n, s)) != cudaSuccess)
     return cuda_status(e, "residual norm backward launch");
   if (wants_columns(a, g)) {

@@ -58,7 +58,8 @@ def test_every_form(stream, branch, kind, post, gate):
 
 
 @pytest.mark.parametrize("d", [1, 2, 7, 33, 64, 100, 255, 768, 1000, 1001, 1024, 2304, 4096, 4100,
-                               5003, 8192, 8200, 12288, 16384, 20001])
+                               5003, 8192, 8200, 12288, 16384, 20001,
+                               32768, 33000, 40001])
 @pytest.mark.parametrize("stream,branch", [(F32, F32), (BF16, BF16), (F32, BF16)])
 def test_every_width(d, stream, branch):
     kind = "layer" if d > 1 else "rms"  # a layer norm of one element is its bias
