@@ -1,0 +1,138 @@
+// Residual norm forward, rows held in registers (norm_team.cuh).
+#include "norm_team.cuh"
+
+namespace snack {
+namespace {
+
+using namespace team;
+
+template <typename TS, typename TB, int S, bool VEC, bool CL, bool LAYER>
+__global__ void __launch_bounds__(kTeamThreads, 2) norm_team_forward(const __grid_constant__ TeamArgs q) {
+  extern __shared__ uint4 smem4[];
+  __shared__ float red[Team<CL>::kFloats];
+  char *const ring = reinterpret_cast<char *>(smem4);
+  const snack_norm_args &a = q.n.a;
+  dependency_wait();
+  dependency_launch();
+  Team<CL> team = make_team<CL>(red);
+  const Columns<TS, TB, VEC> co(q, team.rank);
+  const int64_t first = blockIdx.x / team.size, step = gridDim.x / team.size;
+  const bool has_y = a.y != nullptr, full = a.gate_kind == SNACK_GATE_FULL;
+  const int xb = row_bytes<TS, VEC>(q), bb = row_bytes<TB, VEC>(q), per = xb + bb + (full ? bb : 0);
+  if (VEC && co.count < (int)blockDim.x * C) clear_slots(ring, S * per);
+
+  const auto fetch = [&](int64_t row, int stage) {
+    if (row < a.rows) {
+      char *to = ring + stage * per;
+      copy_row<TS, VEC>(to, static_cast<const TS *>(a.x) + row * a.x_stride, co);
+      if (has_y) copy_row<TB, VEC>(to + xb, static_cast<const TB *>(a.y) + row * a.y_stride, co);
+      if (full) copy_row<TB, VEC>(to + xb + bb, gate_row<TB>(a, row), co);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(first + i * step, i);
+
+  // h = hat nw + nb;  r = a x + gate (hat k1 + k0), where k1 and k0 take in
+  // the branch's scale and a gate that belongs to the column
+  float nw[C], nb[C], k1[C], k0[C];
+  load_params(a.next_weight, a.param_type, co, 1.f, nw);
+  if (LAYER) load_params(a.next_bias, a.param_type, co, 0.f, nb);
+  const auto fold = [&](int64_t row) {
+    load_params(a.post_weight, a.param_type, co, 1.f, k1);
+    if (LAYER || a.post_bias) load_params(a.post_bias, a.param_type, co, 0.f, k0);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      float f = a.branch_scale;
+      if (a.gate_kind == SNACK_GATE_CHANNEL || a.gate_kind == SNACK_GATE_SEQUENCE)
+        f *= co.in(j) ? to_float(gate_row<TB>(a, row)[co.at(j)]) : 0.f;
+      k1[j] *= f;
+      if (LAYER || a.post_bias) k0[j] *= f;
+    }
+  };
+  if (has_y && a.gate_kind != SNACK_GATE_SEQUENCE) fold(0);
+
+  int stage = 0;
+  int64_t group = -1;
+  for (int64_t row = first; row < a.rows; row += step) {
+    float x[C];
+    float ym = 0.f, yr = 1.f, mean = 0.f, rstd = 1.f;
+    copies_wait<S - 2>();
+    if (!VEC) __syncthreads();
+    const char *from = ring + stage * per;
+    take_row<TS, VEC>(from, static_cast<const TS *>(a.x) + row * a.x_stride, co, x);
+#pragma unroll
+    for (int j = 0; j < C; ++j) x[j] *= a.residual_scale;
+    if (has_y) {
+      float y[C];
+      take_row<TB, VEC>(from + xb, static_cast<const TB *>(a.y) + row * a.y_stride, co, y);
+      if (a.gate_kind == SNACK_GATE_SEQUENCE && row / a.group_rows != group) {
+        group = row / a.group_rows;
+        fold(row);
+      }
+      if (a.post_norm) team.template stats<LAYER>(a, co, y, ym, yr);
+      const float tg = a.gate_kind == SNACK_GATE_TOKEN ? to_float(static_cast<const TB *>(a.gate)[row]) : 1.f;
+      float gate[C];
+      if (full) take_row<TB, VEC>(from + xb + bb, gate_row<TB>(a, row), co, gate);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        float u = (LAYER ? y[j] - ym : y[j]) * yr;
+        u = LAYER || a.post_bias ? fmaf(u, k1[j], k0[j]) : u * k1[j];
+        x[j] = fmaf(full ? gate[j] : tg, u, x[j]);
+      }
+    }
+    // vectors: into the slots that this thread read for the row before; else
+    // all have read that row, for they have passed this row's barrier
+    fetch(row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    stage = stage == S - 1 ? 0 : stage + 1;
+    if (q.n.r) store_row<TS, VEC>(static_cast<TS *>(q.n.r) + row * a.width, co, x);
+    if (a.next_norm) {
+      team.template stats<LAYER>(a, co, x, mean, rstd);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const float hat = (LAYER ? x[j] - mean : x[j]) * rstd;
+        x[j] = LAYER ? fmaf(hat, nw[j], nb[j]) : hat * nw[j];
+      }
+      if (!LAYER && a.next_bias) {
+        load_params(a.next_bias, a.param_type, co, 0.f, k0);
+#pragma unroll
+        for (int j = 0; j < C; ++j) x[j] += k0[j];
+        if (has_y && a.post_bias) fold(row);
+      }
+      store_row<TB, VEC>(static_cast<TB *>(q.n.h) + row * a.width, co, x);
+    }
+    if (a.stats && team.rank == 0 && threadIdx.x == 0)
+      reinterpret_cast<float4 *>(a.stats)[row] = make_float4(ym, yr, mean, rstd);
+  }
+  copies_wait<0>();
+  if (CL) cg::this_cluster().sync();  // no block leaves while another may still write to it
+}
+
+template <typename TS, typename TB>
+cudaError_t launch(const TeamPlan &p, int64_t teams, const TeamArgs &q, cudaStream_t s) {
+  SNACK_TEAM(norm_team_forward, TS, TB)
+}
+
+}  // namespace
+
+TeamPlan team_forward(const NormArgs &n) {
+  const snack_norm_args &a = n.a;
+  TeamPlan p = team_shape(a);
+  if (p.threads == 0) return p;
+  const bool full = a.gate_kind == SNACK_GATE_FULL;
+  p.vec = a.width % 8 == 0 && rows16(a.x, a.x_stride, a.stream_type) && rows16(a.y, a.y_stride, a.branch_type) &&
+          (!full || rows16(a.gate, a.gate_stride, a.branch_type)) && aligned_to(n.r, 16) && aligned_to(n.h, 16);
+  team_ring(&p, a, 1, full ? 2 : 1);
+  p.teams = std::min<int64_t>(a.rows, std::max<int64_t>(1, (int64_t)device_sms() * (2 * kTeamThreads / p.threads) / p.cluster));
+  return p;
+}
+
+cudaError_t launch_team_forward(const NormArgs &n, const TeamPlan &p, cudaStream_t s) {
+  const snack_norm_args &a = n.a;
+  const TeamArgs q = {n, p.block_cols, nullptr, nullptr};
+#define SNACK_CALL(TS, TB) return launch<TS, TB>(p, p.teams, q, s);
+  SNACK_NORM_TYPES(SNACK_CALL)
+#undef SNACK_CALL
+}
+
+}  // namespace snack

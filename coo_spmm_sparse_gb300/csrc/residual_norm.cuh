@@ -1,5 +1,5 @@
 // Shared by the residual norm's kernels: residual_norm.cu (checks, any shape)
-// and residual_norm_rows.cu (rows held in registers).
+// and norm_team_*.cu (rows held in registers).
 #pragma once
 
 #include "dense_ops.cuh"
@@ -27,7 +27,7 @@ struct TeamPlan {
   int cluster = 1;
   int block_cols = 0;  // columns of one block
   bool vec = false;    // rows can be read and written in 16-byte vectors
-  int stages = 0;      // rows copied ahead (vec)
+  int stages = 0;      // rows in the ring: one held, the others copied ahead
   size_t smem = 0;
   int64_t teams = 0;
 };

@@ -79,6 +79,13 @@ def test_parameters_in_sixteen_bits(param):
     check(*make((2, 65, 640), "layer", True, "channel", F32, BF16, param=param, seed=4))
 
 
+def test_biases_of_an_rms_norm():
+    for stream, branch in ((F32, F32), (BF16, BF16)):
+        for gate in (None, "channel", "sequence", "token", "full"):
+            x, y, o, dr, dh = make((2, 33, 264), "layer", True, gate, stream, branch, seed=21)
+            check(x, y, dict(o, kind="rms"), dr, dh)
+
+
 def test_strided_rows_and_misaligned_starts():
     for d, off in ((256, 0), (256, 3), (768, 8), (100, 1)):
         x, y, o, dr, dh = make((2, 9, d), "layer", True, "full", BF16, BF16, seed=9)
