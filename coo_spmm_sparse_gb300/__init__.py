@@ -84,6 +84,10 @@ class SnackHandle:
             pass
 
 
+_dense = _abi.load_dense()
+_dense.set_error(SnackError)
+
+
 def _check(status: int, h: SnackHandle | None = None):
     if status != 0:
         msg = _lib.snack_last_error(h.ptr if h is not None else None)
@@ -96,6 +100,13 @@ def _stream(stream, device=None):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _raw_stream(stream):
+    """None (the current stream) or the address of `stream` as a number."""
+    if stream is None:
+        return None
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _dev_f32(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -219,56 +230,6 @@ def snack_prune_regrow(h: SnackHandle, frac: float, seed: int, stream=None):
     _check(_lib.snack_prune_regrow(h.ptr, ctypes.c_float(frac), seed & (2**64 - 1),
                                    _stream(stream), ctypes.byref(p), ctypes.byref(t)), h)
     return int(p.value), int(t.value)
-
-
-_DTYPES = {torch.float32: _abi.F32, torch.bfloat16: _abi.BF16, torch.float16: _abi.F16}
-
-
-def _dense_type(t: torch.Tensor, name: str) -> int:
-    """snack_dtype of a CUDA tensor of the current device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be a CUDA float32, bfloat16 or float16 tensor")
-    return _DTYPES[t.dtype]
-
-
-def _rows(t: torch.Tensor, name: str):
-    """(rows, row stride) of t seen as [rows][last dimension]: its leading
-    dimensions must lie one regular step apart, its last one contiguous."""
-    if t.is_contiguous():
-        return (t.numel() // t.shape[-1] if t.shape[-1] else 0), t.shape[-1]
-    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    rows, step = 1, None
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if n == 1:
-            continue
-        if step is None:
-            step = st
-        elif st != step * rows:
-            raise ValueError(f"{name}: the rows of its leading dimensions are not evenly spaced")
-        rows *= n
-    step = t.shape[-1] if step is None else step
-    if step < t.shape[-1]:
-        raise ValueError(f"{name}: its rows overlap")
-    return rows, step
-
-
-def _same_device(*tensors):
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("all tensors must be on one device")
-    if dev is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"{dev} is not the current CUDA device")
-    return dev
-
-
-def _addr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
 
 
 class _CudaArray:

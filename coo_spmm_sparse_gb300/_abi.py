@@ -8,48 +8,17 @@ fails with an error that says how to build it.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libsnack.so")
+DENSE_PATH = os.path.join(_HERE, "_build", "_dense.so")
 
 i32, i64, u64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 vp, sz = ctypes.c_void_p, ctypes.c_size_t
 P = ctypes.POINTER
-
-# element types of the dense operators (snack_dtype)
-F32, BF16, F16 = 0, 1, 2
-
-
-class NormArgs(ctypes.Structure):
-    """snack_norm_args"""
-    _fields_ = [("rows", i64), ("width", i64), ("group_rows", i64),
-                ("norm_kind", i32), ("post_norm", i32), ("next_norm", i32), ("gate_kind", i32),
-                ("stream_type", i32), ("branch_type", i32), ("param_type", i32),
-                ("reserved", i32),
-                ("residual_scale", f32), ("branch_scale", f32), ("eps", f32),
-                ("reserved_f", f32),
-                ("x", vp), ("y", vp), ("gate", vp),
-                ("x_stride", i64), ("y_stride", i64), ("gate_stride", i64),
-                ("post_weight", vp), ("post_bias", vp), ("next_weight", vp), ("next_bias", vp),
-                ("stats", vp)]
-
-
-class NormGrads(ctypes.Structure):
-    """snack_norm_grads"""
-    _fields_ = [("dr", vp), ("dh", vp), ("dr_stride", i64), ("dh_stride", i64),
-                ("dx", vp), ("dy", vp), ("dgate", vp),
-                ("dpost_weight", vp), ("dpost_bias", vp), ("dnext_weight", vp),
-                ("dnext_bias", vp)]
-
-
-class AdapterArgs(ctypes.Structure):
-    """snack_adapter_args"""
-    _fields_ = [("tokens", i64), ("requests", i64), ("adapters", i64), ("inp", i64),
-                ("out", i64), ("rank", i64), ("type", i32), ("uniform_scale", f32),
-                ("X", vp), ("A", vp), ("B", vp), ("x_stride", i64), ("offsets", vp),
-                ("adapter", vp), ("scale", vp)]
-
 
 # name -> (restype, argtypes), mirroring include/snack.h
 SIGNATURES = {
@@ -69,13 +38,13 @@ SIGNATURES = {
     "snack_export_segments": (ctypes.c_int, [vp, vp, vp, vp, vp, vp]),
     "snack_plan": (ctypes.c_int, [vp, ctypes.c_int, i64, P(i32), P(i32), P(i64), P(i32)]),
     "snack_forward_csr_static": (ctypes.c_int, [i64, i64, i64, vp, vp, vp, vp, vp, i64, vp]),
-    "snack_residual_norm_forward": (ctypes.c_int, [P(NormArgs), vp, vp, vp]),
-    "snack_residual_norm_workspace": (sz, [P(NormArgs)]),
-    "snack_residual_norm_backward": (ctypes.c_int, [P(NormArgs), P(NormGrads), vp, vp]),
-    "snack_adapter_forward_workspace": (sz, [P(AdapterArgs)]),
-    "snack_adapter_forward": (ctypes.c_int, [P(AdapterArgs), vp, i64, vp, vp, vp]),
-    "snack_adapter_backward_workspace": (sz, [P(AdapterArgs)]),
-    "snack_adapter_backward": (ctypes.c_int, [P(AdapterArgs), vp, i64, vp, vp, i64, vp, vp, vp,
+    "snack_residual_norm_forward": (ctypes.c_int, [vp, vp, vp, vp]),
+    "snack_residual_norm_workspace": (sz, [vp]),
+    "snack_residual_norm_backward": (ctypes.c_int, [vp, vp, vp, vp]),
+    "snack_adapter_forward_workspace": (sz, [vp]),
+    "snack_adapter_forward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp]),
+    "snack_adapter_backward_workspace": (sz, [vp]),
+    "snack_adapter_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, i64, vp, vp, vp,
                                               vp]),
     "snack_grad_norm_workspace": (sz, [i64]),
     "snack_grad_norm": (ctypes.c_int, [i64, vp, vp, vp, ctypes.c_int, vp, vp, vp]),
@@ -118,3 +87,15 @@ def load(path: str = LIB_PATH):
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def load_dense(path: str = DENSE_PATH):
+    """Load the native binding of the dense operators (no fallback)."""
+    if not os.path.exists(path):
+        raise ImportError(
+            f"_dense.so not found at {path}; build it with "
+            "`python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader("_dense", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_dense", loader))
+    loader.exec_module(mod)
+    return mod

@@ -2,17 +2,22 @@
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
 coo_spmm_sparse_gb300/_build/libsnack.so against the shared CUDA runtime.
-Rebuilds only when a source or header is newer than the library.
+csrc/binding.cpp, the Python binding of the dense operators, is compiled by
+the host compiler into _build/_dense.so, against libsnack.so and the
+installed torch.  Rebuilds only when a source or header is newer than the
+libraries, or they were built for another machine, Python or torch.
 """
 
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,21 +46,68 @@ def sources():
 
 
 STAMP = os.path.join(BUILD, "machine.txt")
+BINDING = os.path.join(CSRC, "binding.cpp")
+DENSE = os.path.join(BUILD, "_dense.so")
+
+
+def _torch_dir() -> str:
+    """Where torch is installed (without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found: the binding of the dense operators needs it")
+    return os.path.dirname(spec.origin)
+
+
+def _built_for() -> str:
+    """What the built files depend on besides their sources."""
+    try:
+        with open(os.path.join(_torch_dir(), "version.py")) as f:
+            torch_version = next((l.strip() for l in f if l.startswith("__version__")), "")
+    except OSError:
+        torch_version = ""
+    return f"{platform.machine()} python {sys.version_info[0]}.{sys.version_info[1]} torch {torch_version}"
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(DENSE):
         return True
     try:
         with open(STAMP) as f:
-            if f.read().strip() != platform.machine():
-                return True  # built on another CPU architecture
+            if f.read().strip() != _built_for():
+                return True
     except OSError:
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(DENSE))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__]
+        glob.glob(os.path.join(ROOT, "include", "*.h")) + [BINDING, __file__]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _compile_binding(nvcc: str) -> str:
+    """binding.cpp -> object file (the host compiler; no CUDA code in it)."""
+    inc = os.path.join(_torch_dir(), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-Wall",
+           f"-I{os.path.join(ROOT, 'include')}", "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+           os.path.join(os.path.dirname(_cuda_lib_dir(nvcc)), "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-c", BINDING, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {BINDING} failed:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    libs = os.path.join(_torch_dir(), "lib")
+    tmp = DENSE + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-shared", obj, "-o", tmp, f"-L{BUILD}", "-lsnack",
+           "-Wl,-rpath,$ORIGIN", f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking {DENSE} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, DENSE)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -77,8 +129,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding, nvcc)
         objs = list(ex.map(compile_one, srcs))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, "-shared", *ARCH, "-cudart", "shared", "-Xlinker",
            f"-rpath,{_cuda_lib_dir(nvcc)}", *objs, "-o", tmp]
@@ -86,8 +140,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     with open(STAMP, "w") as f:
-        f.write(platform.machine())
+        f.write(_built_for())
     return LIB
 
 

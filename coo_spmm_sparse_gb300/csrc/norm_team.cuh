@@ -223,7 +223,7 @@ struct Team {
       for (int j = 0; j < C; ++j) s[0] = fmaf(v[j], v[j], s[0]);
     }
     sum(s);
-    rstd = 1.f / sqrtf(fmaf(s[0], inv, a.eps));
+    rstd = rsqrtf(fmaf(s[0], inv, a.eps));
   }
 };
 
@@ -312,31 +312,51 @@ cudaError_t launch_team(K kern, const TeamPlan &p, int64_t teams, const TeamArgs
   return e;
 }
 
-// Returns the launch of KERNEL<TS, TB, stages, vectors, cluster, layer norm>
-// by the plan p.  Two stages: fp32 rows with a full gate (five arrays).
-#define SNACK_TEAM_L(KERNEL, TS, TB, CL, L)                                                              \
-  {                                                                                                      \
-    if (p.stages == 3) {                                                                                 \
-      if (p.vec) return launch_team(KERNEL<TS, TB, 3, true, CL, L>, p, teams, q, s);                     \
-      return launch_team(KERNEL<TS, TB, 3, false, CL, L>, p, teams, q, s);                               \
-    }                                                                                                    \
-    if constexpr (sizeof(TB) == 4) {                                                                     \
-      if (p.vec) return launch_team(KERNEL<TS, TB, 2, true, CL, L>, p, teams, q, s);                     \
-      return launch_team(KERNEL<TS, TB, 2, false, CL, L>, p, teams, q, s);                               \
-    }                                                                                                    \
-    return cudaErrorInvalidValue;                                                                        \
+// The forms of a call that are compiled on their own, because their many
+// calls leave no room for the tests and registers of the others: a branch, a
+// norm after it, all results wanted, no gate that belongs to a row, no bias
+// of an rms norm; rows of vectors in one block.
+enum Form { kAny = 0, kFast = 1, kFastPost = 2 };
+
+// Returns the launch of KERNEL<TS, TB, stages, vectors, cluster, layer norm,
+// form> by the plan p.  Two stages: fp32 rows with a full gate (five arrays).
+#define SNACK_TEAM_L(KERNEL, TS, TB, CL, L)                                                       \
+  {                                                                                               \
+    if (p.stages == 3) {                                                                          \
+      if (p.vec) return launch_team(KERNEL<TS, TB, 3, true, CL, L, kAny>, p, teams, q, s);        \
+      return launch_team(KERNEL<TS, TB, 3, false, CL, L, kAny>, p, teams, q, s);                  \
+    }                                                                                             \
+    if constexpr (sizeof(TB) == 4) {                                                              \
+      if (p.vec) return launch_team(KERNEL<TS, TB, 2, true, CL, L, kAny>, p, teams, q, s);        \
+      return launch_team(KERNEL<TS, TB, 2, false, CL, L, kAny>, p, teams, q, s);                  \
+    }                                                                                             \
+    return cudaErrorInvalidValue;                                                                 \
   }
-#define SNACK_TEAM(KERNEL, TS, TB)                                                 \
-  {                                                                                \
-    const bool layer = q.n.a.norm_kind == SNACK_NORM_LAYER;                        \
-    if (p.cluster > 1) {                                                           \
-      if (layer) SNACK_TEAM_L(KERNEL, TS, TB, true, true)                          \
-      else SNACK_TEAM_L(KERNEL, TS, TB, true, false)                               \
-    } else {                                                                       \
-      if (layer) SNACK_TEAM_L(KERNEL, TS, TB, false, true)                         \
-      else SNACK_TEAM_L(KERNEL, TS, TB, false, false)                              \
-    }                                                                              \
+#define SNACK_TEAM_F(KERNEL, TS, TB, L)                                                           \
+  {                                                                                               \
+    if (form == kFastPost) return launch_team(KERNEL<TS, TB, 3, true, false, L, kFastPost>, p, teams, q, s); \
+    return launch_team(KERNEL<TS, TB, 3, true, false, L, kFast>, p, teams, q, s);                 \
   }
+#define SNACK_TEAM(KERNEL, TS, TB)                                                                \
+  {                                                                                               \
+    const bool layer = q.n.a.norm_kind == SNACK_NORM_LAYER;                                       \
+    if (form != kAny && p.vec && p.stages == 3 && p.cluster == 1) {                               \
+      if (layer) SNACK_TEAM_F(KERNEL, TS, TB, true)                                               \
+      else SNACK_TEAM_F(KERNEL, TS, TB, false)                                                    \
+    }                                                                                             \
+    if (p.cluster > 1) {                                                                          \
+      if (layer) SNACK_TEAM_L(KERNEL, TS, TB, true, true)                                         \
+      else SNACK_TEAM_L(KERNEL, TS, TB, true, false)                                              \
+    }                                                                                             \
+    if (layer) SNACK_TEAM_L(KERNEL, TS, TB, false, true)                                          \
+    else SNACK_TEAM_L(KERNEL, TS, TB, false, false)                                               \
+  }
+
+// Whether the options allow a form of their own.
+inline bool plain_options(const snack_norm_args &a) {
+  return a.y && a.next_norm && a.gate_kind != SNACK_GATE_TOKEN && a.gate_kind != SNACK_GATE_FULL &&
+         (a.norm_kind == SNACK_NORM_LAYER || (!a.post_bias && !a.next_bias));
+}
 
 }  // namespace team
 }  // namespace snack

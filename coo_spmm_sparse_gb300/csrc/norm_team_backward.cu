@@ -17,7 +17,7 @@ using namespace team;
 
 // A team takes slabs of rows, each within one group; sum dh rhat and sum dh
 // leave once per team, sum G D yhat and sum G D once per slab.
-template <typename TS, typename TB, int S, bool VEC, bool CL, bool LAYER>
+template <typename TS, typename TB, int S, bool VEC, bool CL, bool LAYER, Form F>
 __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_constant__ TeamArgs q) {
   extern __shared__ uint4 smem4[];
   __shared__ float red[Team<CL>::kFloats];
@@ -29,11 +29,12 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
   Team<CL> team = make_team<CL>(red);
   const Columns<TS, TB, VEC> co(q, team.rank);
   const int64_t me = blockIdx.x / team.size, teams = gridDim.x / team.size;
-  const bool has_y = a.y != nullptr, post = has_y && a.post_norm;
-  const bool full = a.gate_kind == SNACK_GATE_FULL, token = a.gate_kind == SNACK_GATE_TOKEN;
-  const bool has_dh = g.dh && a.next_norm, has_dr = g.dr != nullptr;
+  const bool has_y = F || a.y, post = F ? F == kFastPost : has_y && a.post_norm;
+  const bool full = !F && a.gate_kind == SNACK_GATE_FULL, token = !F && a.gate_kind == SNACK_GATE_TOKEN;
+  const bool has_dh = F || (g.dh && a.next_norm), has_dr = F || g.dr, want_dx = F || g.dx, want_dy = F || g.dy;
   // a bias: the layer norms' own, or one given to an rms norm
-  const bool post_bias = LAYER || a.post_bias, dbias = LAYER || g.dnext_bias || g.dpost_bias || a.post_bias;
+  const bool post_bias = LAYER || (!F && a.post_bias);
+  const bool dbias = LAYER || (!F && (g.dnext_bias || g.dpost_bias || a.post_bias));
   const int xb = row_bytes<TS, VEC>(q), bb = row_bytes<TB, VEC>(q), per = 2 * xb + (2 + (full ? 1 : 0)) * bb;
   const float inv = 1.f / (float)a.width;
   if (VEC && co.count < (int)blockDim.x * C) clear_slots(ring, S * per);
@@ -62,12 +63,13 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
   for (int j = 0; j < C; ++j) s0[j] = s1[j] = 0.f;
 
   for (int64_t slab = me; slab < q.n.slabs; slab += teams) {
-    const int64_t group = slab / q.n.slabs_per_group, k = slab % q.n.slabs_per_group;
-    const int64_t r0 = group * q.n.group_len + k * q.n.slab_rows;
-    const int64_t r1 = min((group + 1) * q.n.group_len, r0 + q.n.slab_rows);
+    // every step-th row of the group: all teams together sweep the rows in
+    // their order
+    const int64_t step = q.n.slabs_per_group, group = slab / step;
+    const int64_t r0 = group * q.n.group_len + slab % step, r1 = (group + 1) * q.n.group_len;
     if (!VEC) __syncthreads();  // the slab before has been read by all
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) fetch(r0 + i, r1, i);
+    for (int i = 0; i < S - 1; ++i) fetch(r0 + i * step, r1, i);
     if (has_y) {
       load_params(a.post_weight, a.param_type, co, 1.f, k1);
       load_params(a.post_bias, a.param_type, co, 0.f, k0);
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
 
     int stage = 0;
     float4 st = r0 < r1 ? reinterpret_cast<const float4 *>(a.stats)[r0] : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t row = r0; row < r1; ++row) {
+    for (int64_t row = r0; row < r1; row += step) {
       // A column beyond the row holds zeros and zero parameters: whatever
       // its hats are, it adds 0 to the row's sums, and nothing of it is stored.
       float rh[C], D[C], yh[C], gate[C];
@@ -95,19 +97,22 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
       if (!VEC) __syncthreads();
       const char *from = ring + stage * per;
       take_row<TS, VEC>(from, x_row(row), co, rh);
-      if (row + 1 < r1) st = reinterpret_cast<const float4 *>(a.stats)[row + 1];
+      if (row + step < r1) st = reinterpret_cast<const float4 *>(a.stats)[row + step];
       const float tg = token ? to_float(static_cast<const TB *>(a.gate)[row]) : 1.f;
       if (full) take_row<TB, VEC>(from + 2 * xb + 2 * bb, gate_row<TB>(a, row), co, gate);
-#pragma unroll
-      for (int j = 0; j < C; ++j) rh[j] *= a.residual_scale;
       if (has_y) {
         take_row<TB, VEC>(from + 2 * xb, y_row(row), co, yh);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          yh[j] = (LAYER ? yh[j] - ym : yh[j]) * yr;
-          const float u = post_bias ? fmaf(k1[j], yh[j], k0[j]) : k1[j] * yh[j];
-          rh[j] = fmaf(full ? gate[j] : tg, u, rh[j]);
+          if (post) yh[j] = (LAYER ? yh[j] - ym : yh[j]) * yr;
+          float u = post_bias ? fmaf(k1[j], yh[j], k0[j]) : k1[j] * yh[j];
+          if (full) u *= gate[j];
+          if (token) u *= tg;
+          rh[j] = fmaf(a.residual_scale, rh[j], u);
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j) rh[j] *= a.residual_scale;
       }
       float c[2] = {0.f, 0.f};
       if (has_dh) {
@@ -145,9 +150,9 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
       }
       // vectors: into the slots that this thread read for the row before; else
       // all have read that row, for they have passed this row's barrier
-      fetch(row + S - 1, r1, stage == 0 ? S - 1 : stage - 1);
+      fetch(row + (S - 1) * step, r1, stage == 0 ? S - 1 : stage - 1);
       stage = stage == S - 1 ? 0 : stage + 1;
-      if (g.dx) {
+      if (want_dx) {
         float v[C];
 #pragma unroll
         for (int j = 0; j < C; ++j) v[j] = a.residual_scale * D[j];
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
           e[1] = e1[0];
         }
       }
-      if (g.dy) {
+      if (want_dy) {
         if (post) {
           const float m1 = LAYER ? e[0] * inv : 0.f, m2 = e[1] * inv;
 #pragma unroll
@@ -293,7 +298,7 @@ __global__ void __launch_bounds__(kFinX *kFinY) norm_team_finish(const __grid_co
 }
 
 template <typename TS, typename TB>
-cudaError_t launch(const TeamPlan &p, int64_t teams, const TeamArgs &q, cudaStream_t s) {
+cudaError_t launch(const TeamPlan &p, int64_t teams, const TeamArgs &q, Form form, cudaStream_t s) {
   SNACK_TEAM(norm_team_backward, TS, TB)
 }
 
@@ -328,8 +333,9 @@ cudaError_t launch_team_backward(const NormArgs &n, const TeamPlan &p, cudaStrea
   const int64_t teams = std::min<int64_t>(p.teams, n.slabs);
   if (next) q.next_parts = n.parts;
   if (post) q.post_parts = n.parts + teams * 2 * a.width;
+  const Form form = !plain_options(a) || !g.dr || !g.dh || !g.dx || !g.dy ? kAny : (a.post_norm ? kFastPost : kFast);
   const auto main = [&]() -> cudaError_t {
-#define SNACK_CALL(TS, TB) return launch<TS, TB>(p, teams, q, s);
+#define SNACK_CALL(TS, TB) return launch<TS, TB>(p, teams, q, form, s);
     SNACK_NORM_TYPES(SNACK_CALL)
 #undef SNACK_CALL
   };

@@ -381,6 +381,7 @@ extern "C" snack_status snack_residual_norm_forward(const snack_norm_args *args,
   n.r = r;
   n.h = h;
   const TeamPlan p = team_forward(n);
+  plan_slabs(&n, p.teams);
   const cudaError_t e = p.threads ? launch_team_forward(n, p, static_cast<cudaStream_t>(stream))
                                   : launch_forward(n, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "residual norm launch");
