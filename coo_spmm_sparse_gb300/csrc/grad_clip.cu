@@ -73,24 +73,25 @@ __device__ __forceinline__ float block_reduce(float v, float *red) {
   return v;
 }
 
-__device__ __forceinline__ bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 template <typename T>
 struct Vec {  // 16 bytes
   static constexpr int N = 16 / sizeof(T);
   uint4 raw;
   __device__ __forceinline__ void load(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
-  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = raw; }
   __device__ __forceinline__ float get(int i) const { return to_float(reinterpret_cast<const T *>(&raw)[i]); }
-  __device__ __forceinline__ void set(int i, float v) { reinterpret_cast<T *>(&raw)[i] = from_float<T>(v); }
 };
 
 template <typename T, bool MAX>
 __device__ __forceinline__ void norm_chunk(const T *p, int n, float (&acc)[4]) {
   constexpr int V = Vec<T>::N;
   const int tid = threadIdx.x;
+  // elements before the first whole vector
+  const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
+  if (tid < head) take<MAX>(acc[0], to_float(p[tid]));
+  p += head;
+  n -= head;
   int done = 0;
-  if (aligned(p)) {
+  {
     const int nv = n / V;
     int i = tid;
     for (; i + 3 * kThreads < nv; i += 4 * kThreads) {
@@ -118,8 +119,9 @@ __global__ void __launch_bounds__(kThreads) norm_partials(const __grid_constant_
                                                           float *partial) {
   __shared__ float red[32];
   dependency_wait();
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float run = 0.f;  // over the chunks; within one, four sums of a thread
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const int k = tensor_of(t, (uint32_t)c);
     const int64_t at = (c - t.first[k]) * (int64_t)t.chunk_elems;
     const int64_t left = t.n[k] - at;
@@ -130,10 +132,11 @@ __global__ void __launch_bounds__(kThreads) norm_partials(const __grid_constant_
       norm_chunk<__nv_bfloat16, MAX>(static_cast<const __nv_bfloat16 *>(t.src[k]) + at, n, acc);
     else
       norm_chunk<__half, MAX>(static_cast<const __half *>(t.src[k]) + at, n, acc);
+    const float v = MAX ? max_nan(max_nan(acc[0], acc[1]), max_nan(acc[2], acc[3]))
+                        : (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    run = MAX ? max_nan(v, run) : run + v;
   }
-  const float v = MAX ? max_nan(max_nan(acc[0], acc[1]), max_nan(acc[2], acc[3]))
-                      : (acc[0] + acc[1]) + (acc[2] + acc[3]);
-  const float s = block_reduce<MAX>(v, red);
+  const float s = block_reduce<MAX>(run, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -154,31 +157,59 @@ __global__ void __launch_bounds__(kThreads) norm_finish(const float *partial, in
   if (threadIdx.x == 0) *norm = v;
 }
 
+// Scales a chunk.  A thread takes the 16 bytes of results at one place; its
+// elements of the source are one vector, or two where the results are the
+// smaller type, if that lies on a 16-byte boundary too.  Where source and
+// result lie differently (gradients packed end to end), results go by whole
+// vectors and elements come singly, which the L1 turns into whole lines.
 template <typename S, typename D>
 __device__ __forceinline__ void scale_chunk(const S *p, D *q, int n, float coef) {
-  constexpr int V = Vec<S>::N;
+  constexpr int V = 16 / sizeof(D), U = 4;
   const int tid = threadIdx.x;
-  int done = 0;
-  if (aligned(p) && aligned(q)) {
-    const int nv = n / V;
-    for (int i = tid; i < nv; i += kThreads) {
-      Vec<S> v;
-      v.load(p + (int64_t)i * V);
-      alignas(16) D out[V];
+  // elements before the first whole vector of results
+  const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(q) & 15)) & 15) / (int)sizeof(D));
+  const int nv = (n - head) / V;
+  const S *pv = p + head;
+  D *qv = q + head;
+  constexpr int SB = V * sizeof(S);  // bytes of the source for one vector of results: 8, 16 or 32
+  const bool vec = (reinterpret_cast<uintptr_t>(pv) & (SB < 16 ? SB - 1 : 15)) == 0;
+  for (int i0 = tid; i0 < nv; i0 += U * kThreads) {
+    alignas(16) S in[U][V];
+    if (vec) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) out[j] = from_float<D>(v.get(j) * coef);
-      D *at = q + (int64_t)i * V;
-#pragma unroll
-      for (int j = 0; j < V; j += 16 / (int)sizeof(D)) {
-        if constexpr (V * sizeof(D) >= 16)
-          *reinterpret_cast<uint4 *>(at + j) = *reinterpret_cast<const uint4 *>(out + j);
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i >= nv) continue;
+        if constexpr (SB == 8)
+          *reinterpret_cast<uint2 *>(in[u]) = *reinterpret_cast<const uint2 *>(pv + (int64_t)i * V);
         else
-          *reinterpret_cast<uint2 *>(at + j) = *reinterpret_cast<const uint2 *>(out + j);
+#pragma unroll
+          for (int b = 0; b < SB / 16; ++b)
+            reinterpret_cast<uint4 *>(in[u])[b] = reinterpret_cast<const uint4 *>(pv + (int64_t)i * V)[b];
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kThreads;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (i < nv) in[u][j] = pv[(int64_t)i * V + j];
       }
     }
-    done = nv * V;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= nv) continue;
+      alignas(16) D out[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) out[j] = from_float<D>(to_float(in[u][j]) * coef);
+      *reinterpret_cast<uint4 *>(qv + (int64_t)i * V) = *reinterpret_cast<const uint4 *>(out);
+    }
   }
-  for (int i = done + tid; i < n; i += kThreads) q[i] = from_float<D>(to_float(p[i]) * coef);
+  // fewer than V elements on either side
+  if (tid < head) q[tid] = from_float<D>(to_float(p[tid]) * coef);
+  const int tail = head + nv * V;
+  if (tid < n - tail) q[tail + tid] = from_float<D>(to_float(p[tail + tid]) * coef);
 }
 
 template <typename S>
@@ -201,7 +232,9 @@ __global__ void __launch_bounds__(kThreads) scale_tensors(const __grid_constant_
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   const float ratio = max_norm / (total + eps);
   const float coef = ratio >= 1.f ? 1.f : ratio;  // a NaN stays
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  // from the last chunk back: what the norm read last is still in L2
+  for (int64_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
+    const int64_t c = t.chunks - 1 - i;
     const int k = tensor_of(t, (uint32_t)c);
     // in place and nothing to clip: what would be written is there already
     if (coef == 1.f && t.dst[k] == t.src[k]) continue;

@@ -315,7 +315,7 @@ cudaError_t launch_team(K kern, const TeamPlan &p, int64_t teams, const TeamArgs
 // The forms of a call that are compiled on their own, because their many
 // calls leave no room for the tests and registers of the others: a branch, a
 // norm after it, all results wanted, no gate that belongs to a row, no bias
-// of an rms norm; rows of vectors in one block.
+// of an rms norm; rows in one block.
 enum Form { kAny = 0, kFast = 1, kFastPost = 2 };
 
 // Returns the launch of KERNEL<TS, TB, stages, vectors, cluster, layer norm,
@@ -334,13 +334,17 @@ enum Form { kAny = 0, kFast = 1, kFastPost = 2 };
   }
 #define SNACK_TEAM_F(KERNEL, TS, TB, L)                                                           \
   {                                                                                               \
-    if (form == kFastPost) return launch_team(KERNEL<TS, TB, 3, true, false, L, kFastPost>, p, teams, q, s); \
-    return launch_team(KERNEL<TS, TB, 3, true, false, L, kFast>, p, teams, q, s);                 \
+    if (p.vec) {                                                                                  \
+      if (form == kFastPost) return launch_team(KERNEL<TS, TB, 3, true, false, L, kFastPost>, p, teams, q, s); \
+      return launch_team(KERNEL<TS, TB, 3, true, false, L, kFast>, p, teams, q, s);               \
+    }                                                                                             \
+    if (form == kFastPost) return launch_team(KERNEL<TS, TB, 3, false, false, L, kFastPost>, p, teams, q, s); \
+    return launch_team(KERNEL<TS, TB, 3, false, false, L, kFast>, p, teams, q, s);                \
   }
 #define SNACK_TEAM(KERNEL, TS, TB)                                                                \
   {                                                                                               \
     const bool layer = q.n.a.norm_kind == SNACK_NORM_LAYER;                                       \
-    if (form != kAny && p.vec && p.stages == 3 && p.cluster == 1) {                               \
+    if (form != kAny && p.stages == 3 && p.cluster == 1) {                               \
       if (layer) SNACK_TEAM_F(KERNEL, TS, TB, true)                                               \
       else SNACK_TEAM_F(KERNEL, TS, TB, false)                                                    \
     }                                                                                             \
