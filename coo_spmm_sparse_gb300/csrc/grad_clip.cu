@@ -9,8 +9,7 @@
 // turn.  Every block leaves one partial sum; whoever needs the norm adds the
 // partials in their order, so that no atomic decides a result's bits.
 #include <algorithm>
-#include <cmath>
-#include <vector>
+#include <type_traits>
 
 #include "dense_ops.cuh"
 
@@ -115,7 +114,7 @@ __device__ __forceinline__ void norm_chunk(const T *p, int n, float (&acc)[4]) {
 }
 
 template <int K, bool MAX>
-__global__ void __launch_bounds__(kThreads) norm_partials(const __grid_constant__ TensorTable<K> t,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_partials(const __grid_constant__ TensorTable<K> t,
                                                           float *partial) {
   __shared__ float red[32];
   dependency_wait();
@@ -157,53 +156,115 @@ __global__ void __launch_bounds__(kThreads) norm_finish(const float *partial, in
   if (threadIdx.x == 0) *norm = v;
 }
 
-// Scales a chunk.  A thread takes the 16 bytes of results at one place; its
-// elements of the source are one vector, or two where the results are the
-// smaller type, if that lies on a 16-byte boundary too.  Where source and
-// result lie differently (gradients packed end to end), results go by whole
-// vectors and elements come singly, which the L1 turns into whole lines.
+// Loads that are the last of their bytes and stores that nothing reads soon
+// leave the L2 to what the norm's pass left in it.
+__device__ __forceinline__ uint2 take_last(const uint2 *p) { return __ldcs(p); }
+__device__ __forceinline__ uint4 take_last(const uint4 *p) { return __ldcs(p); }
+
+__device__ __forceinline__ void words_of(uint2 x, uint32_t *w) {
+  w[0] = x.x;
+  w[1] = x.y;
+}
+__device__ __forceinline__ void words_of(uint4 x, uint32_t *w) {
+  w[0] = x.x;
+  w[1] = x.y;
+  w[2] = x.z;
+  w[3] = x.w;
+}
+
+// N pieces of P (8 or 16 bytes) from the address p on, any multiple of the
+// element size: the aligned pieces that hold them, moved down by the `off`
+// bytes by which p lies above the first.  No piece is read that holds none
+// of them.
+template <typename P, int N>
+__device__ __forceinline__ void load_shifted(const char *p, int off, uint32_t (&w)[N * sizeof(P) / 4]) {
+  constexpr int PW = sizeof(P) / 4, W = N * PW;
+  const P *at = reinterpret_cast<const P *>(p - off);
+  uint32_t v[W + PW];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) {
+    P x = {};
+    if (i < N || off) x = at[i];  // its neighbour reads it too
+    words_of(x, v + i * PW);
+  }
+  if (PW == 4)
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) v[i] = off & 8 ? v[i + 2] : v[i];
+#pragma unroll
+  for (int i = 0; i < W + 1; ++i) v[i] = off & 4 ? v[i + 1] : v[i];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = off & 2 ? __funnelshift_r(v[i], v[i + 1], 16) : v[i];
+}
+
+// Scales a chunk.  A thread takes the 16 bytes of results at one place;
+// where their source does not lie on a boundary of its own size (gradients
+// packed end to end), it is moved into place in registers.  (Single elements
+// took 773 us for 400 M bf16 packed into fp32; 32 bytes of results for a
+// thread, which leaves half sectors to each store, 445 us.)
 template <typename S, typename D>
 __device__ __forceinline__ void scale_chunk(const S *p, D *q, int n, float coef) {
-  constexpr int V = 16 / sizeof(D), U = 4;
+  constexpr int V = 16 / sizeof(D), SB = V * sizeof(S);  // 8, 16 or 32 bytes of the source
+  using P = std::conditional_t<SB == 8, uint2, uint4>;
+  constexpr int N = SB / sizeof(P), W = SB / 4;
   const int tid = threadIdx.x;
   // elements before the first whole vector of results
   const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(q) & 15)) & 15) / (int)sizeof(D));
   const int nv = (n - head) / V;
-  const S *pv = p + head;
-  D *qv = q + head;
-  constexpr int SB = V * sizeof(S);  // bytes of the source for one vector of results: 8, 16 or 32
-  const bool vec = (reinterpret_cast<uintptr_t>(pv) & (SB < 16 ? SB - 1 : 15)) == 0;
-  for (int i0 = tid; i0 < nv; i0 += U * kThreads) {
-    alignas(16) S in[U][V];
-    if (vec) {
+  const char *pv = reinterpret_cast<const char *>(p + head);
+  uint4 *qv = reinterpret_cast<uint4 *>(q + head);
+  const int off = (int)(reinterpret_cast<uintptr_t>(pv) & (sizeof(P) - 1));
+  const auto scale = [&](const uint32_t (&w)[W], int i) {
+    float f[V];
+    if constexpr (sizeof(S) == 4) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kThreads;
-        if (i >= nv) continue;
-        if constexpr (SB == 8)
-          *reinterpret_cast<uint2 *>(in[u]) = *reinterpret_cast<const uint2 *>(pv + (int64_t)i * V);
-        else
-#pragma unroll
-          for (int b = 0; b < SB / 16; ++b)
-            reinterpret_cast<uint4 *>(in[u])[b] = reinterpret_cast<const uint4 *>(pv + (int64_t)i * V)[b];
-      }
+      for (int j = 0; j < V; ++j) f[j] = __uint_as_float(w[j]) * coef;
     } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kThreads;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (i < nv) in[u][j] = pv[(int64_t)i * V + j];
+      for (int j = 0; j < V; j += 2) {
+        unpack2<S>(w[j / 2], f[j], f[j + 1]);
+        f[j] *= coef;
+        f[j + 1] *= coef;
       }
     }
+    if constexpr (sizeof(D) == 4)
+      __stcs(qv + i, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+    else
+      __stcs(qv + i, make_uint4(pack2<D>(f[0], f[1]), pack2<D>(f[2], f[3]), pack2<D>(f[4], f[5]), pack2<D>(f[6], f[7])));
+  };
+  constexpr int U = SB == 32 ? 2 : 4;
+  if (off == 0) {
+    int i = tid;
+    for (; i + (U - 1) * kThreads < nv; i += U * kThreads) {
+      uint32_t w[U][W];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      if (i >= nv) continue;
-      alignas(16) D out[V];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < V; ++j) out[j] = from_float<D>(to_float(in[u][j]) * coef);
-      *reinterpret_cast<uint4 *>(qv + (int64_t)i * V) = *reinterpret_cast<const uint4 *>(out);
+        for (int b = 0; b < N; ++b)
+          words_of(take_last(reinterpret_cast<const P *>(pv) + (int64_t)(i + u * kThreads) * N + b),
+                   w[u] + b * (int)sizeof(P) / 4);
+#pragma unroll
+      for (int u = 0; u < U; ++u) scale(w[u], i + u * kThreads);
+    }
+    for (; i < nv; i += kThreads) {
+      uint32_t w[W];
+#pragma unroll
+      for (int b = 0; b < N; ++b)
+        words_of(take_last(reinterpret_cast<const P *>(pv) + (int64_t)i * N + b), w + b * (int)sizeof(P) / 4);
+      scale(w, i);
+    }
+  } else {
+    int i = tid;
+    for (; i + (U - 1) * kThreads < nv; i += U * kThreads) {
+      uint32_t w[U][W];
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_shifted<P, N>(pv + (int64_t)(i + u * kThreads) * SB, off, w[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) scale(w[u], i + u * kThreads);
+    }
+    for (; i < nv; i += kThreads) {
+      uint32_t w[W];
+      load_shifted<P, N>(pv + (int64_t)i * SB, off, w);
+      scale(w, i);
     }
   }
   // fewer than V elements on either side
@@ -223,7 +284,7 @@ __device__ __forceinline__ void scale_chunk_to(const S *p, void *q, int dtype, i
 }
 
 template <int K, bool MAX>
-__global__ void __launch_bounds__(kThreads) scale_tensors(const __grid_constant__ TensorTable<K> t,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_tensors(const __grid_constant__ TensorTable<K> t,
                                                           const float *partial, int parts, float max_norm,
                                                           float eps, float *norm) {
   __shared__ float red[32];
