@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 4;
+constexpr int64_t kKeepBytes = int64_t(64) << 20;
 constexpr int kMostTable = 1024;  // tensors of one launch: 30 KB of the 32 KB that parameters may take
 
 template <int K>
@@ -25,6 +26,7 @@ struct TensorTable {
   int count;
   int chunk_elems;
   int64_t chunks;
+  int64_t keep_from;  // chunks from here on are read again while they are in the L2
   const void *src[K];
   void *dst[K];
   int64_t n[K];
@@ -76,12 +78,16 @@ template <typename T>
 struct Vec {  // 16 bytes
   static constexpr int N = 16 / sizeof(T);
   uint4 raw;
-  __device__ __forceinline__ void load(const T *p) { raw = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void load(const T *p, uint64_t policy) {
+    asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
+                 : "l"(p), "l"(policy));
+  }
   __device__ __forceinline__ float get(int i) const { return to_float(reinterpret_cast<const T *>(&raw)[i]); }
 };
 
 template <typename T, bool MAX>
-__device__ __forceinline__ void norm_chunk(const T *p, int n, float (&acc)[4]) {
+__device__ __forceinline__ void norm_chunk(const T *p, int n, uint64_t policy, float (&acc)[4]) {
   constexpr int V = Vec<T>::N;
   const int tid = threadIdx.x;
   // elements before the first whole vector
@@ -96,7 +102,7 @@ __device__ __forceinline__ void norm_chunk(const T *p, int n, float (&acc)[4]) {
     for (; i + 3 * kThreads < nv; i += 4 * kThreads) {
       Vec<T> v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k].load(p + (int64_t)(i + k * kThreads) * V);
+      for (int k = 0; k < 4; ++k) v[k].load(p + (int64_t)(i + k * kThreads) * V, policy);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -104,7 +110,7 @@ __device__ __forceinline__ void norm_chunk(const T *p, int n, float (&acc)[4]) {
     }
     for (; i < nv; i += kThreads) {
       Vec<T> v;
-      v.load(p + (int64_t)i * V);
+      v.load(p + (int64_t)i * V, policy);
 #pragma unroll
       for (int j = 0; j < V; ++j) take<MAX>(acc[j & 3], v.get(j));
     }
@@ -118,19 +124,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_partials(const __
                                                           float *partial) {
   __shared__ float red[32];
   dependency_wait();
+  uint64_t keep, leave;  // in the L2, for the pass that scales
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(leave));
   float run = 0.f;  // over the chunks; within one, four sums of a thread
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint64_t policy = c >= t.keep_from ? keep : leave;
     const int k = tensor_of(t, (uint32_t)c);
     const int64_t at = (c - t.first[k]) * (int64_t)t.chunk_elems;
     const int64_t left = t.n[k] - at;
     const int n = left < t.chunk_elems ? (int)left : t.chunk_elems;
     if (t.stype[k] == SNACK_F32)
-      norm_chunk<float, MAX>(static_cast<const float *>(t.src[k]) + at, n, acc);
+      norm_chunk<float, MAX>(static_cast<const float *>(t.src[k]) + at, n, policy, acc);
     else if (t.stype[k] == SNACK_BF16)
-      norm_chunk<__nv_bfloat16, MAX>(static_cast<const __nv_bfloat16 *>(t.src[k]) + at, n, acc);
+      norm_chunk<__nv_bfloat16, MAX>(static_cast<const __nv_bfloat16 *>(t.src[k]) + at, n, policy, acc);
     else
-      norm_chunk<__half, MAX>(static_cast<const __half *>(t.src[k]) + at, n, acc);
+      norm_chunk<__half, MAX>(static_cast<const __half *>(t.src[k]) + at, n, policy, acc);
     const float v = MAX ? max_nan(max_nan(acc[0], acc[1]), max_nan(acc[2], acc[3]))
                         : (acc[0] + acc[1]) + (acc[2] + acc[3]);
     run = MAX ? max_nan(v, run) : run + v;
@@ -341,6 +351,7 @@ int64_t fill(TensorTable<K> &t, const Request &q, int64_t i, int chunk) {
   t.count = 0;
   t.chunks = 0;
   t.chunk_elems = chunk;
+  t.keep_from = 0;
   for (; i < q.count && t.count < K; ++i) {
     if (q.sizes[i] == 0) continue;
     const int64_t c = (q.sizes[i] + chunk - 1) / chunk;
@@ -353,6 +364,16 @@ int64_t fill(TensorTable<K> &t, const Request &q, int64_t i, int chunk) {
     t.dtype[k] = (uint8_t)(q.outs ? q.out_types[i] : q.types[i]);
     t.first[k] = (uint32_t)t.chunks;
     t.chunks += c;
+  }
+  // the last kKeepBytes of the launch
+  int64_t bytes = 0;
+  for (int k = t.count - 1; k >= 0; --k) {
+    const int64_t e = type_bytes(t.stype[k]);
+    if (bytes + t.n[k] * e > kKeepBytes) {
+      t.keep_from = t.first[k] + std::max<int64_t>(0, t.n[k] - (kKeepBytes - bytes) / e) / chunk;
+      break;
+    }
+    bytes += t.n[k] * e;
   }
   return i;
 }
