@@ -119,9 +119,10 @@ __device__ __forceinline__ void zero_row(const AdapterArgs &q, int64_t t) {
 // Up to 1024 requests: every block works all of them out in shared memory
 // (each request compares itself with all others) and places its own share
 // of the tokens; block 0 writes the tables.
-__global__ void __launch_bounds__(kPlanThreads) plan_small(const __grid_constant__ AdapterArgs q) {
-  __shared__ int32_t off[kPlanThreads + 1], key[kPlanThreads], len[kPlanThreads], place[kPlanThreads],
-      tiles_of[kPlanThreads], red[32];
+template <int TH>
+__global__ void __launch_bounds__(TH) plan_small(const __grid_constant__ AdapterArgs q) {
+  __shared__ int32_t off[TH + 1], place[TH], red[32];
+  __shared__ int2 request[TH], leader_of[TH];  // {adapter or -1, tokens}; {adapter, tiles} of the first of each adapter
   dependency_wait();
   dependency_launch();
   const snack_adapter_args &a = q.a;
@@ -135,45 +136,40 @@ __global__ void __launch_bounds__(kPlanThreads) plan_small(const __grid_constant
   __syncthreads();
   int n = -1;
   if (r < R) {
+    const int len = off[r + 1] - off[r];
     n = a.adapter[r];
-    len[r] = off[r + 1] - off[r];
-    if (n < 0 || n >= a.adapters || len[r] == 0) n = -1;
-    key[r] = n;
+    if (n < 0 || n >= a.adapters || len == 0) n = -1;
+    request[r] = make_int2(n, n < 0 ? 0 : len);
   }
   __syncthreads();
   int first = 0, total = 0, all = 0;
   bool leader = n >= 0;
-  if (r < R)
-    for (int j = 0; j < R; ++j) {
-      const int k = key[j];
-      if (k < 0) continue;
-      const int l = len[j];
-      all += l;
-      if (k < n || (k == n && j < r)) first += l;
-      if (k == n) {
-        total += l;
-        if (j < r) leader = false;
-      }
-    }
   if (r < R) {
+#pragma unroll 8
+    for (int j = 0; j < R; ++j) {
+      const int2 o = request[j];  // no tokens where it names no adapter
+      all += o.y;
+      first += o.x < n || (o.x == n && j < r) ? o.y : 0;
+      total += o.x == n ? o.y : 0;
+      leader = leader && !(o.x == n && j < r);
+    }
     place[r] = first;
-    tiles_of[r] = leader ? (total + kTile - 1) / kTile : 0;
+    leader_of[r] = make_int2(n, leader ? (total + kTile - 1) / kTile : 0);
   }
   if (blockIdx.x == 0) {
-    for (int64_t i = r; i < a.adapters; i += kPlanThreads) q.p.index[i] = -1;
+    for (int64_t i = r; i < a.adapters; i += TH) q.p.index[i] = -1;
     __syncthreads();
     int t0 = 0, u = 0, tn = 0, un = 0;
-    if (r < R)
+    if (r < R) {
+#pragma unroll 8
       for (int j = 0; j < R; ++j) {
-        const int c = tiles_of[j];
-        if (c == 0) continue;
-        tn += c;
-        ++un;
-        if (key[j] < n) {
-          t0 += c;
-          ++u;
-        }
+        const int2 o = leader_of[j];
+        tn += o.y;
+        un += o.y > 0;
+        t0 += o.x < n ? o.y : 0;
+        u += o.x < n && o.y > 0;
       }
+    }
     if (r < R && leader) {
       q.p.index[n] = u;
       q.p.used[u] = make_int4(n, first, total, 0);
@@ -187,9 +183,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_small(const __grid_constant
     }
   }
   __syncthreads();
-  for (int64_t t = (int64_t)blockIdx.x * kPlanThreads + r; t < a.tokens; t += (int64_t)gridDim.x * kPlanThreads) {
+  for (int64_t t = (int64_t)blockIdx.x * TH + r; t < a.tokens; t += (int64_t)gridDim.x * TH) {
     const int i = request_of(off, R, (int32_t)t);
-    if (i >= 0 && key[i] >= 0)
+    if (i >= 0 && request[i].x >= 0)
       q.p.perm[place[i] + ((int32_t)t - off[i])] = (int32_t)t;
     else
       zero_row(q, t);
@@ -410,26 +406,27 @@ struct DownArgs {
   float *H;           // [tokens][rank]
 };
 
-// Steps that a lane's copies run ahead: about 96 KB a block, two blocks an SM.
+// A warp's step: two groups of K, 128 bytes of each row of X and W.
 template <int NT>
 struct DownShape {
-  static constexpr int SLOTS = 2 * (kTile / 16) + NT;  // 16-byte slots of a lane and step
-  static constexpr int STAGES = NT <= 2 ? 4 : (NT == 4 ? 3 : 2);
+  static constexpr int ROWS = kTile + NT * 8;
+  static constexpr int STAGES = 2;  // 80 to 128 KB a block, two blocks an SM up to 16 ranks
   static constexpr int LD = NT * 8 + 4;
-  static constexpr size_t RING = (size_t)kWarps * STAGES * SLOTS * 32 * 16;
+  static constexpr size_t RING = (size_t)kWarps * STAGES * ROWS * 128;
   static constexpr size_t PART = sizeof(float) * kWarps * kTile * LD;
   static constexpr size_t SMEM = RING > PART ? RING : PART;
 };
 
 // Block: one tile of kTile tokens, ranks [64 y, 64 y + 64).  Its warps take
-// pairs of groups of K (128 bytes of each row) in turn and meet in shared
-// memory at the end.
+// steps of K in turn and meet in shared memory at the end.  Eight lanes copy
+// the 128 bytes of a row; chunk c of a row lies at c ^ 4 (row & 1), where the
+// eight lanes that read together find two rows' halves in eight bank groups.
 template <typename T, int NT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const __grid_constant__ AdapterArgs q,
                                                                          const __grid_constant__ DownArgs d) {
   using S = DownShape<NT>;
   constexpr int MT = kTile / 16, E = Group<T>::E, KG = Group<T>::K;
-  constexpr int kCols = NT * 8, STAGES = S::STAGES, SLOTS = S::SLOTS;
+  constexpr int kCols = NT * 8, STAGES = S::STAGES;
   extern __shared__ uint4 smem4[];
   float *part = reinterpret_cast<float *>(smem4);  // [kWarps][kTile][LD], over the ring
   dependency_wait();
@@ -438,35 +435,29 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
   const int4 tile = q.p.tiles[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int64_t j0 = (int64_t)blockIdx.y * kRankPass;
-  const T *rows[2 * MT];
-  bool ok[2 * MT];
-#pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) {
-    const int i = m * 8 + g;
-    ok[m] = i < tile.z;
-    rows[m] = static_cast<const T *>(d.X) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.x_stride : 0);
-  }
-  const int64_t wbase = (int64_t)(d.by_used ? tile.w : tile.x) * d.rank;
-  const T *wrow = static_cast<const T *>(d.W) + (wbase + min(j0 + g, d.rank - 1)) * d.K;
-  const int ranks_left = (int)min((int64_t)kRankPass, d.rank - j0) - g;  // row n * 8 + g is there: n * 8 < ranks_left
-  uint4 *ring = smem4 + (int64_t)warp * STAGES * SLOTS * 32 + lane;
+  const T *X = static_cast<const T *>(d.X);
+  const T *W = static_cast<const T *>(d.W) + ((int64_t)(d.by_used ? tile.w : tile.x) * d.rank + j0) * d.K;
+  const int ranks = (int)min((int64_t)kRankPass, d.rank - j0);
+  // token of tile row `lane`, or -1
+  const int mine = lane < tile.z ? q.p.perm[tile.y + lane] : -1;
 
-  // step i of this warp: group ((i / 2) * kWarps + warp) * 2 + i % 2
-  const int groups = (int)((d.K + KG - 1) / KG);
-  const auto group_of = [&](int i) { return ((i >> 1) * kWarps + warp) * 2 + (i & 1); };
-  const int steps = [&] {  // steps whose group is there
-    const int whole = groups / (2 * kWarps) * 2, rest = groups % (2 * kWarps) - 2 * warp;
-    return whole + (rest <= 0 ? 0 : (rest >= 2 ? 2 : rest));
-  }();
+  const int steps = ((int)((d.K + 2 * KG - 1) / (2 * KG)) - warp + kWarps - 1) / kWarps;  // of this warp
+  uint4 *ring = smem4 + (int64_t)warp * STAGES * S::ROWS * 8;
   const auto fetch = [&](int i) {
     if (ALIGNED && i < steps) {
-      const int64_t k = (int64_t)group_of(i) * KG + t * E;
-      uint4 *slot = ring + (i % STAGES) * SLOTS * 32;
+      const int64_t k = ((int64_t)i * kWarps + warp) * 2 * KG + (lane & 7) * E;
+      uint4 *slot = ring + (i % STAGES) * S::ROWS * 8;
+      const int r = lane >> 3, at = r * 8 + ((lane & 7) ^ (4 * (r & 1)));
 #pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) copy16(slot + m * 32, rows[m], k, d.K, ok[m]);
+      for (int m = 0; m < kTile / 4; ++m) {
+        const int tok = __shfl_sync(0xffffffffu, mine, 4 * m + r);
+        copy16(slot + m * 32 + at, X + (int64_t)max(tok, 0) * d.x_stride, k, d.K, tok >= 0);
+      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        copy16(slot + (2 * MT + n) * 32, wrow + (n * 8 < ranks_left ? (int64_t)n * 8 * d.K : 0), k, d.K, n * 8 < ranks_left);
+      for (int n = 0; n < NT * 2; ++n) {
+        const int j = 4 * n + r;
+        copy16(slot + (kTile / 4 + n) * 32 + at, W + (int64_t)(j < ranks ? j : 0) * d.K, k, d.K, j < ranks);
+      }
     }
     if (ALIGNED) copies_commit();
   };
@@ -492,50 +483,61 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   for (int i = 0; i < steps; ++i) {
-    uint4 x[2 * MT], w[NT];
     if (ALIGNED) {
       copies_wait<STAGES - 2>();
-      const uint4 *slot = ring + (i % STAGES) * SLOTS * 32;
-#pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) x[m] = slot[m * 32];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) w[n] = slot[(2 * MT + n) * 32];
-      fetch(i + STAGES - 1);  // into the slots that step i - 1 has read
-    } else {
-      const int64_t k = (int64_t)group_of(i) * KG + t * E;
-#pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) x[m] = load16<T, false>(rows[m], k, d.K, ok[m]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        w[n] = load16<T, false>(wrow + (n * 8 < ranks_left ? (int64_t)n * 8 * d.K : 0), k, d.K, n * 8 < ranks_left);
+      __syncwarp();
+      fetch(i + STAGES - 1);  // into the slots that every lane read before this barrier
     }
-    if constexpr (sizeof(T) == 4) {
-      float xh[2 * MT][4], xl[2 * MT][4];
 #pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) split4(x[m], xh[m], xl[m]);
+    for (int half = 0; half < 2; ++half) {
+      uint4 x[2 * MT], w[NT];
+      if (ALIGNED) {
+        const uint4 *slot = ring + (i % STAGES) * S::ROWS * 8 + g * 8 + ((4 * half + t) ^ (4 * (g & 1)));
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float wh[4], wl[4];
-        split4(w[n], wh, wl);
+        for (int m = 0; m < 2 * MT; ++m) x[m] = slot[m * 64];
 #pragma unroll
-        for (int s = 0; s < 4; s += 2)
+        for (int n = 0; n < NT; ++n) w[n] = slot[(2 * MT + n) * 64];
+      } else {
+        const int64_t k = (((int64_t)i * kWarps + warp) * 2 + half) * KG + t * E;
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) {
+          const int tok = __shfl_sync(0xffffffffu, mine, m * 8 + g);
+          x[m] = load16<T, false>(X + (int64_t)max(tok, 0) * d.x_stride, k, d.K, tok >= 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int j = n * 8 + g;
+          w[n] = load16<T, false>(W + (int64_t)(j < ranks ? j : 0) * d.K, k, d.K, j < ranks);
+        }
+      }
+      if constexpr (sizeof(T) == 4) {
+        float xh[2 * MT][4], xl[2 * MT][4];
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) split4(x[m], xh[m], xl[m]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float wh[4], wl[4];
+          split4(w[n], wh, wl);
+#pragma unroll
+          for (int s = 0; s < 4; s += 2)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_tf32(acc[m][n], xl[2 * m][s], xl[2 * m + 1][s], xl[2 * m][s + 1], xl[2 * m + 1][s + 1], wh[s], wh[s + 1]);
+              mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wl[s], wl[s + 1]);
+              mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wh[s], wh[s + 1]);
+            }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            mma_tf32(acc[m][n], xl[2 * m][s], xl[2 * m + 1][s], xl[2 * m][s + 1], xl[2 * m + 1][s + 1], wh[s], wh[s + 1]);
-            mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wl[s], wl[s + 1]);
-            mma_tf32(acc[m][n], xh[2 * m][s], xh[2 * m + 1][s], xh[2 * m][s + 1], xh[2 * m + 1][s + 1], wh[s], wh[s + 1]);
+            mma_16<T>(acc[m][n], x[2 * m].x, x[2 * m + 1].x, x[2 * m].y, x[2 * m + 1].y, w[n].x, w[n].y);
+            mma_16<T>(acc[m][n], x[2 * m].z, x[2 * m + 1].z, x[2 * m].w, x[2 * m + 1].w, w[n].z, w[n].w);
           }
       }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma_16<T>(acc[m][n], x[2 * m].x, x[2 * m + 1].x, x[2 * m].y, x[2 * m + 1].y, w[n].x, w[n].y);
-          mma_16<T>(acc[m][n], x[2 * m].z, x[2 * m + 1].z, x[2 * m].w, x[2 * m + 1].w, w[n].z, w[n].w);
-        }
     }
-    if ((i & 3) == 3) flush();
+    if (i & 1) flush();
   }
   flush();
   copies_wait<0>();
@@ -572,6 +574,7 @@ struct UpArgs {
   int64_t y_stride, K, rank;
   bool by_used, scaled;
   int64_t blocks;     // blocks side by side over K
+  int groups;         // column groups of a warp
 };
 
 // Columns that a warp takes at once: 64 bytes of each row.
@@ -580,7 +583,7 @@ struct UpShape {
   static constexpr int E = 16 / sizeof(T);
   static constexpr int NT = E / 2;                          // 8-column products side by side
   static constexpr int COLS = 4 * E;                        // 16 or 32
-  static constexpr int GROUPS = 8;                          // column groups of a warp
+  static constexpr int GROUPS = 16;                         // most column groups of a warp
   static constexpr int PER = sizeof(T) == 4 ? 2 : 1;        // instructions for 16 ranks
   static constexpr int WBYTES = 4 * sizeof(T);              // four ranks of a weight row
   // bytes of a warp's step: its rows of Y, and the weights of RG times 16 ranks
@@ -611,7 +614,7 @@ __device__ __forceinline__ void load_ranks(const T *row, int64_t j, int64_t rank
   }
 }
 
-// Block: one tile of kTile tokens, kWarps * GROUPS column groups.  The
+// Block: one tile of kTile tokens, kWarps * groups column groups.  The
 // tile's H is kept in shared memory, split in two parts, in the order in
 // which the lanes want it.  RG: 16-rank groups (1 or 2, weights copied ahead
 // with the rows; 0: any number, weights loaded when they are needed).
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
     rows[m] = static_cast<T *>(d.Y) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.y_stride : 0);
   }
   const T *W = static_cast<const T *>(d.W) + (int64_t)(d.by_used ? tile.w : tile.x) * d.K * d.rank;
-  const int64_t first = (cblock * S::GROUPS * kWarps + warp) * S::COLS;
+  const int64_t first = (cblock * d.groups * kWarps + warp) * S::COLS;
   const auto column = [&](int c) { return first + (int64_t)c * kWarps * S::COLS; };
   // column of product n's index g: the lane that ends up with columns 2t and
   // 2t + 1 of every n holds E columns in a row
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
   const auto fetch = [&](int c) {
     if (!ALIGNED) return;
     const int64_t c0 = column(c);
-    if (c < S::GROUPS && c0 < d.K) {
+    if (c < d.groups && c0 < d.K) {
       char *at = ring + (c % STAGES) * S::step_bytes(RG);
 #pragma unroll
       for (int m = 0; m < 2 * MT; ++m)
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
   }
   __syncthreads();
   const bool wvec = d.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(d.W) & (4 * sizeof(T) - 1)) == 0;
-  for (int c = 0; c < S::GROUPS; ++c) {
+  for (int c = 0; c < d.groups; ++c) {
     const int64_t c0 = column(c);
     if (c0 >= d.K) break;
     uint4 y[2 * MT];
@@ -809,7 +812,17 @@ struct OuterArgs {
   int64_t x_stride, K, rank;
   int64_t chunk;    // places of one block
   int64_t blocks;   // blocks side by side over K
+  int64_t slices;   // chunks
   float *parts;     // [chunk index + used index][rank][K]
+  bool vec;         // the rows of X are vectors
+  void *out;        // dA or dB (null: not wanted)
+  bool scaled;      // times the adapter's scale
+  bool turned;      // out is [adapter][K][rank], not [adapter][rank][K]
+};
+
+// dB and dA: nothing keeps the two apart, so one launch does both.
+struct OuterPair {
+  OuterArgs o[2];
 };
 
 // A lane's copies: 8 KB of rows for a warp.
@@ -825,8 +838,7 @@ struct OuterShape {
 // the used.  The chunk's H lies in shared memory, a token every LD floats:
 // lane (g, t) reads rank g of token t, bank 8 t + g.
 template <typename T, int RM, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_constant__ AdapterArgs q,
-                                                          const __grid_constant__ OuterArgs d) {
+__device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArgs &d, int64_t block) {
   constexpr int E = 16 / sizeof(T), NT = E, COLS = 8 * E, LD = 16 * RM + 8;
   constexpr int TS = sizeof(T) == 4 ? 8 : 16;  // tokens of a step
   constexpr int NR = TS / 4, STAGES = OuterShape<T>::STAGES;
@@ -834,9 +846,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_consta
   extern __shared__ uint4 smem4[];             // the warps' rings, [chunk][LD] floats of H, the chunk's tokens
   float *hs = reinterpret_cast<float *>(smem4 + OuterShape<T>::RING);
   int32_t *tok = reinterpret_cast<int32_t *>(hs + d.chunk * LD);
-  dependency_wait();
-  dependency_launch();
-  const int64_t slice = blockIdx.x / d.blocks, cblock = blockIdx.x % d.blocks;
+  const int64_t slice = block / d.blocks, cblock = block % d.blocks;
   const int64_t p0 = slice * d.chunk;
   const int places = (int)(min((int64_t)q.p.head[2], p0 + d.chunk) - p0);
   if (places <= 0) return;
@@ -1022,42 +1032,98 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_consta
   }
 }
 
-// The parts of each adapter, added in order, rounded once.  TRANSPOSE: the
-// output is [adapter][K][rank].
-template <typename T, bool TRANSPOSE>
-__global__ void __launch_bounds__(kThreads) adapter_outer_finish(const __grid_constant__ AdapterArgs q,
-                                                                 const __grid_constant__ OuterArgs d, T *out,
-                                                                 bool scaled) {
+template <typename T, int RM>
+__global__ void __launch_bounds__(kThreads, 2) adapter_outer(const __grid_constant__ AdapterArgs q,
+                                                          const __grid_constant__ OuterPair pair) {
   dependency_wait();
   dependency_launch();
-  const int64_t per = d.rank * d.K, total = q.a.adapters * per;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kThreads) {
-    const int64_t n = e / per, i = e % per;
+  const int64_t first = pair.o[0].slices * pair.o[0].blocks;
+  const bool second = blockIdx.x >= first;
+  const OuterArgs &d = pair.o[second];
+  const int64_t block = second ? blockIdx.x - first : blockIdx.x;
+  if (d.vec)
+    outer_block<T, RM, true>(q, d, block);
+  else
+    outer_block<T, RM, false>(q, d, block);
+}
+
+// The parts of each adapter, added in order, rounded once.  Block: 32
+// columns of 32 ranks of one adapter (blockIdx.y); the sums turn in shared
+// memory where the output is [adapter][K][rank].
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adapter_outer_finish(const __grid_constant__ AdapterArgs q,
+                                                                 const __grid_constant__ OuterPair pair) {
+  __shared__ float turn[32][33];
+  dependency_wait();
+  dependency_launch();
+  const auto tiles = [](const OuterArgs &d) { return d.out ? (d.K + 31) / 32 * ((d.rank + 31) / 32) : 0; };
+  const int64_t first = tiles(pair.o[0]);
+  const bool second = blockIdx.x >= first;
+  const OuterArgs &d = pair.o[second];
+  const int64_t block = second ? blockIdx.x - first : blockIdx.x, across = (d.K + 31) / 32;
+  const int64_t c0 = block % across * 32, j0 = block / across * 32, per = d.rank * d.K;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  T *out = static_cast<T *>(d.out);
+  for (int64_t n = blockIdx.y; n < q.a.adapters; n += gridDim.y) {
     const int u = q.p.index[n];
-    float s = 0.f;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};  // ranks j0 + ty + 8 i
     if (u >= 0) {
       const int4 use = q.p.used[u];
       const int64_t s0 = use.y / d.chunk + u, s1 = (use.y + use.z - 1) / d.chunk + u;
-      const int64_t at = TRANSPOSE ? (i % d.rank) * d.K + i / d.rank : i;
-      for (int64_t k = s0; k <= s1; ++k) s += d.parts[k * per + at];
-      if (scaled) s *= scale_of(q.a, (int)n);
+      const float *at = d.parts + (j0 + ty) * d.K + c0 + tx;
+      const bool in = c0 + tx < d.K;
+#pragma unroll 4
+      for (int64_t k = s0; k <= s1; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in && j0 + ty + 8 * i < d.rank) s[i] += at[k * per + 8 * i * d.K];
+      if (d.scaled) {
+        const float scale = scale_of(q.a, (int)n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] *= scale;
+      }
     }
-    out[e] = from_float<T>(s);
+    if (d.turned) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turn[ty + 8 * i][tx] = s[i];
+      __syncthreads();
+      // 32 columns of min(32, rank) ranks: runs of ranks, one after another where rank <= 32
+      const int ranks = (int)min((int64_t)32, d.rank - j0), cols = (int)min((int64_t)32, d.K - c0);
+      for (int e = threadIdx.x; e < ranks * cols; e += kThreads) {
+        const int c = e / ranks, j = e % ranks;
+        out[n * per + (c0 + c) * d.rank + j0 + j] = from_float<T>(turn[j][c]);
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + tx < d.K && j0 + ty + 8 * i < d.rank)
+          out[n * per + (j0 + ty + 8 * i) * d.K + c0 + tx] = from_float<T>(s[i]);
+    }
   }
 }
 
-// Weights of the used adapters, each [rows][cols] turned to [cols][rows].
+// Weights of the used adapters, each [rows][cols] turned to [cols][rows];
+// two arrays in one launch.
+struct TurnArgs {
+  const void *in[2];
+  void *out[2];
+  int64_t rows[2], cols[2];
+};
 template <typename T>
-__global__ void __launch_bounds__(kThreads) adapter_turn(const __grid_constant__ AdapterArgs q, const T *in, T *out,
-                                                         int64_t rows, int64_t cols) {
+__global__ void __launch_bounds__(kThreads) adapter_turn(const __grid_constant__ AdapterArgs q,
+                                                         const __grid_constant__ TurnArgs a) {
   __shared__ T tile[32][33];
   dependency_wait();
   dependency_launch();
+  const int64_t first = (a.rows[0] + 31) / 32 * ((a.cols[0] + 31) / 32);
+  const int which = blockIdx.x >= first;
+  const int64_t block = which ? blockIdx.x - first : blockIdx.x, rows = a.rows[which], cols = a.cols[which];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t across = (cols + 31) / 32, r0 = blockIdx.x / across * 32, c0 = blockIdx.x % across * 32;
+  const int64_t across = (cols + 31) / 32, r0 = block / across * 32, c0 = block % across * 32;
   for (int u = blockIdx.y; u < q.p.head[1]; u += gridDim.y) {
-    const T *from = in + (int64_t)q.p.used[u].x * rows * cols;
-    T *to = out + (int64_t)u * rows * cols;
+    const T *from = static_cast<const T *>(a.in[which]) + (int64_t)q.p.used[u].x * rows * cols;
+    T *to = static_cast<T *>(a.out[which]) + (int64_t)u * rows * cols;
 #pragma unroll
     for (int i = ty; i < 32; i += 8)
       if (r0 + i < rows && c0 + tx < cols) tile[i][tx] = from[(r0 + i) * cols + c0 + tx];
@@ -1206,8 +1272,10 @@ int64_t lay_plan(const snack_adapter_args &a, Plan *p, char *ws) {
 cudaError_t launch_plan(const AdapterArgs &q, cudaStream_t s) {
   const snack_adapter_args &a = q.a;
   if (a.requests <= kPlanThreads) {
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(32, (a.tokens + kPlanThreads - 1) / kPlanThreads));
-    return launch_kernel(plan_small, dim3((unsigned)blocks), kPlanThreads, 0, true, s, q);
+    const int th = a.requests <= 128 ? 128 : kPlanThreads;
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(device_sms(), (a.tokens + th - 1) / th));
+    return launch_kernel(th == 128 ? plan_small<128> : plan_small<kPlanThreads>, dim3((unsigned)blocks), th, 0, true,
+                         s, q);
   }
   cudaError_t e = launch_kernel(plan_requests, dim3(1), kPlanThreads, 0, true, s, q);
   if (e != cudaSuccess) return e;
@@ -1243,8 +1311,11 @@ template <typename T>
 cudaError_t launch_up(const AdapterArgs &q, UpArgs d, cudaStream_t s) {
   if (q.p.max_tiles == 0) return cudaSuccess;
   using S = UpShape<T>;
-  const int64_t cols = (int64_t)kWarps * S::GROUPS * S::COLS;
-  d.blocks = (d.K + cols - 1) / cols;
+  // wide blocks prepare H less often; but two blocks an SM should all have work
+  d.groups = S::GROUPS;
+  const auto blocks = [&] { return (d.K + kWarps * d.groups * S::COLS - 1) / (kWarps * d.groups * S::COLS); };
+  while (d.groups > 4 && q.p.max_tiles * blocks() < 3 * (int64_t)device_sms()) d.groups /= 2;
+  d.blocks = blocks();
   if (q.p.max_tiles * d.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)(q.p.max_tiles * d.blocks));
   const bool wvec = d.rank % 4 == 0 && aligned_to(d.W, 4 * sizeof(T));
@@ -1273,38 +1344,46 @@ int64_t outer_bytes(const snack_adapter_args &a, int64_t K) {
   return align16(((a.tokens + chunk - 1) / chunk + used) * a.rank * K * 4);
 }
 
-template <typename T, bool TRANSPOSE>
-cudaError_t launch_outer(const AdapterArgs &q, OuterArgs d, T *out, bool scaled, cudaStream_t s) {
+// dB and dA (those whose `out` is set), then the sums of their parts.
+template <typename T>
+cudaError_t launch_outer(const AdapterArgs &q, OuterPair pair, cudaStream_t s) {
   const snack_adapter_args &a = q.a;
-  d.chunk = outer_chunk(a, d.K);
   const int64_t cols = kWarps * 8 * (16 / (int64_t)sizeof(T)), ranks = outer_ranks(a.rank);
-  d.blocks = (d.K + cols - 1) / cols;
-  const int64_t slices = (a.tokens + d.chunk - 1) / d.chunk;
-  if (slices * d.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(slices * d.blocks), (unsigned)((a.rank + ranks - 1) / ranks));
+  int64_t blocks = 0, tiles = 0, chunk = 0;
+  for (OuterArgs &d : pair.o) {
+    if (!d.out) continue;
+    d.chunk = outer_chunk(a, d.K);
+    d.blocks = (d.K + cols - 1) / cols;
+    d.slices = (a.tokens + d.chunk - 1) / d.chunk;
+    d.vec = vector_rows(d.X, d.x_stride, d.K, a.type);
+    blocks += d.slices * d.blocks;
+    tiles += (d.K + 31) / 32 * ((d.rank + 31) / 32);
+    chunk = std::max(chunk, d.chunk);
+  }
+  if (blocks > 0x7fffffffLL || tiles > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;
   if (q.p.max_used > 0) {
-    const bool vec = vector_rows(d.X, d.x_stride, d.K, a.type);
-    auto k = ranks == 16 ? (vec ? adapter_outer<T, 1, true> : adapter_outer<T, 1, false>)
-                         : (vec ? adapter_outer<T, 2, true> : adapter_outer<T, 2, false>);
-    const size_t smem = (size_t)OuterShape<T>::RING * 16 + (size_t)d.chunk * (ranks + 8 + 1) * 4;
+    auto k = ranks == 16 ? adapter_outer<T, 1> : adapter_outer<T, 2>;
+    const size_t smem = (size_t)OuterShape<T>::RING * 16 + (size_t)chunk * (ranks + 8 + 1) * 4;
     if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
-    if ((e = launch_kernel(k, grid, kThreads, smem, true, s, q, d)) != cudaSuccess) return e;
+    const dim3 grid((unsigned)blocks, (unsigned)((a.rank + ranks - 1) / ranks));
+    if ((e = launch_kernel(k, grid, kThreads, smem, true, s, q, pair)) != cudaSuccess) return e;
   }
-  const int64_t total = a.adapters * a.rank * d.K;
-  const int64_t blocks = std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)device_sms() * 8);
-  return launch_kernel(adapter_outer_finish<T, TRANSPOSE>, dim3((unsigned)blocks), kThreads, 0, true, s, q, d, out,
-                       scaled);
+  const dim3 grid((unsigned)tiles, (unsigned)std::min<int64_t>(a.adapters, 65535));
+  return launch_kernel(adapter_outer_finish<T>, grid, kThreads, 0, true, s, q, pair);
 }
 
+// Turns B (and A, where dX is wanted) of the used adapters.
 template <typename T>
-cudaError_t launch_turn(const AdapterArgs &q, const void *in, void *out, int64_t rows, int64_t cols, cudaStream_t s) {
+cudaError_t launch_turn(const AdapterArgs &q, void *Bt, void *At, cudaStream_t s) {
+  const snack_adapter_args &a = q.a;
   if (q.p.max_used == 0) return cudaSuccess;
-  const int64_t blocks = (rows + 31) / 32 * ((cols + 31) / 32);
+  const TurnArgs t = {{a.B, a.A}, {Bt, At}, {a.out, a.rank}, {a.rank, a.in}};
+  int64_t blocks = 0;
+  for (int i = 0; i < (At ? 2 : 1); ++i) blocks += (t.rows[i] + 31) / 32 * ((t.cols[i] + 31) / 32);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>(q.p.max_used, 65535));
-  return launch_kernel(adapter_turn<T>, grid, kThreads, 0, true, s, q, static_cast<const T *>(in),
-                       static_cast<T *>(out), rows, cols);
+  return launch_kernel(adapter_turn<T>, grid, kThreads, 0, true, s, q, t);
 }
 
 template <typename T>
@@ -1324,7 +1403,7 @@ cudaError_t forward(const AdapterArgs &q, void *Y, int64_t y_stride, cudaStream_
   if (e != cudaSuccess) return e;
   const DownArgs d = {a.X, a.A, a.x_stride, a.in, a.rank, false, false, q.H};
   if ((e = launch_down<T>(q, d, s)) != cudaSuccess) return e;
-  const UpArgs u = {q.H, a.B, Y, y_stride, a.out, a.rank, false, true, 0};
+  const UpArgs u = {q.H, a.B, Y, y_stride, a.out, a.rank, false, true, 0, 0};
   return launch_up<T>(q, u, s);
 }
 
@@ -1337,7 +1416,7 @@ struct Back {
   void *dA, *dB;
   float *dH;      // [tokens][rank]
   void *At, *Bt;  // [used][in][rank], [used][rank][out]
-  float *parts;
+  float *parts_a, *parts_b;
 };
 
 template <typename T>
@@ -1346,22 +1425,19 @@ cudaError_t backward(const AdapterArgs &q, const Back &b, cudaStream_t s) {
   cudaError_t e = launch_plan(q, s);
   if (e != cudaSuccess) return e;
   if (b.dX || b.dA) {
-    if ((e = launch_turn<T>(q, a.B, b.Bt, a.out, a.rank, s)) != cudaSuccess) return e;
+    if ((e = launch_turn<T>(q, b.Bt, b.dX ? b.At : nullptr, s)) != cudaSuccess) return e;
     const DownArgs d = {b.dY, b.Bt, b.dy_stride, a.out, a.rank, true, true, b.dH};
     if ((e = launch_down<T>(q, d, s)) != cudaSuccess) return e;
   }
-  if (b.dB) {
-    const OuterArgs o = {b.H, b.dY, b.dy_stride, a.out, a.rank, 0, 0, b.parts};
-    if ((e = launch_outer<T, true>(q, o, static_cast<T *>(b.dB), true, s)) != cudaSuccess) return e;
-  }
   if (b.dX) {
-    if ((e = launch_turn<T>(q, a.A, b.At, a.rank, a.in, s)) != cudaSuccess) return e;
-    const UpArgs u = {b.dH, b.At, b.dX, b.dx_stride, a.in, a.rank, true, false, 0};
+    const UpArgs u = {b.dH, b.At, b.dX, b.dx_stride, a.in, a.rank, true, false, 0, 0};
     if ((e = launch_up<T>(q, u, s)) != cudaSuccess) return e;
   }
-  if (b.dA) {
-    const OuterArgs o = {b.dH, a.X, a.x_stride, a.in, a.rank, 0, 0, b.parts};
-    if ((e = launch_outer<T, false>(q, o, static_cast<T *>(b.dA), false, s)) != cudaSuccess) return e;
+  if (b.dA || b.dB) {
+    OuterPair pair = {};
+    pair.o[0] = {b.H, b.dY, b.dy_stride, a.out, a.rank, 0, 0, 0, b.parts_b, false, b.dB, true, true};
+    pair.o[1] = {b.dH, a.X, a.x_stride, a.in, a.rank, 0, 0, 0, b.parts_a, false, b.dA, false, false};
+    if ((e = launch_outer<T>(q, pair, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -1407,7 +1483,7 @@ namespace snack {
 namespace {
 
 // The backward's scratch: the plan, dH, turned weights of the used adapters,
-// parts of dA or dB (one after the other).
+// parts of dA and dB.
 int64_t lay_back(const snack_adapter_args &a, Plan *p, Back *b, char *ws) {
   int64_t at = lay_plan(a, p, ws);
   const auto take = [&](int64_t bytes) {
@@ -1419,7 +1495,8 @@ int64_t lay_back(const snack_adapter_args &a, Plan *p, Back *b, char *ws) {
   b->dH = reinterpret_cast<float *>(take(a.tokens * a.rank * 4));
   b->At = take(p->max_used * a.in * a.rank * e);
   b->Bt = take(p->max_used * a.out * a.rank * e);
-  b->parts = reinterpret_cast<float *>(take(std::max(outer_bytes(a, a.in), outer_bytes(a, a.out))));
+  b->parts_a = reinterpret_cast<float *>(take(outer_bytes(a, a.in)));
+  b->parts_b = reinterpret_cast<float *>(take(outer_bytes(a, a.out)));
   return at;
 }
 
