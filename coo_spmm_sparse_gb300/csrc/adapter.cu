@@ -573,8 +573,6 @@ struct UpArgs {
   void *Y;            // rows of K elements, y_stride apart, added to
   int64_t y_stride, K, rank;
   bool by_used, scaled;
-  int64_t blocks;     // blocks side by side over K
-  int groups;         // column groups of a warp
 };
 
 // Columns that a warp takes at once: 64 bytes of each row.
@@ -583,7 +581,7 @@ struct UpShape {
   static constexpr int E = 16 / sizeof(T);
   static constexpr int NT = E / 2;                          // 8-column products side by side
   static constexpr int COLS = 4 * E;                        // 16 or 32
-  static constexpr int GROUPS = 16;                         // most column groups of a warp
+  static constexpr int BLOCK = kWarps * COLS;               // columns that a block takes at once
   static constexpr int PER = sizeof(T) == 4 ? 2 : 1;        // instructions for 16 ranks
   static constexpr int WBYTES = 4 * sizeof(T);              // four ranks of a weight row
   // bytes of a warp's step: its rows of Y, and the weights of RG times 16 ranks
@@ -614,10 +612,12 @@ __device__ __forceinline__ void load_ranks(const T *row, int64_t j, int64_t rank
   }
 }
 
-// Block: one tile of kTile tokens, kWarps * groups column groups.  The
-// tile's H is kept in shared memory, split in two parts, in the order in
-// which the lanes want it.  RG: 16-rank groups (1 or 2, weights copied ahead
-// with the rows; 0: any number, weights loaded when they are needed).
+// Every block takes an equal run of the (tile, column block) pairs, tile by
+// tile, so that all end together (a block for each tile and a few columns
+// left a fifth of the SMs' time idle).  A tile's H is kept in shared memory,
+// split in two parts, in the order in which the lanes want it.  RG: 16-rank
+// groups (1 or 2, weights copied ahead with the rows; 0: any number, weights
+// loaded when they are needed).
 template <typename T, int RG, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant__ AdapterArgs q,
                                                           const __grid_constant__ UpArgs d) {
@@ -627,181 +627,187 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
   extern __shared__ uint4 frag[];            // [16-rank groups][MT][2 (high and low)][PER][32 lanes], then the rings
   dependency_wait();
   dependency_launch();
-  const int64_t which = blockIdx.x / d.blocks, cblock = blockIdx.x % d.blocks;
-  if (which >= q.p.head[0]) return;
-  const int4 tile = q.p.tiles[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int rg = RG > 0 ? RG : (int)((d.rank + 15) / 16);
-  T *rows[2 * MT];
-  bool ok[2 * MT];
-#pragma unroll
-  for (int m = 0; m < 2 * MT; ++m) {
-    const int i = m * 8 + g;
-    ok[m] = i < tile.z;
-    rows[m] = static_cast<T *>(d.Y) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.y_stride : 0);
-  }
-  const T *W = static_cast<const T *>(d.W) + (int64_t)(d.by_used ? tile.w : tile.x) * d.K * d.rank;
-  const int64_t first = (cblock * d.groups * kWarps + warp) * S::COLS;
-  const auto column = [&](int c) { return first + (int64_t)c * kWarps * S::COLS; };
   // column of product n's index g: the lane that ends up with columns 2t and
   // 2t + 1 of every n holds E columns in a row
   const int gcol = (g >> 1) * E + (g & 1);
   char *ring = reinterpret_cast<char *>(frag) + S::frag_bytes(d.rank) + (size_t)warp * STAGES * S::step_bytes(RG);
-  const auto fetch = [&](int c) {
-    if (!ALIGNED) return;
-    const int64_t c0 = column(c);
-    if (c < d.groups && c0 < d.K) {
-      char *at = ring + (c % STAGES) * S::step_bytes(RG);
-#pragma unroll
-      for (int m = 0; m < 2 * MT; ++m)
-        copy16(reinterpret_cast<uint4 *>(at) + m * 32 + lane, rows[m], c0 + t * E, d.K, ok[m]);
-      if (AHEAD) {
-        at += 2 * MT * 512;
-#pragma unroll
-        for (int k = 0; k < RG; ++k)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int64_t col = c0 + gcol + 2 * n;
-            const T *row = W + (col < d.K ? col * d.rank : 0);
-            char *slot = at + ((k * NT + n) * 32 + lane) * S::WBYTES;
-            if constexpr (sizeof(T) == 4)
-              copy16(reinterpret_cast<uint4 *>(slot), row, k * 16 + 4 * t, d.rank, col < d.K);
-            else
-              copy8(reinterpret_cast<uint2 *>(slot), row, k * 16 + 4 * t, d.rank, col < d.K);
-          }
-      }
-    }
-    copies_commit();
-  };
-#pragma unroll
-  for (int c = 0; c < STAGES - 1; ++c) fetch(c);
-
-  const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
-  for (int i = warp; i < rg * MT; i += kWarps) {
-    const int m = i % MT, k = i / MT;
-    float h[2][4];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = m * 16 + half * 8 + g;
-      const float *at = d.H + (row < tile.z ? (int64_t)q.p.perm[tile.y + row] * d.rank : 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t j = k * 16 + 4 * t + e;
-        h[half][e] = row < tile.z && j < d.rank ? at[j] * scale : 0.f;
-      }
-    }
-    uint4 *to = frag + (int64_t)(k * MT + m) * 2 * PER * 32 + lane;
-    if constexpr (sizeof(T) == 4) {
-      float hi[2][4], lo[2][4];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi[half][e] = tf32_of(h[half][e]);
-          lo[half][e] = h[half][e] - hi[half][e];
-        }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        to[(0 * PER + s) * 32] = make_uint4(__float_as_uint(hi[0][2 * s]), __float_as_uint(hi[1][2 * s]),
-                                            __float_as_uint(hi[0][2 * s + 1]), __float_as_uint(hi[1][2 * s + 1]));
-        to[(1 * PER + s) * 32] = make_uint4(__float_as_uint(lo[0][2 * s]), __float_as_uint(lo[1][2 * s]),
-                                            __float_as_uint(lo[0][2 * s + 1]), __float_as_uint(lo[1][2 * s + 1]));
-      }
-    } else {
-      uint4 hi, lo;
-      split_pair<T>(h[0][0], h[0][1], hi.x, lo.x);
-      split_pair<T>(h[1][0], h[1][1], hi.y, lo.y);
-      split_pair<T>(h[0][2], h[0][3], hi.z, lo.z);
-      split_pair<T>(h[1][2], h[1][3], hi.w, lo.w);
-      to[0] = hi;
-      to[32] = lo;
-    }
-  }
-  __syncthreads();
   const bool wvec = d.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(d.W) & (4 * sizeof(T) - 1)) == 0;
-  for (int c = 0; c < d.groups; ++c) {
-    const int64_t c0 = column(c);
-    if (c0 >= d.K) break;
-    uint4 y[2 * MT];
-    const char *at = ring + (c % STAGES) * S::step_bytes(RG);
-    if (ALIGNED) {
-      copies_wait<STAGES - 2>();
+  const int across = (int)((d.K + S::BLOCK - 1) / S::BLOCK);  // column blocks of a tile
+  const int64_t all = (int64_t)q.p.head[0] * across;
+  const int64_t u1 = all * (blockIdx.x + 1) / gridDim.x;
+  int count;  // column blocks of the tile at hand
+  for (int64_t u = all * blockIdx.x / gridDim.x; u < u1; u += count) {
+    const int4 tile = q.p.tiles[u / across];
+    const int c0_block = (int)(u % across);
+    count = (int)min((int64_t)(across - c0_block), u1 - u);
+    T *rows[2 * MT];
+    bool ok[2 * MT];
 #pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) y[m] = reinterpret_cast<const uint4 *>(at)[m * 32 + lane];
-    } else {
-#pragma unroll
-      for (int m = 0; m < 2 * MT; ++m) y[m] = load16<T, false>(rows[m], c0 + t * E, d.K, ok[m]);
+    for (int m = 0; m < 2 * MT; ++m) {
+      const int i = m * 8 + g;
+      ok[m] = i < tile.z;
+      rows[m] = static_cast<T *>(d.Y) + (ok[m] ? (int64_t)q.p.perm[tile.y + i] * d.y_stride : 0);
     }
-    float acc[MT][NT][4];
+    const T *W = static_cast<const T *>(d.W) + (int64_t)(d.by_used ? tile.w : tile.x) * d.K * d.rank;
+    const auto column = [&](int c) { return ((int64_t)(c0_block + c) * kWarps + warp) * S::COLS; };
+    const auto fetch = [&](int c) {
+      if (!ALIGNED) return;
+      const int64_t c0 = column(c);
+      if (c < count && c0 < d.K) {
+        char *at = ring + (c % STAGES) * S::step_bytes(RG);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-#pragma unroll(RG > 0 ? RG : 1)
-    for (int k = 0; k < rg; ++k) {
-      const uint4 *from = frag + (int64_t)k * MT * 2 * PER * 32 + lane;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        alignas(16) T w[4];
+        for (int m = 0; m < 2 * MT; ++m)
+          copy16(reinterpret_cast<uint4 *>(at) + m * 32 + lane, rows[m], c0 + t * E, d.K, ok[m]);
         if (AHEAD) {
-          const char *slot = at + 2 * MT * 512 + ((k * NT + n) * 32 + lane) * S::WBYTES;
-          if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(slot);
-          else
-            *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(slot);
-        } else {
-          const int64_t col = c0 + gcol + 2 * n;
-          load_ranks(W + (col < d.K ? col * d.rank : 0), (int64_t)k * 16 + 4 * t, d.rank, wvec, col < d.K, w);
-        }
-        if constexpr (sizeof(T) == 4) {
-          float wh[4], wl[4];
-          split4(*reinterpret_cast<const uint4 *>(w), wh, wl);
+          at += 2 * MT * 512;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int k = 0; k < RG; ++k)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint4 h = from[((m * 2 + 0) * PER + s) * 32], l = from[((m * 2 + 1) * PER + s) * 32];
-              const auto f = [](uint32_t v) { return __uint_as_float(v); };
-              mma_tf32(acc[m][n], f(l.x), f(l.y), f(l.z), f(l.w), wh[2 * s], wh[2 * s + 1]);
-              mma_tf32(acc[m][n], f(h.x), f(h.y), f(h.z), f(h.w), wl[2 * s], wl[2 * s + 1]);
-              mma_tf32(acc[m][n], f(h.x), f(h.y), f(h.z), f(h.w), wh[2 * s], wh[2 * s + 1]);
+            for (int n = 0; n < NT; ++n) {
+              const int64_t col = c0 + gcol + 2 * n;
+              const T *row = W + (col < d.K ? col * d.rank : 0);
+              char *slot = at + ((k * NT + n) * 32 + lane) * S::WBYTES;
+              if constexpr (sizeof(T) == 4)
+                copy16(reinterpret_cast<uint4 *>(slot), row, k * 16 + 4 * t, d.rank, col < d.K);
+              else
+                copy8(reinterpret_cast<uint2 *>(slot), row, k * 16 + 4 * t, d.rank, col < d.K);
             }
-        } else {
-          const uint2 b = *reinterpret_cast<const uint2 *>(w);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint4 h = from[(m * 2 + 0) * 32], l = from[(m * 2 + 1) * 32];
-            mma_16<T>(acc[m][n], l.x, l.y, l.z, l.w, b.x, b.y);
-            mma_16<T>(acc[m][n], h.x, h.y, h.z, h.w, b.x, b.y);
-          }
         }
       }
-    }
-    fetch(c + STAGES - 1);  // into the slots that step c - 1 has read
+      copies_commit();
+    };
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int c = 0; c < STAGES - 1; ++c) fetch(c);
+
+    const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
+    for (int i = warp; i < rg * MT; i += kWarps) {
+      const int m = i % MT, k = i / MT;
+      float h[2][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!ok[2 * m + half]) continue;
-        T *e = reinterpret_cast<T *>(&y[2 * m + half]);
+        const int row = m * 16 + half * 8 + g;
+        const float *at = d.H + (row < tile.z ? (int64_t)q.p.perm[tile.y + row] * d.rank : 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t j = k * 16 + 4 * t + e;
+          h[half][e] = row < tile.z && j < d.rank ? at[j] * scale : 0.f;
+        }
+      }
+      uint4 *to = frag + (int64_t)(k * MT + m) * 2 * PER * 32 + lane;
+      if constexpr (sizeof(T) == 4) {
+        float hi[2][4], lo[2][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hi[half][e] = tf32_of(h[half][e]);
+            lo[half][e] = h[half][e] - hi[half][e];
+          }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          to[(0 * PER + s) * 32] = make_uint4(__float_as_uint(hi[0][2 * s]), __float_as_uint(hi[1][2 * s]),
+                                              __float_as_uint(hi[0][2 * s + 1]), __float_as_uint(hi[1][2 * s + 1]));
+          to[(1 * PER + s) * 32] = make_uint4(__float_as_uint(lo[0][2 * s]), __float_as_uint(lo[1][2 * s]),
+                                              __float_as_uint(lo[0][2 * s + 1]), __float_as_uint(lo[1][2 * s + 1]));
+        }
+      } else {
+        uint4 hi, lo;
+        split_pair<T>(h[0][0], h[0][1], hi.x, lo.x);
+        split_pair<T>(h[1][0], h[1][1], hi.y, lo.y);
+        split_pair<T>(h[0][2], h[0][3], hi.z, lo.z);
+        split_pair<T>(h[1][2], h[1][3], hi.w, lo.w);
+        to[0] = hi;
+        to[32] = lo;
+      }
+    }
+    __syncthreads();
+    for (int c = 0; c < count; ++c) {
+      const int64_t c0 = column(c);
+      if (c0 >= d.K) break;
+      uint4 y[2 * MT];
+      const char *at = ring + (c % STAGES) * S::step_bytes(RG);
+      if (ALIGNED) {
+        copies_wait<STAGES - 2>();
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) y[m] = reinterpret_cast<const uint4 *>(at)[m * 32 + lane];
+      } else {
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) y[m] = load16<T, false>(rows[m], c0 + t * E, d.K, ok[m]);
+      }
+      float acc[MT][NT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            e[2 * n + i] = from_float<T>(to_float(e[2 * n + i]) + acc[m][n][2 * half + i]);
-        T *to = rows[2 * m + half] + c0 + t * E;
-        if (ALIGNED) {
-          if (c0 + t * E < d.K) *reinterpret_cast<uint4 *>(to) = y[2 * m + half];
-        } else {
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+#pragma unroll(RG > 0 ? RG : 1)
+      for (int k = 0; k < rg; ++k) {
+        const uint4 *from = frag + (int64_t)k * MT * 2 * PER * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (c0 + t * E + i < d.K) to[i] = e[i];
+        for (int n = 0; n < NT; ++n) {
+          alignas(16) T w[4];
+          if (AHEAD) {
+            const char *slot = at + 2 * MT * 512 + ((k * NT + n) * 32 + lane) * S::WBYTES;
+            if constexpr (sizeof(T) == 4)
+              *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(slot);
+            else
+              *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(slot);
+          } else {
+            const int64_t col = c0 + gcol + 2 * n;
+            load_ranks(W + (col < d.K ? col * d.rank : 0), (int64_t)k * 16 + 4 * t, d.rank, wvec, col < d.K, w);
+          }
+          if constexpr (sizeof(T) == 4) {
+            float wh[4], wl[4];
+            split4(*reinterpret_cast<const uint4 *>(w), wh, wl);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                const uint4 h = from[((m * 2 + 0) * PER + s) * 32], l = from[((m * 2 + 1) * PER + s) * 32];
+                const auto f = [](uint32_t v) { return __uint_as_float(v); };
+                mma_tf32(acc[m][n], f(l.x), f(l.y), f(l.z), f(l.w), wh[2 * s], wh[2 * s + 1]);
+                mma_tf32(acc[m][n], f(h.x), f(h.y), f(h.z), f(h.w), wl[2 * s], wl[2 * s + 1]);
+                mma_tf32(acc[m][n], f(h.x), f(h.y), f(h.z), f(h.w), wh[2 * s], wh[2 * s + 1]);
+              }
+          } else {
+            const uint2 b = *reinterpret_cast<const uint2 *>(w);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const uint4 h = from[(m * 2 + 0) * 32], l = from[(m * 2 + 1) * 32];
+              mma_16<T>(acc[m][n], l.x, l.y, l.z, l.w, b.x, b.y);
+              mma_16<T>(acc[m][n], h.x, h.y, h.z, h.w, b.x, b.y);
+            }
+          }
         }
       }
+      fetch(c + STAGES - 1);  // into the slots that step c - 1 has read
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!ok[2 * m + half]) continue;
+          T *e = reinterpret_cast<T *>(&y[2 * m + half]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              e[2 * n + i] = from_float<T>(to_float(e[2 * n + i]) + acc[m][n][2 * half + i]);
+          T *to = rows[2 * m + half] + c0 + t * E;
+          if (ALIGNED) {
+            if (c0 + t * E < d.K) *reinterpret_cast<uint4 *>(to) = y[2 * m + half];
+          } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+              if (c0 + t * E + i < d.K) to[i] = e[i];
+          }
+        }
+    }
+    copies_wait<0>();
+    __syncthreads();  // the next tile's H goes where all have read this one's
   }
-  copies_wait<0>();
 }
 
 // ------------------------------------------------------------------ outer: sum_t h[t] x[t]^T
@@ -1308,16 +1314,11 @@ cudaError_t launch_down(const AdapterArgs &q, const DownArgs &d, cudaStream_t s)
 }
 
 template <typename T>
-cudaError_t launch_up(const AdapterArgs &q, UpArgs d, cudaStream_t s) {
+cudaError_t launch_up(const AdapterArgs &q, const UpArgs &d, cudaStream_t s) {
   if (q.p.max_tiles == 0) return cudaSuccess;
   using S = UpShape<T>;
-  // wide blocks prepare H less often; but two blocks an SM should all have work
-  d.groups = S::GROUPS;
-  const auto blocks = [&] { return (d.K + kWarps * d.groups * S::COLS - 1) / (kWarps * d.groups * S::COLS); };
-  while (d.groups > 4 && q.p.max_tiles * blocks() < 3 * (int64_t)device_sms()) d.groups /= 2;
-  d.blocks = blocks();
-  if (q.p.max_tiles * d.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(q.p.max_tiles * d.blocks));
+  const int64_t most = q.p.max_tiles * ((d.K + S::BLOCK - 1) / S::BLOCK);
+  const dim3 grid((unsigned)std::min<int64_t>(most, 2 * device_sms()));
   const bool wvec = d.rank % 4 == 0 && aligned_to(d.W, 4 * sizeof(T));
   const bool vec = vector_rows(d.Y, d.y_stride, d.K, q.a.type);
   const int rg = !wvec || d.rank > 32 ? 0 : (d.rank > 16 ? 2 : 1);
@@ -1403,7 +1404,7 @@ cudaError_t forward(const AdapterArgs &q, void *Y, int64_t y_stride, cudaStream_
   if (e != cudaSuccess) return e;
   const DownArgs d = {a.X, a.A, a.x_stride, a.in, a.rank, false, false, q.H};
   if ((e = launch_down<T>(q, d, s)) != cudaSuccess) return e;
-  const UpArgs u = {q.H, a.B, Y, y_stride, a.out, a.rank, false, true, 0, 0};
+  const UpArgs u = {q.H, a.B, Y, y_stride, a.out, a.rank, false, true};
   return launch_up<T>(q, u, s);
 }
 
@@ -1430,7 +1431,7 @@ cudaError_t backward(const AdapterArgs &q, const Back &b, cudaStream_t s) {
     if ((e = launch_down<T>(q, d, s)) != cudaSuccess) return e;
   }
   if (b.dX) {
-    const UpArgs u = {b.dH, b.At, b.dX, b.dx_stride, a.in, a.rank, true, false, 0, 0};
+    const UpArgs u = {b.dH, b.At, b.dX, b.dx_stride, a.in, a.rank, true, false};
     if ((e = launch_up<T>(q, u, s)) != cudaSuccess) return e;
   }
   if (b.dA || b.dB) {
