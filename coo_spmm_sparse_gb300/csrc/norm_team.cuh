@@ -28,6 +28,7 @@ constexpr int C = kTeamCols;
 struct TeamArgs {
   NormArgs n;
   int block_cols;
+  int threads;        // of a team in one block
   float *next_parts;  // [teams][2][width]
   float *post_parts;  // [slabs][2][width]
 };
@@ -44,10 +45,12 @@ __host__ __device__ constexpr int piece_bytes(int cols, int size) { return (cols
 template <typename TS, typename TB, bool VEC>
 struct Columns {
   static constexpr int U = VEC ? (sizeof(TB) == 4 ? 4 : 8) : 1;
-  int first;        // the block's first column
-  int count;        // its columns
+  int first;         // the block's first column
+  int count;         // its columns
+  int tid, threads;  // this thread among those of its team's part in the block
   bool ok[C / U];
-  __device__ __forceinline__ Columns(const TeamArgs &q, int rank) {
+  __device__ __forceinline__ Columns(const TeamArgs &q, int rank, int tid_, int threads_)
+      : tid(tid_), threads(threads_) {
     const int64_t c0 = (int64_t)rank * q.block_cols, left = q.n.a.width - c0;
     first = (int)c0;
     count = left < 0 ? 0 : (left < q.block_cols ? (int)left : q.block_cols);
@@ -55,7 +58,7 @@ struct Columns {
     for (int k = 0; k < C / U; ++k) ok[k] = local(k * U) < count;
   }
   __device__ __forceinline__ int local(int j) const {  // column of element j within the block
-    return ((j / U) * (int)blockDim.x + (int)threadIdx.x) * U + j % U;
+    return ((j / U) * threads + tid) * U + j % U;
   }
   __device__ __forceinline__ int at(int j) const { return first + local(j); }
   __device__ __forceinline__ bool in(int j) const { return ok[j / U]; }
@@ -77,19 +80,19 @@ __device__ __forceinline__ void load_params(const void *p, int type, const CO &c
 }
 
 // Copies a row of T ahead: vectors into the thread's own slots (16 bytes
-// each, blockDim.x of them side by side), else all of the block's pieces.
+// each, the team's side by side), else all of the block's pieces.
 template <typename T, bool VEC, typename CO>
 __device__ __forceinline__ void copy_row(char *to, const T *row, const CO &co) {
   if (VEC) {
     constexpr int E = 16 / sizeof(T);
 #pragma unroll
     for (int k = 0; k < slots_of<T>(); ++k)
-      if (co.in(k * E)) copy_async16(to + (k * blockDim.x + threadIdx.x) * 16, row + co.at(k * E));
+      if (co.in(k * E)) copy_async16(to + (k * co.threads + co.tid) * 16, row + co.at(k * E));
   } else {
     const uintptr_t begin = reinterpret_cast<uintptr_t>(row + co.first), base = begin & ~uintptr_t(15);
     const int bytes = (int)(begin - base) + co.count * (int)sizeof(T);
     if (co.count > 0)
-      for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+      for (int i = co.tid * 16; i < bytes; i += co.threads * 16)
         copy_async16(to + i, reinterpret_cast<const char *>(base) + i, bytes - i < 16 ? bytes - i : 16);
   }
 }
@@ -102,7 +105,7 @@ __device__ __forceinline__ void take_row(const char *from, const T *row, const C
     constexpr int E = 16 / sizeof(T);
 #pragma unroll
     for (int k = 0; k < slots_of<T>(); ++k) {
-      const uint4 raw = *reinterpret_cast<const uint4 *>(from + (k * blockDim.x + threadIdx.x) * 16);
+      const uint4 raw = *reinterpret_cast<const uint4 *>(from + (k * co.threads + co.tid) * 16);
       if constexpr (sizeof(T) == 4) {
         v[k * E] = __uint_as_float(raw.x);
         v[k * E + 1] = __uint_as_float(raw.y);
@@ -153,17 +156,30 @@ __device__ __forceinline__ void clear_slots(char *ring, int bytes) {
 
 // Sums over the team.  One barrier each: consecutive sums use alternate
 // halves of `red`.
-template <bool CL>
+template <bool CL, bool MULTI>
 struct Team {
   static constexpr int kMost = kTeamThreads / 32;  // warps of a block
   static constexpr int kFloats = 2 * 3 * kMost * (CL ? kTeamCluster : 1);
   float *red;
   int flip = 0;
-  int rank = 0, size = 1;
+  int rank = 0, size = 1;  // blocks of the team
+  int place = 0, warps_ = 0;  // MULTI: the team's place among those of its block, its warps
+
+  __device__ __forceinline__ int index() const { return MULTI ? place : 0; }
+  __device__ __forceinline__ int warps() const { return MULTI ? warps_ : (int)blockDim.x >> 5; }
+  // The team's threads in this block.
+  __device__ __forceinline__ void barrier() const {
+    if (!MULTI || (int)blockDim.x == warps() * 32)
+      __syncthreads();
+    else if (warps() == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(index() + 1), "r"(warps() * 32) : "memory");
+  }
 
   template <int N>
   __device__ __forceinline__ void sum(float (&v)[N]) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, nw = warps(), w = (int)(threadIdx.x >> 5) - index() * nw;
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
     if (!CL && nw == 1) return;
@@ -186,10 +202,11 @@ struct Team {
         v[k] = warp_sum(s);
       }
     } else {
+      buf += index() * nw;
       if (lane == 0)
 #pragma unroll
         for (int k = 0; k < N; ++k) buf[k * kMost + w] = v[k];
-      __syncthreads();
+      barrier();
       // sixteen lanes hold all warps' sums: four steps
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] = (lane & 15) < nw ? buf[k * kMost + (lane & 15)] : 0.f;
@@ -227,10 +244,15 @@ struct Team {
   }
 };
 
-template <bool CL>
-__device__ __forceinline__ Team<CL> make_team(float *red) {
-  Team<CL> t;
+// `threads`: of a team in this block (MULTI: several teams).
+template <bool CL, bool MULTI>
+__device__ __forceinline__ Team<CL, MULTI> make_team(float *red, int threads) {
+  Team<CL, MULTI> t;
   t.red = red;
+  if (MULTI) {
+    t.warps_ = threads >> 5;
+    t.place = (int)threadIdx.x / threads;
+  }
   if (CL) {
     cg::cluster_group cl = cg::this_cluster();
     t.rank = (int)cl.block_rank();
@@ -252,8 +274,8 @@ __device__ __forceinline__ const TB *gate_row(const snack_norm_args &a, int64_t 
 
 // Bytes of one row of an array of T in the ring.
 template <typename T, bool VEC>
-__device__ __forceinline__ int row_bytes(const TeamArgs &q) {
-  return VEC ? slots_of<T>() * 16 * (int)blockDim.x : piece_bytes(q.block_cols, sizeof(T));
+__device__ __forceinline__ int row_bytes(const TeamArgs &q, int threads) {
+  return VEC ? slots_of<T>() * 16 * threads : piece_bytes(q.block_cols, sizeof(T));
 }
 
 // ------------------------------------------------------------------ host
@@ -285,7 +307,7 @@ inline int ring_row(const TeamPlan &p, const snack_norm_args &a, int ns, int nb)
 
 // Two rows ahead, or one where two do not fit.
 inline void team_ring(TeamPlan *p, const snack_norm_args &a, int ns, int nb) {
-  const size_t row = ring_row(*p, a, ns, nb);
+  const size_t row = (size_t)ring_row(*p, a, ns, nb) * p->per_block;
   p->stages = 3 * row <= 208 * 1024 ? 3 : 2;
   p->smem = p->stages * row;
 }
@@ -296,7 +318,7 @@ cudaError_t launch_team(K kern, const TeamPlan &p, int64_t teams, const TeamArgs
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(teams * p.cluster));
-  cfg.blockDim = dim3((unsigned)p.threads);
+  cfg.blockDim = dim3((unsigned)(p.threads * p.per_block));
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

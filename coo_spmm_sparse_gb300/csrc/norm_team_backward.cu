@@ -15,19 +15,20 @@ namespace {
 
 using namespace team;
 
-// A team takes slabs of rows, each within one group; sum dh rhat and sum dh
-// leave once per team, sum G D yhat and sum G D once per slab.
+// The teams of a block take slabs of rows, each within one group, row by row
+// in turn; sum dh rhat and sum dh leave once per block, sum G D yhat and sum
+// G D once per slab.
 template <typename TS, typename TB, int S, bool VEC, bool CL, bool LAYER, Form F>
 __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_constant__ TeamArgs q) {
   extern __shared__ uint4 smem4[];
-  __shared__ float red[Team<CL>::kFloats];
-  char *const ring = reinterpret_cast<char *>(smem4);
+  __shared__ float red[Team<CL, !CL>::kFloats];
   const snack_norm_args &a = q.n.a;
   const snack_norm_grads &g = q.n.g;
   dependency_wait();
   dependency_launch();
-  Team<CL> team = make_team<CL>(red);
-  const Columns<TS, TB, VEC> co(q, team.rank);
+  Team<CL, !CL> team = make_team<CL, !CL>(red, q.threads);
+  const Columns<TS, TB, VEC> co(q, team.rank, (int)threadIdx.x - team.index() * q.threads, q.threads);
+  const int per_block = (int)blockDim.x / q.threads;
   const int64_t me = blockIdx.x / team.size, teams = gridDim.x / team.size;
   const bool has_y = F || a.y, post = F ? F == kFastPost : has_y && a.post_norm;
   const bool full = !F && a.gate_kind == SNACK_GATE_FULL, token = !F && a.gate_kind == SNACK_GATE_TOKEN;
@@ -35,9 +36,41 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
   // a bias: the layer norms' own, or one given to an rms norm
   const bool post_bias = LAYER || (!F && a.post_bias);
   const bool dbias = LAYER || (!F && (g.dnext_bias || g.dpost_bias || a.post_bias));
-  const int xb = row_bytes<TS, VEC>(q), bb = row_bytes<TB, VEC>(q), per = 2 * xb + (2 + (full ? 1 : 0)) * bb;
+  const int xb = row_bytes<TS, VEC>(q, q.threads), bb = row_bytes<TB, VEC>(q, q.threads), per = 2 * xb + (2 + (full ? 1 : 0)) * bb;
   const float inv = 1.f / (float)a.width;
-  if (VEC && co.count < (int)blockDim.x * C) clear_slots(ring, S * per);
+  char *const whole = reinterpret_cast<char *>(smem4), *const ring = whole + team.index() * S * per;
+  if (VEC && co.count < q.threads * C) clear_slots(whole, per_block * S * per);
+  // the sums of the block's teams, added in their order through the ring
+  const auto join = [&](float (&u)[C], float (&v)[C], float *out) {
+    float *buf = reinterpret_cast<float *>(smem4);
+    for (int k = 0; k + 1 < per_block; ++k) {
+      __syncthreads();
+      if (team.index() == k)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          float *at = buf + (j * q.threads + co.tid) * 2;
+          at[0] = u[j];
+          at[1] = v[j];
+        }
+      __syncthreads();
+      if (team.index() == k + 1)
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const float *at = buf + (j * q.threads + co.tid) * 2;
+          u[j] += at[0];
+          v[j] += at[1];
+        }
+    }
+    if (team.index() == per_block - 1)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (co.in(j)) {
+          out[co.at(j)] = u[j];
+          out[a.width + co.at(j)] = v[j];
+        }
+    __syncthreads();  // the ring is the rows' again
+    if (VEC && per_block > 1 && co.count < q.threads * C) clear_slots(whole, per_block * S * per);
+  };
 
   const auto x_row = [&](int64_t r) { return static_cast<const TS *>(a.x) + r * a.x_stride; };
   const auto y_row = [&](int64_t r) { return static_cast<const TB *>(a.y) + r * a.y_stride; };
@@ -65,9 +98,9 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
   for (int64_t slab = me; slab < q.n.slabs; slab += teams) {
     // every step-th row of the group: all teams together sweep the rows in
     // their order
-    const int64_t step = q.n.slabs_per_group, group = slab / step;
-    const int64_t r0 = group * q.n.group_len + slab % step, r1 = (group + 1) * q.n.group_len;
-    if (!VEC) __syncthreads();  // the slab before has been read by all
+    const int64_t spg = q.n.slabs_per_group, step = spg * per_block, group = slab / spg;
+    const int64_t r0 = group * q.n.group_len + slab % spg + team.index() * spg, r1 = (group + 1) * q.n.group_len;
+    if (!VEC) team.barrier();  // the slab before has been read by all
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch(r0 + i * step, r1, i);
     if (has_y) {
@@ -77,7 +110,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
       for (int j = 0; j < C; ++j) {
         float f = a.branch_scale;
         if (a.gate_kind == SNACK_GATE_CHANNEL || a.gate_kind == SNACK_GATE_SEQUENCE)
-          f *= co.in(j) ? to_float(gate_row<TB>(a, r0)[co.at(j)]) : 0.f;
+          f *= co.in(j) ? to_float(gate_row<TB>(a, group * q.n.group_len)[co.at(j)]) : 0.f;
         k1[j] *= f;
         k0[j] *= f;
       }
@@ -94,7 +127,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
       float rh[C], D[C], yh[C], gate[C];
       const float ym = st.x, yr = st.y, mean = st.z, rstd = st.w;
       copies_wait<S - 2>();
-      if (!VEC) __syncthreads();
+      if (!VEC) team.barrier();
       const char *from = ring + stage * per;
       take_row<TS, VEC>(from, x_row(row), co, rh);
       if (row + step < r1) st = reinterpret_cast<const float4 *>(a.stats)[row + step];
@@ -187,7 +220,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
         team.sum(all);
         e[0] = all[0];
         e[1] = all[1];
-        if (team.rank == 0 && threadIdx.x == 0) static_cast<TB *>(g.dgate)[row] = from_float<TB>(all[2]);
+        if (team.rank == 0 && co.tid == 0) static_cast<TB *>(g.dgate)[row] = from_float<TB>(all[2]);
       } else if (post) {
         if (LAYER) {
           team.sum(e);
@@ -207,25 +240,9 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_backward(const __grid_
       }
     }
     copies_wait<0>();
-    if (q.post_parts) {
-      float *out = q.post_parts + slab * 2 * a.width;
-#pragma unroll
-      for (int j = 0; j < C; ++j)
-        if (co.in(j)) {
-          out[co.at(j)] = s2[j];
-          out[a.width + co.at(j)] = s3[j];
-        }
-    }
+    if (q.post_parts) join(s2, s3, q.post_parts + slab * 2 * a.width);
   }
-  if (q.next_parts) {
-    float *out = q.next_parts + me * 2 * a.width;
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (co.in(j)) {
-        out[co.at(j)] = s0[j];
-        out[a.width + co.at(j)] = s1[j];
-      }
-  }
+  if (q.next_parts) join(s0, s1, q.next_parts + me * 2 * a.width);
   if (CL) cg::this_cluster().sync();
 }
 
@@ -304,9 +321,10 @@ cudaError_t launch(const TeamPlan &p, int64_t teams, const TeamArgs &q, Form for
 
 }  // namespace
 
-// One team for every two rows (a part of the column sums for each team, all
-// read again at the end), at most what 512 threads of 128 registers on each
-// SM hold at once.
+// One team for every two rows, at most what 512 threads of 128 registers on
+// each SM hold at once; on each SM they are one block, which leaves one part
+// of the column sums (a part for each of 585 teams of 128 threads, 4095 x
+// 1001: 9 MB, and 14 us to add them up).
 TeamPlan team_backward(const NormArgs &n) {
   const snack_norm_args &a = n.a;
   const snack_norm_grads &g = n.g;
@@ -317,16 +335,18 @@ TeamPlan team_backward(const NormArgs &n) {
           (!full || rows16(a.gate, a.gate_stride, a.branch_type)) && rows16(g.dr, g.dr_stride, a.stream_type) &&
           rows16(g.dh, g.dh_stride, a.branch_type) && aligned_to(g.dx, 16) && aligned_to(g.dy, 16) &&
           (!full || aligned_to(g.dgate, 16));
+  const int64_t sms = device_sms(), fit = kTeamThreads / p.threads;
+  const int64_t teams = std::max<int64_t>(1, std::min<int64_t>((a.rows + 1) / 2, std::max<int64_t>(1, sms * fit / p.cluster)));
+  if (p.cluster == 1) p.per_block = (int)std::max<int64_t>(1, std::min<int64_t>(fit, teams / sms));
   team_ring(&p, a, 2, full ? 3 : 2);
-  const int64_t most = std::max<int64_t>(1, (int64_t)device_sms() * (kTeamThreads / p.threads) / p.cluster);
-  p.teams = std::max<int64_t>(1, std::min<int64_t>((a.rows + 1) / 2, most));
+  p.teams = (teams + p.per_block - 1) / p.per_block;
   return p;
 }
 
 cudaError_t launch_team_backward(const NormArgs &n, const TeamPlan &p, cudaStream_t s) {
   const snack_norm_args &a = n.a;
   const snack_norm_grads &g = n.g;
-  TeamArgs q = {n, p.block_cols, nullptr, nullptr};
+  TeamArgs q = {n, p.block_cols, p.threads, nullptr, nullptr};
   const bool seq = a.gate_kind == SNACK_GATE_SEQUENCE;
   const bool next = g.dnext_weight || g.dnext_bias;
   const bool post = g.dpost_weight || g.dpost_bias || (g.dgate && (a.gate_kind == SNACK_GATE_CHANNEL || seq));

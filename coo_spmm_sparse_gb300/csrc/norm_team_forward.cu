@@ -9,18 +9,18 @@ using namespace team;
 template <typename TS, typename TB, int S, bool VEC, bool CL, bool LAYER, Form F>
 __global__ void __launch_bounds__(kTeamThreads, 2) norm_team_forward(const __grid_constant__ TeamArgs q) {
   extern __shared__ uint4 smem4[];
-  __shared__ float red[Team<CL>::kFloats];
+  __shared__ float red[Team<CL, false>::kFloats];
   char *const ring = reinterpret_cast<char *>(smem4);
   const snack_norm_args &a = q.n.a;
   dependency_wait();
   dependency_launch();
-  Team<CL> team = make_team<CL>(red);
-  const Columns<TS, TB, VEC> co(q, team.rank);
+  Team<CL, false> team = make_team<CL, false>(red, blockDim.x);
+  const Columns<TS, TB, VEC> co(q, team.rank, threadIdx.x, blockDim.x);
   const int64_t me = blockIdx.x / team.size, teams = gridDim.x / team.size, step = q.n.slabs_per_group;
   const bool has_y = F || a.y, full = !F && a.gate_kind == SNACK_GATE_FULL;
   const bool token = !F && a.gate_kind == SNACK_GATE_TOKEN, post = F ? F == kFastPost : has_y && a.post_norm;
   const bool next = F || a.next_norm, has_k0 = LAYER || (!F && a.post_bias);
-  const int xb = row_bytes<TS, VEC>(q), bb = row_bytes<TB, VEC>(q), per = xb + bb + (full ? bb : 0);
+  const int xb = row_bytes<TS, VEC>(q, blockDim.x), bb = row_bytes<TB, VEC>(q, blockDim.x), per = xb + bb + (full ? bb : 0);
   if (VEC && co.count < (int)blockDim.x * C) clear_slots(ring, S * per);
 
   const auto fetch = [&](int64_t row, int64_t end, int stage) {
@@ -134,7 +134,7 @@ TeamPlan team_forward(const NormArgs &n) {
 
 cudaError_t launch_team_forward(const NormArgs &n, const TeamPlan &p, cudaStream_t s) {
   const snack_norm_args &a = n.a;
-  const TeamArgs q = {n, p.block_cols, nullptr, nullptr};
+  const TeamArgs q = {n, p.block_cols, p.threads, nullptr, nullptr};
   const Form form = !plain_options(a) || !n.r || !a.stats ? kAny : (a.post_norm ? kFastPost : kFast);
 #define SNACK_CALL(TS, TB) return launch<TS, TB>(p, p.teams, q, form, s);
   SNACK_NORM_TYPES(SNACK_CALL)

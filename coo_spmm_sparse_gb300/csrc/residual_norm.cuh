@@ -23,13 +23,14 @@ constexpr int kTeamThreads = 512;  // most threads of one block
 constexpr int kTeamCluster = 8;    // most blocks of one team
 
 struct TeamPlan {
-  int threads = 0;   // 0: the row is too wide for a team
+  int threads = 0;   // of a team in one block; 0: the row is too wide for a team
+  int per_block = 1; // teams of one block
   int cluster = 1;
   int block_cols = 0;  // columns of one block
   bool vec = false;    // rows can be read and written in 16-byte vectors
   int stages = 0;      // rows in the ring: one held, the others copied ahead
   size_t smem = 0;
-  int64_t teams = 0;
+  int64_t teams = 0;  // blocks (or clusters) in all
 };
 
 TeamPlan team_forward(const NormArgs &n);
