@@ -28,12 +28,17 @@
 // what is left out is below 2^-22 of a product.  Running sums leave the
 // matrix unit's accumulator every few steps for a 32-bit sum that rounds to
 // nearest.
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "dense_ops.cuh"
 
 namespace snack {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -334,6 +339,20 @@ __device__ __forceinline__ void mma_16<__half>(float (&c)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The power of two that brings the largest finite magnitude of some 32-bit
+// floats (its bits) to [2^14, 2^15): float16 holds neither more than 65504 nor
+// the small values of a gradient to more than 2^-25, which two parts of it,
+// scaled so, do to 2^-22 of any value down to 2^-16 of the largest.
+__device__ __forceinline__ float half_scale(uint32_t largest) {
+  const int e = (int)(largest >> 23) - 127;  // -127: zeros and subnormals
+  const int up = min(max(14 - e, -126), 126);
+  return __uint_as_float((uint32_t)(up + 127) << 23);
+}
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+
 // Two values as one register of T pairs, and what that rounding left out as another.
 template <typename T>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo) {
@@ -417,8 +436,11 @@ struct DownShape {
   static constexpr size_t SMEM = RING > PART ? RING : PART;
 };
 
-// Block: one tile of kTile tokens, ranks [64 y, 64 y + 64).  Its warps take
-// steps of K in turn and meet in shared memory at the end.  Eight lanes copy
+// Block, or a cluster of blocks where there are few tiles: one tile of kTile
+// tokens, ranks [64 y, 64 y + 64).  The warps take steps of K in turn and
+// meet in shared memory at the end, a cluster's blocks in each other's.
+// (One block for each of 8 tiles of 4096 columns: 16 steps for every warp,
+// each of which waits for memory.)  Eight lanes copy
 // the 128 bytes of a row; chunk c of a row lies at c ^ 4 (row & 1), where the
 // eight lanes that read together find two rows' halves in eight bank groups.
 template <typename T, int NT, bool ALIGNED>
@@ -431,9 +453,13 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
   float *part = reinterpret_cast<float *>(smem4);  // [kWarps][kTile][LD], over the ring
   dependency_wait();
   dependency_launch();
-  if ((int)blockIdx.x >= q.p.head[0]) return;
-  const int4 tile = q.p.tiles[blockIdx.x];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = (int)cluster.num_blocks(), rank_of = (int)cluster.block_rank();
+  const int which = (int)blockIdx.x / blocks;
+  if (which >= q.p.head[0]) return;  // the whole cluster
+  const int4 tile = q.p.tiles[which];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int worker = rank_of * kWarps + warp, workers = blocks * kWarps;
   const int64_t j0 = (int64_t)blockIdx.y * kRankPass;
   const T *X = static_cast<const T *>(d.X);
   const T *W = static_cast<const T *>(d.W) + ((int64_t)(d.by_used ? tile.w : tile.x) * d.rank + j0) * d.K;
@@ -441,11 +467,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
   // token of tile row `lane`, or -1
   const int mine = lane < tile.z ? q.p.perm[tile.y + lane] : -1;
 
-  const int steps = ((int)((d.K + 2 * KG - 1) / (2 * KG)) - warp + kWarps - 1) / kWarps;  // of this warp
+  const int steps = ((int)((d.K + 2 * KG - 1) / (2 * KG)) - worker + workers - 1) / workers;  // of this warp
   uint4 *ring = smem4 + (int64_t)warp * STAGES * S::ROWS * 8;
   const auto fetch = [&](int i) {
     if (ALIGNED && i < steps) {
-      const int64_t k = ((int64_t)i * kWarps + warp) * 2 * KG + (lane & 7) * E;
+      const int64_t k = ((int64_t)i * workers + worker) * 2 * KG + (lane & 7) * E;
       uint4 *slot = ring + (i % STAGES) * S::ROWS * 8;
       const int r = lane >> 3, at = r * 8 + ((lane & 7) ^ (4 * (r & 1)));
 #pragma unroll
@@ -498,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
 #pragma unroll
         for (int n = 0; n < NT; ++n) w[n] = slot[(2 * MT + n) * 64];
       } else {
-        const int64_t k = (((int64_t)i * kWarps + warp) * 2 + half) * KG + t * E;
+        const int64_t k = (((int64_t)i * workers + worker) * 2 + half) * KG + t * E;
 #pragma unroll
         for (int m = 0; m < 2 * MT; ++m) {
           const int tok = __shfl_sync(0xffffffffu, mine, m * 8 + g);
@@ -555,14 +581,36 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
     }
   __syncthreads();
   const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
-  for (int e = threadIdx.x; e < kTile * kCols; e += kThreads) {
-    const int i = e / kCols, j = e % kCols;
-    if (i >= tile.z || j0 + j >= d.rank) continue;
+  const auto block_sum_at = [&](int i, int j) {
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s += part[((int64_t)w * kTile + i) * LD + j];
-    d.H[(int64_t)q.p.perm[tile.y + i] * d.rank + j0 + j] = s * scale;
+    return s;
+  };
+  const auto put = [&](int i, int j, float s) {
+    if (i < tile.z && j < ranks) d.H[(int64_t)q.p.perm[tile.y + i] * d.rank + j0 + j] = s * scale;
+  };
+  if (blocks == 1) {
+    for (int e = threadIdx.x; e < kTile * kCols; e += kThreads) put(e / kCols, e % kCols, block_sum_at(e / kCols, e % kCols));
+    return;
   }
+  // each block's sums over its warps' first part, then every block adds its share of all blocks'
+  float own[kTile * kCols / kThreads];
+#pragma unroll
+  for (int k = 0; k < kTile * kCols / kThreads; ++k) {
+    const int e = k * kThreads + threadIdx.x;
+    own[k] = block_sum_at(e / kCols, e % kCols);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kTile * kCols / kThreads; ++k) part[k * kThreads + threadIdx.x] = own[k];
+  cluster.sync();
+  for (int e = rank_of * kThreads + threadIdx.x; e < kTile * kCols; e += blocks * kThreads) {
+    float s = 0.f;
+    for (int b = 0; b < blocks; ++b) s += cluster.map_shared_rank(part, b)[e];
+    put(e / kCols, e % kCols, s);
+  }
+  cluster.sync();  // no block leaves while another reads its sums
 }
 
 // ------------------------------------------------------------------ up: Y += H W^T
@@ -637,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
   const int across = (int)((d.K + S::BLOCK - 1) / S::BLOCK);  // column blocks of a tile
   const int64_t all = (int64_t)q.p.head[0] * across;
   const int64_t u1 = all * (blockIdx.x + 1) / gridDim.x;
+  __shared__ uint32_t largest;
   int count;  // column blocks of the tile at hand
   for (int64_t u = all * blockIdx.x / gridDim.x; u < u1; u += count) {
     const int4 tile = q.p.tiles[u / across];
@@ -682,18 +731,27 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
     for (int c = 0; c < STAGES - 1; ++c) fetch(c);
 
     const float scale = d.scaled ? scale_of(q.a, tile.x) : 1.f;
+    const auto h_at = [&](int row, int64_t j) {
+      return row < tile.z && j < d.rank ? d.H[(int64_t)q.p.perm[tile.y + row] * d.rank + j] * scale : 0.f;
+    };
+    float fit = 1.f;  // float16: power of two that the tile's H is scaled by
+    if constexpr (std::is_same_v<T, __half>) {
+      if (threadIdx.x == 0) largest = 0u;
+      __syncthreads();
+      uint32_t most = 0u;
+      for (int i = threadIdx.x; i < kTile * d.rank; i += kThreads) most = max(most, finite_bits(h_at(i / (int)d.rank, i % d.rank)));
+      atomicMax(&largest, most);
+      __syncthreads();
+      fit = half_scale(largest);
+    }
     for (int i = warp; i < rg * MT; i += kWarps) {
       const int m = i % MT, k = i / MT;
       float h[2][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int row = m * 16 + half * 8 + g;
-        const float *at = d.H + (row < tile.z ? (int64_t)q.p.perm[tile.y + row] * d.rank : 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t j = k * 16 + 4 * t + e;
-          h[half][e] = row < tile.z && j < d.rank ? at[j] * scale : 0.f;
-        }
+        for (int e = 0; e < 4; ++e) h[half][e] = h_at(row, k * 16 + 4 * t + e) * fit;
       }
       uint4 *to = frag + (int64_t)(k * MT + m) * 2 * PER * 32 + lane;
       if constexpr (sizeof(T) == 4) {
@@ -794,7 +852,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              e[2 * n + i] = from_float<T>(to_float(e[2 * n + i]) + acc[m][n][2 * half + i]);
+              e[2 * n + i] = from_float<T>(std::is_same_v<T, __half>
+                                             ? fmaf(acc[m][n][2 * half + i], 1.f / fit, to_float(e[2 * n + i]))
+                                             : to_float(e[2 * n + i]) + acc[m][n][2 * half + i]);
           T *to = rows[2 * m + half] + c0 + t * E;
           if (ALIGNED) {
             if (c0 + t * E < d.K) *reinterpret_cast<uint4 *>(to) = y[2 * m + half];
@@ -895,6 +955,8 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
   const T *copy_from = X + (copy_ok ? c0 + (lane & 7) * E : 0);
   uint4 *ring = smem4 + warp * STAGES * NR * 32;
   bool first = true;
+  float fit = 1.f;  // float16: power of two that the chunk's H is scaled by
+  __shared__ uint32_t largest;
   for (int p = 0; p < places; ++u) {
     const int4 use = q.p.used[u];
     const int end = (int)min((int64_t)places, (int64_t)use.y + use.z - p0);
@@ -948,7 +1010,15 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
         copies_wait<STAGES - 1>();
       else
         copies_wait<0>();
+      if (std::is_same_v<T, __half> && threadIdx.x == 0) largest = 0u;
       __syncthreads();
+      if constexpr (std::is_same_v<T, __half>) {
+        uint32_t most = 0u;
+        for (int i = threadIdx.x; i < places * 16 * RM; i += kThreads) most = max(most, finite_bits(hs[i / (16 * RM) * LD + i % (16 * RM)]));
+        atomicMax(&largest, most);
+        __syncthreads();
+        fit = half_scale(largest);
+      }
       first = false;
     }
     for (int step = 0; step < steps; ++step) {
@@ -967,7 +1037,10 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
         else
           x[i] = load16<T, false>(X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K, k < end);
 #pragma unroll
-        for (int m = 0; m < 2 * RM; ++m) h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
+        for (int m = 0; m < 2 * RM; ++m) {
+          h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
+          if (std::is_same_v<T, __half>) h[i][m] *= fit;
+        }
       }
       fetch(step + STAGES - 1);  // into the slots that every lane read before this step's barrier
       if constexpr (sizeof(T) == 4) {
@@ -1032,7 +1105,7 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const int64_t c = c0 + (2 * t + i) * E + n;
-            if (c < d.K) out[j * d.K + c] = sum[m][n][2 * half + i];
+            if (c < d.K) out[j * d.K + c] = std::is_same_v<T, __half> ? sum[m][n][2 * half + i] * (1.f / fit) : sum[m][n][2 * half + i];
           }
       }
   }
@@ -1143,6 +1216,23 @@ __global__ void __launch_bounds__(kThreads) adapter_turn(const __grid_constant__
 
 // ------------------------------------------------------------------ few tokens
 
+// Up to this many tokens are taken one by one, forward and backward: the
+// weights of each are read for it alone, and no plan is made.  4096 x 4096
+// at rank 16, fp32, one by one / by tiles: forward 128 tokens 14.6 / 14 us
+// (10: 8.4 us); forward + backward of 64 tokens of one adapter 50 / 46 us
+// and of 16 adapters 35 / 74 us, of 128 tokens 63 / 46 and 52 / 74 us.
+constexpr int kFewTokens = 128, kFewTokensBack = 64;
+
+struct FewArgs {
+  const void *dY;
+  int64_t dy_stride;
+  const float *H;
+  void *dX;
+  int64_t dx_stride;
+  void *dA, *dB;
+  float *dH;
+};
+
 // The adapter of token t by the caller's offsets, or -1.
 __device__ __forceinline__ int adapter_of(const snack_adapter_args &a, int64_t t) {
   const int i = request_of(a.offsets, (int)a.requests, (int32_t)t);
@@ -1217,6 +1307,146 @@ __global__ void __launch_bounds__(kThreads) adapter_few_up(const __grid_constant
   *y = from_float<T>(y0 + s);
 }
 
+// dH of few tokens.  Block (token, 16 ranks): a thread takes every 256th row of B.
+constexpr int kFewRanks = 16;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adapter_few_rank(const __grid_constant__ AdapterArgs q,
+                                                             const __grid_constant__ FewArgs b) {
+  constexpr int E = 16 / sizeof(T);
+  __shared__ float part[kWarps][kFewRanks];
+  dependency_wait();
+  dependency_launch();
+  const snack_adapter_args &a = q.a;
+  const int64_t tkn = blockIdx.x, j0 = (int64_t)blockIdx.y * kFewRanks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = adapter_of(a, tkn), ranks = (int)min((int64_t)kFewRanks, a.rank - j0);
+  float s[kFewRanks];
+#pragma unroll
+  for (int j = 0; j < kFewRanks; ++j) s[j] = 0.f;
+  if (n >= 0) {
+    const T *dy = static_cast<const T *>(b.dY) + tkn * b.dy_stride;
+    const T *w = static_cast<const T *>(a.B) + (int64_t)n * a.out * a.rank + j0;
+    const bool vec = a.rank % E == 0 && (reinterpret_cast<uintptr_t>(a.B) & 15) == 0;
+#pragma unroll 2
+    for (int64_t o = threadIdx.x; o < a.out; o += kThreads) {
+      const float d = to_float(dy[o]);
+      if (vec) {
+#pragma unroll
+        for (int v = 0; v < kFewRanks / E; ++v) {
+          const uint4 x = load16<T, true>(w + o * a.rank, v * E, ranks, true);
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[v * E + e] = fmaf(d, to_float(reinterpret_cast<const T *>(&x)[e]), s[v * E + e]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kFewRanks; ++j)
+          if (j < ranks) s[j] = fmaf(d, to_float(w[o * a.rank + j]), s[j]);
+      }
+    }
+  }
+  // sixteen sums over the warp: each step halves the ranks that a lane still holds
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const bool up = lane & o;
+      const float send = up ? s[j] : s[j + o], keep = up ? s[j + o] : s[j];
+      s[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
+  if (lane < kFewRanks) part[warp][lane] = s[0];
+  __syncthreads();
+  if (threadIdx.x < ranks) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
+    b.dH[tkn * a.rank + j0 + threadIdx.x] = n < 0 ? 0.f : v * scale_of(a, n);
+  }
+}
+
+// dX of few tokens.  Block (256 columns, token).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adapter_few_input(const __grid_constant__ AdapterArgs q,
+                                                              const __grid_constant__ FewArgs b) {
+  extern __shared__ float h[];
+  dependency_wait();
+  dependency_launch();
+  const snack_adapter_args &a = q.a;
+  const int64_t tkn = blockIdx.y, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int n = adapter_of(a, tkn);
+  if (n < 0) return;
+  for (int64_t j = threadIdx.x; j < a.rank; j += kThreads) h[j] = b.dH[tkn * a.rank + j];
+  __syncthreads();
+  if (i >= a.in) return;
+  const T *w = static_cast<const T *>(a.A) + (int64_t)n * a.rank * a.in + i;
+  T *dx = static_cast<T *>(b.dX) + tkn * b.dx_stride + i;
+  const float x0 = to_float(*dx);
+  float s = 0.f;
+#pragma unroll 8
+  for (int64_t j = 0; j < a.rank; ++j) s = fmaf(h[j], to_float(w[j * a.in]), s);
+  *dx = from_float<T>(x0 + s);
+}
+
+// dA and dB of few tokens.  Block (256 columns of in, then of out; adapter;
+// 16 ranks): the adapter's tokens in their order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) adapter_few_weights(const __grid_constant__ AdapterArgs q,
+                                                                const __grid_constant__ FewArgs b) {
+  __shared__ int tok[kFewTokensBack], counts[kFewTokensBack / 32];
+  __shared__ float h[kFewTokensBack][kFewRanks];
+  dependency_wait();
+  dependency_launch();
+  const snack_adapter_args &a = q.a;
+  const int64_t in_blocks = b.dA ? (a.in + kThreads - 1) / kThreads : 0;
+  const bool db = blockIdx.x >= in_blocks;
+  const int64_t K = db ? a.out : a.in, j0 = (int64_t)blockIdx.z * kFewRanks;
+  const int64_t i = (int64_t)(blockIdx.x - (db ? in_blocks : 0)) * kThreads + threadIdx.x;
+  const int ranks = (int)min((int64_t)kFewRanks, a.rank - j0);
+  const int mine = threadIdx.x < a.tokens ? adapter_of(a, threadIdx.x) : -1;
+  const T *X = static_cast<const T *>(db ? b.dY : a.X) + (i < K ? i : 0);
+  const int64_t stride = db ? b.dy_stride : a.x_stride;
+  const float *H = db ? b.H : b.dH;
+  for (int64_t n = blockIdx.y; n < a.adapters; n += gridDim.y) {
+    __syncthreads();  // the adapter before is done with the shared arrays
+    const bool is = mine == n;
+    const uint32_t vote = __ballot_sync(0xffffffffu, is);
+    if (threadIdx.x < kFewTokensBack && (threadIdx.x & 31) == 0) counts[threadIdx.x / 32] = __popc(vote);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kFewTokensBack / 32; ++w) {
+      before += w < (int)threadIdx.x / 32 ? counts[w] : 0;
+      all += counts[w];
+    }
+    if (is) tok[before + __popc(vote & ((1u << (threadIdx.x & 31)) - 1))] = threadIdx.x;
+    __syncthreads();
+    for (int e = threadIdx.x; e < all * kFewRanks; e += kThreads) {
+      const int k = e / kFewRanks, j = e % kFewRanks;
+      h[k][j] = j < ranks ? H[tok[k] * a.rank + j0 + j] : 0.f;
+    }
+    __syncthreads();
+    if (i >= K) continue;
+    float s[kFewRanks];
+#pragma unroll
+    for (int j = 0; j < kFewRanks; ++j) s[j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < all; ++k) {
+      const float x = to_float(X[tok[k] * stride]);
+#pragma unroll
+      for (int j = 0; j < kFewRanks; ++j) s[j] = fmaf(h[k][j], x, s[j]);
+    }
+    const float scale = db && all > 0 ? scale_of(a, (int)n) : 1.f;
+#pragma unroll
+    for (int j = 0; j < kFewRanks; ++j) {
+      if (j >= ranks) continue;
+      if (db)
+        static_cast<T *>(b.dB)[(n * a.out + i) * a.rank + j0 + j] = from_float<T>(s[j] * scale);
+      else
+        static_cast<T *>(b.dA)[(n * a.rank + j0 + j) * a.in + i] = from_float<T>(s[j]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ host
 
 const char *bad_args(const snack_adapter_args *a) {
@@ -1248,10 +1478,6 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width, int type) {
 }
 
 int64_t align16(int64_t b) { return (b + 15) / 16 * 16; }
-
-// Up to this many tokens are taken one by one: the weights of each are read
-// for it alone, and no plan is made.
-constexpr int64_t kFewTokens = 128;
 
 // Lays the plan out in `ws` (null: only its size).
 int64_t lay_plan(const snack_adapter_args &a, Plan *p, char *ws) {
@@ -1296,11 +1522,16 @@ bool vector_rows(const void *p, int64_t stride, int64_t width, int type) {
 
 template <typename T, int NT>
 cudaError_t launch_down_nt(const AdapterArgs &q, const DownArgs &d, bool vec, cudaStream_t s) {
-  const dim3 grid((unsigned)q.p.max_tiles, (unsigned)((d.rank + kRankPass - 1) / kRankPass));
   const size_t smem = DownShape<NT>::SMEM;
   auto k = vec ? adapter_down<T, NT, true> : adapter_down<T, NT, false>;
   const cudaError_t e = allow_smem(k, smem);
-  return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
+  // blocks of a tile: while all of them fit the GPU at once and each warp keeps a step
+  const int64_t room = (int64_t)device_sms() * (NT <= 2 ? 2 : 1);
+  int64_t blocks = 1;
+  while (blocks < 8 && 2 * q.p.max_tiles * blocks <= room && d.K > blocks * kWarps * 2 * Group<T>::K) blocks *= 2;
+  if (q.p.max_tiles * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(q.p.max_tiles * blocks), (unsigned)((d.rank + kRankPass - 1) / kRankPass));
+  return e != cudaSuccess ? e : launch_clusters(k, grid, (int)blocks, kThreads, smem, true, s, q, d);
 }
 
 template <typename T>
@@ -1329,15 +1560,21 @@ cudaError_t launch_up(const AdapterArgs &q, const UpArgs &d, cudaStream_t s) {
   return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
 }
 
-// Places of one block of `outer`: one round of blocks, two on each SM; at
-// least 64 places (below it the parts cost more than the split gains), at
-// most 448 at 16 ranks and 256 at 32 (two blocks' rings and H fit an SM).
+// Places of one block of `outer`: one round of blocks, two on each SM.  At
+// least 64 places, below which the parts cost more than the split gains, but
+// no more than an adapter has on average (a block that meets many adapters
+// waits for the first rows of each): 128 tokens of 16 adapters, 4096 x 4096
+// at rank 16, forward + backward 90 -> 72 us with 16 places, 256 tokens of
+// one adapter 46 -> 55.  At most 448 at 16 ranks and 256 at 32 (two blocks'
+// rings and H fit an SM).
 int64_t outer_chunk(const snack_adapter_args &a, int64_t K) {
   const int64_t cols = kWarps * 8 * (16 / type_bytes(a.type)), ranks = outer_ranks(a.rank);
   const int64_t blocks = (K + cols - 1) / cols * ((a.rank + ranks - 1) / ranks);
   const int64_t split = std::max<int64_t>(1, (int64_t)device_sms() * 2 / blocks);
+  const int64_t used = std::max<int64_t>(1, std::min(a.adapters, std::min(a.requests, a.tokens)));
+  const int64_t least = std::max<int64_t>(16, std::min<int64_t>(64, a.tokens / used / 16 * 16));
   const int64_t c = (a.tokens + split - 1) / split;
-  return std::max<int64_t>(64, std::min<int64_t>(ranks == 16 ? 448 : 256, (c + 15) / 16 * 16));
+  return std::max<int64_t>(least, std::min<int64_t>(ranks == 16 ? 448 : 256, (c + 15) / 16 * 16));
 }
 
 int64_t outer_bytes(const snack_adapter_args &a, int64_t K) {
@@ -1421,8 +1658,27 @@ struct Back {
 };
 
 template <typename T>
+cudaError_t few_backward(const AdapterArgs &q, const Back &b, cudaStream_t s) {
+  const snack_adapter_args &a = q.a;
+  const FewArgs f = {b.dY, b.dy_stride, b.H, b.dX, b.dx_stride, b.dA, b.dB, b.dH};
+  const unsigned tokens = (unsigned)a.tokens, passes = (unsigned)((a.rank + kFewRanks - 1) / kFewRanks);
+  const int64_t in = (a.in + kThreads - 1) / kThreads, out = (a.out + kThreads - 1) / kThreads;
+  cudaError_t e = cudaSuccess;
+  if (b.dX || b.dA) e = launch_kernel(adapter_few_rank<T>, dim3(tokens, passes), kThreads, 0, true, s, q, f);
+  if (e == cudaSuccess && b.dX)
+    e = launch_kernel(adapter_few_input<T>, dim3((unsigned)in, tokens), kThreads, (size_t)a.rank * 4, true, s, q, f);
+  const int64_t blocks = (b.dA ? in : 0) + (b.dB ? out : 0);
+  if (e == cudaSuccess && blocks > 0)
+    e = launch_kernel(adapter_few_weights<T>,
+                      dim3((unsigned)blocks, (unsigned)std::min<int64_t>(a.adapters, 65535), passes), kThreads, 0,
+                      true, s, q, f);
+  return e;
+}
+
+template <typename T>
 cudaError_t backward(const AdapterArgs &q, const Back &b, cudaStream_t s) {
   const snack_adapter_args &a = q.a;
+  if (a.tokens <= kFewTokensBack) return few_backward<T>(q, b, s);
   cudaError_t e = launch_plan(q, s);
   if (e != cudaSuccess) return e;
   if (b.dX || b.dA) {
@@ -1452,7 +1708,7 @@ cudaError_t backward(const AdapterArgs &q, const Back &b, cudaStream_t s) {
 
 extern "C" size_t snack_adapter_forward_workspace(const snack_adapter_args *args) {
   using namespace snack;
-  if (bad_args(args) || args->tokens <= kFewTokens) return 16;
+  if (bad_args(args) || args->tokens <= kFewTokens) return 0;
   Plan p;
   return (size_t)lay_plan(*args, &p, nullptr);
 }
@@ -1464,7 +1720,7 @@ extern "C" snack_status snack_adapter_forward(const snack_adapter_args *args, vo
   const snack_adapter_args &a = *args;
   if (a.tokens == 0) return SNACK_OK;
   if (!Y || !H) return refuse(SNACK_ERR_INVALID_ARG, "Y or H is NULL");
-  if (!workspace || !aligned_to(workspace, 16))
+  if (a.tokens > kFewTokens && (!workspace || !aligned_to(workspace, 16)))
     return refuse(SNACK_ERR_INVALID_ARG, "workspace must be 16-byte aligned device memory");
   if (a.tokens > 1 && y_stride < a.out) return refuse(SNACK_ERR_INVALID_ARG, "y_stride is below out");
   if (!aligned_to(Y, type_bytes(a.type)) || !aligned_to(H, 4))
@@ -1475,7 +1731,7 @@ extern "C" snack_status snack_adapter_forward(const snack_adapter_args *args, vo
   AdapterArgs q = {};
   q.a = a;
   q.H = H;
-  lay_plan(a, &q.p, static_cast<char *>(workspace));
+  if (a.tokens > kFewTokens) lay_plan(a, &q.p, static_cast<char *>(workspace));
   const cudaError_t e = SNACK_TYPES(a.type, forward, q, Y, y_stride, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "adapter launch");
 }
@@ -1486,6 +1742,10 @@ namespace {
 // The backward's scratch: the plan, dH, turned weights of the used adapters,
 // parts of dA and dB.
 int64_t lay_back(const snack_adapter_args &a, Plan *p, Back *b, char *ws) {
+  if (a.tokens <= kFewTokensBack) {
+    b->dH = reinterpret_cast<float *>(ws);
+    return align16(std::max<int64_t>(4, a.tokens * a.rank * 4));
+  }
   int64_t at = lay_plan(a, p, ws);
   const auto take = [&](int64_t bytes) {
     char *r = ws ? ws + at : nullptr;
@@ -1518,7 +1778,7 @@ extern "C" snack_status snack_adapter_backward(const snack_adapter_args *args, c
   using namespace snack;
   if (const char *bad = bad_args(args)) return refuse(SNACK_ERR_INVALID_ARG, bad);
   const snack_adapter_args &a = *args;
-  if (!workspace || !aligned_to(workspace, 16))
+  if (a.tokens > 0 && (!workspace || !aligned_to(workspace, 16)))
     return refuse(SNACK_ERR_INVALID_ARG, "workspace must be 16-byte aligned device memory");
   if (a.tokens > 0 && (!dY || !H)) return refuse(SNACK_ERR_INVALID_ARG, "dY or H is NULL");
   if (a.tokens > 1 && (dy_stride < a.out || (dX && dx_stride < a.in)))

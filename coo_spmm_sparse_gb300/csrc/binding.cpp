@@ -141,6 +141,7 @@ struct Stream {
     }
   }
   at::Tensor scratch(size_t bytes, c10::Device d) const {
+    if (bytes == 0) return at::Tensor();
     at::Tensor t = empty({(int64_t)bytes}, at::kByte, d);
     if (given)
       c10::cuda::CUDACachingAllocator::recordStream(
@@ -148,6 +149,8 @@ struct Stream {
     return t;
   }
 };
+
+void *scratch_addr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 double number(PyObject *o) {
   const double v = PyFloat_AsDouble(o);
@@ -343,7 +346,7 @@ PyObject *norm_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
     g.dnext_weight = param("dnext_weight", 2);
     g.dnext_bias = param("dnext_bias", 3);
     const at::Tensor ws = s.scratch(snack_residual_norm_workspace(&m.a), m.dev.dev);
-    check(snack_residual_norm_backward(&m.a, &g, ws.data_ptr(), s.raw));
+    check(snack_residual_norm_backward(&m.a, &g, scratch_addr(ws), s.raw));
     return hold.release();
   });
 }
@@ -456,7 +459,7 @@ PyObject *adapter_forward(PyObject *, PyObject *const *o, Py_ssize_t n) {
       H = m.hidden(o[7]);
     }
     const at::Tensor ws = s.scratch(snack_adapter_forward_workspace(&m.a), m.dev.dev);
-    check(snack_adapter_forward(&m.a, Y.data_ptr(), ys, H, ws.data_ptr(), s.raw));
+    check(snack_adapter_forward(&m.a, Y.data_ptr(), ys, H, scratch_addr(ws), s.raw));
     return Py_BuildValue("(NN)", same(o[6]), fresh.defined() ? wrap(fresh) : same(o[7]));
   });
 }
@@ -487,7 +490,7 @@ PyObject *adapter_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
     }
     const at::Tensor ws = s.scratch(snack_adapter_backward_workspace(&m.a), m.dev.dev);
     check(snack_adapter_backward(&m.a, dY.data_ptr(), dys, H, dX, dxs, need_dw ? dA.data_ptr() : nullptr,
-                                 need_dw ? dB.data_ptr() : nullptr, ws.data_ptr(), s.raw));
+                                 need_dw ? dB.data_ptr() : nullptr, scratch_addr(ws), s.raw));
     return Py_BuildValue("(NNN)", !need_dx ? same(Py_None) : (fresh.defined() ? wrap(fresh) : same(o[8])),
                          need_dw ? wrap(dA) : same(Py_None), need_dw ? wrap(dB) : same(Py_None));
   });
@@ -584,7 +587,7 @@ PyObject *grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int64_t c = (int64_t)g.l->ptr.size();
     const at::Tensor ws = s.scratch(snack_grad_norm_workspace(c), g.l->dev);
     check(snack_grad_norm(c, const_cast<const void *const *>(g.l->ptr.data()), g.l->size.data(), g.l->type.data(),
-                          kind, static_cast<float *>(norm.data_ptr()), ws.data_ptr(), s.raw));
+                          kind, static_cast<float *>(norm.data_ptr()), scratch_addr(ws), s.raw));
     return o[2] == Py_None ? wrap(norm) : same(o[2]);
   });
 }
@@ -610,7 +613,7 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
     check(snack_clip_grad_norm(c, const_cast<const void *const *>(g.l->ptr.data()),
                                out ? out->l->ptr.data() : nullptr, g.l->size.data(), g.l->type.data(),
                                out ? out->l->type.data() : nullptr, kind, (float)max_norm, (float)number(o[4]),
-                               static_cast<float *>(norm.data_ptr()), ws.data_ptr(), s.raw));
+                               static_cast<float *>(norm.data_ptr()), scratch_addr(ws), s.raw));
     return o[5] == Py_None ? wrap(norm) : same(o[5]);
   });
 }

@@ -314,24 +314,10 @@ inline void team_ring(TeamPlan *p, const snack_norm_args &a, int ns, int nb) {
 
 template <typename K>
 cudaError_t launch_team(K kern, const TeamPlan &p, int64_t teams, const TeamArgs &q, cudaStream_t s) {
-  cudaError_t e = allow_smem(kern, p.smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(teams * p.cluster));
-  cfg.blockDim = dim3((unsigned)(p.threads * p.per_block));
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, q);
-  if (e == cudaSuccess) count_launches(1);
-  return e;
+  const cudaError_t e = allow_smem(kern, p.smem);
+  return e != cudaSuccess ? e
+                          : launch_clusters(kern, dim3((unsigned)(teams * p.cluster)), p.cluster,
+                                            p.threads * p.per_block, p.smem, true, s, q);
 }
 
 // The forms of a call that are compiled on their own, because their many

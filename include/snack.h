@@ -308,7 +308,7 @@ snack_status snack_forward_csr_static(int64_t out_features, int64_t in_features,
  * is stored.  They allocate nothing: where a call needs scratch, the caller
  * passes a `workspace` of the size that the matching *_workspace() call gives
  * (16-byte aligned device memory, in use until the call's work on `stream` is
- * done; its contents need not be set).  Results do not depend on the order in
+ * done; its contents need not be set; NULL where that size is 0).  Results do not depend on the order in
  * which blocks run: the same inputs give the same bits.  Errors are reported
  * through snack_last_error(NULL).  All are asynchronous on `stream`, do not
  * synchronise and can be captured into a CUDA graph.  The paper has no

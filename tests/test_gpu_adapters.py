@@ -70,6 +70,13 @@ def test_one_token_per_request(dt, T):
     check(make(list(range(T + 1)), which, 7, 160, 96, 16, dt, seed=T))
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T", [64, 65, 128, 129, 300])
+@pytest.mark.parametrize("inp,out,rank", [(2304, 768, 12), (1001, 4096, 33), (64, 2048, 16)])
+def test_few_tiles_of_wide_rows(dt, T, inp, out, rank):
+    check(make([0, 7, 50, T], [1, 0, 1], 2, inp, out, rank, dt, seed=T))
+
+
 @pytest.mark.parametrize("T,R,N", [(1, 1, 1), (700, 1, 1), (1500, 40, 3), (1031, 9, 30),
                                    (300, 300, 2), (2100, 1500, 40)])
 def test_many_requests_and_tokens(T, R, N):
@@ -123,6 +130,19 @@ def test_strided_rows_and_misaligned_starts(dt, pad, at):
 
     for k in ("X", "Y", "dX", "dY"):
         c[k] = wide(c[k])
+    check(c)
+
+
+@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("size", [2.0 ** -14, 1.0, 2.0 ** 9])
+def test_float16_beyond_its_range(T, size):
+    """H of up to 2^18 and gradients of 2^-14 in float16: what lies between the
+    two products never is a float16."""
+    c = make([0, 9, T], [1, 0], 2, 192, 160, 16, F16, seed=T)
+    c["X"] = (c["X"].float() * size).half()
+    c["A"] = (c["A"].float() * max(1.0, size / 8)).half()
+    c["B"] = (c["B"].float() / max(1.0, size * size / 8)).half()
+    c["dY"] = (c["dY"].float() * min(size, 1 / size)).half()
     check(c)
 
 
