@@ -909,8 +909,9 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
   constexpr int TS = sizeof(T) == 4 ? 8 : 16;  // tokens of a step
   constexpr int NR = TS / 4, STAGES = OuterShape<T>::STAGES;
   constexpr int FLUSH = 32 / TS;               // steps between two sums outside the matrix unit
-  extern __shared__ uint4 smem4[];             // the warps' rings, [chunk][LD] floats of H, the chunk's tokens
-  float *hs = reinterpret_cast<float *>(smem4 + OuterShape<T>::RING);
+  extern __shared__ uint4 smem4[];             // the warps' rings, the chunk's rows, [chunk][LD] floats of H, its tokens
+  int64_t *row_of = reinterpret_cast<int64_t *>(smem4 + OuterShape<T>::RING);  // elements before the row of X
+  float *hs = reinterpret_cast<float *>(row_of + d.chunk);
   int32_t *tok = reinterpret_cast<int32_t *>(hs + d.chunk * LD);
   const int64_t slice = block / d.blocks, cblock = block % d.blocks;
   const int64_t p0 = slice * d.chunk;
@@ -919,7 +920,10 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
   const int64_t j0 = (int64_t)blockIdx.y * 16 * RM;
   // the chunk's tokens, then their H: two rounds of loads, each all at once,
   // the second one over while the first rows of X are on their way
-  for (int i = threadIdx.x; i < places; i += kThreads) tok[i] = q.p.perm[p0 + i];
+  for (int i = threadIdx.x; i < places; i += kThreads) {
+    tok[i] = q.p.perm[p0 + i];
+    row_of[i] = tok[i] * d.x_stride;
+  }
   // the first adapter of the chunk: the last used one that begins at or before p0
   int u = 0;
   {
@@ -999,7 +1003,7 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
           const int row = 4 * i + (lane >> 3), k = p + step * TS + row;
           const bool in = copy_ok && k < end;
           copy16(ring + (step % STAGES) * NR * 32 + row * 8 + ((lane & 7) ^ turn(row)),
-                 copy_from + (in ? tok[k] * d.x_stride : 0), 0, 1, in);
+                 copy_from + (in ? row_of[k] : 0), 0, 1, in);
         }
       copies_commit();
     };
@@ -1035,7 +1039,7 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
         if (ALIGNED)
           x[i] = ring[(step % STAGES) * NR * 32 + row * 8 + (g ^ turn(row))];
         else
-          x[i] = load16<T, false>(X + (k < end ? (int64_t)tok[k] * d.x_stride : 0), col, d.K, k < end);
+          x[i] = load16<T, false>(X + (k < end ? row_of[k] : 0), col, d.K, k < end);
 #pragma unroll
         for (int m = 0; m < 2 * RM; ++m) {
           h[i][m] = k < end ? hs[k * LD + m * 8 + g] : 0.f;
@@ -1602,7 +1606,7 @@ cudaError_t launch_outer(const AdapterArgs &q, OuterPair pair, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (q.p.max_used > 0) {
     auto k = ranks == 16 ? adapter_outer<T, 1> : adapter_outer<T, 2>;
-    const size_t smem = (size_t)OuterShape<T>::RING * 16 + (size_t)chunk * (ranks + 8 + 1) * 4;
+    const size_t smem = (size_t)OuterShape<T>::RING * 16 + (size_t)chunk * ((ranks + 8 + 1) * 4 + 8);
     if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
     const dim3 grid((unsigned)blocks, (unsigned)((a.rank + ranks - 1) / ranks));
     if ((e = launch_kernel(k, grid, kThreads, smem, true, s, q, pair)) != cudaSuccess) return e;

@@ -222,6 +222,43 @@ def test_module_matches_autograd_of_the_definition():
         assert torch.allclose(got[k].double(), v.grad, rtol=1e-4, atol=1e-5 * float(scale)), k
 
 
+def test_plain_norm_carries_both_gradients():
+    import coo_spmm_sparse_gb300 as sn
+    torch.manual_seed(1)
+    x = torch.randn(3, 5, 160, device="cuda", requires_grad=True)
+    w = torch.randn(160, device="cuda", requires_grad=True)
+    c1, c2 = torch.randn(2, 3, 5, 160, device="cuda")
+    r, h = sn.snack_residual_norm(x, next_weight=w, kind="layer")
+    ((r * c1).sum() + (h * c2).sum()).backward()
+    x64, w64 = (t.detach().double().requires_grad_() for t in (x, w))
+    hh = torch.nn.functional.layer_norm(x64, (160,), w64, None, 1e-5)
+    ((x64 * c1.double()).sum() + (hh * c2.double()).sum()).backward()
+    assert torch.equal(r, x)
+    for got, want in ((x.grad, x64.grad), (w.grad, w64.grad)):
+        assert torch.allclose(got.double(), want, rtol=1e-4, atol=1e-5 * float(want.abs().max()))
+    # only one of the two is used
+    x.grad = None
+    sn.snack_residual_norm(x, next_weight=w)[1].square().sum().backward()
+    assert x.grad is not None
+
+
+def test_mixed_types_through_the_module():
+    import coo_spmm_sparse_gb300 as sn
+    torch.manual_seed(2)
+    m = sn.SnackResidualNorm(256, kind="rms", post=True, gate="channel", gate_init=0.25)
+    x = torch.randn(2, 6, 256, device="cuda", requires_grad=True)
+    y = torch.randn(2, 6, 256, device="cuda").bfloat16().requires_grad_()
+    r, h = m(x, y)
+    assert r.dtype == F32 and h.dtype == BF16
+    (r.sum() + h.float().square().sum()).backward()
+    assert x.grad.dtype == F32 and y.grad.dtype == BF16 and m.gate.grad.dtype == F32
+    want = dense_ref.residual_norm(x, y, kind="rms", post_norm=True, post_weight=m.post_weight,
+                                   gate=m.gate.detach().bfloat16(), next_weight=m.next_weight,
+                                   dr=torch.ones_like(x), dh=(2 * h.detach().float()).bfloat16())
+    for got, k in ((x.grad, "dx"), (y.grad, "dy"), (m.next_weight.grad, "dnext_weight")):
+        assert_within(k, got, *want[k])
+
+
 def test_same_bits_every_time_and_on_another_stream():
     import coo_spmm_sparse_gb300 as sn
     x, y, o, dr, dh = make((4, 513, 768), "rms", True, "sequence", BF16, BF16, seed=12)
