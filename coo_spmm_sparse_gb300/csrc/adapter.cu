@@ -4,30 +4,33 @@
 //   dH[t] = s_n B_n^T dY[t],  dX[t] += A_n^T dH[t],
 //   dA_n = sum_t dH[t] X[t]^T,  dB_n = s_n sum_t dY[t] H[t]^T
 //
-// Memory bound for ranks up to about 64: every element of X, Y, dY and dX
-// takes 2 * rank multiply-adds.  Few tokens (decoding): a block for each
-// token, the weights are the work.  Many tokens: they are first grouped by
-// adapter (`plan`), so that requests that share one fill tiles together,
-// and each product then runs over tiles of 32 tokens on the matrix
+// Memory bound for ranks up to about 32: every element of X, Y, dY and dX
+// takes 2 * rank multiply-adds.  Few tokens (decoding): a cluster of blocks
+// for each token, the weights are the work.  Many tokens: they are first
+// grouped by adapter (`plan`), so that requests that share one fill tiles
+// together, and each product then runs over tiles of 32 tokens on the matrix
 // instructions:
 //
 //   down   [tokens x K] x [K x rank]   K split over the block's warps, one sum through shared memory
 //   up     [tokens x rank] x [rank x K], added to the rows in place
 //   outer  [rank x tokens] x [tokens x K], tokens split over blocks, parts added in order
 //
-// Operands go from memory straight into the registers that the matrix
-// instruction wants them in.  The order in which the summed index is fed to
-// it is free as long as both operands keep it, so a lane takes 16 contiguous
-// bytes of a row and the four lanes of a row take 64.  A lane's rows come by
-// asynchronous copies into slots of shared memory that it alone reads: they
-// are registers that can wait for memory, several steps ahead, and need no
-// barrier.  (Loads into registers left 64 bytes in flight per lane at one
-// block per SM: 47 us for `down` and 80 us for `outer` over 134 MB.)
-// fp32 operands are split
-// into two tf32 parts, x = hi + lo, and hi*hi + hi*lo + lo*hi is summed:
-// what is left out is below 2^-22 of a product.  Running sums leave the
-// matrix unit's accumulator every few steps for a 32-bit sum that rounds to
-// nearest.
+// The order in which the summed index is fed to a matrix instruction is free
+// as long as both operands keep it, so a lane takes 16 contiguous bytes of a
+// row as they lie in memory, and rows may be any tokens.  Rows come by
+// asynchronous copies into a ring of shared memory that belongs to one warp:
+// registers that can wait for memory, and no barrier of the block.  (Loads
+// into registers left one block's 64 bytes a lane in flight: 47 us for `down`
+// and 80 us for `outer` over 134 MB; now 31 and 32 us.)
+//
+// fp32 operands are split into two tf32 parts, x = hi + lo, and hi*hi + hi*lo
+// + lo*hi is summed: what is left out is below 2^-22 of a product.  Running
+// sums leave the matrix unit's accumulator every 32 summed elements for a
+// 32-bit sum that rounds to nearest (kept in it over 300 tokens, dA was 2.4e-6
+// off in the 2-norm; so 6.6e-7).
+//
+// 8192 tokens, 4096 -> 4096, 4 adapters of rank 16, fp32: forward and backward
+// 240 us, 160 us of which is the traffic at 6.7 TB/s.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -429,7 +432,7 @@ struct DownArgs {
 template <int NT>
 struct DownShape {
   static constexpr int ROWS = kTile + NT * 8;
-  static constexpr int STAGES = 2;  // 80 to 128 KB a block, two blocks an SM up to 16 ranks
+  static constexpr int STAGES = 2;  // 80 to 192 KB a block: two blocks an SM up to 16 ranks, one above
   static constexpr int LD = NT * 8 + 4;
   static constexpr size_t RING = (size_t)kWarps * STAGES * ROWS * 128;
   static constexpr size_t PART = sizeof(float) * kWarps * kTile * LD;
@@ -1222,10 +1225,11 @@ __global__ void __launch_bounds__(kThreads) adapter_turn(const __grid_constant__
 
 // Up to this many tokens are taken one by one, forward and backward: the
 // weights of each are read for it alone, and no plan is made.  4096 x 4096
-// at rank 16, fp32, one by one / by tiles: forward 128 tokens 14.6 / 14 us
-// (10: 8.4 us); forward + backward of 64 tokens of one adapter 50 / 46 us
-// and of 16 adapters 35 / 74 us, of 128 tokens 63 / 46 and 52 / 74 us.
-constexpr int kFewTokens = 128, kFewTokensBack = 64;
+// at rank 16, fp32, one by one / by tiles: forward 10 tokens 7, 64 10.3, 100
+// 16.8 / 13.5 us (768 -> 2304 at rank 8: 100 tokens 9 / 12.4); forward +
+// backward of 64 tokens of one adapter 50 / 46 us and of 16 adapters 35 / 74
+// us, of 128 tokens 63 / 46 and 52 / 74 us.
+constexpr int kFewTokens = 96, kFewTokensBack = 64;
 
 struct FewArgs {
   const void *dY;
@@ -1245,70 +1249,126 @@ __device__ __forceinline__ int adapter_of(const snack_adapter_args &a, int64_t t
   return n >= 0 && n < a.adapters ? n : -1;
 }
 
-// A warp for each (token, rank).
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) adapter_few_down(const __grid_constant__ AdapterArgs q) {
-  constexpr int E = 16 / sizeof(T), U = 4;
-  dependency_wait();
-  dependency_launch();
-  const snack_adapter_args &a = q.a;
-  const int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (at >= a.tokens * a.rank) return;
-  const int64_t tkn = at / a.rank, j = at % a.rank;
-  const int lane = threadIdx.x & 31;
-  const int n = adapter_of(a, tkn);
-  float s = 0.f;
-  if (n >= 0) {
-    const T *x = static_cast<const T *>(a.X) + tkn * a.x_stride;
-    const T *w = static_cast<const T *>(a.A) + ((int64_t)n * a.rank + j) * a.in;
-    for (int64_t k0 = lane * E; k0 < a.in; k0 += U * 32 * E) {
-      uint4 xv[U], wv[U];
+// The same for one token, by a whole warp: the requests that begin at or
+// before it are counted 128 at a time, so that two rounds of loads do (a
+// search by halves waits for memory at every step).
+__device__ __forceinline__ int adapter_of_warp(const snack_adapter_args &a, int64_t t) {
+  constexpr int kMost = 1024;
+  if (a.requests > kMost) return adapter_of(a, t);
+  const int lane = threadIdx.x & 31, R = (int)a.requests;
+  int begun = 0;
+  for (int b = 0; b < R; b += 128) {
+    bool is[4];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        xv[u] = load16<T, ALIGNED>(x, k0 + u * 32 * E, a.in, true);
-        wv[u] = load16<T, ALIGNED>(w, k0 + u * 32 * E, a.in, true);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          s = fmaf(to_float(reinterpret_cast<const T *>(&xv[u])[e]), to_float(reinterpret_cast<const T *>(&wv[u])[e]), s);
+    for (int i = 0; i < 4; ++i) {
+      const int r = b + 32 * i + lane;
+      is[i] = r < R && a.offsets[r] <= t;
     }
-    s = warp_sum(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) begun += __popc(__ballot_sync(0xffffffffu, is[i]));
   }
-  if (lane == 0) q.H[at] = s;
+  if (begun == 0) return -1;
+  const int end = a.offsets[begun], n = a.adapter[begun - 1];
+  return t < end && n >= 0 && n < a.adapters ? n : -1;
 }
 
-// Block (256 columns, token): one thread for each column.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) adapter_few_up(const __grid_constant__ AdapterArgs q, T *Y,
-                                                           int64_t y_stride) {
-  extern __shared__ float h[];
+// Forward of few tokens: a cluster of blocks for each token.  Every block
+// takes a share of X's row and of each row of A, sends its sums to the
+// others' shared memory, and then has H and a share of the columns of Y.  The
+// rows of B that it will need are on their way from the start.  (Two kernels,
+// one for H and one for Y, took 9.8 us for 64 tokens, 4096 -> 4096 at rank 16
+// in bf16, and 5.7 us for 8 tokens, 768 -> 2304 at rank 8.)
+constexpr int kFewBlocks = 8;
+constexpr int kFewAhead = 32 * 1024;  // most bytes of B copied ahead by a block
+
+template <typename T, bool ALIGNED>
+__global__ void __cluster_dims__(kFewBlocks, 1, 1) __launch_bounds__(kThreads)
+    adapter_few(const __grid_constant__ AdapterArgs q, T *Y, int64_t y_stride, bool ahead) {
+  constexpr int E = 16 / sizeof(T), J = 4;
+  extern __shared__ uint4 smem4[];  // [blocks][rank] floats: all blocks' sums; [rank]: scaled H; rows of B
   const snack_adapter_args &a = q.a;
+  cg::cluster_group cluster = cg::this_cluster();
+  constexpr int blocks = kFewBlocks;
+  const int part = (int)cluster.block_rank(), rank = (int)a.rank;
+  float *sums = reinterpret_cast<float *>(smem4), *h = sums + blocks * rank;
+  T *rows = reinterpret_cast<T *>(smem4 + ((blocks + 1) * rank + 3) / 4);
   dependency_wait();
   dependency_launch();
-  const int64_t tkn = blockIdx.y, o = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int n = adapter_of(a, tkn);
-  if (n < 0) return;
-  const float scale = scale_of(a, n);
-  for (int64_t j = threadIdx.x; j < a.rank; j += kThreads) h[j] = q.H[tkn * a.rank + j] * scale;
-  __syncthreads();
-  if (o >= a.out) return;
-  T *y = Y + tkn * y_stride + o;
-  const T *w = static_cast<const T *>(a.B) + ((int64_t)n * a.out + o) * a.rank;
-  constexpr int E = 16 / sizeof(T);
-  const float y0 = to_float(*y);
-  float s = 0.f;
-  if (a.rank % E == 0 && (reinterpret_cast<uintptr_t>(a.B) & 15) == 0) {
-    for (int64_t j = 0; j < a.rank; j += E) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(w + j);
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(h[j + e], to_float(reinterpret_cast<const T *>(&v)[e]), s);
-    }
-  } else {
-    for (int64_t j = 0; j < a.rank; ++j) s = fmaf(h[j], to_float(w[j]), s);
+  const int64_t tkn = blockIdx.x / blocks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = adapter_of_warp(a, tkn);
+  if (n < 0) {  // the whole cluster
+    for (int j = part * kThreads + threadIdx.x; j < rank; j += blocks * kThreads) q.H[tkn * rank + j] = 0.f;
+    return;
   }
-  *y = from_float<T>(y0 + s);
+  // this block's columns of Y, from a multiple of 8 on
+  const int64_t share = ((a.out + blocks - 1) / blocks + 7) / 8 * 8;
+  const int64_t o0 = min(a.out, part * share), o1 = min(a.out, o0 + share);
+  const T *B = static_cast<const T *>(a.B) + ((int64_t)n * a.out + o0) * rank;
+  if (ahead) {
+    const int64_t bytes = (o1 - o0) * rank * (int64_t)sizeof(T);
+    for (int64_t i = threadIdx.x * 16; i < bytes; i += kThreads * 16)
+      copy_async16(reinterpret_cast<char *>(rows) + i, reinterpret_cast<const char *>(B) + i);
+  }
+  copies_commit();
+  T *y = Y + tkn * y_stride + o0;
+  const float y0 = threadIdx.x < o1 - o0 ? to_float(y[threadIdx.x]) : 0.f;
+
+  const int64_t slice = ((a.in + blocks - 1) / blocks + E - 1) / E * E;
+  const int64_t k0 = min(a.in, part * slice), k1 = min(a.in, k0 + slice);
+  const T *x = static_cast<const T *>(a.X) + tkn * a.x_stride;
+  const T *A = static_cast<const T *>(a.A) + (int64_t)n * rank * a.in;
+  cluster.sync();  // all blocks are there: their shared memory may be written
+  for (int j0 = warp * J; j0 < rank; j0 += kWarps * J) {
+    float s[J];
+#pragma unroll
+    for (int i = 0; i < J; ++i) s[i] = 0.f;
+#pragma unroll 2
+    for (int64_t k = k0 + lane * E; k < k1; k += 32 * E) {
+      const uint4 xv = load16<T, ALIGNED>(x, k, k1, true);
+      uint4 w[J];
+#pragma unroll
+      for (int i = 0; i < J; ++i) w[i] = load16<T, ALIGNED>(A + (int64_t)min(j0 + i, rank - 1) * a.in, k, k1, j0 + i < rank);
+#pragma unroll
+      for (int i = 0; i < J; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          s[i] = fmaf(to_float(reinterpret_cast<const T *>(&xv)[e]), to_float(reinterpret_cast<const T *>(&w[i])[e]), s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < J; ++i) s[i] = warp_sum(s[i]);
+    // lane 8 i + b sends rank j0 + i to block b
+    const int i = lane >> 3;
+    const float v = i == 0 ? s[0] : i == 1 ? s[1] : i == 2 ? s[2] : s[3];
+    if (j0 + i < rank) cluster.map_shared_rank(sums, lane & 7)[part * rank + j0 + i] = v;
+  }
+  cluster.sync();  // and none leaves before all have written
+  const float scale = scale_of(a, n);
+  for (int j = threadIdx.x; j < rank; j += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int b = 0; b < blocks; ++b) v += sums[b * rank + j];
+    h[j] = v * scale;
+    if (part == 0) q.H[tkn * rank + j] = v;
+  }
+  copies_wait<0>();
+  __syncthreads();
+  const bool vec = rank % E == 0 && (reinterpret_cast<uintptr_t>(a.B) & 15) == 0;
+  for (int64_t o = threadIdx.x; o < o1 - o0; o += kThreads) {
+    const T *w = ahead ? rows + o * rank : B + o * rank;
+    float s = 0.f;
+    if (vec) {
+#pragma unroll 4
+      for (int j = 0; j < rank; j += E) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(w + j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s = fmaf(h[j + e], to_float(reinterpret_cast<const T *>(&v)[e]), s);
+      }
+    } else {
+      for (int j = 0; j < rank; ++j) s = fmaf(h[j], to_float(w[j]), s);
+    }
+    y[o] = from_float<T>((o < kThreads ? y0 : to_float(y[o])) + s);
+  }
 }
 
 // dH of few tokens.  Block (token, 16 ranks): a thread takes every 256th row of B.
@@ -1323,7 +1383,7 @@ __global__ void __launch_bounds__(kThreads) adapter_few_rank(const __grid_consta
   const snack_adapter_args &a = q.a;
   const int64_t tkn = blockIdx.x, j0 = (int64_t)blockIdx.y * kFewRanks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = adapter_of(a, tkn), ranks = (int)min((int64_t)kFewRanks, a.rank - j0);
+  const int n = adapter_of_warp(a, tkn), ranks = (int)min((int64_t)kFewRanks, a.rank - j0);
   float s[kFewRanks];
 #pragma unroll
   for (int j = 0; j < kFewRanks; ++j) s[j] = 0.f;
@@ -1377,7 +1437,7 @@ __global__ void __launch_bounds__(kThreads) adapter_few_input(const __grid_const
   dependency_launch();
   const snack_adapter_args &a = q.a;
   const int64_t tkn = blockIdx.y, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int n = adapter_of(a, tkn);
+  const int n = adapter_of_warp(a, tkn);
   if (n < 0) return;
   for (int64_t j = threadIdx.x; j < a.rank; j += kThreads) h[j] = b.dH[tkn * a.rank + j];
   __syncthreads();
@@ -1632,14 +1692,15 @@ template <typename T>
 cudaError_t forward(const AdapterArgs &q, void *Y, int64_t y_stride, cudaStream_t s) {
   const snack_adapter_args &a = q.a;
   if (a.tokens <= kFewTokens) {
-    const dim3 grid((unsigned)((a.tokens * a.rank + kWarps - 1) / kWarps));
-    auto k = vector_rows(a.X, a.x_stride, a.in, a.type) && aligned_to(a.A, 16) ? adapter_few_down<T, true>
-                                                                                : adapter_few_down<T, false>;
-    cudaError_t e = launch_kernel(k, grid, kThreads, 0, true, s, q);
-    if (e != cudaSuccess) return e;
-    const dim3 up((unsigned)((a.out + kThreads - 1) / kThreads), (unsigned)a.tokens);
-    return launch_kernel(adapter_few_up<T>, up, kThreads, (size_t)a.rank * 4, true, s, q, static_cast<T *>(Y),
-                         y_stride);
+    constexpr int64_t blocks = kFewBlocks;
+    const int64_t share = ((a.out + blocks - 1) / blocks + 7) / 8 * 8, bytes = share * a.rank * (int64_t)sizeof(T);
+    const bool ahead = bytes <= kFewAhead && aligned_to(a.B, 16) && a.out * a.rank * (int64_t)sizeof(T) % 16 == 0;
+    const size_t smem = (size_t)((blocks + 1) * a.rank + 3) / 4 * 16 + (ahead ? (size_t)bytes : 0);
+    auto k = vector_rows(a.X, a.x_stride, a.in, a.type) && aligned_to(a.A, 16) ? adapter_few<T, true> : adapter_few<T, false>;
+    const cudaError_t e = allow_smem(k, smem);
+    return e != cudaSuccess ? e
+                            : launch_kernel(k, dim3((unsigned)(a.tokens * blocks)), kThreads, smem, true, s, q,
+                                            static_cast<T *>(Y), y_stride, ahead);
   }
   cudaError_t e = launch_plan(q, s);
   if (e != cudaSuccess) return e;

@@ -397,7 +397,9 @@ snack_status snack_residual_norm_backward(const snack_norm_args *args,
  * is outside [0, adapters), and tokens outside every request, keep their Y
  * (H is zero there).  offsets [requests + 1] (non-decreasing, in [0, tokens])
  * and adapter [requests] are int32 device arrays and never read by the host;
- * values that break this are clamped, never followed out of bounds.
+ * values that break this are clamped, never followed out of bounds.  In fp32
+ * an operand beyond 2^128 - 2^116, infinities among them, may give NaN where
+ * the sum is infinite.
  * X and Y rows lie x_stride / y_stride elements apart.  X, Y, A and B are of
  * `type`; scale and H [tokens][rank] are fp32.  H is what the backward call
  * reads.  Limits: 1 <= rank <= 512, tokens, requests, in, out < 2^31,
