@@ -24,9 +24,9 @@
 // and 80 us for `outer` over 134 MB; now 31 and 32 us.)
 //
 // fp32 operands are split into two tf32 parts, x = hi + lo, and hi*hi + hi*lo
-// + lo*hi is summed: what is left out is below 2^-22 of a product.  Running
-// sums leave the matrix unit's accumulator every 32 summed elements for a
-// 32-bit sum that rounds to nearest (kept in it over 300 tokens, dA was 2.4e-6
+// + lo*hi is summed: what is left out is below 2^-22 of a product.  Their
+// running sums leave the matrix unit's accumulator every 32 summed elements for
+// a 32-bit sum that rounds to nearest (kept in it over 300 tokens, dA was 2.4e-6
 // off in the 2-norm; so 6.6e-7).
 //
 // 8192 tokens, 4096 -> 4096, 4 adapters of rank 16, fp32: forward and backward
@@ -51,6 +51,13 @@ constexpr int kRankPass = 64;        // ranks that one pass of `down` sums
 
 // Ranks that one pass of `outer` sums.
 __host__ __device__ constexpr int outer_ranks(int64_t rank) { return rank <= 16 ? 16 : 32; }
+
+// Whether running sums leave the matrix unit now and then: 16-bit results
+// (rounded to 2^-8 or 2^-11) do not show what its accumulator cuts off over some
+// hundred steps (1e-6), and the second set of sums costs registers that the
+// 32-rank products do not have.
+template <typename T>
+constexpr bool kFlush = sizeof(T) == 4;
 
 // Tokens grouped by adapter.
 struct Plan {
@@ -490,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
     }
     if (ALIGNED) copies_commit();
   };
-  float sum[MT][NT][4], acc[MT][NT][4];
+  float sum[MT][NT][4], fresh[MT][NT][4];
+  auto &acc = kFlush<T> ? fresh : sum;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -498,15 +506,17 @@ __global__ void __launch_bounds__(kThreads, NT <= 4 ? 2 : 1) adapter_down(const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[m][n][i] = acc[m][n][i] = 0.f;
   const auto flush = [&] {
+    if constexpr (kFlush<T>) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[m][n][i] += acc[m][n][i];
-          acc[m][n][i] = 0.f;
-        }
+          for (int i = 0; i < 4; ++i) {
+            sum[m][n][i] += acc[m][n][i];
+            acc[m][n][i] = 0.f;
+          }
+    }
   };
 
 #pragma unroll
@@ -668,7 +678,8 @@ __device__ __forceinline__ void load_ranks(const T *row, int64_t j, int64_t rank
 // left a fifth of the SMs' time idle).  A tile's H is kept in shared memory,
 // split in two parts, in the order in which the lanes want it.  RG: 16-rank
 // groups (1 or 2, weights copied ahead with the rows; 0: any number, weights
-// loaded when they are needed).
+// loaded when they are needed: ahead, 64 ranks measured the same in fp32 and
+// 350 us for 330 in bf16, forward and backward).
 template <typename T, int RG, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant__ AdapterArgs q,
                                                           const __grid_constant__ UpArgs d) {
@@ -974,7 +985,8 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.f;
-    float acc[RM][NT][4];
+    float fresh[RM][NT][4];
+    auto &acc = kFlush<T> ? fresh : sum;
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
@@ -982,15 +994,17 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
     const auto flush = [&] {
+      if constexpr (kFlush<T>) {
 #pragma unroll
-      for (int m = 0; m < RM; ++m)
+        for (int m = 0; m < RM; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum[m][n][i] += acc[m][n][i];
-            acc[m][n][i] = 0.f;
-          }
+            for (int i = 0; i < 4; ++i) {
+              sum[m][n][i] += acc[m][n][i];
+              acc[m][n][i] = 0.f;
+            }
+      }
     };
     const int steps = (end - p + TS - 1) / TS;
     // Eight lanes copy a row's 128 bytes (one line for each request: by the
@@ -1155,14 +1169,14 @@ __global__ void __launch_bounds__(kThreads) adapter_outer_finish(const __grid_co
     float s[4] = {0.f, 0.f, 0.f, 0.f};  // ranks j0 + ty + 8 i
     if (u >= 0) {
       const int4 use = q.p.used[u];
-      const int64_t s0 = use.y / d.chunk + u, s1 = (use.y + use.z - 1) / d.chunk + u;
-      const float *at = d.parts + (j0 + ty) * d.K + c0 + tx;
+      const int chunk = (int)d.chunk, s0 = use.y / chunk + u, s1 = (use.y + use.z - 1) / chunk + u;
+      const float *at = d.parts + s0 * per + (j0 + ty) * d.K + c0 + tx;
       const bool in = c0 + tx < d.K;
-#pragma unroll 4
-      for (int64_t k = s0; k <= s1; ++k)
+#pragma unroll 8
+      for (int k = s0; k <= s1; ++k, at += per)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (in && j0 + ty + 8 * i < d.rank) s[i] += at[k * per + 8 * i * d.K];
+          if (in && j0 + ty + 8 * i < d.rank) s[i] += at[8 * i * d.K];
       if (d.scaled) {
         const float scale = scale_of(q.a, (int)n);
 #pragma unroll

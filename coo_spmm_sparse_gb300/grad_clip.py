@@ -37,7 +37,7 @@ def snack_tensor_list(tensors) -> SnackTensorList:
 
 
 def _handle(tensors):
-    return tensors.handle if isinstance(tensors, SnackTensorList) else list(tensors)
+    return tensors.handle if isinstance(tensors, SnackTensorList) else tensors
 
 
 def snack_grad_norm(grads, norm_type: float = 2.0, norm: torch.Tensor | None = None,
