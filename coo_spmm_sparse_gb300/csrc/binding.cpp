@@ -9,8 +9,8 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -20,6 +20,7 @@
 #include <cstring>
 #include <limits>
 #include <memory>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -126,27 +127,22 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
   return at::detail::empty_cuda(sizes, type, dev, std::nullopt);
 }
 
-// The stream of a call and scratch that stays reserved until its work is done.
+// The stream of a call.  One that is given is made current for the call: what
+// it allocates and clears belongs to that stream, as under torch.cuda.stream().
 struct Stream {
   void *raw;
-  bool given = false;
-  c10::DeviceIndex dev;
-  Stream(PyObject *o, c10::Device d) : dev(d.index()) {
+  std::optional<c10::cuda::CUDAStreamGuard> guard;
+  Stream(PyObject *o, c10::Device d) {
     if (o == Py_None) {
-      raw = c10::cuda::getCurrentCUDAStream(dev).stream();
-    } else {
-      raw = PyLong_AsVoidPtr(o);
-      if (PyErr_Occurred()) throw Raised{};
-      given = true;
+      raw = c10::cuda::getCurrentCUDAStream(d.index()).stream();
+      return;
     }
+    raw = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Raised{};
+    guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), d.index()));
   }
   at::Tensor scratch(size_t bytes, c10::Device d) const {
-    if (bytes == 0) return at::Tensor();
-    at::Tensor t = empty({(int64_t)bytes}, at::kByte, d);
-    if (given)
-      c10::cuda::CUDACachingAllocator::recordStream(
-          t.storage().data_ptr(), c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), dev));
-    return t;
+    return bytes ? empty({(int64_t)bytes}, at::kByte, d) : at::Tensor();
   }
 };
 
@@ -582,8 +578,8 @@ PyObject *grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
     count(n, 4);
     const ListArg g(o[0]);
     const int kind = norm_kind(o[1]);
-    const at::Tensor norm = norm_out(o[2], g.l->dev);
     const Stream s(o[3], g.l->dev);
+    const at::Tensor norm = norm_out(o[2], g.l->dev);
     const int64_t c = (int64_t)g.l->ptr.size();
     const at::Tensor ws = s.scratch(snack_grad_norm_workspace(c), g.l->dev);
     check(snack_grad_norm(c, const_cast<const void *const *>(g.l->ptr.data()), g.l->size.data(), g.l->type.data(),
@@ -606,8 +602,8 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
       if (out->l->size != g.l->size) value_error("out must hold as many elements as grads, tensor by tensor");
       if (out->l->dev != g.l->dev) value_error("all tensors must be on one device");
     }
-    const at::Tensor norm = norm_out(o[5], g.l->dev);
     const Stream s(o[6], g.l->dev);
+    const at::Tensor norm = norm_out(o[5], g.l->dev);
     const int64_t c = (int64_t)g.l->ptr.size();
     const at::Tensor ws = s.scratch(snack_grad_norm_workspace(c), g.l->dev);
     check(snack_clip_grad_norm(c, const_cast<const void *const *>(g.l->ptr.data()),

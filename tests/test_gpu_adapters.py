@@ -224,6 +224,26 @@ def test_same_bits_every_time_and_on_another_stream():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [40, 300])
+def test_fresh_dx_on_a_given_stream(T):
+    """What the call allocates and clears is in the order of the stream it is
+    given, not of the current one, which is kept busy here."""
+    import coo_spmm_sparse_gb300 as sn
+    c = make([0, 9, T], [1, 0], 2, 256, 192, 8, F32, seed=7)
+    args = (c["A"], c["B"], c["offsets"], c["which"], c["scale"])
+    want = dense_ref.adapter(c["X"], c["Y"], *args, dY=c["dY"])
+    busy = torch.randn(8192, 8192, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        busy = busy @ busy * 1e-4
+    Y, H = sn.snack_adapter_forward(c["X"], *args, c["Y"], stream=s)
+    dX, dA, dB = sn.snack_adapter_backward(c["X"], c["dY"], *args, H, stream=s)
+    torch.cuda.synchronize()
+    for k, v in (("Y", Y), ("H", H), ("dX", dX), ("dA", dA), ("dB", dB)):
+        assert_within(k, v, *want[k])
+
+
 def test_module_beside_a_sparse_layer():
     import coo_spmm_sparse_gb300 as sn
     lin = sn.SnackLinear(256, 192, 5000, seed=1)
