@@ -18,6 +18,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 4;
+// What the norm's pass asks the L2 to keep for the pass that scales: half of
+// it.  40.6 M fp32 gradients: 84 us without, 81 / 79 / 80 us at 32 / 64 / 90
+// MB; 400 M bf16 into fp32 513 -> 504 us.
 constexpr int64_t kKeepBytes = int64_t(64) << 20;
 constexpr int kMostTable = 1024;  // tensors of one launch: 30 KB of the 32 KB that parameters may take
 

@@ -64,13 +64,6 @@ struct Columns {
   __device__ __forceinline__ bool in(int j) const { return ok[j / U]; }
 };
 
-// C elements of an array (0 beyond the row).
-template <typename T, typename CO>
-__device__ __forceinline__ void load_plain(const T *row, const CO &co, float (&v)[C]) {
-#pragma unroll
-  for (int j = 0; j < C; ++j) v[j] = co.in(j) ? to_float(row[co.at(j)]) : 0.f;
-}
-
 // Parameters of the thread's columns (`other` where there is no vector, 0
 // beyond the row: what such a column adds to any sum is 0).
 template <typename CO>

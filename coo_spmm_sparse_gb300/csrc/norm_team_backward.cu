@@ -336,8 +336,9 @@ TeamPlan team_backward(const NormArgs &n) {
           rows16(g.dh, g.dh_stride, a.branch_type) && aligned_to(g.dx, 16) && aligned_to(g.dy, 16) &&
           (!full || aligned_to(g.dgate, 16));
   const int64_t sms = device_sms(), fit = kTeamThreads / p.threads;
+  const int64_t group = a.gate_kind == SNACK_GATE_SEQUENCE ? a.group_rows : a.rows;  // rows that a block's teams share
   const int64_t teams = std::max<int64_t>(1, std::min<int64_t>((a.rows + 1) / 2, std::max<int64_t>(1, sms * fit / p.cluster)));
-  if (p.cluster == 1) p.per_block = (int)std::max<int64_t>(1, std::min<int64_t>(fit, teams / sms));
+  if (p.cluster == 1) p.per_block = (int)std::max<int64_t>(1, std::min(std::min(fit, teams / sms), group));
   team_ring(&p, a, 2, full ? 3 : 2);
   p.teams = (teams + p.per_block - 1) / p.per_block;
   return p;
