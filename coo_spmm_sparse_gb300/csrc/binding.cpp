@@ -499,11 +499,14 @@ struct List {
   std::vector<int64_t> size;
   std::vector<int32_t> type;
   c10::Device dev{c10::kCUDA, -1};
+  // What holds the tensors: nobody else may (those of a generator), and their
+  // memory must not be handed out before the call's work is in the stream.
+  std::unique_ptr<PyObject, void (*)(PyObject *)> hold{nullptr, [](PyObject *p) { Py_DECREF(p); }};
 
   explicit List(PyObject *seq) {
     PyObject *fast = PySequence_Fast(seq, "a list of tensors, or a SnackTensorList");
     if (!fast) throw Raised{};
-    std::unique_ptr<PyObject, void (*)(PyObject *)> hold(fast, [](PyObject *p) { Py_DECREF(p); });
+    hold.reset(fast);
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
     PyObject **items = PySequence_Fast_ITEMS(fast);
     ptr.reserve(n);

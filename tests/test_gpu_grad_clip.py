@@ -194,3 +194,20 @@ def test_refusals():
     with pytest.raises(sn.SnackError) as e:
         sn.snack_clip_grad_norm(ts, 1.0, eps=-1.0)
     assert e.value.status == 1
+
+
+def test_tensors_that_only_the_call_holds():
+    """A generator's tensors live until the call has launched its work: their
+    memory is not handed out for the call's own scratch or result."""
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([1000 + 64 * i for i in range(40)], [F32], 8)
+    want = norm64([t * 3 for t in ts], 2.0)
+    for _ in range(3):
+        got = float(sn.snack_grad_norm(t * 3 for t in ts))
+        assert abs(got - want) <= 1e-5 * want
+        out = [torch.empty_like(t) for t in ts]
+        got = float(sn.snack_clip_grad_norm((t * 3 for t in ts), 0.5 * want, out=iter(out)))
+        assert abs(got - want) <= 1e-5 * want
+        for t, o in zip(ts, out):
+            v = t.double() * 3 * 0.5 * want / (want + 1e-6)
+            assert_within("clipped", o, v, 2 * v.abs())
