@@ -494,6 +494,7 @@ PyObject *adapter_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
 
 // ------------------------------------------------------------------ gradient norm
 
+// Addresses, sizes and types of a list's tensors.
 struct List {
   std::vector<void *> ptr;
   std::vector<int64_t> size;
@@ -508,7 +509,7 @@ struct List {
     if (!fast) throw Raised{};
     hold.reset(fast);
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
-    PyObject **items = PySequence_Fast_ITEMS(fast);
+    PyObject *const *items = PySequence_Fast_ITEMS(fast);
     ptr.reserve(n);
     size.reserve(n);
     type.reserve(n);
@@ -526,6 +527,20 @@ struct List {
       type.push_back(k);
     }
     if (n == 0) dev = c10::Device(c10::kCUDA, c10::cuda::current_device());
+  }
+
+  // Whether the tensors lie where they were found: `.data = `, set_(),
+  // resize_() and Module.to() give a tensor other memory, type or size.
+  bool current() const {
+    PyObject *const *items = PySequence_Fast_ITEMS(hold.get());
+    const size_t n = ptr.size();
+    for (size_t i = 0; i < n; ++i) {
+      const c10::TensorImpl *t = THPVariable_Unpack(items[i]).unsafeGetTensorImpl();
+      if (t->data() != ptr[i] || t->numel() != size[i] || !t->is_contiguous() ||
+          type_code(c10::typeMetaToScalarType(t->dtype())) != type[i])
+        return false;
+    }
+    return true;
   }
 };
 
@@ -549,7 +564,11 @@ struct ListArg {
   const List *l;
   explicit ListArg(PyObject *o) {
     if (PyCapsule_IsValid(o, kListName)) {
-      l = static_cast<const List *>(PyCapsule_GetPointer(o, kListName));
+      // a kept list means its tensors, wherever they lie by now: if one has
+      // moved all are checked again, and the memory of before is not touched
+      List *kept = static_cast<List *>(PyCapsule_GetPointer(o, kListName));
+      if (!kept->current()) *kept = List(kept->hold.get());
+      l = kept;
     } else {
       own = std::make_unique<List>(o);
       l = own.get();

@@ -387,12 +387,13 @@ cudaError_t run(const Request &q, bool clip) {
   for (int64_t i = 0; i < q.count; ++i) total += q.sizes[i];
   const int chunk = chunk_length(total);
   static thread_local TensorTable<K> t;
-  int parts = 0;
+  int parts = 0, launches = 0;
   cudaError_t e;
   int64_t next = 0;
   while (next < q.count) {
     next = fill(t, q, next, chunk);
     if (t.count == 0) break;
+    ++launches;
     const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
     e = launch_kernel(norm_partials<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, q.partial + parts);
     if (e != cudaSuccess) return e;
@@ -401,16 +402,19 @@ cudaError_t run(const Request &q, bool clip) {
   if (!clip || parts == 0)
     return launch_kernel(norm_finish<MAX>, dim3(1), kThreads, 0, true, q.s, (const float *)q.partial, parts,
                          q.norm);
+  // the table of a list that one launch took whole is still there
+  const bool one = launches == 1 && t.count > 0;
   bool first = true;
-  for (next = 0; next < q.count;) {
-    next = fill(t, q, next, chunk);
+  next = 0;
+  do {
+    if (!one) next = fill(t, q, next, chunk);
     if (t.count == 0) break;
     const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
     e = launch_kernel(scale_tensors<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, (const float *)q.partial,
                       parts, q.max_norm, q.eps, first ? q.norm : nullptr);
     if (e != cudaSuccess) return e;
     first = false;
-  }
+  } while (!one && next < q.count);
   return cudaSuccess;
 }
 

@@ -3,11 +3,13 @@
     norm = snack_grad_norm(grads)                       # sqrt of the sum of all squares
     norm = snack_clip_grad_norm(grads, max_norm)        # and grads *= min(1, max_norm / (norm + eps))
 
-``grads`` is a list of CUDA tensors (float32, bfloat16, float16, mixed) or a
-``SnackTensorList`` of them.  A list is checked on every call; a
-``SnackTensorList`` was checked when it was made: keep one where the
-gradients stay in place from step to step (``zero_grad(set_to_none=False)``,
-a flat buffer, a captured graph).
+``grads`` is a list of contiguous CUDA tensors (float32, bfloat16, float16,
+mixed) or a ``SnackTensorList`` of them.  A list is checked on every call; a
+``SnackTensorList`` was checked when it was made, and a call looks only at
+whether its tensors are where they were: keep one where the gradients stay in
+place from step to step (``zero_grad(set_to_none=False)``, a flat buffer).
+A captured graph reads and writes the memory that the tensors had when it was
+captured.
 """
 
 from __future__ import annotations
@@ -18,13 +20,14 @@ from . import _dense, _raw_stream
 
 
 class SnackTensorList:
-    """A list of CUDA tensors, checked once.  It holds the tensors, so their
-    memory stays theirs; what they contain may change at any time."""
+    """A list of CUDA tensors, checked once.  It holds the tensors; what they
+    contain may change at any time, and a tensor that was given other memory,
+    another type or size is checked again by the next call."""
 
     __slots__ = ("tensors", "handle")
 
     def __init__(self, tensors):
-        self.tensors = list(tensors)
+        self.tensors = tuple(tensors)
         self.handle = _dense.tensor_list(self.tensors)
 
     def __len__(self):

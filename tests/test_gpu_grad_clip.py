@@ -211,3 +211,48 @@ def test_tensors_that_only_the_call_holds():
         for t, o in zip(ts, out):
             v = t.double() * 3 * 0.5 * want / (want + 1e-6)
             assert_within("clipped", o, v, 2 * v.abs())
+
+
+def test_kept_list_follows_its_tensors():
+    """A kept list means its tensors, not the memory that they had when it
+    was made: new storage, type or size is seen by the next call."""
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([4096, 70_001, 5], [F32], 9)
+    kept = sn.snack_tensor_list(ts)
+    old = [t.clone() for t in ts]
+    held = ts[1].data  # the memory of before stays somebody else's
+    ts[0].data = torch.full((4096,), 2.0, device="cuda")        # other memory
+    ts[1].data = (ts[1].data * 0.5).bfloat16()                  # another type
+    with torch.no_grad():
+        ts[2].set_(torch.full((9,), 3.0, device="cuda"))        # another size
+    want = norm64(ts, 2.0)
+    assert abs(float(sn.snack_grad_norm(kept)) - want) <= 1e-5 * want
+    before = [t.clone() for t in ts]
+    sn.snack_clip_grad_norm(kept, 0.25 * want)
+    for t, b in zip(ts, before):
+        v = b.double() * 0.25 * want / (want + 1e-6)
+        assert_within("clipped", t, v, 2 * v.abs())
+    assert torch.equal(held, old[1])
+    out = sn.snack_tensor_list([torch.empty_like(t) for t in ts])
+    sn.snack_clip_grad_norm(kept, 1.0, out=out)
+    ts[0].data = torch.ones(7, device="cuda")
+    with pytest.raises(ValueError, match="as many elements"):
+        sn.snack_clip_grad_norm(kept, 1.0, out=out)
+    ts[0].data = torch.ones(4, 6, device="cuda").t()
+    with pytest.raises(ValueError, match="contiguous"):
+        sn.snack_grad_norm(kept)
+    ts[0].data = torch.ones(6, device="cuda", dtype=torch.float64)
+    with pytest.raises(TypeError):
+        sn.snack_grad_norm(kept)
+
+
+def test_empty_tensors_after_a_full_table():
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([40] * 1024 + [0] * 1030 + [3], [F32], 12)
+    for gs in (ts, ts[:-1]):
+        want = norm64(gs, 2.0)
+        before = [t.clone() for t in gs]
+        assert abs(float(sn.snack_clip_grad_norm(gs, 0.5 * want)) - want) <= 1e-5 * want
+        for t, b in zip(gs, before):
+            v = b.double() * 0.5 * want / (want + 1e-6)
+            assert_within("clipped", t, v, 2 * v.abs())
