@@ -325,6 +325,8 @@ PyObject *norm_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const auto put = [&](const char *name, const at::Tensor *like, at::ScalarType type) -> void * {
       if (!like) return nullptr;
       at::Tensor t = empty(like->sizes(), type, m.dev.dev);
+      // without rows every sum is zero, and the C call writes no gate of a group that has none
+      if (m.a.rows == 0) t.zero_();
       PyObject *w = wrap(t);
       const int bad = w ? PyDict_SetItemString(out, name, w) : -1;
       Py_XDECREF(w);

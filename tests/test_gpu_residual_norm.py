@@ -310,3 +310,19 @@ def test_refusals():
         sn.snack_residual_norm_backward(dr, dh, x, y, stats[:1])
     with pytest.raises(ValueError):
         sn.snack_residual_norm_backward(dr, dh, x, y, stats, next_norm=False)
+
+
+@pytest.mark.parametrize("stream,branch", [(F32, F32), (F32, BF16)])
+def test_gate_of_sequences_without_rows(stream, branch):
+    """Sequences of no rows: their gates have no terms, so their gradient is zero."""
+    import coo_spmm_sparse_gb300 as sn
+    x, y, o, dr, dh = make((2, 4, 64), "layer", True, "sequence", stream, branch, seed=13)
+    x, y, dr, dh = (t[:, :0] for t in (x, y, dr, dh))
+    _, _, stats = sn.snack_residual_norm_forward(x, y, **o)
+    for n in (64, 128):  # what the allocator hands out next holds no zeros
+        junk = [torch.full((n,), float("nan"), device="cuda") for _ in range(16)]
+        del junk
+    g = sn.snack_residual_norm_backward(dr, dh, x, y, stats, **o)
+    assert torch.equal(g["dgate"], torch.zeros(2, 1, 64, dtype=branch, device="cuda"))
+    for k in ("dpost_weight", "dpost_bias", "dnext_weight", "dnext_bias"):
+        assert torch.equal(g[k], torch.zeros(64, device="cuda")), k
