@@ -354,7 +354,11 @@ cudaError_t launch_team_backward(const NormArgs &n, const TeamPlan &p, cudaStrea
   const int64_t teams = std::min<int64_t>(p.teams, n.slabs);
   if (next) q.next_parts = n.parts;
   if (post) q.post_parts = n.parts + teams * 2 * a.width;
-  const Form form = !plain_options(a) || !g.dr || !g.dh || !g.dx || !g.dy ? kAny : (a.post_norm ? kFastPost : kFast);
+  // an rms norm's forms of their own keep no sums for biases
+  const bool dbias = a.norm_kind == SNACK_NORM_RMS && (g.dnext_bias || g.dpost_bias);
+  const Form form = !plain_options(a) || dbias || !g.dr || !g.dh || !g.dx || !g.dy
+                        ? kAny
+                        : (a.post_norm ? kFastPost : kFast);
   const auto main = [&]() -> cudaError_t {
 #define SNACK_CALL(TS, TB) return launch<TS, TB>(p, teams, q, form, s);
     SNACK_NORM_TYPES(SNACK_CALL)

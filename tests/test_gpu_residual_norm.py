@@ -326,3 +326,32 @@ def test_gate_of_sequences_without_rows(stream, branch):
     assert torch.equal(g["dgate"], torch.zeros(2, 1, 64, dtype=branch, device="cuda"))
     for k in ("dpost_weight", "dpost_bias", "dnext_weight", "dnext_bias"):
         assert torch.equal(g[k], torch.zeros(64, device="cuda")), k
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("gate", [None, "channel", "token", "sequence", "full"])
+@pytest.mark.parametrize("d", [256, 250, 33000])
+def test_gradients_of_biases_that_are_not_there(kind, post, gate, d):
+    """The C call writes every gradient it is asked for: that of a bias left
+    out (NULL: zero) is the same sum as that of a bias of zeros."""
+    import dense_abi as abi
+    x, y, o, dr, dh = make((3, 5, d), kind, post, gate, F32, F32, seed=14)
+    zeros = torch.zeros(d, device="cuda")
+    o["next_bias"] = zeros
+    if post:
+        o["post_bias"] = zeros
+    want = dense_ref.residual_norm(x, y, dr=dr, dh=dh, **o)
+    rows = [t.reshape(15, d) for t in (x, y, dr, dh)]
+    stats, r, h = torch.empty(15, 4, device="cuda"), torch.empty_like(rows[0]), torch.empty_like(rows[0])
+    opts = {k: v for k, v in o.items() if k not in ("next_bias", "post_bias")}
+    a = abi.norm_args(*rows[:2], stats, gate_kind=gate, group_rows=5 if gate == "sequence" else 0,
+                      **opts)
+    assert abi.norm_forward(a, r, h) == 0
+    names = ["dnext_weight", "dnext_bias"] + (["dpost_weight", "dpost_bias"] if post else [])
+    got = {k: torch.full((d,), float("nan"), device="cuda") for k in names}
+    got.update(dx=torch.empty_like(r), dy=torch.empty_like(r))
+    assert abi.norm_backward(a, dr=rows[2], dh=rows[3], **got) == 0
+    torch.cuda.synchronize()
+    for k, v in got.items():
+        assert_within(k, v.reshape(want[k][0].shape), *want[k])
