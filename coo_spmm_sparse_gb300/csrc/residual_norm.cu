@@ -319,6 +319,8 @@ const char *bad_args(const snack_norm_args *a) {
   if (a->gate_kind == SNACK_GATE_SEQUENCE && (a->group_rows < 1 || a->rows % a->group_rows != 0))
     return "group_rows must divide rows";
   if (!(a->eps >= 0.f)) return "eps must be >= 0";
+  if (!a->post_norm && (a->post_weight || a->post_bias)) return "post_weight or post_bias without post_norm";
+  if (!a->next_norm && (a->next_weight || a->next_bias)) return "next_weight or next_bias without next_norm";
   if (a->rows == 0) return nullptr;
   if (!a->x) return "x is NULL";
   if ((a->gate_kind != SNACK_GATE_NONE) && (!a->gate || !a->y)) return "a gate needs gate and y";
@@ -332,6 +334,15 @@ const char *bad_args(const snack_norm_args *a) {
       !aligned_to(a->next_bias, tp))
     return "a pointer is not aligned to its elements";
   if (a->stats && !aligned_to(a->stats, 16)) return "stats must be 16-byte aligned";
+  return nullptr;
+}
+
+// Gradients of what the call does not have.
+const char *bad_grads(const snack_norm_args &a, const snack_norm_grads &g) {
+  if (!a.post_norm && (g.dpost_weight || g.dpost_bias)) return "dpost_weight or dpost_bias without post_norm";
+  if (!a.next_norm && (g.dh || g.dnext_weight || g.dnext_bias)) return "dh, dnext_weight or dnext_bias without next_norm";
+  if (a.gate_kind == SNACK_GATE_NONE && g.dgate) return "dgate without a gate";
+  if (a.rows > 0 && !a.y && g.dy) return "dy without y";
   return nullptr;
 }
 
@@ -409,6 +420,7 @@ extern "C" snack_status snack_residual_norm_backward(const snack_norm_args *args
   using namespace snack;
   if (const char *bad = bad_args(args)) return refuse(SNACK_ERR_INVALID_ARG, bad);
   if (!grads) return refuse(SNACK_ERR_INVALID_ARG, "grads is NULL");
+  if (const char *bad = bad_grads(*args, *grads)) return refuse(SNACK_ERR_INVALID_ARG, bad);
   const snack_norm_args &a = *args;
   const snack_norm_grads &g = *grads;
   const int64_t ts = type_bytes(a.stream_type), tb = type_bytes(a.branch_type), tp = type_bytes(a.param_type);

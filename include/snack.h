@@ -338,6 +338,8 @@ typedef enum {
  * by sqrt(variance + eps) (biased variance), SNACK_NORM_RMS divides by
  * sqrt(mean of squares + eps).  N sees r before r is rounded to stream_type.
  * y == NULL leaves the branch out (r = residual_scale * x): a plain norm.
+ * A weight or bias without its norm is refused, and so is a gradient of what
+ * the call does not have (a norm, a gate, y).
  *
  * x, r, dr and dx are of stream_type; y, h, gate, dy, dh and dgate of
  * branch_type; weights, biases and their gradients of param_type.

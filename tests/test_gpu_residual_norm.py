@@ -355,3 +355,30 @@ def test_gradients_of_biases_that_are_not_there(kind, post, gate, d):
     torch.cuda.synchronize()
     for k, v in got.items():
         assert_within(k, v.reshape(want[k][0].shape), *want[k])
+
+
+@pytest.mark.parametrize("d", [256, 33000])
+def test_what_belongs_to_no_option_is_refused(d):
+    """Weights, biases and gradients of a norm, gate or branch that is not
+    there: refused by the C calls at every width."""
+    import dense_abi as abi
+    x, y = torch.randn(2, 3, d, device="cuda")
+    w, stats = torch.ones(d, device="cuda"), torch.empty(3, 4, device="cuda")
+    r, h, dx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    for name in ("post_weight", "post_bias"):
+        assert abi.norm_forward(abi.norm_args(x, y, stats, **{name: w}), r, h) == abi.INVALID_ARG
+        assert name[5:] in abi.lib().snack_last_error(None).decode()
+    for name in ("next_weight", "next_bias"):
+        a = abi.norm_args(x, y, stats, next_norm=0, **{name: w})
+        assert abi.norm_forward(a, r, None) == abi.INVALID_ARG
+    a = abi.norm_args(x, y, stats)
+    assert abi.norm_forward(a, r, h) == 0
+    for name in ("dpost_weight", "dpost_bias", "dgate"):
+        assert abi.norm_backward(a, dr=x, dh=y, dx=dx, **{name: w}) == abi.INVALID_ARG
+    a.next_norm = 0
+    for grads in (dict(dnext_weight=w), dict(dnext_bias=w), dict(dh=y)):
+        assert abi.norm_backward(a, dr=x, dx=dx, **grads) == abi.INVALID_ARG
+    a = abi.norm_args(x, None, stats)
+    assert abi.norm_forward(a, r, h) == 0
+    assert abi.norm_backward(a, dr=x, dh=y, dx=dx, dy=r) == abi.INVALID_ARG
+    assert abi.norm_backward(a, dr=x, dh=y, dx=dx) == 0
