@@ -121,13 +121,15 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Raises the kernel's limit of dynamic shared memory where it may be above
-// the default (48 KB with the kernel's static part, at most 8 KB here).
+// Lets the kernel be launched with that much dynamic shared memory, where it
+// may be above the default (48 KB with the kernel's static part, at most 8 KB
+// here).  The limit belongs to the kernel, not to the call: it is raised once,
+// to all that a block can have, because a limit set to this call's size could
+// be lowered by another host thread before the launch.
+cudaError_t raise_smem_limit(const void *kern);  // dense_ops.cu
 template <typename K>
 inline cudaError_t allow_smem(K kern, size_t bytes) {
-  return bytes <= 40 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return bytes <= 40 * 1024 ? cudaSuccess : raise_smem_limit(reinterpret_cast<const void *>(kern));
 }
 
 template <typename... KArgs, typename... Args>

@@ -382,3 +382,34 @@ def test_what_belongs_to_no_option_is_refused(d):
     assert abi.norm_forward(a, r, h) == 0
     assert abi.norm_backward(a, dr=x, dh=y, dx=dx, dy=r) == abi.INVALID_ARG
     assert abi.norm_backward(a, dr=x, dh=y, dx=dx) == 0
+
+
+def test_calls_of_two_host_threads():
+    """The C calls run from any host thread: two threads at widths whose
+    kernels take unlike amounts of shared memory do not disturb each other."""
+    import threading
+    import dense_abi as abi
+    widths, failed = (4096, 2048), []
+    start = threading.Barrier(2)
+
+    def work(d):
+        s = torch.cuda.Stream()
+        x, y, stats = torch.randn(2, d, device="cuda"), torch.randn(2, d, device="cuda"), \
+            torch.empty(2, 4, device="cuda")
+        r, h = torch.empty_like(x), torch.empty_like(x)
+        torch.cuda.synchronize()
+        a = abi.norm_args(x, y, stats)
+        start.wait()
+        for _ in range(20000):
+            st = abi.norm_forward(a, r, h, s.cuda_stream)
+            if st != 0:
+                failed.append((d, st, abi.lib().snack_last_error(None)))
+                return
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
