@@ -17,6 +17,7 @@ import math
 import torch
 
 from . import _dense, _raw_stream
+from ._autograd import first_derivative
 
 
 def snack_adapter_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -53,6 +54,7 @@ class _AdapterFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @first_derivative
     def backward(ctx, dY):
         X, A, B, offsets, adapter, H = ctx.saved_tensors
         need = ctx.needs_input_grad

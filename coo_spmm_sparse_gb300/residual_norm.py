@@ -15,6 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import _dense, _raw_stream
+from ._autograd import first_derivative
 
 _KINDS = {"layer": 0, "rms": 1}
 
@@ -68,6 +69,7 @@ class _ResidualNormFunction(torch.autograd.Function):
         return (r.view_as(r) if r is x else r), h
 
     @staticmethod
+    @first_derivative
     def backward(ctx, dr, dh):
         x, y, gate, pw, pb, nw, nb, stats = ctx.saved_tensors
         if dr is None and dh is None:

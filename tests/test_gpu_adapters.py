@@ -308,3 +308,21 @@ def test_refusals():
         sn.snack_adapter_backward(sq["X"], sq["dY"], sq["A"], sq["B"], sq["offsets"], sq["which"],
                                   1.0, H, dX=sq["dY"])
     assert e.value.status == 1
+
+
+def test_second_derivatives_raise():
+    """The backward's results carry no graph: differentiating them again
+    raises, whatever the incoming gradient, where a constant would be wrong."""
+    import coo_spmm_sparse_gb300 as sn
+    ad = sn.SnackAdapters(2, 64, 48, 4, seed=3)
+    with torch.no_grad():
+        ad.B.normal_(0, 0.3)
+    off = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    which = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    for loss in (lambda y: y.sum(), lambda y: y.square().sum()):
+        x = torch.randn(9, 64, device="cuda", requires_grad=True)
+        for t in (x, ad.A, ad.B):
+            y = ad(x, torch.zeros(9, 48, device="cuda"), off, which)
+            g, = torch.autograd.grad(loss(y), t, create_graph=True)
+            with pytest.raises(RuntimeError, match="second derivative"):
+                (y.sum() + g.square().sum()).backward()

@@ -413,3 +413,18 @@ def test_calls_of_two_host_threads():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+def test_second_derivatives_raise():
+    """The backward's results carry no graph: differentiating them again
+    raises, whatever the incoming gradient, where a constant would be wrong."""
+    import coo_spmm_sparse_gb300 as sn
+    for loss in (lambda r, h: h.sum(), lambda r, h: (r * h).sum()):
+        x = torch.randn(3, 64, device="cuda", requires_grad=True)
+        y = torch.randn(3, 64, device="cuda", requires_grad=True)
+        w = torch.ones(64, device="cuda", requires_grad=True)
+        for i, t in enumerate((x, y, w)):
+            r, h = sn.snack_residual_norm(x, y, next_weight=w)
+            g, = torch.autograd.grad(loss(r, h), t, create_graph=True)
+            with pytest.raises(RuntimeError, match="second derivative"):
+                (h.sum() + g.square().sum()).backward()
