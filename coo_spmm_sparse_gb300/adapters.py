@@ -47,6 +47,8 @@ class _AdapterFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, Y, A, B, offsets, adapter, scale):
+        if ctx.needs_input_grad[6]:
+            raise ValueError("scale has no gradient here: detach it, or scale B")
         _, H = snack_adapter_forward(X, A, B, offsets, adapter, scale, Y)
         ctx.mark_dirty(Y)
         ctx.scale = scale
@@ -72,7 +74,8 @@ class SnackAdapters(torch.nn.Module):
     B [adapters][out][rank] zero, so that a new adapter changes nothing.
 
     ``forward(x, y, offsets, adapter)`` adds their part to the projection's
-    output y (in place) and returns it.  ``scale`` is alpha / rank."""
+    output y (in place) and returns it.  ``scale`` is alpha / rank; it may be
+    set to another number or to float32 [adapters] that wants no gradient."""
 
     def __init__(self, adapters: int, in_features: int, out_features: int, rank: int,
                  alpha: float | None = None, seed: int = 0, dtype=torch.float32, device=None):

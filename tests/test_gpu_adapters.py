@@ -326,3 +326,16 @@ def test_second_derivatives_raise():
             g, = torch.autograd.grad(loss(y), t, create_graph=True)
             with pytest.raises(RuntimeError, match="second derivative"):
                 (y.sum() + g.square().sum()).backward()
+
+
+def test_a_scale_that_wants_a_gradient_is_refused():
+    import coo_spmm_sparse_gb300 as sn
+    ad = sn.SnackAdapters(2, 64, 48, 4, seed=3)
+    off = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    which = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    x = torch.randn(9, 64, device="cuda", requires_grad=True)
+    ad.scale = torch.ones(2, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="scale"):
+        ad(x, torch.zeros(9, 48, device="cuda"), off, which)
+    ad.scale = torch.ones(2, device="cuda")
+    ad(x, torch.zeros(9, 48, device="cuda"), off, which).sum().backward()
