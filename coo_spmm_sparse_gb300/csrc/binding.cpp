@@ -84,6 +84,14 @@ const at::Tensor *dense_or_none(PyObject *o, const char *name) {
 
 const void *addr(const at::Tensor *t) { return t ? t->data_ptr() : nullptr; }
 
+// Tells autograd that the call writes t, a tensor of the caller's: what kept
+// it for a backward pass then raises rather than use the new values.
+// (Inference tensors have no version.)
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *o) { written(THPVariable_Unpack(o)); }
+
 // (rows, row stride) of t seen as [rows][last dimension].
 struct Rows {
   int64_t n, step;
@@ -458,6 +466,8 @@ PyObject *adapter_forward(PyObject *, PyObject *const *o, Py_ssize_t n) {
     }
     const at::Tensor ws = s.scratch(snack_adapter_forward_workspace(&m.a), m.dev.dev);
     check(snack_adapter_forward(&m.a, Y.data_ptr(), ys, H, scratch_addr(ws), s.raw));
+    written(Y);
+    if (!fresh.defined()) written(o[7]);
     return Py_BuildValue("(NN)", same(o[6]), fresh.defined() ? wrap(fresh) : same(o[7]));
   });
 }
@@ -489,6 +499,7 @@ PyObject *adapter_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const at::Tensor ws = s.scratch(snack_adapter_backward_workspace(&m.a), m.dev.dev);
     check(snack_adapter_backward(&m.a, dY.data_ptr(), dys, H, dX, dxs, need_dw ? dA.data_ptr() : nullptr,
                                  need_dw ? dB.data_ptr() : nullptr, scratch_addr(ws), s.raw));
+    if (need_dx && !fresh.defined()) written(o[8]);
     return Py_BuildValue("(NNN)", !need_dx ? same(Py_None) : (fresh.defined() ? wrap(fresh) : same(o[8])),
                          need_dw ? wrap(dA) : same(Py_None), need_dw ? wrap(dB) : same(Py_None));
   });
@@ -578,6 +589,12 @@ struct ListArg {
     if (l->dev.index() != c10::cuda::current_device())
       value_error("cuda:" + std::to_string(l->dev.index()) + " is not the current CUDA device");
   }
+  // (Not of a kept list: 96 tensors of one add 1 us to a call of 9.)
+  void written_all() const {
+    if (!own) return;
+    PyObject *const *items = PySequence_Fast_ITEMS(own->hold.get());
+    for (size_t i = 0; i < own->ptr.size(); ++i) written(items[i]);
+  }
 };
 
 int norm_kind(PyObject *o) {
@@ -608,6 +625,7 @@ PyObject *grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const at::Tensor ws = s.scratch(snack_grad_norm_workspace(c), g.l->dev);
     check(snack_grad_norm(c, const_cast<const void *const *>(g.l->ptr.data()), g.l->size.data(), g.l->type.data(),
                           kind, static_cast<float *>(norm.data_ptr()), scratch_addr(ws), s.raw));
+    if (o[2] != Py_None) written(o[2]);
     return o[2] == Py_None ? wrap(norm) : same(o[2]);
   });
 }
@@ -634,6 +652,8 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
                                out ? out->l->ptr.data() : nullptr, g.l->size.data(), g.l->type.data(),
                                out ? out->l->type.data() : nullptr, kind, (float)max_norm, (float)number(o[4]),
                                static_cast<float *>(norm.data_ptr()), scratch_addr(ws), s.raw));
+    (out ? *out : g).written_all();
+    if (o[5] != Py_None) written(o[5]);
     return o[5] == Py_None ? wrap(norm) : same(o[5]);
   });
 }

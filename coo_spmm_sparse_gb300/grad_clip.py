@@ -22,7 +22,9 @@ from . import _dense, _raw_stream
 class SnackTensorList:
     """A list of CUDA tensors, checked once.  It holds the tensors; what they
     contain may change at any time, and a tensor that was given other memory,
-    another type or size is checked again by the next call."""
+    another type or size is checked again by the next call.  A call that writes
+    them does not move their autograd versions, as one on a list does: keep no
+    list of tensors that a graph has saved."""
 
     __slots__ = ("tensors", "handle")
 

@@ -339,3 +339,29 @@ def test_a_scale_that_wants_a_gradient_is_refused():
         ad(x, torch.zeros(9, 48, device="cuda"), off, which)
     ad.scale = torch.ones(2, device="cuda")
     ad(x, torch.zeros(9, 48, device="cuda"), off, which).sum().backward()
+
+
+def test_writes_in_place_are_seen_by_autograd():
+    """A tensor that autograd keeps for a backward pass and a call then
+    changes: the backward pass raises, it does not use the changed values."""
+    import coo_spmm_sparse_gb300 as sn
+    c = make([0, 9, 40], [1, 0], 2, 64, 48, 8, F32, seed=9)
+    args = (c["A"], c["B"], c["offsets"], c["which"], c["scale"])
+    w = torch.ones(48, device="cuda", requires_grad=True)
+    z = (c["Y"] * w).sum()
+    _, H = sn.snack_adapter_forward(c["X"], *args, c["Y"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    z = (c["dX"] * w).sum()
+    sn.snack_adapter_backward(c["X"], c["dY"], *args, H, dX=c["dX"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    z = (H * w).sum()
+    sn.snack_adapter_forward(c["X"], *args, c["Y"], H=H)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+    with torch.inference_mode():  # tensors without a version
+        c = make([0, 9, 40], [1, 0], 2, 64, 48, 8, F32, seed=9)
+        check(c)

@@ -256,3 +256,24 @@ def test_empty_tensors_after_a_full_table():
         for t, b in zip(gs, before):
             v = b.double() * 0.5 * want / (want + 1e-6)
             assert_within("clipped", t, v, 2 * v.abs())
+
+
+def test_writes_in_place_are_seen_by_autograd():
+    """A tensor that autograd keeps for a backward pass and a call then
+    changes: the backward pass raises, it does not use the changed values."""
+    import coo_spmm_sparse_gb300 as sn
+    g, o = torch.randn(64, device="cuda"), torch.randn(64, device="cuda")
+    norm = torch.ones((), device="cuda")
+    kept = sn.snack_tensor_list([g])
+    for changed, call in ((g, lambda: sn.snack_clip_grad_norm([g], 1e-3)),
+                          (o, lambda: sn.snack_clip_grad_norm(kept, 1.0, out=[o])),
+                          (norm, lambda: sn.snack_grad_norm(kept, norm=norm))):
+        w = torch.ones(changed.shape, device="cuda", requires_grad=True)
+        z = (changed * w).sum()
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            z.backward()
+    with torch.inference_mode():  # tensors without a version
+        g = torch.ones(64, device="cuda")
+        sn.snack_clip_grad_norm([g], 1.0)
+        assert abs(float(g[0]) - 1 / 8) <= 1e-5
