@@ -973,7 +973,7 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
   const T *copy_from = X + (copy_ok ? c0 + (lane & 7) * E : 0);
   uint4 *ring = smem4 + warp * STAGES * NR * 32;
   bool first = true;
-  float fit = 1.f;  // float16: power of two that the chunk's H is scaled by
+  float fit = 1.f;  // float16: power of two that an adapter's H is scaled by
   __shared__ uint32_t largest;
   for (int p = 0; p < places; ++u) {
     const int4 use = q.p.used[u];
@@ -1031,16 +1031,20 @@ __device__ __forceinline__ void outer_block(const AdapterArgs &q, const OuterArg
         copies_wait<STAGES - 1>();
       else
         copies_wait<0>();
-      if (std::is_same_v<T, __half> && threadIdx.x == 0) largest = 0u;
       __syncthreads();
-      if constexpr (std::is_same_v<T, __half>) {
-        uint32_t most = 0u;
-        for (int i = threadIdx.x; i < places * 16 * RM; i += kThreads) most = max(most, finite_bits(hs[i / (16 * RM) * LD + i % (16 * RM)]));
-        atomicMax(&largest, most);
-        __syncthreads();
-        fit = half_scale(largest);
-      }
       first = false;
+    }
+    if constexpr (std::is_same_v<T, __half>) {
+      // of this adapter's tokens alone: its neighbours' may lie far above them
+      __syncthreads();  // all have read the scale of the adapter before
+      if (threadIdx.x == 0) largest = 0u;
+      __syncthreads();
+      uint32_t most = 0u;
+      for (int i = threadIdx.x; i < (end - p) * 16 * RM; i += kThreads)
+        most = max(most, finite_bits(hs[(p + i / (16 * RM)) * LD + i % (16 * RM)]));
+      atomicMax(&largest, most);
+      __syncthreads();
+      fit = half_scale(largest);
     }
     for (int step = 0; step < steps; ++step) {
       uint4 x[NR];

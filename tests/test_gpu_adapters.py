@@ -365,3 +365,21 @@ def test_writes_in_place_are_seen_by_autograd():
     with torch.inference_mode():  # tensors without a version
         c = make([0, 9, 40], [1, 0], 2, 64, 48, 8, F32, seed=9)
         check(c)
+
+
+@pytest.mark.parametrize("which", [[0, 1], [1, 0]])
+def test_float16_adapters_of_unlike_magnitudes(which):
+    """Two adapters whose H and dH lie 2^36 apart, side by side in one call:
+    each one's gradients are those that it has alone."""
+    c = make([0, 70, 150], which, 2, 192, 160, 8, F16, seed=10)
+    small = slice(0, 70) if which[0] == 1 else slice(70, 150)
+    large = slice(70, 150) if which[0] == 1 else slice(0, 70)
+    for k, f in (("X", 2.0 ** -12), ("dY", 2.0 ** 9)):  # adapter 1: H of 2^-24, dB of 2^-12
+        c[k][small] = (c[k][small].float() * f).half()
+    c["A"][1] = (c["A"][1].float() * 2.0 ** -9).half()
+    c["B"][1] = (c["B"][1].float() * 2.0 ** -9).half()
+    for k, f in (("X", 2.0 ** 9), ("dY", 2.0 ** -9)):   # adapter 0: H of 2^12
+        c[k][large] = (c[k][large].float() * f).half()
+    c["A"][0] = (c["A"][0].float() * 2.0 ** 3).half()
+    c["B"][0] = (c["B"][0].float() * 2.0 ** -6).half()
+    check(c)
