@@ -679,12 +679,16 @@ __device__ __forceinline__ void load_ranks(const T *row, int64_t j, int64_t rank
 // split in two parts, in the order in which the lanes want it.  RG: 16-rank
 // groups (1 or 2, weights copied ahead with the rows; 0: any number, weights
 // loaded when they are needed: ahead, 64 ranks measured the same in fp32 and
-// 350 us for 330 in bf16, forward and backward).
+// 350 us for 330 in bf16, forward and backward; -1: fp32 above 64 ranks, summed
+// 64 at a time in the matrix unit: 512 positive terms kept in it came out
+// 3.8e-6 off, so 4.1e-7, at 226 us for 213 of a forward of 4096 tokens, 1024
+// -> 1024; up to 64 ranks they are 4.6e-7 off as they are).
 template <typename T, int RG, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant__ AdapterArgs q,
                                                           const __grid_constant__ UpArgs d) {
   using S = UpShape<T>;
   constexpr int MT = kTile / 16, E = S::E, NT = S::NT, PER = S::PER, STAGES = S::stages(RG);
+  constexpr int STEP = S::step_bytes(RG > 0 ? RG : 0);
   constexpr bool AHEAD = ALIGNED && RG > 0;  // rows and weights both in vectors
   extern __shared__ uint4 frag[];            // [16-rank groups][MT][2 (high and low)][PER][32 lanes], then the rings
   dependency_wait();
@@ -694,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
   // column of product n's index g: the lane that ends up with columns 2t and
   // 2t + 1 of every n holds E columns in a row
   const int gcol = (g >> 1) * E + (g & 1);
-  char *ring = reinterpret_cast<char *>(frag) + S::frag_bytes(d.rank) + (size_t)warp * STAGES * S::step_bytes(RG);
+  char *ring = reinterpret_cast<char *>(frag) + S::frag_bytes(d.rank) + (size_t)warp * STAGES * STEP;
   const bool wvec = d.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(d.W) & (4 * sizeof(T) - 1)) == 0;
   const int across = (int)((d.K + S::BLOCK - 1) / S::BLOCK);  // column blocks of a tile
   const int64_t all = (int64_t)q.p.head[0] * across;
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
       if (!ALIGNED) return;
       const int64_t c0 = column(c);
       if (c < count && c0 < d.K) {
-        char *at = ring + (c % STAGES) * S::step_bytes(RG);
+        char *at = ring + (c % STAGES) * STEP;
 #pragma unroll
         for (int m = 0; m < 2 * MT; ++m)
           copy16(reinterpret_cast<uint4 *>(at) + m * 32 + lane, rows[m], c0 + t * E, d.K, ok[m]);
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
       const int64_t c0 = column(c);
       if (c0 >= d.K) break;
       uint4 y[2 * MT];
-      const char *at = ring + (c % STAGES) * S::step_bytes(RG);
+      const char *at = ring + (c % STAGES) * STEP;
       if (ALIGNED) {
         copies_wait<STAGES - 2>();
 #pragma unroll
@@ -815,8 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-#pragma unroll(RG > 0 ? RG : 1)
-      for (int k = 0; k < rg; ++k) {
+      const auto multiply = [&](int k) {
         const uint4 *from = frag + (int64_t)k * MT * 2 * PER * 32 + lane;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -854,6 +857,25 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up(const __grid_constant_
             }
           }
         }
+      };
+      if constexpr (RG < 0) {
+        float sum[MT][NT][4];
+        for (int k0 = 0; k0 < rg; k0 += 4) {
+#pragma unroll 1
+          for (int k = k0; k < min(rg, k0 + 4); ++k) multiply(k);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                sum[m][n][i] = k0 ? sum[m][n][i] + acc[m][n][i] : acc[m][n][i];
+                acc[m][n][i] = k0 + 4 < rg ? 0.f : sum[m][n][i];
+              }
+        }
+      } else {
+#pragma unroll(RG > 0 ? RG : 1)
+        for (int k = 0; k < rg; ++k) multiply(k);
       }
       fetch(c + STAGES - 1);  // into the slots that step c - 1 has read
 #pragma unroll
@@ -1634,10 +1656,12 @@ cudaError_t launch_up(const AdapterArgs &q, const UpArgs &d, cudaStream_t s) {
   const dim3 grid((unsigned)std::min<int64_t>(most, 2 * device_sms()));
   const bool wvec = d.rank % 4 == 0 && aligned_to(d.W, 4 * sizeof(T));
   const bool vec = vector_rows(d.Y, d.y_stride, d.K, q.a.type);
-  const int rg = !wvec || d.rank > 32 ? 0 : (d.rank > 16 ? 2 : 1);
-  auto k = !vec ? adapter_up<T, 0, false>
-                : (rg == 0 ? adapter_up<T, 0, true> : (rg == 1 ? adapter_up<T, 1, true> : adapter_up<T, 2, true>));
-  const size_t smem = S::smem(vec ? rg : 0, d.rank);
+  const int rg = !vec || !wvec || d.rank > 32 ? 0 : (d.rank > 16 ? 2 : 1);
+  constexpr int kHigh = kFlush<T> ? -1 : 0;  // the form above 64 ranks
+  auto k = rg == 2 ? adapter_up<T, 2, true> : adapter_up<T, 1, true>;
+  if (rg == 0) k = vec ? adapter_up<T, 0, true> : adapter_up<T, 0, false>;
+  if (d.rank > 64) k = vec ? adapter_up<T, kHigh, true> : adapter_up<T, kHigh, false>;
+  const size_t smem = S::smem(rg, d.rank);
   const cudaError_t e = allow_smem(k, smem);
   return e != cudaSuccess ? e : launch_kernel(k, grid, kThreads, smem, true, s, q, d);
 }

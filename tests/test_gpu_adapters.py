@@ -383,3 +383,35 @@ def test_float16_adapters_of_unlike_magnitudes(which):
     c["A"][0] = (c["A"][0].float() * 2.0 ** 3).half()
     c["B"][0] = (c["B"][0].float() * 2.0 ** -6).half()
     check(c)
+
+
+@pytest.mark.parametrize("rank", [64, 512])
+def test_sums_over_high_ranks(rank):
+    """Terms of one sign, where a sum that is cut off rather than rounded at
+    every step drifts: H exact (one-hot rows of X pick weights of 8 bits), all
+    of B positive.  Held to 3e-6 of the sum: 2^-21 for the split of a product,
+    2^-24 on average for each of the 24 steps of 64 summed elements in the
+    matrix unit, cut off between 0 and 2^-23 (1.4e-6, and 7e-7 for the spread of
+    24 such cuts over the outputs), 2^-25 for each of 8 sums outside it."""
+    import coo_spmm_sparse_gb300 as sn
+    T, inp, out = 200, 64, 192
+    c = make([0, T], [0], 1, inp, out, rank, F32, seed=rank)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    c["X"] = torch.zeros(T, inp, device="cuda")
+    c["X"][torch.arange(T), torch.arange(T) % inp] = 1.0
+    c["A"] = torch.randint(128, 256, c["A"].shape, generator=g, device="cuda").float()
+    c["B"] = torch.rand(c["B"].shape, generator=g, device="cuda") + 0.5
+    Y, H = sn.snack_adapter_forward(c["X"], c["A"], c["B"], c["offsets"], c["which"], 1.0,
+                                    torch.zeros(T, out, device="cuda"))
+    assert torch.equal(H, c["X"] @ c["A"][0].T)
+    want = H.double() @ c["B"][0].double().T
+    worst = ((Y.double() - want).abs() / want).max()
+    print("worst", rank, float(worst))
+    assert float(worst) <= 3e-6
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+@pytest.mark.parametrize("rank", [131, 256, 300, 512])
+@pytest.mark.parametrize("T", [60, 150])
+def test_high_ranks(dt, rank, T):
+    check(make([0, 33, 90 if T > 90 else 40, T], [1, 0, 1], 2, 96, 160, rank, dt, T=T, seed=rank))
