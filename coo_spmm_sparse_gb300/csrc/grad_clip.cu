@@ -8,6 +8,13 @@
 // into chunks of equal length that the blocks of a persistent grid take in
 // turn.  Every block leaves one partial sum; whoever needs the norm adds the
 // partials in their order, so that no atomic decides a result's bits.
+//
+// Squares leave the range of 32-bit floats long before a norm does.  A thread
+// sums its part of a chunk as it is; a sum that is too large or too small to
+// be exact is taken again of values scaled by a power of two, and such sums
+// are kept apart from the others (three accumulators, after J. L. Blue, "A
+// portable Fortran program to find the Euclidean norm of a vector", ACM TOMS
+// 4, 1978, chosen here for a thread's part instead of every element).
 #include <algorithm>
 #include <type_traits>
 
@@ -77,6 +84,28 @@ __device__ __forceinline__ float block_reduce(float v, float *red) {
   return v;
 }
 
+// Sums of squares as they are, and of values times kUp and times kDown.  A
+// thread's part of a chunk has at most 160 elements, and there are less than
+// 2^30 parts.  Kept as they are, sums of 2^-100 to 2^90: squares that are
+// subnormal are off by 2^-150 each, and all parts together stay below 2^120.
+// Scaled up, elements of 2^-149 to 2^-50 have squares of 2^-118 to 2^80; the
+// largest of a part scaled down, 2^41 to 2^128, has one of 2^-98 to 2^76.
+struct Sums {
+  float mid, low, high;
+};
+constexpr float kLeast = 0x1p-100f, kMost = 0x1p90f, kUp = 0x1p90f, kDown = 0x1p-90f;
+
+// Over the block, the same in every thread.
+template <bool MAX>
+__device__ __forceinline__ Sums block_sums(Sums v, float *red) {
+  v.mid = block_reduce<MAX>(v.mid, red);
+  if (!MAX && __syncthreads_or(v.low != 0.f || v.high != 0.f)) {
+    v.low = block_reduce<false>(v.low, red);
+    v.high = block_reduce<false>(v.high, red);
+  }
+  return v;
+}
+
 template <typename T>
 struct Vec {  // 16 bytes
   static constexpr int N = 16 / sizeof(T);
@@ -86,16 +115,22 @@ struct Vec {  // 16 bytes
                  : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
                  : "l"(p), "l"(policy));
   }
+  __device__ __forceinline__ uint32_t any() const { return raw.x | raw.y | raw.z | raw.w; }
   __device__ __forceinline__ float get(int i) const { return to_float(reinterpret_cast<const T *>(&raw)[i]); }
 };
 
 template <typename T, bool MAX>
-__device__ __forceinline__ void norm_chunk(const T *p, int n, uint64_t policy, float (&acc)[4]) {
+__device__ __forceinline__ void norm_chunk(const T *p, int n, uint64_t policy, float (&acc)[4], uint32_t &bits) {
   constexpr int V = Vec<T>::N;
   const int tid = threadIdx.x;
   // elements before the first whole vector
   const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
-  if (tid < head) take<MAX>(acc[0], to_float(p[tid]));
+  const auto one = [&](T x) {
+    const float v = to_float(x);
+    take<MAX>(acc[0], v);
+    bits |= v != 0.f;
+  };
+  if (tid < head) one(p[tid]);
   p += head;
   n -= head;
   int done = 0;
@@ -107,66 +142,129 @@ __device__ __forceinline__ void norm_chunk(const T *p, int n, uint64_t policy, f
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k].load(p + (int64_t)(i + k * kThreads) * V, policy);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) {
+        bits |= v[k].any();
 #pragma unroll
         for (int j = 0; j < V; ++j) take<MAX>(acc[k], v[k].get(j));
+      }
     }
     for (; i < nv; i += kThreads) {
       Vec<T> v;
       v.load(p + (int64_t)i * V, policy);
+      bits |= v.any();
 #pragma unroll
       for (int j = 0; j < V; ++j) take<MAX>(acc[j & 3], v.get(j));
     }
     done = nv * V;
   }
-  for (int i = done + tid; i < n; i += kThreads) take<MAX>(acc[0], to_float(p[i]));
+  for (int i = done + tid; i < n; i += kThreads) one(p[i]);
+}
+
+// The same thread's elements again, times `scale`.
+template <typename T>
+__device__ __noinline__ float norm_chunk_scaled(const T *p, int n, float scale) {
+  constexpr int V = Vec<T>::N;
+  const int tid = threadIdx.x;
+  const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
+  float s = 0.f;
+  const auto add = [&](int i) {
+    const float v = to_float(p[i]) * scale;
+    s = fmaf(v, v, s);
+  };
+  if (tid < head) add(tid);
+  const int nv = (n - head) / V;
+  for (int i = tid; i < nv; i += kThreads)
+    for (int j = 0; j < V; ++j) add(head + i * V + j);
+  for (int i = head + nv * V + tid; i < n; i += kThreads) add(i);
+  return s;
+}
+
+// One chunk's part of this thread.
+template <typename T, bool MAX>
+__device__ __forceinline__ void add_chunk(const void *src, int64_t at, int n, uint64_t policy, Sums &run) {
+  const T *p = static_cast<const T *>(src) + at;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t bits = 0;  // of all elements
+  norm_chunk<T, MAX>(p, n, policy, acc, bits);
+  if (MAX) {
+    run.mid = max_nan(max_nan(max_nan(acc[0], acc[1]), max_nan(acc[2], acc[3])), run.mid);
+    return;
+  }
+  const float v = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  if (v >= kLeast && v <= kMost)
+    run.mid += v;
+  else if (v < kLeast) {
+    if (bits & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) run.low += norm_chunk_scaled(p, n, kUp);
+  } else {
+    run.high += norm_chunk_scaled(p, n, kDown);  // infinities and NaN too
+  }
 }
 
 template <int K, bool MAX>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_partials(const __grid_constant__ TensorTable<K> t,
-                                                          float *partial) {
+                                                          float4 *partial) {
   __shared__ float red[32];
   dependency_wait();
   uint64_t keep, leave;  // in the L2, for the pass that scales
   asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(leave));
-  float run = 0.f;  // over the chunks; within one, four sums of a thread
+  Sums run = {0.f, 0.f, 0.f};  // over the chunks; within one, four sums of a thread
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const uint64_t policy = c >= t.keep_from ? keep : leave;
     const int k = tensor_of(t, (uint32_t)c);
     const int64_t at = (c - t.first[k]) * (int64_t)t.chunk_elems;
     const int64_t left = t.n[k] - at;
     const int n = left < t.chunk_elems ? (int)left : t.chunk_elems;
     if (t.stype[k] == SNACK_F32)
-      norm_chunk<float, MAX>(static_cast<const float *>(t.src[k]) + at, n, policy, acc);
+      add_chunk<float, MAX>(t.src[k], at, n, policy, run);
     else if (t.stype[k] == SNACK_BF16)
-      norm_chunk<__nv_bfloat16, MAX>(static_cast<const __nv_bfloat16 *>(t.src[k]) + at, n, policy, acc);
+      add_chunk<__nv_bfloat16, MAX>(t.src[k], at, n, policy, run);
     else
-      norm_chunk<__half, MAX>(static_cast<const __half *>(t.src[k]) + at, n, policy, acc);
-    const float v = MAX ? max_nan(max_nan(acc[0], acc[1]), max_nan(acc[2], acc[3]))
-                        : (acc[0] + acc[1]) + (acc[2] + acc[3]);
-    run = MAX ? max_nan(v, run) : run + v;
+      add_chunk<__half, MAX>(t.src[k], at, n, policy, run);
   }
-  const float s = block_reduce<MAX>(run, red);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+  run = block_sums<MAX>(run, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = make_float4(run.mid, run.low, run.high, 0.f);
 }
+
+// The norm, root * unit.  unit is 1 unless squares have left the range.
+struct Norm {
+  float root, unit;
+  __device__ __forceinline__ float value() const { return root * unit; }
+  // min(1, max_norm / (norm + eps)).  A norm that no float holds, or only as
+  // a subnormal, is taken in its own unit.
+  __device__ __forceinline__ float factor(float max_norm, float eps) const {
+    const float v = value();
+    float ratio = max_norm / (v + eps);
+    if (unit > 1.f && v > 0x1p120f) ratio = (max_norm * kDown) / (root + eps * kDown);
+    if (unit < 1.f && eps < kLeast) ratio = (max_norm * kUp) / (root + eps * kUp);
+    return ratio >= 1.f ? 1.f : ratio;  // a NaN stays
+  }
+};
 
 // The norm from all partials, the same in every thread of every block.
 template <bool MAX>
-__device__ __forceinline__ float whole_norm(const float *partial, int parts, float *red) {
-  float v = 0.f;
-  for (int i = threadIdx.x; i < parts; i += kThreads) v = MAX ? max_nan(partial[i], v) : v + partial[i];
-  v = block_reduce<MAX>(v, red);
-  return MAX ? v : sqrtf(v);
+__device__ __forceinline__ Norm whole_norm(const float4 *partial, int parts, float *red) {
+  Sums v = {0.f, 0.f, 0.f};
+  for (int i = threadIdx.x; i < parts; i += kThreads) {
+    const float4 p = partial[i];
+    v.mid = MAX ? max_nan(p.x, v.mid) : v.mid + p.x;
+    v.low += p.y;
+    v.high += p.z;
+  }
+  v = block_sums<MAX>(v, red);
+  if (MAX) return {v.mid, 1.f};
+  // all three in the unit of the largest; what is below its last bit may be lost
+  if (v.high != 0.f) return {sqrtf(fmaf(v.mid * kDown, kDown, v.high)), kUp};
+  if (v.low != 0.f && v.mid < 0x1p-60f) return {sqrtf(fmaf(v.mid * kUp, kUp, v.low)), kDown};
+  return {sqrtf(fmaf(v.low * kDown, kDown, v.mid)), 1.f};
 }
 
 template <bool MAX>
-__global__ void __launch_bounds__(kThreads) norm_finish(const float *partial, int parts, float *norm) {
+__global__ void __launch_bounds__(kThreads) norm_finish(const float4 *partial, int parts, float *norm) {
   __shared__ float red[32];
   dependency_wait();
-  const float v = whole_norm<MAX>(partial, parts, red);
-  if (threadIdx.x == 0) *norm = v;
+  const Norm v = whole_norm<MAX>(partial, parts, red);
+  if (threadIdx.x == 0) *norm = v.value();
 }
 
 // Loads that are the last of their bytes and stores that nothing reads soon
@@ -298,14 +396,13 @@ __device__ __forceinline__ void scale_chunk_to(const S *p, void *q, int dtype, i
 
 template <int K, bool MAX>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) scale_tensors(const __grid_constant__ TensorTable<K> t,
-                                                          const float *partial, int parts, float max_norm,
+                                                          const float4 *partial, int parts, float max_norm,
                                                           float eps, float *norm) {
   __shared__ float red[32];
   dependency_wait();
-  const float total = whole_norm<MAX>(partial, parts, red);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  const float ratio = max_norm / (total + eps);
-  const float coef = ratio >= 1.f ? 1.f : ratio;  // a NaN stays
+  const Norm total = whole_norm<MAX>(partial, parts, red);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total.value();
+  const float coef = total.factor(max_norm, eps);
   // from the last chunk back: what the norm read last is still in L2
   for (int64_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
     const int64_t c = t.chunks - 1 - i;
@@ -332,7 +429,7 @@ struct Request {
   const int32_t *types, *out_types;
   float max_norm, eps;
   float *norm;
-  float *partial;
+  float4 *partial;
   cudaStream_t s;
 };
 
@@ -400,7 +497,7 @@ cudaError_t run(const Request &q, bool clip) {
     parts += g;
   }
   if (!clip || parts == 0)
-    return launch_kernel(norm_finish<MAX>, dim3(1), kThreads, 0, true, q.s, (const float *)q.partial, parts,
+    return launch_kernel(norm_finish<MAX>, dim3(1), kThreads, 0, true, q.s, (const float4 *)q.partial, parts,
                          q.norm);
   // the table of a list that one launch took whole is still there
   const bool one = launches == 1 && t.count > 0;
@@ -410,7 +507,7 @@ cudaError_t run(const Request &q, bool clip) {
     if (!one) next = fill(t, q, next, chunk);
     if (t.count == 0) break;
     const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
-    e = launch_kernel(scale_tensors<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, (const float *)q.partial,
+    e = launch_kernel(scale_tensors<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, (const float4 *)q.partial,
                       parts, q.max_norm, q.eps, first ? q.norm : nullptr);
     if (e != cudaSuccess) return e;
     first = false;
@@ -461,16 +558,16 @@ snack_status dispatch(const Request &q, int norm_kind, bool clip) {
 }  // namespace snack
 
 extern "C" size_t snack_grad_norm_workspace(int64_t count) {
-  // one float per block and launch
+  // one partial per block and launch
   const int64_t launches = (count < 0 ? 0 : count) / snack::kMostTable + 2;
-  return (size_t)launches * snack::grid_blocks() * sizeof(float);
+  return (size_t)launches * snack::grid_blocks() * sizeof(float4);
 }
 
 extern "C" snack_status snack_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes,
                                         const int32_t *types, int norm_kind, float *norm, void *workspace,
                                         void *stream) {
   const snack::Request q = {count, grads, nullptr, sizes, types, nullptr, 0.f, 0.f, norm,
-                            static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)};
+                            static_cast<float4 *>(workspace), static_cast<cudaStream_t>(stream)};
   const snack_status st = snack::check(q, norm_kind, workspace, false);
   return st == SNACK_OK ? snack::dispatch(q, norm_kind, false) : st;
 }
@@ -480,7 +577,7 @@ extern "C" snack_status snack_clip_grad_norm(int64_t count, const void *const *g
                                              const int32_t *out_types, int norm_kind, float max_norm,
                                              float eps, float *norm, void *workspace, void *stream) {
   const snack::Request q = {count,    grads, outs, sizes, types, out_types,
-                            max_norm, eps,   norm, static_cast<float *>(workspace),
+                            max_norm, eps,   norm, static_cast<float4 *>(workspace),
                             static_cast<cudaStream_t>(stream)};
   const snack_status st = snack::check(q, norm_kind, workspace, true);
   return st == SNACK_OK ? snack::dispatch(q, norm_kind, true) : st;

@@ -57,7 +57,8 @@ def snack_clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, out=Non
     """Scale the gradients by min(1, max_norm / (norm + eps)) and return their
     norm before that, as one float32 on the device.  In place, or into ``out``
     (a list or SnackTensorList of the same sizes; its types may differ, e.g.
-    float32 buffers of an optimizer for bfloat16 gradients).  A NaN norm makes
+    float32 buffers of an optimizer for bfloat16 gradients).  ``out`` must not
+    overlap the gradients otherwise; this is not checked.  A NaN gradient makes
     every result NaN; an infinite one zeros what is finite."""
     return _dense.clip_grad_norm(_handle(grads), max_norm, norm_type,
                                  None if out is None else _handle(out), eps, norm,

@@ -441,7 +441,9 @@ snack_status snack_adapter_backward(const snack_adapter_args *args, const void *
  * contiguous elements of types[i]; the arrays of pointers, sizes and types
  * are host memory, read before the call returns.  *norm (device) receives
  * the norm; NaN or infinities in a gradient make it NaN or infinite, and no
- * gradient at all makes it 0.
+ * gradient at all makes it 0.  Squares outside the range of fp32 are summed
+ * in another unit: the norm of finite gradients is infinite only where no
+ * fp32 holds it, and clipping then still scales by it.
  */
 size_t snack_grad_norm_workspace(int64_t count);
 snack_status snack_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes,

@@ -277,3 +277,38 @@ def test_writes_in_place_are_seen_by_autograd():
         g = torch.ones(64, device="cuda")
         sn.snack_clip_grad_norm([g], 1.0)
         assert abs(float(g[0]) - 1 / 8) <= 1e-5
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-25, 1e-18, 1e-15, 1e18, 1e25, 1e35])
+def test_magnitudes_whose_squares_leave_the_range(dt, size):
+    """The norm of finite gradients is theirs wherever it is a float32
+    itself, and clipping scales them by it."""
+    import coo_spmm_sparse_gb300 as sn
+    ts = tensors([5, 4096, 70_001], [dt], 11, std=1.0, offset=1)
+    for mixed in (False, True):
+        gs = [(t.double() * size).to(dt) for t in ts]
+        if mixed:  # among gradients of ordinary size
+            gs[1] = ts[1] * 1e-3
+        want = norm64(gs, 2.0)
+        got = float(sn.snack_grad_norm(gs))
+        assert abs(got - want) <= 1e-5 * want
+        before = [t.clone() for t in gs]
+        sn.snack_clip_grad_norm(gs, 0.5 * want, eps=0.0)
+        for t, b in zip(gs, before):
+            v = b.double() * 0.5
+            # float32 and bfloat16 below 2^-126 keep no more than half their last bit
+            tiny = 2.0 ** -149 if dt == F32 else 2.0 ** -134
+            err = (t.double() - v).abs()
+            assert bool((err <= (1e-5 + (2.0 ** -8 if dt == BF16 else 0)) * v.abs() + tiny).all())
+
+
+def test_a_norm_beyond_float32():
+    """Finite gradients whose norm no float32 holds: the norm is infinite,
+    the factor is not lost."""
+    import coo_spmm_sparse_gb300 as sn
+    g = torch.full((4096,), 3e38, device="cuda")
+    assert float(sn.snack_grad_norm([g])) == math.inf
+    sn.snack_clip_grad_norm([g], 1e30)
+    want = 1e30 / 64
+    assert bool(((g.double() - want).abs() <= 1e-5 * want).all())
