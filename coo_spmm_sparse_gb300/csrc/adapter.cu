@@ -1572,13 +1572,25 @@ const char *bad_args(const snack_adapter_args *a) {
   return nullptr;
 }
 
-bool overlap(const void *p, int64_t pb, const void *q, int64_t qb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
-  return p && q && x < y + (uintptr_t)qb && y < x + (uintptr_t)pb;
-}
+// Rows of `width` elements, `stride` apart.
+struct RowsAt {
+  const void *p;
+  int64_t stride, width;
+};
 
-int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width, int type) {
-  return rows < 1 ? 0 : ((rows - 1) * stride + width) * type_bytes(type);
+// Whether two arrays of as many rows share an element.  Column ranges of one
+// buffer (equal strides) do not; of other strides over one piece of memory,
+// which nothing needs, it is not worked out.
+bool overlap(const RowsAt &a, const RowsAt &b, int64_t rows, int type) {
+  if (!a.p || !b.p || rows < 1) return false;
+  const int64_t e = type_bytes(type);
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const auto bytes = [&](const RowsAt &r) { return (uintptr_t)(((rows - 1) * r.stride + r.width) * e); };
+  if (x >= y + bytes(b) || y >= x + bytes(a)) return false;
+  if (rows == 1 || a.stride != b.stride) return true;
+  const int64_t step = a.stride * e;
+  const int64_t at = x <= y ? (int64_t)((y - x) % step) : (step - (int64_t)((x - y) % step)) % step;  // b's columns from a's on
+  return at < a.width * e || at + b.width * e > step;
 }
 
 int64_t align16(int64_t b) { return (b + 15) / 16 * 16; }
@@ -1832,7 +1844,7 @@ extern "C" snack_status snack_adapter_forward(const snack_adapter_args *args, vo
   if (a.tokens > 1 && y_stride < a.out) return refuse(SNACK_ERR_INVALID_ARG, "y_stride is below out");
   if (!aligned_to(Y, type_bytes(a.type)) || !aligned_to(H, 4))
     return refuse(SNACK_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  if (overlap(a.X, rows_bytes(a.tokens, a.x_stride, a.in, a.type), Y, rows_bytes(a.tokens, y_stride, a.out, a.type)))
+  if (overlap({a.X, a.x_stride, a.in}, {Y, y_stride, a.out}, a.tokens, a.type))
     return refuse(SNACK_ERR_INVALID_ARG, "Y overlaps X");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AdapterArgs q = {};
@@ -1893,9 +1905,8 @@ extern "C" snack_status snack_adapter_backward(const snack_adapter_args *args, c
   const int64_t e0 = type_bytes(a.type);
   if (!aligned_to(dY, e0) || !aligned_to(dX, e0) || !aligned_to(dA, e0) || !aligned_to(dB, e0) || !aligned_to(H, 4))
     return refuse(SNACK_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  const int64_t dxb = rows_bytes(a.tokens, dx_stride, a.in, a.type);
-  if (overlap(a.X, rows_bytes(a.tokens, a.x_stride, a.in, a.type), dX, dxb) ||
-      overlap(dY, rows_bytes(a.tokens, dy_stride, a.out, a.type), dX, dxb))
+  const RowsAt dx = {dX, dx_stride, a.in};
+  if (overlap({a.X, a.x_stride, a.in}, dx, a.tokens, a.type) || overlap({dY, dy_stride, a.out}, dx, a.tokens, a.type))
     return refuse(SNACK_ERR_INVALID_ARG, "dX overlaps X or dY");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.adapters == 0) return SNACK_OK;

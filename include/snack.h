@@ -405,7 +405,8 @@ snack_status snack_residual_norm_backward(const snack_norm_args *args,
  * X and Y rows lie x_stride / y_stride elements apart.  X, Y, A and B are of
  * `type`; scale and H [tokens][rank] are fp32.  H is what the backward call
  * reads.  Limits: 1 <= rank <= 512, tokens, requests, in, out < 2^31,
- * adapters <= 65536.  X and Y must not overlap.
+ * adapters <= 65536.  X and Y must not overlap; column ranges of the rows of
+ * one buffer do not.
  */
 typedef struct {
   int64_t tokens, requests, adapters, in, out, rank;

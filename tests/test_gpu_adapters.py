@@ -415,3 +415,28 @@ def test_sums_over_high_ranks(rank):
 @pytest.mark.parametrize("T", [60, 150])
 def test_high_ranks(dt, rank, T):
     check(make([0, 33, 90 if T > 90 else 40, T], [1, 0, 1], 2, 96, 160, rank, dt, T=T, seed=rank))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T", [40, 200])
+def test_column_ranges_of_one_buffer(dt, T):
+    """X and Y, and X, dY and dX, side by side in the rows of one buffer:
+    ranges that share no element are no overlap."""
+    import coo_spmm_sparse_gb300 as sn
+    c = make([0, 9, T], [1, 0], 2, 96, 128, 8, dt, seed=T)
+    wide = torch.zeros(T, 96 + 128 + 128 + 96, dtype=dt, device="cuda")
+    at = 0
+    for k in ("X", "Y", "dY", "dX"):
+        v = wide[:, at: at + c[k].shape[1]]
+        v.copy_(c[k])
+        at += c[k].shape[1]
+        c[k] = v
+    check(c)
+    args = (c["A"], c["B"], c["offsets"], c["which"], c["scale"])
+    for lo in (88, 95):  # Y's first columns are X's last
+        with pytest.raises(sn.SnackError) as e:
+            sn.snack_adapter_forward(c["X"], *args, wide[:, lo: lo + 128])
+        assert e.value.status == 1 and "overlaps" in str(e.value)
+    other = wide.view(-1)[: T * 224].view(T, 224)[:, 96:]  # rows of another length over the same memory
+    with pytest.raises(sn.SnackError):
+        sn.snack_adapter_forward(c["X"], *args, other)
