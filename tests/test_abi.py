@@ -84,3 +84,37 @@ def test_missing_library_fails_loudly(tmp_path):
             _abi.load(str(tmp_path / "nope.so"))
     finally:
         _abi._lib = saved
+
+
+def test_library_builds_without_torch(tmp_path, monkeypatch, capsys):
+    """The C ABI library needs no torch: without it the library alone is
+    built; with it, another torch version rebuilds the binding alone."""
+    import types
+    b, ran = _builder(), []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(b, "subprocess", types.SimpleNamespace(run=run))
+    for name, f in (("BUILD", ""), ("LIB", "libsnack.so"), ("DENSE", "_dense.so"),
+                    ("STAMP", "machine.txt"), ("DENSE_STAMP", "dense.txt")):
+        monkeypatch.setattr(b, name, str(tmp_path / f), raising=False)
+    monkeypatch.setattr(b, "_torch_dir", lambda: None)
+    assert b.build() == b.LIB and os.path.exists(b.LIB) and not os.path.exists(b.DENSE)
+    assert not any("binding.cpp" in a for cmd in ran for a in cmd)
+    assert "torch not found" in capsys.readouterr().err
+    ran.clear()
+    b.build()  # nothing is stale
+    assert not ran
+    torch_dir = tmp_path / "torch"
+    torch_dir.mkdir()
+    monkeypatch.setattr(b, "_torch_dir", lambda: str(torch_dir))
+    for version in ("1", "2"):
+        (torch_dir / "version.py").write_text(f"__version__ = '{version}'\n")
+        b.build()
+        assert len(ran) == 2 and os.path.exists(b.DENSE)  # compiled and linked, no kernel among them
+        ran.clear()
+        b.build()
+        assert not ran
