@@ -25,9 +25,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 4;
-// What the norm's pass asks the L2 to keep for the pass that scales: half of
-// it.  40.6 M fp32 gradients: 84 us without, 81 / 79 / 80 us at 32 / 64 / 90
-// MB; 400 M bf16 into fp32 513 -> 504 us.
+// The last bytes that the norm's pass reads as any kernel does, all before
+// them to be evicted first: half of the L2, left for the pass that scales.
+// 40.6 M fp32 gradients: 81 us (79 / 80 with 64 / 90 MB that are evicted last,
+// 84 without a difference); 400 M bf16 into fp32 510 us (505; 513).  Evicted
+// last, they would stay when the call is over: four reads of 96 MB after it
+// took 98 us for 75.
 constexpr int64_t kKeepBytes = int64_t(64) << 20;
 constexpr int kMostTable = 1024;  // tensors of one launch: 30 KB of the 32 KB that parameters may take
 
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_partials(const __
   __shared__ float red[32];
   dependency_wait();
   uint64_t keep, leave;  // in the L2, for the pass that scales
-  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(leave));
   Sums run = {0.f, 0.f, 0.f};  // over the chunks; within one, four sums of a thread
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
