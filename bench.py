@@ -605,10 +605,12 @@ def run_ours(args):
             "launches_per_step": int(launches_per_step),
             "clocks": clk,
             "wall_s_timed_region": round(wall, 4),
-            "ops": ops,
-            "train_step": train,
-            "extra_ops": extra,
+            # each op where it takes longest; the tables of all go to stderr (26 KB
+            # with them, the line did not arrive whole where its reader cuts it off)
+            "ops": [max((o for o in ops if o["op"] == k), key=lambda o: o["us"])
+                    for k in dict.fromkeys(o["op"] for o in ops)],
         }
+        sys.stderr.write(json.dumps({"ops": ops, "train_step": train, "extra_ops": extra}) + "\n")
         print(json.dumps(line), flush=True)
 
 

@@ -72,3 +72,19 @@ def test_our_arm_line():
     assert 0 < lo <= mid <= hi
     for o in d["ops"]:
         assert o["us"] > 0 and o["us_median"] > 0 and o["gather_gbs"] > 0
+
+
+@pytest.mark.gpu
+def test_line_stays_short_and_the_tables_go_to_stderr():
+    """A reader that cuts long lines off gets the whole result: below 6 KB
+    with every table asked for, and the tables on stderr."""
+    out = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), "--workload", "toy256",
+                          "--steps", "3", "--warmup", "3", "--cpu-seconds", "1"],
+                         capture_output=True, text=True, timeout=600, cwd=ROOT)
+    assert out.returncode == 0, out.stderr[-2000:]
+    line = [l for l in out.stdout.splitlines() if l.startswith("{")]
+    assert len(line) == 1 and len(line[0]) < 6000, len(line[0])
+    ops = json.loads(line[0])["ops"]
+    tables = json.loads([l for l in out.stderr.splitlines() if l.startswith('{"ops"')][0])
+    assert len(tables["extra_ops"]) > 10 and all(o in tables["ops"] for o in ops)
+    assert {o["op"] for o in ops} == {o["op"] for o in tables["ops"]}
