@@ -88,3 +88,25 @@ def test_line_stays_short_and_the_tables_go_to_stderr():
     tables = json.loads([l for l in out.stderr.splitlines() if l.startswith('{"ops"')][0])
     assert len(tables["extra_ops"]) > 10 and all(o in tables["ops"] for o in ops)
     assert {o["op"] for o in ops} == {o["op"] for o in tables["ops"]}
+
+
+def test_recorded_traffic_belongs_to_the_sparse_layer(tmp_path):
+    """Counters recorded of the sparse kernels stay valid when the dense
+    operators' sources change, and not when their own do."""
+    import shutil
+    sys.path.insert(0, ROOT)
+    import bench
+    csrc = tmp_path / "csrc"
+    shutil.copytree(os.path.join(ROOT, "coo_spmm_sparse_gb300", "csrc"), csrc)
+    want = bench.kernel_source_sha()
+    for name in bench.DENSE_SOURCES:
+        assert (csrc / name).exists()
+        (csrc / name).write_text("int changed;")
+    assert bench.kernel_source_sha(str(csrc)) == want
+    with open(csrc / "spmm_kernels.cuh", "a") as f:
+        f.write("// a comment\n")
+    assert bench.kernel_source_sha(str(csrc)) == want
+    with open(csrc / "spmm_kernels.cuh", "a") as f:
+        f.write("int changed;\n")
+    assert bench.kernel_source_sha(str(csrc)) != want
+    assert bench.recorded_traffic("fwd:large90:B64", "other") is None
