@@ -25,9 +25,15 @@
 //
 // fp32 operands are split into two tf32 parts, x = hi + lo, and hi*hi + hi*lo
 // + lo*hi is summed: what is left out is below 2^-22 of a product.  Their
-// running sums leave the matrix unit's accumulator every 32 summed elements for
-// a 32-bit sum that rounds to nearest (kept in it over 300 tokens, dA was 2.4e-6
-// off in the 2-norm; so 6.6e-7).
+// running sums leave the matrix unit's accumulator every 32 (outer) or 64
+// (down; up above 64 ranks) summed elements for a 32-bit sum that rounds to
+// nearest (kept in it over 300 tokens, dA was 2.4e-6 off in the 2-norm; so
+// 6.6e-7).
+//
+// H and dH are fp32 in memory.  In 16-bit products they are two parts of the
+// type, hi + lo: 16 bits of them in bf16 (off by 2^-17), 22 in fp16, beside
+// the 8 and 11 bits to which the results are rounded.  Few tokens take them
+// as they are.
 //
 // 8192 tokens, 4096 -> 4096, 4 adapters of rank 16, fp32: forward and backward
 // 240 us, 160 us of which is the traffic at 6.7 TB/s.
@@ -1268,7 +1274,9 @@ __global__ void __launch_bounds__(kThreads) adapter_turn(const __grid_constant__
 // at rank 16, fp32, one by one / by tiles: forward 10 tokens 7, 64 10.3, 100
 // 16.8 / 13.5 us (768 -> 2304 at rank 8: 100 tokens 9 / 12.4); forward +
 // backward of 64 tokens of one adapter 50 / 46 us and of 16 adapters 35 / 74
-// us, of 128 tokens 63 / 46 and 52 / 74 us.
+// us, of 128 tokens 63 / 46 and 52 / 74 us.  The count alone decides, which
+// at the first and the last of these four is the slower way: how many tokens
+// share an adapter is not known to the host, and rank does not enter.
 constexpr int kFewTokens = 96, kFewTokensBack = 64;
 
 struct FewArgs {

@@ -27,10 +27,10 @@ constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 4;
 // The last bytes that the norm's pass reads as any kernel does, all before
 // them to be evicted first: half of the L2, left for the pass that scales.
-// 40.6 M fp32 gradients: 81 us (79 / 80 with 64 / 90 MB that are evicted last,
-// 84 without a difference); 400 M bf16 into fp32 510 us (505; 513).  Evicted
-// last, they would stay when the call is over: four reads of 96 MB after it
-// took 98 us for 75.
+// 40.6 M fp32 gradients at 32 / 64 / 96 / 128 MB: 82.1 / 80.7 / 81.0 / 82.6 us,
+// without a difference 83.5; 400 M bf16 into fp32 511.3 / 510.6 / 511.8 /
+// 512.5, 518.1.  (Evicted last, 505 us; but then they stay when the call is
+// over, and four reads of 96 MB after it took 98 us for 75.)
 constexpr int64_t kKeepBytes = int64_t(64) << 20;
 constexpr int kMostTable = 1024;  // tensors of one launch: 30 KB of the 32 KB that parameters may take
 

@@ -398,10 +398,13 @@ snack_status snack_residual_norm_backward(const snack_norm_args *args,
  * `uniform_scale` where scale is NULL).  Tokens of a request whose adapter
  * is outside [0, adapters), and tokens outside every request, keep their Y
  * (H is zero there).  offsets [requests + 1] (non-decreasing, in [0, tokens])
- * and adapter [requests] are int32 device arrays and never read by the host;
- * values that break this are clamped, never followed out of bounds.  In fp32
- * an operand beyond 2^128 - 2^116, infinities among them, may give NaN where
- * the sum is infinite.
+ * and adapter [requests] are int32 device arrays and never read by the host.
+ * Where offsets break this, nothing outside the tensors is read or written;
+ * which request such a token belongs to is not defined, and may differ with
+ * the number of tokens and between the forward and the backward call.
+ * An infinite operand may give NaN where the sum is infinite: in fp32 one
+ * beyond 2^128 - 2^116, in 16-bit types an infinite X or dY and an H or dH that
+ * the type cannot hold (bf16) or that is infinite.
  * X and Y rows lie x_stride / y_stride elements apart.  X, Y, A and B are of
  * `type`; scale and H [tokens][rank] are fp32.  H is what the backward call
  * reads.  Limits: 1 <= rank <= 512, tokens, requests, in, out < 2^31,

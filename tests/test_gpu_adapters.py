@@ -440,3 +440,22 @@ def test_column_ranges_of_one_buffer(dt, T):
     other = wide.view(-1)[: T * 224].view(T, 224)[:, 96:]  # rows of another length over the same memory
     with pytest.raises(sn.SnackError):
         sn.snack_adapter_forward(c["X"], *args, other)
+
+
+@pytest.mark.parametrize("T", [40, 90, 200])
+def test_offsets_out_of_order_stay_in_bounds(T):
+    """Offsets that decrease or lie outside [0, tokens]: which request a token
+    then belongs to is not defined; nothing outside the tensors is written,
+    and every row is one of the three that its adapters can give."""
+    import coo_spmm_sparse_gb300 as sn
+    c = make([0, 30, 10, T + 50, -7, T - 3], [1, 0, 1, 0, 1], 2, 64, 96, 8, F32, T=T, seed=T)
+    flat = torch.full(((T + 2) * 96,), 7.0, device="cuda")
+    y0, Y = c["Y"].clone(), flat[96: 96 + T * 96].view(T, 96)
+    Y.copy_(c["Y"])
+    sn.snack_adapter_forward(c["X"], c["A"], c["B"], c["offsets"], c["which"], c["scale"], Y)
+    assert (flat[:96] == 7).all() and (flat[-96:] == 7).all()
+    rows = [y0] + [y0 + c["scale"][n] * (c["X"].double() @ c["A"][n].double().T
+                                         @ c["B"][n].double().T) for n in range(2)]
+    near = torch.stack([torch.isclose(Y.double(), v.double(), rtol=1e-4, atol=1e-4).all(1)
+                        for v in rows])
+    assert near.any(0).all()
