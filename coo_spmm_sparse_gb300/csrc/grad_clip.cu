@@ -481,6 +481,24 @@ int64_t fill(TensorTable<K> &t, const Request &q, int64_t i, int chunk) {
   return i;
 }
 
+// launch_kernel() without its copy of the table (6 or 30 KB).
+template <int K, typename... P>
+cudaError_t launch_table(void (*kern)(TensorTable<K>, P...), int blocks, cudaStream_t s, TensorTable<K> &t, P... rest) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void *args[] = {&t, &rest...};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kern), args);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
 template <int K, bool MAX>
 cudaError_t run(const Request &q, bool clip) {
   int64_t total = 0;
@@ -495,7 +513,7 @@ cudaError_t run(const Request &q, bool clip) {
     if (t.count == 0) break;
     ++launches;
     const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
-    e = launch_kernel(norm_partials<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, q.partial + parts);
+    e = launch_table<K>(norm_partials<K, MAX>, g, q.s, t, q.partial + parts);
     if (e != cudaSuccess) return e;
     parts += g;
   }
@@ -510,8 +528,8 @@ cudaError_t run(const Request &q, bool clip) {
     if (!one) next = fill(t, q, next, chunk);
     if (t.count == 0) break;
     const int g = (int)std::min<int64_t>(t.chunks, grid_blocks());
-    e = launch_kernel(scale_tensors<K, MAX>, dim3(g), kThreads, 0, true, q.s, t, (const float4 *)q.partial,
-                      parts, q.max_norm, q.eps, first ? q.norm : nullptr);
+    e = launch_table<K>(scale_tensors<K, MAX>, g, q.s, t, (const float4 *)q.partial, parts, q.max_norm, q.eps,
+                        first ? q.norm : (float *)nullptr);
     if (e != cudaSuccess) return e;
     first = false;
   } while (!one && next < q.count);
