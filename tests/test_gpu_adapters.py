@@ -459,3 +459,27 @@ def test_offsets_out_of_order_stay_in_bounds(T):
     near = torch.stack([torch.isclose(Y.double(), v.double(), rtol=1e-4, atol=1e-4).all(1)
                         for v in rows])
     assert near.any(0).all()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in X, Y and dX: the last rows are as they are alone."""
+    import coo_spmm_sparse_gb300 as sn
+    T, inp, rank = 530_000, 4096, 8
+    g = torch.Generator(device="cuda").manual_seed(11)
+    X, Y, dX = (torch.empty(T, inp, dtype=BF16, device="cuda").normal_(generator=g) for _ in range(3))
+    A = torch.randn(2, rank, inp, generator=g, device="cuda").mul_(inp ** -0.5).to(BF16)
+    B = torch.randn(2, inp, rank, generator=g, device="cuda").to(BF16)
+    last = slice(T - 40, T)
+    off = torch.tensor([0, T - 20, T], dtype=torch.int32, device="cuda")
+    which = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    tail = torch.tensor([0, 20, 40], dtype=torch.int32)
+    dY = Y.clone()
+    want = dense_ref.adapter(X[last], Y[last], A, B, tail, which, 0.5, dY=dY[last], dX=dX[last])
+    Y, H = sn.snack_adapter_forward(X, A, B, off, which, 0.5, Y)
+    dX, dA, dB = sn.snack_adapter_backward(X, dY, A, B, off, which, 0.5, H, dX=dX)
+    for k, v in (("Y", Y), ("H", H), ("dX", dX)):
+        assert_within(k, v[last], *want[k])
+    assert torch.isfinite(dA).all() and torch.isfinite(dB).all()
+    alone = dense_ref.adapter(X[-20:], Y[-20:], A, B, tail[:2], which[1:], 0.5, dY=dY[-20:])
+    assert_within("dA", dA[0], alone["dA"][0][0], alone["dA"][1][0])
+    assert_within("dB", dB[0], alone["dB"][0][0], alone["dB"][1][0])

@@ -341,3 +341,15 @@ def test_what_runs_next_keeps_its_cache():
     for call in (lambda: sn.snack_grad_norm(kept), lambda: sn.snack_clip_grad_norm(kept, 1e9)):
         ratios.append(min(after(call) for _ in range(5)) / plain)
     assert max(ratios) <= 1.15, ratios
+
+
+def test_offsets_beyond_32_bits():
+    import coo_spmm_sparse_gb300 as sn
+    n = 2 ** 31 + 70_001
+    t = torch.full((n,), 0.5, dtype=BF16, device="cuda")
+    t[-1] = 256.0
+    want = math.sqrt((n - 1) * 0.25 + 65536.0)
+    got = float(sn.snack_clip_grad_norm([t], 0.5 * want))
+    assert abs(got - want) <= 1e-5 * want
+    assert float(t[-1]) == 128.0 and float(t[0]) == float(t[-2]) == 0.25
+    assert float(t[2 ** 31 - 5: 2 ** 31 + 5].float().sum()) == 2.5

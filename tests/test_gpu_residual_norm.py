@@ -428,3 +428,22 @@ def test_second_derivatives_raise():
             g, = torch.autograd.grad(loss(r, h), t, create_graph=True)
             with pytest.raises(RuntimeError, match="second derivative"):
                 (h.sum() + g.square().sum()).backward()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows are as they are alone."""
+    import coo_spmm_sparse_gb300 as sn
+    rows, d = 66_000, 32_768
+    g = torch.Generator(device="cuda").manual_seed(15)
+    x, y, dr, dh = (torch.empty(1, rows, d, dtype=BF16, device="cuda").normal_(generator=g)
+                    for _ in range(4))
+    o = dict(kind="rms", post_norm=True, gate=torch.rand(1, rows, 1, device="cuda").to(BF16),
+             next_weight=torch.rand(d, generator=g, device="cuda"))
+    r, h, stats = sn.snack_residual_norm_forward(x, y, **o)
+    got = dict(sn.snack_residual_norm_backward(dr, dh, x, y, stats, **o), r=r, h=h)
+    last = slice(rows - 3, rows)
+    tail = [t[:, last].contiguous() for t in (x, y, dr, dh)]
+    want = dense_ref.residual_norm(*tail[:2], dr=tail[2], dh=tail[3],
+                                   **dict(o, gate=o["gate"][:, last]))
+    for k in ("r", "h", "dx", "dy", "dgate"):
+        assert_within(k, got[k][:, last], *want[k])
