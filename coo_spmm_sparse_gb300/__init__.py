@@ -25,6 +25,9 @@ Around the layers (fp32, bfloat16 and float16; no handle):
     dX, dA, dB = snack_adapter_backward(X, dY, A, B, offsets, adapter, scale, H)
     norm = snack_grad_norm(grads)                           # grad_clip.py
     norm = snack_clip_grad_norm(grads, max_norm)
+    out, lse = snack_attention_forward(q, k, v, ...)        # attention.py
+    dq, dk, dv = snack_attention_backward(dout, q, k, v, out, lse, ...)
+    y = snack_dropout_forward(x, p, seed, residual)         # dropout.py
 """
 
 from __future__ import annotations
@@ -46,6 +49,8 @@ __all__ = [
     "snack_residual_norm_forward", "snack_residual_norm_backward", "snack_residual_norm", "SnackResidualNorm",
     "snack_adapter_forward", "snack_adapter_backward", "SnackAdapters",
     "SnackTensorList", "snack_tensor_list", "snack_grad_norm", "snack_clip_grad_norm",
+    "snack_attention_forward", "snack_attention_backward", "snack_attention", "snack_packed_attention",
+    "snack_dropout_forward", "snack_dropout_backward", "snack_dropout",
 ]
 
 
@@ -486,6 +491,9 @@ class SnackLinear(torch.nn.Module):
 
 
 from .adapters import SnackAdapters, snack_adapter_backward, snack_adapter_forward  # noqa: E402
+from .attention import (snack_attention, snack_attention_backward,  # noqa: E402
+                        snack_attention_forward, snack_packed_attention)
+from .dropout import snack_dropout, snack_dropout_backward, snack_dropout_forward  # noqa: E402
 from .grad_clip import (SnackTensorList, snack_clip_grad_norm, snack_grad_norm,  # noqa: E402
                         snack_tensor_list)
 from .residual_norm import (SnackResidualNorm, snack_residual_norm,  # noqa: E402

@@ -50,6 +50,12 @@ SIGNATURES = {
     "snack_grad_norm": (ctypes.c_int, [i64, vp, vp, vp, ctypes.c_int, vp, vp, vp]),
     "snack_clip_grad_norm": (ctypes.c_int, [i64, vp, vp, vp, vp, vp, ctypes.c_int, f32, f32, vp,
                                             vp, vp]),
+    "snack_attention_forward_workspace": (sz, [vp]),
+    "snack_attention_forward": (ctypes.c_int, [vp, vp, vp, vp, vp, vp]),
+    "snack_attention_backward_workspace": (sz, [vp]),
+    "snack_attention_backward": (ctypes.c_int, [vp, vp, vp, vp]),
+    "snack_dropout": (ctypes.c_int, [i64, vp, ctypes.c_int, vp, vp, ctypes.c_int, f32, u64, vp,
+                                     vp]),
     "snack_launch_count": (u64, []),
     "snack_debug_fail_alloc": (None, [i64]),
     "snack_device_error": (ctypes.c_int, [vp, P(ctypes.c_int), vp]),

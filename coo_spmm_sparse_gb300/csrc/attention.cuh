@@ -1,0 +1,155 @@
+// What the attention kernels share: the call as the device sees it, its
+// sequences and tiles, the mask that dropout makes of a probability's place.
+#pragma once
+
+#include "counter_random.cuh"
+#include "dense_ops.cuh"
+
+namespace snack {
+
+struct Strided {
+  void *p;
+  int64_t seq, token, head;  // elements
+};
+
+struct AttnCall {
+  Strided q, k, v, out, dout, dq, dk, dv;
+  float *lse;    // [heads][rows]: log of the sum of exp(scale * q . k), -inf where no key is seen
+  float *delta;  // [heads][rows]: dout . out
+  float *part;   // partial results of a split call
+  const uint32_t *peak;  // bits of the largest |dout| and |v| (float16)
+  int64_t rows;  // rows of lse for a head: all tokens of q
+  int sequences, q_tokens, k_tokens;
+  int heads, key_heads, group, d;
+  int causal, splits, chunk;
+  float scale, scale_log2;  // scale * log2(e)
+  const int32_t *q_offsets, *k_offsets, *q_lengths, *k_lengths;
+  uint32_t drop;  // 0: no dropout; else a probability is kept where its 16 bits are at least this
+  float keep_scale;  // 1 without dropout
+  uint64_t seed;
+  const uint64_t *seed_at;
+
+  __device__ __forceinline__ uint64_t draws() const { return seed_at ? *seed_at : seed; }
+};
+
+// The tokens of one sequence on one side.  `base` is the address part that
+// does not depend on the head; rows `valid` .. cover-1 belong to the tensor
+// but not to the sequence (padding): their results are zero.
+struct Span {
+  int64_t row;  // number of the first token among all
+  int valid, cover;
+  int seq;  // of a dense side; 0 in a ragged one, whose tokens are numbered through
+};
+
+// Sequences are numbered 0 .. sequences-1 in a dense side.  A ragged side has
+// two more, without partners on the other side: the tokens before the first
+// offset (number 0) and behind the last (sequences + 1), whose results are
+// zero.  Broken offsets are cut to the tensor: nothing outside is touched.
+__device__ __forceinline__ int clamped(const int32_t *offsets, int i, int tokens) {
+  const int v = offsets[i];
+  return v < 0 ? 0 : (v > tokens ? tokens : v);
+}
+
+__device__ __forceinline__ int ragged_begin(const int32_t *offsets, int s, int tokens) {
+  return s == 0 ? 0 : clamped(offsets, s - 1, tokens);
+}
+__device__ __forceinline__ int ragged_end(const int32_t *offsets, int s, int n, int tokens) {
+  return s == n + 1 ? tokens : clamped(offsets, s, tokens);
+}
+
+// The span of sequence `s` of the side that is cut into tiles.
+__device__ __forceinline__ Span own_span(const int32_t *offsets, const int32_t *lengths, int s, int n, int tokens) {
+  Span sp;
+  if (offsets) {
+    const int a = ragged_begin(offsets, s, tokens), b = ragged_end(offsets, s, n, tokens);
+    sp.row = a;
+    sp.cover = b > a ? b - a : 0;
+    sp.valid = s == 0 || s == n + 1 ? 0 : sp.cover;
+    sp.seq = 0;
+    return sp;
+  }
+  sp.row = (int64_t)s * tokens;
+  sp.cover = tokens;
+  sp.valid = lengths ? min(max(lengths[s], 0), tokens) : tokens;
+  sp.seq = s;
+  return sp;
+}
+
+// The span of the same sequence on the other side; `ragged` says how s is
+// numbered.
+__device__ __forceinline__ Span other_span(const int32_t *offsets, const int32_t *lengths, int s, bool ragged, int n,
+                                           int tokens) {
+  const int i = ragged ? s - 1 : s;
+  if (i < 0 || i >= n) return Span{0, 0, 0, 0};
+  if (offsets) return own_span(offsets, nullptr, i + 1, n, tokens);
+  return own_span(nullptr, lengths, i, n, tokens);
+}
+
+// Sequence and tile of tile number t, where each sequence has ceil(cover *
+// per_token / tile_rows) tiles.  Called by whole warps.  s < 0: no such tile.
+// Tiles of a sequence are numbered from its end where `back`: under a causal
+// mask the later rows have the most to do and start first.
+struct Place {
+  int s, tile;
+};
+__device__ __forceinline__ Place find_tile(const int32_t *offsets, int n, int tokens, int per_token, int tile_rows,
+                                           int t, bool back) {
+  if (!offsets) {
+    const int per = (int)(((int64_t)tokens * per_token + tile_rows - 1) / tile_rows);
+    const int s = t / per, i = t - s * per;
+    if (s >= n) return Place{-1, 0};
+    return Place{s, back ? per - 1 - i : i};
+  }
+  const int lane = threadIdx.x & 31;
+  for (int s0 = 0; s0 < n + 2; s0 += 32) {
+    const int s = s0 + lane;
+    int own = 0;
+    if (s < n + 2) {
+      const int a = ragged_begin(offsets, s, tokens), b = ragged_end(offsets, s, n, tokens);
+      if (b > a) own = (int)(((int64_t)(b - a) * per_token + tile_rows - 1) / tile_rows);
+    }
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, t < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int cnt = __shfl_sync(0xffffffffu, own, l), end = __shfl_sync(0xffffffffu, upto, l);
+      const int i = t - (end - cnt);
+      return Place{s0 + l, back ? cnt - 1 - i : i};
+    }
+    t -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return Place{-1, 0};
+}
+
+// Tiles that a grid needs so that every sequence finds all of its own.
+// The launches of attention on mma.sync, by type (attention_rows_*.cu).
+template <typename T>
+cudaError_t rows_forward_launch(const AttnCall &c, bool few, cudaStream_t s);
+template <typename T>
+cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
+
+inline int64_t tiles_of(bool ragged, int64_t n, int64_t tokens, int64_t per_token, int64_t tile_rows) {
+  const int64_t per = (tokens * per_token + tile_rows - 1) / tile_rows;
+  return ragged ? per + n + 2 : n * per;
+}
+
+// Keys that query i of a sequence sees: j < seen_keys(...).
+__device__ __forceinline__ int seen_keys(int causal, int i, int nq, int nk) {
+  return causal ? min(nk, i + nk - nq + 1) : nk;
+}
+
+// The number of the draw that decides about keys 4c .. 4c+3 of a query row is
+// row * 2^30 + c, with row = token * heads + head.
+__device__ __forceinline__ uint64_t dropout_row(uint64_t seed, int64_t token, int heads, int head) {
+  return seed + ((((uint64_t)token * heads + head) << 30) + 1ull) * kSplitMixStep;
+}
+__device__ __forceinline__ uint64_t dropout_draw(uint64_t row, int key) {
+  return splitmix_finish(row + (uint64_t)(uint32_t)(key >> 2) * kSplitMixStep);
+}
+
+}  // namespace snack

@@ -658,6 +658,218 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ attention and dropout
+
+// A number of the dropout's seed, or a device tensor that holds it.
+struct Seed {
+  uint64_t value = 0;
+  const uint64_t *at = nullptr;
+  const at::Tensor *tensor = nullptr;
+  explicit Seed(PyObject *o) {
+    if (is_tensor(o)) {
+      const at::Tensor &t = THPVariable_Unpack(o);
+      if (!t.is_cuda() || t.scalar_type() != at::kLong || t.numel() != 1)
+        type_error("seed must be a number or one CUDA int64");
+      tensor = &t;
+      at = static_cast<const uint64_t *>(t.data_ptr());
+      return;
+    }
+    value = PyLong_AsUnsignedLongLongMask(o);
+    if (PyErr_Occurred()) throw Raised{};
+  }
+};
+
+// q, k, v, then kAttentionOptions: causal, scale, q_offsets, k_offsets,
+// q_lengths, k_lengths, dropout, seed.
+constexpr int kAttentionOptions = 8;
+struct Attention {
+  snack_attention_args a{};
+  Device dev;
+  const at::Tensor *q, *k, *v;
+  bool q_ragged, k_ragged;
+
+  static const at::Tensor *ints(PyObject *o, const char *name) {
+    return o == Py_None ? nullptr : &Adapter::ints(o, name);
+  }
+
+  // Strides of t, which is [sequences][tokens][heads][d], or [tokens][heads][d] where ragged.
+  static void strides(const at::Tensor &t, int64_t (&s)[3], const char *name) {
+    const int64_t n = t.dim();
+    if (t.size(n - 1) > 1 && t.stride(n - 1) != 1)
+      value_error(std::string(name) + " must be contiguous along its last dimension");
+    s[0] = n == 4 ? t.stride(0) : 0;
+    s[1] = t.stride(n - 3);
+    s[2] = t.stride(n - 2);
+  }
+
+  const at::Tensor &like_q(PyObject *o, const char *name, int64_t (&s)[3]) { return like(o, *q, name, "q", s); }
+  const at::Tensor &like(PyObject *o, const at::Tensor &other, const char *name, const char *of, int64_t (&s)[3]) {
+    const at::Tensor &t = dense(o, name);
+    if (t.scalar_type() != other.scalar_type()) type_error(std::string(name) + " must have " + of + "'s type");
+    if (t.sizes() != other.sizes())
+      value_error(std::string(name) + " " + shape(t) + " must have " + of + "'s shape " + shape(other));
+    strides(t, s, name);
+    dev.add(&t);
+    return t;
+  }
+
+  Attention(PyObject *q_, PyObject *k_, PyObject *v_, PyObject *const *o) {
+    q = &dense(q_, "q");
+    k = &dense(k_, "k");
+    v = &dense(v_, "v");
+    a.causal = truth(o[0]);
+    const at::Tensor *const qo = ints(o[2], "q_offsets"), *const ko = ints(o[3], "k_offsets");
+    const at::Tensor *const ql = ints(o[4], "q_lengths"), *const kl = ints(o[5], "k_lengths");
+    a.dropout = (float)number(o[6]);
+    if (!(a.dropout >= 0.f && a.dropout < 1.f)) value_error("dropout must be at least 0 and below 1");
+    const Seed seed(o[7]);
+    a.seed = seed.value;
+    a.seed_at = seed.at;
+    q_ragged = qo != nullptr;
+    k_ragged = ko != nullptr;
+    if (k->scalar_type() != q->scalar_type() || v->scalar_type() != q->scalar_type())
+      type_error("q, k and v must have one type");
+    if (q->dim() != (q_ragged ? 3 : 4))
+      value_error(q_ragged ? "q must be [tokens][heads][d] with q_offsets, got " + shape(*q)
+                           : "q must be [sequences][tokens][heads][d], got " + shape(*q));
+    if (k->dim() != (k_ragged ? 3 : 4))
+      value_error(k_ragged ? "k must be [tokens][heads][d] with k_offsets, got " + shape(*k)
+                           : "k must be [sequences][tokens][heads][d], got " + shape(*k));
+    if (v->sizes() != k->sizes()) value_error("v " + shape(*v) + " must have k's shape " + shape(*k));
+    const int64_t d = q->size(-1), heads = q->size(-2), key_heads = k->size(-2);
+    if (k->size(-1) != d) value_error("q and k must have one head size");
+    if (d < 1 || d > 128) value_error("the head size must be 1 to 128, got " + std::to_string(d));
+    if (key_heads < 1 || heads < 1 || heads % key_heads || heads > 65536)
+      value_error(std::to_string(heads) + " heads are not a multiple of " + std::to_string(key_heads) +
+                  " key heads (at most 65536)");
+    if ((q_ragged && ql) || (k_ragged && kl)) value_error("a side has offsets or lengths, not both");
+    const auto count_of = [&](const at::Tensor *off, const at::Tensor &t, const char *name) {
+      if (off && off->numel() < 1) value_error(std::string(name) + " must have at least one element");
+      return off ? off->numel() - 1 : t.size(0);
+    };
+    a.sequences = count_of(qo, *q, "q_offsets");
+    if (count_of(ko, *k, "k_offsets") != a.sequences) value_error("q and k must have the same number of sequences");
+    for (const at::Tensor *l : {ql, kl})
+      if (l && l->numel() != a.sequences) value_error("lengths must have one element for each sequence");
+    a.q_tokens = q->size(q_ragged ? 0 : 1);
+    a.k_tokens = k->size(k_ragged ? 0 : 1);
+    a.heads = (int32_t)heads;
+    a.key_heads = (int32_t)key_heads;
+    a.head_size = (int32_t)d;
+    a.type = type_code(q->scalar_type());
+    a.scale = o[1] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : (float)number(o[1]);
+    if (!std::isfinite(a.scale)) value_error("scale must be finite");
+    for (const at::Tensor *t : {q, k, v, qo, ko, ql, kl, seed.tensor}) dev.add(t);
+    a.q = addr(q);
+    a.k = addr(k);
+    a.v = addr(v);
+    strides(*q, a.q_stride, "q");
+    strides(*k, a.k_stride, "k");
+    strides(*v, a.v_stride, "v");
+    const auto at_ = [](const at::Tensor *t) { return static_cast<const int32_t *>(addr(t)); };
+    a.q_offsets = at_(qo);
+    a.k_offsets = at_(ko);
+    a.q_lengths = at_(ql);
+    a.k_lengths = at_(kl);
+  }
+
+  std::vector<int64_t> lse_shape() const {
+    if (q_ragged) return {a.heads, a.q_tokens};
+    return {a.heads, a.sequences, a.q_tokens};
+  }
+};
+
+// q, k, v, options, stream
+PyObject *attention_forward(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 3 + kAttentionOptions + 1);
+    Attention m(o[0], o[1], o[2], o + 3);
+    const Stream s(o[3 + kAttentionOptions], m.dev.dev);
+    const at::Tensor out = empty(m.q->sizes(), m.q->scalar_type(), m.dev.dev);
+    const at::Tensor lse = empty(m.lse_shape(), at::kFloat, m.dev.dev);
+    int64_t stride[3];
+    Attention::strides(out, stride, "out");
+    const at::Tensor ws = s.scratch(snack_attention_forward_workspace(&m.a), m.dev.dev);
+    check(snack_attention_forward(&m.a, out.data_ptr(), stride, static_cast<float *>(lse.data_ptr()),
+                                  scratch_addr(ws), s.raw));
+    return Py_BuildValue("(NN)", wrap(out), wrap(lse));
+  });
+}
+
+// dout, q, k, v, out, lse, options, dq, dk, dv, need_dq, need_dkv, stream
+PyObject *attention_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 6 + kAttentionOptions + 6);
+    Attention m(o[1], o[2], o[3], o + 6);
+    PyObject *const *const r = o + 6 + kAttentionOptions;
+    snack_attention_grads g{};
+    g.dout = m.like_q(o[0], "dout", g.dout_stride).data_ptr();
+    g.out = m.like_q(o[4], "out", g.out_stride).data_ptr();
+    const at::Tensor &lse = dense(o[5], "lse");
+    if (lse.scalar_type() != at::kFloat || !lse.is_contiguous() || lse.numel() != m.q->numel() / m.a.head_size)
+      value_error("lse must be the forward call's: " + std::to_string(m.q->numel() / m.a.head_size) +
+                  " contiguous float32");
+    m.dev.add(&lse);
+    g.lse = static_cast<const float *>(lse.data_ptr());
+    const bool need_dq = truth(r[3]), need_dkv = truth(r[4]);
+    const Stream s(r[5], m.dev.dev);
+    at::Tensor fresh[3];
+    PyObject *res[3] = {Py_None, Py_None, Py_None};
+    const auto result = [&](int i, const at::Tensor &like, const char *name, const char *of, int64_t (&st)[3],
+                            bool need) -> void * {
+      if (!need) return nullptr;
+      if (r[i] != Py_None) {
+        const at::Tensor &t = m.like(r[i], like, name, of, st);
+        for (int64_t k = 0; k < t.dim() - 1; ++k)
+          if (t.size(k) > 1 && t.stride(k) == 0) value_error(std::string(name) + ": its elements overlap");
+        res[i] = r[i];
+        return t.data_ptr();
+      }
+      fresh[i] = empty(like.sizes(), like.scalar_type(), m.dev.dev);
+      Attention::strides(fresh[i], st, name);
+      return fresh[i].data_ptr();
+    };
+    g.dq = result(0, *m.q, "dq", "q", g.dq_stride, need_dq);
+    g.dk = result(1, *m.k, "dk", "k", g.dk_stride, need_dkv);
+    g.dv = result(2, *m.v, "dv", "v", g.dv_stride, need_dkv);
+    const at::Tensor ws = s.scratch(snack_attention_backward_workspace(&m.a), m.dev.dev);
+    check(snack_attention_backward(&m.a, &g, scratch_addr(ws), s.raw));
+    for (int i = 0; i < 3; ++i)
+      if (res[i] != Py_None) written(res[i]);
+    const auto give = [&](int i) { return fresh[i].defined() ? wrap(fresh[i]) : same(res[i]); };
+    return Py_BuildValue("(NNN)", give(0), give(1), give(2));
+  });
+}
+
+// x, residual, dtype of y, p, seed, stream
+PyObject *dropout(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    count(n, 6);
+    const at::Tensor &x = dense(o[0], "x");
+    const at::Tensor *const res = dense_or_none(o[1], "residual");
+    if (!x.is_contiguous() || (res && !res->is_contiguous())) value_error("x and residual must be contiguous");
+    if (res && res->sizes() != x.sizes())
+      value_error("residual " + shape(*res) + " must have x's shape " + shape(x));
+    at::ScalarType type = res ? res->scalar_type() : x.scalar_type();
+    if (o[2] != Py_None) {
+      if (!THPDtype_Check(o[2]) || type_code(reinterpret_cast<THPDtype *>(o[2])->scalar_type) < 0)
+        type_error("dtype must be float32, bfloat16 or float16");
+      type = reinterpret_cast<THPDtype *>(o[2])->scalar_type;
+      if (res && type != res->scalar_type()) type_error("the result has the residual's type");
+    }
+    const double p = number(o[3]);
+    if (!(p >= 0.0 && p < 1.0)) value_error("p must be at least 0 and below 1");
+    const Seed seed(o[4]);
+    Device dev;
+    for (const at::Tensor *t : {&x, res, seed.tensor}) dev.add(t);
+    const Stream s(o[5], dev.dev);
+    const at::Tensor y = empty(x.sizes(), type, dev.dev);
+    check(snack_dropout(x.numel(), x.data_ptr(), type_code(x.scalar_type()), addr(res), y.data_ptr(), type_code(type),
+                        (float)p, seed.value, seed.at, s.raw));
+    return wrap(y);
+  });
+}
+
 PyObject *set_error(PyObject *, PyObject *e) {
   Py_INCREF(e);
   Py_XSETREF(g_error, e);
@@ -667,7 +879,8 @@ PyObject *set_error(PyObject *, PyObject *e) {
 #define SNACK_FN(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SNACK_FN(norm_forward),    SNACK_FN(norm_backward), SNACK_FN(adapter_forward),
                          SNACK_FN(adapter_backward), SNACK_FN(tensor_list),   SNACK_FN(grad_norm),
-                         SNACK_FN(clip_grad_norm),   {"set_error", set_error, METH_O, nullptr},
+                         SNACK_FN(clip_grad_norm),   SNACK_FN(attention_forward), SNACK_FN(attention_backward),
+                         SNACK_FN(dropout),          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dense", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

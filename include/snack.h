@@ -465,6 +465,100 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
                                   float eps, float *norm, void *workspace, void *stream);
 
 /*
+ * Attention of `heads` query heads over `key_heads` heads of keys and values
+ * (heads a multiple of key_heads; query head h reads key head
+ * h / (heads / key_heads)).  For query i of a sequence with nq queries and nk
+ * keys, over the keys j that it sees (all, or with `causal` those with
+ * j <= i + nk - nq, so that the last query sees every key):
+ *
+ *   P[i][j] = exp(scale * q[i] . k[j]) / sum_j' exp(scale * q[i] . k[j'])
+ *   out[i]  = sum_j M[i][j] * P[i][j] * v[j],   lse[i] = log of that sum
+ *
+ * A query that sees no key has out = 0 and lse = -infinity.
+ *
+ * Each side (q; k and v) is dense or ragged.  Dense: `sequences` sequences of
+ * *_tokens tokens; *_lengths (int32 [sequences] on the device, or NULL) says
+ * how many of them a sequence has, what lies behind is neither read nor seen,
+ * and results there are zero.  Ragged: *_offsets (int32 [sequences + 1] on the
+ * device) and *_tokens tokens in all, sequence n owning offsets[n] ..
+ * offsets[n+1]-1; results of tokens outside every sequence are zero.  Offsets
+ * and lengths are never read by the host; where they are not non-decreasing
+ * and within the tokens, nothing outside the tensors is touched, and which
+ * results are written is not defined.  A ragged side excludes lengths.
+ *
+ * Element (n, t, h, e) of a tensor lies at n * stride[0] + t * stride[1] +
+ * h * stride[2] + e (a ragged side has n = 0).  Inputs may overlap in any way.
+ *
+ * Dropout: with T = round(65536 * dropout), M[i][j] is 0 where the 16 bits
+ * from 16 * (j mod 4) on of the SplitMix64 draw number
+ * (token * heads + head) * 2^30 + j / 4 of the seed are below T, else
+ * 65536 / (65536 - T); `token` counts the query tokens of all sequences
+ * (n * q_tokens + i where q is dense).  The seed is *seed_at (device memory,
+ * read when the kernels run) where that is not NULL, else `seed`.
+ *
+ * All tensors are of `type`; lse is fp32 [heads][query tokens of all
+ * sequences].  Products are summed in 32 bits.  In 16-bit types P, and in
+ * the backward pass dS, are rounded to the type before the second product (as
+ * tensor instructions take both operands in one type).  Within a sequence an
+ * infinite or NaN element of k or v may reach queries that do not see it.
+ * Limits: 1 <= head_size <= 128, heads <= 65536; tokens, and q_tokens *
+ * (heads / key_heads), below 2^31 - 4096.
+ */
+typedef struct {
+  int64_t sequences, q_tokens, k_tokens;
+  int32_t heads, key_heads, head_size, type;
+  int32_t causal;
+  float scale, dropout;
+  int32_t reserved;
+  uint64_t seed;
+  const uint64_t *seed_at;
+  const void *q, *k, *v;
+  int64_t q_stride[3], k_stride[3], v_stride[3];
+  const int32_t *q_offsets, *k_offsets, *q_lengths, *k_lengths;
+} snack_attention_args;
+
+size_t snack_attention_forward_workspace(const snack_attention_args *args);
+snack_status snack_attention_forward(const snack_attention_args *args, void *out,
+                                     const int64_t *out_stride, float *lse, void *workspace,
+                                     void *stream);
+
+/*
+ * Gradients of out, from the out and lse that the forward call wrote with the
+ * same args (the probabilities are made again, never stored):
+ *   delta[i] = dout[i] . out[i],
+ *   dS[i][j] = P[i][j] * (M[i][j] * (dout[i] . v[j]) - delta[i]),
+ *   dq[i] = scale * sum_j dS[i][j] k[j],   dk[j] = scale * sum_i dS[i][j] q[i],
+ *   dv[j] = sum_i M[i][j] P[i][j] dout[i],
+ * dk and dv summed over the query heads that share them.  dq, dk and dv are
+ * overwritten and must not overlap one another or an input; each may be NULL.
+ * No atomics: the same inputs give the same bits.
+ */
+typedef struct {
+  const void *dout, *out;
+  const float *lse;
+  void *dq, *dk, *dv;
+  int64_t dout_stride[3], out_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+} snack_attention_grads;
+
+size_t snack_attention_backward_workspace(const snack_attention_args *args);
+snack_status snack_attention_backward(const snack_attention_args *args,
+                                      const snack_attention_grads *grads, void *workspace,
+                                      void *stream);
+
+/*
+ * Dropout of n contiguous elements: y = residual + M * x (residual NULL: M * x),
+ * x of x_type, residual and y of y_type.  With T = round(65536 * p), M is 0
+ * for element e where the 16 bits from 16 * (e mod 4) on of the SplitMix64 draw
+ * number e / 4 of the seed are below T, else 65536 / (65536 - T).  The mask is
+ * not stored: the gradient of x is the same call on the gradient of y, with the
+ * same p and seed and no residual.  seed_at as for the attention.  y may be
+ * residual, or x of y's type; no other overlap.  0 <= p < 1 - 2^-17.
+ */
+snack_status snack_dropout(int64_t n, const void *x, int x_type, const void *residual, void *y,
+                           int y_type, float p, uint64_t seed, const uint64_t *seed_at,
+                           void *stream);
+
+/*
  * Read and clear the handle's device error flag: *flag = 1 if, since the
  * last read, a kernel of this handle gave up a bounded wait on one of its
  * own shared-memory copies (its outputs for that call are then not to be
