@@ -23,9 +23,11 @@ draws new masks where it also changes that tensor.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
-from . import _dense, _raw_stream
+from . import _check, _dense, _lib, _raw_stream, _stream
 from ._autograd import first_derivative
 
 
@@ -52,6 +54,14 @@ def snack_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     return _dense.attention_backward(dout, q, k, v, out, lse, causal, scale, q_offsets, k_offsets,
                                      q_lengths, k_lengths, dropout, seed, dq, dk, dv, need_dq,
                                      need_dkv, _raw_stream(stream))
+
+
+def snack_attention_error(stream=None) -> bool:
+    """Read and clear the current device's flag: True if a kernel of an attention call gave
+    up a bounded wait since the last read (its results are then wrong).  Synchronises."""
+    flag = ctypes.c_int()
+    _check(_lib.snack_attention_error(ctypes.byref(flag), _stream(stream)))
+    return bool(flag.value)
 
 
 def _rows_contiguous(t):

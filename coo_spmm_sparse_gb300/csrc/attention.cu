@@ -214,11 +214,13 @@ AttnCall call_of(const snack_attention_args *a) {
 // How a forward call is cut: few rows (16 to a block) where blocks of 128
 // would leave SMs idle, and its keys in parts where even those do.
 struct Cut {
-  bool few = false;
+  bool tiles = false, few = false;
   int splits = 1, chunk = 0;
 };
-Cut cut_of(const AttnCall &c) {
+Cut cut_of(const AttnCall &c, int type) {
   Cut cut;
+  cut.tiles = c.q_tokens >= 64 && tile_forward_fits(c, type);
+  if (cut.tiles) return cut;
   const bool ragged = c.q_offsets != nullptr;
   const int64_t sms = device_sms();
   cut.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
@@ -242,7 +244,7 @@ cudaError_t forward_typed(const AttnCall &c, bool few, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t backward_typed(AttnCall c, uint32_t *peak, cudaStream_t s) {
+cudaError_t backward_typed(AttnCall c, int type, uint32_t *peak, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   cudaError_t e = cudaSuccess;
   if (peak) {
@@ -266,6 +268,7 @@ cudaError_t backward_typed(AttnCall c, uint32_t *peak, cudaStream_t s) {
       e = launch_kernel(attention_delta<T, false>, dim3(blocks), 256, 0, false, s, c, peak);
     if (e != cudaSuccess) return e;
   }
+  if (c.q_tokens >= 64 && c.k_tokens >= 64 && tile_backward_fits(c, type)) return tile_backward_launch(c, type, s);
   return rows_backward_launch<T>(c, s);
 }
 
@@ -277,7 +280,7 @@ using namespace snack;
 extern "C" size_t snack_attention_forward_workspace(const snack_attention_args *a) {
   if (!a || check_args(a) != SNACK_OK) return 0;
   const AttnCall c = call_of(a);
-  const Cut cut = cut_of(c);
+  const Cut cut = cut_of(c, a->type);
   return cut.splits > 1 ? (size_t)cut.splits * c.rows * c.heads * (c.d + 1) * sizeof(float) : 0;
 }
 
@@ -290,7 +293,7 @@ extern "C" snack_status snack_attention_forward(const snack_attention_args *a, v
   if (!out || !out_stride || !lse) return bad("out, its strides or lse is NULL");
   c.out = strided(out, out_stride);
   c.lse = lse;
-  const Cut cut = cut_of(c);
+  const Cut cut = cut_of(c, a->type);
   c.splits = cut.splits;
   c.chunk = cut.chunk;
   if (cut.splits > 1) {
@@ -298,10 +301,20 @@ extern "C" snack_status snack_attention_forward(const snack_attention_args *a, v
     c.part = static_cast<float *>(workspace);
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->type == SNACK_F32    ? forward_typed<float>(c, cut.few, s)
+  const cudaError_t e = cut.tiles                 ? tile_forward_launch(c, a->type, s)
+                        : a->type == SNACK_F32  ? forward_typed<float>(c, cut.few, s)
                         : a->type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, cut.few, s)
                                                 : forward_typed<__half>(c, cut.few, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention forward");
+}
+
+extern "C" snack_status snack_attention_error(int *flag, void *stream) {
+  if (!flag) return bad("flag is NULL");
+  *flag = 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = tile_forward_failed(flag, s);
+  if (e == cudaSuccess) e = tile_backward_failed(flag, s);
+  return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention error flag");
 }
 
 extern "C" size_t snack_attention_backward_workspace(const snack_attention_args *a) {
@@ -330,8 +343,8 @@ extern "C" snack_status snack_attention_backward(const snack_attention_args *a, 
   }
   c.delta = reinterpret_cast<float *>(static_cast<char *>(workspace) + (peak ? 16 : 0));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->type == SNACK_F32    ? backward_typed<float>(c, peak, s)
-                        : a->type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, peak, s)
-                                                : backward_typed<__half>(c, peak, s);
+  const cudaError_t e = a->type == SNACK_F32    ? backward_typed<float>(c, a->type, peak, s)
+                        : a->type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, a->type, peak, s)
+                                                : backward_typed<__half>(c, a->type, peak, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention backward");
 }

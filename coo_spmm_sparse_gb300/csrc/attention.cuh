@@ -126,16 +126,35 @@ __device__ __forceinline__ Place find_tile(const int32_t *offsets, int n, int to
   return Place{-1, 0};
 }
 
-// Tiles that a grid needs so that every sequence finds all of its own.
 // The launches of attention on mma.sync, by type (attention_rows_*.cu).
 template <typename T>
 cudaError_t rows_forward_launch(const AttnCall &c, bool few, cudaStream_t s);
 template <typename T>
 cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
 
+// Those of attention on tcgen05 (attention_tiles*.cu): which calls they take,
+// and whether one of their bounded waits has run out since the last question.
+bool tile_forward_fits(const AttnCall &c, int type);
+cudaError_t tile_forward_launch(const AttnCall &c, int type, cudaStream_t s);
+cudaError_t tile_forward_failed(int *flag, cudaStream_t s);
+bool tile_backward_fits(const AttnCall &c, int type);
+cudaError_t tile_backward_launch(const AttnCall &c, int type, cudaStream_t s);
+cudaError_t tile_backward_failed(int *flag, cudaStream_t s);
+
+// Tiles that a grid needs so that every sequence finds all of its own.
 inline int64_t tiles_of(bool ragged, int64_t n, int64_t tokens, int64_t per_token, int64_t tile_rows) {
   const int64_t per = (tokens * per_token + tile_rows - 1) / tile_rows;
   return ragged ? per + n + 2 : n * per;
+}
+
+// float16 holds neither a small gradient's dS nor small probabilities well:
+// the backward kernels take P 2^14 fold there, and dS times the power of two
+// that keeps the largest that |dout| and |v| allow below 2^15.
+constexpr float kHalfP = 14.f;
+__device__ __forceinline__ float half_ds_scale(const AttnCall &c) {
+  const float most = 2.f * (float)c.d * __uint_as_float(c.peak[0]) * __uint_as_float(c.peak[1]) * c.keep_scale;
+  if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
+  return exp2f((float)min(max(14 - ilogbf(most), -100), 100));
 }
 
 // Keys that query i of a sequence sees: j < seen_keys(...).

@@ -463,18 +463,10 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_forward(const AttnCall c) {
 // With P of the forward call's lse made again,
 //   dP = M * (dout . v),  dS = P * (dP - delta),  dq = scale * dS k,
 //   dk = scale * dS^T q,  dv = (M * P)^T dout.
-// float16 holds neither a small gradient's dS nor small probabilities well:
-// there P is taken 2^14 fold, and dS times the power of two that keeps the
-// largest that |dout| and |v| allow below 2^15.
-constexpr float kHalfP = 14.f;
-
 template <typename T>
 __device__ __forceinline__ float ds_scale(const AttnCall &c) {
   if constexpr (!std::is_same<T, __half>::value) return 1.f;
-  const float a = __uint_as_float(c.peak[0]), b = __uint_as_float(c.peak[1]);
-  const float most = 2.f * (float)c.d * a * b * c.keep_scale;
-  if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
-  return exp2f((float)min(max(14 - ilogbf(most), -100), 100));
+  return half_ds_scale(c);
 }
 
 template <typename T, int DP, int WM, int WN, int BQ>

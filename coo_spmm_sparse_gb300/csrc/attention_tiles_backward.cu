@@ -1,0 +1,570 @@
+// The backward call of the attention on tcgen05: one kernel for the gradients
+// of keys and values, one for those of the queries.  Each makes the scores
+// again (seven products in all, where one kernel for everything would take
+// five but add up dq in an order that is not fixed).
+#include "attention_tiles.cuh"
+
+namespace snack {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kHalf = kTile / 2;  // columns of a tile that a warpgroup takes
+constexpr int kStatWarp = 10;
+
+template <typename T>
+__device__ __forceinline__ float ds_scale(const AttnCall &c) {
+  if constexpr (!std::is_same<T, __half>::value) return 1.f;
+  return half_ds_scale(c);
+}
+
+// ------------------------------------------------------------------ keys and values
+
+struct KeyBars {
+  uint64_t kv, q_full[2], q_empty[2], d_full[2], d_empty[2], stat_full[2], stat_empty[2];
+  uint64_t scores, probs, dprobs, dscores, done, cut, drain;
+  uint32_t tmem;
+  int failed;
+  alignas(16) float lse[2][kTile];
+  alignas(16) float delta[2][kTile];
+};
+
+template <int DP>
+constexpr size_t keys_smem() { return 1024 + (size_t)6 * tile_bytes<DP>(); }
+
+// A tile of 128 keys (rows of every product: a thread has a key), past which
+// the query tiles of all heads that share it stream:
+//   S^T = K Q^T,  P^T = exp2(S^T - lse),  dP^T = V dO^T,  dS^T = P^T (dP^T - delta),
+//   dV += P^T dO,  dK += dS^T Q.
+// Order of the products: dV(n), S(n+1), dK(n), dP(n+1), so that the
+// exponentials of n+1 run while dK(n) and dP(n+1) do, and dS(n+1) while dV(n+1)
+// does.  Scores, dP and both sums fill the 512 columns of tensor memory.
+template <typename T, int DP, bool DROP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_backward_keys(const AttnCall c, const __grid_constant__ TileMaps maps) {
+  extern __shared__ unsigned char raw[];
+  __shared__ KeyBars bars;
+  unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<DP>();
+  unsigned char *const sq = sv + tile_bytes<DP>(), *const sd = sq + 2 * tile_bytes<DP>();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int *const failed = &bars.failed;
+
+  const int kh = blockIdx.x % c.key_heads, G = c.group;
+  const Place at = find_tile(c.k_offsets, c.sequences, c.k_tokens, 1, kTile, blockIdx.x / c.key_heads, false);
+  if (at.s < 0) return;
+  const Span ks = own_span(c.k_offsets, c.k_lengths, at.s, c.sequences, c.k_tokens);
+  const Span qs = other_span(c.q_offsets, c.q_lengths, at.s, c.k_offsets != nullptr, c.sequences, c.q_tokens);
+  const int j0 = at.tile * kTile, nq = qs.valid, nk = ks.valid;
+  const int tile0 = (c.causal ? max(0, j0 - (nk - nq)) : 0) / kTile;
+  const int tiles = j0 < nk ? max(0, (nq + kTile - 1) / kTile - tile0) : 0;
+  const int all = tiles * G;
+
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      tc::bar_init(&bars.kv, 2);
+      for (int i = 0; i < 2; ++i) {
+        tc::bar_init(&bars.q_full[i], 1);
+        tc::bar_init(&bars.q_empty[i], 1);
+        tc::bar_init(&bars.d_full[i], 1);
+        tc::bar_init(&bars.d_empty[i], 1);
+        tc::bar_init(&bars.stat_full[i], 32);
+        tc::bar_init(&bars.stat_empty[i], 256);
+      }
+      tc::bar_init(&bars.scores, 1);
+      tc::bar_init(&bars.probs, 256);
+      tc::bar_init(&bars.dprobs, 1);
+      tc::bar_init(&bars.dscores, 256);
+      tc::bar_init(&bars.done, 1);
+      tc::bar_init(&bars.cut, 1);
+      tc::bar_init(&bars.drain, 1);
+      bars.failed = 0;
+      tc::fence_bar_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc(&bars.tmem, 512);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bars.tmem;  // S, dP, dV, dK
+
+  if (warp >= kCopyWarp) {
+    tc::leave_registers<kOtherRegisters>();
+    if (warp == kCopyWarp && all > 0) {
+      const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+      int cut_phase = 0, n = 0, parts = 0;
+      bool ok = true;
+      if (lane == 0) {
+        copy_tile<DP>(sk, &maps.k, &bars.kv, kh, k_token + j0, ks.seq);
+        copy_tile<DP>(sv, &maps.v, &bars.kv, kh, k_token + j0, ks.seq);
+      }
+      for (; n < all && ok; ++n) {
+        const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile, head = kh * G + g;
+        for (int side = 0; side < 2 && ok; ++side) {
+          uint64_t *const full = side ? &bars.d_full[slot] : &bars.q_full[slot];
+          if (n >= 2)
+            ok = __all_sync(0xffffffffu, tc::bar_wait(side ? &bars.d_empty[slot] : &bars.q_empty[slot],
+                                                      (n / 2 - 1) & 1, failed));
+          if (!ok) break;
+          unsigned char *const to = (side ? sd : sq) + slot * tile_bytes<DP>();
+          const CUtensorMap *const map = side ? &maps.dout : &maps.q;
+          if (q0 + kTile > nq)
+            ok = copy_tile_cut<DP>(to, map, full, &bars.cut, &cut_phase, head, q_token + q0, qs.seq, nq - q0, failed);
+          else if (lane == 0)
+            copy_tile<DP>(to, map, full, head, q_token + q0, qs.seq);
+          __syncwarp();
+          if (ok) ++parts;
+        }
+      }
+      if (*failed) {
+        int unseen = 0;
+        tc::bar_wait(&bars.kv, 0, &unseen);
+        for (int i = max(0, parts - 4); i < parts; ++i)
+          tc::bar_wait(i & 1 ? &bars.d_full[i / 2 & 1] : &bars.q_full[i / 2 & 1], (i / 4) & 1, &unseen);
+      }
+    } else if (warp == kMmaWarp) {
+      if (lane == 0 && all > 0) {
+        constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
+        const uint32_t k0 = tc::smem_addr(sk), v0 = tc::smem_addr(sv), q0 = tc::smem_addr(sq), d0 = tc::smem_addr(sd);
+        const uint32_t t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + DP;
+        const auto scores = [&](int n) {
+          if (!tc::bar_wait(&bars.q_full[n & 1], (n / 2) & 1, failed)) return false;
+          tc::mma_rows<DP>(t_s, k0, kBlock, q0 + (n & 1) * tile_bytes<DP>(), kBlock, by_rows);
+          tc::commit(&bars.scores);
+          return true;
+        };
+        const auto dprobs = [&](int n) {
+          if (!tc::bar_wait(&bars.d_full[n & 1], (n / 2) & 1, failed)) return false;
+          tc::mma_rows<DP>(t_dp, v0, kBlock, d0 + (n & 1) * tile_bytes<DP>(), kBlock, by_rows);
+          tc::commit(&bars.dprobs);
+          return true;
+        };
+        bool ok = tc::bar_wait(&bars.kv, 0, failed) && scores(0) && dprobs(0);
+        for (int n = 0; n < all && ok; ++n) {
+          ok = tc::bar_wait(&bars.probs, n & 1, failed);
+          if (!ok) break;
+          tc::fence_after();
+          tc::mma_sums<kTile>(t_dv, t_s, kHalf, kHalf, d0 + (n & 1) * tile_bytes<DP>(), kBlock, by_cols, n > 0);
+          tc::commit(&bars.d_empty[n & 1]);
+          if (n + 1 < all) ok = scores(n + 1);
+          ok = ok && tc::bar_wait(&bars.dscores, n & 1, failed);
+          if (!ok) break;
+          tc::fence_after();
+          tc::mma_sums<kTile>(t_dk, t_dp, kHalf, kHalf, q0 + (n & 1) * tile_bytes<DP>(), kBlock, by_cols, n > 0);
+          tc::commit(&bars.q_empty[n & 1]);
+          if (n + 1 < all) ok = dprobs(n + 1);
+        }
+        tc::commit(&bars.done);
+        tc::commit(&bars.drain);
+        int unseen = 0;
+        tc::bar_wait(&bars.drain, 0, &unseen);
+      }
+      __syncwarp();
+    } else if (warp == kStatWarp) {
+      const float up = std::is_same<T, __half>::value ? kHalfP : 0.f;
+      for (int n = 0; n < all; ++n) {
+        const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile;
+        const int64_t place = (int64_t)(kh * G + g) * c.rows + qs.row;
+        float lse[4], delta[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = q0 + lane + 32 * x;
+          lse[x] = i < nq ? c.lse[place + i] * kLog2e : INFINITY;
+          if (lse[x] == -INFINITY) lse[x] = INFINITY;  // a row that sees nothing: its probabilities are zero
+          delta[x] = i < nq ? c.delta[place + i] : 0.f;
+        }
+        if (n >= 2 && !__all_sync(0xffffffffu, tc::bar_wait(&bars.stat_empty[slot], (n / 2 - 1) & 1, failed))) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          bars.lse[slot][lane + 32 * x] = lse[x] - up;
+          bars.delta[slot][lane + 32 * x] = delta[x];
+        }
+        tc::bar_arrive(&bars.stat_full[slot]);
+      }
+    }
+  } else {
+    tc::take_registers<kRowRegisters>();
+    const int w = warp >> 2, j = j0 + (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
+    const float cs = c.scale_log2, ds = ds_scale<T>(c);
+    const float ds_by_p = std::is_same<T, __half>::value ? ds * exp2f(-kHalfP) : 1.f;
+    const uint64_t seed = DROP ? c.draws() : 0;
+    bool ok = true;
+    for (int n = 0; n < all; ++n) {
+      const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile + w * kHalf;
+      uint64_t kept[4];  // of the four keys whose draws are shared, for 64 queries
+      if (DROP) {
+        uint64_t own = 0;
+#pragma unroll
+        for (int x = 0; x < kHalf; x += 4) {
+          // this lane draws for one of four queries, for four keys
+          const uint64_t z = dropout_draw(
+              dropout_row(seed, qs.row + q0 + x + (lane & 3), c.heads, kh * G + g), j);
+          uint32_t bits = 0;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) bits |= draw_lane(z, y) >= c.drop ? 1u << y : 0u;
+          own |= (uint64_t)bits << x;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) kept[y] = __shfl_sync(0xffffffffu, own, (lane & ~3) + y) >> (lane & 3);
+      }
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.stat_full[slot], (n / 2) & 1, failed) &&
+                                       tc::bar_wait(&bars.scores, n & 1, failed));
+      if (!ok) break;
+      tc::fence_after();
+      float p[kHalf];
+      tc::load32(s_at, p);
+      tc::load32(s_at + 32, p + 32);
+      tc::wait_loads();
+#pragma unroll
+      for (int x = 0; x < kHalf; x += 4) {
+        const float4 l = *reinterpret_cast<const float4 *>(&bars.lse[slot][w * kHalf + x]);
+        p[x] = tc::exp2_fast(fmaf(p[x], cs, -l.x));
+        p[x + 1] = tc::exp2_fast(fmaf(p[x + 1], cs, -l.y));
+        p[x + 2] = tc::exp2_fast(fmaf(p[x + 2], cs, -l.z));
+        p[x + 3] = tc::exp2_fast(fmaf(p[x + 3], cs, -l.w));
+      }
+      if (c.causal) {
+        const int lo = j - (nk - nq) - q0;  // the first query that sees this key
+        if (__any_sync(0xffffffffu, lo > 0))
+#pragma unroll
+          for (int x = 0; x < kHalf; ++x) p[x] = x >= lo ? p[x] : 0.f;
+      }
+      {
+        uint32_t out[32];
+#pragma unroll
+        for (int x = 0; x < kHalf; x += 2) {
+          const float a = !DROP || (kept[x & 3] >> (x & ~3) & 1) ? p[x] : 0.f;
+          const float b = !DROP || (kept[(x + 1) & 3] >> (x & ~3) & 1) ? p[x + 1] : 0.f;
+          out[x / 2] = pack2<T>(a, b);
+        }
+        tc::store32(s_at, out);
+      }
+      tc::wait_stores();
+      tc::fence_before();
+      tc::bar_arrive(&bars.probs);
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs, n & 1, failed));
+      if (!ok) break;
+      tc::fence_after();
+      float t[kHalf];
+      tc::load32(dp_at, t);
+      tc::load32(dp_at + 32, t + 32);
+      tc::wait_loads();
+      {
+        uint32_t out[32];
+#pragma unroll
+        for (int x = 0; x < kHalf; x += 4) {
+          const float4 d = *reinterpret_cast<const float4 *>(&bars.delta[slot][w * kHalf + x]);
+          const float dd[4] = {d.x, d.y, d.z, d.w};
+          float r[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float v = t[x + y];
+            if (DROP) v = kept[y] >> x & 1 ? v * c.keep_scale : 0.f;
+            r[y] = p[x + y] * (std::is_same<T, __half>::value ? (v - dd[y]) * ds_by_p : v - dd[y]);
+          }
+          out[x / 2] = pack2<T>(r[0], r[1]);
+          out[x / 2 + 1] = pack2<T>(r[2], r[3]);
+        }
+        tc::store32(dp_at, out);
+      }
+      tc::wait_stores();
+      tc::fence_before();
+      tc::bar_arrive(&bars.dscores);
+      tc::bar_arrive(&bars.stat_empty[slot]);
+    }
+    if (ok && all > 0) {
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed));
+      tc::fence_after();
+    }
+    const Strided &to = w ? c.dv : c.dk;  // a warpgroup each
+    if (ok && to.p) {
+      T *row = nullptr;
+      if (j < ks.cover)
+        row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
+              kh * to.head;
+      const float factor = w ? (std::is_same<T, __half>::value ? exp2f(-kHalfP) : 1.f) * c.keep_scale : c.scale / ds;
+      store_sums<T, DP>(tmem + lanes + 2 * kTile + (w ? 0 : DP), row, factor, c.d, all > 0, j >= nk);
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && bars.failed) g_attention_failed = 1;
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::tmem_free(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ queries
+
+struct QueryBars {
+  uint64_t qd, k_full[3], k_empty[3], v_full[2], v_empty[2];
+  uint64_t scores[2], read[2], dprobs[2], dscores[2], done, cut, drain;
+  uint32_t tmem;
+  int failed;
+};
+
+template <int DP>
+constexpr size_t queries_smem() { return 1024 + (size_t)7 * tile_bytes<DP>(); }
+
+// A tile of 128 queries of one head, past which the keys stream:
+//   S = Q K^T,  P = exp2(S - lse),  dP = dO V^T,  dS = P (dP - delta),  dQ += dS K.
+// Scores and dP take turns in three buffers of tensor memory (S(n) in 2n mod 3,
+// dP(n) in 2n+1 mod 3), so that S(n+1) is there before the rows are done with n.
+// Order of the products: dP(n+1), dQ(n), S(n+2).
+template <typename T, int DP, bool DROP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_backward_queries(const AttnCall c, const __grid_constant__ TileMaps maps) {
+  extern __shared__ unsigned char raw[];
+  __shared__ QueryBars bars;
+  unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<DP>();
+  unsigned char *const sk = sd + tile_bytes<DP>(), *const sv = sk + 3 * tile_bytes<DP>();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int *const failed = &bars.failed;
+
+  const int head = blockIdx.x % c.heads, kh = head / c.group;
+  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, kTile, blockIdx.x / c.heads, c.causal);
+  if (at.s < 0) return;
+  const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
+  const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
+  const int i0 = at.tile * kTile, nq = qs.valid, nk = ks.valid;
+  const int last = min(i0 + kTile, nq) - 1;
+  const int all = i0 < nq ? (max(0, seen_keys(c.causal, last, nq, nk)) + kTile - 1) / kTile : 0;
+
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      tc::bar_init(&bars.qd, 2);
+      for (int i = 0; i < 3; ++i) {
+        tc::bar_init(&bars.k_full[i], 1);
+        tc::bar_init(&bars.k_empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        tc::bar_init(&bars.v_full[i], 1);
+        tc::bar_init(&bars.v_empty[i], 1);
+        tc::bar_init(&bars.scores[i], 1);
+        tc::bar_init(&bars.read[i], 256);
+        tc::bar_init(&bars.dprobs[i], 1);
+        tc::bar_init(&bars.dscores[i], 256);
+      }
+      tc::bar_init(&bars.done, 1);
+      tc::bar_init(&bars.cut, 1);
+      tc::bar_init(&bars.drain, 1);
+      bars.failed = 0;
+      tc::fence_bar_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc(&bars.tmem, 512);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bars.tmem;  // three buffers, dQ
+
+  if (warp >= kCopyWarp) {
+    tc::leave_registers<kOtherRegisters>();
+    if (warp == kCopyWarp && all > 0) {
+      const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+      int cut_phase = 0, ks_done = 0, vs_done = 0;
+      bool ok = true;
+      if (lane == 0) {
+        copy_tile<DP>(sq, &maps.q, &bars.qd, head, q_token + i0, qs.seq);
+        copy_tile<DP>(sd, &maps.dout, &bars.qd, head, q_token + i0, qs.seq);
+      }
+      for (int n = 0; n < all && ok; ++n) {
+        if (n >= 3) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[n % 3], (n / 3 - 1) & 1, failed));
+        if (!ok) break;
+        unsigned char *const to = sk + n % 3 * tile_bytes<DP>();
+        if ((n + 1) * kTile > nk)
+          ok = copy_tile_cut<DP>(to, &maps.k, &bars.k_full[n % 3], &bars.cut, &cut_phase, kh, k_token + n * kTile,
+                                 ks.seq, nk - n * kTile, failed);
+        else if (lane == 0)
+          copy_tile<DP>(to, &maps.k, &bars.k_full[n % 3], kh, k_token + n * kTile, ks.seq);
+        __syncwarp();
+        if (!ok) break;
+        ++ks_done;
+        if (n >= 2) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.v_empty[n & 1], (n / 2 - 1) & 1, failed));
+        if (!ok) break;
+        if (lane == 0)
+          copy_tile<DP>(sv + (n & 1) * tile_bytes<DP>(), &maps.v, &bars.v_full[n & 1], kh, k_token + n * kTile, ks.seq);
+        __syncwarp();
+        ++vs_done;
+      }
+      if (*failed) {
+        int unseen = 0;
+        tc::bar_wait(&bars.qd, 0, &unseen);
+        for (int i = max(0, ks_done - 3); i < ks_done; ++i) tc::bar_wait(&bars.k_full[i % 3], (i / 3) & 1, &unseen);
+        for (int i = max(0, vs_done - 2); i < vs_done; ++i) tc::bar_wait(&bars.v_full[i & 1], (i / 2) & 1, &unseen);
+      }
+    } else if (warp == kMmaWarp) {
+      if (lane == 0 && all > 0) {
+        constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
+        const uint32_t q0 = tc::smem_addr(sq), d0 = tc::smem_addr(sd), k0 = tc::smem_addr(sk), v0 = tc::smem_addr(sv);
+        const auto scores = [&](int n) {
+          if (!tc::bar_wait(&bars.k_full[n % 3], (n / 3) & 1, failed)) return false;
+          tc::mma_rows<DP>(tmem + 2 * n % 3 * kTile, q0, kBlock, k0 + n % 3 * tile_bytes<DP>(), kBlock, by_rows);
+          tc::commit(&bars.scores[n & 1]);
+          return true;
+        };
+        const auto dprobs = [&](int n) {
+          if (!tc::bar_wait(&bars.v_full[n & 1], (n / 2) & 1, failed)) return false;
+          tc::mma_rows<DP>(tmem + (2 * n + 1) % 3 * kTile, d0, kBlock, v0 + (n & 1) * tile_bytes<DP>(), kBlock, by_rows);
+          tc::commit(&bars.dprobs[n & 1]);
+          tc::commit(&bars.v_empty[n & 1]);
+          return true;
+        };
+        bool ok = tc::bar_wait(&bars.qd, 0, failed) && scores(0) && dprobs(0) && (all < 2 || scores(1));
+        for (int n = 0; n < all && ok; ++n) {
+          if (n + 1 < all) {
+            ok = tc::bar_wait(&bars.read[n & 1], (n / 2) & 1, failed);
+            tc::fence_after();
+            ok = ok && dprobs(n + 1);
+          }
+          ok = ok && tc::bar_wait(&bars.dscores[n & 1], (n / 2) & 1, failed);
+          if (!ok) break;
+          tc::fence_after();
+          tc::mma_sums<kTile>(tmem + 3 * kTile, tmem + (2 * n + 1) % 3 * kTile, kHalf, kHalf,
+                              k0 + n % 3 * tile_bytes<DP>(), kBlock, by_cols, n > 0);
+          tc::commit(&bars.k_empty[n % 3]);
+          if (n + 2 < all) ok = scores(n + 2);
+        }
+        tc::commit(&bars.done);
+        tc::commit(&bars.drain);
+        int unseen = 0;
+        tc::bar_wait(&bars.drain, 0, &unseen);
+      }
+      __syncwarp();
+    }
+  } else {
+    tc::take_registers<kRowRegisters>();
+    const int w = warp >> 2, i = i0 + (warp & 3) * 32 + lane;
+    const uint32_t at_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const float cs = c.scale_log2, ds = ds_scale<T>(c);
+    float lse = 0.f, delta = 0.f;
+    int lim = 0;
+    if (i < nq) {
+      const int64_t place = (int64_t)head * c.rows + qs.row + i;
+      lse = c.lse[place] * kLog2e;
+      delta = c.delta[place];
+      if (lse == -INFINITY)
+        lse = 0.f;
+      else
+        lim = max(0, seen_keys(c.causal, i, nq, nk));
+    }
+    const uint64_t draw = DROP ? dropout_row(c.draws(), qs.row + i, c.heads, head) : 0;
+    bool ok = true;
+    for (int n = 0; n < all; ++n) {
+      const int b = n & 1, phase = (n / 2) & 1, key0 = n * kTile + w * kHalf;
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[b], phase, failed));
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t s_at = at_lane + 2 * n % 3 * kTile + w * kHalf, dp_at = at_lane + (2 * n + 1) % 3 * kTile + w * kHalf;
+      float p[kHalf];
+      tc::load32(s_at, p);
+      tc::load32(s_at + 32, p + 32);
+      tc::wait_loads();
+      tc::fence_before();
+      tc::bar_arrive(&bars.read[b]);
+#pragma unroll
+      for (int x = 0; x < kHalf; ++x) p[x] = tc::exp2_fast(fmaf(p[x], cs, -lse));
+      const int left = lim - key0;
+      const bool cut = __any_sync(0xffffffffu, left < kHalf);
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs[b], phase, failed));
+      if (!ok) break;
+      tc::fence_after();
+      float t[kHalf];
+      tc::load32(dp_at, t);
+      tc::load32(dp_at + 32, t + 32);
+      tc::wait_loads();
+      if (DROP) {
+#pragma unroll
+        for (int x = 0; x < kHalf; x += 4) {
+          const uint64_t z = dropout_draw(draw, key0 + x);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) t[x + y] = draw_lane(z, y) >= c.drop ? t[x + y] * c.keep_scale : 0.f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kHalf; ++x)
+        t[x] = p[x] * (std::is_same<T, __half>::value ? (t[x] - delta) * ds : t[x] - delta);
+      if (cut)
+#pragma unroll
+        for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
+      uint32_t out[32];
+#pragma unroll
+      for (int x = 0; x < kHalf; x += 2) out[x / 2] = pack2<T>(t[x], t[x + 1]);
+      tc::store32(dp_at, out);
+      tc::wait_stores();
+      tc::fence_before();
+      tc::bar_arrive(&bars.dscores[b]);
+    }
+    if (ok && all > 0) {
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed));
+      tc::fence_after();
+    }
+    if (ok) {
+      T *row = nullptr;
+      const int from = w * (DP / 2);  // a warpgroup stores half of the columns
+      if (i < qs.cover)
+        row = static_cast<T *>(c.dq.p) +
+              (c.q_offsets ? (qs.row + i) * c.dq.token : qs.seq * c.dq.seq + i * c.dq.token) + head * c.dq.head + from;
+      store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, c.scale / ds, c.d - from, all > 0, lim == 0);
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && bars.failed) g_attention_failed = 1;
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::tmem_free(tmem, 512);
+  }
+}
+
+template <typename T, int DP, bool DROP>
+cudaError_t backward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
+  if (c.dk.p || c.dv.p) {
+    const auto kern = tile_backward_keys<T, DP, DROP>;
+    cudaError_t e = allow_smem(kern, keys_smem<DP>());
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = tiles_of(c.k_offsets != nullptr, c.sequences, c.k_tokens, 1, kTile) * c.key_heads;
+    e = launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, keys_smem<DP>(), false, s, c, m);
+    if (e != cudaSuccess) return e;
+  }
+  if (!c.dq.p) return cudaSuccess;
+  const auto kern = tile_backward_queries<T, DP, DROP>;
+  const cudaError_t e = allow_smem(kern, queries_smem<DP>());
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, kTile) * c.heads;
+  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, queries_smem<DP>(), false, s, c, m);
+}
+
+template <typename T>
+cudaError_t backward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
+  if (c.d <= 64) return c.drop ? backward_launch<T, 64, true>(c, m, s) : backward_launch<T, 64, false>(c, m, s);
+  return c.drop ? backward_launch<T, 128, true>(c, m, s) : backward_launch<T, 128, false>(c, m, s);
+}
+
+}  // namespace
+
+bool tile_backward_fits(const AttnCall &c, int type) {
+  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
+  return tiles_fit(c, type) && even(c.q, c.heads, c.q_tokens, qn) && even(c.dout, c.heads, c.q_tokens, qn) &&
+         even(c.k, c.key_heads, c.k_tokens, kn) && even(c.v, c.key_heads, c.k_tokens, kn) &&
+         (!c.dq.p || even(c.dq, c.heads, c.q_tokens, qn)) && (!c.dk.p || even(c.dk, c.key_heads, c.k_tokens, kn)) &&
+         (!c.dv.p || even(c.dv, c.key_heads, c.k_tokens, kn));
+}
+
+cudaError_t tile_backward_launch(const AttnCall &c, int type, cudaStream_t s) {
+  TileMaps m = {};
+  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
+  if (!map_of(&m.q, type, c.q, c.d, c.heads, c.q_tokens, qn) ||
+      !map_of(&m.dout, type, c.dout, c.d, c.heads, c.q_tokens, qn) ||
+      !map_of(&m.k, type, c.k, c.d, c.key_heads, c.k_tokens, kn) ||
+      !map_of(&m.v, type, c.v, c.d, c.key_heads, c.k_tokens, kn))
+    return cudaErrorInvalidValue;
+  return type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, m, s) : backward_typed<__half>(c, m, s);
+}
+
+cudaError_t tile_backward_failed(int *flag, cudaStream_t s) { return read_failed(flag, s); }
+
+}  // namespace snack

@@ -1,0 +1,292 @@
+// The forward call of the attention on tcgen05.
+#include "attention_tiles.cuh"
+
+namespace snack {
+namespace {
+
+constexpr int kForwardSlots = 4;  // tiles of keys and values in flight, in turn
+
+template <int DP>
+constexpr size_t tile_forward_smem() { return 1024 + (size_t)(2 + kForwardSlots) * tile_bytes<DP>(); }
+
+struct ForwardBars {
+  uint64_t q[2], full[kForwardSlots], empty[kForwardSlots], scores[2], probs[2], done[2], cut, drain;
+  uint32_t tmem;
+  int failed;
+};
+
+// Two tiles of 128 query rows share the keys: two heads of a group over the
+// same tokens where the group is even, else neighbouring tokens of one head.
+// While the rows of one tile are exponentiated, the products of the other run.
+//
+// The accumulated row is multiplied down only when the maximum has grown by
+// more than 2^8 since the last time: until then probabilities are up to 2^8
+// fold, which the 32-bit sums hold as well.
+template <typename T, int DP, bool DROP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_forward(const AttnCall c, const __grid_constant__ TileMaps maps) {
+  extern __shared__ unsigned char raw[];
+  __shared__ ForwardBars bars;
+  unsigned char *const sq = align1024(raw), *const ring = sq + 2 * tile_bytes<DP>();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int *const failed = &bars.failed;
+
+  const bool by_heads = c.group % 2 == 0;
+  const int units = by_heads ? c.heads / 2 : c.heads, u = blockIdx.x % units;
+  const int rows = by_heads ? kTile : 2 * kTile;
+  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, rows, blockIdx.x / units, c.causal);
+  if (at.s < 0) return;
+  const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
+  const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
+  const int nq = qs.valid, nk = ks.valid;
+  int first[2], steps[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    first[t] = at.tile * rows + (by_heads ? 0 : t * kTile);
+    const int last = min(first[t] + kTile, nq) - 1;
+    steps[t] = first[t] < nq ? (max(0, seen_keys(c.causal, last, nq, nk)) + kTile - 1) / kTile : 0;
+  }
+  const int all = max(steps[0], steps[1]);
+  const int head0 = by_heads ? 2 * u : u, kh = head0 / c.group;
+
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        tc::bar_init(&bars.q[i], 1);
+        tc::bar_init(&bars.scores[i], 1);
+        tc::bar_init(&bars.probs[i], 128);
+        tc::bar_init(&bars.done[i], 1);
+      }
+      for (int i = 0; i < kForwardSlots; ++i) {
+        tc::bar_init(&bars.full[i], 1);
+        tc::bar_init(&bars.empty[i], 1);
+      }
+      tc::bar_init(&bars.cut, 1);
+      tc::bar_init(&bars.drain, 1);
+      bars.failed = 0;
+      tc::fence_bar_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc(&bars.tmem, 512);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bars.tmem;  // scores of the two tiles, then their sums
+  if (warp >= kCopyWarp) {
+  tc::leave_registers<kOtherRegisters>();
+  if (warp == kCopyWarp) {
+    const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+    int cut_phase = 0, item = 0;
+    bool ok = true;
+    if (lane == 0)
+      for (int t = 0; t < 2; ++t)
+        if (steps[t])
+          copy_tile<DP>(sq + t * tile_bytes<DP>(), &maps.q, &bars.q[t], head0 + (by_heads ? t : 0), q_token + first[t],
+                        qs.seq);
+    for (int j = 0; j < all && ok; ++j) {
+      for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
+        const int slot = item % kForwardSlots;
+        if (item >= kForwardSlots)
+          ok = __all_sync(0xffffffffu,
+                          tc::bar_wait(&bars.empty[slot], (item / kForwardSlots - 1) & 1, failed));
+        if (!ok) break;
+        unsigned char *const to = ring + slot * tile_bytes<DP>();
+        const int token = k_token + j * kTile;
+        if (kv && (j + 1) * kTile > nk)
+          ok = copy_tile_cut<DP>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq,
+                                 nk - j * kTile, failed);
+        else if (lane == 0)
+          copy_tile<DP>(to, kv ? &maps.v : &maps.k, &bars.full[slot], kh, token, ks.seq);
+        __syncwarp();
+      }
+    }
+    // copies in flight end before the block does, also where a wait has given up
+    for (int i = max(0, item - kForwardSlots); i < item && *failed; ++i) {
+      int unseen = 0;
+      tc::bar_wait(&bars.full[i % kForwardSlots], (i / kForwardSlots) & 1, &unseen);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && all > 0) {
+      constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
+      const uint32_t q0 = tc::smem_addr(sq), r0 = tc::smem_addr(ring);
+      const auto tile_at = [&](int item) { return r0 + (uint32_t)(item % kForwardSlots) * tile_bytes<DP>(); };
+      const auto wait_item = [&](int item) {
+        return tc::bar_wait(&bars.full[item % kForwardSlots], (item / kForwardSlots) & 1, failed);
+      };
+      bool ok = wait_item(0);
+      for (int t = 0; t < 2 && ok; ++t)
+        if (steps[t]) {
+          ok = tc::bar_wait(&bars.q[t], 0, failed);
+          tc::fence_after();
+          if (ok) tc::mma_rows<DP>(tmem + t * kTile, q0 + t * tile_bytes<DP>(), kBlock, tile_at(0), kBlock, by_rows);
+          tc::commit(&bars.scores[t]);
+        }
+      tc::commit(&bars.empty[0]);
+      for (int j = 0; j < all && ok; ++j) {
+        ok = wait_item(2 * j + 1) && (j + 1 >= all || wait_item(2 * j + 2));
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j >= steps[t]) continue;
+          ok = tc::bar_wait(&bars.probs[t], j & 1, failed);
+          if (!ok) break;
+          tc::fence_after();
+          tc::mma_sums<kTile>(tmem + 2 * kTile + t * DP, tmem + t * kTile, kTile, 0, tile_at(2 * j + 1), kBlock,
+                              by_cols, j > 0);
+          if (j + 1 < steps[t]) {
+            tc::mma_rows<DP>(tmem + t * kTile, q0 + t * tile_bytes<DP>(), kBlock, tile_at(2 * j + 2), kBlock, by_rows);
+            tc::commit(&bars.scores[t]);
+          } else {
+            tc::commit(&bars.done[t]);
+          }
+        }
+        tc::commit(&bars.empty[(2 * j + 1) % kForwardSlots]);
+        if (j + 1 < all) tc::commit(&bars.empty[(2 * j + 2) % kForwardSlots]);
+      }
+      tc::commit(&bars.drain);
+      int unseen = 0;
+      tc::bar_wait(&bars.drain, 0, &unseen);
+    }
+    __syncwarp();
+  }
+  } else {
+    tc::take_registers<kRowRegisters>();
+    const int t = warp >> 2, head = head0 + (by_heads ? t : 0);
+    const int i = first[t] + (warp & 3) * 32 + lane;  // token of this thread's row
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
+    const int lim = i < nq ? max(0, seen_keys(c.causal, i, nq, nk)) : 0;
+    const float cs = c.scale_log2;
+    uint64_t draw = 0;
+    if (DROP) draw = dropout_row(c.draws(), qs.row + i, c.heads, head);
+    float m = -INFINITY, sum = 0.f;
+    bool ok = true;
+    for (int j = 0; j < steps[t]; ++j) {
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
+      if (!ok) break;
+      tc::fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int x = 0; x < kTile; x += 32) tc::load32(s_at + x, s + x);
+      tc::wait_loads();
+      const int left = lim - j * kTile;  // keys of this tile that the row sees
+      if (__any_sync(0xffffffffu, left < kTile)) {
+#pragma unroll
+        for (int x = 0; x < kTile; ++x) s[x] = x < left ? s[x] : -INFINITY;
+      }
+      float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int x = 4; x < kTile; ++x) top[x & 3] = fmaxf(top[x & 3], s[x]);
+      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const float grown = fmaxf(m, most);
+      const bool up = j == 0 || (grown - m) * cs > 8.f;
+      if (j > 0 && __any_sync(0xffffffffu, up)) {
+        const float shrink = up ? tc::exp2_fast((m - grown) * cs) : 1.f;
+        sum *= shrink;
+#pragma unroll
+        for (int x = 0; x < DP; x += 32) {
+          float o[32];
+          tc::load32(o_at + x, o);
+          tc::wait_loads();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= shrink;
+          tc::store32(o_at + x, reinterpret_cast<const uint32_t *>(o));
+        }
+      }
+      if (up) m = grown;
+      const float off = m == -INFINITY ? 0.f : -m * cs;
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < kTile; x += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          float a = tc::exp2_fast(fmaf(s[x + e], cs, off)), b = tc::exp2_fast(fmaf(s[x + e + 1], cs, off));
+          part[e & 2] += a;
+          part[(e & 2) + 1] += b;
+          if (DROP) {
+            s[x + e] = a;
+            s[x + e + 1] = b;
+          } else {
+            p[e / 2] = pack2<T>(a, b);
+          }
+        }
+        if (DROP) {
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const uint64_t z = dropout_draw(draw, j * kTile + x + e);
+            float k[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) k[y] = draw_lane(z, y) >= c.drop ? s[x + e + y] : 0.f;
+            p[e / 2] = pack2<T>(k[0], k[1]);
+            p[e / 2 + 1] = pack2<T>(k[2], k[3]);
+          }
+        }
+        tc::store32(s_at + x / 2, p);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      tc::wait_stores();
+      tc::fence_before();
+      tc::bar_arrive(&bars.probs[t]);
+    }
+    if (ok && steps[t]) {
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));
+      tc::fence_after();
+    }
+    if (ok) {
+      const bool mine = i < qs.cover;
+      T *row = nullptr;
+      if (mine)
+        row = static_cast<T *>(c.out.p) + (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) +
+              head * c.out.head;
+      store_sums<T, DP>(o_at, row, c.keep_scale / sum, c.d, steps[t] > 0, sum == 0.f);
+      if (mine)
+        c.lse[(int64_t)head * c.rows + qs.row + i] = sum == 0.f ? -INFINITY : m * c.scale + logf(sum);
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && bars.failed) g_attention_failed = 1;
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::tmem_free(tmem, 512);
+  }
+}
+
+}  // namespace
+
+bool tile_forward_fits(const AttnCall &c, int type) {
+  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
+  return tiles_fit(c, type) && even(c.q, c.heads, c.q_tokens, qn) && even(c.k, c.key_heads, c.k_tokens, kn) &&
+         even(c.v, c.key_heads, c.k_tokens, kn) && even(c.out, c.heads, c.q_tokens, qn);
+}
+
+template <typename T, int DP, bool DROP>
+static cudaError_t forward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
+  const bool by_heads = c.group % 2 == 0;
+  const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, by_heads ? kTile : 2 * kTile) *
+                         (by_heads ? c.heads / 2 : c.heads);
+  const auto kern = tile_forward<T, DP, DROP>;
+  const cudaError_t e = allow_smem(kern, tile_forward_smem<DP>());
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, tile_forward_smem<DP>(), false, s, c, m);
+}
+
+template <typename T>
+static cudaError_t forward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
+  if (c.d <= 64) return c.drop ? forward_launch<T, 64, true>(c, m, s) : forward_launch<T, 64, false>(c, m, s);
+  return c.drop ? forward_launch<T, 128, true>(c, m, s) : forward_launch<T, 128, false>(c, m, s);
+}
+
+cudaError_t tile_forward_launch(const AttnCall &c, int type, cudaStream_t s) {
+  TileMaps m = {};
+  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
+  if (!map_of(&m.q, type, c.q, c.d, c.heads, c.q_tokens, qn) ||
+      !map_of(&m.k, type, c.k, c.d, c.key_heads, c.k_tokens, kn) ||
+      !map_of(&m.v, type, c.v, c.d, c.key_heads, c.k_tokens, kn))
+    return cudaErrorInvalidValue;
+  return type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, m, s) : forward_typed<__half>(c, m, s);
+}
+
+cudaError_t tile_forward_failed(int *flag, cudaStream_t s) { return read_failed(flag, s); }
+
+}  // namespace snack

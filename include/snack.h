@@ -546,6 +546,14 @@ snack_status snack_attention_backward(const snack_attention_args *args,
                                       void *stream);
 
 /*
+ * Read and clear the current device's flag of the attention calls: *flag = 1
+ * if, since the last read, a kernel gave up a bounded wait on its own copies
+ * or products (the results of that call are then not to be trusted).
+ * Synchronises `stream`.
+ */
+snack_status snack_attention_error(int *flag, void *stream);
+
+/*
  * Dropout of n contiguous elements: y = residual + M * x (residual NULL: M * x),
  * x of x_type, residual and y of y_type.  With T = round(65536 * p), M is 0
  * for element e where the 16 bits from 16 * (e mod 4) on of the SplitMix64 draw
