@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ KeyBars bars;
   unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<DP>();
   unsigned char *const sq = sv + tile_bytes<DP>(), *const sd = sq + 2 * tile_bytes<DP>();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
   const int kh = blockIdx.x % c.key_heads, G = c.group;
@@ -66,13 +66,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::bar_init(&bars.q_empty[i], 1);
         tc::bar_init(&bars.d_full[i], 1);
         tc::bar_init(&bars.d_empty[i], 1);
-        tc::bar_init(&bars.stat_full[i], 32);
-        tc::bar_init(&bars.stat_empty[i], 256);
+        tc::bar_init(&bars.stat_full[i], 1);
+        tc::bar_init(&bars.stat_empty[i], 8);
       }
       tc::bar_init(&bars.scores, 1);
-      tc::bar_init(&bars.probs, 256);
+      tc::bar_init(&bars.probs, 8);
       tc::bar_init(&bars.dprobs, 1);
-      tc::bar_init(&bars.dscores, 256);
+      tc::bar_init(&bars.dscores, 8);
       tc::bar_init(&bars.done, 1);
       tc::bar_init(&bars.cut, 1);
       tc::bar_init(&bars.drain, 1);
@@ -122,39 +122,61 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tc::bar_wait(i & 1 ? &bars.d_full[i / 2 & 1] : &bars.q_full[i / 2 & 1], (i / 4) & 1, &unseen);
       }
     } else if (warp == kMmaWarp) {
-      if (lane == 0 && all > 0) {
+      // the whole warp goes along, so that descriptors stay in uniform registers
+      if (all > 0) {
         constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
-        const uint32_t k0 = tc::smem_addr(sk), v0 = tc::smem_addr(sv), q0 = tc::smem_addr(sq), d0 = tc::smem_addr(sd);
+        constexpr uint32_t kStep = tile_bytes<DP>() / 16;
+        const bool leader = tc::elect_one();
+        const uint32_t k0 = tc::desc_rows(tc::smem_addr(sk)), v0 = tc::desc_rows(tc::smem_addr(sv));
+        const uint32_t q0 = tc::desc_rows(tc::smem_addr(sq)), d0 = tc::desc_rows(tc::smem_addr(sd));
+        const uint32_t q0c = tc::desc_columns(tc::smem_addr(sq), kBlock), d0c = tc::desc_columns(tc::smem_addr(sd), kBlock);
         const uint32_t t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + DP;
+        const auto wait = [&](uint64_t *bar, int phase) {
+          const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
+          tc::fence_after();
+          return done;
+        };
         const auto scores = [&](int n) {
-          if (!tc::bar_wait(&bars.q_full[n & 1], (n / 2) & 1, failed)) return false;
-          tc::mma_rows<DP>(t_s, k0, kBlock, q0 + (n & 1) * tile_bytes<DP>(), kBlock, by_rows);
-          tc::commit(&bars.scores);
-          return true;
+          const bool done = wait(&bars.q_full[n & 1], (n / 2) & 1);
+          if (done && leader) {
+            tc::mma_rows<DP>(t_s, k0, q0 + (n & 1) * kStep, kBlock, by_rows);
+            tc::commit(&bars.scores);
+          }
+          __syncwarp();
+          return done;
         };
         const auto dprobs = [&](int n) {
-          if (!tc::bar_wait(&bars.d_full[n & 1], (n / 2) & 1, failed)) return false;
-          tc::mma_rows<DP>(t_dp, v0, kBlock, d0 + (n & 1) * tile_bytes<DP>(), kBlock, by_rows);
-          tc::commit(&bars.dprobs);
-          return true;
+          const bool done = wait(&bars.d_full[n & 1], (n / 2) & 1);
+          if (done && leader) {
+            tc::mma_rows<DP>(t_dp, v0, d0 + (n & 1) * kStep, kBlock, by_rows);
+            tc::commit(&bars.dprobs);
+          }
+          __syncwarp();
+          return done;
         };
-        bool ok = tc::bar_wait(&bars.kv, 0, failed) && scores(0) && dprobs(0);
+        bool ok = wait(&bars.kv, 0) && scores(0) && dprobs(0);
         for (int n = 0; n < all && ok; ++n) {
-          ok = tc::bar_wait(&bars.probs, n & 1, failed);
+          ok = wait(&bars.probs, n & 1);
           if (!ok) break;
-          tc::fence_after();
-          tc::mma_sums<kTile>(t_dv, t_s, kHalf, kHalf, d0 + (n & 1) * tile_bytes<DP>(), kBlock, by_cols, n > 0);
-          tc::commit(&bars.d_empty[n & 1]);
+          if (leader) {
+            tc::mma_sums<kTile>(t_dv, t_s, kHalf, kHalf, d0c + (n & 1) * kStep, by_cols, n > 0);
+            tc::commit(&bars.d_empty[n & 1]);
+          }
+          __syncwarp();
           if (n + 1 < all) ok = scores(n + 1);
-          ok = ok && tc::bar_wait(&bars.dscores, n & 1, failed);
+          ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
-          tc::fence_after();
-          tc::mma_sums<kTile>(t_dk, t_dp, kHalf, kHalf, q0 + (n & 1) * tile_bytes<DP>(), kBlock, by_cols, n > 0);
-          tc::commit(&bars.q_empty[n & 1]);
+          if (leader) {
+            tc::mma_sums<kTile>(t_dk, t_dp, kHalf, kHalf, q0c + (n & 1) * kStep, by_cols, n > 0);
+            tc::commit(&bars.q_empty[n & 1]);
+          }
+          __syncwarp();
           if (n + 1 < all) ok = dprobs(n + 1);
         }
-        tc::commit(&bars.done);
-        tc::commit(&bars.drain);
+        if (leader) {
+          tc::commit(&bars.done);
+          tc::commit(&bars.drain);
+        }
         int unseen = 0;
         tc::bar_wait(&bars.drain, 0, &unseen);
       }
@@ -175,10 +197,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (n >= 2 && !__all_sync(0xffffffffu, tc::bar_wait(&bars.stat_empty[slot], (n / 2 - 1) & 1, failed))) break;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          bars.lse[slot][lane + 32 * x] = lse[x] - up;
-          bars.delta[slot][lane + 32 * x] = delta[x];
+          bars.lse[slot][lane + 32 * x] = up - lse[x];  // as they are added
+          bars.delta[slot][lane + 32 * x] = -delta[x];
         }
-        tc::bar_arrive(&bars.stat_full[slot]);
+        tc::bar_arrive_warp(&bars.stat_full[slot]);
       }
     }
   } else {
@@ -186,7 +208,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int w = warp >> 2, j = j0 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
-    const float cs = c.scale_log2, ds = ds_scale<T>(c);
+    const float ds = ds_scale<T>(c);
+    const float2 cs2 = make_float2(c.scale_log2, c.scale_log2);
     const float ds_by_p = std::is_same<T, __half>::value ? ds * exp2f(-kHalfP) : 1.f;
     const uint64_t seed = DROP ? c.draws() : 0;
     bool ok = true;
@@ -219,10 +242,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int x = 0; x < kHalf; x += 4) {
         const float4 l = *reinterpret_cast<const float4 *>(&bars.lse[slot][w * kHalf + x]);
-        p[x] = tc::exp2_fast(fmaf(p[x], cs, -l.x));
-        p[x + 1] = tc::exp2_fast(fmaf(p[x + 1], cs, -l.y));
-        p[x + 2] = tc::exp2_fast(fmaf(p[x + 2], cs, -l.z));
-        p[x + 3] = tc::exp2_fast(fmaf(p[x + 3], cs, -l.w));
+        const float2 a = tc::fma2(make_float2(p[x], p[x + 1]), cs2, make_float2(l.x, l.y));
+        const float2 b = tc::fma2(make_float2(p[x + 2], p[x + 3]), cs2, make_float2(l.z, l.w));
+        p[x] = tc::exp2_fast(a.x);
+        p[x + 1] = tc::exp2_fast(a.y);
+        p[x + 2] = tc::exp2_fast(b.x);
+        p[x + 3] = tc::exp2_fast(b.y);
       }
       if (c.causal) {
         const int lo = j - (nk - nq) - q0;  // the first query that sees this key
@@ -242,7 +267,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       tc::wait_stores();
       tc::fence_before();
-      tc::bar_arrive(&bars.probs);
+      tc::bar_arrive_warp(&bars.probs);
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs, n & 1, failed));
       if (!ok) break;
       tc::fence_after();
@@ -255,23 +280,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < kHalf; x += 4) {
           const float4 d = *reinterpret_cast<const float4 *>(&bars.delta[slot][w * kHalf + x]);
-          const float dd[4] = {d.x, d.y, d.z, d.w};
-          float r[4];
+          float v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            float v = t[x + y];
-            if (DROP) v = kept[y] >> x & 1 ? v * c.keep_scale : 0.f;
-            r[y] = p[x + y] * (std::is_same<T, __half>::value ? (v - dd[y]) * ds_by_p : v - dd[y]);
+            v[y] = t[x + y];
+            if (DROP) v[y] = kept[y] >> x & 1 ? v[y] * c.keep_scale : 0.f;
           }
-          out[x / 2] = pack2<T>(r[0], r[1]);
-          out[x / 2 + 1] = pack2<T>(r[2], r[3]);
+          const float2 u0 = tc::add2(make_float2(v[0], v[1]), make_float2(d.x, d.y));
+          const float2 u1 = tc::add2(make_float2(v[2], v[3]), make_float2(d.z, d.w));
+          float2 r0 = tc::mul2(make_float2(p[x], p[x + 1]), u0), r1 = tc::mul2(make_float2(p[x + 2], p[x + 3]), u1);
+          if constexpr (std::is_same<T, __half>::value) {
+            r0 = tc::mul2(r0, make_float2(ds_by_p, ds_by_p));
+            r1 = tc::mul2(r1, make_float2(ds_by_p, ds_by_p));
+          }
+          out[x / 2] = pack2<T>(r0.x, r0.y);
+          out[x / 2 + 1] = pack2<T>(r1.x, r1.y);
         }
         tc::store32(dp_at, out);
       }
       tc::wait_stores();
       tc::fence_before();
-      tc::bar_arrive(&bars.dscores);
-      tc::bar_arrive(&bars.stat_empty[slot]);
+      tc::bar_arrive_warp(&bars.dscores);
+      if (lane == 0) tc::bar_arrive(&bars.stat_empty[slot]);
     }
     if (ok && all > 0) {
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed));
@@ -320,7 +350,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ QueryBars bars;
   unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<DP>();
   unsigned char *const sk = sd + tile_bytes<DP>(), *const sv = sk + 3 * tile_bytes<DP>();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
   const int head = blockIdx.x % c.heads, kh = head / c.group;
@@ -343,9 +373,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::bar_init(&bars.v_full[i], 1);
         tc::bar_init(&bars.v_empty[i], 1);
         tc::bar_init(&bars.scores[i], 1);
-        tc::bar_init(&bars.read[i], 256);
+        tc::bar_init(&bars.read[i], 8);
         tc::bar_init(&bars.dprobs[i], 1);
-        tc::bar_init(&bars.dscores[i], 256);
+        tc::bar_init(&bars.dscores[i], 8);
       }
       tc::bar_init(&bars.done, 1);
       tc::bar_init(&bars.cut, 1);
@@ -397,39 +427,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int i = max(0, vs_done - 2); i < vs_done; ++i) tc::bar_wait(&bars.v_full[i & 1], (i / 2) & 1, &unseen);
       }
     } else if (warp == kMmaWarp) {
-      if (lane == 0 && all > 0) {
+      if (all > 0) {
         constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
-        const uint32_t q0 = tc::smem_addr(sq), d0 = tc::smem_addr(sd), k0 = tc::smem_addr(sk), v0 = tc::smem_addr(sv);
+        constexpr uint32_t kStep = tile_bytes<DP>() / 16;
+        const bool leader = tc::elect_one();
+        const uint32_t q0 = tc::desc_rows(tc::smem_addr(sq)), d0 = tc::desc_rows(tc::smem_addr(sd));
+        const uint32_t k0 = tc::desc_rows(tc::smem_addr(sk)), v0 = tc::desc_rows(tc::smem_addr(sv));
+        const uint32_t k0c = tc::desc_columns(tc::smem_addr(sk), kBlock);
+        const auto wait = [&](uint64_t *bar, int phase) {
+          const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
+          tc::fence_after();
+          return done;
+        };
         const auto scores = [&](int n) {
-          if (!tc::bar_wait(&bars.k_full[n % 3], (n / 3) & 1, failed)) return false;
-          tc::mma_rows<DP>(tmem + 2 * n % 3 * kTile, q0, kBlock, k0 + n % 3 * tile_bytes<DP>(), kBlock, by_rows);
-          tc::commit(&bars.scores[n & 1]);
-          return true;
+          const bool done = wait(&bars.k_full[n % 3], (n / 3) & 1);
+          if (done && leader) {
+            tc::mma_rows<DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep, kBlock, by_rows);
+            tc::commit(&bars.scores[n & 1]);
+          }
+          __syncwarp();
+          return done;
         };
         const auto dprobs = [&](int n) {
-          if (!tc::bar_wait(&bars.v_full[n & 1], (n / 2) & 1, failed)) return false;
-          tc::mma_rows<DP>(tmem + (2 * n + 1) % 3 * kTile, d0, kBlock, v0 + (n & 1) * tile_bytes<DP>(), kBlock, by_rows);
-          tc::commit(&bars.dprobs[n & 1]);
-          tc::commit(&bars.v_empty[n & 1]);
-          return true;
-        };
-        bool ok = tc::bar_wait(&bars.qd, 0, failed) && scores(0) && dprobs(0) && (all < 2 || scores(1));
-        for (int n = 0; n < all && ok; ++n) {
-          if (n + 1 < all) {
-            ok = tc::bar_wait(&bars.read[n & 1], (n / 2) & 1, failed);
-            tc::fence_after();
-            ok = ok && dprobs(n + 1);
+          const bool done = wait(&bars.v_full[n & 1], (n / 2) & 1);
+          if (done && leader) {
+            tc::mma_rows<DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep, kBlock, by_rows);
+            tc::commit(&bars.dprobs[n & 1]);
+            tc::commit(&bars.v_empty[n & 1]);
           }
-          ok = ok && tc::bar_wait(&bars.dscores[n & 1], (n / 2) & 1, failed);
+          __syncwarp();
+          return done;
+        };
+        bool ok = wait(&bars.qd, 0) && scores(0) && dprobs(0) && (all < 2 || scores(1));
+        for (int n = 0; n < all && ok; ++n) {
+          if (n + 1 < all) ok = wait(&bars.read[n & 1], (n / 2) & 1) && dprobs(n + 1);
+          ok = ok && wait(&bars.dscores[n & 1], (n / 2) & 1);
           if (!ok) break;
-          tc::fence_after();
-          tc::mma_sums<kTile>(tmem + 3 * kTile, tmem + (2 * n + 1) % 3 * kTile, kHalf, kHalf,
-                              k0 + n % 3 * tile_bytes<DP>(), kBlock, by_cols, n > 0);
-          tc::commit(&bars.k_empty[n % 3]);
+          if (leader) {
+            tc::mma_sums<kTile>(tmem + 3 * kTile, tmem + (2 * n + 1) % 3 * kTile, kHalf, kHalf, k0c + n % 3 * kStep,
+                                by_cols, n > 0);
+            tc::commit(&bars.k_empty[n % 3]);
+          }
+          __syncwarp();
           if (n + 2 < all) ok = scores(n + 2);
         }
-        tc::commit(&bars.done);
-        tc::commit(&bars.drain);
+        if (leader) {
+          tc::commit(&bars.done);
+          tc::commit(&bars.drain);
+        }
         int unseen = 0;
         tc::bar_wait(&bars.drain, 0, &unseen);
       }
@@ -439,7 +484,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::take_registers<kRowRegisters>();
     const int w = warp >> 2, i = i0 + (warp & 3) * 32 + lane;
     const uint32_t at_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float cs = c.scale_log2, ds = ds_scale<T>(c);
+    const float ds = ds_scale<T>(c);
     float lse = 0.f, delta = 0.f;
     int lim = 0;
     if (i < nq) {
@@ -451,6 +496,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       else
         lim = max(0, seen_keys(c.causal, i, nq, nk));
     }
+    const float2 cs2 = make_float2(c.scale_log2, c.scale_log2), off2 = make_float2(-lse, -lse);
+    const float2 delta2 = make_float2(-delta, -delta);
     const uint64_t draw = DROP ? dropout_row(c.draws(), qs.row + i, c.heads, head) : 0;
     bool ok = true;
     for (int n = 0; n < all; ++n) {
@@ -464,9 +511,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::load32(s_at + 32, p + 32);
       tc::wait_loads();
       tc::fence_before();
-      tc::bar_arrive(&bars.read[b]);
+      tc::bar_arrive_warp(&bars.read[b]);
 #pragma unroll
-      for (int x = 0; x < kHalf; ++x) p[x] = tc::exp2_fast(fmaf(p[x], cs, -lse));
+      for (int x = 0; x < kHalf; x += 2) {
+        const float2 a = tc::fma2(make_float2(p[x], p[x + 1]), cs2, off2);
+        p[x] = tc::exp2_fast(a.x);
+        p[x + 1] = tc::exp2_fast(a.y);
+      }
       const int left = lim - key0;
       const bool cut = __any_sync(0xffffffffu, left < kHalf);
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs[b], phase, failed));
@@ -485,8 +536,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
 #pragma unroll
-      for (int x = 0; x < kHalf; ++x)
-        t[x] = p[x] * (std::is_same<T, __half>::value ? (t[x] - delta) * ds : t[x] - delta);
+      for (int x = 0; x < kHalf; x += 2) {
+        float2 a = tc::add2(make_float2(t[x], t[x + 1]), delta2);
+        if constexpr (std::is_same<T, __half>::value) a = tc::mul2(a, make_float2(ds, ds));
+        a = tc::mul2(a, make_float2(p[x], p[x + 1]));
+        t[x] = a.x;
+        t[x + 1] = a.y;
+      }
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
@@ -496,7 +552,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::store32(dp_at, out);
       tc::wait_stores();
       tc::fence_before();
-      tc::bar_arrive(&bars.dscores[b]);
+      tc::bar_arrive_warp(&bars.dscores[b]);
     }
     if (ok && all > 0) {
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed));

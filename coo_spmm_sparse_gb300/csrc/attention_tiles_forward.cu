@@ -10,7 +10,7 @@ template <int DP>
 constexpr size_t tile_forward_smem() { return 1024 + (size_t)(2 + kForwardSlots) * tile_bytes<DP>(); }
 
 struct ForwardBars {
-  uint64_t q[2], full[kForwardSlots], empty[kForwardSlots], scores[2], probs[2], done[2], cut, drain;
+  uint64_t q[2], full[kForwardSlots], empty[kForwardSlots], scores[2], probs[2][2], done[2], cut, drain;
   uint32_t tmem;
   int failed;
 };
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ unsigned char raw[];
   __shared__ ForwardBars bars;
   unsigned char *const sq = align1024(raw), *const ring = sq + 2 * tile_bytes<DP>();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
   const bool by_heads = c.group % 2 == 0;
@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int i = 0; i < 2; ++i) {
         tc::bar_init(&bars.q[i], 1);
         tc::bar_init(&bars.scores[i], 1);
-        tc::bar_init(&bars.probs[i], 128);
+        tc::bar_init(&bars.probs[i][0], 4);
+        tc::bar_init(&bars.probs[i][1], 4);
         tc::bar_init(&bars.done[i], 1);
       }
       for (int i = 0; i < kForwardSlots; ++i) {
@@ -107,42 +108,58 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::bar_wait(&bars.full[i % kForwardSlots], (i / kForwardSlots) & 1, &unseen);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && all > 0) {
+    // the whole warp goes along, so that descriptors stay in uniform registers
+    if (all > 0) {
       constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
-      const uint32_t q0 = tc::smem_addr(sq), r0 = tc::smem_addr(ring);
-      const auto tile_at = [&](int item) { return r0 + (uint32_t)(item % kForwardSlots) * tile_bytes<DP>(); };
+      const bool leader = tc::elect_one();
+      const uint32_t q0 = tc::desc_rows(tc::smem_addr(sq)), k0 = tc::desc_rows(tc::smem_addr(ring));
+      const uint32_t v0 = tc::desc_columns(tc::smem_addr(ring), kBlock);
+      constexpr uint32_t kStep = tile_bytes<DP>() / 16;
+      const auto wait = [&](uint64_t *bar, int phase) {
+        const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
+        tc::fence_after();
+        return done;
+      };
       const auto wait_item = [&](int item) {
-        return tc::bar_wait(&bars.full[item % kForwardSlots], (item / kForwardSlots) & 1, failed);
+        return wait(&bars.full[item % kForwardSlots], (item / kForwardSlots) & 1);
       };
       bool ok = wait_item(0);
       for (int t = 0; t < 2 && ok; ++t)
         if (steps[t]) {
-          ok = tc::bar_wait(&bars.q[t], 0, failed);
-          tc::fence_after();
-          if (ok) tc::mma_rows<DP>(tmem + t * kTile, q0 + t * tile_bytes<DP>(), kBlock, tile_at(0), kBlock, by_rows);
-          tc::commit(&bars.scores[t]);
+          ok = wait(&bars.q[t], 0);
+          if (ok && leader) {
+            tc::mma_rows<DP>(tmem + t * kTile, q0 + t * kStep, k0, kBlock, by_rows);
+            tc::commit(&bars.scores[t]);
+          }
         }
-      tc::commit(&bars.empty[0]);
+      if (leader) tc::commit(&bars.empty[0]);
       for (int j = 0; j < all && ok; ++j) {
+        const uint32_t v_at = v0 + (2 * j + 1) % kForwardSlots * kStep, k_at = k0 + (2 * j + 2) % kForwardSlots * kStep;
         ok = wait_item(2 * j + 1) && (j + 1 >= all || wait_item(2 * j + 2));
         for (int t = 0; t < 2 && ok; ++t) {
           if (j >= steps[t]) continue;
-          ok = tc::bar_wait(&bars.probs[t], j & 1, failed);
-          if (!ok) break;
-          tc::fence_after();
-          tc::mma_sums<kTile>(tmem + 2 * kTile + t * DP, tmem + t * kTile, kTile, 0, tile_at(2 * j + 1), kBlock,
-                              by_cols, j > 0);
-          if (j + 1 < steps[t]) {
-            tc::mma_rows<DP>(tmem + t * kTile, q0 + t * tile_bytes<DP>(), kBlock, tile_at(2 * j + 2), kBlock, by_rows);
-            tc::commit(&bars.scores[t]);
-          } else {
-            tc::commit(&bars.done[t]);
+          const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * DP;
+          ok = wait(&bars.probs[t][0], j & 1);
+          if (ok && leader) tc::mma_sums<kTile / 2>(o_at, s_at, kTile, 0, v_at, by_cols, j > 0);
+          ok = ok && wait(&bars.probs[t][1], j & 1);
+          if (ok && leader) {
+            tc::mma_sums<kTile / 2>(o_at, s_at, kTile, 0, v_at, by_cols, true, kTile / 2);
+            if (j + 1 < steps[t]) {
+              tc::mma_rows<DP>(s_at, q0 + t * kStep, k_at, kBlock, by_rows);
+              tc::commit(&bars.scores[t]);
+            } else {
+              tc::commit(&bars.done[t]);
+            }
           }
+          __syncwarp();
         }
-        tc::commit(&bars.empty[(2 * j + 1) % kForwardSlots]);
-        if (j + 1 < all) tc::commit(&bars.empty[(2 * j + 2) % kForwardSlots]);
+        if (leader) {
+          tc::commit(&bars.empty[(2 * j + 1) % kForwardSlots]);
+          if (j + 1 < all) tc::commit(&bars.empty[(2 * j + 2) % kForwardSlots]);
+        }
+        __syncwarp();
       }
-      tc::commit(&bars.drain);
+      if (leader) tc::commit(&bars.drain);
       int unseen = 0;
       tc::bar_wait(&bars.drain, 0, &unseen);
     }
@@ -175,7 +192,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int x = 4; x < kTile; ++x) top[x & 3] = fmaxf(top[x & 3], s[x]);
+      for (int x = 4; x < kTile - 4; x += 8)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) top[y] = tc::max3(top[y], s[x + y], s[x + 4 + y]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) top[y] = fmaxf(top[y], s[kTile - 4 + y]);
       const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const float grown = fmaxf(m, most);
       const bool up = j == 0 || (grown - m) * cs > 8.f;
@@ -194,20 +215,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (up) m = grown;
       const float off = m == -INFINITY ? 0.f : -m * cs;
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
+      float2 part[2] = {};
 #pragma unroll
       for (int x = 0; x < kTile; x += 64) {
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
-          float a = tc::exp2_fast(fmaf(s[x + e], cs, off)), b = tc::exp2_fast(fmaf(s[x + e + 1], cs, off));
-          part[e & 2] += a;
-          part[(e & 2) + 1] += b;
+          float2 a = tc::fma2(make_float2(s[x + e], s[x + e + 1]), cs2, off2);
+          a.x = tc::exp2_fast(a.x);
+          a.y = tc::exp2_fast(a.y);
+          part[e / 2 & 1] = tc::add2(part[e / 2 & 1], a);
           if (DROP) {
-            s[x + e] = a;
-            s[x + e + 1] = b;
+            s[x + e] = a.x;
+            s[x + e + 1] = a.y;
           } else {
-            p[e / 2] = pack2<T>(a, b);
+            p[e / 2] = pack2<T>(a.x, a.y);
           }
         }
         if (DROP) {
@@ -222,11 +245,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         tc::store32(s_at + x / 2, p);
+        tc::wait_stores();
+        tc::fence_before();
+        tc::bar_arrive_warp(&bars.probs[t][x / 64]);
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
-      tc::wait_stores();
-      tc::fence_before();
-      tc::bar_arrive(&bars.probs[t]);
+      sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
     }
     if (ok && steps[t]) {
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));

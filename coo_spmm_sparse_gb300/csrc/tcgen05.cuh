@@ -25,6 +25,13 @@ __device__ __forceinline__ void bar_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
 }
 
+// One arrival for a whole warp, after what its lanes have read and written
+// (256 arrivals one by one took about as long as a product).
+__device__ __forceinline__ void bar_arrive_warp(uint64_t *b) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(b);
+}
+
 // Waits for the phase of that parity, for 2^22 polls at most, or until another
 // wait of the block has given up; false: the caller leaves its loop.
 constexpr int kPolls = 1 << 22;
@@ -104,12 +111,13 @@ __device__ __forceinline__ void store32(uint32_t addr, const uint32_t *r) {
 // 1024-byte groups of eight, swizzled.  By rows (the summed index runs along a
 // row): groups of eight rows are 1024 bytes apart.  By columns (the summed
 // index runs down the rows): `block` bytes from one 64-column block to the next.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_columns(uint32_t addr, uint32_t block) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(block >> 4) << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
+//
+// A descriptor's upper word is the same for both; a step along the matrix adds
+// to the lower one.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return ((addr & 0x3ffff) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_columns(uint32_t addr, uint32_t block) {
+  return ((addr & 0x3ffff) >> 4) | ((block >> 4) << 16);
 }
 
 // 128 x n sums in 32 bits of 16-bit operands; b_columns: b is read by columns.
@@ -119,17 +127,27 @@ __host__ __device__ constexpr uint32_t mma_kind(int n, bool b_columns) {
   return (1u << 4) | (t << 7) | (t << 10) | (b_columns ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17) | (8u << 24);
 }
 
-// d (tensor memory) = or += a * b over 16 of the summed index.  One thread.
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+// One thread of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+  return yes != 0;
+}
+
+// d (tensor memory) = or += a * b over 16 of the summed index.  One thread;
+// a and b are lower words of descriptors, or tensor memory.
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      "{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "n"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      "{\n.reg .pred p;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 y, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "n"(kDescHigh)
       : "memory");
 }
 // The barrier is arrived at once all MMAs issued so far by this thread are complete.
@@ -150,23 +168,53 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// d (128 x n) = or += rows a times rows b: K wide, both 64-column blocks a_block / b_block bytes apart.
-template <int K>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t a_block, uint32_t b, uint32_t b_block,
-                                         uint32_t kind) {
-#pragma unroll
-  for (int k = 0; k < K; k += 16)
-    mma(d, desc_rows(a + (k / 64) * a_block + (k % 64) * 2), desc_rows(b + (k / 64) * b_block + (k % 64) * 2), kind,
-        k > 0);
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<uint64_t *>(&d))
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+        "l"(*reinterpret_cast<uint64_t *>(&c)));
+  return d;
 }
-// d = or += a (tensor memory, K 16-bit values a row) times b, K rows read by columns.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<uint64_t *>(&d))
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<uint64_t *>(&d))
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// d (128 x n) = or += rows a times rows b: K wide, their 64-column blocks
+// `block` bytes apart.  a, b: descriptors of the first columns.
+template <int K>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t block, uint32_t kind) {
+#pragma unroll
+  for (int k = 0; k < K; k += 16) {
+    const uint32_t step = ((k / 64) * block + (k % 64) * 2) >> 4;
+    mma(d, a + step, b + step, kind, k > 0);
+  }
+}
+// d = or += a (tensor memory, 16-bit values) times b, K rows read by columns, from row `from` on.
 // Every `run` values of a lie together, `gap` columns from one run to the next.
 template <int K>
-__device__ __forceinline__ void mma_sums(uint32_t d, uint32_t a, int run, int gap, uint32_t b, uint32_t b_block,
-                                         uint32_t kind, bool add) {
+__device__ __forceinline__ void mma_sums(uint32_t d, uint32_t a, int run, int gap, uint32_t b, uint32_t kind, bool add,
+                                         int from = 0) {
 #pragma unroll
-  for (int k = 0; k < K; k += 16)
-    mma_tmem(d, a + (k / run) * gap + (k % run) / 2, desc_columns(b + k * 128, b_block), kind, add || k > 0);
+  for (int k = from; k < from + K; k += 16)
+    mma_tmem(d, a + (k / run) * gap + (k % run) / 2, b + k * 8, kind, add || k > from);
 }
 
 }  // namespace tc
