@@ -8,7 +8,7 @@
 namespace snack {
 namespace {
 
-constexpr int kTeam = 16;  // lanes that share a row of dout and out
+constexpr int kTeam = 16;  // lanes that share a row of v
 
 template <typename T>
 __device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[16 / sizeof(T)]) {
@@ -47,43 +47,71 @@ __device__ __forceinline__ float larger(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(fabsf(b))));
 }
 
-// delta = dout . out for every row and head; with `peak` also the largest |dout|.
-template <typename T, bool VEC>
+// delta = dout . out for every row and head; with `peak` also the largest
+// |dout|.  A team of lanes takes a row with one 16-byte load of each tensor a
+// lane, and kItems rows at a time, whose loads are in flight together.
+constexpr int kItems = 4;
+template <typename T, int TEAM, bool VEC>
 __global__ void __launch_bounds__(256) attention_delta(const AttnCall c, uint32_t *peak) {
-  constexpr int E = 16 / sizeof(T);
-  const int lane = threadIdx.x % kTeam;
-  const int64_t item = (int64_t)blockIdx.x * (256 / kTeam) + threadIdx.x / kTeam;
-  const int64_t row = item / c.heads;
-  const int head = (int)(item - row * c.heads);
-  float sum = 0.f, top = 0.f;
-  int seq = 0, token = 0;
-  const bool have = row < c.rows && in_sequence(c.q_offsets, c.q_lengths, c.sequences, c.q_tokens, row, &seq, &token);
-  if (have) {
+  constexpr int E = 16 / sizeof(T), kTeams = 256 / TEAM;
+  const int lane = threadIdx.x % TEAM;
+  const int64_t first = (int64_t)blockIdx.x * (kTeams * kItems) + threadIdx.x / TEAM;
+  float sum[kItems] = {}, top = 0.f;
+  int64_t place[kItems];
+  uint4 x[kItems], y[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int64_t item = first + i * kTeams, row = item / c.heads;
+    const int head = (int)(item - row * c.heads);
+    int seq = 0, token = 0;
+    const bool have = row < c.rows && in_sequence(c.q_offsets, c.q_lengths, c.sequences, c.q_tokens, row, &seq, &token);
+    place[i] = have ? (int64_t)head * c.rows + row : -1;
+    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+    if (!have) continue;
     const T *d = static_cast<const T *>(c.dout.p) + seq * c.dout.seq + token * c.dout.token + head * c.dout.head;
     const T *o = static_cast<const T *>(c.out.p) + seq * c.out.seq + token * c.out.token + head * c.out.head;
     if (VEC) {
-      for (int col = lane * E; col < c.d; col += kTeam * E) {
-        float x[E], y[E];
-        unpack16<T>(*reinterpret_cast<const uint4 *>(d + col), x);
-        unpack16<T>(*reinterpret_cast<const uint4 *>(o + col), y);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          sum += x[e] * y[e];
-          top = larger(top, x[e]);
-        }
+      if (lane * E < c.d) {
+        x[i] = *reinterpret_cast<const uint4 *>(d + lane * E);
+        y[i] = *reinterpret_cast<const uint4 *>(o + lane * E);
       }
     } else {
-      for (int col = lane; col < c.d; col += kTeam) {
-        const float x = to_float(d[col]);
-        sum += x * to_float(o[col]);
-        top = larger(top, x);
+      for (int col = lane; col < c.d; col += TEAM) {
+        const float v = to_float(d[col]);
+        sum[i] += v * to_float(o[col]);
+        top = larger(top, v);
       }
     }
   }
 #pragma unroll
-  for (int o = kTeam / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (have && lane == 0) c.delta[(int64_t)head * c.rows + row] = sum;
+  for (int i = 0; i < kItems; ++i) {
+    if (VEC) {
+      float a[E], b[E];
+      unpack16<T>(x[i], a);
+      unpack16<T>(y[i], b);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        sum[i] += a[e] * b[e];
+        top = larger(top, a[e]);
+      }
+    }
+#pragma unroll
+    for (int o = TEAM / 2; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    if (place[i] >= 0 && lane == 0) c.delta[place[i]] = sum[i];
+  }
   if (peak) block_peak(top, peak);
+}
+
+template <typename T>
+cudaError_t delta_launch(const AttnCall &c, bool vec, uint32_t *peak, cudaStream_t s) {
+  const int lanes = vec ? (c.d * (int)sizeof(T) + 15) / 16 : 32;
+  const int team = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
+  const int64_t each = 256 / team * kItems;
+  const dim3 grid((unsigned)((c.rows * c.heads + each - 1) / each));
+  if (!vec) return launch_kernel(attention_delta<T, 32, false>, grid, 256, 0, false, s, c, peak);
+  return team == 8    ? launch_kernel(attention_delta<T, 8, true>, grid, 256, 0, false, s, c, peak)
+         : team == 16 ? launch_kernel(attention_delta<T, 16, true>, grid, 256, 0, false, s, c, peak)
+                      : launch_kernel(attention_delta<T, 32, true>, grid, 256, 0, false, s, c, peak);
 }
 
 // The largest |v| of the sequences' keys.
@@ -105,35 +133,52 @@ __global__ void __launch_bounds__(256) attention_peak(const AttnCall c, int64_t 
 }
 
 // Joins the parts of a split forward call: a warp for each row and head.
+// Launched early; waits for the parts' kernel here.
+constexpr int kMostSplits = 128;
 template <typename T>
-__global__ void __launch_bounds__(256) join_splits(const AttnCall c) {
+__global__ void __launch_bounds__(128) join_splits(const AttnCall c) {
+  dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t items = c.rows * c.heads, item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t items = c.rows * c.heads, item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (item >= items) return;
   const int64_t row = item / c.heads;
   const int head = (int)(item - row * c.heads);
   const float *lse = c.part + (int64_t)c.splits * items * c.d + item;
-  float top = -INFINITY;
-  for (int s = lane; s < c.splits; s += 32) top = fmaxf(top, lse[s * items]);
+  float w[kMostSplits / 32], top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMostSplits / 32; ++i) {
+    const int s = i * 32 + lane;
+    w[i] = s < c.splits ? lse[s * items] : -INFINITY;
+    top = fmaxf(top, w[i]);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float from = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[4] = {};
-  for (int s = 0; s < c.splits; ++s) {
-    const float w = expf(lse[s * items] - from);
-    if (w == 0.f) continue;  // a part without keys
-    sum += w;
-    const float *o = c.part + (s * items + item) * c.d;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < c.d) acc[i] += w * o[lane + 32 * i];
+  for (int i = 0; i < kMostSplits / 32; ++i) {
+    w[i] = expf(w[i] - from);
+    sum += w[i];
+  }
+  sum = warp_sum(sum);
+  float acc[4] = {};
+#pragma unroll
+  for (int i = 0; i < kMostSplits / 32; ++i) {
+    const int n = min(32, c.splits - i * 32);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float by = __shfl_sync(0xffffffffu, w[i], s);
+      const float *o = c.part + ((i * 32 + s) * items + item) * c.d;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (lane + 32 * x < c.d && by != 0.f) acc[x] += by * o[lane + 32 * x];  // 0: a part without keys
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t seq = c.q_offsets ? 0 : row / c.q_tokens, token = c.q_offsets ? row : row - seq * c.q_tokens;
   T *out = static_cast<T *>(c.out.p) + seq * c.out.seq + token * c.out.token + head * c.out.head;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < c.d) out[lane + 32 * i] = from_float<T>(acc[i] * inv);
+  for (int x = 0; x < 4; ++x)
+    if (lane + 32 * x < c.d) out[lane + 32 * x] = from_float<T>(acc[x] * inv);
   if (lane == 0) c.lse[(int64_t)head * c.rows + row] = sum == 0.f ? -INFINITY : from + logf(sum);
 }
 
@@ -226,20 +271,22 @@ Cut cut_of(const AttnCall &c, int type) {
   cut.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
   if (!cut.few) return cut;
   const int64_t blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
-  const int64_t step = 128;  // what a block takes in one step, at most
-  const int64_t want = blocks ? (4 * sms + blocks - 1) / blocks : 1, most = (c.k_tokens + step - 1) / step;
-  const int64_t splits = std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)128));
+  // chunks of 512 keys at least: below that a block starts and ends more than it reads
+  const int64_t want = blocks ? 8 * sms / blocks : 1, most = c.k_tokens / 512;
+  const int64_t splits = std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)kMostSplits));
   if (splits == 1) return cut;
-  cut.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, step);
+  cut.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 64);
   cut.splits = (int)((c.k_tokens + cut.chunk - 1) / cut.chunk);
   return cut;
 }
 
 template <typename T>
-cudaError_t forward_typed(const AttnCall &c, bool few, cudaStream_t s) {
-  cudaError_t e = rows_forward_launch<T>(c, few, s);
+cudaError_t forward_typed(const AttnCall &c, const Cut &cut, int type, cudaStream_t s) {
+  if (cut.tiles) return tile_forward_launch(c, type, s);
+  if (!cut.few) return rows_forward_launch<T>(c, s);
+  cudaError_t e = few_forward_launch(c, type, s);
   if (e == cudaSuccess && c.splits > 1)
-    e = launch_kernel(join_splits<T>, dim3((unsigned)((c.rows * c.heads + 7) / 8)), 256, 0, false, s, c);
+    e = launch_kernel(join_splits<T>, dim3((unsigned)((c.rows * c.heads + 3) / 4)), 128, 0, true, s, c);
   return e;
 }
 
@@ -258,14 +305,10 @@ cudaError_t backward_typed(AttnCall c, int type, uint32_t *peak, cudaStream_t s)
     c.peak = peak;
   }
   if (c.rows) {
-    const unsigned blocks = (unsigned)((c.rows * c.heads + 256 / kTeam - 1) / (256 / kTeam));
     const auto even = [](const Strided &t) {
       return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
     };
-    if (c.d % E == 0 && even(c.dout) && even(c.out))
-      e = launch_kernel(attention_delta<T, true>, dim3(blocks), 256, 0, false, s, c, peak);
-    else
-      e = launch_kernel(attention_delta<T, false>, dim3(blocks), 256, 0, false, s, c, peak);
+    e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out), peak, s);
     if (e != cudaSuccess) return e;
   }
   if (c.q_tokens >= 64 && c.k_tokens >= 64 && tile_backward_fits(c, type)) return tile_backward_launch(c, type, s);
@@ -301,10 +344,9 @@ extern "C" snack_status snack_attention_forward(const snack_attention_args *a, v
     c.part = static_cast<float *>(workspace);
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cut.tiles                 ? tile_forward_launch(c, a->type, s)
-                        : a->type == SNACK_F32  ? forward_typed<float>(c, cut.few, s)
-                        : a->type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, cut.few, s)
-                                                : forward_typed<__half>(c, cut.few, s);
+  const cudaError_t e = a->type == SNACK_F32    ? forward_typed<float>(c, cut, a->type, s)
+                        : a->type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, cut, a->type, s)
+                                                : forward_typed<__half>(c, cut, a->type, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention forward");
 }
 
@@ -314,6 +356,7 @@ extern "C" snack_status snack_attention_error(int *flag, void *stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = tile_forward_failed(flag, s);
   if (e == cudaSuccess) e = tile_backward_failed(flag, s);
+  if (e == cudaSuccess) e = few_forward_failed(flag, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention error flag");
 }
 

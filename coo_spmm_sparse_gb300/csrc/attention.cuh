@@ -128,9 +128,13 @@ __device__ __forceinline__ Place find_tile(const int32_t *offsets, int n, int to
 
 // The launches of attention on mma.sync, by type (attention_rows_*.cu).
 template <typename T>
-cudaError_t rows_forward_launch(const AttnCall &c, bool few, cudaStream_t s);
+cudaError_t rows_forward_launch(const AttnCall &c, cudaStream_t s);
 template <typename T>
 cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
+
+// The forward call of few rows (attention_few.cu).
+cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s);
+cudaError_t few_forward_failed(int *flag, cudaStream_t s);
 
 // Those of attention on tcgen05 (attention_tiles*.cu): which calls they take,
 // and whether one of their bounded waits has run out since the last question.
@@ -140,6 +144,21 @@ cudaError_t tile_forward_failed(int *flag, cudaStream_t s);
 bool tile_backward_fits(const AttnCall &c, int type);
 cudaError_t tile_backward_launch(const AttnCall &c, int type, cudaStream_t s);
 cudaError_t tile_backward_failed(int *flag, cudaStream_t s);
+
+// Reads a sticky flag of the current device and clears it.
+template <typename S>
+inline cudaError_t read_flag(S &symbol, int *flag, cudaStream_t s) {
+  int v = 0;
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v) {
+    e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    *flag = 1;
+  }
+  return e;
+}
 
 // Tiles that a grid needs so that every sequence finds all of its own.
 inline int64_t tiles_of(bool ragged, int64_t n, int64_t tokens, int64_t per_token, int64_t tile_rows) {

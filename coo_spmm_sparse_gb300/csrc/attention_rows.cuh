@@ -295,150 +295,12 @@ __device__ __forceinline__ void add_shares(float (&o)[DP / 8][4], float *room, i
 
 // ------------------------------------------------------------------ forward
 
-template <typename T, int DP, int WM, int WN, int BN>
-constexpr size_t rows_forward_smem() {
-  return (size_t)(16 * WM + 2 * 2 * WN * BN) * (DP + 8) * sizeof(T);
-}
-
-// Softmax with a running maximum and sum.  Grid: x = tile * key_heads + key
-// head, y = split (c.chunk keys each; the parts are joined by join_splits).
-template <typename T, int DP, int WM, int WN, int BN>
-__global__ void __launch_bounds__(32 * WM * WN) rows_forward(const AttnCall c) {
-  using Ops = Tile<T, DP>;
-  constexpr int kLd = Ops::kLd, NB = BN / 8, STEP = WN * BN;
-  extern __shared__ __align__(16) unsigned char smem[];
-  T *sq = reinterpret_cast<T *>(smem);
-  T *skv = sq + 16 * WM * kLd;  // [2 stages][K, V][STEP]
-  __shared__ float stat[2][WN][16 * WM];
-
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp / WN, wn = warp % WN;
-  const int kh = blockIdx.x % c.key_heads, G = c.group;
-  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, G, 16 * WM, blockIdx.x / c.key_heads, c.causal);
-  if (at.s < 0) return;
-  const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
-  const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
-  const int r0 = at.tile * 16 * WM, nq = qs.valid, nk = ks.valid;
-  const int last = min((r0 + 16 * WM - 1) / G, nq - 1);
-  const int begin = blockIdx.y * c.chunk;
-  int end = last >= 0 && r0 / G < nq ? max(0, seen_keys(c.causal, last, nq, nk)) : 0;
-  end = min(end, c.splits > 1 ? begin + c.chunk : end);
-
-  const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, kh * G, G, c.d);
-  const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
-
-  // the two rows of this lane
-  int token[2], head[2], lim[2];
-  uint64_t draw[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = r0 + wm * 16 + (lane >> 2) + 8 * h;
-    token[h] = r / G;
-    head[h] = kh * G + r % G;
-    lim[h] = token[h] < nq ? min(end, seen_keys(c.causal, token[h], nq, nk)) : 0;
-    if (c.drop) draw[h] = dropout_row(c.draws(), qs.row + token[h], c.heads, head[h]);
-  }
-
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[DP / 8][4] = {};
-  const auto copy_step = [&](int stage, int key0) {
-    T *k = skv + stage * 2 * STEP * kLd;
-    copy_rows<T, DP>(k, kr, key0, STEP, end);
-    copy_rows<T, DP>(k + STEP * kLd, vr, key0, STEP, end);
-  };
-  if (begin < end) {
-    copy_rows<T, DP>(sq, qr, r0, 16 * WM, nq * G);
-    copy_step(0, begin);
-  }
-  copies_commit();
-  for (int key0 = begin, stage = 0; key0 < end; key0 += STEP, stage ^= 1) {
-    if (key0 + STEP < end) copy_step(stage ^ 1, key0 + STEP);
-    copies_commit();
-    copies_wait<1>();
-    __syncthreads();
-    const T *k = skv + (stage * 2 * STEP + wn * BN) * kLd, *v = k + STEP * kLd;
-    const int key = key0 + wn * BN;
-    if (key < end) {
-      float s[NB][4] = {};
-      Ops::template rows_by_rows<NB>(s, sq + wm * 16 * kLd, k, lane);
-      float top[2] = {m[0], m[1]};
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = e >> 1;
-          s[n][e] = key + Ops::column(n, lane, e & 1) < lim[h] ? s[n][e] * c.scale_log2 : -INFINITY;
-          top[h] = fmaxf(top[h], s[n][e]);
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-        const float from = top[h] == -INFINITY ? 0.f : top[h];
-        const float shrink = exp2f(m[h] - from);
-        m[h] = top[h];
-        l[h] *= shrink;
-#pragma unroll
-        for (int n = 0; n < DP / 8; ++n) {
-          o[n][2 * h] *= shrink;
-          o[n][2 * h + 1] *= shrink;
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[n][2 * h + e] = exp2f(s[n][2 * h + e] - from);
-            sum += s[n][2 * h + e];
-          }
-        l[h] += sum;
-        if (c.drop) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            const int j = key + Ops::column(n, lane, 0);
-            const uint64_t z = dropout_draw(draw[h], j);
-            if (draw_lane(z, j & 3) < c.drop) s[n][2 * h] = 0.f;
-            if (draw_lane(z, (key + Ops::column(n, lane, 1)) & 3) < c.drop) s[n][2 * h + 1] = 0.f;
-          }
-        }
-      }
-      Ops::template sums_by_rows<NB>(o, s, v, lane);
-    }
-    __syncthreads();
-  }
-  copies_wait<0>();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-  }
-  if constexpr (WN > 1) {
-    const int row = wm * 16 + (lane >> 2);
-    if ((lane & 3) == 0)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        stat[0][wn][row + 8 * h] = m[h];
-        stat[1][wn][row + 8 * h] = l[h];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < WN; ++w) top = fmaxf(top, stat[0][w][row + 8 * h]);
-      const float from = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int w = 0; w < WN; ++w) sum += stat[1][w][row + 8 * h] * exp2f(stat[0][w][row + 8 * h] - from);
-      const float shrink = exp2f(m[h] - from);
-#pragma unroll
-      for (int n = 0; n < DP / 8; ++n) {
-        o[n][2 * h] *= shrink;
-        o[n][2 * h + 1] *= shrink;
-      }
-      m[h] = top;
-      l[h] = sum;
-    }
-    add_shares<DP, WM, WN>(o, reinterpret_cast<float *>(smem), wm, wn, lane);
-    if (wn != 0) return;
-  }
+// The last step of 16 rows: the sums times 1 / l, and the log of the sum (or,
+// in a split call, both as a part).  One warp.
+template <typename T, int DP>
+__device__ __forceinline__ void finish_rows(const AttnCall &c, const Span &qs, const float (&o)[DP / 8][4],
+                                            const float (&m)[2], const float (&l)[2], const int (&token)[2],
+                                            const int (&head)[2], int lane) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (token[h] >= qs.cover) continue;
@@ -450,12 +312,123 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_forward(const AttnCall c) {
       store_row<float, DP>(c.part + slot * c.d, o, h, inv, c.d, lane);
       if ((lane & 3) == 0) c.part[(int64_t)c.splits * c.rows * c.heads * c.d + slot] = lse;
     } else {
-      T *out = static_cast<T *>(c.out.p) + (c.q_offsets ? row * c.out.token : qs.seq * c.out.seq + token[h] * c.out.token) +
-               head[h] * c.out.head;
+      T *out = static_cast<T *>(c.out.p) +
+               (c.q_offsets ? row * c.out.token : qs.seq * c.out.seq + token[h] * c.out.token) + head[h] * c.out.head;
       store_row<T, DP>(out, o, h, inv, c.d, lane);
       if ((lane & 3) == 0) c.lse[(int64_t)head[h] * c.rows + row] = lse;
     }
   }
+}
+
+template <typename T, int DP, int WM, int BN>
+constexpr size_t rows_forward_smem() {
+  return (size_t)(16 * WM + 2 * 2 * BN) * (DP + 8) * sizeof(T);
+}
+
+// Softmax with a running maximum and sum.  Grid: tile * key_heads + key head.
+template <typename T, int DP, int WM, int BN>
+__global__ void __launch_bounds__(32 * WM) rows_forward(const AttnCall c) {
+  using Ops = Tile<T, DP>;
+  constexpr int kLd = Ops::kLd, NB = BN / 8;
+  extern __shared__ __align__(16) unsigned char smem[];
+  T *sq = reinterpret_cast<T *>(smem);
+  T *skv = sq + 16 * WM * kLd;  // [2 stages][K, V][BN]
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kh = blockIdx.x % c.key_heads, G = c.group;
+  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, G, 16 * WM, blockIdx.x / c.key_heads, c.causal);
+  if (at.s < 0) return;
+  const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
+  const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
+  const int r0 = at.tile * 16 * WM, nq = qs.valid, nk = ks.valid;
+  const int last = min((r0 + 16 * WM - 1) / G, nq - 1);
+  const int end = r0 / G < nq ? max(0, seen_keys(c.causal, last, nq, nk)) : 0;
+
+  const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, kh * G, G, c.d);
+  const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
+
+  // the two rows of this lane
+  int token[2], head[2], lim[2];
+  uint64_t draw[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + warp * 16 + (lane >> 2) + 8 * h;
+    token[h] = r / G;
+    head[h] = kh * G + r % G;
+    lim[h] = token[h] < nq ? min(end, seen_keys(c.causal, token[h], nq, nk)) : 0;
+    if (c.drop) draw[h] = dropout_row(c.draws(), qs.row + token[h], c.heads, head[h]);
+  }
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[DP / 8][4] = {};
+  const auto copy_step = [&](int stage, int key0) {
+    T *k = skv + stage * 2 * BN * kLd;
+    copy_rows<T, DP>(k, kr, key0, BN, end);
+    copy_rows<T, DP>(k + BN * kLd, vr, key0, BN, end);
+  };
+  if (end > 0) {
+    copy_rows<T, DP>(sq, qr, r0, 16 * WM, nq * G);
+    copy_step(0, 0);
+  }
+  copies_commit();
+  for (int key = 0, stage = 0; key < end; key += BN, stage ^= 1) {
+    if (key + BN < end) copy_step(stage ^ 1, key + BN);
+    copies_commit();
+    copies_wait<1>();
+    __syncthreads();
+    const T *k = skv + stage * 2 * BN * kLd, *v = k + BN * kLd;
+    float s[NB][4] = {};
+    Ops::template rows_by_rows<NB>(s, sq + warp * 16 * kLd, k, lane);
+    float top[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int h = e >> 1;
+        s[n][e] = key + Ops::column(n, lane, e & 1) < lim[h] ? s[n][e] * c.scale_log2 : -INFINITY;
+        top[h] = fmaxf(top[h], s[n][e]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+      const float from = top[h] == -INFINITY ? 0.f : top[h];
+      const float shrink = exp2f(m[h] - from);
+      m[h] = top[h];
+      l[h] *= shrink;
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        o[n][2 * h] *= shrink;
+        o[n][2 * h + 1] *= shrink;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][2 * h + e] = exp2f(s[n][2 * h + e] - from);
+          sum += s[n][2 * h + e];
+        }
+      l[h] += sum;
+      if (c.drop) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const int j = key + Ops::column(n, lane, 0);
+          const uint64_t z = dropout_draw(draw[h], j);
+          if (draw_lane(z, j & 3) < c.drop) s[n][2 * h] = 0.f;
+          if (draw_lane(z, (key + Ops::column(n, lane, 1)) & 3) < c.drop) s[n][2 * h + 1] = 0.f;
+        }
+      }
+    }
+    Ops::template sums_by_rows<NB>(o, s, v, lane);
+    __syncthreads();
+  }
+  copies_wait<0>();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+  }
+  finish_rows<T, DP>(c, qs, o, m, l, token, head, lane);
 }
 
 // ------------------------------------------------------------------ backward

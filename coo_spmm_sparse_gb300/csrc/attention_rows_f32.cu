@@ -1,6 +1,6 @@
 #include "attention_rows_launch.cuh"
 
 namespace snack {
-template cudaError_t rows_forward_launch<float>(const AttnCall &, bool, cudaStream_t);
+template cudaError_t rows_forward_launch<float>(const AttnCall &, cudaStream_t);
 template cudaError_t rows_backward_launch<float>(const AttnCall &, cudaStream_t);
 }  // namespace snack

@@ -19,18 +19,6 @@ namespace snack {
 
 // Sticky: a wait of one of this file's kernels has run out since the last read.
 static __device__ int g_attention_failed = 0;
-static inline cudaError_t read_failed(int *flag, cudaStream_t s) {
-  int v = 0;
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_attention_failed, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && v) {
-    e = cudaMemcpyToSymbolAsync(g_attention_failed, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    *flag = 1;
-  }
-  return e;
-}
 
 constexpr int kTile = 128;
 // Warps 0-7: rows; 8: copies; 9: MMAs; 10: statistics of

@@ -621,6 +621,6 @@ cudaError_t tile_backward_launch(const AttnCall &c, int type, cudaStream_t s) {
   return type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, m, s) : backward_typed<__half>(c, m, s);
 }
 
-cudaError_t tile_backward_failed(int *flag, cudaStream_t s) { return read_failed(flag, s); }
+cudaError_t tile_backward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }
 
 }  // namespace snack

@@ -310,6 +310,6 @@ cudaError_t tile_forward_launch(const AttnCall &c, int type, cudaStream_t s) {
   return type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, m, s) : forward_typed<__half>(c, m, s);
 }
 
-cudaError_t tile_forward_failed(int *flag, cudaStream_t s) { return read_failed(flag, s); }
+cudaError_t tile_forward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }
 
 }  // namespace snack
