@@ -132,54 +132,39 @@ __global__ void __launch_bounds__(256) attention_peak(const AttnCall c, int64_t 
   block_peak(top, peak);
 }
 
-// Joins the parts of a split forward call: a warp for each row and head.
-// Launched early; waits for the parts' kernel here.
+// Joins the parts of a split forward call: a block for each row and head, a
+// thread for each column.  Launched early; waits for the parts' kernel here.
 constexpr int kMostSplits = 128;
 template <typename T>
 __global__ void __launch_bounds__(128) join_splits(const AttnCall c) {
+  __shared__ float weight[kMostSplits], top_of[4], sum_of[4];
   dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t items = c.rows * c.heads, item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= items) return;
-  const int64_t row = item / c.heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t items = c.rows * c.heads, item = blockIdx.x, row = item / c.heads;
   const int head = (int)(item - row * c.heads);
-  const float *lse = c.part + (int64_t)c.splits * items * c.d + item;
-  float w[kMostSplits / 32], top = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMostSplits / 32; ++i) {
-    const int s = i * 32 + lane;
-    w[i] = s < c.splits ? lse[s * items] : -INFINITY;
-    top = fmaxf(top, w[i]);
-  }
+  const float *const parts = c.part + item * c.d + tid, *const lse = c.part + (int64_t)c.splits * items * c.d + item;
+  const float own = tid < c.splits ? lse[tid * items] : -INFINITY;
+  float top = own;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float from = top == -INFINITY ? 0.f : top;
-#pragma unroll
-  for (int i = 0; i < kMostSplits / 32; ++i) {
-    w[i] = expf(w[i] - from);
-    sum += w[i];
-  }
-  sum = warp_sum(sum);
-  float acc[4] = {};
-#pragma unroll
-  for (int i = 0; i < kMostSplits / 32; ++i) {
-    const int n = min(32, c.splits - i * 32);
+  if (lane == 0) top_of[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(top_of[0], top_of[1]), fmaxf(top_of[2], top_of[3]));
+  const float w = expf(own - (top == -INFINITY ? 0.f : top));
+  weight[tid] = w;
+  const float part = warp_sum(w);
+  if (lane == 0) sum_of[warp] = part;
+  __syncthreads();
+  const float sum = (sum_of[0] + sum_of[1]) + (sum_of[2] + sum_of[3]);
+  if (tid < c.d) {
+    float acc = 0.f;
 #pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-      const float by = __shfl_sync(0xffffffffu, w[i], s);
-      const float *o = c.part + ((i * 32 + s) * items + item) * c.d;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (lane + 32 * x < c.d && by != 0.f) acc[x] += by * o[lane + 32 * x];  // 0: a part without keys
-    }
+    for (int s = 0; s < c.splits; ++s) acc += weight[s] * parts[s * items * c.d];  // (a part without keys is zero)
+    const int64_t seq = c.q_offsets ? 0 : row / c.q_tokens, token = c.q_offsets ? row : row - seq * c.q_tokens;
+    T *out = static_cast<T *>(c.out.p) + seq * c.out.seq + token * c.out.token + head * c.out.head;
+    out[tid] = from_float<T>(sum == 0.f ? 0.f : acc / sum);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t seq = c.q_offsets ? 0 : row / c.q_tokens, token = c.q_offsets ? row : row - seq * c.q_tokens;
-  T *out = static_cast<T *>(c.out.p) + seq * c.out.seq + token * c.out.token + head * c.out.head;
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (lane + 32 * x < c.d) out[lane + 32 * x] = from_float<T>(acc[x] * inv);
-  if (lane == 0) c.lse[(int64_t)head * c.rows + row] = sum == 0.f ? -INFINITY : from + logf(sum);
+  if (tid == 0) c.lse[(int64_t)head * c.rows + row] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 // ------------------------------------------------------------------ host
@@ -214,7 +199,7 @@ snack_status check_args(const snack_attention_args *a) {
   const auto tiles = [&](const int32_t *off, int64_t tokens, int64_t per) {
     return tiles_of(off != nullptr, a->sequences, tokens, per, 16) * a->key_heads;
   };
-  if (tiles(a->q_offsets, a->q_tokens, group) >= lim || tiles(a->k_offsets, a->k_tokens, 1) >= lim ||
+  if (tiles(a->q_offsets, a->q_tokens, group) + tiles(a->k_offsets, a->k_tokens, 1) >= lim ||
       rows * a->heads >= lim * 8)
     return refuse(SNACK_ERR_UNSUPPORTED, "too many rows for one launch");
   const int64_t strides[] = {a->q_stride[0], a->q_stride[1], a->q_stride[2], a->k_stride[0], a->k_stride[1],
@@ -272,7 +257,7 @@ Cut cut_of(const AttnCall &c, int type) {
   if (!cut.few) return cut;
   const int64_t blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
   // chunks of 512 keys at least: below that a block starts and ends more than it reads
-  const int64_t want = blocks ? 8 * sms / blocks : 1, most = c.k_tokens / 512;
+  const int64_t want = blocks ? 16 * sms / blocks : 1, most = c.k_tokens / 512;
   const int64_t splits = std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)kMostSplits));
   if (splits == 1) return cut;
   cut.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 64);
@@ -286,7 +271,7 @@ cudaError_t forward_typed(const AttnCall &c, const Cut &cut, int type, cudaStrea
   if (!cut.few) return rows_forward_launch<T>(c, s);
   cudaError_t e = few_forward_launch(c, type, s);
   if (e == cudaSuccess && c.splits > 1)
-    e = launch_kernel(join_splits<T>, dim3((unsigned)((c.rows * c.heads + 3) / 4)), 128, 0, true, s, c);
+    e = launch_kernel(join_splits<T>, dim3((unsigned)(c.rows * c.heads)), 128, 0, true, s, c);
   return e;
 }
 
@@ -356,7 +341,6 @@ extern "C" snack_status snack_attention_error(int *flag, void *stream) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = tile_forward_failed(flag, s);
   if (e == cudaSuccess) e = tile_backward_failed(flag, s);
-  if (e == cudaSuccess) e = few_forward_failed(flag, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention error flag");
 }
 

@@ -134,7 +134,6 @@ cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
 
 // The forward call of few rows (attention_few.cu).
 cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s);
-cudaError_t few_forward_failed(int *flag, cudaStream_t s);
 
 // Those of attention on tcgen05 (attention_tiles*.cu): which calls they take,
 // and whether one of their bounded waits has run out since the last question.

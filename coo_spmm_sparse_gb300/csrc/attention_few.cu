@@ -1,51 +1,39 @@
 // The forward call of few query rows (decode steps, short prompts): 16 rows to
-// a block, whose four warps take the keys in turn, each on its own.
+// a block, whose warps take the keys in turn, each on its own.
 //
-// The caches' bytes are the work.  A lane copies a row of a warp's next tile
-// (16 keys and their values; 8 in 32 bits at head sizes above 64) with one bulk
-// copy, three tiles deep, complete on the warp's own barrier: no barrier of the
-// block and hardly an instruction is spent on a copy, where 16-byte copies by
-// every thread took most of the instructions and held the kernel at 2.4 TB/s.
-// Rows that are not whole aligned vectors are copied element by element.
-// Long caches are cut into chunks for more blocks, joined by join_splits.
+// The caches' bytes are the work.  A warp copies its next tiles (16 keys and
+// their values; 8 in 32 bits at head sizes above 64) with 16-byte asynchronous
+// copies whose addresses advance by constants, and waits for its own copies
+// only: no barrier of the block until the end.  (Copies whose rows and columns
+// were computed for each vector took most of the instructions and held the
+// kernel at 2.4 TB/s; one bulk copy a row reached 4.3.)  Long caches are cut
+// into chunks for more blocks, joined by join_splits.
 #include "attention_rows.cuh"
-#include "tcgen05.cuh"
 
 namespace snack {
 namespace {
 
-__device__ int g_few_failed = 0;
-
-constexpr int kWarps = 4, kStages = 3;
-
-template <typename T, int DP>
+// Four warps, three tiles each; sixteen warps with one tile each where there are
+// few blocks, so that short caches take one step.
+template <typename T, int DP, int W>
 struct Few {
   static constexpr int kKeys = sizeof(T) == 4 && DP > 64 ? 8 : 16;  // of a warp's tile
-  static constexpr int kStep = kWarps * kKeys, kLd = DP + 8;
+  static constexpr int kStages = W == 4 ? 3 : 1, kStep = W * kKeys, kLd = DP + 8;
   static constexpr int kTileElems = 2 * kKeys * kLd;
-  static constexpr size_t ring = (size_t)kWarps * kStages * kTileElems * sizeof(T);
-  static constexpr size_t room = (size_t)(kWarps - 1) * 16 * kLd * sizeof(float);
+  static constexpr size_t ring = (size_t)W * kStages * kTileElems * sizeof(T);
+  static constexpr size_t room = (size_t)W * 16 * kLd * sizeof(float);
   static constexpr size_t smem = 16 * kLd * sizeof(T) + (ring > room ? ring : room);
 };
 
-__device__ __forceinline__ void copy_row(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc::smem_addr(to)),
-               "l"(from), "r"(bytes), "r"(tc::smem_addr(bar))
-               : "memory");
-}
-
-template <typename T, int DP>
-__global__ void __launch_bounds__(32 * kWarps) few_forward(const AttnCall c) {
+template <typename T, int DP, int W>
+__global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
   using Ops = Tile<T, DP>;
-  using F = Few<T, DP>;
-  constexpr int kLd = F::kLd, NB = F::kKeys / 8, KEYS = F::kKeys;
+  using F = Few<T, DP, W>;
+  constexpr int kLd = F::kLd, kKeys = F::kKeys, NB = kKeys / 8, kStages = F::kStages;
+  constexpr int E = 16 / sizeof(T), kChunks = DP / E, kRows = 32 / kChunks;  // rows that a warp copies at once
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ uint64_t bars[kWarps][kStages];
-  __shared__ float stat[2][kWarps][16];
-  __shared__ int failed_flag;
+  __shared__ float stat[2][W][16];
   T *const sq = reinterpret_cast<T *>(smem);
-  volatile int *const failed = &failed_flag;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kh = blockIdx.x % c.key_heads, G = c.group;
@@ -61,61 +49,49 @@ __global__ void __launch_bounds__(32 * kWarps) few_forward(const AttnCall c) {
 
   T *const ring = sq + 16 * kLd + warp * kStages * F::kTileElems;
   const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
-  const uint32_t row_bytes = (uint32_t)(c.d * sizeof(T));
-  const bool bulk = kr.vec && vr.vec && row_bytes % 16 == 0;
+  const bool vec = kr.vec && vr.vec;
+  const int first = begin + warp * kKeys;
+  const int steps = first < end ? (end - first + F::kStep - 1) / F::kStep : 0;
+  const int my_row = lane / kChunks, my_col = lane % kChunks * E;
+  const int bytes = max(0, min(E, c.d - my_col)) * (int)sizeof(T);  // what lies behind the head size becomes zero
+  // Rows behind the last key become zeros too: values that meet zero probabilities have to be numbers.
+  const auto copy_tile = [&](int step) {
+    const int key0 = first + step * F::kStep;
+    T *const k = ring + step % kStages * F::kTileElems;
+    if (vec) {
+      T *const to = k + my_row * kLd + my_col;
+      const T *const pk = kr.base + (int64_t)(key0 + my_row) * kr.token + my_col;
+      const T *const pv = vr.base + (int64_t)(key0 + my_row) * vr.token + my_col;
+#pragma unroll
+      for (int i = 0; i < kKeys; i += kRows) {
+        const int n = key0 + my_row + i < end ? bytes : 0;
+        copy_async16(to + i * kLd, n ? pk + i * kr.token : kr.base, n);
+        copy_async16(to + (kKeys + i) * kLd, n ? pv + i * vr.token : vr.base, n);
+      }
+    } else {
+      for (int r = 0; r < kKeys; ++r)
+        for (int col = lane; col < DP; col += 32) {
+          const bool have = key0 + r < end && col < c.d;
+          k[r * kLd + col] = have ? kr.row(key0 + r)[col] : from_float<T>(0.f);
+          k[(kKeys + r) * kLd + col] = have ? vr.row(key0 + r)[col] : from_float<T>(0.f);
+        }
+    }
+  };
+  // the keys are on their way before the queries are waited for
+  constexpr int kAhead = kStages > 1 ? kStages - 1 : 1;
   if (begin < end) {
     const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, kh * G, G, c.d);
     copy_rows<T, DP>(sq, qr, r0, 16, nq * G);
-    // columns behind the head size stay zero; what is copied never reaches them
-    if (c.d < DP)
-      for (int r = lane; r < kStages * 2 * KEYS; r += 32)
-        for (int col = c.d; col < DP; ++col) ring[r * kLd + col] = from_float<T>(0.f);
   }
   copies_commit();
-  if (threadIdx.x == 0) failed_flag = 0;
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) tc::bar_init(&bars[warp][s], 1);
-    tc::fence_bar_init();
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    if (i < steps) copy_tile(i);
+    copies_commit();
   }
-  tc::fence_async_proxy();
-  copies_wait<0>();
-  __syncthreads();
-
-  const int first = begin + warp * KEYS;
-  const int steps = first < end ? (end - first + F::kStep - 1) / F::kStep : 0;
-  const auto copy_tile = [&](int step) {
-    const int key0 = first + step * F::kStep, rows = min(KEYS, end - key0), stage = step % kStages;
-    T *const k = ring + stage * F::kTileElems, *const v = k + KEYS * kLd;
-    uint64_t *const bar = &bars[warp][stage];
-    if (bulk) {
-      if (lane == 0) tc::bar_expect(bar, 2 * rows * row_bytes);
-      __syncwarp();
-    }
-    for (int r = lane; r < 2 * KEYS; r += 32) {
-      const bool is_v = r >= KEYS;
-      const int i = is_v ? r - KEYS : r;
-      T *const to = (is_v ? v : k) + i * kLd;
-      const T *const from = (is_v ? vr : kr).row(key0 + min(i, rows - 1));
-      if (i >= rows) {  // values that meet zero probabilities have to be numbers
-        for (int col = 0; col < DP; ++col) to[col] = from_float<T>(0.f);
-      } else if (bulk) {
-        copy_row(to, from, row_bytes, bar);
-      }
-    }
-    if (!bulk) {
-      for (int r = 0; r < 2 * rows; ++r) {
-        const bool is_v = r >= rows;
-        const int i = is_v ? r - rows : r;
-        const T *const from = (is_v ? vr : kr).row(key0 + i);
-        T *const to = (is_v ? v : k) + i * kLd;
-        for (int col = lane; col < c.d; col += 32) to[col] = from[col];
-      }
-      __syncwarp();
-    }
-  };
 
   // the two rows of this lane; the second eight hold nothing where there are no more rows
-  const bool both = r0 + 8 < min(qs.cover * G, nq * G);
+  const int rows = min(16, nq * G - r0);
   int token[2], head[2], lim[2];
   uint64_t draw[2];
 #pragma unroll
@@ -128,21 +104,23 @@ __global__ void __launch_bounds__(32 * kWarps) few_forward(const AttnCall c) {
   }
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[DP / 8][4] = {};
-  for (int i = 0; i < min(steps, kStages - 1); ++i) copy_tile(i);
-  bool ok = true;
+  copies_wait<kAhead>();
+  __syncthreads();
   for (int step = 0; step < steps; ++step) {
-    const int stage = step % kStages, key = first + step * F::kStep;
-    if (step + kStages - 1 < steps) copy_tile(step + kStages - 1);
-    if (bulk) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars[warp][stage], (step / kStages) & 1, failed));
-    if (!ok) break;
+    const int key = first + step * F::kStep;
+    if (kStages > 1) {
+      if (step + kAhead < steps) copy_tile(step + kAhead);
+      copies_commit();
+    }
+    copies_wait<kStages - 1>();
     __syncwarp();
-    const T *const k = ring + stage * F::kTileElems, *const v = k + KEYS * kLd;
+    const T *const k = ring + step % kStages * F::kTileElems, *const v = k + kKeys * kLd;
     float s[NB][4] = {};
     Ops::template rows_by_rows<NB>(s, sq, k, lane);
     float shrink[2] = {1.f, 1.f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (h == 1 && !both) {
+      if (h == 1 && rows <= 8) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) s[n][2] = s[n][3] = 0.f;
         continue;
@@ -189,60 +167,95 @@ __global__ void __launch_bounds__(32 * kWarps) few_forward(const AttnCall c) {
     }
     Ops::template sums_by_rows<NB>(o, s, v, lane);
     __syncwarp();
+    if (kStages == 1 && step + 1 < steps) {
+      copy_tile(step + 1);
+      copies_commit();
+    }
   }
-  if (!ok) {  // the copies of this warp end before the block does
-    int unseen = 0;
-    for (int s = 0; s < kStages; ++s)
-      for (int phase = 0; phase < 2; ++phase) tc::bar_wait(&bars[warp][s], phase, &unseen);
-  }
+  copies_wait<0>();
   dependency_launch();
+  const int row = lane >> 2;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-  }
-  const int row = lane >> 2;
-  if ((lane & 3) == 0)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    if ((lane & 3) == 0) {
       stat[0][warp][row + 8 * h] = m[h];
       stat[1][warp][row + 8 * h] = l[h];
     }
-  __syncthreads();
-  if (threadIdx.x == 0 && failed_flag) g_few_failed = 1;
+  }
+  __syncthreads();  // (and the tiles are read: their memory takes the warps' sums)
+  float *const room = reinterpret_cast<float *>(sq + 16 * kLd);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float top = -INFINITY, sum = 0.f;
+    if (row + 8 * h >= rows) continue;
+    float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[0][w][row + 8 * h]);
-    const float from = top == -INFINITY ? 0.f : top;
+    for (int w = 0; w < W; ++w) top = fmaxf(top, stat[0][w][row + 8 * h]);
+    const float shrink = exp2f(m[h] - (top == -INFINITY ? 0.f : top));
+    float *const to = room + (warp * 16 + row + 8 * h) * kLd + 2 * (lane & 3);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += stat[1][w][row + 8 * h] * exp2f(stat[0][w][row + 8 * h] - from);
-    const float shrink = exp2f(m[h] - from);
-#pragma unroll
-    for (int n = 0; n < DP / 8; ++n) {
-      o[n][2 * h] *= shrink;
-      o[n][2 * h + 1] *= shrink;
-    }
-    m[h] = top;
-    l[h] = sum;
+    for (int n = 0; n < DP / 8; ++n)
+      *reinterpret_cast<float2 *>(to + n * 8) = make_float2(o[n][2 * h] * shrink, o[n][2 * h + 1] * shrink);
   }
-  add_shares<DP, 1, kWarps>(o, reinterpret_cast<float *>(sq + 16 * kLd), 0, warp, lane);
-  if (warp == 0) finish_rows<T, DP>(c, qs, o, m, l, token, head, lane);
+  __syncthreads();
+  // a warp takes a row, a lane its columns: the warps' sums in their order
+  for (int r = warp; r < 16; r += W) {
+    const int i = (r0 + r) / G, hd = kh * G + (r0 + r) % G;
+    if (i >= qs.cover) break;
+    float top = -INFINITY, sum = 0.f, sums[DP / 32] = {};
+    if (r < rows) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, stat[0][w][r]);
+      const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        sum += stat[1][w][r] * exp2f(stat[0][w][r] - from);
+#pragma unroll
+        for (int x = 0; x < DP / 32; ++x) sums[x] += room[(w * 16 + r) * kLd + lane + 32 * x];
+      }
+    }
+    const float by = sum == 0.f ? 0.f : c.keep_scale / sum;
+    const float lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const int64_t token_row = qs.row + i, slot = (blockIdx.y * c.rows + token_row) * c.heads + hd;
+    T *const out = static_cast<T *>(c.out.p) +
+                   (c.q_offsets ? token_row * c.out.token : qs.seq * c.out.seq + i * c.out.token) + hd * c.out.head;
+#pragma unroll
+    for (int x = 0; x < DP / 32; ++x) {
+      const int col = lane + 32 * x;
+      if (col >= c.d) break;
+      if (c.splits > 1)
+        c.part[slot * c.d + col] = sum == 0.f ? 0.f : sums[x] * by;
+      else
+        out[col] = from_float<T>(sum == 0.f ? 0.f : sums[x] * by);
+    }
+    if (lane == 0) {
+      if (c.splits > 1)
+        c.part[(int64_t)c.splits * c.rows * c.heads * c.d + slot] = lse;
+      else
+        c.lse[(int64_t)hd * c.rows + token_row] = lse;
+    }
+  }
+}
+
+template <typename T, int DP, int W>
+cudaError_t few_sized(const AttnCall &c, int64_t blocks, cudaStream_t s) {
+  const auto kern = few_forward<T, DP, W>;
+  const cudaError_t e = allow_smem(kern, Few<T, DP, W>::smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)blocks, (unsigned)c.splits), 32 * W, Few<T, DP, W>::smem, false, s, c);
 }
 
 template <typename T, int DP>
-cudaError_t few_sized(const AttnCall &c, cudaStream_t s) {
+cudaError_t few_warps(const AttnCall &c, cudaStream_t s) {
   const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
-  const auto kern = few_forward<T, DP>;
-  const cudaError_t e = allow_smem(kern, Few<T, DP>::smem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)blocks, (unsigned)c.splits), 32 * kWarps, Few<T, DP>::smem, false, s, c);
+  if (blocks * c.splits <= device_sms()) return few_sized<T, DP, 16>(c, blocks, s);
+  return few_sized<T, DP, 4>(c, blocks, s);
 }
 
 template <typename T>
 cudaError_t few_typed(const AttnCall &c, cudaStream_t s) {
-  return c.d <= 64 ? few_sized<T, 64>(c, s) : few_sized<T, 128>(c, s);
+  return c.d <= 64 ? few_warps<T, 64>(c, s) : few_warps<T, 128>(c, s);
 }
 
 }  // namespace
@@ -252,7 +265,5 @@ cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s) {
          : type == SNACK_BF16 ? few_typed<__nv_bfloat16>(c, s)
                               : few_typed<__half>(c, s);
 }
-
-cudaError_t few_forward_failed(int *flag, cudaStream_t s) { return read_flag(g_few_failed, flag, s); }
 
 }  // namespace snack

@@ -133,6 +133,9 @@ struct Tile<float, DP> {
     const int g = lane >> 2, t = lane & 3;
     const float *pa = a + g * kLd + 2 * t;
     const float *pb = b + turned(g) * kLd + 2 * t;
+    // where few blocks of sums would wait for one another, each product has its own
+    constexpr bool kApart = NB <= 2;
+    float cross[kApart ? NB : 1][2][4] = {};
 #pragma unroll 4
     for (int k = 0; k < DP; k += 8) {
       const float2 a0 = *reinterpret_cast<const float2 *>(pa + k);
@@ -148,11 +151,16 @@ struct Tile<float, DP> {
       for (int n = 0; n < NB; ++n) {
         const float2 y = *reinterpret_cast<const float2 *>(pb + n * 8 * kLd + k);
         const float h0 = tf32_part(y.x), h1 = tf32_part(y.y);
-        mma_k8(acc[n], lo, h0, h1);
-        mma_k8(acc[n], hi, tf32_part(y.x - h0), tf32_part(y.y - h1));
+        mma_k8(kApart ? cross[n][0] : acc[n], lo, h0, h1);
+        mma_k8(kApart ? cross[n][1] : acc[n], hi, tf32_part(y.x - h0), tf32_part(y.y - h1));
         mma_k8(acc[n], hi, h0, h1);
       }
     }
+    if (kApart)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += cross[n][0][i] + cross[n][1][i];
   }
 
   template <int NB>
@@ -295,8 +303,7 @@ __device__ __forceinline__ void add_shares(float (&o)[DP / 8][4], float *room, i
 
 // ------------------------------------------------------------------ forward
 
-// The last step of 16 rows: the sums times 1 / l, and the log of the sum (or,
-// in a split call, both as a part).  One warp.
+// The last step of 16 rows: the sums times 1 / l, and the log of the sum.  One warp.
 template <typename T, int DP>
 __device__ __forceinline__ void finish_rows(const AttnCall &c, const Span &qs, const float (&o)[DP / 8][4],
                                             const float (&m)[2], const float (&l)[2], const int (&token)[2],
@@ -307,16 +314,10 @@ __device__ __forceinline__ void finish_rows(const AttnCall &c, const Span &qs, c
     const float inv = l[h] == 0.f ? 0.f : c.keep_scale / l[h];
     const float lse = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
     const int64_t row = qs.row + token[h];
-    if (c.splits > 1) {
-      const int64_t slot = (blockIdx.y * c.rows + row) * c.heads + head[h];
-      store_row<float, DP>(c.part + slot * c.d, o, h, inv, c.d, lane);
-      if ((lane & 3) == 0) c.part[(int64_t)c.splits * c.rows * c.heads * c.d + slot] = lse;
-    } else {
-      T *out = static_cast<T *>(c.out.p) +
-               (c.q_offsets ? row * c.out.token : qs.seq * c.out.seq + token[h] * c.out.token) + head[h] * c.out.head;
-      store_row<T, DP>(out, o, h, inv, c.d, lane);
-      if ((lane & 3) == 0) c.lse[(int64_t)head[h] * c.rows + row] = lse;
-    }
+    T *out = static_cast<T *>(c.out.p) +
+             (c.q_offsets ? row * c.out.token : qs.seq * c.out.seq + token[h] * c.out.token) + head[h] * c.out.head;
+    store_row<T, DP>(out, o, h, inv, c.d, lane);
+    if ((lane & 3) == 0) c.lse[(int64_t)head[h] * c.rows + row] = lse;
   }
 }
 
@@ -451,7 +452,7 @@ constexpr size_t rows_backward_smem() {
 
 // Gradients of 16 * WM keys and values: the query rows that see them stream past.
 template <typename T, int DP, int WM, int WN, int BQ>
-__global__ void __launch_bounds__(32 * WM * WN) rows_backward_keys(const AttnCall c) {
+__device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
   using Ops = Tile<T, DP>;
   constexpr int kLd = Ops::kLd, NB = BQ / 8, STEP = WN * BQ;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -461,8 +462,8 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_backward_keys(const AttnCal
   __shared__ uint64_t s_draw[2][STEP];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp / WN, wn = warp % WN;
-  const int kh = blockIdx.x % c.key_heads, G = c.group;
-  const Place at = find_tile(c.k_offsets, c.sequences, c.k_tokens, 1, 16 * WM, blockIdx.x / c.key_heads, false);
+  const int kh = block % c.key_heads, G = c.group;
+  const Place at = find_tile(c.k_offsets, c.sequences, c.k_tokens, 1, 16 * WM, block / c.key_heads, false);
   if (at.s < 0) return;
   const Span ks = own_span(c.k_offsets, c.k_lengths, at.s, c.sequences, c.k_tokens);
   const Span qs = other_span(c.q_offsets, c.q_lengths, at.s, c.k_offsets != nullptr, c.sequences, c.q_tokens);
@@ -482,31 +483,47 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_backward_keys(const AttnCal
     T *q = sqd + stage * 2 * STEP * kLd;
     copy_rows<T, DP>(q, qr, row0, STEP, end);
     copy_rows<T, DP>(q + STEP * kLd, dr, row0, STEP, end);
-    for (int i = threadIdx.x; i < STEP; i += blockDim.x) {
-      const int r = row0 + i, token = r / G, head = kh * G + (r - token * G);
-      float lse = INFINITY, delta = 0.f;
-      int lim = 0;
-      if (r < end) {
-        const int64_t place = (int64_t)head * c.rows + qs.row + token;
-        lse = c.lse[place] * kLog2e;
-        delta = c.delta[place];
-        lim = lse == -INFINITY ? 0 : seen_keys(c.causal, token, nq, nk);
-      }
-      s_lse[stage][i] = lse - p_up;
-      s_delta[stage][i] = delta;
-      s_lim[stage][i] = lim;
-      if (c.drop) s_draw[stage][i] = dropout_row(seed, qs.row + token, c.heads, head);
+  };
+  // a thread's row of the next step: loaded before a step is computed, stored after it
+  static_assert(STEP <= 32 * WM * WN, "a thread for each row of a step");
+  float next_lse = 0.f, next_delta = 0.f;
+  int next_lim = 0;
+  uint64_t next_draw = 0;
+  const auto load_row = [&](int row0) {
+    if (threadIdx.x >= STEP) return;
+    const int r = row0 + threadIdx.x, token = r / G, head = kh * G + (r - token * G);
+    next_lse = INFINITY;
+    next_delta = 0.f;
+    next_lim = 0;
+    if (r < end) {
+      const int64_t place = (int64_t)head * c.rows + qs.row + token;
+      next_lse = c.lse[place];
+      next_delta = c.delta[place];
+      next_lim = seen_keys(c.causal, token, nq, nk);
     }
+    if (c.drop) next_draw = dropout_row(seed, qs.row + token, c.heads, head);
+  };
+  const auto store_row_stats = [&](int stage) {
+    if (threadIdx.x >= STEP) return;
+    s_lse[stage][threadIdx.x] = next_lse * kLog2e - p_up;
+    s_delta[stage][threadIdx.x] = next_delta;
+    s_lim[stage][threadIdx.x] = next_lse == -INFINITY ? 0 : next_lim;
+    if (c.drop) s_draw[stage][threadIdx.x] = next_draw;
   };
   const int row_begin = first * G;
   if (row_begin < end) {
     copy_rows<T, DP>(sk, kr, j0, 16 * WM, nk);
     copy_rows<T, DP>(sv, vr, j0, 16 * WM, nk);
     copy_step(0, row_begin);
+    load_row(row_begin);
+    store_row_stats(0);
   }
   copies_commit();
   for (int row0 = row_begin, stage = 0; row0 < end; row0 += STEP, stage ^= 1) {
-    if (row0 + STEP < end) copy_step(stage ^ 1, row0 + STEP);
+    if (row0 + STEP < end) {
+      copy_step(stage ^ 1, row0 + STEP);
+      load_row(row0 + STEP);
+    }
     copies_commit();
     copies_wait<1>();
     __syncthreads();
@@ -537,6 +554,7 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_backward_keys(const AttnCal
       Ops::template sums_by_rows<NB>(dv, p, d, lane);
       Ops::template sums_by_rows<NB>(dk, t, q, lane);
     }
+    if (row0 + STEP < end) store_row_stats(stage ^ 1);
     __syncthreads();
   }
   copies_wait<0>();
@@ -559,15 +577,15 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_backward_keys(const AttnCal
 
 // Gradients of 16 * WM query rows: the keys and values that they see stream past.
 template <typename T, int DP, int WM, int WN, int BN>
-__global__ void __launch_bounds__(32 * WM * WN) rows_backward_queries(const AttnCall c) {
+__device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
   using Ops = Tile<T, DP>;
   constexpr int kLd = Ops::kLd, NB = BN / 8, STEP = WN * BN;
   extern __shared__ __align__(16) unsigned char smem[];
   T *sq = reinterpret_cast<T *>(smem), *sd = sq + 16 * WM * kLd, *skv = sd + 16 * WM * kLd;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp / WN, wn = warp % WN;
-  const int kh = blockIdx.x % c.key_heads, G = c.group;
-  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, G, 16 * WM, blockIdx.x / c.key_heads, c.causal);
+  const int kh = block % c.key_heads, G = c.group;
+  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, G, 16 * WM, block / c.key_heads, c.causal);
   if (at.s < 0) return;
   const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
   const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
@@ -654,6 +672,16 @@ __global__ void __launch_bounds__(32 * WM * WN) rows_backward_queries(const Attn
              head[h] * c.dq.head;
     store_row<T, DP>(row, dq, h, c.scale / ds, c.d, lane);
   }
+}
+
+// The first `key_blocks` blocks take keys, the others queries.  ONLY: the
+// kernel has code for one of them (1: keys, 2: queries) and that one's registers.
+template <typename T, int DP, int WM, int WN, int BN, int ONLY>
+__global__ void __launch_bounds__(32 * WM * WN) rows_backward(const AttnCall c, int key_blocks) {
+  if (ONLY == 1 || (ONLY == 0 && (int)blockIdx.x < key_blocks))
+    keys_of_rows<T, DP, WM, WN, BN>(c, blockIdx.x);
+  else
+    queries_of_rows<T, DP, WM, WN, BN>(c, blockIdx.x - key_blocks);
 }
 
 }  // namespace snack

@@ -15,50 +15,44 @@ struct Shapes {
   static constexpr int kBackward = 32, kFewBackward = kWide ? 16 : 32;
 };
 
-template <typename K>
-inline cudaError_t launch_rows(K kern, int64_t blocks, int threads, size_t smem, const AttnCall &c,
-                               cudaStream_t s) {
-  if (blocks == 0) return cudaSuccess;
-  const cudaError_t e = allow_smem(kern, smem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)blocks), threads, smem, false, s, c);
-}
-
 template <typename T, int DP>
 cudaError_t rows_forward_size(const AttnCall &c, cudaStream_t s) {
   constexpr int kKeys = sizeof(T) == 4 ? 32 : 64;
-  return launch_rows(rows_forward<T, DP, 8, kKeys>,
-                     tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, c.group, 128) * c.key_heads, 256,
-                     rows_forward_smem<T, DP, 8, kKeys>(), c, s);
+  const auto kern = rows_forward<T, DP, 8, kKeys>;
+  constexpr size_t smem = rows_forward_smem<T, DP, 8, kKeys>();
+  const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, c.group, 128) * c.key_heads;
+  if (blocks == 0) return cudaSuccess;
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)blocks), 256, smem, false, s, c);
 }
 
+template <typename T, int DP, int WM, int WN, int BN, int ONLY>
+cudaError_t rows_backward_blocks(const AttnCall &c, int64_t keys, int64_t queries, cudaStream_t s) {
+  if (keys + queries == 0) return cudaSuccess;
+  const auto kern = rows_backward<T, DP, WM, WN, BN, ONLY>;
+  constexpr size_t smem = rows_backward_smem<T, DP, WM, WN, BN>();
+  const cudaError_t e = allow_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)(keys + queries)), 32 * WM * WN, smem, false, s, c, (int)keys);
+}
+
+// Few rows: keys and queries in one launch, side by side (256 tokens of 12
+// heads of 64 in 32 bits took 49 us in two).  Many: one after the other, each
+// with the registers that it needs.
 template <typename T, int DP>
 cudaError_t rows_backward_size(const AttnCall &c, cudaStream_t s) {
   using S = Shapes<T>;
-  cudaError_t e = cudaSuccess;
-  if (c.dk.p || c.dv.p) {
-    const bool ragged = c.k_offsets != nullptr;
-    const int64_t many = tiles_of(ragged, c.sequences, c.k_tokens, 1, 64) * c.key_heads;
-    if (many < device_sms())
-      e = launch_rows(rows_backward_keys<T, DP, 1, 4, S::kFewBackward>,
-                      tiles_of(ragged, c.sequences, c.k_tokens, 1, 16) * c.key_heads, 128,
-                      rows_backward_smem<T, DP, 1, 4, S::kFewBackward>(), c, s);
-    else
-      e = launch_rows(rows_backward_keys<T, DP, 4, 2, S::kBackward>, many, 256,
-                      rows_backward_smem<T, DP, 4, 2, S::kBackward>(), c, s);
-  }
-  if (e == cudaSuccess && c.dq.p) {
-    const bool ragged = c.q_offsets != nullptr;
-    const int64_t many = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 64) * c.key_heads;
-    if (many < device_sms())
-      e = launch_rows(rows_backward_queries<T, DP, 1, 4, S::kFewBackward>,
-                      tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads, 128,
-                      rows_backward_smem<T, DP, 1, 4, S::kFewBackward>(), c, s);
-    else
-      e = launch_rows(rows_backward_queries<T, DP, 4, 2, S::kBackward>, many, 256,
-                      rows_backward_smem<T, DP, 4, 2, S::kBackward>(), c, s);
-  }
-  return e;
+  const auto keys = [&](int rows) {
+    return c.dk.p || c.dv.p ? tiles_of(c.k_offsets != nullptr, c.sequences, c.k_tokens, 1, rows) * c.key_heads : 0;
+  };
+  const auto queries = [&](int rows) {
+    return c.dq.p ? tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, c.group, rows) * c.key_heads : 0;
+  };
+  if (keys(64) + queries(64) < 2 * device_sms())
+    return rows_backward_blocks<T, DP, 1, 4, S::kFewBackward, 0>(c, keys(16), queries(16), s);
+  const cudaError_t e = rows_backward_blocks<T, DP, 4, 2, S::kBackward, 1>(c, keys(64), 0, s);
+  return e != cudaSuccess ? e : rows_backward_blocks<T, DP, 4, 2, S::kBackward, 2>(c, 0, queries(64), s);
 }
 
 template <typename T>

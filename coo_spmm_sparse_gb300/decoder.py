@@ -7,9 +7,15 @@ tokens instead of WikiText-103.
 Every block's four projections (c_attn 768->2304, attention c_proj
 768->768, c_fc 768->3072, MLP c_proj 3072->768) are ``SnackLinear`` layers
 at the given sparsity: their forward and backward run in the library's
-kernels.  Token and position embeddings, layer norms, the attention
-arithmetic (softmax(QK^T / sqrt(d)) V, causal), GELU and the tied LM head
-stay dense PyTorch: the paper makes only the Linear projections sparse.
+kernels, and so does the causal attention between them
+(``snack_packed_attention`` on c_attn's output).  Token and position
+embeddings, layer norms, GELU and the tied LM head stay dense PyTorch: the
+paper makes only the Linear projections sparse.
+
+``dropout`` (0 by default) is GPT-2's: of the embeddings, of the attention's
+probabilities and of a block's outputs before they join the residual stream,
+while the model is in training mode.  Call n of the model draws its masks
+from seeds 4096 * n + place.
 
 The training step is plain SGD on every parameter (the sparse values are
 updated in place through their Parameter views) and, every
@@ -25,7 +31,7 @@ from dataclasses import dataclass
 import torch
 import torch.nn.functional as F
 
-from . import SnackLinear
+from . import SnackLinear, snack_dropout, snack_packed_attention
 
 
 def nnz_for(out: int, inp: int, sparsity_pct: float) -> int:
@@ -46,6 +52,7 @@ class DecoderConfig:
     sparsity: float = 99.0
     std: float = 0.02
     seed: int = 0
+    dropout: float = 0.0
 
 
 class Block(torch.nn.Module):
@@ -68,15 +75,17 @@ class Block(torch.nn.Module):
     def sparse_layers(self):
         return [self.c_attn, self.attn_c_proj, self.c_fc, self.mlp_c_proj]
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
-        B, T, d = x.shape
-        h = self.heads
-        q, k, v = self.c_attn(self.ln_1(x)).split(d, dim=2)
-        q, k, v = (t.view(B, T, h, d // h).transpose(1, 2) for t in (q, k, v))
-        a = F.scaled_dot_product_attention(q, k, v, is_causal=True)
-        x = x + self.attn_c_proj(a.transpose(1, 2).reshape(B, T, d))
-        x = x + self.mlp_c_proj(F.gelu(self.c_fc(self.ln_2(x)), approximate="tanh"))
-        return x
+    def forward(self, x: torch.Tensor, dropout: float = 0.0, seed: int = 0) -> torch.Tensor:
+        a = snack_packed_attention(self.c_attn(self.ln_1(x)), self.heads, dropout=dropout,
+                                   seed=seed)
+        x = join(x, self.attn_c_proj(a), dropout, seed + 1)
+        return join(x, self.mlp_c_proj(F.gelu(self.c_fc(self.ln_2(x)), approximate="tanh")),
+                    dropout, seed + 2)
+
+
+def join(x: torch.Tensor, y: torch.Tensor, dropout: float, seed: int) -> torch.Tensor:
+    """x + y, with dropout of y."""
+    return snack_dropout(y, dropout, seed, residual=x) if dropout else x + y
 
 
 class SparseDecoder(torch.nn.Module):
@@ -94,6 +103,7 @@ class SparseDecoder(torch.nn.Module):
             self.wpe.weight.copy_(torch.randn(cfg.ctx, cfg.d, generator=g) * 0.01)
         self.blocks = torch.nn.ModuleList(Block(cfg, i) for i in range(cfg.layers))
         self.ln_f = torch.nn.LayerNorm(cfg.d, device=dev)
+        self.calls = 0  # with dropout; its masks' seeds follow
         self.to(dev)
 
     def sparse_layers(self):
@@ -103,8 +113,13 @@ class SparseDecoder(torch.nn.Module):
         B, T = idx.shape
         pos = torch.arange(T, device=idx.device)
         x = self.wte(idx) + self.wpe(pos)
-        for b in self.blocks:
-            x = b(x)
+        p = self.cfg.dropout if self.training else 0.0
+        seed = 4096 * self.calls
+        if p:
+            self.calls += 1
+            x = snack_dropout(x, p, seed)
+        for i, b in enumerate(self.blocks):
+            x = b(x, p, seed + 4 * i + 1)
         return F.linear(self.ln_f(x), self.wte.weight)  # tied LM head
 
     def loss(self, idx: torch.Tensor) -> torch.Tensor:

@@ -21,7 +21,8 @@ from __future__ import annotations
 import torch
 import torch.nn.functional as F
 
-from . import SnackAdapters, SnackResidualNorm, snack_clip_grad_norm, snack_residual_norm
+from . import (SnackAdapters, SnackResidualNorm, snack_clip_grad_norm, snack_packed_attention,
+               snack_residual_norm)
 from .decoder import DecoderConfig, SparseDecoder
 
 
@@ -45,11 +46,8 @@ class AdaptedBlock(torch.nn.Module):
 
     def attention(self, h, requests):
         b = self.block
-        B, T, d = h.shape
-        q, k, v = self.project(0, b.c_attn, h, requests).split(d, dim=2)
-        q, k, v = (t.view(B, T, b.heads, d // b.heads).transpose(1, 2) for t in (q, k, v))
-        a = F.scaled_dot_product_attention(q, k, v, is_causal=True)
-        return self.project(1, b.attn_c_proj, a.transpose(1, 2).reshape(B, T, d), requests)
+        a = snack_packed_attention(self.project(0, b.c_attn, h, requests), b.heads)
+        return self.project(1, b.attn_c_proj, a, requests)
 
     def mlp(self, h, requests):
         b = self.block
