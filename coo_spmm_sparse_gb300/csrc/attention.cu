@@ -114,22 +114,76 @@ cudaError_t delta_launch(const AttnCall &c, bool vec, uint32_t *peak, cudaStream
                       : launch_kernel(attention_delta<T, 32, true>, grid, 256, 0, false, s, c, peak);
 }
 
-// The largest |v| of the sequences' keys.
+// One tensor of a call and what is made of it.
+struct Source {
+  Strided from;
+  const int32_t *offsets, *lengths;
+  int tokens, heads;
+  int64_t rows;    // tokens of all sequences
+  uint32_t *peak;  // receives the bits of the largest magnitude
+  __half *parts;   // receives the float16 parts
+};
+struct Sources {
+  Source t[4];
+};
+
+// The largest magnitude of each tensor, over the sequences' tokens.  Grid: y = tensor.
 template <typename T>
-__global__ void __launch_bounds__(256) attention_peak(const AttnCall c, int64_t rows, uint32_t *peak) {
+__global__ void __launch_bounds__(256) attention_peak(const Sources all, int sequences, int d) {
+  const Source &t = all.t[blockIdx.y];
   const int lane = threadIdx.x % kTeam;
   float top = 0.f;
-  const int64_t items = rows * c.key_heads;
+  const int64_t items = t.rows * t.heads;
   for (int64_t item = (int64_t)blockIdx.x * (256 / kTeam) + threadIdx.x / kTeam; item < items;
        item += (int64_t)gridDim.x * (256 / kTeam)) {
-    const int64_t row = item / c.key_heads;
+    const int64_t row = item / t.heads;
     int seq, token;
-    if (!in_sequence(c.k_offsets, c.k_lengths, c.sequences, c.k_tokens, row, &seq, &token)) continue;
-    const T *v = static_cast<const T *>(c.v.p) + seq * c.v.seq + token * c.v.token +
-                 (item - row * c.key_heads) * c.v.head;
-    for (int col = lane; col < c.d; col += kTeam) top = larger(top, to_float(v[col]));
+    if (!in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token)) continue;
+    const T *v = static_cast<const T *>(t.from.p) + seq * t.from.seq + token * t.from.token +
+                 (item - row * t.heads) * t.from.head;
+    for (int col = lane; col < d; col += kTeam) top = larger(top, to_float(v[col]));
   }
-  block_peak(top, peak);
+  block_peak(top, t.peak);
+}
+
+// Every tensor as two float16 parts of its elements times the power of two that
+// brings its largest to [2^14, 2^15): rows of 64 high and 64 low halves, zeros
+// behind the head size and for tokens outside every sequence.  Grid: y = tensor.
+__global__ void __launch_bounds__(256) split_parts(const Sources all, int sequences, int d) {
+  const Source &t = all.t[blockIdx.y];
+  const int col = threadIdx.x % kTeam * 4;
+  const float by = exp2f((float)power_to_half(*t.peak));
+  const int64_t items = t.rows * t.heads;
+  for (int64_t item = (int64_t)blockIdx.x * (256 / kTeam) + threadIdx.x / kTeam; item < items;
+       item += (int64_t)gridDim.x * (256 / kTeam)) {
+    const int64_t row = item / t.heads;
+    int seq, token;
+    float x[4] = {};
+    if (in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token)) {
+      const float *v = static_cast<const float *>(t.from.p) + seq * t.from.seq + token * t.from.token +
+                       (item - row * t.heads) * t.from.head + col;
+      if ((reinterpret_cast<uintptr_t>(v) & 15) == 0 && col + 4 <= d) {
+        const float4 f = *reinterpret_cast<const float4 *>(v);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < d) x[e] = v[e];
+      }
+    }
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float a, b;
+      const float u = x[2 * e] * by, w = x[2 * e + 1] * by;
+      hi[e] = pack2<__half>(u, w);
+      unpack2<__half>(hi[e], a, b);
+      lo[e] = pack2<__half>(u - a, w - b);
+    }
+    __half *to = t.parts + item * 128 + col;
+    *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2 *>(to + 64) = make_uint2(lo[0], lo[1]);
+  }
 }
 
 // Joins the parts of a split forward call: a block for each row and head, a
@@ -241,34 +295,117 @@ AttnCall call_of(const snack_attention_args *a) {
   return c;
 }
 
-// How a forward call is cut: few rows (16 to a block) where blocks of 128
-// would leave SMs idle, and its keys in parts where even those do.
-struct Cut {
-  bool tiles = false, few = false;
+// How a call is computed, and what of the workspace it takes.
+struct Plan {
+  bool tiles = false, few = false;  // on tcgen05; in blocks of 16 rows
   int splits = 1, chunk = 0;
+  size_t delta = 0, parts[4] = {}, bytes = 0;  // offsets: after the peaks; q, k, v, dout
 };
-Cut cut_of(const AttnCall &c, int type) {
-  Cut cut;
-  cut.tiles = c.q_tokens >= 64 && tile_forward_fits(c, type);
-  if (cut.tiles) return cut;
+constexpr size_t kPeaks = 256;
+
+// The parts of 32-bit operands.
+void plan_parts(Plan *p, const AttnCall &c, bool backward) {
+  const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
+  const int64_t rows[4] = {c.rows * c.heads, keys * c.key_heads, keys * c.key_heads, backward ? c.rows * c.heads : 0};
+  for (int i = 0; i < 4; ++i) {
+    p->parts[i] = p->bytes;
+    p->bytes += rows[i] * 128 * sizeof(__half);
+  }
+}
+
+constexpr double kTilesFrom32 = 4e6;
+// 16-bit calls go to the tiles from 64 query tokens on.  32-bit ones pay for
+// making the parts first (two launches, three or four tensors read twice).
+bool worth_tiles(const AttnCall &c, int type) {
+  if (c.q_tokens < 64 || c.k_tokens < 64) return false;
+  return type != SNACK_F32 || (double)c.rows * c.heads * c.k_tokens >= kTilesFrom32;
+}
+
+// Few rows (16 to a block) where blocks of 128 would leave SMs idle, and the
+// keys in parts where even those do.
+Plan plan_forward(const AttnCall &c, int type) {
+  Plan p;
+  p.tiles = worth_tiles(c, type) && tile_forward_fits(c, type);
+  if (p.tiles) {
+    if (type == SNACK_F32) {
+      p.bytes = kPeaks;
+      plan_parts(&p, c, false);
+    }
+    return p;
+  }
   const bool ragged = c.q_offsets != nullptr;
   const int64_t sms = device_sms();
-  cut.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
-  if (!cut.few) return cut;
+  p.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
+  if (!p.few) return p;
   const int64_t blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
   // chunks of 512 keys at least: below that a block starts and ends more than it reads
   const int64_t want = blocks ? 16 * sms / blocks : 1, most = c.k_tokens / 512;
   const int64_t splits = std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)kMostSplits));
-  if (splits == 1) return cut;
-  cut.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 64);
-  cut.splits = (int)((c.k_tokens + cut.chunk - 1) / cut.chunk);
-  return cut;
+  if (splits == 1) return p;
+  p.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 64);
+  p.splits = (int)((c.k_tokens + p.chunk - 1) / p.chunk);
+  if (p.splits > 1) p.bytes = (size_t)p.splits * c.rows * c.heads * (c.d + 1) * sizeof(float);
+  return p;
+}
+
+Plan plan_backward(const AttnCall &c, int type) {
+  Plan p;
+  p.bytes = kPeaks;
+  p.delta = p.bytes;
+  p.bytes += round_up(c.rows * c.heads * (int64_t)sizeof(float), 256);
+  p.tiles = worth_tiles(c, type) && tile_backward_fits(c, type);
+  if (p.tiles && type == SNACK_F32) plan_parts(&p, c, true);
+  return p;
+}
+
+// q, k, v and dout of a call; peaks in the order that AttnCall has them in.
+Sources sources_of(const AttnCall &c, const Plan &p, char *workspace) {
+  Sources s;
+  uint32_t *const peak = reinterpret_cast<uint32_t *>(workspace);
+  const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
+  const Strided *const from[4] = {&c.q, &c.k, &c.v, &c.dout};
+  const int at[4] = {2, 3, 1, 0};
+  for (int i = 0; i < 4; ++i) {
+    const bool own = i == 0 || i == 3;
+    s.t[i] = Source{*from[i], own ? c.q_offsets : c.k_offsets, own ? c.q_lengths : c.k_lengths,
+                    own ? c.q_tokens : c.k_tokens, own ? c.heads : c.key_heads, own ? c.rows : keys, peak + at[i],
+                    reinterpret_cast<__half *>(workspace + p.parts[i])};
+  }
+  return s;
+}
+
+unsigned spread(int64_t items) {
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 15) / 16, 16 * device_sms()));
+}
+
+// Makes the parts of 32-bit operands; `tensors`: 3 (forward) or 4.
+cudaError_t make_parts(AttnCall *c, const Plan &p, int tensors, char *workspace, SplitParts *parts, cudaStream_t s) {
+  const Sources all = sources_of(*c, p, workspace);
+  cudaError_t e = cudaMemsetAsync(workspace, 0, 4 * sizeof(uint32_t), s);
+  int64_t most = 0;
+  for (int i = 0; i < tensors; ++i) most = std::max(most, all.t[i].rows * all.t[i].heads);
+  const dim3 grid(spread(most), (unsigned)tensors);
+  if (e == cudaSuccess) e = launch_kernel(attention_peak<float>, grid, 256, 0, false, s, all, c->sequences, c->d);
+  if (e == cudaSuccess) e = launch_kernel(split_parts, grid, 256, 0, false, s, all, c->sequences, c->d);
+  c->peak = reinterpret_cast<const uint32_t *>(workspace);
+  *parts = SplitParts{all.t[0].parts, all.t[1].parts, all.t[2].parts, all.t[3].parts};
+  return e;
 }
 
 template <typename T>
-cudaError_t forward_typed(const AttnCall &c, const Cut &cut, int type, cudaStream_t s) {
-  if (cut.tiles) return tile_forward_launch(c, type, s);
-  if (!cut.few) return rows_forward_launch<T>(c, s);
+cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
+  if (p.tiles) {
+    SplitParts parts = {};
+    if (type == SNACK_F32) {
+      const cudaError_t e = make_parts(&c, p, 3, workspace, &parts, s);
+      if (e != cudaSuccess) return e;
+    }
+    return tile_forward_launch(c, type, parts, s);
+  }
+  if (!p.few) return rows_forward_launch<T>(c, s);
+  c.splits = p.splits;
+  c.chunk = p.chunk;
+  c.part = reinterpret_cast<float *>(workspace);
   cudaError_t e = few_forward_launch(c, type, s);
   if (e == cudaSuccess && c.splits > 1)
     e = launch_kernel(join_splits<T>, dim3((unsigned)(c.rows * c.heads)), 128, 0, true, s, c);
@@ -276,19 +413,24 @@ cudaError_t forward_typed(const AttnCall &c, const Cut &cut, int type, cudaStrea
 }
 
 template <typename T>
-cudaError_t backward_typed(AttnCall c, int type, uint32_t *peak, cudaStream_t s) {
+cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   cudaError_t e = cudaSuccess;
-  if (peak) {
-    if ((e = cudaMemsetAsync(peak, 0, 2 * sizeof(uint32_t), s)) != cudaSuccess) return e;
-    const int64_t rows = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
-    if (rows) {
-      const int64_t blocks = std::min<int64_t>((rows * c.key_heads + 15) / 16, 8 * device_sms());
-      e = launch_kernel(attention_peak<T>, dim3((unsigned)blocks), 256, 0, false, s, c, rows, peak + 1);
-      if (e != cudaSuccess) return e;
-    }
+  SplitParts parts = {};
+  uint32_t *peak = nullptr;  // where delta leaves the largest |dout|
+  if (p.tiles && type == SNACK_F32) {
+    e = make_parts(&c, p, 4, workspace, &parts, s);
+  } else if (type == SNACK_F16) {
+    peak = reinterpret_cast<uint32_t *>(workspace);
     c.peak = peak;
+    e = cudaMemsetAsync(peak, 0, 2 * sizeof(uint32_t), s);
+    Sources v = sources_of(c, p, workspace);
+    v.t[0] = v.t[2];
+    const int64_t items = v.t[0].rows * v.t[0].heads;
+    if (e == cudaSuccess && items)
+      e = launch_kernel(attention_peak<T>, dim3(spread(items)), 256, 0, false, s, v, c.sequences, c.d);
   }
+  if (e != cudaSuccess) return e;
   if (c.rows) {
     const auto even = [](const Strided &t) {
       return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
@@ -296,8 +438,7 @@ cudaError_t backward_typed(AttnCall c, int type, uint32_t *peak, cudaStream_t s)
     e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out), peak, s);
     if (e != cudaSuccess) return e;
   }
-  if (c.q_tokens >= 64 && c.k_tokens >= 64 && tile_backward_fits(c, type)) return tile_backward_launch(c, type, s);
-  return rows_backward_launch<T>(c, s);
+  return p.tiles ? tile_backward_launch(c, type, parts, s) : rows_backward_launch<T>(c, s);
 }
 
 }  // namespace
@@ -307,9 +448,7 @@ using namespace snack;
 
 extern "C" size_t snack_attention_forward_workspace(const snack_attention_args *a) {
   if (!a || check_args(a) != SNACK_OK) return 0;
-  const AttnCall c = call_of(a);
-  const Cut cut = cut_of(c, a->type);
-  return cut.splits > 1 ? (size_t)cut.splits * c.rows * c.heads * (c.d + 1) * sizeof(float) : 0;
+  return plan_forward(call_of(a), a->type).bytes;
 }
 
 extern "C" snack_status snack_attention_forward(const snack_attention_args *a, void *out, const int64_t *out_stride,
@@ -319,19 +458,16 @@ extern "C" snack_status snack_attention_forward(const snack_attention_args *a, v
   AttnCall c = call_of(a);
   if (c.rows == 0) return SNACK_OK;
   if (!out || !out_stride || !lse) return bad("out, its strides or lse is NULL");
+  // the plan knows the arguments alone, so that it is the one the workspace was asked for
+  const Plan p = plan_forward(c, a->type);
+  if (p.bytes && !workspace) return bad("workspace is NULL");
   c.out = strided(out, out_stride);
   c.lse = lse;
-  const Cut cut = cut_of(c, a->type);
-  c.splits = cut.splits;
-  c.chunk = cut.chunk;
-  if (cut.splits > 1) {
-    if (!workspace) return bad("workspace is NULL");
-    c.part = static_cast<float *>(workspace);
-  }
+  char *const ws = static_cast<char *>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->type == SNACK_F32    ? forward_typed<float>(c, cut, a->type, s)
-                        : a->type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, cut, a->type, s)
-                                                : forward_typed<__half>(c, cut, a->type, s);
+  const cudaError_t e = a->type == SNACK_F32    ? forward_typed<float>(c, p, a->type, ws, s)
+                        : a->type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, p, a->type, ws, s)
+                                                : forward_typed<__half>(c, p, a->type, ws, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention forward");
 }
 
@@ -346,8 +482,7 @@ extern "C" snack_status snack_attention_error(int *flag, void *stream) {
 
 extern "C" size_t snack_attention_backward_workspace(const snack_attention_args *a) {
   if (!a || check_args(a) != SNACK_OK) return 0;
-  const AttnCall c = call_of(a);
-  return (size_t)c.rows * c.heads * sizeof(float) + (a->type == SNACK_F16 ? 16 : 0);
+  return plan_backward(call_of(a), a->type).bytes;
 }
 
 extern "C" snack_status snack_attention_backward(const snack_attention_args *a, const snack_attention_grads *g,
@@ -356,22 +491,21 @@ extern "C" snack_status snack_attention_backward(const snack_attention_args *a, 
   if (st != SNACK_OK) return st;
   if (!g) return bad("grads is NULL");
   AttnCall c = call_of(a);
-  if (c.rows && (!g->dout || !g->out || !g->lse || !workspace)) return bad("dout, out, lse or workspace is NULL");
+  if (!workspace) return bad("workspace is NULL");
+  if (c.rows && (!g->dout || !g->out || !g->lse)) return bad("dout, out or lse is NULL");
   c.dout = strided(g->dout, g->dout_stride);
+  // (what dout decides, whether a 16-bit call can go to the tiles, takes no workspace)
+  const Plan p = plan_backward(c, a->type);
   c.out = strided(g->out, g->out_stride);
   c.dq = strided(g->dq, g->dq_stride);
   c.dk = strided(g->dk, g->dk_stride);
   c.dv = strided(g->dv, g->dv_stride);
   c.lse = const_cast<float *>(g->lse);
-  uint32_t *peak = nullptr;
-  if (a->type == SNACK_F16) {
-    if (!workspace) return bad("workspace is NULL");
-    peak = static_cast<uint32_t *>(workspace);
-  }
-  c.delta = reinterpret_cast<float *>(static_cast<char *>(workspace) + (peak ? 16 : 0));
+  char *const ws = static_cast<char *>(workspace);
+  c.delta = reinterpret_cast<float *>(ws + p.delta);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->type == SNACK_F32    ? backward_typed<float>(c, a->type, peak, s)
-                        : a->type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, a->type, peak, s)
-                                                : backward_typed<__half>(c, a->type, peak, s);
+  const cudaError_t e = a->type == SNACK_F32    ? backward_typed<float>(c, p, a->type, ws, s)
+                        : a->type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, p, a->type, ws, s)
+                                                : backward_typed<__half>(c, p, a->type, ws, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention backward");
 }

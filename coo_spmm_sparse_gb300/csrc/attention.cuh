@@ -17,7 +17,7 @@ struct AttnCall {
   float *lse;    // [heads][rows]: log of the sum of exp(scale * q . k), -inf where no key is seen
   float *delta;  // [heads][rows]: dout . out
   float *part;   // partial results of a split call
-  const uint32_t *peak;  // bits of the largest |dout| and |v| (float16)
+  const uint32_t *peak;  // bits of the largest |dout|, |v|, |q|, |k| (float16: the first two)
   int64_t rows;  // rows of lse for a head: all tokens of q
   int sequences, q_tokens, k_tokens;
   int heads, key_heads, group, d;
@@ -135,13 +135,18 @@ cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
 // The forward call of few rows (attention_few.cu).
 cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s);
 
+// Where the float16 parts of 32-bit operands are: [tokens][heads][high 64, low 64].
+struct SplitParts {
+  void *q, *k, *v, *dout;
+};
+
 // Those of attention on tcgen05 (attention_tiles*.cu): which calls they take,
 // and whether one of their bounded waits has run out since the last question.
 bool tile_forward_fits(const AttnCall &c, int type);
-cudaError_t tile_forward_launch(const AttnCall &c, int type, cudaStream_t s);
+cudaError_t tile_forward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s);
 cudaError_t tile_forward_failed(int *flag, cudaStream_t s);
 bool tile_backward_fits(const AttnCall &c, int type);
-cudaError_t tile_backward_launch(const AttnCall &c, int type, cudaStream_t s);
+cudaError_t tile_backward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s);
 cudaError_t tile_backward_failed(int *flag, cudaStream_t s);
 
 // Reads a sticky flag of the current device and clears it.
@@ -173,6 +178,13 @@ __device__ __forceinline__ float half_ds_scale(const AttnCall &c) {
   const float most = 2.f * (float)c.d * __uint_as_float(c.peak[0]) * __uint_as_float(c.peak[1]) * c.keep_scale;
   if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
   return exp2f((float)min(max(14 - ilogbf(most), -100), 100));
+}
+
+// The power of two that brings the largest magnitude to [2^14, 2^15).
+__device__ __forceinline__ int power_to_half(uint32_t peak) {
+  const float v = __uint_as_float(peak);
+  if (!(v > 0.f) || !(v < INFINITY)) return 0;
+  return min(max(14 - ilogbf(v), -113), 120);
 }
 
 // Keys that query i of a sequence sees: j < seen_keys(...).

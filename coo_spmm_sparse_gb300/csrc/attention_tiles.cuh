@@ -1,4 +1,5 @@
-// Attention on tcgen05: 16-bit types, tiles of 128 x 128.
+// Attention on tcgen05: tiles of 128 x 128; 16-bit types, and 32-bit floats
+// with head sizes up to 64.
 //
 // TMA brings tiles of 128 tokens of a head into shared memory; one thread
 // issues the MMAs; eight warps read the scores from tensor memory, a thread a
@@ -10,6 +11,15 @@
 // padding.  Scores of them are masked; rows of the operand that meets masked
 // (zero) entries in the second product are set to zero, since what lies there
 // may not be finite.
+//
+// 32-bit floats arrive as two float16 parts of a tensor scaled by a power of two
+// to below 2^15, x = hi + lo (made by split_parts in attention.cu): 22 bits of
+// everything above 2^-17 of the tensor's largest, and never more than 2^-39 of
+// that off.  A row has its 64 high halves, then its 64 low ones, and a product
+// is hi*hi + hi*lo + lo*hi; probabilities (2^14 fold) and gradients of scores
+// are split the same way.  Three products at the rate of 16 bits cost half of
+// three tf32 ones.  The sums leave tensor memory after every tile for 32-bit
+// sums in the rows' registers: the matrix unit cuts off what it adds.
 #pragma once
 
 #include "attention.cuh"
@@ -30,6 +40,20 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9;
 struct TileMaps {
   CUtensorMap q, k, v, dout;
 };
+
+template <typename T>
+struct Operand {
+  using type = T;
+  static constexpr bool kSplit = false;
+};
+template <>
+struct Operand<float> {
+  using type = __half;
+  static constexpr bool kSplit = true;
+};
+// Columns of a tile in shared memory.
+template <typename T, int DP>
+__host__ __device__ constexpr int wide() { return Operand<T>::kSplit ? 2 * DP : DP; }
 
 // Bytes of a tile: DP / 64 blocks of 128 rows of 128 bytes.
 template <int DP>
@@ -83,19 +107,111 @@ __device__ __forceinline__ void store_sums(uint32_t from, T *row, float factor, 
       tc::wait_loads();
     }
     if (row) {
+      const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (some && !zero) {
-          u.x = pack2<T>(v[i] * factor, v[i + 1] * factor);
-          u.y = pack2<T>(v[i + 2] * factor, v[i + 3] * factor);
-          u.z = pack2<T>(v[i + 4] * factor, v[i + 5] * factor);
-          u.w = pack2<T>(v[i + 6] * factor, v[i + 7] * factor);
+        if (c + i >= d) break;  // (the head size is a multiple of eight)
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          u[e] = some && !zero ? pack2<T>(v[i + 2 * e] * factor, v[i + 2 * e + 1] * factor) : 0;
+        if (vec) {
+          *reinterpret_cast<uint4 *>(row + c + i) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+          unsigned short *const to = reinterpret_cast<unsigned short *>(row + c + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            to[2 * e] = (unsigned short)u[e];
+            to[2 * e + 1] = (unsigned short)(u[e] >> 16);
+          }
         }
-        if (c + i < d) *reinterpret_cast<uint4 *>(row + c + i) = u;
       }
     }
     __syncwarp();
+  }
+}
+
+// Rows a times rows b, over the head size.
+template <typename T, int DP>
+__device__ __forceinline__ void products(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t kind = tc::mma_kind<typename Operand<T>::type>(kTile, false);
+  if constexpr (!Operand<T>::kSplit) {
+    tc::mma_rows<DP>(d, a, b, kBlock, kind);
+  } else {
+    constexpr uint32_t low = kBlock / 16;
+#pragma unroll
+    for (int k = 0; k < DP; k += 16) tc::mma(d, a + low + k / 8, b + k / 8, kind, k > 0);
+#pragma unroll
+    for (int k = 0; k < DP; k += 16) tc::mma(d, a + k / 8, b + low + k / 8, kind, true);
+#pragma unroll
+    for (int k = 0; k < DP; k += 16) tc::mma(d, a + k / 8, b + k / 8, kind, true);
+  }
+}
+// Probabilities (or gradients of scores) in tensor memory, halves of 64 tokens
+// 64 columns apart, times rows b: tokens [from, from + K).  Split: every 32
+// tokens have their high parts, then their low ones (in the columns that their
+// 32 sums had), and the result always begins anew.
+template <typename T, int DP, int K>
+__device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint32_t b, bool add, int from = 0) {
+  constexpr uint32_t kind = tc::mma_kind<typename Operand<T>::type>(DP, true);
+  if constexpr (!Operand<T>::kSplit) {
+    tc::mma_sums<K>(d, a, kTile / 2, kTile / 2, b, kind, add, from);
+  } else {
+    constexpr uint32_t low = kBlock / 16;
+#pragma unroll
+    for (int k = from; k < from + K; k += 16) {
+      const uint32_t hi = a + k / 32 * 32 + k % 32 / 2;
+      tc::mma_tmem(d, hi + 16, b + k * 8, kind, k > 0);
+      tc::mma_tmem(d, hi, b + low + k * 8, kind, true);
+      tc::mma_tmem(d, hi, b + k * 8, kind, true);
+    }
+  }
+}
+
+// 32 values of a row as high and low parts: columns [0, 16) and [16, 32) from `at` on.
+__device__ __forceinline__ void store_parts(uint32_t at, const float *v) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float a, b;
+    hi[e] = pack2<__half>(v[2 * e], v[2 * e + 1]);
+    unpack2<__half>(hi[e], a, b);
+    lo[e] = pack2<__half>(v[2 * e] - a, v[2 * e + 1] - b);
+  }
+  tc::store16(at, hi);
+  tc::store16(at + 16, lo);
+}
+
+// o += N columns of tensor memory.
+template <int N>
+__device__ __forceinline__ void add_sums(float *o, uint32_t from) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    float v[32];
+    tc::load32(from + c, v);
+    tc::wait_loads();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[c + e] += v[e];
+  }
+}
+
+// Stores N columns of a row, or those of them below d; row NULL: nothing.
+template <int N>
+__device__ __forceinline__ void store_floats(float *row, const float *v, float factor, int d, bool zero) {
+  if (!row) return;
+  const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0 && d % 4 == 0;
+#pragma unroll
+  for (int c = 0; c < N; c += 4) {
+    const float4 f = zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                          : make_float4(v[c] * factor, v[c + 1] * factor, v[c + 2] * factor, v[c + 3] * factor);
+    if (vec) {
+      if (c < d) *reinterpret_cast<float4 *>(row + c) = f;
+    } else {
+      if (c < d) row[c] = f.x;
+      if (c + 1 < d) row[c + 1] = f.y;
+      if (c + 2 < d) row[c + 2] = f.z;
+      if (c + 3 < d) row[c + 3] = f.w;
+    }
   }
 }
 
@@ -131,15 +247,30 @@ static inline bool map_of(CUtensorMap *m, int type, const Strided &t, int64_t d,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// What TMA and 16-byte stores need: 16-byte aligned rows, and no dimension
-// that repeats the same memory.
+// What TMA needs: 16-byte aligned rows, and no dimension that repeats the same
+// memory.
 static inline bool even(const Strided &t, int64_t heads, int64_t tokens, int64_t seqs) {
   const auto good = [](int64_t n, int64_t s) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 38); };
   return aligned_to(t.p, 16) && good(heads, t.head) && good(tokens, t.token) && good(seqs, t.seq);
 }
 
 static inline bool tiles_fit(const AttnCall &c, int type) {
-  return type != SNACK_F32 && c.d % 8 == 0 && c.scale > 0.f && c.k_tokens > 0 && c.q_tokens > 0 && c.sequences > 0;
+  return (type == SNACK_F32 ? c.d <= 64 : c.d % 8 == 0) && c.scale > 0.f && c.k_tokens > 0 && c.q_tokens > 0 &&
+         c.sequences > 0;
+}
+
+// The maps of a call's operands: its tensors, or their float16 parts.
+static inline bool maps_of(TileMaps *m, const AttnCall &c, int type, const SplitParts &parts, bool backward) {
+  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
+  const bool split = type == SNACK_F32;
+  const auto map = [&](CUtensorMap *to, const Strided &t, void *part, int64_t heads, int64_t tokens, int64_t seqs) {
+    const int64_t row = 2 * 64;
+    return split ? map_of(to, SNACK_F16, Strided{part, tokens * heads * row, heads * row, row}, row, heads, tokens, seqs)
+                 : map_of(to, type, t, c.d, heads, tokens, seqs);
+  };
+  return map(&m->q, c.q, parts.q, c.heads, c.q_tokens, qn) && map(&m->k, c.k, parts.k, c.key_heads, c.k_tokens, kn) &&
+         map(&m->v, c.v, parts.v, c.key_heads, c.k_tokens, kn) &&
+         (!backward || map(&m->dout, c.dout, parts.dout, c.heads, c.q_tokens, qn));
 }
 
 }  // namespace snack

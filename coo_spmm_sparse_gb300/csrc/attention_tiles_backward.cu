@@ -11,10 +11,35 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = kTile / 2;  // columns of a tile that a warpgroup takes
 constexpr int kStatWarp = 10;
 
+// 32 values of a row, columns [x, x + 32) of a warpgroup's 64 that begin at
+// `at`, as the left operand of a product.
+template <typename T>
+__device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) {
+  if constexpr (Operand<T>::kSplit) {
+    store_parts(at + x, v);
+  } else {
+    uint32_t out[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) out[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+    tc::store16(at + x / 2, out);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ float ds_scale(const AttnCall &c) {
-  if constexpr (!std::is_same<T, __half>::value) return 1.f;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return 1.f;
   return half_ds_scale(c);
+}
+
+// Split operands are scaled by powers of two: what takes them out again.
+struct Scales {
+  float scores, dprobs, q, k, dout;
+};
+template <typename T>
+__device__ __forceinline__ Scales scales_of(const AttnCall &c) {
+  if constexpr (!Operand<T>::kSplit) return Scales{c.scale_log2, 1.f, 1.f, 1.f, 1.f};
+  const auto back = [&](int i) { return exp2f((float)-power_to_half(c.peak[i])); };
+  return Scales{c.scale_log2 * back(2) * back(3), back(0) * back(1), back(2), back(3), back(0)};
 }
 
 // ------------------------------------------------------------------ keys and values
@@ -28,8 +53,8 @@ struct KeyBars {
   alignas(16) float delta[2][kTile];
 };
 
-template <int DP>
-constexpr size_t keys_smem() { return 1024 + (size_t)6 * tile_bytes<DP>(); }
+template <int W>
+constexpr size_t keys_smem() { return 1024 + (size_t)6 * tile_bytes<W>(); }
 
 // A tile of 128 keys (rows of every product: a thread has a key), past which
 // the query tiles of all heads that share it stream:
@@ -41,10 +66,12 @@ constexpr size_t keys_smem() { return 1024 + (size_t)6 * tile_bytes<DP>(); }
 template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_keys(const AttnCall c, const __grid_constant__ TileMaps maps) {
+  constexpr int W = wide<T, DP>();
+  constexpr bool kSplit = Operand<T>::kSplit, kUp = !std::is_same<T, __nv_bfloat16>::value;  // kUp: float16 operands
   extern __shared__ unsigned char raw[];
   __shared__ KeyBars bars;
-  unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<DP>();
-  unsigned char *const sq = sv + tile_bytes<DP>(), *const sd = sq + 2 * tile_bytes<DP>();
+  unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<W>();
+  unsigned char *const sq = sv + tile_bytes<W>(), *const sd = sq + 2 * tile_bytes<W>();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
@@ -94,8 +121,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int cut_phase = 0, n = 0, parts = 0;
       bool ok = true;
       if (lane == 0) {
-        copy_tile<DP>(sk, &maps.k, &bars.kv, kh, k_token + j0, ks.seq);
-        copy_tile<DP>(sv, &maps.v, &bars.kv, kh, k_token + j0, ks.seq);
+        copy_tile<W>(sk, &maps.k, &bars.kv, kh, k_token + j0, ks.seq);
+        copy_tile<W>(sv, &maps.v, &bars.kv, kh, k_token + j0, ks.seq);
       }
       for (; n < all && ok; ++n) {
         const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile, head = kh * G + g;
@@ -105,12 +132,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ok = __all_sync(0xffffffffu, tc::bar_wait(side ? &bars.d_empty[slot] : &bars.q_empty[slot],
                                                       (n / 2 - 1) & 1, failed));
           if (!ok) break;
-          unsigned char *const to = (side ? sd : sq) + slot * tile_bytes<DP>();
+          unsigned char *const to = (side ? sd : sq) + slot * tile_bytes<W>();
           const CUtensorMap *const map = side ? &maps.dout : &maps.q;
           if (q0 + kTile > nq)
-            ok = copy_tile_cut<DP>(to, map, full, &bars.cut, &cut_phase, head, q_token + q0, qs.seq, nq - q0, failed);
+            ok = copy_tile_cut<W>(to, map, full, &bars.cut, &cut_phase, head, q_token + q0, qs.seq, nq - q0, failed);
           else if (lane == 0)
-            copy_tile<DP>(to, map, full, head, q_token + q0, qs.seq);
+            copy_tile<W>(to, map, full, head, q_token + q0, qs.seq);
           __syncwarp();
           if (ok) ++parts;
         }
@@ -124,8 +151,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else if (warp == kMmaWarp) {
       // the whole warp goes along, so that descriptors stay in uniform registers
       if (all > 0) {
-        constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
-        constexpr uint32_t kStep = tile_bytes<DP>() / 16;
+        constexpr uint32_t kStep = tile_bytes<W>() / 16;
         const bool leader = tc::elect_one();
         const uint32_t k0 = tc::desc_rows(tc::smem_addr(sk)), v0 = tc::desc_rows(tc::smem_addr(sv));
         const uint32_t q0 = tc::desc_rows(tc::smem_addr(sq)), d0 = tc::desc_rows(tc::smem_addr(sd));
@@ -139,7 +165,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.q_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            tc::mma_rows<DP>(t_s, k0, q0 + (n & 1) * kStep, kBlock, by_rows);
+            products<T, DP>(t_s, k0, q0 + (n & 1) * kStep);
             tc::commit(&bars.scores);
           }
           __syncwarp();
@@ -148,7 +174,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.d_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            tc::mma_rows<DP>(t_dp, v0, d0 + (n & 1) * kStep, kBlock, by_rows);
+            products<T, DP>(t_dp, v0, d0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs);
           }
           __syncwarp();
@@ -159,7 +185,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = wait(&bars.probs, n & 1);
           if (!ok) break;
           if (leader) {
-            tc::mma_sums<kTile>(t_dv, t_s, kHalf, kHalf, d0c + (n & 1) * kStep, by_cols, n > 0);
+            sums<T, DP, kTile>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.d_empty[n & 1]);
           }
           __syncwarp();
@@ -167,7 +193,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
           if (leader) {
-            tc::mma_sums<kTile>(t_dk, t_dp, kHalf, kHalf, q0c + (n & 1) * kStep, by_cols, n > 0);
+            sums<T, DP, kTile>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.q_empty[n & 1]);
           }
           __syncwarp();
@@ -182,7 +208,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     } else if (warp == kStatWarp) {
-      const float up = std::is_same<T, __half>::value ? kHalfP : 0.f;
+      const float up = kUp ? kHalfP : 0.f;
       for (int n = 0; n < all; ++n) {
         const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile;
         const int64_t place = (int64_t)(kh * G + g) * c.rows + qs.row;
@@ -209,8 +235,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
     const float ds = ds_scale<T>(c);
-    const float2 cs2 = make_float2(c.scale_log2, c.scale_log2);
-    const float ds_by_p = std::is_same<T, __half>::value ? ds * exp2f(-kHalfP) : 1.f;
+    const Scales by = scales_of<T>(c);
+    const float2 cs2 = make_float2(by.scores, by.scores);
+    const float ds_by_p = kUp ? ds * exp2f(-kHalfP) : 1.f;
+    float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
+    constexpr int kDpChunk = kSplit ? 32 : kHalf;  // what registers leave room for
     const uint64_t seed = DROP ? c.draws() : 0;
     bool ok = true;
     for (int n = 0; n < all; ++n) {
@@ -235,6 +264,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                        tc::bar_wait(&bars.scores, n & 1, failed));
       if (!ok) break;
       tc::fence_after();
+      if constexpr (kSplit)
+        if (w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile);  // dV of the tile before
       float p[kHalf];
       tc::load32(s_at, p);
       tc::load32(s_at + 32, p + 32);
@@ -255,15 +286,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int x = 0; x < kHalf; ++x) p[x] = x >= lo ? p[x] : 0.f;
       }
-      {
-        uint32_t out[32];
 #pragma unroll
-        for (int x = 0; x < kHalf; x += 2) {
-          const float a = !DROP || (kept[x & 3] >> (x & ~3) & 1) ? p[x] : 0.f;
-          const float b = !DROP || (kept[(x + 1) & 3] >> (x & ~3) & 1) ? p[x + 1] : 0.f;
-          out[x / 2] = pack2<T>(a, b);
-        }
-        tc::store32(s_at, out);
+      for (int x = 0; x < kHalf; x += 32) {
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = !DROP || (kept[e & 3] >> ((x + e) & ~3) & 1) ? p[x + e] : 0.f;
+        store_row32<T>(s_at, x, v);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -271,32 +299,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs, n & 1, failed));
       if (!ok) break;
       tc::fence_after();
-      float t[kHalf];
-      tc::load32(dp_at, t);
-      tc::load32(dp_at + 32, t + 32);
-      tc::wait_loads();
-      {
-        uint32_t out[32];
+      if constexpr (kSplit)
+        if (!w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + DP);  // dK of the tile before
 #pragma unroll
-        for (int x = 0; x < kHalf; x += 4) {
-          const float4 d = *reinterpret_cast<const float4 *>(&bars.delta[slot][w * kHalf + x]);
+      for (int c0 = 0; c0 < kHalf; c0 += kDpChunk) {
+        float t[kDpChunk];
+#pragma unroll
+        for (int x = 0; x < kDpChunk; x += 32) tc::load32(dp_at + c0 + x, t + x);
+        tc::wait_loads();
+#pragma unroll
+        for (int x = 0; x < kDpChunk; x += 4) {
+          const float4 d = *reinterpret_cast<const float4 *>(&bars.delta[slot][w * kHalf + c0 + x]);
           float v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            v[y] = t[x + y];
-            if (DROP) v[y] = kept[y] >> x & 1 ? v[y] * c.keep_scale : 0.f;
+            v[y] = kSplit ? t[x + y] * by.dprobs : t[x + y];
+            if (DROP) v[y] = kept[y] >> (c0 + x) & 1 ? v[y] * c.keep_scale : 0.f;
           }
           const float2 u0 = tc::add2(make_float2(v[0], v[1]), make_float2(d.x, d.y));
           const float2 u1 = tc::add2(make_float2(v[2], v[3]), make_float2(d.z, d.w));
-          float2 r0 = tc::mul2(make_float2(p[x], p[x + 1]), u0), r1 = tc::mul2(make_float2(p[x + 2], p[x + 3]), u1);
-          if constexpr (std::is_same<T, __half>::value) {
+          float2 r0 = tc::mul2(make_float2(p[c0 + x], p[c0 + x + 1]), u0);
+          float2 r1 = tc::mul2(make_float2(p[c0 + x + 2], p[c0 + x + 3]), u1);
+          if constexpr (kUp) {
             r0 = tc::mul2(r0, make_float2(ds_by_p, ds_by_p));
             r1 = tc::mul2(r1, make_float2(ds_by_p, ds_by_p));
           }
-          out[x / 2] = pack2<T>(r0.x, r0.y);
-          out[x / 2 + 1] = pack2<T>(r1.x, r1.y);
+          t[x] = r0.x;
+          t[x + 1] = r0.y;
+          t[x + 2] = r1.x;
+          t[x + 3] = r1.y;
         }
-        tc::store32(dp_at, out);
+#pragma unroll
+        for (int x = 0; x < kDpChunk; x += 32) store_row32<T>(dp_at, c0 + x, t + x);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -313,8 +347,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j < ks.cover)
         row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
               kh * to.head;
-      const float factor = w ? (std::is_same<T, __half>::value ? exp2f(-kHalfP) : 1.f) * c.keep_scale : c.scale / ds;
-      store_sums<T, DP>(tmem + lanes + 2 * kTile + (w ? 0 : DP), row, factor, c.d, all > 0, j >= nk);
+      const float factor = w ? (kUp ? exp2f(-kHalfP) : 1.f) * c.keep_scale * by.dout : c.scale / ds * by.q;
+      if constexpr (kSplit) {
+        if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP));
+        store_floats<DP>(row, acc, factor, c.d, j >= nk);
+      } else {
+        store_sums<T, DP>(tmem + lanes + 2 * kTile + (w ? 0 : DP), row, factor, c.d, all > 0, j >= nk);
+      }
     }
     tc::fence_before();
   }
@@ -335,8 +374,8 @@ struct QueryBars {
   int failed;
 };
 
-template <int DP>
-constexpr size_t queries_smem() { return 1024 + (size_t)7 * tile_bytes<DP>(); }
+template <int W>
+constexpr size_t queries_smem() { return 1024 + (size_t)7 * tile_bytes<W>(); }
 
 // A tile of 128 queries of one head, past which the keys stream:
 //   S = Q K^T,  P = exp2(S - lse),  dP = dO V^T,  dS = P (dP - delta),  dQ += dS K.
@@ -346,10 +385,12 @@ constexpr size_t queries_smem() { return 1024 + (size_t)7 * tile_bytes<DP>(); }
 template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_queries(const AttnCall c, const __grid_constant__ TileMaps maps) {
+  constexpr int W = wide<T, DP>();
+  constexpr bool kSplit = Operand<T>::kSplit, kUp = !std::is_same<T, __nv_bfloat16>::value;  // kUp: float16 operands
   extern __shared__ unsigned char raw[];
   __shared__ QueryBars bars;
-  unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<DP>();
-  unsigned char *const sk = sd + tile_bytes<DP>(), *const sv = sk + 3 * tile_bytes<DP>();
+  unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<W>();
+  unsigned char *const sk = sd + tile_bytes<W>(), *const sv = sk + 3 * tile_bytes<W>();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
@@ -398,25 +439,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int cut_phase = 0, ks_done = 0, vs_done = 0;
       bool ok = true;
       if (lane == 0) {
-        copy_tile<DP>(sq, &maps.q, &bars.qd, head, q_token + i0, qs.seq);
-        copy_tile<DP>(sd, &maps.dout, &bars.qd, head, q_token + i0, qs.seq);
+        copy_tile<W>(sq, &maps.q, &bars.qd, head, q_token + i0, qs.seq);
+        copy_tile<W>(sd, &maps.dout, &bars.qd, head, q_token + i0, qs.seq);
       }
       for (int n = 0; n < all && ok; ++n) {
         if (n >= 3) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[n % 3], (n / 3 - 1) & 1, failed));
         if (!ok) break;
-        unsigned char *const to = sk + n % 3 * tile_bytes<DP>();
+        unsigned char *const to = sk + n % 3 * tile_bytes<W>();
         if ((n + 1) * kTile > nk)
-          ok = copy_tile_cut<DP>(to, &maps.k, &bars.k_full[n % 3], &bars.cut, &cut_phase, kh, k_token + n * kTile,
+          ok = copy_tile_cut<W>(to, &maps.k, &bars.k_full[n % 3], &bars.cut, &cut_phase, kh, k_token + n * kTile,
                                  ks.seq, nk - n * kTile, failed);
         else if (lane == 0)
-          copy_tile<DP>(to, &maps.k, &bars.k_full[n % 3], kh, k_token + n * kTile, ks.seq);
+          copy_tile<W>(to, &maps.k, &bars.k_full[n % 3], kh, k_token + n * kTile, ks.seq);
         __syncwarp();
         if (!ok) break;
         ++ks_done;
         if (n >= 2) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.v_empty[n & 1], (n / 2 - 1) & 1, failed));
         if (!ok) break;
         if (lane == 0)
-          copy_tile<DP>(sv + (n & 1) * tile_bytes<DP>(), &maps.v, &bars.v_full[n & 1], kh, k_token + n * kTile, ks.seq);
+          copy_tile<W>(sv + (n & 1) * tile_bytes<W>(), &maps.v, &bars.v_full[n & 1], kh, k_token + n * kTile, ks.seq);
         __syncwarp();
         ++vs_done;
       }
@@ -428,8 +469,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       if (all > 0) {
-        constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
-        constexpr uint32_t kStep = tile_bytes<DP>() / 16;
+        constexpr uint32_t kStep = tile_bytes<W>() / 16;
         const bool leader = tc::elect_one();
         const uint32_t q0 = tc::desc_rows(tc::smem_addr(sq)), d0 = tc::desc_rows(tc::smem_addr(sd));
         const uint32_t k0 = tc::desc_rows(tc::smem_addr(sk)), v0 = tc::desc_rows(tc::smem_addr(sv));
@@ -442,7 +482,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.k_full[n % 3], (n / 3) & 1);
           if (done && leader) {
-            tc::mma_rows<DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep, kBlock, by_rows);
+            products<T, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
             tc::commit(&bars.scores[n & 1]);
           }
           __syncwarp();
@@ -451,7 +491,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.v_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            tc::mma_rows<DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep, kBlock, by_rows);
+            products<T, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs[n & 1]);
             tc::commit(&bars.v_empty[n & 1]);
           }
@@ -464,8 +504,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores[n & 1], (n / 2) & 1);
           if (!ok) break;
           if (leader) {
-            tc::mma_sums<kTile>(tmem + 3 * kTile, tmem + (2 * n + 1) % 3 * kTile, kHalf, kHalf, k0c + n % 3 * kStep,
-                                by_cols, n > 0);
+            // split: two buffers in turn, each added to the rows' own sums two tiles later
+            sums<T, DP, kTile>(tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), tmem + (2 * n + 1) % 3 * kTile,
+                               k0c + n % 3 * kStep, n > 0);
             tc::commit(&bars.k_empty[n % 3]);
           }
           __syncwarp();
@@ -496,7 +537,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       else
         lim = max(0, seen_keys(c.causal, i, nq, nk));
     }
-    const float2 cs2 = make_float2(c.scale_log2, c.scale_log2), off2 = make_float2(-lse, -lse);
+    const Scales by = scales_of<T>(c);
+    float acc[kSplit ? DP / 2 : 1] = {};  // split: the sums of this warpgroup's half of the columns
+    const float2 cs2 = make_float2(by.scores, by.scores), off2 = make_float2(-lse, -lse);
     const float2 delta2 = make_float2(-delta, -delta);
     const uint64_t draw = DROP ? dropout_row(c.draws(), qs.row + i, c.heads, head) : 0;
     bool ok = true;
@@ -505,6 +548,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[b], phase, failed));
       if (!ok) break;
       tc::fence_after();
+      if constexpr (kSplit)
+        if (n > 1) add_sums<DP / 2>(acc, at_lane + 3 * kTile + b * DP + w * (DP / 2));  // of two tiles before
       const uint32_t s_at = at_lane + 2 * n % 3 * kTile + w * kHalf, dp_at = at_lane + (2 * n + 1) % 3 * kTile + w * kHalf;
       float p[kHalf];
       tc::load32(s_at, p);
@@ -535,10 +580,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int y = 0; y < 4; ++y) t[x + y] = draw_lane(z, y) >= c.drop ? t[x + y] * c.keep_scale : 0.f;
         }
       }
+      if constexpr (kSplit)
+#pragma unroll
+        for (int x = 0; x < kHalf; ++x) t[x] *= by.dprobs;
 #pragma unroll
       for (int x = 0; x < kHalf; x += 2) {
         float2 a = tc::add2(make_float2(t[x], t[x + 1]), delta2);
-        if constexpr (std::is_same<T, __half>::value) a = tc::mul2(a, make_float2(ds, ds));
+        if constexpr (kUp) a = tc::mul2(a, make_float2(ds, ds));
         a = tc::mul2(a, make_float2(p[x], p[x + 1]));
         t[x] = a.x;
         t[x + 1] = a.y;
@@ -546,10 +594,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
-      uint32_t out[32];
-#pragma unroll
-      for (int x = 0; x < kHalf; x += 2) out[x / 2] = pack2<T>(t[x], t[x + 1]);
-      tc::store32(dp_at, out);
+      store_row32<T>(dp_at, 0, t);
+      store_row32<T>(dp_at, 32, t + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores[b]);
@@ -564,7 +610,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (i < qs.cover)
         row = static_cast<T *>(c.dq.p) +
               (c.q_offsets ? (qs.row + i) * c.dq.token : qs.seq * c.dq.seq + i * c.dq.token) + head * c.dq.head + from;
-      store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, c.scale / ds, c.d - from, all > 0, lim == 0);
+      if constexpr (kSplit) {
+        for (int n = max(0, all - 2); n < all; ++n) add_sums<DP / 2>(acc, at_lane + 3 * kTile + (n & 1) * DP + from);
+        store_floats<DP / 2>(row, acc, c.scale / ds * by.k, c.d - from, lim == 0);
+      } else {
+        store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, c.scale / ds, c.d - from, all > 0, lim == 0);
+      }
     }
     tc::fence_before();
   }
@@ -578,47 +629,46 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 template <typename T, int DP, bool DROP>
 cudaError_t backward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
+  constexpr int W = wide<T, DP>();
   if (c.dk.p || c.dv.p) {
     const auto kern = tile_backward_keys<T, DP, DROP>;
-    cudaError_t e = allow_smem(kern, keys_smem<DP>());
+    cudaError_t e = allow_smem(kern, keys_smem<W>());
     if (e != cudaSuccess) return e;
     const int64_t blocks = tiles_of(c.k_offsets != nullptr, c.sequences, c.k_tokens, 1, kTile) * c.key_heads;
-    e = launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, keys_smem<DP>(), false, s, c, m);
+    e = launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, keys_smem<W>(), false, s, c, m);
     if (e != cudaSuccess) return e;
   }
   if (!c.dq.p) return cudaSuccess;
   const auto kern = tile_backward_queries<T, DP, DROP>;
-  const cudaError_t e = allow_smem(kern, queries_smem<DP>());
+  const cudaError_t e = allow_smem(kern, queries_smem<W>());
   if (e != cudaSuccess) return e;
   const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, kTile) * c.heads;
-  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, queries_smem<DP>(), false, s, c, m);
+  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, queries_smem<W>(), false, s, c, m);
 }
 
 template <typename T>
 cudaError_t backward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
-  if (c.d <= 64) return c.drop ? backward_launch<T, 64, true>(c, m, s) : backward_launch<T, 64, false>(c, m, s);
-  return c.drop ? backward_launch<T, 128, true>(c, m, s) : backward_launch<T, 128, false>(c, m, s);
+  if constexpr (!Operand<T>::kSplit)
+    if (c.d > 64) return c.drop ? backward_launch<T, 128, true>(c, m, s) : backward_launch<T, 128, false>(c, m, s);
+  return c.drop ? backward_launch<T, 64, true>(c, m, s) : backward_launch<T, 64, false>(c, m, s);
 }
 
 }  // namespace
 
 bool tile_backward_fits(const AttnCall &c, int type) {
   const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
-  return tiles_fit(c, type) && even(c.q, c.heads, c.q_tokens, qn) && even(c.dout, c.heads, c.q_tokens, qn) &&
-         even(c.k, c.key_heads, c.k_tokens, kn) && even(c.v, c.key_heads, c.k_tokens, kn) &&
-         (!c.dq.p || even(c.dq, c.heads, c.q_tokens, qn)) && (!c.dk.p || even(c.dk, c.key_heads, c.k_tokens, kn)) &&
-         (!c.dv.p || even(c.dv, c.key_heads, c.k_tokens, kn));
+  if (!tiles_fit(c, type)) return false;
+  if (type == SNACK_F32) return true;
+  return even(c.q, c.heads, c.q_tokens, qn) && (!c.dout.p || even(c.dout, c.heads, c.q_tokens, qn)) &&
+         even(c.k, c.key_heads, c.k_tokens, kn) && even(c.v, c.key_heads, c.k_tokens, kn);
 }
 
-cudaError_t tile_backward_launch(const AttnCall &c, int type, cudaStream_t s) {
+cudaError_t tile_backward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s) {
   TileMaps m = {};
-  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
-  if (!map_of(&m.q, type, c.q, c.d, c.heads, c.q_tokens, qn) ||
-      !map_of(&m.dout, type, c.dout, c.d, c.heads, c.q_tokens, qn) ||
-      !map_of(&m.k, type, c.k, c.d, c.key_heads, c.k_tokens, kn) ||
-      !map_of(&m.v, type, c.v, c.d, c.key_heads, c.k_tokens, kn))
-    return cudaErrorInvalidValue;
-  return type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, m, s) : backward_typed<__half>(c, m, s);
+  if (!maps_of(&m, c, type, parts, true)) return cudaErrorInvalidValue;
+  return type == SNACK_F32    ? backward_typed<float>(c, m, s)
+         : type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, m, s)
+                              : backward_typed<__half>(c, m, s);
 }
 
 cudaError_t tile_backward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }

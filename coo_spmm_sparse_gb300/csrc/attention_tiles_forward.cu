@@ -4,10 +4,11 @@
 namespace snack {
 namespace {
 
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kForwardSlots = 4;  // tiles of keys and values in flight, in turn
 
-template <int DP>
-constexpr size_t tile_forward_smem() { return 1024 + (size_t)(2 + kForwardSlots) * tile_bytes<DP>(); }
+template <int W>
+constexpr size_t tile_forward_smem() { return 1024 + (size_t)(2 + kForwardSlots) * tile_bytes<W>(); }
 
 struct ForwardBars {
   uint64_t q[2], full[kForwardSlots], empty[kForwardSlots], scores[2], probs[2][2], done[2], cut, drain;
@@ -25,9 +26,11 @@ struct ForwardBars {
 template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_forward(const AttnCall c, const __grid_constant__ TileMaps maps) {
+  constexpr int W = wide<T, DP>();
+  constexpr bool kSplit = Operand<T>::kSplit;
   extern __shared__ unsigned char raw[];
   __shared__ ForwardBars bars;
-  unsigned char *const sq = align1024(raw), *const ring = sq + 2 * tile_bytes<DP>();
+  unsigned char *const sq = align1024(raw), *const ring = sq + 2 * tile_bytes<W>();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (lane == 0)
       for (int t = 0; t < 2; ++t)
         if (steps[t])
-          copy_tile<DP>(sq + t * tile_bytes<DP>(), &maps.q, &bars.q[t], head0 + (by_heads ? t : 0), q_token + first[t],
+          copy_tile<W>(sq + t * tile_bytes<W>(), &maps.q, &bars.q[t], head0 + (by_heads ? t : 0), q_token + first[t],
                         qs.seq);
     for (int j = 0; j < all && ok; ++j) {
       for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
@@ -92,13 +95,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = __all_sync(0xffffffffu,
                           tc::bar_wait(&bars.empty[slot], (item / kForwardSlots - 1) & 1, failed));
         if (!ok) break;
-        unsigned char *const to = ring + slot * tile_bytes<DP>();
+        unsigned char *const to = ring + slot * tile_bytes<W>();
         const int token = k_token + j * kTile;
         if (kv && (j + 1) * kTile > nk)
-          ok = copy_tile_cut<DP>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq,
+          ok = copy_tile_cut<W>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq,
                                  nk - j * kTile, failed);
         else if (lane == 0)
-          copy_tile<DP>(to, kv ? &maps.v : &maps.k, &bars.full[slot], kh, token, ks.seq);
+          copy_tile<W>(to, kv ? &maps.v : &maps.k, &bars.full[slot], kh, token, ks.seq);
         __syncwarp();
       }
     }
@@ -110,11 +113,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp == kMmaWarp) {
     // the whole warp goes along, so that descriptors stay in uniform registers
     if (all > 0) {
-      constexpr uint32_t by_rows = tc::mma_kind<T>(kTile, false), by_cols = tc::mma_kind<T>(DP, true);
       const bool leader = tc::elect_one();
       const uint32_t q0 = tc::desc_rows(tc::smem_addr(sq)), k0 = tc::desc_rows(tc::smem_addr(ring));
       const uint32_t v0 = tc::desc_columns(tc::smem_addr(ring), kBlock);
-      constexpr uint32_t kStep = tile_bytes<DP>() / 16;
+      constexpr uint32_t kStep = tile_bytes<W>() / 16;
       const auto wait = [&](uint64_t *bar, int phase) {
         const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
         tc::fence_after();
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (steps[t]) {
           ok = wait(&bars.q[t], 0);
           if (ok && leader) {
-            tc::mma_rows<DP>(tmem + t * kTile, q0 + t * kStep, k0, kBlock, by_rows);
+            products<T, DP>(tmem + t * kTile, q0 + t * kStep, k0);
             tc::commit(&bars.scores[t]);
           }
         }
@@ -140,12 +142,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (j >= steps[t]) continue;
           const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * DP;
           ok = wait(&bars.probs[t][0], j & 1);
-          if (ok && leader) tc::mma_sums<kTile / 2>(o_at, s_at, kTile, 0, v_at, by_cols, j > 0);
+          if (ok && leader) sums<T, DP, kTile / 2>(o_at, s_at, v_at, j > 0);
           ok = ok && wait(&bars.probs[t][1], j & 1);
           if (ok && leader) {
-            tc::mma_sums<kTile / 2>(o_at, s_at, kTile, 0, v_at, by_cols, true, kTile / 2);
+            sums<T, DP, kTile / 2>(o_at, s_at, v_at, true, kTile / 2);
             if (j + 1 < steps[t]) {
-              tc::mma_rows<DP>(s_at, q0 + t * kStep, k_at, kBlock, by_rows);
+              products<T, DP>(s_at, q0 + t * kStep, k_at);
               tc::commit(&bars.scores[t]);
             } else {
               tc::commit(&bars.done[t]);
@@ -177,6 +179,84 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (DROP) draw = dropout_row(c.draws(), qs.row + i, c.heads, head);
     float m = -INFINITY, sum = 0.f;
     bool ok = true;
+    if constexpr (kSplit) {
+      // Two passes over the scores in tensor memory, 64 at a time: a row's sums
+      // stay in registers beside them.
+      const float cs = c.scale_log2 * exp2f((float)-power_to_half(c.peak[2])) * exp2f((float)-power_to_half(c.peak[3]));
+      float o[DP] = {};
+      for (int j = 0; j < steps[t]; ++j) {
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
+        if (!ok) break;
+        tc::fence_after();
+        if (j > 0) add_sums<DP>(o, o_at);  // of the tile before: complete when these scores are
+        const int left = lim - j * kTile;  // keys of this tile that the row sees
+        const bool cut = __any_sync(0xffffffffu, left < kTile);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < kTile; x += 64) {
+          float s[64];
+          tc::load32(s_at + x, s);
+          tc::load32(s_at + x + 32, s + 32);
+          tc::wait_loads();
+          if (cut)
+#pragma unroll
+            for (int e = 0; e < 64; ++e) s[e] = x + e < left ? s[e] : -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 64; e += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) top[y] = tc::max3(top[y], s[e + y], s[e + 4 + y]);
+        }
+        const float grown = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        const float shrink = grown == -INFINITY ? 1.f : tc::exp2_fast((m - grown) * cs);
+        m = grown;
+        sum *= shrink;
+        if (__any_sync(0xffffffffu, shrink != 1.f))
+#pragma unroll
+          for (int e = 0; e < DP; ++e) o[e] *= shrink;
+        const float off = m == -INFINITY ? kHalfP : kHalfP - m * cs;
+        float part[4] = {};
+#pragma unroll
+        for (int x = 0; x < kTile; x += 64) {
+          float s[64];
+          tc::load32(s_at + x, s);
+          tc::load32(s_at + x + 32, s + 32);
+          tc::wait_loads();
+#pragma unroll
+          for (int e = 0; e < 64; ++e) s[e] = tc::exp2_fast(fmaf(s[e], cs, off));
+          if (cut)
+#pragma unroll
+            for (int e = 0; e < 64; ++e) s[e] = x + e < left ? s[e] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) part[e & 3] += s[e];
+          if (DROP)
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const uint64_t z = dropout_draw(draw, j * kTile + x + e);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) s[e + y] = draw_lane(z, y) >= c.drop ? s[e + y] : 0.f;
+            }
+          store_parts(s_at + x, s);
+          store_parts(s_at + x + 32, s + 32);
+          tc::wait_stores();
+          tc::fence_before();
+          tc::bar_arrive_warp(&bars.probs[t][x / 64]);
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+      }
+      if (ok && steps[t]) {
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));
+        tc::fence_after();
+        if (ok) add_sums<DP>(o, o_at);
+      }
+      if (ok && i < qs.cover) {
+        float *const row = static_cast<float *>(c.out.p) +
+                           (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) +
+                           head * c.out.head;
+        store_floats<DP>(row, o, c.keep_scale / sum * exp2f((float)-power_to_half(c.peak[1])), c.d, sum == 0.f);
+        c.lse[(int64_t)head * c.rows + qs.row + i] =
+            sum == 0.f ? -INFINITY : m * cs * kLn2 + (logf(sum) - kHalfP * kLn2);
+      }
+    } else {
     for (int j = 0; j < steps[t]; ++j) {
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
       if (!ok) break;
@@ -244,7 +324,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             p[e / 2 + 1] = pack2<T>(k[2], k[3]);
           }
         }
-        tc::store32(s_at + x / 2, p);
+        tc::store32(s_at + x, p);
         tc::wait_stores();
         tc::fence_before();
         tc::bar_arrive_warp(&bars.probs[t][x / 64]);
@@ -265,6 +345,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (mine)
         c.lse[(int64_t)head * c.rows + qs.row + i] = sum == 0.f ? -INFINITY : m * c.scale + logf(sum);
     }
+    }
     tc::fence_before();
   }
   __syncthreads();
@@ -279,8 +360,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 bool tile_forward_fits(const AttnCall &c, int type) {
   const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
-  return tiles_fit(c, type) && even(c.q, c.heads, c.q_tokens, qn) && even(c.k, c.key_heads, c.k_tokens, kn) &&
-         even(c.v, c.key_heads, c.k_tokens, kn) && even(c.out, c.heads, c.q_tokens, qn);
+  return tiles_fit(c, type) &&
+         (type == SNACK_F32 || (even(c.q, c.heads, c.q_tokens, qn) && even(c.k, c.key_heads, c.k_tokens, kn) &&
+                                even(c.v, c.key_heads, c.k_tokens, kn)));
 }
 
 template <typename T, int DP, bool DROP>
@@ -289,25 +371,25 @@ static cudaError_t forward_launch(const AttnCall &c, const TileMaps &m, cudaStre
   const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, by_heads ? kTile : 2 * kTile) *
                          (by_heads ? c.heads / 2 : c.heads);
   const auto kern = tile_forward<T, DP, DROP>;
-  const cudaError_t e = allow_smem(kern, tile_forward_smem<DP>());
+  constexpr size_t smem = tile_forward_smem<wide<T, DP>()>();
+  const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, tile_forward_smem<DP>(), false, s, c, m);
+  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, smem, false, s, c, m);
 }
 
 template <typename T>
 static cudaError_t forward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
-  if (c.d <= 64) return c.drop ? forward_launch<T, 64, true>(c, m, s) : forward_launch<T, 64, false>(c, m, s);
-  return c.drop ? forward_launch<T, 128, true>(c, m, s) : forward_launch<T, 128, false>(c, m, s);
+  if constexpr (!Operand<T>::kSplit)
+    if (c.d > 64) return c.drop ? forward_launch<T, 128, true>(c, m, s) : forward_launch<T, 128, false>(c, m, s);
+  return c.drop ? forward_launch<T, 64, true>(c, m, s) : forward_launch<T, 64, false>(c, m, s);
 }
 
-cudaError_t tile_forward_launch(const AttnCall &c, int type, cudaStream_t s) {
+cudaError_t tile_forward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s) {
   TileMaps m = {};
-  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
-  if (!map_of(&m.q, type, c.q, c.d, c.heads, c.q_tokens, qn) ||
-      !map_of(&m.k, type, c.k, c.d, c.key_heads, c.k_tokens, kn) ||
-      !map_of(&m.v, type, c.v, c.d, c.key_heads, c.k_tokens, kn))
-    return cudaErrorInvalidValue;
-  return type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, m, s) : forward_typed<__half>(c, m, s);
+  if (!maps_of(&m, c, type, parts, false)) return cudaErrorInvalidValue;
+  return type == SNACK_F32    ? forward_typed<float>(c, m, s)
+         : type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, m, s)
+                              : forward_typed<__half>(c, m, s);
 }
 
 cudaError_t tile_forward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }
