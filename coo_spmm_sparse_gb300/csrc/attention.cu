@@ -8,7 +8,6 @@
 namespace snack {
 namespace {
 
-constexpr int kTeam = 16;  // lanes that share a row of v
 
 template <typename T>
 __device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[16 / sizeof(T)]) {
@@ -30,7 +29,7 @@ __device__ __forceinline__ bool in_sequence(const int32_t *offsets, const int32_
     *token = (int)row;
     return row >= clamped(offsets, 0, tokens) && row < clamped(offsets, n, tokens);
   }
-  *seq = (int)(row / tokens);
+  *seq = row >> 31 ? (int)(row / tokens) : (int)((uint32_t)row / (uint32_t)tokens);
   *token = (int)(row - (int64_t)*seq * tokens);
   return !lengths || *token < lengths[*seq];
 }
@@ -61,7 +60,8 @@ __global__ void __launch_bounds__(256) attention_delta(const AttnCall c, uint32_
   uint4 x[kItems], y[kItems];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    const int64_t item = first + i * kTeams, row = item / c.heads;
+    const int64_t item = first + i * kTeams;
+    const int64_t row = item >> 31 ? item / c.heads : (int64_t)((uint32_t)item / (uint32_t)c.heads);
     const int head = (int)(item - row * c.heads);
     int seq = 0, token = 0;
     const bool have = row < c.rows && in_sequence(c.q_offsets, c.q_lengths, c.sequences, c.q_tokens, row, &seq, &token);
@@ -127,21 +127,51 @@ struct Sources {
   Source t[4];
 };
 
+// A warp takes a token, a lane four columns of one of its heads at a time: one
+// division a token, where one for every row of a head took longer than the
+// memory does.  16 column places a head in the parts, as many as it has else.
+__device__ __forceinline__ bool token_of(const Source &t, int sequences, int64_t row, int64_t *at) {
+  int seq, token;
+  const bool have = in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token);
+  *at = seq * t.from.seq + token * t.from.token;
+  return have;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_four(const T *v, int left, float (&x)[4]) {
+  if (left >= 4 && (reinterpret_cast<uintptr_t>(v) & (4 * sizeof(T) - 1)) == 0) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(v);
+      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2 *>(v);
+      unpack2<T>(u.x, x[0], x[1]);
+      unpack2<T>(u.y, x[2], x[3]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = e < left ? to_float(v[e]) : 0.f;
+  }
+}
+
 // The largest magnitude of each tensor, over the sequences' tokens.  Grid: y = tensor.
 template <typename T>
 __global__ void __launch_bounds__(256) attention_peak(const Sources all, int sequences, int d) {
   const Source &t = all.t[blockIdx.y];
-  const int lane = threadIdx.x % kTeam;
+  const int lane = threadIdx.x & 31, places = (d + 3) / 4, work = t.heads * places;
   float top = 0.f;
-  const int64_t items = t.rows * t.heads;
-  for (int64_t item = (int64_t)blockIdx.x * (256 / kTeam) + threadIdx.x / kTeam; item < items;
-       item += (int64_t)gridDim.x * (256 / kTeam)) {
-    const int64_t row = item / t.heads;
-    int seq, token;
-    if (!in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token)) continue;
-    const T *v = static_cast<const T *>(t.from.p) + seq * t.from.seq + token * t.from.token +
-                 (item - row * t.heads) * t.from.head;
-    for (int col = lane; col < d; col += kTeam) top = larger(top, to_float(v[col]));
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
+    int64_t at;
+    if (!token_of(t, sequences, row, &at)) continue;
+    const T *const v = static_cast<const T *>(t.from.p) + at;
+#pragma unroll 4
+    for (int i = lane; i < work; i += 32) {
+      const int head = i / places, col = (i - head * places) * 4;
+      float x[4];
+      load_four(v + head * t.from.head + col, d - col, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = larger(top, x[e]);
+    }
   }
   block_peak(top, t.peak);
 }
@@ -151,38 +181,31 @@ __global__ void __launch_bounds__(256) attention_peak(const Sources all, int seq
 // behind the head size and for tokens outside every sequence.  Grid: y = tensor.
 __global__ void __launch_bounds__(256) split_parts(const Sources all, int sequences, int d) {
   const Source &t = all.t[blockIdx.y];
-  const int col = threadIdx.x % kTeam * 4;
+  const int lane = threadIdx.x & 31, work = t.heads * 16;
   const float by = exp2f((float)power_to_half(*t.peak));
-  const int64_t items = t.rows * t.heads;
-  for (int64_t item = (int64_t)blockIdx.x * (256 / kTeam) + threadIdx.x / kTeam; item < items;
-       item += (int64_t)gridDim.x * (256 / kTeam)) {
-    const int64_t row = item / t.heads;
-    int seq, token;
-    float x[4] = {};
-    if (in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token)) {
-      const float *v = static_cast<const float *>(t.from.p) + seq * t.from.seq + token * t.from.token +
-                       (item - row * t.heads) * t.from.head + col;
-      if ((reinterpret_cast<uintptr_t>(v) & 15) == 0 && col + 4 <= d) {
-        const float4 f = *reinterpret_cast<const float4 *>(v);
-        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-      } else {
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
+    int64_t at;
+    const bool have = token_of(t, sequences, row, &at);
+    const float *const v = static_cast<const float *>(t.from.p) + at;
+    __half *const parts = t.parts + row * t.heads * 128;
+#pragma unroll 4
+    for (int i = lane; i < work; i += 32) {
+      const int head = i / 16, col = i % 16 * 4;
+      float x[4] = {};
+      if (have && col < d) load_four(v + head * t.from.head + col, d - col, x);
+      uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < d) x[e] = v[e];
+      for (int e = 0; e < 2; ++e) {
+        float a, b;
+        const float u = x[2 * e] * by, w = x[2 * e + 1] * by;
+        hi[e] = pack2<__half>(u, w);
+        unpack2<__half>(hi[e], a, b);
+        lo[e] = pack2<__half>(u - a, w - b);
       }
+      __half *const to = parts + head * 128 + col;
+      *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2 *>(to + 64) = make_uint2(lo[0], lo[1]);
     }
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float a, b;
-      const float u = x[2 * e] * by, w = x[2 * e + 1] * by;
-      hi[e] = pack2<__half>(u, w);
-      unpack2<__half>(hi[e], a, b);
-      lo[e] = pack2<__half>(u - a, w - b);
-    }
-    __half *to = t.parts + item * 128 + col;
-    *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2 *>(to + 64) = make_uint2(lo[0], lo[1]);
   }
 }
 
@@ -374,8 +397,8 @@ Sources sources_of(const AttnCall &c, const Plan &p, char *workspace) {
   return s;
 }
 
-unsigned spread(int64_t items) {
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + 15) / 16, 16 * device_sms()));
+unsigned spread(int64_t rows) {  // a warp for each, or as many as are resident together
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, 8 * device_sms()));
 }
 
 // Makes the parts of 32-bit operands; `tensors`: 3 (forward) or 4.
@@ -383,7 +406,7 @@ cudaError_t make_parts(AttnCall *c, const Plan &p, int tensors, char *workspace,
   const Sources all = sources_of(*c, p, workspace);
   cudaError_t e = cudaMemsetAsync(workspace, 0, 4 * sizeof(uint32_t), s);
   int64_t most = 0;
-  for (int i = 0; i < tensors; ++i) most = std::max(most, all.t[i].rows * all.t[i].heads);
+  for (int i = 0; i < tensors; ++i) most = std::max(most, all.t[i].rows);
   const dim3 grid(spread(most), (unsigned)tensors);
   if (e == cudaSuccess) e = launch_kernel(attention_peak<float>, grid, 256, 0, false, s, all, c->sequences, c->d);
   if (e == cudaSuccess) e = launch_kernel(split_parts, grid, 256, 0, false, s, all, c->sequences, c->d);
@@ -426,9 +449,8 @@ cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace,
     e = cudaMemsetAsync(peak, 0, 2 * sizeof(uint32_t), s);
     Sources v = sources_of(c, p, workspace);
     v.t[0] = v.t[2];
-    const int64_t items = v.t[0].rows * v.t[0].heads;
-    if (e == cudaSuccess && items)
-      e = launch_kernel(attention_peak<T>, dim3(spread(items)), 256, 0, false, s, v, c.sequences, c.d);
+    if (e == cudaSuccess && v.t[0].rows)
+      e = launch_kernel(attention_peak<T>, dim3(spread(v.t[0].rows)), 256, 0, false, s, v, c.sequences, c.d);
   }
   if (e != cudaSuccess) return e;
   if (c.rows) {
