@@ -2,6 +2,7 @@
 // them (delta, the joining of split calls).
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "attention.cuh"
 
@@ -34,13 +35,19 @@ __device__ __forceinline__ bool in_sequence(const int32_t *offsets, const int32_
   return !lengths || *token < lengths[*seq];
 }
 
+// One atomic maximum a block, and none where the peak is as large already: an
+// atomic for every warp of a grid on one address took longer than the reads.
 __device__ __forceinline__ void block_peak(float v, uint32_t *peak) {
+  __shared__ uint32_t tops[8];
+  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v));  // magnitudes: their bits order as they do
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t most = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, __float_as_uint(v), o);
-    if (other > __float_as_uint(v)) v = __uint_as_float(other);  // magnitudes: their bits order as they do
+    for (int w = 0; w < 8; ++w) most = max(most, tops[w]);
+    if (most > *const_cast<volatile uint32_t *>(peak)) atomicMax(peak, most);
   }
-  if ((threadIdx.x & 31) == 0 && __float_as_uint(v) > 0) atomicMax(peak, __float_as_uint(v));
 }
 __device__ __forceinline__ float larger(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(fabsf(b))));
@@ -127,9 +134,9 @@ struct Sources {
   Source t[4];
 };
 
-// A warp takes a token, a lane four columns of one of its heads at a time: one
+// A warp takes a token, a lane 16 bytes of one of its heads at a time: one
 // division a token, where one for every row of a head took longer than the
-// memory does.  16 column places a head in the parts, as many as it has else.
+// memory does.
 __device__ __forceinline__ bool token_of(const Source &t, int sequences, int64_t row, int64_t *at) {
   int seq, token;
   const bool have = in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token);
@@ -137,74 +144,101 @@ __device__ __forceinline__ bool token_of(const Source &t, int sequences, int64_t
   return have;
 }
 
+// 16 bytes of elements from v on, of which `left` are there.
 template <typename T>
-__device__ __forceinline__ void load_four(const T *v, int left, float (&x)[4]) {
-  if (left >= 4 && (reinterpret_cast<uintptr_t>(v) & (4 * sizeof(T) - 1)) == 0) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(v);
-      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2 *>(v);
-      unpack2<T>(u.x, x[0], x[1]);
-      unpack2<T>(u.y, x[2], x[3]);
-    }
-  } else {
+__device__ __forceinline__ uint4 load_vector(const T *v, int left) {
+  constexpr int E = 16 / sizeof(T);
+  if (left >= E && (reinterpret_cast<uintptr_t>(v) & 15) == 0) return *reinterpret_cast<const uint4 *>(v);
+  uint4 u = make_uint4(0, 0, 0, 0);
+  T x[E];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = e < left ? to_float(v[e]) : 0.f;
-  }
+  for (int e = 0; e < E; ++e) x[e] = e < left ? v[e] : from_float<T>(0.f);
+  memcpy(&u, x, 16);
+  return u;
 }
 
-// The largest magnitude of each tensor, over the sequences' tokens.  Grid: y = tensor.
+// The largest magnitude of each tensor, over the sequences' tokens.  Heads that
+// lie end to end are read as one row.  Grid: y = tensor.
 template <typename T>
 __global__ void __launch_bounds__(256) attention_peak(const Sources all, int sequences, int d) {
+  constexpr int E = 16 / sizeof(T), kAhead = 6;
   const Source &t = all.t[blockIdx.y];
-  const int lane = threadIdx.x & 31, places = (d + 3) / 4, work = t.heads * places;
+  const bool flat = t.from.head == d || t.heads == 1;
+  const int lane = threadIdx.x & 31, heads = flat ? 1 : t.heads, width = flat ? t.heads * d : d;
   float top = 0.f;
   for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
     int64_t at;
     if (!token_of(t, sequences, row, &at)) continue;
-    const T *const v = static_cast<const T *>(t.from.p) + at;
-#pragma unroll 4
-    for (int i = lane; i < work; i += 32) {
-      const int head = i / places, col = (i - head * places) * 4;
-      float x[4];
-      load_four(v + head * t.from.head + col, d - col, x);
+    for (int head = 0; head < heads; ++head) {
+      const T *const v = static_cast<const T *>(t.from.p) + at + head * t.from.head;
+      for (int col = lane * E; col < width; col += 32 * E * kAhead) {
+        uint4 u[kAhead];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = larger(top, x[e]);
+        for (int i = 0; i < kAhead; ++i) {
+          const int c = col + i * 32 * E;
+          u[i] = c < width ? load_vector(v + c, width - c) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float x[E];
+          unpack16<T>(u[i], x);
+#pragma unroll
+          for (int e = 0; e < E; ++e) top = larger(top, x[e]);
+        }
+      }
     }
   }
   block_peak(top, t.peak);
 }
 
-// Every tensor as two float16 parts of its elements times the power of two that
-// brings its largest to [2^14, 2^15): rows of 64 high and 64 low halves, zeros
-// behind the head size and for tokens outside every sequence.  Grid: y = tensor.
-__global__ void __launch_bounds__(256) split_parts(const Sources all, int sequences, int d) {
+// Every tensor in float16, its elements times the power of two that brings its
+// largest to [2^14, 2^15): rows of W columns of each head (zeros behind the head
+// size and for tokens outside every sequence).  32-bit floats as two parts, 64
+// high and 64 low halves; bfloat16's eight bits lose nothing down to 2^-28 of
+// the largest, and what lies below is never more than 2^-39 of it off.  Grid: y =
+// tensor.
+template <typename T, int W>
+__global__ void __launch_bounds__(256) half_parts(const Sources all, int sequences, int d) {
+  constexpr bool kSplit = sizeof(T) == 4;
+  constexpr int E = 16 / sizeof(T), kPlaces = (kSplit ? W / 2 : W) / E, kAhead = 4;
   const Source &t = all.t[blockIdx.y];
-  const int lane = threadIdx.x & 31, work = t.heads * 16;
+  const int lane = threadIdx.x & 31, work = t.heads * kPlaces;
   const float by = exp2f((float)power_to_half(*t.peak));
   for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
     int64_t at;
     const bool have = token_of(t, sequences, row, &at);
-    const float *const v = static_cast<const float *>(t.from.p) + at;
-    __half *const parts = t.parts + row * t.heads * 128;
-#pragma unroll 4
-    for (int i = lane; i < work; i += 32) {
-      const int head = i / 16, col = i % 16 * 4;
-      float x[4] = {};
-      if (have && col < d) load_four(v + head * t.from.head + col, d - col, x);
-      uint32_t hi[2], lo[2];
+    const T *const v = static_cast<const T *>(t.from.p) + at;
+    __half *const parts = t.parts + row * t.heads * W;
+    for (int i0 = lane; i0 < work; i0 += 32 * kAhead) {
+      uint4 u[kAhead];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float a, b;
-        const float u = x[2 * e] * by, w = x[2 * e + 1] * by;
-        hi[e] = pack2<__half>(u, w);
-        unpack2<__half>(hi[e], a, b);
-        lo[e] = pack2<__half>(u - a, w - b);
+      for (int n = 0; n < kAhead; ++n) {
+        const int i = i0 + n * 32, head = i / kPlaces, col = i % kPlaces * E;
+        u[n] = have && i < work && col < d ? load_vector(v + head * t.from.head + col, d - col) : make_uint4(0, 0, 0, 0);
       }
-      __half *const to = parts + head * 128 + col;
-      *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2 *>(to + 64) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const int i = i0 + n * 32, head = i / kPlaces, col = i % kPlaces * E;
+        if (i >= work) break;
+        float x[E];
+        unpack16<T>(u[n], x);
+        uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          float a, b;
+          const float l = x[2 * e] * by, r = x[2 * e + 1] * by;
+          hi[e] = pack2<__half>(l, r);
+          unpack2<__half>(hi[e], a, b);
+          lo[e] = pack2<__half>(l - a, r - b);
+        }
+        __half *const to = parts + head * W + col;
+        if constexpr (kSplit) {
+          *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2 *>(to + W / 2) = make_uint2(lo[0], lo[1]);
+        } else {
+          *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        }
+      }
     }
   }
 }
@@ -326,13 +360,19 @@ struct Plan {
 };
 constexpr size_t kPeaks = 256;
 
-// The parts of 32-bit operands.
-void plan_parts(Plan *p, const AttnCall &c, bool backward) {
+// Operands that are made in float16 first: those of 32-bit calls, and bfloat16's
+// of backward calls.  There the gradients of the scores are an operand too:
+// rounded to bfloat16 they made dq and dk 1.5 times as far off as the rounding of
+// the results alone, in float16 1.1 times, for 5 % of a long call's time.
+int part_width(const AttnCall &c, int type, bool backward) {
+  return type == SNACK_F32 ? 128 : type == SNACK_BF16 && backward ? (c.d <= 64 ? 64 : 128) : 0;
+}
+void plan_parts(Plan *p, const AttnCall &c, int width, bool backward) {
   const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
   const int64_t rows[4] = {c.rows * c.heads, keys * c.key_heads, keys * c.key_heads, backward ? c.rows * c.heads : 0};
   for (int i = 0; i < 4; ++i) {
     p->parts[i] = p->bytes;
-    p->bytes += rows[i] * 128 * sizeof(__half);
+    p->bytes += rows[i] * width * sizeof(__half);
   }
 }
 
@@ -350,9 +390,10 @@ Plan plan_forward(const AttnCall &c, int type) {
   Plan p;
   p.tiles = worth_tiles(c, type) && tile_forward_fits(c, type);
   if (p.tiles) {
-    if (type == SNACK_F32) {
+    const int width = part_width(c, type, false);
+    if (width) {
       p.bytes = kPeaks;
-      plan_parts(&p, c, false);
+      plan_parts(&p, c, width, false);
     }
     return p;
   }
@@ -377,7 +418,8 @@ Plan plan_backward(const AttnCall &c, int type) {
   p.delta = p.bytes;
   p.bytes += round_up(c.rows * c.heads * (int64_t)sizeof(float), 256);
   p.tiles = worth_tiles(c, type) && tile_backward_fits(c, type);
-  if (p.tiles && type == SNACK_F32) plan_parts(&p, c, true);
+  const int width = part_width(c, type, true);
+  if (p.tiles && width) plan_parts(&p, c, width, true);
   return p;
 }
 
@@ -401,26 +443,34 @@ unsigned spread(int64_t rows) {  // a warp for each, or as many as are resident 
   return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, 8 * device_sms()));
 }
 
-// Makes the parts of 32-bit operands; `tensors`: 3 (forward) or 4.
-cudaError_t make_parts(AttnCall *c, const Plan &p, int tensors, char *workspace, SplitParts *parts, cudaStream_t s) {
+// Makes the float16 parts of a call's operands: q, k, v and, backward, dout,
+// whose peak is there already.
+template <typename T>
+cudaError_t make_parts(AttnCall *c, const Plan &p, int width, bool backward, char *workspace, SplitParts *parts,
+                       cudaStream_t s) {
   const Sources all = sources_of(*c, p, workspace);
-  cudaError_t e = cudaMemsetAsync(workspace, 0, 4 * sizeof(uint32_t), s);
-  int64_t most = 0;
-  for (int i = 0; i < tensors; ++i) most = std::max(most, all.t[i].rows);
-  const dim3 grid(spread(most), (unsigned)tensors);
-  if (e == cudaSuccess) e = launch_kernel(attention_peak<float>, grid, 256, 0, false, s, all, c->sequences, c->d);
-  if (e == cudaSuccess) e = launch_kernel(split_parts, grid, 256, 0, false, s, all, c->sequences, c->d);
-  c->peak = reinterpret_cast<const uint32_t *>(workspace);
-  *parts = SplitParts{all.t[0].parts, all.t[1].parts, all.t[2].parts, all.t[3].parts};
+  const unsigned blocks = spread(std::max(all.t[0].rows, all.t[1].rows));
+  cudaError_t e = launch_kernel(attention_peak<T>, dim3(blocks, 3), 256, 0, false, s, all, c->sequences, c->d);
+  if (e == cudaSuccess)
+    e = launch_kernel(width == 64 ? half_parts<T, 64> : half_parts<T, 128>, dim3(blocks, backward ? 4 : 3), 256, 0,
+                      false, s, all, c->sequences, c->d);
+  *parts = SplitParts{width, all.t[0].parts, all.t[1].parts, all.t[2].parts, all.t[3].parts};
   return e;
+}
+
+cudaError_t clear_peaks(AttnCall *c, char *workspace, cudaStream_t s) {
+  c->peak = reinterpret_cast<const uint32_t *>(workspace);
+  return cudaMemsetAsync(workspace, 0, 4 * sizeof(uint32_t), s);
 }
 
 template <typename T>
 cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   if (p.tiles) {
     SplitParts parts = {};
-    if (type == SNACK_F32) {
-      const cudaError_t e = make_parts(&c, p, 3, workspace, &parts, s);
+    const int width = part_width(c, type, false);
+    if (width) {
+      cudaError_t e = clear_peaks(&c, workspace, s);
+      if (e == cudaSuccess) e = make_parts<T>(&c, p, width, false, workspace, &parts, s);
       if (e != cudaSuccess) return e;
     }
     return tile_forward_launch(c, type, parts, s);
@@ -438,28 +488,27 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
 template <typename T>
 cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  cudaError_t e = cudaSuccess;
-  SplitParts parts = {};
-  uint32_t *peak = nullptr;  // where delta leaves the largest |dout|
-  if (p.tiles && type == SNACK_F32) {
-    e = make_parts(&c, p, 4, workspace, &parts, s);
-  } else if (type == SNACK_F16) {
-    peak = reinterpret_cast<uint32_t *>(workspace);
-    c.peak = peak;
-    e = cudaMemsetAsync(peak, 0, 2 * sizeof(uint32_t), s);
-    Sources v = sources_of(c, p, workspace);
-    v.t[0] = v.t[2];
-    if (e == cudaSuccess && v.t[0].rows)
-      e = launch_kernel(attention_peak<T>, dim3(spread(v.t[0].rows)), 256, 0, false, s, v, c.sequences, c.d);
-  }
-  if (e != cudaSuccess) return e;
-  if (c.rows) {
+  const int width = part_width(c, type, true);
+  const bool made = p.tiles && width, peaks = made || type == SNACK_F16;
+  cudaError_t e = peaks ? clear_peaks(&c, workspace, s) : cudaSuccess;
+  if (e == cudaSuccess && c.rows) {
     const auto even = [](const Strided &t) {
       return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
     };
-    e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out), peak, s);
-    if (e != cudaSuccess) return e;
+    e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out),
+                        peaks ? reinterpret_cast<uint32_t *>(workspace) : nullptr, s);
   }
+  if (e != cudaSuccess) return e;
+  SplitParts parts = {};
+  if (made) {
+    e = make_parts<T>(&c, p, width, true, workspace, &parts, s);
+  } else if (type == SNACK_F16) {
+    Sources v = sources_of(c, p, workspace);
+    v.t[0] = v.t[2];
+    if (v.t[0].rows)
+      e = launch_kernel(attention_peak<T>, dim3(spread(v.t[0].rows)), 256, 0, false, s, v, c.sequences, c.d);
+  }
+  if (e != cudaSuccess) return e;
   return p.tiles ? tile_backward_launch(c, type, parts, s) : rows_backward_launch<T>(c, s);
 }
 

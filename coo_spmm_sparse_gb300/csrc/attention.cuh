@@ -135,8 +135,9 @@ cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
 // The forward call of few rows (attention_few.cu).
 cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s);
 
-// Where the float16 parts of 32-bit operands are: [tokens][heads][high 64, low 64].
+// Where operands made in float16 are: [tokens][heads][width]; width 0: none are.
 struct SplitParts {
+  int width;
   void *q, *k, *v, *dout;
 };
 

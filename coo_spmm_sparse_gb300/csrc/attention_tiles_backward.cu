@@ -25,19 +25,18 @@ __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) 
   }
 }
 
+// All operands are float16: bfloat16's are made in it first, 32-bit floats' in
+// two parts.
 template <typename T>
-__device__ __forceinline__ float ds_scale(const AttnCall &c) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) return 1.f;
-  return half_ds_scale(c);
-}
+using Parts = typename std::conditional<Operand<T>::kSplit, float, __half>::type;
 
-// Split operands are scaled by powers of two: what takes them out again.
+// Operands that were made are scaled by powers of two: what takes them out again.
 struct Scales {
   float scores, dprobs, q, k, dout;
 };
 template <typename T>
 __device__ __forceinline__ Scales scales_of(const AttnCall &c) {
-  if constexpr (!Operand<T>::kSplit) return Scales{c.scale_log2, 1.f, 1.f, 1.f, 1.f};
+  if constexpr (std::is_same<T, __half>::value) return Scales{c.scale_log2, 1.f, 1.f, 1.f, 1.f};
   const auto back = [&](int i) { return exp2f((float)-power_to_half(c.peak[i])); };
   return Scales{c.scale_log2 * back(2) * back(3), back(0) * back(1), back(2), back(3), back(0)};
 }
@@ -67,7 +66,7 @@ template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_keys(const AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
-  constexpr bool kSplit = Operand<T>::kSplit, kUp = !std::is_same<T, __nv_bfloat16>::value;  // kUp: float16 operands
+  constexpr bool kSplit = Operand<T>::kSplit, kScaled = !std::is_same<T, __half>::value;
   extern __shared__ unsigned char raw[];
   __shared__ KeyBars bars;
   unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<W>();
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.q_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<T, DP>(t_s, k0, q0 + (n & 1) * kStep);
+            products<Parts<T>, DP>(t_s, k0, q0 + (n & 1) * kStep);
             tc::commit(&bars.scores);
           }
           __syncwarp();
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.d_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<T, DP>(t_dp, v0, d0 + (n & 1) * kStep);
+            products<Parts<T>, DP>(t_dp, v0, d0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs);
           }
           __syncwarp();
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = wait(&bars.probs, n & 1);
           if (!ok) break;
           if (leader) {
-            sums<T, DP, kTile>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
+            sums<Parts<T>, DP, kTile>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.d_empty[n & 1]);
           }
           __syncwarp();
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
           if (leader) {
-            sums<T, DP, kTile>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
+            sums<Parts<T>, DP, kTile>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.q_empty[n & 1]);
           }
           __syncwarp();
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     } else if (warp == kStatWarp) {
-      const float up = kUp ? kHalfP : 0.f;
+      constexpr float up = kHalfP;
       for (int n = 0; n < all; ++n) {
         const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile;
         const int64_t place = (int64_t)(kh * G + g) * c.rows + qs.row;
@@ -234,10 +233,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int w = warp >> 2, j = j0 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
-    const float ds = ds_scale<T>(c);
+    const float ds = half_ds_scale(c);
     const Scales by = scales_of<T>(c);
     const float2 cs2 = make_float2(by.scores, by.scores);
-    const float ds_by_p = kUp ? ds * exp2f(-kHalfP) : 1.f;
+    const float ds_by_p = ds * exp2f(-kHalfP);
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
     constexpr int kDpChunk = kSplit ? 32 : kHalf;  // what registers leave room for
     const uint64_t seed = DROP ? c.draws() : 0;
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = !DROP || (kept[e & 3] >> ((x + e) & ~3) & 1) ? p[x + e] : 0.f;
-        store_row32<T>(s_at, x, v);
+        store_row32<Parts<T>>(s_at, x, v);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -313,24 +312,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           float v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            v[y] = kSplit ? t[x + y] * by.dprobs : t[x + y];
+            v[y] = kScaled ? t[x + y] * by.dprobs : t[x + y];
             if (DROP) v[y] = kept[y] >> (c0 + x) & 1 ? v[y] * c.keep_scale : 0.f;
           }
           const float2 u0 = tc::add2(make_float2(v[0], v[1]), make_float2(d.x, d.y));
           const float2 u1 = tc::add2(make_float2(v[2], v[3]), make_float2(d.z, d.w));
           float2 r0 = tc::mul2(make_float2(p[c0 + x], p[c0 + x + 1]), u0);
           float2 r1 = tc::mul2(make_float2(p[c0 + x + 2], p[c0 + x + 3]), u1);
-          if constexpr (kUp) {
-            r0 = tc::mul2(r0, make_float2(ds_by_p, ds_by_p));
-            r1 = tc::mul2(r1, make_float2(ds_by_p, ds_by_p));
-          }
+          r0 = tc::mul2(r0, make_float2(ds_by_p, ds_by_p));
+          r1 = tc::mul2(r1, make_float2(ds_by_p, ds_by_p));
           t[x] = r0.x;
           t[x + 1] = r0.y;
           t[x + 2] = r1.x;
           t[x + 3] = r1.y;
         }
 #pragma unroll
-        for (int x = 0; x < kDpChunk; x += 32) store_row32<T>(dp_at, c0 + x, t + x);
+        for (int x = 0; x < kDpChunk; x += 32) store_row32<Parts<T>>(dp_at, c0 + x, t + x);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -347,7 +344,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j < ks.cover)
         row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
               kh * to.head;
-      const float factor = w ? (kUp ? exp2f(-kHalfP) : 1.f) * c.keep_scale * by.dout : c.scale / ds * by.q;
+      const float factor = w ? exp2f(-kHalfP) * c.keep_scale * by.dout : c.scale / ds * by.q;
       if constexpr (kSplit) {
         if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP));
         store_floats<DP>(row, acc, factor, c.d, j >= nk);
@@ -386,7 +383,7 @@ template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_queries(const AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
-  constexpr bool kSplit = Operand<T>::kSplit, kUp = !std::is_same<T, __nv_bfloat16>::value;  // kUp: float16 operands
+  constexpr bool kSplit = Operand<T>::kSplit, kScaled = !std::is_same<T, __half>::value;
   extern __shared__ unsigned char raw[];
   __shared__ QueryBars bars;
   unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<W>();
@@ -482,7 +479,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.k_full[n % 3], (n / 3) & 1);
           if (done && leader) {
-            products<T, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
+            products<Parts<T>, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
             tc::commit(&bars.scores[n & 1]);
           }
           __syncwarp();
@@ -491,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.v_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<T, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
+            products<Parts<T>, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs[n & 1]);
             tc::commit(&bars.v_empty[n & 1]);
           }
@@ -505,7 +502,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           if (leader) {
             // split: two buffers in turn, each added to the rows' own sums two tiles later
-            sums<T, DP, kTile>(tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), tmem + (2 * n + 1) % 3 * kTile,
+            sums<Parts<T>, DP, kTile>(tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), tmem + (2 * n + 1) % 3 * kTile,
                                k0c + n % 3 * kStep, n > 0);
             tc::commit(&bars.k_empty[n % 3]);
           }
@@ -525,7 +522,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::take_registers<kRowRegisters>();
     const int w = warp >> 2, i = i0 + (warp & 3) * 32 + lane;
     const uint32_t at_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float ds = ds_scale<T>(c);
+    const float ds = half_ds_scale(c);
     float lse = 0.f, delta = 0.f;
     int lim = 0;
     if (i < nq) {
@@ -580,13 +577,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int y = 0; y < 4; ++y) t[x + y] = draw_lane(z, y) >= c.drop ? t[x + y] * c.keep_scale : 0.f;
         }
       }
-      if constexpr (kSplit)
+      if constexpr (kScaled)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] *= by.dprobs;
 #pragma unroll
       for (int x = 0; x < kHalf; x += 2) {
         float2 a = tc::add2(make_float2(t[x], t[x + 1]), delta2);
-        if constexpr (kUp) a = tc::mul2(a, make_float2(ds, ds));
+        a = tc::mul2(a, make_float2(ds, ds));
         a = tc::mul2(a, make_float2(p[x], p[x + 1]));
         t[x] = a.x;
         t[x + 1] = a.y;
@@ -594,8 +591,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
-      store_row32<T>(dp_at, 0, t);
-      store_row32<T>(dp_at, 32, t + 32);
+      store_row32<Parts<T>>(dp_at, 0, t);
+      store_row32<Parts<T>>(dp_at, 32, t + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores[b]);
@@ -614,7 +611,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int n = max(0, all - 2); n < all; ++n) add_sums<DP / 2>(acc, at_lane + 3 * kTile + (n & 1) * DP + from);
         store_floats<DP / 2>(row, acc, c.scale / ds * by.k, c.d - from, lim == 0);
       } else {
-        store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, c.scale / ds, c.d - from, all > 0, lim == 0);
+        store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, c.scale / ds * by.k, c.d - from, all > 0, lim == 0);
       }
     }
     tc::fence_before();
@@ -658,7 +655,7 @@ cudaError_t backward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s)
 bool tile_backward_fits(const AttnCall &c, int type) {
   const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
   if (!tiles_fit(c, type)) return false;
-  if (type == SNACK_F32) return true;
+  if (type != SNACK_F16) return true;  // their operands are made as TMA wants them
   return even(c.q, c.heads, c.q_tokens, qn) && (!c.dout.p || even(c.dout, c.heads, c.q_tokens, qn)) &&
          even(c.k, c.key_heads, c.k_tokens, kn) && even(c.v, c.key_heads, c.k_tokens, kn);
 }

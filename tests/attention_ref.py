@@ -78,10 +78,12 @@ def one_sequence(q, k, v, *, causal, scale, M=None, dout=None, dtype=None):
     e_dP = 2.0 ** -18 * M * (dout.abs() @ v.abs().mT)
     e_delta = ((dout.abs() * e_out).sum(-1, keepdim=True) + 1e-5 * (dout.abs() * out.abs()).sum(-1, keepdim=True))
     e_dS = dS.abs() * (share + u) + P * (e_dP + e_delta)
-    if half:  # dS is scaled so that its bound 2 d max|dout| max|v| max(M) is at least 2^13: a step is 2^-25 there
-        top = dout.abs().max() * v.abs().max() * M.max() if dout.numel() and v.numel() else 0.0
-        e_dS = e_dS + seen * (2 * q.shape[-1] * top * 2.0 ** -38)
-        low = 2.0 ** -39 * seen  # P is taken 2^14 fold
+    # Operands of the backward products may be float16 (32-bit floats in two parts): dS is scaled
+    # so that its bound 2 d max|dout| max|v| max(M) is at least 2^13, and half a step of the
+    # smallest float16 is 2^-25: 2^-38 of the bound.  P is taken 2^14 fold: 2^-39.
+    top = dout.abs().max() * v.abs().max() * M.max() if dout.numel() and v.numel() else 0.0
+    e_dS = e_dS + seen * (2 * q.shape[-1] * top * 2.0 ** -38)
+    low = 2.0 ** -39 * seen
     res["dq"] = (scale * dS @ k, abs(scale) * (e_dS + 1e-5 * dS.abs()) @ k.abs())
     res["dk"] = (scale * dS.mT @ q, abs(scale) * (e_dS + 1e-5 * dS.abs()).mT @ q.abs())
     res["dv"] = (PM.mT @ dout, (PM * (share + u) + low * M).mT @ dout.abs())
