@@ -355,7 +355,7 @@ AttnCall call_of(const snack_attention_args *a) {
 // How a call is computed, and what of the workspace it takes.
 struct Plan {
   bool tiles = false, few = false;  // on tcgen05; in blocks of 16 rows
-  int splits = 1, chunk = 0;
+  int splits = 1, chunk = 0, width = 0;  // width: columns of operands made in float16; 0: none are
   size_t delta = 0, parts[4] = {}, bytes = 0;  // offsets: after the peaks; q, k, v, dout
 };
 constexpr size_t kPeaks = 256;
@@ -364,8 +364,11 @@ constexpr size_t kPeaks = 256;
 // of backward calls.  There the gradients of the scores are an operand too:
 // rounded to bfloat16 they made dq and dk 1.5 times as far off as the rounding of
 // the results alone, in float16 1.1 times, for 5 % of a long call's time.
+// 16-bit tensors that TMA cannot bring as they lie (odd head sizes, addresses or
+// strides) are made too: else mma.sync would take them, several times slower.
 int part_width(const AttnCall &c, int type, bool backward) {
-  return type == SNACK_F32 ? 128 : type == SNACK_BF16 && backward ? (c.d <= 64 ? 64 : 128) : 0;
+  if (type == SNACK_F32) return 128;
+  return (type == SNACK_BF16 && backward) || !tiles_read(c) ? (c.d <= 64 ? 64 : 128) : 0;
 }
 void plan_parts(Plan *p, const AttnCall &c, int width, bool backward) {
   const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
@@ -376,24 +379,30 @@ void plan_parts(Plan *p, const AttnCall &c, int width, bool backward) {
   }
 }
 
-constexpr double kTilesFrom32 = 4e6;
-// 16-bit calls go to the tiles from 64 query tokens on.  32-bit ones pay for
-// making the parts first (two launches, three or four tensors read twice).
-bool worth_tiles(const AttnCall &c, int type) {
+// The tiles take calls from 64 query tokens on, where there is work for them:
+// X = query rows (tokens * heads) * keys.  Measured with 12 heads of 64, bf16,
+// tiles and mma.sync, us: forward 1 x 256 x 256 (X = 8e5) 11, 9; 4 x 256 x 256
+// (3e6) 11, 17; 1 x 1024 x 1024 (1.3e7) 19, 41; backward 35, 23; 37, 45; 50, 92.
+// fp32, where the operands are made first: forward 4 x 256 x 256 28, 29; 8 x 256
+// x 256 (6e6) 32, 55; backward, 8 x 256 x 256, 66, 132.
+// Few rows over many keys leave the forward tiles alone with their keys, which
+// blocks of 16 rows share out: 1 x 64 x 4096 45, 19; 1 x 128 x 8192 66, 52.
+bool worth_tiles(const AttnCall &c, int type, bool backward) {
   if (c.q_tokens < 64 || c.k_tokens < 64) return false;
-  return type != SNACK_F32 || (double)c.rows * c.heads * c.k_tokens >= kTilesFrom32;
+  const double rows = (double)c.rows * c.heads, x = rows * c.k_tokens;
+  return x >= (type == SNACK_F32 && !backward ? 4e6 : 2e6) && (backward || rows >= 2048);
 }
 
 // Few rows (16 to a block) where blocks of 128 would leave SMs idle, and the
 // keys in parts where even those do.
 Plan plan_forward(const AttnCall &c, int type) {
   Plan p;
-  p.tiles = worth_tiles(c, type) && tile_forward_fits(c, type);
+  p.tiles = worth_tiles(c, type, false) && tiles_take(c, type);
   if (p.tiles) {
-    const int width = part_width(c, type, false);
-    if (width) {
+    p.width = part_width(c, type, false);
+    if (p.width) {
       p.bytes = kPeaks;
-      plan_parts(&p, c, width, false);
+      plan_parts(&p, c, p.width, false);
     }
     return p;
   }
@@ -417,9 +426,9 @@ Plan plan_backward(const AttnCall &c, int type) {
   p.bytes = kPeaks;
   p.delta = p.bytes;
   p.bytes += round_up(c.rows * c.heads * (int64_t)sizeof(float), 256);
-  p.tiles = worth_tiles(c, type) && tile_backward_fits(c, type);
-  const int width = part_width(c, type, true);
-  if (p.tiles && width) plan_parts(&p, c, width, true);
+  p.tiles = worth_tiles(c, type, true) && tiles_take(c, type);
+  p.width = p.tiles ? part_width(c, type, true) : 0;
+  if (p.width) plan_parts(&p, c, p.width, true);
   return p;
 }
 
@@ -446,15 +455,15 @@ unsigned spread(int64_t rows) {  // a warp for each, or as many as are resident 
 // Makes the float16 parts of a call's operands: q, k, v and, backward, dout,
 // whose peak is there already.
 template <typename T>
-cudaError_t make_parts(AttnCall *c, const Plan &p, int width, bool backward, char *workspace, SplitParts *parts,
-                       cudaStream_t s) {
+cudaError_t make_parts(AttnCall *c, const Plan &p, bool backward, char *workspace, SplitParts *parts, cudaStream_t s) {
   const Sources all = sources_of(*c, p, workspace);
   const unsigned blocks = spread(std::max(all.t[0].rows, all.t[1].rows));
   cudaError_t e = launch_kernel(attention_peak<T>, dim3(blocks, 3), 256, 0, false, s, all, c->sequences, c->d);
   if (e == cudaSuccess)
-    e = launch_kernel(width == 64 ? half_parts<T, 64> : half_parts<T, 128>, dim3(blocks, backward ? 4 : 3), 256, 0,
+    e = launch_kernel(p.width == 64 ? half_parts<T, 64> : half_parts<T, 128>, dim3(blocks, backward ? 4 : 3), 256, 0,
                       false, s, all, c->sequences, c->d);
-  *parts = SplitParts{width, all.t[0].parts, all.t[1].parts, all.t[2].parts, all.t[3].parts};
+  c->made = 1;
+  *parts = SplitParts{p.width, all.t[0].parts, all.t[1].parts, all.t[2].parts, all.t[3].parts};
   return e;
 }
 
@@ -467,10 +476,9 @@ template <typename T>
 cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   if (p.tiles) {
     SplitParts parts = {};
-    const int width = part_width(c, type, false);
-    if (width) {
+    if (p.width) {
       cudaError_t e = clear_peaks(&c, workspace, s);
-      if (e == cudaSuccess) e = make_parts<T>(&c, p, width, false, workspace, &parts, s);
+      if (e == cudaSuccess) e = make_parts<T>(&c, p, false, workspace, &parts, s);
       if (e != cudaSuccess) return e;
     }
     return tile_forward_launch(c, type, parts, s);
@@ -488,8 +496,7 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
 template <typename T>
 cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  const int width = part_width(c, type, true);
-  const bool made = p.tiles && width, peaks = made || type == SNACK_F16;
+  const bool peaks = p.width || type == SNACK_F16;
   cudaError_t e = peaks ? clear_peaks(&c, workspace, s) : cudaSuccess;
   if (e == cudaSuccess && c.rows) {
     const auto even = [](const Strided &t) {
@@ -500,8 +507,8 @@ cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace,
   }
   if (e != cudaSuccess) return e;
   SplitParts parts = {};
-  if (made) {
-    e = make_parts<T>(&c, p, width, true, workspace, &parts, s);
+  if (p.width) {
+    e = make_parts<T>(&c, p, true, workspace, &parts, s);
   } else if (type == SNACK_F16) {
     Sources v = sources_of(c, p, workspace);
     v.t[0] = v.t[2];
@@ -509,7 +516,9 @@ cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace,
       e = launch_kernel(attention_peak<T>, dim3(spread(v.t[0].rows)), 256, 0, false, s, v, c.sequences, c.d);
   }
   if (e != cudaSuccess) return e;
-  return p.tiles ? tile_backward_launch(c, type, parts, s) : rows_backward_launch<T>(c, s);
+  // (a float16 call whose dout alone lies badly was not planned for)
+  if (p.tiles && (p.width || tiles_read(c))) return tile_backward_launch(c, type, parts, s);
+  return rows_backward_launch<T>(c, s);
 }
 
 }  // namespace
@@ -564,9 +573,8 @@ extern "C" snack_status snack_attention_backward(const snack_attention_args *a, 
   AttnCall c = call_of(a);
   if (!workspace) return bad("workspace is NULL");
   if (c.rows && (!g->dout || !g->out || !g->lse)) return bad("dout, out or lse is NULL");
+  const Plan p = plan_backward(c, a->type);  // before dout: the plan that the workspace was asked for
   c.dout = strided(g->dout, g->dout_stride);
-  // (what dout decides, whether a 16-bit call can go to the tiles, takes no workspace)
-  const Plan p = plan_backward(c, a->type);
   c.out = strided(g->out, g->out_stride);
   c.dq = strided(g->dq, g->dq_stride);
   c.dk = strided(g->dk, g->dk_stride);

@@ -22,6 +22,7 @@ struct AttnCall {
   int sequences, q_tokens, k_tokens;
   int heads, key_heads, group, d;
   int causal, splits, chunk;
+  int made;  // the operands were made in float16, scaled by the powers of two of their peaks
   float scale, scale_log2;  // scale * log2(e)
   const int32_t *q_offsets, *k_offsets, *q_lengths, *k_lengths;
   uint32_t drop;  // 0: no dropout; else a probability is kept where its 16 bits are at least this
@@ -142,11 +143,12 @@ struct SplitParts {
 };
 
 // Those of attention on tcgen05 (attention_tiles*.cu): which calls they take,
-// and whether one of their bounded waits has run out since the last question.
-bool tile_forward_fits(const AttnCall &c, int type);
+// whether TMA can bring a 16-bit call's tensors as they lie (else they are made in
+// float16 first), and whether one of their bounded waits has run out since the last question.
+bool tiles_take(const AttnCall &c, int type);
+bool tiles_read(const AttnCall &c);  // as the tensors lie
 cudaError_t tile_forward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s);
 cudaError_t tile_forward_failed(int *flag, cudaStream_t s);
-bool tile_backward_fits(const AttnCall &c, int type);
 cudaError_t tile_backward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s);
 cudaError_t tile_backward_failed(int *flag, cudaStream_t s);
 

@@ -107,10 +107,10 @@ __device__ __forceinline__ void store_sums(uint32_t from, T *row, float factor, 
       tc::wait_loads();
     }
     if (row) {
-      const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
+      const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0 && d % 8 == 0;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
-        if (c + i >= d) break;  // (the head size is a multiple of eight)
+        if (c + i >= d) break;
         uint32_t u[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -120,15 +120,23 @@ __device__ __forceinline__ void store_sums(uint32_t from, T *row, float factor, 
         } else {
           unsigned short *const to = reinterpret_cast<unsigned short *>(row + c + i);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            to[2 * e] = (unsigned short)u[e];
-            to[2 * e + 1] = (unsigned short)(u[e] >> 16);
-          }
+          for (int e = 0; e < 8; ++e)
+            if (c + i + e < d) to[e] = (unsigned short)(u[e / 2] >> (16 * (e & 1)));
         }
       }
     }
     __syncwarp();
   }
+}
+
+// Operands that were made are scaled by powers of two: what takes them out again.
+struct Scales {
+  float scores, dprobs, q, k, v, dout;
+};
+__device__ __forceinline__ Scales scales_of(const AttnCall &c) {
+  if (!c.made) return Scales{c.scale_log2, 1.f, 1.f, 1.f, 1.f, 1.f};
+  const auto back = [&](int i) { return exp2f((float)-power_to_half(c.peak[i])); };
+  return Scales{c.scale_log2 * back(2) * back(3), back(0) * back(1), back(2), back(3), back(1), back(0)};
 }
 
 // Rows a times rows b, over the head size.
@@ -252,11 +260,6 @@ static inline bool map_of(CUtensorMap *m, int type, const Strided &t, int64_t d,
 static inline bool even(const Strided &t, int64_t heads, int64_t tokens, int64_t seqs) {
   const auto good = [](int64_t n, int64_t s) { return n <= 1 || (s > 0 && s % 8 == 0 && s < (int64_t)1 << 38); };
   return aligned_to(t.p, 16) && good(heads, t.head) && good(tokens, t.token) && good(seqs, t.seq);
-}
-
-static inline bool tiles_fit(const AttnCall &c, int type) {
-  return (type == SNACK_F32 ? c.d <= 64 : c.d % 8 == 0) && c.scale > 0.f && c.k_tokens > 0 && c.q_tokens > 0 &&
-         c.sequences > 0;
 }
 
 // The maps of a call's operands: its tensors, or their float16 parts.

@@ -30,17 +30,6 @@ __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) 
 template <typename T>
 using Parts = typename std::conditional<Operand<T>::kSplit, float, __half>::type;
 
-// Operands that were made are scaled by powers of two: what takes them out again.
-struct Scales {
-  float scores, dprobs, q, k, dout;
-};
-template <typename T>
-__device__ __forceinline__ Scales scales_of(const AttnCall &c) {
-  if constexpr (std::is_same<T, __half>::value) return Scales{c.scale_log2, 1.f, 1.f, 1.f, 1.f};
-  const auto back = [&](int i) { return exp2f((float)-power_to_half(c.peak[i])); };
-  return Scales{c.scale_log2 * back(2) * back(3), back(0) * back(1), back(2), back(3), back(0)};
-}
-
 // ------------------------------------------------------------------ keys and values
 
 struct KeyBars {
@@ -66,7 +55,7 @@ template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_keys(const AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
-  constexpr bool kSplit = Operand<T>::kSplit, kScaled = !std::is_same<T, __half>::value;
+  constexpr bool kSplit = Operand<T>::kSplit;
   extern __shared__ unsigned char raw[];
   __shared__ KeyBars bars;
   unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<W>();
@@ -234,7 +223,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
     const float ds = half_ds_scale(c);
-    const Scales by = scales_of<T>(c);
+    const Scales by = scales_of(c);
     const float2 cs2 = make_float2(by.scores, by.scores);
     const float ds_by_p = ds * exp2f(-kHalfP);
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
@@ -312,7 +301,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           float v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            v[y] = kScaled ? t[x + y] * by.dprobs : t[x + y];
+            v[y] = t[x + y] * by.dprobs;
             if (DROP) v[y] = kept[y] >> (c0 + x) & 1 ? v[y] * c.keep_scale : 0.f;
           }
           const float2 u0 = tc::add2(make_float2(v[0], v[1]), make_float2(d.x, d.y));
@@ -383,7 +372,7 @@ template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_queries(const AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
-  constexpr bool kSplit = Operand<T>::kSplit, kScaled = !std::is_same<T, __half>::value;
+  constexpr bool kSplit = Operand<T>::kSplit;
   extern __shared__ unsigned char raw[];
   __shared__ QueryBars bars;
   unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<W>();
@@ -534,7 +523,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       else
         lim = max(0, seen_keys(c.causal, i, nq, nk));
     }
-    const Scales by = scales_of<T>(c);
+    const Scales by = scales_of(c);
     float acc[kSplit ? DP / 2 : 1] = {};  // split: the sums of this warpgroup's half of the columns
     const float2 cs2 = make_float2(by.scores, by.scores), off2 = make_float2(-lse, -lse);
     const float2 delta2 = make_float2(-delta, -delta);
@@ -577,12 +566,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int y = 0; y < 4; ++y) t[x + y] = draw_lane(z, y) >= c.drop ? t[x + y] * c.keep_scale : 0.f;
         }
       }
-      if constexpr (kScaled)
-#pragma unroll
-        for (int x = 0; x < kHalf; ++x) t[x] *= by.dprobs;
 #pragma unroll
       for (int x = 0; x < kHalf; x += 2) {
-        float2 a = tc::add2(make_float2(t[x], t[x + 1]), delta2);
+        float2 a = tc::fma2(make_float2(t[x], t[x + 1]), make_float2(by.dprobs, by.dprobs), delta2);
         a = tc::mul2(a, make_float2(ds, ds));
         a = tc::mul2(a, make_float2(p[x], p[x + 1]));
         t[x] = a.x;
@@ -651,14 +637,6 @@ cudaError_t backward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s)
 }
 
 }  // namespace
-
-bool tile_backward_fits(const AttnCall &c, int type) {
-  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
-  if (!tiles_fit(c, type)) return false;
-  if (type != SNACK_F16) return true;  // their operands are made as TMA wants them
-  return even(c.q, c.heads, c.q_tokens, qn) && (!c.dout.p || even(c.dout, c.heads, c.q_tokens, qn)) &&
-         even(c.k, c.key_heads, c.k_tokens, kn) && even(c.v, c.key_heads, c.k_tokens, kn);
-}
 
 cudaError_t tile_backward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s) {
   TileMaps m = {};

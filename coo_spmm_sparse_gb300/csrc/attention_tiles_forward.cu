@@ -23,7 +23,7 @@ struct ForwardBars {
 // The accumulated row is multiplied down only when the maximum has grown by
 // more than 2^8 since the last time: until then probabilities are up to 2^8
 // fold, which the 32-bit sums hold as well.
-template <typename T, int DP, bool DROP>
+template <typename T, int DP, bool DROP, typename Op>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_forward(const AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (steps[t]) {
           ok = wait(&bars.q[t], 0);
           if (ok && leader) {
-            products<T, DP>(tmem + t * kTile, q0 + t * kStep, k0);
+            products<Op, DP>(tmem + t * kTile, q0 + t * kStep, k0);
             tc::commit(&bars.scores[t]);
           }
         }
@@ -142,12 +142,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (j >= steps[t]) continue;
           const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * DP;
           ok = wait(&bars.probs[t][0], j & 1);
-          if (ok && leader) sums<T, DP, kTile / 2>(o_at, s_at, v_at, j > 0);
+          if (ok && leader) sums<Op, DP, kTile / 2>(o_at, s_at, v_at, j > 0);
           ok = ok && wait(&bars.probs[t][1], j & 1);
           if (ok && leader) {
-            sums<T, DP, kTile / 2>(o_at, s_at, v_at, true, kTile / 2);
+            sums<Op, DP, kTile / 2>(o_at, s_at, v_at, true, kTile / 2);
             if (j + 1 < steps[t]) {
-              products<T, DP>(s_at, q0 + t * kStep, k_at);
+              products<Op, DP>(s_at, q0 + t * kStep, k_at);
               tc::commit(&bars.scores[t]);
             } else {
               tc::commit(&bars.done[t]);
@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
     const int lim = i < nq ? max(0, seen_keys(c.causal, i, nq, nk)) : 0;
-    const float cs = c.scale_log2;
+    const Scales by = scales_of(c);
+    const float cs = by.scores;
     uint64_t draw = 0;
     if (DROP) draw = dropout_row(c.draws(), qs.row + i, c.heads, head);
     float m = -INFINITY, sum = 0.f;
@@ -182,7 +183,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if constexpr (kSplit) {
       // Two passes over the scores in tensor memory, 64 at a time: a row's sums
       // stay in registers beside them.
-      const float cs = c.scale_log2 * exp2f((float)-power_to_half(c.peak[2])) * exp2f((float)-power_to_half(c.peak[3]));
       float o[DP] = {};
       for (int j = 0; j < steps[t]; ++j) {
         ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float *const row = static_cast<float *>(c.out.p) +
                            (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) +
                            head * c.out.head;
-        store_floats<DP>(row, o, c.keep_scale / sum * exp2f((float)-power_to_half(c.peak[1])), c.d, sum == 0.f);
+        store_floats<DP>(row, o, c.keep_scale / sum * by.v, c.d, sum == 0.f);
         c.lse[(int64_t)head * c.rows + qs.row + i] =
             sum == 0.f ? -INFINITY : m * cs * kLn2 + (logf(sum) - kHalfP * kLn2);
       }
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             s[x + e] = a.x;
             s[x + e + 1] = a.y;
           } else {
-            p[e / 2] = pack2<T>(a.x, a.y);
+            p[e / 2] = pack2<Op>(a.x, a.y);
           }
         }
         if (DROP) {
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float k[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) k[y] = draw_lane(z, y) >= c.drop ? s[x + e + y] : 0.f;
-            p[e / 2] = pack2<T>(k[0], k[1]);
-            p[e / 2 + 1] = pack2<T>(k[2], k[3]);
+            p[e / 2] = pack2<Op>(k[0], k[1]);
+            p[e / 2 + 1] = pack2<Op>(k[2], k[3]);
           }
         }
         tc::store32(s_at + x, p);
@@ -341,9 +341,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (mine)
         row = static_cast<T *>(c.out.p) + (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) +
               head * c.out.head;
-      store_sums<T, DP>(o_at, row, c.keep_scale / sum, c.d, steps[t] > 0, sum == 0.f);
+      store_sums<T, DP>(o_at, row, c.keep_scale / sum * by.v, c.d, steps[t] > 0, sum == 0.f);
       if (mine)
-        c.lse[(int64_t)head * c.rows + qs.row + i] = sum == 0.f ? -INFINITY : m * c.scale + logf(sum);
+        c.lse[(int64_t)head * c.rows + qs.row + i] = sum == 0.f ? -INFINITY : m * cs * kLn2 + logf(sum);
     }
     }
     tc::fence_before();
@@ -358,38 +358,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 }  // namespace
 
-bool tile_forward_fits(const AttnCall &c, int type) {
-  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
-  return tiles_fit(c, type) &&
-         (type == SNACK_F32 || (even(c.q, c.heads, c.q_tokens, qn) && even(c.k, c.key_heads, c.k_tokens, kn) &&
-                                even(c.v, c.key_heads, c.k_tokens, kn)));
+bool tiles_take(const AttnCall &c, int type) {
+  return (type != SNACK_F32 || c.d <= 64) && c.scale > 0.f && c.k_tokens > 0 && c.q_tokens > 0 && c.sequences > 0;
 }
 
-template <typename T, int DP, bool DROP>
+bool tiles_read(const AttnCall &c) {
+  const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
+  return c.d % 8 == 0 && even(c.q, c.heads, c.q_tokens, qn) && even(c.k, c.key_heads, c.k_tokens, kn) &&
+         even(c.v, c.key_heads, c.k_tokens, kn) && (!c.dout.p || even(c.dout, c.heads, c.q_tokens, qn));
+}
+
+template <typename T, int DP, bool DROP, typename Op>
 static cudaError_t forward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
   const bool by_heads = c.group % 2 == 0;
   const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, by_heads ? kTile : 2 * kTile) *
                          (by_heads ? c.heads / 2 : c.heads);
-  const auto kern = tile_forward<T, DP, DROP>;
+  const auto kern = tile_forward<T, DP, DROP, Op>;
   constexpr size_t smem = tile_forward_smem<wide<T, DP>()>();
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, smem, false, s, c, m);
 }
 
-template <typename T>
+template <typename T, typename Op>
 static cudaError_t forward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
   if constexpr (!Operand<T>::kSplit)
-    if (c.d > 64) return c.drop ? forward_launch<T, 128, true>(c, m, s) : forward_launch<T, 128, false>(c, m, s);
-  return c.drop ? forward_launch<T, 64, true>(c, m, s) : forward_launch<T, 64, false>(c, m, s);
+    if (c.d > 64)
+      return c.drop ? forward_launch<T, 128, true, Op>(c, m, s) : forward_launch<T, 128, false, Op>(c, m, s);
+  return c.drop ? forward_launch<T, 64, true, Op>(c, m, s) : forward_launch<T, 64, false, Op>(c, m, s);
 }
 
 cudaError_t tile_forward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s) {
   TileMaps m = {};
   if (!maps_of(&m, c, type, parts, false)) return cudaErrorInvalidValue;
-  return type == SNACK_F32    ? forward_typed<float>(c, m, s)
-         : type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, m, s)
-                              : forward_typed<__half>(c, m, s);
+  if (type == SNACK_F32) return forward_typed<float, float>(c, m, s);
+  if (type == SNACK_F16) return forward_typed<__half, __half>(c, m, s);
+  return c.made ? forward_typed<__nv_bfloat16, __half>(c, m, s) : forward_typed<__nv_bfloat16, __nv_bfloat16>(c, m, s);
 }
 
 cudaError_t tile_forward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }

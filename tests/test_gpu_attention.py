@@ -79,6 +79,32 @@ def test_long_sequences_that_fill_the_gpu(dtype, n, length, heads, key_heads, d)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [1, 33, 40, 63, 64, 100, 128])
+@pytest.mark.parametrize("dropout", [0.0, 0.2])
+def test_tensors_that_cannot_be_copied_as_they_lie(dtype, d, dropout):
+    """Odd head sizes, addresses off 16 bytes and heads before tokens, at sizes where the operands
+    are made in float16 first (32-bit floats from 4e6 query rows times keys on)."""
+    g = gen(d)
+    n, length = 2, 777
+    q, dout = (rnd(g, (n, length, 6, d + 1), dtype)[..., 1:] for _ in range(2))
+    k = rnd(g, (n, 3, length, d), dtype).transpose(1, 2)
+    v = rnd(g, (n, length, 1, d), dtype).expand(n, length, 3, d)
+    check(q, k, v, dout, dropout=dropout, seed=d)
+    check(q, k, v, dout.contiguous(), causal=False, k_lengths=ints(777, 300))
+
+
+def test_operands_of_every_magnitude():
+    """Tensors far from one another and from 1, channels and tokens far from their tensor's largest."""
+    for dtype in (F32, BF16):
+        for scales in ((1e-9, 1e9, 1e5), (1e6, 1e-6, 1e-12), (1.0, 1.0, 1e20)):
+            g = gen(3)
+            q, k, v = (rnd(g, (1, 1100, 4, 64), dtype, s) for s in scales)
+            v[..., ::7] *= 1e-3
+            q[:, ::5] *= 1e-2
+            check(q, k, v, rnd(g, (1, 1100, 4, 64), dtype, 1e-6))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,q,k", [(1, 1, 32768), (2, 1, 5000), (4, 2, 3001), (40, 1, 700), (1, 19, 9000)])
 def test_few_queries_over_long_caches(dtype, n, q, k):
     g = gen(k)
@@ -347,6 +373,43 @@ def test_captured_calls_draw_again_when_their_seed_changes():
         out, lse = sn.snack_attention_forward(q, k, v, dropout=0.5, seed=100 + step)
         want = (out, *sn.snack_attention_backward(dout, q, k, v, out, lse, dropout=0.5, seed=100 + step))
         assert all(torch.equal(a, b) for a, b in zip(res, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_calls_on_two_streams_and_in_two_graphs(dtype):
+    """Two calls at once, each with its own workspace: the same results as alone."""
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(16)
+    sets = [[rnd(g, (2, 900, 6, 64), dtype) for _ in range(4)] for _ in range(2)]
+
+    def both(q, k, v, dout):
+        out, lse = sn.snack_attention_forward(q, k, v)
+        return (out, *sn.snack_attention_backward(dout, q, k, v, out, lse))
+
+    want = [both(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(both(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    graphs, res = [], []
+    for s in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            res.append(both(*s))
+    for _ in range(3):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert not sn.snack_attention_error()
 
 
 def test_a_given_stream():
