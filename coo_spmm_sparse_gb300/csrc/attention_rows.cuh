@@ -443,23 +443,23 @@ __device__ __forceinline__ float ds_scale(const AttnCall &c) {
   return half_ds_scale(c);
 }
 
-template <typename T, int DP, int WM, int WN, int BQ>
+template <typename T, int DP, int WM, int WN, int BQ, int ST>
 constexpr size_t rows_backward_smem() {
-  const size_t tiles = (size_t)(2 * 16 * WM + 2 * 2 * WN * BQ) * (DP + 8) * sizeof(T);
+  const size_t tiles = (size_t)(2 * 16 * WM + ST * 2 * WN * BQ) * (DP + 8) * sizeof(T);
   const size_t room = (size_t)(WN - 1) * WM * 16 * (DP + 8) * sizeof(float);
   return tiles > room ? tiles : room;
 }
 
 // Gradients of 16 * WM keys and values: the query rows that see them stream past.
-template <typename T, int DP, int WM, int WN, int BQ>
+template <typename T, int DP, int WM, int WN, int BQ, int ST>
 __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
   using Ops = Tile<T, DP>;
   constexpr int kLd = Ops::kLd, NB = BQ / 8, STEP = WN * BQ;
   extern __shared__ __align__(16) unsigned char smem[];
   T *sk = reinterpret_cast<T *>(smem), *sv = sk + 16 * WM * kLd, *sqd = sv + 16 * WM * kLd;
-  __shared__ float s_lse[2][STEP], s_delta[2][STEP];
-  __shared__ int s_lim[2][STEP];
-  __shared__ uint64_t s_draw[2][STEP];
+  __shared__ float s_lse[ST][STEP], s_delta[ST][STEP];
+  __shared__ int s_lim[ST][STEP];
+  __shared__ uint64_t s_draw[ST][STEP];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp / WN, wn = warp % WN;
   const int kh = block % c.key_heads, G = c.group;
@@ -519,13 +519,14 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
     store_row_stats(0);
   }
   copies_commit();
-  for (int row0 = row_begin, stage = 0; row0 < end; row0 += STEP, stage ^= 1) {
-    if (row0 + STEP < end) {
-      copy_step(stage ^ 1, row0 + STEP);
+  for (int row0 = row_begin, stage = 0; row0 < end; row0 += STEP, stage ^= ST - 1) {
+    const bool more = row0 + STEP < end;
+    if (more) {
+      if (ST == 2) copy_step(stage ^ 1, row0 + STEP);
       load_row(row0 + STEP);
     }
-    copies_commit();
-    copies_wait<1>();
+    if (ST == 2) copies_commit();
+    copies_wait<ST - 1>();
     __syncthreads();
     const T *q = sqd + (stage * 2 * STEP + wn * BQ) * kLd, *d = q + STEP * kLd;
     if (row0 + wn * BQ < end) {
@@ -554,8 +555,13 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
       Ops::template sums_by_rows<NB>(dv, p, d, lane);
       Ops::template sums_by_rows<NB>(dk, t, q, lane);
     }
-    if (row0 + STEP < end) store_row_stats(stage ^ 1);
+    if (ST == 2 && more) store_row_stats(stage ^ 1);
     __syncthreads();
+    if (ST == 1 && more) {
+      copy_step(0, row0 + STEP);
+      store_row_stats(0);
+      copies_commit();
+    }
   }
   copies_wait<0>();
   if constexpr (WN > 1) {
@@ -576,7 +582,7 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
 }
 
 // Gradients of 16 * WM query rows: the keys and values that they see stream past.
-template <typename T, int DP, int WM, int WN, int BN>
+template <typename T, int DP, int WM, int WN, int BN, int ST>
 __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
   using Ops = Tile<T, DP>;
   constexpr int kLd = Ops::kLd, NB = BN / 8, STEP = WN * BN;
@@ -630,10 +636,12 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
     copy_step(0, 0);
   }
   copies_commit();
-  for (int key0 = 0, stage = 0; key0 < end; key0 += STEP, stage ^= 1) {
-    if (key0 + STEP < end) copy_step(stage ^ 1, key0 + STEP);
-    copies_commit();
-    copies_wait<1>();
+  for (int key0 = 0, stage = 0; key0 < end; key0 += STEP, stage ^= ST - 1) {
+    if (ST == 2) {
+      if (key0 + STEP < end) copy_step(stage ^ 1, key0 + STEP);
+      copies_commit();
+    }
+    copies_wait<ST - 1>();
     __syncthreads();
     const T *k = skv + (stage * 2 * STEP + wn * BN) * kLd, *v = k + STEP * kLd;
     const int key = key0 + wn * BN;
@@ -658,6 +666,10 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
       Ops::template sums_by_rows<NB>(dq, t, k, lane);
     }
     __syncthreads();
+    if (ST == 1 && key0 + STEP < end) {
+      copy_step(0, key0 + STEP);
+      copies_commit();
+    }
   }
   copies_wait<0>();
   if constexpr (WN > 1) {
@@ -676,12 +688,12 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
 
 // The first `key_blocks` blocks take keys, the others queries.  ONLY: the
 // kernel has code for one of them (1: keys, 2: queries) and that one's registers.
-template <typename T, int DP, int WM, int WN, int BN, int ONLY>
+template <typename T, int DP, int WM, int WN, int BN, int ST, int ONLY>
 __global__ void __launch_bounds__(32 * WM * WN) rows_backward(const AttnCall c, int key_blocks) {
   if (ONLY == 1 || (ONLY == 0 && (int)blockIdx.x < key_blocks))
-    keys_of_rows<T, DP, WM, WN, BN>(c, blockIdx.x);
+    keys_of_rows<T, DP, WM, WN, BN, ST>(c, blockIdx.x);
   else
-    queries_of_rows<T, DP, WM, WN, BN>(c, blockIdx.x - key_blocks);
+    queries_of_rows<T, DP, WM, WN, BN, ST>(c, blockIdx.x - key_blocks);
 }
 
 }  // namespace snack
