@@ -64,6 +64,13 @@ __device__ __forceinline__ unsigned char *align1024(unsigned char *p) {
   return p + ((1024 - (tc::smem_addr(p) & 1023)) & 1023);
 }
 
+// A block without a tile returns the tensor memory that it was given.
+__device__ __forceinline__ void leave_block(int warp, const uint32_t *tmem) {
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kMmaWarp) tc::tmem_free(*tmem, 512);
+}
+
 // Starts the copy of a tile; one thread.
 template <int DP>
 __device__ __forceinline__ void copy_tile(unsigned char *to, const CUtensorMap *map, uint64_t *bar, int head,

@@ -63,9 +63,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
+  // the queries' kernel, which needs nothing of this one, may begin on SMs that this one leaves
+  dependency_launch();
+  // barriers, tensor memory and the block's place are made ready side by side
+  if (warp == kCopyWarp && lane == 0) {
+    tc::bar_init(&bars.kv, 2);
+    for (int i = 0; i < 2; ++i) {
+      tc::bar_init(&bars.q_full[i], 1);
+      tc::bar_init(&bars.q_empty[i], 1);
+      tc::bar_init(&bars.d_full[i], 1);
+      tc::bar_init(&bars.d_empty[i], 1);
+      tc::bar_init(&bars.stat_full[i], 1);
+      tc::bar_init(&bars.stat_empty[i], 8);
+    }
+    tc::bar_init(&bars.scores, 1);
+    tc::bar_init(&bars.probs, 8);
+    tc::bar_init(&bars.dprobs, 1);
+    tc::bar_init(&bars.dscores, 8);
+    tc::bar_init(&bars.done, 1);
+    tc::bar_init(&bars.cut, 1);
+    tc::bar_init(&bars.drain, 1);
+    bars.failed = 0;
+    tc::fence_bar_init();
+    tc::prefetch_map(&maps.k);
+    tc::prefetch_map(&maps.v);
+    tc::prefetch_map(&maps.q);
+    tc::prefetch_map(&maps.dout);
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&bars.tmem, 512);
+    tc::fence_before();
+  }
   const int kh = blockIdx.x % c.key_heads, G = c.group;
   const Place at = find_tile(c.k_offsets, c.sequences, c.k_tokens, 1, kTile, blockIdx.x / c.key_heads, false);
-  if (at.s < 0) return;
+  if (at.s < 0) return leave_block(warp, &bars.tmem);
   const Span ks = own_span(c.k_offsets, c.k_lengths, at.s, c.sequences, c.k_tokens);
   const Span qs = other_span(c.q_offsets, c.q_lengths, at.s, c.k_offsets != nullptr, c.sequences, c.q_tokens);
   const int j0 = at.tile * kTile, nq = qs.valid, nk = ks.valid;
@@ -73,30 +104,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tiles = j0 < nk ? max(0, (nq + kTile - 1) / kTile - tile0) : 0;
   const int all = tiles * G;
 
-  if (warp == kMmaWarp) {
-    if (lane == 0) {
-      tc::bar_init(&bars.kv, 2);
-      for (int i = 0; i < 2; ++i) {
-        tc::bar_init(&bars.q_full[i], 1);
-        tc::bar_init(&bars.q_empty[i], 1);
-        tc::bar_init(&bars.d_full[i], 1);
-        tc::bar_init(&bars.d_empty[i], 1);
-        tc::bar_init(&bars.stat_full[i], 1);
-        tc::bar_init(&bars.stat_empty[i], 8);
-      }
-      tc::bar_init(&bars.scores, 1);
-      tc::bar_init(&bars.probs, 8);
-      tc::bar_init(&bars.dprobs, 1);
-      tc::bar_init(&bars.dscores, 8);
-      tc::bar_init(&bars.done, 1);
-      tc::bar_init(&bars.cut, 1);
-      tc::bar_init(&bars.drain, 1);
-      bars.failed = 0;
-      tc::fence_bar_init();
-    }
-    __syncwarp();
-    tc::tmem_alloc(&bars.tmem, 512);
-    tc::fence_before();
+  const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+  if (warp == kCopyWarp && lane == 0 && all > 0) {
+    copy_tile<W>(sk, &maps.k, &bars.kv, kh, k_token + j0, ks.seq);
+    copy_tile<W>(sv, &maps.v, &bars.kv, kh, k_token + j0, ks.seq);
   }
   __syncthreads();
   tc::fence_after();
@@ -105,13 +116,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp >= kCopyWarp) {
     tc::leave_registers<kOtherRegisters>();
     if (warp == kCopyWarp && all > 0) {
-      const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
       int cut_phase = 0, n = 0, parts = 0;
       bool ok = true;
-      if (lane == 0) {
-        copy_tile<W>(sk, &maps.k, &bars.kv, kh, k_token + j0, ks.seq);
-        copy_tile<W>(sv, &maps.v, &bars.kv, kh, k_token + j0, ks.seq);
-      }
       for (; n < all && ok; ++n) {
         const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile, head = kh * G + g;
         for (int side = 0; side < 2 && ok; ++side) {
@@ -380,39 +386,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
+  if (warp == kCopyWarp && lane == 0) {
+    tc::bar_init(&bars.qd, 2);
+    for (int i = 0; i < 3; ++i) {
+      tc::bar_init(&bars.k_full[i], 1);
+      tc::bar_init(&bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::bar_init(&bars.v_full[i], 1);
+      tc::bar_init(&bars.v_empty[i], 1);
+      tc::bar_init(&bars.scores[i], 1);
+      tc::bar_init(&bars.read[i], 8);
+      tc::bar_init(&bars.dprobs[i], 1);
+      tc::bar_init(&bars.dscores[i], 8);
+    }
+    tc::bar_init(&bars.done, 1);
+    tc::bar_init(&bars.cut, 1);
+    tc::bar_init(&bars.drain, 1);
+    bars.failed = 0;
+    tc::fence_bar_init();
+    tc::prefetch_map(&maps.q);
+    tc::prefetch_map(&maps.dout);
+    tc::prefetch_map(&maps.k);
+    tc::prefetch_map(&maps.v);
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&bars.tmem, 512);
+    tc::fence_before();
+  }
   const int head = blockIdx.x % c.heads, kh = head / c.group;
   const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, kTile, blockIdx.x / c.heads, c.causal);
-  if (at.s < 0) return;
+  if (at.s < 0) {
+    if (blockIdx.x == gridDim.x - 1) dependency_wait();
+    return leave_block(warp, &bars.tmem);
+  }
   const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
   const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
   const int i0 = at.tile * kTile, nq = qs.valid, nk = ks.valid;
   const int last = min(i0 + kTile, nq) - 1;
   const int all = i0 < nq ? (max(0, seen_keys(c.causal, last, nq, nk)) + kTile - 1) / kTile : 0;
 
-  if (warp == kMmaWarp) {
-    if (lane == 0) {
-      tc::bar_init(&bars.qd, 2);
-      for (int i = 0; i < 3; ++i) {
-        tc::bar_init(&bars.k_full[i], 1);
-        tc::bar_init(&bars.k_empty[i], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        tc::bar_init(&bars.v_full[i], 1);
-        tc::bar_init(&bars.v_empty[i], 1);
-        tc::bar_init(&bars.scores[i], 1);
-        tc::bar_init(&bars.read[i], 8);
-        tc::bar_init(&bars.dprobs[i], 1);
-        tc::bar_init(&bars.dscores[i], 8);
-      }
-      tc::bar_init(&bars.done, 1);
-      tc::bar_init(&bars.cut, 1);
-      tc::bar_init(&bars.drain, 1);
-      bars.failed = 0;
-      tc::fence_bar_init();
-    }
-    __syncwarp();
-    tc::tmem_alloc(&bars.tmem, 512);
-    tc::fence_before();
+  const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+  if (warp == kCopyWarp && lane == 0 && all > 0) {
+    copy_tile<W>(sq, &maps.q, &bars.qd, head, q_token + i0, qs.seq);
+    copy_tile<W>(sd, &maps.dout, &bars.qd, head, q_token + i0, qs.seq);
   }
   __syncthreads();
   tc::fence_after();
@@ -421,13 +438,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp >= kCopyWarp) {
     tc::leave_registers<kOtherRegisters>();
     if (warp == kCopyWarp && all > 0) {
-      const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
       int cut_phase = 0, ks_done = 0, vs_done = 0;
       bool ok = true;
-      if (lane == 0) {
-        copy_tile<W>(sq, &maps.q, &bars.qd, head, q_token + i0, qs.seq);
-        copy_tile<W>(sd, &maps.dout, &bars.qd, head, q_token + i0, qs.seq);
-      }
       for (int n = 0; n < all && ok; ++n) {
         if (n >= 3) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[n % 3], (n / 3 - 1) & 1, failed));
         if (!ok) break;
@@ -608,6 +620,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::fence_after();
     tc::tmem_free(tmem, 512);
   }
+  // what follows in the stream waits for this kernel only: its last block waits for the keys'
+  if (blockIdx.x == gridDim.x - 1) dependency_wait();
 }
 
 template <typename T, int DP, bool DROP>
@@ -626,7 +640,7 @@ cudaError_t backward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s
   const cudaError_t e = allow_smem(kern, queries_smem<W>());
   if (e != cudaSuccess) return e;
   const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, kTile) * c.heads;
-  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, queries_smem<W>(), false, s, c, m);
+  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, queries_smem<W>(), c.dk.p || c.dv.p, s, c, m);
 }
 
 template <typename T>

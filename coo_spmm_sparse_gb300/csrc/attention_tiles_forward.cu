@@ -34,11 +34,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int *const failed = &bars.failed;
 
+  // barriers, tensor memory and the block's place are made ready side by side
+  if (warp == kCopyWarp && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::bar_init(&bars.q[i], 1);
+      tc::bar_init(&bars.scores[i], 1);
+      tc::bar_init(&bars.probs[i][0], 4);
+      tc::bar_init(&bars.probs[i][1], 4);
+      tc::bar_init(&bars.done[i], 1);
+    }
+    for (int i = 0; i < kForwardSlots; ++i) {
+      tc::bar_init(&bars.full[i], 1);
+      tc::bar_init(&bars.empty[i], 1);
+    }
+    tc::bar_init(&bars.cut, 1);
+    tc::bar_init(&bars.drain, 1);
+    bars.failed = 0;
+    tc::fence_bar_init();
+    tc::prefetch_map(&maps.q);
+    tc::prefetch_map(&maps.k);
+    tc::prefetch_map(&maps.v);
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&bars.tmem, 512);
+    tc::fence_before();
+  }
   const bool by_heads = c.group % 2 == 0;
   const int units = by_heads ? c.heads / 2 : c.heads, u = blockIdx.x % units;
   const int rows = by_heads ? kTile : 2 * kTile;
   const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, rows, blockIdx.x / units, c.causal);
-  if (at.s < 0) return;
+  if (at.s < 0) return leave_block(warp, &bars.tmem);
   const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
   const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
   const int nq = qs.valid, nk = ks.valid;
@@ -52,27 +77,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int all = max(steps[0], steps[1]);
   const int head0 = by_heads ? 2 * u : u, kh = head0 / c.group;
 
-  if (warp == kMmaWarp) {
-    if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
-        tc::bar_init(&bars.q[i], 1);
-        tc::bar_init(&bars.scores[i], 1);
-        tc::bar_init(&bars.probs[i][0], 4);
-        tc::bar_init(&bars.probs[i][1], 4);
-        tc::bar_init(&bars.done[i], 1);
-      }
-      for (int i = 0; i < kForwardSlots; ++i) {
-        tc::bar_init(&bars.full[i], 1);
-        tc::bar_init(&bars.empty[i], 1);
-      }
-      tc::bar_init(&bars.cut, 1);
-      tc::bar_init(&bars.drain, 1);
-      bars.failed = 0;
-      tc::fence_bar_init();
-    }
-    __syncwarp();
-    tc::tmem_alloc(&bars.tmem, 512);
-    tc::fence_before();
+  const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+  if (warp == kCopyWarp && lane == 0 && all > 0) {
+    for (int t = 0; t < 2; ++t)
+      if (steps[t])
+        copy_tile<W>(sq + t * tile_bytes<W>(), &maps.q, &bars.q[t], head0 + (by_heads ? t : 0), q_token + first[t],
+                     qs.seq);
+    copy_tile<W>(ring, &maps.k, &bars.full[0], kh, k_token, ks.seq);
   }
   __syncthreads();
   tc::fence_after();
@@ -80,16 +91,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp >= kCopyWarp) {
   tc::leave_registers<kOtherRegisters>();
   if (warp == kCopyWarp) {
-    const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
     int cut_phase = 0, item = 0;
     bool ok = true;
-    if (lane == 0)
-      for (int t = 0; t < 2; ++t)
-        if (steps[t])
-          copy_tile<W>(sq + t * tile_bytes<W>(), &maps.q, &bars.q[t], head0 + (by_heads ? t : 0), q_token + first[t],
-                        qs.seq);
     for (int j = 0; j < all && ok; ++j) {
       for (int kv = 0; kv < 2 && ok; ++kv, ++item) {
+        if (item == 0) continue;  // on its way since the start
         const int slot = item % kForwardSlots;
         if (item >= kForwardSlots)
           ok = __all_sync(0xffffffffu,
