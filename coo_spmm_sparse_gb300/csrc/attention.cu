@@ -282,6 +282,8 @@ __global__ void __launch_bounds__(128) join_splits(const AttnCall c) {
 
 int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
+constexpr int64_t kTileRows = 128;  // of the tiles' kernels
+
 bool dense_or_ragged(const int32_t *offsets, const int32_t *lengths) { return !(offsets && lengths); }
 
 snack_status bad(const std::string &m) { return refuse(SNACK_ERR_INVALID_ARG, m); }
@@ -310,7 +312,10 @@ snack_status check_args(const snack_attention_args *a) {
   const auto tiles = [&](const int32_t *off, int64_t tokens, int64_t per) {
     return tiles_of(off != nullptr, a->sequences, tokens, per, 16) * a->key_heads;
   };
+  if (a->sequences > (1 << 16) && (a->q_offsets || a->k_offsets))
+    return refuse(SNACK_ERR_UNSUPPORTED, "a ragged side takes at most 2^16 sequences");  // every block looks for its own
   if (tiles(a->q_offsets, a->q_tokens, group) + tiles(a->k_offsets, a->k_tokens, 1) >= lim ||
+      tiles_of(a->q_offsets != nullptr, a->sequences, a->q_tokens, 1, kTileRows) * a->heads >= lim ||
       rows * a->heads >= lim * 8)
     return refuse(SNACK_ERR_UNSUPPORTED, "too many rows for one launch");
   const int64_t strides[] = {a->q_stride[0], a->q_stride[1], a->q_stride[2], a->k_stride[0], a->k_stride[1],
@@ -540,7 +545,7 @@ extern "C" snack_status snack_attention_forward(const snack_attention_args *a, v
   if (!out || !out_stride || !lse) return bad("out, its strides or lse is NULL");
   // the plan knows the arguments alone, so that it is the one the workspace was asked for
   const Plan p = plan_forward(c, a->type);
-  if (p.bytes && !workspace) return bad("workspace is NULL");
+  if (p.bytes && (!workspace || !aligned_to(workspace, 16))) return bad("workspace is NULL or not 16-byte aligned");
   c.out = strided(out, out_stride);
   c.lse = lse;
   char *const ws = static_cast<char *>(workspace);
@@ -571,7 +576,7 @@ extern "C" snack_status snack_attention_backward(const snack_attention_args *a, 
   if (st != SNACK_OK) return st;
   if (!g) return bad("grads is NULL");
   AttnCall c = call_of(a);
-  if (!workspace) return bad("workspace is NULL");
+  if (!workspace || !aligned_to(workspace, 16)) return bad("workspace is NULL or not 16-byte aligned");
   if (c.rows && (!g->dout || !g->out || !g->lse)) return bad("dout, out or lse is NULL");
   const Plan p = plan_backward(c, a->type);  // before dout: the plan that the workspace was asked for
   c.dout = strided(g->dout, g->dout_stride);

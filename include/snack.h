@@ -497,12 +497,19 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
  * read when the kernels run) where that is not NULL, else `seed`.
  *
  * All tensors are of `type`; lse is fp32 [heads][query tokens of all
- * sequences].  Products are summed in 32 bits.  In 16-bit types P, and in
- * the backward pass dS, are rounded to the type before the second product (as
- * tensor instructions take both operands in one type).  Within a sequence an
- * infinite or NaN element of k or v may reach queries that do not see it.
- * Limits: 1 <= head_size <= 128, heads <= 65536; tokens, and q_tokens *
- * (heads / key_heads), below 2^31 - 4096.
+ * sequences].  Products are summed in 32 bits.  In 16-bit types P is rounded to
+ * the type before the second product, as tensor instructions take both
+ * operands in one type.  32-bit calls of some size (head_size up to 64, see
+ * attention.cu) take each operand as two float16 parts of the tensor times a
+ * power of two: 22 bits of what lies above 2^-17 of the tensor's largest
+ * element, and nothing more than 2^-39 of that off.  Gradients of scores and
+ * probabilities are split, or in 16-bit types rounded to float16, the same
+ * way: a term dS[i][j] is never more than 2^-38 of
+ * 2 * head_size * max|dout| * max|v| / (1 - dropout) off by that.  An infinite
+ * or NaN element inside a sequence may reach results that do not depend on it.
+ * Limits: 1 <= head_size <= 128, heads <= 65536, ragged sides of at most 65536
+ * sequences; tokens, and q_tokens * (heads / key_heads), below 2^31 - 4096.
+ * Workspaces are 16-byte aligned and hold nothing from one call to the next.
  */
 typedef struct {
   int64_t sequences, q_tokens, k_tokens;

@@ -51,6 +51,8 @@ def forward(a):
     (dict(k_stride=(i64 * 3)(-1, 1, 1)), INVALID), (dict(v_stride=(i64 * 3)(1, 1, -1)), INVALID),
     (dict(q_tokens=2 ** 31), UNSUPPORTED), (dict(k_tokens=2 ** 31), UNSUPPORTED),
     (dict(q_tokens=2 ** 30, heads=4), UNSUPPORTED), (dict(sequences=2 ** 25), UNSUPPORTED),
+    (dict(sequences=2 ** 16 + 1, q_offsets=FAKE), UNSUPPORTED), (dict(sequences=2 ** 16 + 1, k_offsets=FAKE), UNSUPPORTED),
+    (dict(sequences=2 ** 16, q_offsets=FAKE, heads=2 ** 16, key_heads=1), UNSUPPORTED),
     (dict(heads=2 ** 17, key_heads=2), UNSUPPORTED), (dict(sequences=2 ** 20, q_tokens=2 ** 20), UNSUPPORTED),
     (dict(sequences=2 ** 12, q_tokens=2 ** 20, dropout=0.1), UNSUPPORTED),
 ])
@@ -75,6 +77,7 @@ def test_attention_needs_its_results():
     full = dict(dout=FAKE, out=FAKE, lse=FAKE)
     assert back(ctypes.byref(a), None, FAKE, None) == INVALID
     assert back(ctypes.byref(a), ctypes.byref(Grads(**full)), None, None) == INVALID
+    assert back(ctypes.byref(a), ctypes.byref(Grads(**full)), FAKE + 8, None) == INVALID
     for missing in full:
         assert back(ctypes.byref(a), ctypes.byref(Grads(**{**full, missing: None})), FAKE, None) == INVALID
 
