@@ -361,7 +361,7 @@ AttnCall call_of(const snack_attention_args *a) {
 struct Plan {
   bool tiles = false, few = false;  // on tcgen05; in blocks of 16 rows
   int splits = 1, chunk = 0, width = 0;  // width: columns of operands made in float16; 0: none are
-  size_t delta = 0, parts[4] = {}, bytes = 0;  // offsets: after the peaks; q, k, v, dout
+  size_t delta = 0, part = 0, parts[4] = {}, bytes = 0;  // offsets; parts: of q, k, v, dout
 };
 constexpr size_t kPeaks = 256;
 
@@ -390,39 +390,46 @@ void plan_parts(Plan *p, const AttnCall &c, int width, bool backward) {
 // (3e6) 11, 17; 1 x 1024 x 1024 (1.3e7) 19, 41; backward 35, 23; 37, 45; 50, 92.
 // fp32, where the operands are made first: forward 4 x 256 x 256 28, 29; 8 x 256
 // x 256 (6e6) 32, 55; backward, 8 x 256 x 256, 66, 132.
-// Few rows over many keys leave the forward tiles alone with their keys, which
-// blocks of 16 rows share out: 1 x 64 x 4096 45, 19; 1 x 128 x 8192 66, 52.
+// Few rows over many keys are too few for the forward tiles even with the keys
+// in parts.
 bool worth_tiles(const AttnCall &c, int type, bool backward) {
   if (c.q_tokens < 64 || c.k_tokens < 64) return false;
   const double rows = (double)c.rows * c.heads, x = rows * c.k_tokens;
-  return x >= (type == SNACK_F32 && !backward ? 4e6 : 2e6) && (backward || rows >= 2048);
+  return x >= (type == SNACK_F32 && !backward ? 4e6 : 2e6) && (backward || rows >= 1024);
 }
 
-// Few rows (16 to a block) where blocks of 128 would leave SMs idle, and the
-// keys in parts where even those do.
+// Off the tiles, few rows (16 to a block) where blocks of 128 would leave SMs
+// idle; and the keys in parts where the blocks still do.
 Plan plan_forward(const AttnCall &c, int type) {
   Plan p;
+  const int64_t sms = device_sms();
   p.tiles = worth_tiles(c, type, false) && tiles_take(c, type);
+  int64_t blocks, least, want;  // least keys of a part: below that it starts and ends more than it reads
   if (p.tiles) {
     p.width = part_width(c, type, false);
     if (p.width) {
       p.bytes = kPeaks;
       plan_parts(&p, c, p.width, false);
     }
-    return p;
+    blocks = tile_forward_blocks(c);
+    least = 1024;
+    want = blocks ? sms / blocks : 1;
+  } else {
+    const bool ragged = c.q_offsets != nullptr;
+    p.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
+    if (!p.few) return p;
+    blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
+    least = 512;
+    want = blocks ? 16 * sms / blocks : 1;
   }
-  const bool ragged = c.q_offsets != nullptr;
-  const int64_t sms = device_sms();
-  p.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
-  if (!p.few) return p;
-  const int64_t blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
-  // chunks of 512 keys at least: below that a block starts and ends more than it reads
-  const int64_t want = blocks ? 16 * sms / blocks : 1, most = c.k_tokens / 512;
-  const int64_t splits = std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)kMostSplits));
-  if (splits == 1) return p;
-  p.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 64);
+  const int64_t splits = std::min(std::min(want, c.k_tokens / least), (int64_t)kMostSplits);
+  if (splits <= 1) return p;
+  p.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 128);
   p.splits = (int)((c.k_tokens + p.chunk - 1) / p.chunk);
-  if (p.splits > 1) p.bytes = (size_t)p.splits * c.rows * c.heads * (c.d + 1) * sizeof(float);
+  if (p.splits > 1) {
+    p.part = p.bytes;
+    p.bytes += (size_t)p.splits * c.rows * c.heads * (c.d + 1) * sizeof(float);
+  }
   return p;
 }
 
@@ -479,20 +486,21 @@ cudaError_t clear_peaks(AttnCall *c, char *workspace, cudaStream_t s) {
 
 template <typename T>
 cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
+  if (!p.tiles && !p.few) return rows_forward_launch<T>(c, s);
+  c.splits = p.splits;
+  c.chunk = p.chunk;
+  c.part = reinterpret_cast<float *>(workspace + p.part);
+  cudaError_t e = cudaSuccess;
   if (p.tiles) {
     SplitParts parts = {};
     if (p.width) {
-      cudaError_t e = clear_peaks(&c, workspace, s);
+      e = clear_peaks(&c, workspace, s);
       if (e == cudaSuccess) e = make_parts<T>(&c, p, false, workspace, &parts, s);
-      if (e != cudaSuccess) return e;
     }
-    return tile_forward_launch(c, type, parts, s);
+    if (e == cudaSuccess) e = tile_forward_launch(c, type, parts, s);
+  } else {
+    e = few_forward_launch(c, type, s);
   }
-  if (!p.few) return rows_forward_launch<T>(c, s);
-  c.splits = p.splits;
-  c.chunk = p.chunk;
-  c.part = reinterpret_cast<float *>(workspace);
-  cudaError_t e = few_forward_launch(c, type, s);
   if (e == cudaSuccess && c.splits > 1)
     e = launch_kernel(join_splits<T>, dim3((unsigned)(c.rows * c.heads)), 128, 0, true, s, c);
   return e;

@@ -147,6 +147,7 @@ struct SplitParts {
 // float16 first), and whether one of their bounded waits has run out since the last question.
 bool tiles_take(const AttnCall &c, int type);
 bool tiles_read(const AttnCall &c);  // as the tensors lie
+int64_t tile_forward_blocks(const AttnCall &c);
 cudaError_t tile_forward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s);
 cudaError_t tile_forward_failed(int *flag, cudaStream_t s);
 cudaError_t tile_backward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s);

@@ -13,16 +13,17 @@
 namespace snack {
 namespace {
 
-// Four warps, three tiles each; sixteen warps with one tile each where there are
+// Four warps, three tiles each (two in 32 bits: two blocks to an SM); sixteen warps with one tile each where there are
 // few blocks, so that short caches take one step.
 template <typename T, int DP, int W>
 struct Few {
   static constexpr int kKeys = sizeof(T) == 4 && DP > 64 ? 8 : 16;  // of a warp's tile
-  static constexpr int kStages = W == 4 ? 3 : 1, kStep = W * kKeys, kLd = DP + 8;
+  static constexpr int kStages = W != 4 ? 1 : sizeof(T) == 4 ? 2 : 3, kStep = W * kKeys, kLd = DP + 8;
   static constexpr int kTileElems = 2 * kKeys * kLd;
   static constexpr size_t ring = (size_t)W * kStages * kTileElems * sizeof(T);
   static constexpr size_t room = (size_t)W * 16 * kLd * sizeof(float);
-  static constexpr size_t smem = 16 * kLd * sizeof(T) + (ring > room ? ring : room);
+  static constexpr int kQueries = (sizeof(T) == 4 ? 2 : 1) * 16 * kLd;  // 32 bits: high and low parts
+  static constexpr size_t smem = kQueries * sizeof(T) + (ring > room ? ring : room);
 };
 
 template <typename T, int DP, int W>
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
   int end = r0 / G < nq ? max(0, seen_keys(c.causal, last, nq, nk)) : 0;
   if (c.splits > 1) end = min(end, begin + c.chunk);
 
-  T *const ring = sq + 16 * kLd + warp * kStages * F::kTileElems;
+  T *const ring = sq + F::kQueries + warp * kStages * F::kTileElems;
   const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
   const bool vec = kr.vec && vr.vec;
   const int first = begin + warp * kKeys;
@@ -70,10 +71,19 @@ __global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
       }
     } else {
       for (int r = 0; r < kKeys; ++r)
+#pragma unroll
         for (int col = lane; col < DP; col += 32) {
           const bool have = key0 + r < end && col < c.d;
-          k[r * kLd + col] = have ? kr.row(key0 + r)[col] : from_float<T>(0.f);
-          k[(kKeys + r) * kLd + col] = have ? vr.row(key0 + r)[col] : from_float<T>(0.f);
+          const int64_t row = have ? key0 + r : 0;
+          const T *const fk = have ? kr.base + row * kr.token + col : kr.base;
+          const T *const fv = have ? vr.base + row * vr.token + col : vr.base;
+          if constexpr (sizeof(T) == 4) {
+            copy_async4(k + r * kLd + col, fk, have ? 4 : 0);
+            copy_async4(k + (kKeys + r) * kLd + col, fv, have ? 4 : 0);
+          } else {
+            k[r * kLd + col] = have ? *fk : from_float<T>(0.f);
+            k[(kKeys + r) * kLd + col] = have ? *fv : from_float<T>(0.f);
+          }
         }
     }
   };
@@ -106,6 +116,15 @@ __global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[DP / 8][4] = {};
   copies_wait<kAhead>();
   __syncthreads();
+  constexpr bool kParts = sizeof(T) == 4;
+  if constexpr (kParts) {  // the queries' parts are made once, not for every tile of keys
+    for (int i = threadIdx.x; i < 16 * kLd; i += 32 * W) {
+      const float x = sq[i], hi = tf32_part(x);
+      sq[i] = hi;
+      sq[16 * kLd + i] = tf32_part(x - hi);
+    }
+    __syncthreads();
+  }
   for (int step = 0; step < steps; ++step) {
     const int key = first + step * F::kStep;
     if (kStages > 1) {
@@ -116,7 +135,10 @@ __global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
     __syncwarp();
     const T *const k = ring + step % kStages * F::kTileElems, *const v = k + kKeys * kLd;
     float s[NB][4] = {};
-    Ops::template rows_by_rows<NB>(s, sq, k, lane);
+    if constexpr (kParts)
+      Ops::template rows_by_rows<NB, true>(s, sq, k, lane, 16 * kLd);
+    else
+      Ops::template rows_by_rows<NB>(s, sq, k, lane);
     float shrink[2] = {1.f, 1.f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -185,7 +207,7 @@ __global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
     }
   }
   __syncthreads();  // (and the tiles are read: their memory takes the warps' sums)
-  float *const room = reinterpret_cast<float *>(sq + 16 * kLd);
+  float *const room = reinterpret_cast<float *>(sq + F::kQueries);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (row + 8 * h >= rows) continue;

@@ -127,32 +127,43 @@ struct Tile<float, DP> {
     return nb * 8 + turned(2 * (lane & 3) + e);
   }
 
-  template <int NB>
-  static __device__ __forceinline__ void rows_by_rows(float (&acc)[NB][4], const float *a, const float *b,
-                                                      int lane) {
+  // The small products have sums of their own: those of the large ones are cut
+  // off a third as often, and where few blocks of sums would wait for one
+  // another (NB <= 2) each product goes its own way.  SPLIT: rows a have their
+  // high parts there and their low ones `low` elements further on.
+  template <int NB, bool SPLIT = false>
+  static __device__ __forceinline__ void rows_by_rows(float (&acc)[NB][4], const float *a, const float *b, int lane,
+                                                      int low = 0) {
     const int g = lane >> 2, t = lane & 3;
     const float *pa = a + g * kLd + 2 * t;
     const float *pb = b + turned(g) * kLd + 2 * t;
-    // where few blocks of sums would wait for one another, each product has its own
-    constexpr bool kApart = NB <= 2;
-    float cross[kApart ? NB : 1][2][4] = {};
+    constexpr int kOwn = NB <= 2 ? 2 : 1;
+    constexpr bool kApart = NB <= 4;
+    float cross[kApart ? NB : 1][kOwn][4] = {};
 #pragma unroll 4
     for (int k = 0; k < DP; k += 8) {
+      float hi[4], lo[4];
       const float2 a0 = *reinterpret_cast<const float2 *>(pa + k);
       const float2 a1 = *reinterpret_cast<const float2 *>(pa + 8 * kLd + k);
-      const float x[4] = {a0.x, a1.x, a0.y, a1.y};
-      float hi[4], lo[4];
+      if (SPLIT) {
+        const float2 l0 = *reinterpret_cast<const float2 *>(pa + low + k);
+        const float2 l1 = *reinterpret_cast<const float2 *>(pa + low + 8 * kLd + k);
+        hi[0] = a0.x, hi[1] = a1.x, hi[2] = a0.y, hi[3] = a1.y;
+        lo[0] = l0.x, lo[1] = l1.x, lo[2] = l0.y, lo[3] = l1.y;
+      } else {
+        const float x[4] = {a0.x, a1.x, a0.y, a1.y};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        hi[i] = tf32_part(x[i]);
-        lo[i] = tf32_part(x[i] - hi[i]);
+        for (int i = 0; i < 4; ++i) {
+          hi[i] = tf32_part(x[i]);
+          lo[i] = tf32_part(x[i] - hi[i]);
+        }
       }
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         const float2 y = *reinterpret_cast<const float2 *>(pb + n * 8 * kLd + k);
         const float h0 = tf32_part(y.x), h1 = tf32_part(y.y);
         mma_k8(kApart ? cross[n][0] : acc[n], lo, h0, h1);
-        mma_k8(kApart ? cross[n][1] : acc[n], hi, tf32_part(y.x - h0), tf32_part(y.y - h1));
+        mma_k8(kApart ? cross[n][kOwn - 1] : acc[n], hi, tf32_part(y.x - h0), tf32_part(y.y - h1));
         mma_k8(acc[n], hi, h0, h1);
       }
     }
@@ -160,7 +171,7 @@ struct Tile<float, DP> {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] += cross[n][0][i] + cross[n][1][i];
+        for (int i = 0; i < 4; ++i) acc[n][i] += kOwn == 2 ? cross[n][0][i] + cross[n][kOwn - 1][i] : cross[n][0][i];
   }
 
   template <int NB>
@@ -219,6 +230,13 @@ struct Rows {
   }
 };
 
+// Four bytes; `bytes` 0: zeros.
+__device__ __forceinline__ void copy_async4(void *slot, const void *from, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(slot)),
+               "l"(from), "r"(bytes)
+               : "memory");
+}
+
 // Copies `count` rows from r0 on into a tile; rows at or beyond `end` and
 // columns beyond the head size become zeros.  Every thread of the block takes
 // part; the copies are complete after a commit, a wait and a barrier.
@@ -236,6 +254,9 @@ __device__ __forceinline__ void copy_rows(T *tile, const Rows<T> &src, int r0, i
     const T *from = src.row(r0 + r) + col;
     if (src.vec) {
       copy_async16(to, from, have * (int)sizeof(T));
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) copy_async4(to + e, e < have ? from + e : from, e < have ? 4 : 0);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) to[e] = e < have ? from[e] : from_float<T>(0.f);
@@ -689,7 +710,7 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
 // The first `key_blocks` blocks take keys, the others queries.  ONLY: the
 // kernel has code for one of them (1: keys, 2: queries) and that one's registers.
 template <typename T, int DP, int WM, int WN, int BN, int ST, int ONLY>
-__global__ void __launch_bounds__(32 * WM * WN) rows_backward(const AttnCall c, int key_blocks) {
+__global__ void __launch_bounds__(32 * WM * WN, DP == 64 && ONLY == 2 ? 2 : 1) rows_backward(const AttnCall c, int key_blocks) {
   if (ONLY == 1 || (ONLY == 0 && (int)blockIdx.x < key_blocks))
     keys_of_rows<T, DP, WM, WN, BN, ST>(c, blockIdx.x);
   else

@@ -68,16 +68,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
   const int nq = qs.valid, nk = ks.valid;
   int first[2], steps[2];
+  const int begin = c.splits > 1 ? (int)blockIdx.y * (c.chunk / kTile) : 0;  // the first tile of keys
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     first[t] = at.tile * rows + (by_heads ? 0 : t * kTile);
     const int last = min(first[t] + kTile, nq) - 1;
-    steps[t] = first[t] < nq ? (max(0, seen_keys(c.causal, last, nq, nk)) + kTile - 1) / kTile : 0;
+    int end = first[t] < nq ? (max(0, seen_keys(c.causal, last, nq, nk)) + kTile - 1) / kTile : 0;
+    if (c.splits > 1) end = min(end, begin + c.chunk / kTile);
+    steps[t] = max(0, end - begin);
   }
   const int all = max(steps[0], steps[1]);
   const int head0 = by_heads ? 2 * u : u, kh = head0 / c.group;
 
-  const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
+  const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = (c.k_offsets ? (int)ks.row : 0) + begin * kTile;
   if (warp == kCopyWarp && lane == 0 && all > 0) {
     for (int t = 0; t < 2; ++t)
       if (steps[t])
@@ -103,9 +106,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok) break;
         unsigned char *const to = ring + slot * tile_bytes<W>();
         const int token = k_token + j * kTile;
-        if (kv && (j + 1) * kTile > nk)
-          ok = copy_tile_cut<W>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq,
-                                 nk - j * kTile, failed);
+        const int left = nk - (begin + j) * kTile;
+        if (kv && left < kTile)
+          ok = copy_tile_cut<W>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq, left, failed);
         else if (lane == 0)
           copy_tile<W>(to, kv ? &maps.v : &maps.k, &bars.full[slot], kh, token, ks.seq);
         __syncwarp();
@@ -179,7 +182,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int i = first[t] + (warp & 3) * 32 + lane;  // token of this thread's row
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
-    const int lim = i < nq ? max(0, seen_keys(c.causal, i, nq, nk)) : 0;
+    // keys that the row sees from the block's first on; a block with a part of the keys leaves a part
+    const int lim = i < nq ? max(0, seen_keys(c.causal, i, nq, nk) - begin * kTile) : 0;
+    const int64_t slot = (blockIdx.y * c.rows + qs.row + i) * c.heads + head;
+    float *const part_lse = c.part + (int64_t)c.splits * c.rows * c.heads * c.d + slot;
     const Scales by = scales_of(c);
     const float cs = by.scores;
     uint64_t draw = 0;
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (DROP)
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
-              const uint64_t z = dropout_draw(draw, j * kTile + x + e);
+              const uint64_t z = dropout_draw(draw, (begin + j) * kTile + x + e);
 #pragma unroll
               for (int y = 0; y < 4; ++y) s[e + y] = draw_lane(z, y) >= c.drop ? s[e + y] : 0.f;
             }
@@ -255,11 +261,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (ok) add_sums<DP>(o, o_at);
       }
       if (ok && i < qs.cover) {
-        float *const row = static_cast<float *>(c.out.p) +
-                           (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) +
-                           head * c.out.head;
+        float *const row = c.splits > 1 ? c.part + slot * c.d
+                                        : static_cast<float *>(c.out.p) + head * c.out.head +
+                                              (c.q_offsets ? (qs.row + i) * c.out.token
+                                                           : qs.seq * c.out.seq + i * c.out.token);
         store_floats<DP>(row, o, c.keep_scale / sum * by.v, c.d, sum == 0.f);
-        c.lse[(int64_t)head * c.rows + qs.row + i] =
+        *(c.splits > 1 ? part_lse : c.lse + (int64_t)head * c.rows + qs.row + i) =
             sum == 0.f ? -INFINITY : m * cs * kLn2 + (logf(sum) - kHalfP * kLn2);
       }
     } else {
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (DROP) {
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
-            const uint64_t z = dropout_draw(draw, j * kTile + x + e);
+            const uint64_t z = dropout_draw(draw, (begin + j) * kTile + x + e);
             float k[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) k[y] = draw_lane(z, y) >= c.drop ? s[x + e + y] : 0.f;
@@ -343,13 +350,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (ok) {
       const bool mine = i < qs.cover;
-      T *row = nullptr;
+      const float factor = c.keep_scale / sum * by.v;
+      if (c.splits > 1) {
+#pragma unroll
+        for (int x = 0; x < DP; x += 32) {
+          float v[32];
+          if (steps[t] > 0) {
+            tc::load32(o_at + x, v);
+            tc::wait_loads();
+          }
+          store_floats<32>(mine ? c.part + slot * c.d + x : nullptr, v, factor, c.d - x, sum == 0.f);
+          __syncwarp();
+        }
+      } else {
+        T *row = nullptr;
+        if (mine)
+          row = static_cast<T *>(c.out.p) +
+                (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) + head * c.out.head;
+        store_sums<T, DP>(o_at, row, factor, c.d, steps[t] > 0, sum == 0.f);
+      }
       if (mine)
-        row = static_cast<T *>(c.out.p) + (c.q_offsets ? (qs.row + i) * c.out.token : qs.seq * c.out.seq + i * c.out.token) +
-              head * c.out.head;
-      store_sums<T, DP>(o_at, row, c.keep_scale / sum * by.v, c.d, steps[t] > 0, sum == 0.f);
-      if (mine)
-        c.lse[(int64_t)head * c.rows + qs.row + i] = sum == 0.f ? -INFINITY : m * cs * kLn2 + logf(sum);
+        *(c.splits > 1 ? part_lse : c.lse + (int64_t)head * c.rows + qs.row + i) =
+            sum == 0.f ? -INFINITY : m * cs * kLn2 + logf(sum);
     }
     }
     tc::fence_before();
@@ -374,16 +396,19 @@ bool tiles_read(const AttnCall &c) {
          even(c.v, c.key_heads, c.k_tokens, kn) && (!c.dout.p || even(c.dout, c.heads, c.q_tokens, qn));
 }
 
+int64_t tile_forward_blocks(const AttnCall &c) {
+  const bool by_heads = c.group % 2 == 0;
+  return tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, by_heads ? kTile : 2 * kTile) *
+         (by_heads ? c.heads / 2 : c.heads);
+}
+
 template <typename T, int DP, bool DROP, typename Op>
 static cudaError_t forward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
-  const bool by_heads = c.group % 2 == 0;
-  const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, by_heads ? kTile : 2 * kTile) *
-                         (by_heads ? c.heads / 2 : c.heads);
   const auto kern = tile_forward<T, DP, DROP, Op>;
   constexpr size_t smem = tile_forward_smem<wide<T, DP>()>();
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, smem, false, s, c, m);
+  return launch_kernel(kern, dim3((unsigned)tile_forward_blocks(c), (unsigned)c.splits), kTileThreads, smem, false, s, c, m);
 }
 
 template <typename T, typename Op>

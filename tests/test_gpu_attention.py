@@ -93,6 +93,20 @@ def test_tensors_that_cannot_be_copied_as_they_lie(dtype, d, dropout):
     check(q, k, v, dout.contiguous(), causal=False, k_lengths=ints(777, 300))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,q,k,d", [(1, 130, 9000, 64), (2, 200, 6001, 128), (1, 300, 2100, 80), (3, 64, 20000, 64)])
+def test_many_queries_over_keys_in_parts(dtype, n, q, k, d):
+    g = gen(k)
+    fill = torch.randint(q - 10, k + 1, (n,), generator=g, device="cuda").to(torch.int32)
+    args = [rnd(g, (n, q, 8, d), dtype), rnd(g, (n, k, 2, d), dtype), rnd(g, (n, k, 2, d), dtype)]
+    for t in args[1:]:
+        for i in range(n):
+            t[i, fill[i]:] = float("nan")
+    check(*args, None, k_lengths=fill)
+    check(*args, None, k_lengths=fill, causal=False, dropout=0.3, seed=11)
+    check(*args, rnd(g, (n, q, 8, d), dtype), k_lengths=fill)
+
+
 def test_operands_of_every_magnitude():
     """Tensors far from one another and from 1, channels and tokens far from their tensor's largest."""
     for dtype in (F32, BF16):
