@@ -203,9 +203,13 @@ def read_peak():
 
 # Sources of the operators on dense activations: none of the sparse layer's
 # code is compiled from them.
-DENSE_SOURCES = ("adapter.cu", "dense_ops.cu", "dense_ops.cuh", "grad_clip.cu", "norm_team.cuh",
+DENSE_SOURCES = ("adapter.cu", "attention.cu", "attention.cuh", "attention_few.cu",
+                 "attention_rows.cuh", "attention_rows_bf16.cu", "attention_rows_f16.cu",
+                 "attention_rows_f32.cu", "attention_rows_launch.cuh", "attention_tiles.cuh",
+                 "attention_tiles_backward.cu", "attention_tiles_forward.cu", "counter_random.cuh",
+                 "dense_ops.cu", "dense_ops.cuh", "dropout.cu", "grad_clip.cu", "norm_team.cuh",
                  "norm_team_backward.cu", "norm_team_forward.cu", "residual_norm.cu",
-                 "residual_norm.cuh")
+                 "residual_norm.cuh", "tcgen05.cuh")
 
 
 def kernel_source_sha(csrc: str | None = None) -> str:

@@ -307,6 +307,9 @@ snack_status check_args(const snack_attention_args *a) {
   if (a->k_tokens >= lim - 4096 || a->q_tokens >= lim || a->q_tokens * group >= lim - 4096)
     return refuse(SNACK_ERR_UNSUPPORTED, "tokens, and query tokens * group, must be below 2^31 - 4096");
   const int64_t rows = a->q_offsets ? a->q_tokens : a->sequences * a->q_tokens;
+  const int64_t keys = a->k_offsets ? a->k_tokens : a->sequences * a->k_tokens;
+  if (rows >= (int64_t)1 << 40 || keys >= (int64_t)1 << 40)
+    return refuse(SNACK_ERR_UNSUPPORTED, "more than 2^40 tokens");
   if (a->dropout > 0.f && rows * a->heads >= (int64_t)1 << 34)
     return refuse(SNACK_ERR_UNSUPPORTED, "dropout takes fewer than 2^34 query rows (tokens * heads)");
   const auto tiles = [&](const int32_t *off, int64_t tokens, int64_t per) {
@@ -322,7 +325,6 @@ snack_status check_args(const snack_attention_args *a) {
                              a->k_stride[2], a->v_stride[0], a->v_stride[1], a->v_stride[2]};
   for (int64_t s : strides)
     if (s < 0) return bad("negative strides");
-  const int64_t keys = a->k_offsets ? a->k_tokens : a->sequences * a->k_tokens;
   if ((rows && !a->q) || (keys && (!a->k || !a->v))) return bad("q, k or v is NULL");
   return SNACK_OK;
 }

@@ -55,6 +55,8 @@ def forward(a):
     (dict(sequences=2 ** 16, q_offsets=FAKE, heads=2 ** 16, key_heads=1), UNSUPPORTED),
     (dict(heads=2 ** 17, key_heads=2), UNSUPPORTED), (dict(sequences=2 ** 20, q_tokens=2 ** 20), UNSUPPORTED),
     (dict(sequences=2 ** 12, q_tokens=2 ** 20, dropout=0.1), UNSUPPORTED),
+    (dict(sequences=2 ** 24, q_tokens=2 ** 31 - 8192, heads=2 ** 16, key_heads=2 ** 16), UNSUPPORTED),
+    (dict(sequences=2 ** 24, k_tokens=2 ** 31 - 8192, heads=2 ** 16, key_heads=2 ** 16), UNSUPPORTED),
 ])
 def test_attention_refuses(change, status):
     a = args(**change)

@@ -502,3 +502,39 @@ def test_refusals():
         with pytest.raises(err):
             b(*args, **opts)
     assert out.sum() == 0
+
+
+@pytest.mark.slow
+def test_caches_of_more_than_2_31_elements():
+    """The last sequence of such a cache against the same keys in a tensor of their own (two
+    ways to cut the keys: each within the other's bound), forward in every form, and backward."""
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(17)
+    n, room, heads, d = 4, 70001, 64, 128
+    k, v = (torch.empty(n, room, heads, d, device="cuda", dtype=BF16) for _ in range(2))
+    assert k.numel() > 2 ** 31
+    for i in range(n):
+        k[i].normal_(generator=g)
+        v[i].normal_(generator=g)
+    for q_tokens in (1, 40, 256):
+        q = rnd(g, (n, q_tokens, heads, d), BF16)
+        fill = ints(5, 70001, 1000, 69990)
+        out, lse = sn.snack_attention_forward(q, k, v, k_lengths=fill)
+        for i in (1, 3):
+            m = int(fill[i])
+            alone, log = sn.snack_attention_forward(q[i: i + 1], k[i: i + 1, :m].clone(), v[i: i + 1, :m].clone())
+            # 70000 keys of one size: a result is about 1/260, a probability off by 2^-8 of itself
+            assert float((out[i].double() - alone[0].double()).abs().max()) <= 2.0 ** -8 * float(alone.abs().max()) + 1e-4
+            assert torch.allclose(lse[:, i], log[:, 0], atol=1e-4)
+    rows = slice(69000, 69200)
+    ks, vs = (t[:, rows].expand(n, 200, heads, d) for t in (k, v))
+    q, dout = (rnd(g, (n, 200, heads, d), BF16) for _ in range(2))
+    out, lse = sn.snack_attention_forward(q, ks, vs)
+    got = sn.snack_attention_backward(dout, q, ks, vs, out, lse)
+    want = sn.snack_attention_backward(dout, q, ks.contiguous(), vs.contiguous(), out, lse)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_no_wait_has_run_out():
+    import coo_spmm_sparse_gb300 as sn
+    assert not sn.snack_attention_error() and not sn.snack_attention_error(torch.cuda.Stream())
