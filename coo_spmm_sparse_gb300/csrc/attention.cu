@@ -109,8 +109,95 @@ __global__ void __launch_bounds__(256) attention_delta(const AttnCall c, uint32_
   if (peak) block_peak(top, peak);
 }
 
+// 16 bytes of elements from v on, of which `left` are there.
+template <typename T>
+__device__ __forceinline__ uint4 load_vector(const T *v, int left) {
+  constexpr int E = 16 / sizeof(T);
+  if (left >= E && (reinterpret_cast<uintptr_t>(v) & 15) == 0) return *reinterpret_cast<const uint4 *>(v);
+  uint4 u = make_uint4(0, 0, 0, 0);
+  T x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = e < left ? v[e] : from_float<T>(0.f);
+  memcpy(&u, x, 16);
+  return u;
+}
+
+// delta of 16-bit calls with at most 64 keys: sum_j M P (dout . v_j), from the
+// tensors themselves.  out is rounded, and over a handful of keys what that does
+// to delta made dq and dk twice as far off as the rounding of the results alone;
+// over more it is lost among them.  A warp takes a row and head, a lane a key.
+constexpr int kFewKeys = 64;
+template <typename T>
+__global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c, uint32_t *peak) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), row = item / c.heads;
+  const int head = (int)(item - row * c.heads), kh = head / c.group;
+  float top = 0.f;
+  int seq = 0, token = 0;
+  if (row < c.rows && in_sequence(c.q_offsets, c.q_lengths, c.sequences, c.q_tokens, row, &seq, &token)) {
+    const T *const q = static_cast<const T *>(c.q.p) + seq * c.q.seq + token * c.q.token + head * c.q.head;
+    const T *const d = static_cast<const T *>(c.dout.p) + seq * c.dout.seq + token * c.dout.token + head * c.dout.head;
+    int s = seq;
+    if (c.q_offsets) {  // the last sequence that begins at or before the row
+      int lo = 0, hi = c.sequences;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (clamped(c.q_offsets, mid, c.q_tokens) <= row) lo = mid; else hi = mid;
+      }
+      s = lo;
+    }
+    const Span qs = own_span(c.q_offsets, c.q_lengths, c.q_offsets ? s + 1 : s, c.sequences, c.q_tokens);
+    const Span ks = own_span(c.k_offsets, c.k_lengths, c.k_offsets ? s + 1 : s, c.sequences, c.k_tokens);
+    const int i = c.q_offsets ? (int)(row - qs.row) : token;
+    const int64_t place = (int64_t)head * c.rows + row;
+    const int seen = min(kFewKeys, seen_keys(c.causal, i, qs.valid, ks.valid));
+    float term = 0.f;
+    constexpr int E = 16 / sizeof(T);
+    for (int col = lane * E; col < c.d; col += 32 * E) {
+      float g[E];
+      unpack16<T>(load_vector(d + col, c.d - col), g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) top = larger(top, g[e]);
+    }
+    for (int j = lane; j < seen; j += 32) {
+      const int64_t at = c.k_offsets ? ks.row + j : j;
+      const T *const k = static_cast<const T *>(c.k.p) + ks.seq * c.k.seq + at * c.k.token + kh * c.k.head;
+      const T *const v = static_cast<const T *>(c.v.p) + ks.seq * c.v.seq + at * c.v.token + kh * c.v.head;
+      float score = 0.f, dprob = 0.f;
+#pragma unroll 2
+      for (int col = 0; col < c.d; col += E) {
+        float x[4][E];
+        unpack16<T>(load_vector(q + col, c.d - col), x[0]);
+        unpack16<T>(load_vector(k + col, c.d - col), x[1]);
+        unpack16<T>(load_vector(d + col, c.d - col), x[2]);
+        unpack16<T>(load_vector(v + col, c.d - col), x[3]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          score = fmaf(x[0][e], x[1][e], score);
+          dprob = fmaf(x[2][e], x[3][e], dprob);
+        }
+      }
+      float p = expf(score * c.scale - c.lse[place]) * dprob;
+      if (c.drop) {
+        const uint64_t z = dropout_draw(dropout_row(c.draws(), row, c.heads, head), j);
+        p = draw_lane(z, j & 3) >= c.drop ? p * c.keep_scale : 0.f;
+      }
+      term += p;
+    }
+    const float delta = warp_sum(term);
+    if (lane == 0) c.delta[place] = delta;
+  }
+  if (peak) block_peak(top, peak);
+}
+
 template <typename T>
 cudaError_t delta_launch(const AttnCall &c, bool vec, uint32_t *peak, cudaStream_t s) {
+  // (a warp's lanes read 32 rows of k and v side by side, 8 * d places of the L1 for 32 keys: about
+  // 10 us at this limit, where the plain form takes 4)
+  if (sizeof(T) == 2 && c.k_tokens <= kFewKeys &&
+      (double)c.rows * c.heads * ((c.k_tokens + 31) / 32) * c.d <= 360000.0)
+    return launch_kernel(attention_delta_few_keys<T>, dim3((unsigned)((c.rows * c.heads + 7) / 8)), 256, 0, false, s, c,
+                         peak);
   const int lanes = vec ? (c.d * (int)sizeof(T) + 15) / 16 : 32;
   const int team = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const int64_t each = 256 / team * kItems;
@@ -142,19 +229,6 @@ __device__ __forceinline__ bool token_of(const Source &t, int sequences, int64_t
   const bool have = in_sequence(t.offsets, t.lengths, sequences, t.tokens, row, &seq, &token);
   *at = seq * t.from.seq + token * t.from.token;
   return have;
-}
-
-// 16 bytes of elements from v on, of which `left` are there.
-template <typename T>
-__device__ __forceinline__ uint4 load_vector(const T *v, int left) {
-  constexpr int E = 16 / sizeof(T);
-  if (left >= E && (reinterpret_cast<uintptr_t>(v) & 15) == 0) return *reinterpret_cast<const uint4 *>(v);
-  uint4 u = make_uint4(0, 0, 0, 0);
-  T x[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = e < left ? v[e] : from_float<T>(0.f);
-  memcpy(&u, x, 16);
-  return u;
 }
 
 // The largest magnitude of each tensor, over the sequences' tokens.  Heads that
@@ -319,7 +393,7 @@ snack_status check_args(const snack_attention_args *a) {
     return refuse(SNACK_ERR_UNSUPPORTED, "a ragged side takes at most 2^16 sequences");  // every block looks for its own
   if (tiles(a->q_offsets, a->q_tokens, group) + tiles(a->k_offsets, a->k_tokens, 1) >= lim ||
       tiles_of(a->q_offsets != nullptr, a->sequences, a->q_tokens, 1, kTileRows) * a->heads >= lim ||
-      rows * a->heads >= lim * 8)
+      rows * a->heads >= lim * 4)
     return refuse(SNACK_ERR_UNSUPPORTED, "too many rows for one launch");
   const int64_t strides[] = {a->q_stride[0], a->q_stride[1], a->q_stride[2], a->k_stride[0], a->k_stride[1],
                              a->k_stride[2], a->v_stride[0], a->v_stride[1], a->v_stride[2]};

@@ -90,18 +90,24 @@ struct Tile {
     }
   }
 
-  // o (16 x DP) += p (16 x 8 * NB, as the first product left it) times rows b.
-  template <int NB>
+  // o (16 x DP) += p (16 x 8 * NB, as the first product left it) times rows b;
+  // FINE: p in two parts of the type instead of rounded to it.
+  template <int NB, bool FINE = false>
   static __device__ __forceinline__ void sums_by_rows(float (&o)[DP / 8][4], const float (&p)[NB][4], const T *b,
                                                       int lane) {
-    uint32_t fa[NB / 2][4];
+    uint32_t fa[NB / 2][4], low[FINE ? NB / 2 : 1][4];
 #pragma unroll
-    for (int k = 0; k < NB / 2; ++k) {
-      fa[k][0] = pack2<T>(p[2 * k][0], p[2 * k][1]);
-      fa[k][1] = pack2<T>(p[2 * k][2], p[2 * k][3]);
-      fa[k][2] = pack2<T>(p[2 * k + 1][0], p[2 * k + 1][1]);
-      fa[k][3] = pack2<T>(p[2 * k + 1][2], p[2 * k + 1][3]);
-    }
+    for (int k = 0; k < NB / 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = p[2 * k + (i >> 1)][(i & 1) * 2], y = p[2 * k + (i >> 1)][(i & 1) * 2 + 1];
+        fa[k][i] = pack2<T>(x, y);
+        if (FINE) {
+          float u, v;
+          unpack2<T>(fa[k][i], u, v);
+          low[k][i] = pack2<T>(x - u, y - v);
+        }
+      }
     const T *pb = b + ((lane & 7) + ((lane >> 3) & 1) * 8) * kLd + ((lane >> 4) & 1) * 8;
 #pragma unroll
     for (int n = 0; n < DP / 8; n += 2) {
@@ -109,6 +115,10 @@ struct Tile {
       for (int k = 0; k < NB / 2; ++k) {
         uint32_t fb[4];
         ldmatrix4_turned(fb, pb + k * 16 * kLd + n * 8);
+        if (FINE) {
+          mma_k16<T>(o[n], low[k], fb[0], fb[1]);
+          mma_k16<T>(o[n + 1], low[k], fb[2], fb[3]);
+        }
         mma_k16<T>(o[n], fa[k], fb[0], fb[1]);
         mma_k16<T>(o[n + 1], fa[k], fb[2], fb[3]);
       }
@@ -174,7 +184,7 @@ struct Tile<float, DP> {
         for (int i = 0; i < 4; ++i) acc[n][i] += kOwn == 2 ? cross[n][0][i] + cross[n][kOwn - 1][i] : cross[n][0][i];
   }
 
-  template <int NB>
+  template <int NB, bool FINE = false>  // (always in two parts)
   static __device__ __forceinline__ void sums_by_rows(float (&o)[DP / 8][4], const float (&p)[NB][4],
                                                       const float *b, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -458,6 +468,10 @@ __global__ void __launch_bounds__(32 * WM) rows_forward(const AttnCall c) {
 // With P of the forward call's lse made again,
 //   dP = M * (dout . v),  dS = P * (dP - delta),  dq = scale * dS k,
 //   dk = scale * dS^T q,  dv = (M * P)^T dout.
+// A row that sees one key has P = 1 whatever the score: dS is zero, not what two
+// roundings of the same product differ by.
+// dS is taken in two parts of the type: rounded to it, it made dq and dk 1.6
+// times as far off as the rounding of the results alone.
 template <typename T>
 __device__ __forceinline__ float ds_scale(const AttnCall &c) {
   if constexpr (!std::is_same<T, __half>::value) return 1.f;
@@ -569,12 +583,12 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
             float mult = 1.f;
             if (c.drop)
               mult = draw_lane(dropout_draw(s_draw[stage][i], j), j & 3) >= c.drop ? c.keep_scale : 0.f;
-            t[n][x] = seen ? prob * ((t[n][x] * mult - delta) * ds_by_p) : 0.f;
+            t[n][x] = seen && lim > 1 ? prob * ((t[n][x] * mult - delta) * ds_by_p) : 0.f;
             p[n][x] = mult != 0.f ? prob : 0.f;
           }
         }
       Ops::template sums_by_rows<NB>(dv, p, d, lane);
-      Ops::template sums_by_rows<NB>(dk, t, q, lane);
+      Ops::template sums_by_rows<NB, true>(dk, t, q, lane);
     }
     if (ST == 2 && more) store_row_stats(stage ^ 1);
     __syncthreads();
@@ -680,11 +694,11 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
           for (int e = 0; e < 2; ++e) {
             const int je = key + Ops::column(n, lane, e), x = 2 * h + e;
             const float mult = !c.drop ? 1.f : (draw_lane(z, je & 3) >= c.drop ? c.keep_scale : 0.f);
-            t[n][x] = je < lim[h]
+            t[n][x] = je < lim[h] && lim[h] > 1
                           ? exp2f(p[n][x] * c.scale_log2 - lse[h]) * ((t[n][x] * mult - delta[h]) * ds) : 0.f;
           }
         }
-      Ops::template sums_by_rows<NB>(dq, t, k, lane);
+      Ops::template sums_by_rows<NB, true>(dq, t, k, lane);
     }
     __syncthreads();
     if (ST == 1 && key0 + STEP < end) {

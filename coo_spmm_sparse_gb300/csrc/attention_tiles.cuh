@@ -183,6 +183,20 @@ __device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint32_t b, bool ad
   }
 }
 
+// Gradients of scores in two parts (laid out as above) times rows b in one:
+// where the operands' type holds the results no better than it holds them,
+// rounding them once more would make the results 1.5 times as far off.
+template <int DP>
+__device__ __forceinline__ void fine_sums(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t kind = tc::mma_kind<__half>(DP, true);
+#pragma unroll
+  for (int k = 0; k < kTile; k += 16) {
+    const uint32_t hi = a + k / 32 * 32 + k % 32 / 2;
+    tc::mma_tmem(d, hi + 16, b + k * 8, kind, add || k > 0);
+    tc::mma_tmem(d, hi, b + k * 8, kind, true);
+  }
+}
+
 // 32 values of a row as high and low parts: columns [0, 16) and [16, 32) from `at` on.
 __device__ __forceinline__ void store_parts(uint32_t at, const float *v) {
   uint32_t hi[16], lo[16];

@@ -25,10 +25,16 @@ __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) 
   }
 }
 
+// float16 calls: the results are float16 too, so that dS is taken in two parts.
+template <typename T>
+constexpr bool kFine = std::is_same<T, __half>::value;
+
 // All operands are float16: bfloat16's are made in it first, 32-bit floats' in
 // two parts.
 template <typename T>
 using Parts = typename std::conditional<Operand<T>::kSplit, float, __half>::type;
+template <typename T>  // of the gradients of the scores
+using ScoreParts = typename std::conditional<kFine<T>, float, Parts<T>>::type;
 
 // ------------------------------------------------------------------ keys and values
 
@@ -187,7 +193,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
           if (leader) {
-            sums<Parts<T>, DP, kTile>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
+            if constexpr (kFine<T>)
+              fine_sums<DP>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
+            else
+              sums<Parts<T>, DP, kTile>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.q_empty[n & 1]);
           }
           __syncwarp();
@@ -234,6 +243,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float ds_by_p = ds * exp2f(-kHalfP);
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
     constexpr int kDpChunk = kSplit ? 32 : kHalf;  // what registers leave room for
+    const bool alone = nk == 1 || (c.causal && j0 == 0 && (warp & 3) == 0);
     const uint64_t seed = DROP ? c.draws() : 0;
     bool ok = true;
     for (int n = 0; n < all; ++n) {
@@ -321,8 +331,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           t[x + 2] = r1.x;
           t[x + 3] = r1.y;
         }
+        if (alone) {  // queries that see one key: P = 1 whatever the score, dS is zero
 #pragma unroll
-        for (int x = 0; x < kDpChunk; x += 32) store_row32<Parts<T>>(dp_at, c0 + x, t + x);
+          for (int x = 0; x < kDpChunk; ++x)
+            if (nk == 1 || (j == 0 && q0 + c0 + x == nq - nk)) t[x] = 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < kDpChunk; x += 32) store_row32<ScoreParts<T>>(dp_at, c0 + x, t + x);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -503,8 +518,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           if (leader) {
             // split: two buffers in turn, each added to the rows' own sums two tiles later
-            sums<Parts<T>, DP, kTile>(tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), tmem + (2 * n + 1) % 3 * kTile,
-                               k0c + n % 3 * kStep, n > 0);
+            const uint32_t to = tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), ds_at = tmem + (2 * n + 1) % 3 * kTile;
+            if constexpr (kFine<T>)
+              fine_sums<DP>(to, ds_at, k0c + n % 3 * kStep, n > 0);
+            else
+              sums<Parts<T>, DP, kTile>(to, ds_at, k0c + n % 3 * kStep, n > 0);
             tc::commit(&bars.k_empty[n % 3]);
           }
           __syncwarp();
@@ -534,6 +552,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         lse = 0.f;
       else
         lim = max(0, seen_keys(c.causal, i, nq, nk));
+      if (lim == 1) lim = 0;  // P = 1 whatever the score: dS is zero
     }
     const Scales by = scales_of(c);
     float acc[kSplit ? DP / 2 : 1] = {};  // split: the sums of this warpgroup's half of the columns
@@ -589,8 +608,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
-      store_row32<Parts<T>>(dp_at, 0, t);
-      store_row32<Parts<T>>(dp_at, 32, t + 32);
+      store_row32<ScoreParts<T>>(dp_at, 0, t);
+      store_row32<ScoreParts<T>>(dp_at, 32, t + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores[b]);

@@ -245,6 +245,29 @@ def test_scores_of_every_size(dtype, nq, nk):
     check(q * 0, k, v, dout)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_queries_that_see_one_key_move_no_score(dtype):
+    """Softmax of one score is 1: dq and dk are exactly zero, not what two roundings leave."""
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(18)
+    for n, nq, room, opts in ((10, 1, 1, {}), (3, 300, 300, dict(causal=False)), (200, 70, 70, dict(causal=False))):
+        q, dout = (rnd(g, (n, nq, 4, 64), dtype) for _ in range(2))
+        k, v = (rnd(g, (n, room, 2, 64), dtype) for _ in range(2))
+        o = dict(k_lengths=torch.ones(n, dtype=torch.int32, device="cuda"), dropout=0.2, seed=1, **opts)
+        out, lse = sn.snack_attention_forward(q, k, v, **o)
+        dq, dk, dv = sn.snack_attention_backward(dout, q, k, v, out, lse, **o)
+        assert not dq.any() and not dk.any() and dv[:, 0].any()
+    # the first query of a causal call, among others
+    q, k, v, dout = (rnd(g, (2, 900, 4, 64), dtype) for _ in range(4))
+    out, lse = sn.snack_attention_forward(q, k, v)
+    dout[:, 1:] = 0
+    dq, dk, dv = sn.snack_attention_backward(dout, q, k, v, out, lse)
+    assert not dq[:, 0].any() and not dk.any()
+    # its probability is exp(s - lse): off by a share 2 * 2^-18 * A + 2^-16 at most, A below 16 here
+    share = 2.0 ** -13 + 2.0 ** -16 + attention_ref.U[dtype]
+    assert ((dv[:, 0].double() - dout[:, 0].double()).abs() <= share * dout[:, 0].double().abs() + 1e-7).all()
+
+
 def test_small_float16_gradients():
     """A loss that is a mean makes gradients that float16 only holds as subnormals."""
     g = gen(8)
