@@ -122,11 +122,17 @@ __device__ __forceinline__ uint4 load_vector(const T *v, int left) {
   return u;
 }
 
-// delta of 16-bit calls with at most 64 keys: sum_j M P (dout . v_j), from the
-// tensors themselves.  out is rounded, and over a handful of keys what that does
-// to delta made dq and dk twice as far off as the rounding of the results alone;
-// over more it is lost among them.  A warp takes a row and head, a lane a key.
-constexpr int kFewKeys = 64;
+// delta of 16-bit calls with few keys: sum_j M P (dout . v_j), from the tensors
+// themselves.  out is rounded, and with delta from it causal calls' dq and dk were
+// off by this many times what rounding the results alone costs (worst of 5 draws,
+// three shapes): 7.3 at 2 keys, 2.1 at 8, 1.6 at 32 and 1.3 at 64; from here 1.0.
+// A warp takes a row and head, a lane a key, so a warp's loads of k and v lie in 32
+// rows, and that is what it costs.  Whole backward calls, from out / from here (us,
+// steps of 2): bf16 8 x 16 tokens, 24 heads over 12 of 128 (work 393216) 31 / 37;
+// 24 tokens (589824) 35 / 49; 6 x 32 tokens, 24 over 12 of 64, every key seen
+// (294912) 25 / 37; 8 x 64 tokens, 24 over 12 of 128: 61 / 125.  So up to 32 keys
+// and a work of 400000; above it delta is of out: at 8 x 24 tokens 1.3 times.
+constexpr int kFewKeys = 32;
 template <typename T>
 __global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c, uint32_t *peak) {
   const int lane = threadIdx.x & 31;
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c
     const Span ks = own_span(c.k_offsets, c.k_lengths, c.k_offsets ? s + 1 : s, c.sequences, c.k_tokens);
     const int i = c.q_offsets ? (int)(row - qs.row) : token;
     const int64_t place = (int64_t)head * c.rows + row;
-    const int seen = min(kFewKeys, seen_keys(c.causal, i, qs.valid, ks.valid));
+    const int seen = seen_keys(c.causal, i, qs.valid, ks.valid);
     float term = 0.f;
     constexpr int E = 16 / sizeof(T);
     for (int col = lane * E; col < c.d; col += 32 * E) {
@@ -190,12 +196,20 @@ __global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c
   if (peak) block_peak(top, peak);
 }
 
+// What that kernel reads, in products.  A causal call's rows before its last
+// k_tokens see no key and are not counted, though each still takes a warp: causal
+// bf16 8 x 1024 queries over 2 keys, 12 heads of 64, 41 / 76 us for dq and dk 2.25
+// times as far off or 1.0; 2 x 2115 over 8, 24 heads of 128, 70 / 104 for 1.6 or 1.0.
+constexpr double kFewKeysWork = 400000.0;
+inline double few_keys_work(const AttnCall &c) {
+  const double keys = c.k_offsets ? (double)c.k_tokens : (double)c.sequences * c.k_tokens;
+  const double rows = (double)c.rows;
+  return (c.causal && keys < rows ? keys : rows) * c.heads * c.d;
+}
+
 template <typename T>
 cudaError_t delta_launch(const AttnCall &c, bool vec, uint32_t *peak, cudaStream_t s) {
-  // (a warp's lanes read 32 rows of k and v side by side, 8 * d places of the L1 for 32 keys: about
-  // 10 us at this limit, where the plain form takes 4)
-  if (sizeof(T) == 2 && c.k_tokens <= kFewKeys &&
-      (double)c.rows * c.heads * ((c.k_tokens + 31) / 32) * c.d <= 360000.0)
+  if (sizeof(T) == 2 && c.k_tokens <= kFewKeys && few_keys_work(c) <= kFewKeysWork)
     return launch_kernel(attention_delta_few_keys<T>, dim3((unsigned)((c.rows * c.heads + 7) / 8)), 256, 0, false, s, c,
                          peak);
   const int lanes = vec ? (c.d * (int)sizeof(T) + 15) / 16 : 32;

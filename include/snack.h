@@ -503,9 +503,9 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
  * attention.cu) take each operand as two float16 parts of the tensor times a
  * power of two: 22 bits of what lies above 2^-17 of the tensor's largest
  * element, and nothing more than 2^-39 of that off.  Gradients of scores and
- * probabilities are split, or in 16-bit types rounded to float16, the same
- * way: a term dS[i][j] is never more than 2^-38 of
- * 2 * head_size * max|dout| * max|v| / (1 - dropout) off by that.  An infinite
+ * probabilities are split the same way (16-bit calls of such size: float16 in one
+ * part, but for float16 calls' gradients of scores, in two): in 32-bit calls a
+ * term dS[i][j] is never more than 2^-38 of 2 * head_size * max|dout| * max|v| / (1 - dropout) off by that.  An infinite
  * or NaN element inside a sequence may reach results that do not depend on it.
  * Limits: 1 <= head_size <= 128, heads <= 65536, ragged sides of at most 65536
  * sequences; tokens, and q_tokens * (heads / key_heads), below 2^31 - 4096.
@@ -536,7 +536,11 @@ snack_status snack_attention_forward(const snack_attention_args *args, void *out
  *   dS[i][j] = P[i][j] * (M[i][j] * (dout[i] . v[j]) - delta[i]),
  *   dq[i] = scale * sum_j dS[i][j] k[j],   dk[j] = scale * sum_i dS[i][j] q[i],
  *   dv[j] = sum_i M[i][j] P[i][j] dout[i],
- * dk and dv summed over the query heads that share them.  dq, dk and dv are
+ * dk and dv summed over the query heads that share them.  16-bit calls of some
+ * rows over at most 32 keys (see attention.cu) take delta as the sum over j of
+ * M[i][j] P[i][j] (dout[i] . v[j]) instead, without out's rounding.  A query that
+ * sees one key moves no score, so its dS is exactly 0 (with dropout too: delta and
+ * the term are one value).  dq, dk and dv are
  * overwritten and must not overlap one another or an input; each may be NULL.
  * No atomics: the same inputs give the same bits.
  */

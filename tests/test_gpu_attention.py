@@ -268,6 +268,38 @@ def test_queries_that_see_one_key_move_no_score(dtype):
     assert ((dv[:, 0].double() - dout[:, 0].double()).abs() <= share * dout[:, 0].double().abs() + 1e-7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n, nq, nk, heads, key_heads, d, causal", [
+    (1, 2, 2, 8, 8, 64, True), (2, 32, 32, 2, 1, 48, True), (3, 5, 9, 4, 2, 65, False),
+    (8, 16, 16, 24, 12, 128, True),   # rows * heads * d = 393216
+    (8, 1024, 2, 12, 12, 64, True)])  # most rows see no key
+def test_gradients_of_few_keys_are_free_of_the_rounding_of_out(dtype, n, nq, nk, heads, key_heads, d, causal):
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(19)
+    q, dout = (rnd(g, (n, nq, heads, d), dtype) for _ in range(2))
+    k, v = (rnd(g, (n, nk, key_heads, d), dtype) for _ in range(2))
+    opts = dict(causal=causal, dropout=0.2, seed=3)
+    out, lse = sn.snack_attention_forward(q, k, v, **opts)
+    want = sn.snack_attention_backward(dout, q, k, v, out, lse, **opts)
+    other = out * (1 + torch.finfo(dtype).eps)
+    assert not torch.equal(other, out)
+    got = sn.snack_attention_backward(dout, q, k, v, other, lse, **opts)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_few_keys_on_both_sides_of_the_rule(dtype):
+    g = gen(20)
+    for n, length in ((2, 32), (2, 33), (8, 17), (300, 2)):
+        q, dout = (rnd(g, (n, length, 24, 128), dtype) for _ in range(2))
+        k, v = (rnd(g, (n, length, 12, 128), dtype) for _ in range(2))
+        check(q, k, v, dout, dropout=0.2, seed=1)
+    at = offsets(0, 3, 1, 12, 16)  # 32 tokens
+    q, dout = (rnd(g, (32, 4, 72), dtype) for _ in range(2))
+    k, v = (rnd(g, (32, 2, 72), dtype) for _ in range(2))
+    check(q, k, v, dout, q_offsets=at, k_offsets=at)
+
+
 def test_small_float16_gradients():
     """A loss that is a mean makes gradients that float16 only holds as subnormals."""
     g = gen(8)
