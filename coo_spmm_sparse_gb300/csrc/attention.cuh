@@ -196,6 +196,15 @@ __device__ __forceinline__ int seen_keys(int causal, int i, int nq, int nk) {
   return causal ? min(nk, i + nk - nq + 1) : nk;
 }
 
+// The first query that sees one of the keys from j0 on; nq where there is none: a
+// tile that lies wholly in padding has no queries (j0 - nk + nq would be up to
+// j0 then, and that times the group passes 31 bits).
+__host__ __device__ inline int first_query(int causal, int j0, int nq, int nk) {
+  if (j0 >= nk) return nq;
+  const int first = causal ? j0 - nk + nq : 0;
+  return first > 0 ? first : 0;
+}
+
 // The number of the draw that decides about keys 4c .. 4c+3 of a query row is
 // row * 2^30 + c, with row = token * heads + head.
 __device__ __forceinline__ uint64_t dropout_row(uint64_t seed, int64_t token, int heads, int head) {

@@ -503,8 +503,7 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
   const Span ks = own_span(c.k_offsets, c.k_lengths, at.s, c.sequences, c.k_tokens);
   const Span qs = other_span(c.q_offsets, c.q_lengths, at.s, c.k_offsets != nullptr, c.sequences, c.q_tokens);
   const int j0 = at.tile * 16 * WM, nq = qs.valid, nk = ks.valid;
-  const int first = c.causal ? max(0, j0 - (nk - nq)) : 0;
-  const int end = j0 < nk ? nq * G : 0;  // rows; none see padding
+  const int row_begin = first_query(c.causal, j0, nq, nk) * G, end = nq * G;  // rows; none see padding
 
   const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
   const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, kh * G, G, c.d);
@@ -545,7 +544,6 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
     s_lim[stage][threadIdx.x] = next_lse == -INFINITY ? 0 : next_lim;
     if (c.drop) s_draw[stage][threadIdx.x] = next_draw;
   };
-  const int row_begin = first * G;
   if (row_begin < end) {
     copy_rows<T, DP>(sk, kr, j0, 16 * WM, nk);
     copy_rows<T, DP>(sv, vr, j0, 16 * WM, nk);

@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const Span ks = own_span(c.k_offsets, c.k_lengths, at.s, c.sequences, c.k_tokens);
   const Span qs = other_span(c.q_offsets, c.q_lengths, at.s, c.k_offsets != nullptr, c.sequences, c.q_tokens);
   const int j0 = at.tile * kTile, nq = qs.valid, nk = ks.valid;
-  const int tile0 = (c.causal ? max(0, j0 - (nk - nq)) : 0) / kTile;
-  const int tiles = j0 < nk ? max(0, (nq + kTile - 1) / kTile - tile0) : 0;
+  const int first = first_query(c.causal, j0, nq, nk), tile0 = first / kTile;
+  const int tiles = first < nq ? (nq + kTile - 1) / kTile - tile0 : 0;
   const int all = tiles * G;
 
   const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = c.k_offsets ? (int)ks.row : 0;
