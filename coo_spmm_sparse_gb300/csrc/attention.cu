@@ -515,7 +515,7 @@ Plan plan_forward(const AttnCall &c, int type) {
   const int64_t splits = std::min(std::min(want, c.k_tokens / least), (int64_t)kMostSplits);
   if (splits <= 1) return p;
   p.chunk = (int)round_up((c.k_tokens + splits - 1) / splits, 128);
-  p.splits = (int)((c.k_tokens + p.chunk - 1) / p.chunk);
+  p.splits = (int)(((int64_t)c.k_tokens + p.chunk - 1) / p.chunk);
   if (p.splits > 1) {
     p.part = p.bytes;
     p.bytes += (size_t)p.splits * c.rows * c.heads * (c.d + 1) * sizeof(float);

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * W) few_forward(const AttnCall c) {
   const int last = min((r0 + 15) / G, nq - 1);
   const int begin = blockIdx.y * c.chunk;
   int end = r0 / G < nq ? max(0, seen_keys(c.causal, last, nq, nk)) : 0;
-  if (c.splits > 1) end = min(end, begin + c.chunk);
+  if (c.splits > 1) end = begin + min(end - begin, c.chunk);  // (begin + chunk may pass 31 bits)
 
   T *const ring = sq + F::kQueries + warp * kStages * F::kTileElems;
   const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
