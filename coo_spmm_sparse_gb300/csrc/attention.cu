@@ -229,7 +229,7 @@ struct Source {
   int tokens, heads;
   int64_t rows;    // tokens of all sequences
   uint32_t *peak;  // receives the bits of the largest magnitude
-  __half *parts;   // receives the float16 parts
+  void *made;      // receives what the tiles read
 };
 struct Sources {
   Source t[4];
@@ -279,24 +279,23 @@ __global__ void __launch_bounds__(256) attention_peak(const Sources all, int seq
   block_peak(top, t.peak);
 }
 
-// Every tensor in float16, its elements times the power of two that brings its
-// largest to [2^14, 2^15): rows of W columns of each head (zeros behind the head
-// size and for tokens outside every sequence).  32-bit floats as two parts, 64
-// high and 64 low halves; bfloat16's eight bits lose nothing down to 2^-28 of
-// the largest, and what lies below is never more than 2^-39 of it off.  Grid: y =
+// Every tensor as TMA can bring it: rows of W columns of each head (zeros behind the
+// head size and for tokens outside every sequence).  16-bit types as they are.
+// 32-bit floats as two float16 parts, 64 high and 64 low halves, of the elements
+// times the power of two that brings the tensor's largest to [2^14, 2^15).  Grid: y =
 // tensor.
 template <typename T, int W>
-__global__ void __launch_bounds__(256) half_parts(const Sources all, int sequences, int d) {
+__global__ void __launch_bounds__(256) tile_operands(const Sources all, int sequences, int d) {
   constexpr bool kSplit = sizeof(T) == 4;
   constexpr int E = 16 / sizeof(T), kPlaces = (kSplit ? W / 2 : W) / E, kAhead = 4;
   const Source &t = all.t[blockIdx.y];
   const int lane = threadIdx.x & 31, work = t.heads * kPlaces;
-  const float by = exp2f((float)power_to_half(*t.peak));
+  const float by = kSplit ? exp2f((float)power_to_half(*t.peak)) : 1.f;
   for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
     int64_t at;
     const bool have = token_of(t, sequences, row, &at);
     const T *const v = static_cast<const T *>(t.from.p) + at;
-    __half *const parts = t.parts + row * t.heads * W;
+    uint16_t *const made = static_cast<uint16_t *>(t.made) + row * t.heads * W;
     for (int i0 = lane; i0 < work; i0 += 32 * kAhead) {
       uint4 u[kAhead];
 #pragma unroll
@@ -308,23 +307,23 @@ __global__ void __launch_bounds__(256) half_parts(const Sources all, int sequenc
       for (int n = 0; n < kAhead; ++n) {
         const int i = i0 + n * 32, head = i / kPlaces, col = i % kPlaces * E;
         if (i >= work) break;
-        float x[E];
-        unpack16<T>(u[n], x);
-        uint32_t hi[E / 2], lo[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          float a, b;
-          const float l = x[2 * e] * by, r = x[2 * e + 1] * by;
-          hi[e] = pack2<__half>(l, r);
-          unpack2<__half>(hi[e], a, b);
-          lo[e] = pack2<__half>(l - a, r - b);
-        }
-        __half *const to = parts + head * W + col;
+        uint16_t *const to = made + head * W + col;
         if constexpr (kSplit) {
+          float x[E];
+          unpack16<T>(u[n], x);
+          uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            float a, b;
+            const float l = x[2 * e] * by, r = x[2 * e + 1] * by;
+            hi[e] = pack2<__half>(l, r);
+            unpack2<__half>(hi[e], a, b);
+            lo[e] = pack2<__half>(l - a, r - b);
+          }
           *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2 *>(to + W / 2) = make_uint2(lo[0], lo[1]);
         } else {
-          *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(to) = u[n];
         }
       }
     }
@@ -450,27 +449,24 @@ AttnCall call_of(const snack_attention_args *a) {
 // How a call is computed, and what of the workspace it takes.
 struct Plan {
   bool tiles = false, few = false;  // on tcgen05; in blocks of 16 rows
-  int splits = 1, chunk = 0, width = 0;  // width: columns of operands made in float16; 0: none are
+  int splits = 1, chunk = 0, width = 0;  // width: columns of operands that are made; 0: none are
   size_t delta = 0, part = 0, parts[4] = {}, bytes = 0;  // offsets; parts: of q, k, v, dout
 };
 constexpr size_t kPeaks = 256;
 
-// Operands that are made in float16 first: those of 32-bit calls, and bfloat16's
-// of backward calls.  There the gradients of the scores are an operand too:
-// rounded to bfloat16 they made dq and dk 1.5 times as far off as the rounding of
-// the results alone, in float16 1.1 times, for 5 % of a long call's time.
-// 16-bit tensors that TMA cannot bring as they lie (odd head sizes, addresses or
-// strides) are made too: else mma.sync would take them, several times slower.
-int part_width(const AttnCall &c, int type, bool backward) {
+// Operands that are made first: those of 32-bit calls, and 16-bit tensors that TMA
+// cannot bring as they lie (odd head sizes, addresses or strides): else mma.sync
+// would take them, several times slower.
+int part_width(const AttnCall &c, int type) {
   if (type == SNACK_F32) return 128;
-  return (type == SNACK_BF16 && backward) || !tiles_read(c) ? (c.d <= 64 ? 64 : 128) : 0;
+  return tiles_read(c) ? 0 : c.d <= 64 ? 64 : 128;
 }
 void plan_parts(Plan *p, const AttnCall &c, int width, bool backward) {
   const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
   const int64_t rows[4] = {c.rows * c.heads, keys * c.key_heads, keys * c.key_heads, backward ? c.rows * c.heads : 0};
   for (int i = 0; i < 4; ++i) {
     p->parts[i] = p->bytes;
-    p->bytes += rows[i] * width * sizeof(__half);
+    p->bytes += rows[i] * width * 2;
   }
 }
 
@@ -496,7 +492,7 @@ Plan plan_forward(const AttnCall &c, int type) {
   p.tiles = worth_tiles(c, type, false) && tiles_take(c, type);
   int64_t blocks, least, want;  // least keys of a part: below that it starts and ends more than it reads
   if (p.tiles) {
-    p.width = part_width(c, type, false);
+    p.width = part_width(c, type);
     if (p.width) {
       p.bytes = kPeaks;
       plan_parts(&p, c, p.width, false);
@@ -529,7 +525,7 @@ Plan plan_backward(const AttnCall &c, int type) {
   p.delta = p.bytes;
   p.bytes += round_up(c.rows * c.heads * (int64_t)sizeof(float), 256);
   p.tiles = worth_tiles(c, type, true) && tiles_take(c, type);
-  p.width = p.tiles ? part_width(c, type, true) : 0;
+  p.width = p.tiles ? part_width(c, type) : 0;
   if (p.width) plan_parts(&p, c, p.width, true);
   return p;
 }
@@ -545,7 +541,7 @@ Sources sources_of(const AttnCall &c, const Plan &p, char *workspace) {
     const bool own = i == 0 || i == 3;
     s.t[i] = Source{*from[i], own ? c.q_offsets : c.k_offsets, own ? c.q_lengths : c.k_lengths,
                     own ? c.q_tokens : c.k_tokens, own ? c.heads : c.key_heads, own ? c.rows : keys, peak + at[i],
-                    reinterpret_cast<__half *>(workspace + p.parts[i])};
+                    workspace + p.parts[i]};
   }
   return s;
 }
@@ -554,18 +550,20 @@ unsigned spread(int64_t rows) {  // a warp for each, or as many as are resident 
   return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, 8 * device_sms()));
 }
 
-// Makes the float16 parts of a call's operands: q, k, v and, backward, dout,
-// whose peak is there already.
+// Makes a call's operands: q, k, v and, backward, dout, whose peak is there already.
 template <typename T>
 cudaError_t make_parts(AttnCall *c, const Plan &p, bool backward, char *workspace, SplitParts *parts, cudaStream_t s) {
   const Sources all = sources_of(*c, p, workspace);
   const unsigned blocks = spread(std::max(all.t[0].rows, all.t[1].rows));
-  cudaError_t e = launch_kernel(attention_peak<T>, dim3(blocks, 3), 256, 0, false, s, all, c->sequences, c->d);
+  cudaError_t e = cudaSuccess;
+  if (sizeof(T) == 4) {
+    e = launch_kernel(attention_peak<T>, dim3(blocks, 3), 256, 0, false, s, all, c->sequences, c->d);
+    c->made = 1;
+  }
   if (e == cudaSuccess)
-    e = launch_kernel(p.width == 64 ? half_parts<T, 64> : half_parts<T, 128>, dim3(blocks, backward ? 4 : 3), 256, 0,
-                      false, s, all, c->sequences, c->d);
-  c->made = 1;
-  *parts = SplitParts{p.width, all.t[0].parts, all.t[1].parts, all.t[2].parts, all.t[3].parts};
+    e = launch_kernel(p.width == 64 ? tile_operands<T, 64> : tile_operands<T, 128>, dim3(blocks, backward ? 4 : 3), 256,
+                      0, false, s, all, c->sequences, c->d);
+  *parts = SplitParts{p.width, all.t[0].made, all.t[1].made, all.t[2].made, all.t[3].made};
   return e;
 }
 
@@ -584,7 +582,7 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
   if (p.tiles) {
     SplitParts parts = {};
     if (p.width) {
-      e = clear_peaks(&c, workspace, s);
+      if (type == SNACK_F32) e = clear_peaks(&c, workspace, s);
       if (e == cudaSuccess) e = make_parts<T>(&c, p, false, workspace, &parts, s);
     }
     if (e == cudaSuccess) e = tile_forward_launch(c, type, parts, s);
@@ -599,7 +597,7 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
 template <typename T>
 cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  const bool peaks = p.width || type == SNACK_F16;
+  const bool peaks = type == SNACK_F16 || (type == SNACK_F32 && p.width);
   cudaError_t e = peaks ? clear_peaks(&c, workspace, s) : cudaSuccess;
   if (e == cudaSuccess && c.rows) {
     const auto even = [](const Strided &t) {
@@ -610,9 +608,8 @@ cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace,
   }
   if (e != cudaSuccess) return e;
   SplitParts parts = {};
-  if (p.width) {
-    e = make_parts<T>(&c, p, true, workspace, &parts, s);
-  } else if (type == SNACK_F16) {
+  if (p.width) e = make_parts<T>(&c, p, true, workspace, &parts, s);
+  if (e == cudaSuccess && type == SNACK_F16) {
     Sources v = sources_of(c, p, workspace);
     v.t[0] = v.t[2];
     if (v.t[0].rows)

@@ -17,12 +17,12 @@ struct AttnCall {
   float *lse;    // [heads][rows]: log of the sum of exp(scale * q . k), -inf where no key is seen
   float *delta;  // [heads][rows]: dout . out
   float *part;   // partial results of a split call
-  const uint32_t *peak;  // bits of the largest |dout|, |v|, |q|, |k| (float16: the first two)
+  const uint32_t *peak;  // bits of the largest |dout|, |v|, |q|, |k| (float16: the first two; bfloat16: none)
   int64_t rows;  // rows of lse for a head: all tokens of q
   int sequences, q_tokens, k_tokens;
   int heads, key_heads, group, d;
   int causal, splits, chunk;
-  int made;  // the operands were made in float16, scaled by the powers of two of their peaks
+  int made;  // 32-bit operands: made as two float16 parts, scaled by the powers of two of their peaks
   float scale, scale_log2;  // scale * log2(e)
   const int32_t *q_offsets, *k_offsets, *q_lengths, *k_lengths;
   uint32_t drop;  // 0: no dropout; else a probability is kept where its 16 bits are at least this
@@ -136,15 +136,15 @@ cudaError_t rows_backward_launch(const AttnCall &c, cudaStream_t s);
 // The forward call of few rows (attention_few.cu).
 cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s);
 
-// Where operands made in float16 are: [tokens][heads][width]; width 0: none are.
+// Where operands that were made are: [tokens][heads][width]; width 0: none are.
 struct SplitParts {
   int width;
   void *q, *k, *v, *dout;
 };
 
 // Those of attention on tcgen05 (attention_tiles*.cu): which calls they take,
-// whether TMA can bring a 16-bit call's tensors as they lie (else they are made in
-// float16 first), and whether one of their bounded waits has run out since the last question.
+// whether TMA can bring a 16-bit call's tensors as they lie (else they are copied
+// first), and whether one of their bounded waits has run out since the last question.
 bool tiles_take(const AttnCall &c, int type);
 bool tiles_read(const AttnCall &c);  // as the tensors lie
 int64_t tile_forward_blocks(const AttnCall &c);

@@ -13,7 +13,7 @@
 // may not be finite.
 //
 // 32-bit floats arrive as two float16 parts of a tensor scaled by a power of two
-// to below 2^15, x = hi + lo (made by split_parts in attention.cu): 22 bits of
+// to below 2^15, x = hi + lo (made by tile_operands in attention.cu): 22 bits of
 // everything above 2^-17 of the tensor's largest, and never more than 2^-39 of
 // that off.  A row has its 64 high halves, then its 64 low ones, and a product
 // is hi*hi + hi*lo + lo*hi; probabilities (2^14 fold) and gradients of scores
@@ -136,7 +136,7 @@ __device__ __forceinline__ void store_sums(uint32_t from, T *row, float factor, 
   }
 }
 
-// Operands that were made are scaled by powers of two: what takes them out again.
+// 32-bit operands' parts are scaled by powers of two: what takes them out again.
 struct Scales {
   float scores, dprobs, q, k, v, dout;
 };
@@ -183,12 +183,12 @@ __device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint32_t b, bool ad
   }
 }
 
-// Gradients of scores in two parts (laid out as above) times rows b in one:
-// where the operands' type holds the results no better than it holds them,
+// Gradients of scores in two parts of 16-bit type T (laid out as above) times rows b
+// in one: where the operands' type holds the results no better than it holds them,
 // rounding them once more would make the results 1.5 times as far off.
-template <int DP>
+template <typename T, int DP>
 __device__ __forceinline__ void fine_sums(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  constexpr uint32_t kind = tc::mma_kind<__half>(DP, true);
+  constexpr uint32_t kind = tc::mma_kind<T>(DP, true);
 #pragma unroll
   for (int k = 0; k < kTile; k += 16) {
     const uint32_t hi = a + k / 32 * 32 + k % 32 / 2;
@@ -198,14 +198,15 @@ __device__ __forceinline__ void fine_sums(uint32_t d, uint32_t a, uint32_t b, bo
 }
 
 // 32 values of a row as high and low parts: columns [0, 16) and [16, 32) from `at` on.
+template <typename T>
 __device__ __forceinline__ void store_parts(uint32_t at, const float *v) {
   uint32_t hi[16], lo[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     float a, b;
-    hi[e] = pack2<__half>(v[2 * e], v[2 * e + 1]);
-    unpack2<__half>(hi[e], a, b);
-    lo[e] = pack2<__half>(v[2 * e] - a, v[2 * e + 1] - b);
+    hi[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+    unpack2<T>(hi[e], a, b);
+    lo[e] = pack2<T>(v[2 * e] - a, v[2 * e + 1] - b);
   }
   tc::store16(at, hi);
   tc::store16(at + 16, lo);
@@ -283,12 +284,12 @@ static inline bool even(const Strided &t, int64_t heads, int64_t tokens, int64_t
   return aligned_to(t.p, 16) && good(heads, t.head) && good(tokens, t.token) && good(seqs, t.seq);
 }
 
-// The maps of a call's operands: its tensors, or their float16 parts.
+// The maps of a call's operands: its tensors, or what was made of them.
 static inline bool maps_of(TileMaps *m, const AttnCall &c, int type, const SplitParts &parts, bool backward) {
   const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
   const auto map = [&](CUtensorMap *to, const Strided &t, void *part, int64_t heads, int64_t tokens, int64_t seqs) {
     const int64_t row = parts.width;
-    return row ? map_of(to, SNACK_F16, Strided{part, tokens * heads * row, heads * row, row}, row, heads, tokens, seqs)
+    return row ? map_of(to, type == SNACK_F32 ? SNACK_F16 : type, Strided{part, tokens * heads * row, heads * row, row}, row, heads, tokens, seqs)
                  : map_of(to, type, t, c.d, heads, tokens, seqs);
   };
   return map(&m->q, c.q, parts.q, c.heads, c.q_tokens, qn) && map(&m->k, c.k, parts.k, c.key_heads, c.k_tokens, kn) &&

@@ -11,12 +11,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = kTile / 2;  // columns of a tile that a warpgroup takes
 constexpr int kStatWarp = 10;
 
-// 32 values of a row, columns [x, x + 32) of a warpgroup's 64 that begin at
+// 32 probabilities of a row, columns [x, x + 32) of a warpgroup's 64 that begin at
 // `at`, as the left operand of a product.
 template <typename T>
 __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) {
   if constexpr (Operand<T>::kSplit) {
-    store_parts(at + x, v);
+    store_parts<__half>(at + x, v);
   } else {
     uint32_t out[16];
 #pragma unroll
@@ -25,16 +25,30 @@ __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) 
   }
 }
 
-// float16 calls: the results are float16 too, so that dS is taken in two parts.
+// The gradients of the scores, always in two parts: in 16-bit types rounding them to
+// one made dq and dk 1.5 times as far off as the rounding of the results alone.
 template <typename T>
-constexpr bool kFine = std::is_same<T, __half>::value;
+__device__ __forceinline__ void store_score32(uint32_t at, int x, const float *v) {
+  store_parts<typename Operand<T>::type>(at + x, v);
+}
+template <typename T, int DP>
+__device__ __forceinline__ void score_sums(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  if constexpr (Operand<T>::kSplit)
+    sums<T, DP, kTile>(d, a, b, add);
+  else
+    fine_sums<T, DP>(d, a, b, add);
+}
 
-// All operands are float16: bfloat16's are made in it first, 32-bit floats' in
-// two parts.
+// float16 operands hold neither small probabilities nor small gradients of scores:
+// they are taken times powers of two.  bfloat16 has the range of 32 bits.
 template <typename T>
-using Parts = typename std::conditional<Operand<T>::kSplit, float, __half>::type;
-template <typename T>  // of the gradients of the scores
-using ScoreParts = typename std::conditional<kFine<T>, float, Parts<T>>::type;
+constexpr bool kScaled = !std::is_same<T, __nv_bfloat16>::value;
+template <typename T>
+constexpr float kUp = kScaled<T> ? kHalfP : 0.f;  // the power of the probabilities
+template <typename T>
+__device__ __forceinline__ float ds_scale(const AttnCall &c) {
+  return kScaled<T> ? half_ds_scale(c) : 1.f;
+}
 
 // ------------------------------------------------------------------ keys and values
 
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.q_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<Parts<T>, DP>(t_s, k0, q0 + (n & 1) * kStep);
+            products<T, DP>(t_s, k0, q0 + (n & 1) * kStep);
             tc::commit(&bars.scores);
           }
           __syncwarp();
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.d_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<Parts<T>, DP>(t_dp, v0, d0 + (n & 1) * kStep);
+            products<T, DP>(t_dp, v0, d0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs);
           }
           __syncwarp();
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = wait(&bars.probs, n & 1);
           if (!ok) break;
           if (leader) {
-            sums<Parts<T>, DP, kTile>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
+            sums<T, DP, kTile>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.d_empty[n & 1]);
           }
           __syncwarp();
@@ -193,10 +207,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
           if (leader) {
-            if constexpr (kFine<T>)
-              fine_sums<DP>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
-            else
-              sums<Parts<T>, DP, kTile>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
+            score_sums<T, DP>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.q_empty[n & 1]);
           }
           __syncwarp();
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     } else if (warp == kStatWarp) {
-      constexpr float up = kHalfP;
+      constexpr float up = kUp<T>;
       for (int n = 0; n < all; ++n) {
         const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile;
         const int64_t place = (int64_t)(kh * G + g) * c.rows + qs.row;
@@ -237,10 +248,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int w = warp >> 2, j = j0 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
-    const float ds = half_ds_scale(c);
+    const float ds = ds_scale<T>(c);
     const Scales by = scales_of(c);
     const float2 cs2 = make_float2(by.scores, by.scores);
-    const float ds_by_p = ds * exp2f(-kHalfP);
+    const float ds_by_p = ds * exp2f(-kUp<T>);
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
     constexpr int kDpChunk = kSplit ? 32 : kHalf;  // what registers leave room for
     const bool alone = nk == 1 || (c.causal && j0 == 0 && (warp & 3) == 0);
@@ -295,7 +306,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = !DROP || (kept[e & 3] >> ((x + e) & ~3) & 1) ? p[x + e] : 0.f;
-        store_row32<Parts<T>>(s_at, x, v);
+        store_row32<T>(s_at, x, v);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (nk == 1 || (j == 0 && q0 + c0 + x == nq - nk)) t[x] = 0.f;
         }
 #pragma unroll
-        for (int x = 0; x < kDpChunk; x += 32) store_row32<ScoreParts<T>>(dp_at, c0 + x, t + x);
+        for (int x = 0; x < kDpChunk; x += 32) store_score32<T>(dp_at, c0 + x, t + x);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -354,7 +365,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j < ks.cover)
         row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
               kh * to.head;
-      const float factor = w ? exp2f(-kHalfP) * c.keep_scale * by.dout : c.scale / ds * by.q;
+      const float factor = w ? exp2f(-kUp<T>) * c.keep_scale * by.dout : c.scale / ds * by.q;
       if constexpr (kSplit) {
         if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP));
         store_floats<DP>(row, acc, factor, c.d, j >= nk);
@@ -495,7 +506,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.k_full[n % 3], (n / 3) & 1);
           if (done && leader) {
-            products<Parts<T>, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
+            products<T, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
             tc::commit(&bars.scores[n & 1]);
           }
           __syncwarp();
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.v_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<Parts<T>, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
+            products<T, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs[n & 1]);
             tc::commit(&bars.v_empty[n & 1]);
           }
@@ -519,10 +530,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (leader) {
             // split: two buffers in turn, each added to the rows' own sums two tiles later
             const uint32_t to = tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), ds_at = tmem + (2 * n + 1) % 3 * kTile;
-            if constexpr (kFine<T>)
-              fine_sums<DP>(to, ds_at, k0c + n % 3 * kStep, n > 0);
-            else
-              sums<Parts<T>, DP, kTile>(to, ds_at, k0c + n % 3 * kStep, n > 0);
+            score_sums<T, DP>(to, ds_at, k0c + n % 3 * kStep, n > 0);
             tc::commit(&bars.k_empty[n % 3]);
           }
           __syncwarp();
@@ -541,7 +549,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::take_registers<kRowRegisters>();
     const int w = warp >> 2, i = i0 + (warp & 3) * 32 + lane;
     const uint32_t at_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float ds = half_ds_scale(c);
+    const float ds = ds_scale<T>(c);
     float lse = 0.f, delta = 0.f;
     int lim = 0;
     if (i < nq) {
@@ -608,8 +616,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
-      store_row32<ScoreParts<T>>(dp_at, 0, t);
-      store_row32<ScoreParts<T>>(dp_at, 32, t + 32);
+      store_score32<T>(dp_at, 0, t);
+      store_score32<T>(dp_at, 32, t + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores[b]);

@@ -23,7 +23,7 @@ struct ForwardBars {
 // The accumulated row is multiplied down only when the maximum has grown by
 // more than 2^8 since the last time: until then probabilities are up to 2^8
 // fold, which the 32-bit sums hold as well.
-template <typename T, int DP, bool DROP, typename Op>
+template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_forward(const AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (steps[t]) {
           ok = wait(&bars.q[t], 0);
           if (ok && leader) {
-            products<Op, DP>(tmem + t * kTile, q0 + t * kStep, k0);
+            products<T, DP>(tmem + t * kTile, q0 + t * kStep, k0);
             tc::commit(&bars.scores[t]);
           }
         }
@@ -151,12 +151,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (j >= steps[t]) continue;
           const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * DP;
           ok = wait(&bars.probs[t][0], j & 1);
-          if (ok && leader) sums<Op, DP, kTile / 2>(o_at, s_at, v_at, j > 0);
+          if (ok && leader) sums<T, DP, kTile / 2>(o_at, s_at, v_at, j > 0);
           ok = ok && wait(&bars.probs[t][1], j & 1);
           if (ok && leader) {
-            sums<Op, DP, kTile / 2>(o_at, s_at, v_at, true, kTile / 2);
+            sums<T, DP, kTile / 2>(o_at, s_at, v_at, true, kTile / 2);
             if (j + 1 < steps[t]) {
-              products<Op, DP>(s_at, q0 + t * kStep, k_at);
+              products<T, DP>(s_at, q0 + t * kStep, k_at);
               tc::commit(&bars.scores[t]);
             } else {
               tc::commit(&bars.done[t]);
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
               for (int y = 0; y < 4; ++y) s[e + y] = draw_lane(z, y) >= c.drop ? s[e + y] : 0.f;
             }
-          store_parts(s_at + x, s);
-          store_parts(s_at + x + 32, s + 32);
+          store_parts<__half>(s_at + x, s);
+          store_parts<__half>(s_at + x + 32, s + 32);
           tc::wait_stores();
           tc::fence_before();
           tc::bar_arrive_warp(&bars.probs[t][x / 64]);
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             s[x + e] = a.x;
             s[x + e + 1] = a.y;
           } else {
-            p[e / 2] = pack2<Op>(a.x, a.y);
+            p[e / 2] = pack2<T>(a.x, a.y);
           }
         }
         if (DROP) {
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float k[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) k[y] = draw_lane(z, y) >= c.drop ? s[x + e + y] : 0.f;
-            p[e / 2] = pack2<Op>(k[0], k[1]);
-            p[e / 2 + 1] = pack2<Op>(k[2], k[3]);
+            p[e / 2] = pack2<T>(k[0], k[1]);
+            p[e / 2 + 1] = pack2<T>(k[2], k[3]);
           }
         }
         tc::store32(s_at + x, p);
@@ -402,29 +402,29 @@ int64_t tile_forward_blocks(const AttnCall &c) {
          (by_heads ? c.heads / 2 : c.heads);
 }
 
-template <typename T, int DP, bool DROP, typename Op>
+template <typename T, int DP, bool DROP>
 static cudaError_t forward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
-  const auto kern = tile_forward<T, DP, DROP, Op>;
+  const auto kern = tile_forward<T, DP, DROP>;
   constexpr size_t smem = tile_forward_smem<wide<T, DP>()>();
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3((unsigned)tile_forward_blocks(c), (unsigned)c.splits), kTileThreads, smem, false, s, c, m);
 }
 
-template <typename T, typename Op>
+template <typename T>
 static cudaError_t forward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
   if constexpr (!Operand<T>::kSplit)
     if (c.d > 64)
-      return c.drop ? forward_launch<T, 128, true, Op>(c, m, s) : forward_launch<T, 128, false, Op>(c, m, s);
-  return c.drop ? forward_launch<T, 64, true, Op>(c, m, s) : forward_launch<T, 64, false, Op>(c, m, s);
+      return c.drop ? forward_launch<T, 128, true>(c, m, s) : forward_launch<T, 128, false>(c, m, s);
+  return c.drop ? forward_launch<T, 64, true>(c, m, s) : forward_launch<T, 64, false>(c, m, s);
 }
 
 cudaError_t tile_forward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s) {
   TileMaps m = {};
   if (!maps_of(&m, c, type, parts, false)) return cudaErrorInvalidValue;
-  if (type == SNACK_F32) return forward_typed<float, float>(c, m, s);
-  if (type == SNACK_F16) return forward_typed<__half, __half>(c, m, s);
-  return c.made ? forward_typed<__nv_bfloat16, __half>(c, m, s) : forward_typed<__nv_bfloat16, __nv_bfloat16>(c, m, s);
+  return type == SNACK_F32    ? forward_typed<float>(c, m, s)
+         : type == SNACK_BF16 ? forward_typed<__nv_bfloat16>(c, m, s)
+                              : forward_typed<__half>(c, m, s);
 }
 
 cudaError_t tile_forward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }

@@ -33,3 +33,106 @@ def test_the_longest_cache(dtype):
         assert abs(float(lse) - math.log(n)) <= 2.0 ** -20 * math.log(n)
         # half of 2^31 draws: off by some 2^-16 of them
         assert torch.allclose(out.flatten().double(), v[0, 0, 0].double(), rtol=2.0 ** -7 if dtype != F32 else 2.0 ** -12)
+
+
+# ---------------------------------------------------------------- sequences far apart in magnitude
+
+RANGE_TYPES = [BF16]
+
+
+def run(q, k, v, dout, **opts):
+    import coo_spmm_sparse_gb300 as sn
+    out, lse = sn.snack_attention_forward(q, k, v, **opts)
+    return (out, lse, *sn.snack_attention_backward(dout, q, k, v, out, lse, **opts))
+
+
+def same_but_for_powers(got, want, power):
+    """got = want * 2^power, bit for bit; float16 results that are subnormal may round apart."""
+    w = want.double() * 2.0 ** power
+    if got.dtype == F16:
+        assert bool(((got.double() - w).abs() <= 2.0 ** -24 * max(1.0, 2.0 ** power)).all())
+    else:
+        assert torch.equal(got.double(), w)
+
+
+def layouts(d, n, length):
+    """(shape of a side, options, slices of the sequences): dense, padded and ragged; the sizes that
+    take the tiles, and those that do not."""
+    ends = torch.tensor([0, *([length] * n)]).cumsum(0).to(torch.int32).cuda()
+    fill = torch.tensor([length - 37 * i for i in range(n)], dtype=torch.int32).cuda()
+    per = [(i, slice(0, length)) for i in range(n)]
+    return [((n, length), {}, per), ((n, length), dict(q_lengths=fill, k_lengths=fill), per),
+            ((n * length,), dict(q_offsets=ends, k_offsets=ends), [slice(i * length, (i + 1) * length) for i in range(n)])]
+
+
+@pytest.mark.parametrize("dtype", RANGE_TYPES)
+@pytest.mark.parametrize("length,d", [(40, 64), (700, 64), (700, 65), (700, 128), (515, 100)])
+@pytest.mark.parametrize("dropout", [0.0, 0.2])
+def test_a_sequence_does_not_change_with_the_others_magnitudes(dtype, length, d, dropout):
+    """Sequence n's q, k, v and dout times powers of two of its own: its results are those times
+    powers of two, whatever the others are.  (Nothing of a call may be scaled by what another
+    sequence holds; powers of two change no rounding.)"""
+    far = 4 if dtype == F16 else 24
+    for shape, opts, at in layouts(d, 3, length):
+        g = gen(length + d)
+        q, dout = (rnd(g, (*shape, 6, d), dtype) for _ in range(2))
+        k, v = (rnd(g, (*shape, 2, d), dtype) for _ in range(2))
+        opts = dict(opts, dropout=dropout, seed=7)
+        want = run(q, k, v, dout, **opts)
+        for powers in (((0, 0, 0), (far, -far, far // 2), (-far, 0, -far)), ((0, 0, far), (0, far, 0), (far, 0, 0))):
+            x = [t.clone() for t in (q, k, v, dout)]
+            for s, (a, b, c) in zip(at, powers):
+                for t, p in zip(x, (a, -a, b, c)):
+                    t[s] *= 2.0 ** p
+            got = run(*x, **opts)
+            assert torch.equal(got[1], want[1])
+            for s, (a, b, c) in zip(at, powers):
+                for y, w, p in zip((got[0], *got[2:]), (want[0], *want[2:]), (b, b + c - a, b + c + a, c)):
+                    same_but_for_powers(y[s], w[s], p)
+
+
+@pytest.mark.parametrize("dtype", RANGE_TYPES)
+@pytest.mark.parametrize("length,d", [(40, 64), (700, 64), (700, 65), (700, 128)])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_what_is_not_finite_stays_in_its_sequence(dtype, length, d, value):
+    for shape, opts, at in layouts(d, 3, length):
+        g = gen(length + d)
+        x = [rnd(g, (*shape, h, d), dtype) for h in (6, 2, 2, 6)]
+        want = run(*x, **opts)
+        for t in x:
+            t[at[1]][20, 1, 3] = value
+        got = run(*x, **opts)
+        for s in (at[0], at[2]):
+            for y, w in zip((got[0], *got[2:]), (want[0], *want[2:])):
+                assert torch.equal(y[s], w[s])
+
+
+@pytest.mark.parametrize("dtype", RANGE_TYPES)
+@pytest.mark.parametrize("ratio", [2.0 ** -7, 2.0 ** -13, 2.0 ** -17])
+@pytest.mark.parametrize("length,d", [(1100, 64), (1100, 65), (1000, 128), (200, 64)])
+def test_tokens_whose_gradients_lie_far_apart(dtype, ratio, length, d):
+    """dq of a token is linear in its own dout, so that its bound is the bound of a call whose
+    dout are all of one size, times its size.  Keys that only late tokens see have dk and dv
+    bounded by what those tokens bring."""
+    import attention_ref
+    g = gen(d)
+    q, dout = (rnd(g, (1, length, 4, d), dtype) for _ in range(2))
+    k, v = (rnd(g, (1, length, 2, d), dtype) for _ in range(2))
+    flat = attention_ref.attention(q, k, v, dout=dout)
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps  # a step of a subnormal result
+    every = torch.ones(length, device="cuda", dtype=torch.float64)
+    every[1::2] = ratio
+    late = torch.ones_like(every)
+    late[length // 2:] = ratio
+    for size in (every, late):
+        size = size[None, :, None, None]
+        _, _, dq, dk, dv = run(q, k, v, (dout * size.to(dtype)))
+        err = (dq.double() - flat["dq"][0] * size).abs()
+        assert bool((err <= 1.01 * flat["dq"][1] * size + tiny).all()), float((err / (flat["dq"][1] * size)).max())
+    first = (length // 2 + 127) // 128 * 128  # keys from here on: late tokens' only
+    small = dout.clone()
+    small[:, :length // 2] = 0
+    want = attention_ref.attention(q, k, v, dout=small)
+    for name, got in (("dk", dk), ("dv", dv)):
+        ref, bound = (t[:, first:] * ratio for t in want[name])
+        assert bool(((got[:, first:].double() - ref).abs() <= 1.01 * bound + tiny).all()), name
