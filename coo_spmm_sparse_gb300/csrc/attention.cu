@@ -597,7 +597,7 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
 template <typename T>
 cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  const bool peaks = type == SNACK_F16 || (type == SNACK_F32 && p.width);
+  const bool peaks = type == SNACK_F32 && p.width;
   cudaError_t e = peaks ? clear_peaks(&c, workspace, s) : cudaSuccess;
   if (e == cudaSuccess && c.rows) {
     const auto even = [](const Strided &t) {
@@ -609,12 +609,6 @@ cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace,
   if (e != cudaSuccess) return e;
   SplitParts parts = {};
   if (p.width) e = make_parts<T>(&c, p, true, workspace, &parts, s);
-  if (e == cudaSuccess && type == SNACK_F16) {
-    Sources v = sources_of(c, p, workspace);
-    v.t[0] = v.t[2];
-    if (v.t[0].rows)
-      e = launch_kernel(attention_peak<T>, dim3(spread(v.t[0].rows)), 256, 0, false, s, v, c.sequences, c.d);
-  }
   if (e != cudaSuccess) return e;
   // (a float16 call whose dout alone lies badly was not planned for)
   if (p.tiles && (p.width || tiles_read(c))) return tile_backward_launch(c, type, parts, s);

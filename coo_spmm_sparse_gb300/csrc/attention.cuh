@@ -17,7 +17,7 @@ struct AttnCall {
   float *lse;    // [heads][rows]: log of the sum of exp(scale * q . k), -inf where no key is seen
   float *delta;  // [heads][rows]: dout . out
   float *part;   // partial results of a split call
-  const uint32_t *peak;  // bits of the largest |dout|, |v|, |q|, |k| (float16: the first two; bfloat16: none)
+  const uint32_t *peak;  // 32-bit operands that are made: bits of the largest |dout|, |v|, |q|, |k|
   int64_t rows;  // rows of lse for a head: all tokens of q
   int sequences, q_tokens, k_tokens;
   int heads, key_heads, group, d;
@@ -174,14 +174,28 @@ inline int64_t tiles_of(bool ragged, int64_t n, int64_t tokens, int64_t per_toke
   return ragged ? per + n + 2 : n * per;
 }
 
-// float16 holds neither a small gradient's dS nor small probabilities well:
-// the backward kernels take P 2^14 fold there, and dS times the power of two
-// that keeps the largest that |dout| and |v| allow below 2^15.
+// float16 holds neither a small gradient's dS nor small probabilities well: the
+// backward kernels take P 2^14 fold there, and a row's dS (a query's where dq is
+// summed, a key's where dk is) times a power of two of its own, which the row's sums
+// are divided by again.  Nothing of it comes from other rows: with one power for a
+// call, tokens whose dout was 1e-4 of the largest had dq off by 7e-3 in 32 bits.
+//
+// 2^power brings a magnitude with these exponent bits (of a 32-bit float) to
+// [2^top, 2^(top + 1)); a row without one, or one that is not finite, takes `other`.
 constexpr float kHalfP = 14.f;
-__device__ __forceinline__ float half_ds_scale(const AttnCall &c) {
-  const float most = 2.f * (float)c.d * __uint_as_float(c.peak[0]) * __uint_as_float(c.peak[1]) * c.keep_scale;
-  if (!(most > 0.f) || !(most < INFINITY)) return 1.f;
-  return exp2f((float)min(max(14 - ilogbf(most), -100), 100));
+constexpr int kMostPower = 100;
+__device__ __forceinline__ uint32_t exponent_bits(float magnitude) { return __float_as_uint(magnitude) >> 23; }
+__device__ __forceinline__ int row_power(uint32_t exponent, int top, int other) {
+  return exponent == 0 || exponent == 255 ? other : min(max(top + 127 - (int)exponent, -kMostPower), kMostPower);
+}
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }  // |n| <= 126
+
+// The power of a row whose sums stay where they are from step to step: they are
+// multiplied down when a step's largest would pass 2^15.  Sixteen fold room is left,
+// so that this is rare; two float16 parts still reach down to 2^-36 of the largest.
+__device__ __forceinline__ int running_power(int power, uint32_t exponent) {
+  const int need = row_power(exponent, 11, power);
+  return power > need + 3 ? need : power;
 }
 
 // The power of two that brings the largest magnitude to [2^14, 2^15).

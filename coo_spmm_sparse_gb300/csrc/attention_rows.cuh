@@ -472,10 +472,52 @@ __global__ void __launch_bounds__(32 * WM) rows_forward(const AttnCall c) {
 // roundings of the same product differ by.
 // dS is taken in two parts of the type: rounded to it, it made dq and dk 1.6
 // times as far off as the rounding of the results alone.
-template <typename T>
-__device__ __forceinline__ float ds_scale(const AttnCall &c) {
-  if constexpr (!std::is_same<T, __half>::value) return 1.f;
-  return half_ds_scale(c);
+
+// float16: brings a step's dS of a lane's two rows into range and the sums so far to
+// the same power.  The four lanes of a row agree.
+template <typename T, int DP, int NB>
+__device__ __forceinline__ void scale_rows(float (&t)[NB][4], float (&sums)[DP / 8][4], int (&power)[2]) {
+  if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float top = 0.f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) top = fmaxf(top, fmaxf(fabsf(t[n][2 * h]), fabsf(t[n][2 * h + 1])));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int now = running_power(power[h], exponent_bits(top));
+      if (now != power[h]) {
+        const float by = exp2f((float)(now - power[h]));
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n) {
+          sums[n][2 * h] *= by;
+          sums[n][2 * h + 1] *= by;
+        }
+        power[h] = now;
+      }
+      const float up = power_of_two(now);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        t[n][2 * h] *= up;
+        t[n][2 * h + 1] *= up;
+      }
+    }
+  }
+}
+// Takes those powers out again.
+template <typename T, int DP>
+__device__ __forceinline__ void unscale_rows(float (&sums)[DP / 8][4], const int (&power)[2]) {
+  if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float by = power_of_two(-power[h]);
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n) {
+        sums[n][2 * h] *= by;
+        sums[n][2 * h + 1] *= by;
+      }
+    }
+  }
 }
 
 template <typename T, int DP, int WM, int WN, int BQ, int ST>
@@ -509,10 +551,10 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
   const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, kh * G, G, c.d);
   const Rows<T> dr(c.dout, qs, c.q_offsets != nullptr, kh * G, G, c.d);
   const uint64_t seed = c.drop ? c.draws() : 0;
-  const float ds = ds_scale<T>(c), p_up = std::is_same<T, __half>::value ? kHalfP : 0.f;
-  const float ds_by_p = ds * exp2f(-p_up);
+  const float p_up = std::is_same<T, __half>::value ? kHalfP : 0.f, p_down = exp2f(-p_up);
 
   float dk[DP / 8][4] = {}, dv[DP / 8][4] = {};
+  int power[2] = {kMostPower, kMostPower};
   const auto copy_step = [&](int stage, int row0) {
     T *q = sqd + stage * 2 * STEP * kLd;
     copy_rows<T, DP>(q, qr, row0, STEP, end);
@@ -581,10 +623,11 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
             float mult = 1.f;
             if (c.drop)
               mult = draw_lane(dropout_draw(s_draw[stage][i], j), j & 3) >= c.drop ? c.keep_scale : 0.f;
-            t[n][x] = seen && lim > 1 ? prob * ((t[n][x] * mult - delta) * ds_by_p) : 0.f;
+            t[n][x] = seen && lim > 1 ? prob * ((t[n][x] * mult - delta) * p_down) : 0.f;
             p[n][x] = mult != 0.f ? prob : 0.f;
           }
         }
+      scale_rows<T, DP>(t, dk, power);
       Ops::template sums_by_rows<NB>(dv, p, d, lane);
       Ops::template sums_by_rows<NB, true>(dk, t, q, lane);
     }
@@ -597,6 +640,7 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
     }
   }
   copies_wait<0>();
+  unscale_rows<T, DP>(dk, power);
   if constexpr (WN > 1) {
     add_shares<DP, WM, WN>(dv, reinterpret_cast<float *>(smem), wm, wn, lane);
     add_shares<DP, WM, WN>(dk, reinterpret_cast<float *>(smem), wm, wn, lane);
@@ -609,8 +653,8 @@ __device__ __forceinline__ void keys_of_rows(const AttnCall &c, int block) {
     const auto row = [&](const Strided &s) {
       return static_cast<T *>(s.p) + (c.k_offsets ? (ks.row + j) * s.token : ks.seq * s.seq + j * s.token) + kh * s.head;
     };
-    if (c.dk.p) store_row<T, DP>(row(c.dk), dk, h, c.scale / ds, c.d, lane);
-    if (c.dv.p) store_row<T, DP>(row(c.dv), dv, h, exp2f(-p_up) * c.keep_scale, c.d, lane);
+    if (c.dk.p) store_row<T, DP>(row(c.dk), dk, h, c.scale, c.d, lane);
+    if (c.dv.p) store_row<T, DP>(row(c.dv), dv, h, p_down * c.keep_scale, c.d, lane);
   }
 }
 
@@ -635,7 +679,6 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
   const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, kh * G, G, c.d);
   const Rows<T> dr(c.dout, qs, c.q_offsets != nullptr, kh * G, G, c.d);
   const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
-  const float ds = ds_scale<T>(c);
 
   int token[2], head[2], lim[2];
   float lse[2], delta[2];
@@ -658,6 +701,7 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
   }
 
   float dq[DP / 8][4] = {};
+  int power[2] = {kMostPower, kMostPower};
   const auto copy_step = [&](int stage, int key0) {
     T *k = skv + stage * 2 * STEP * kLd;
     copy_rows<T, DP>(k, kr, key0, STEP, end);
@@ -693,9 +737,10 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
             const int je = key + Ops::column(n, lane, e), x = 2 * h + e;
             const float mult = !c.drop ? 1.f : (draw_lane(z, je & 3) >= c.drop ? c.keep_scale : 0.f);
             t[n][x] = je < lim[h] && lim[h] > 1
-                          ? exp2f(p[n][x] * c.scale_log2 - lse[h]) * ((t[n][x] * mult - delta[h]) * ds) : 0.f;
+                          ? exp2f(p[n][x] * c.scale_log2 - lse[h]) * (t[n][x] * mult - delta[h]) : 0.f;
           }
         }
+      scale_rows<T, DP>(t, dq, power);
       Ops::template sums_by_rows<NB, true>(dq, t, k, lane);
     }
     __syncthreads();
@@ -705,6 +750,7 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
     }
   }
   copies_wait<0>();
+  unscale_rows<T, DP>(dq, power);
   if constexpr (WN > 1) {
     add_shares<DP, WM, WN>(dq, reinterpret_cast<float *>(smem), wm, wn, lane);
     if (wn != 0) return;
@@ -715,7 +761,7 @@ __device__ __forceinline__ void queries_of_rows(const AttnCall &c, int block) {
     T *row = static_cast<T *>(c.dq.p) +
              (c.q_offsets ? (qs.row + token[h]) * c.dq.token : qs.seq * c.dq.seq + token[h] * c.dq.token) +
              head[h] * c.dq.head;
-    store_row<T, DP>(row, dq, h, c.scale / ds, c.d, lane);
+    store_row<T, DP>(row, dq, h, c.scale, c.d, lane);
   }
 }
 

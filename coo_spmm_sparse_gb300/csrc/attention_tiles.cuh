@@ -212,16 +212,16 @@ __device__ __forceinline__ void store_parts(uint32_t at, const float *v) {
   tc::store16(at + 16, lo);
 }
 
-// o += N columns of tensor memory.
+// o += N columns of tensor memory times a factor.
 template <int N>
-__device__ __forceinline__ void add_sums(float *o, uint32_t from) {
+__device__ __forceinline__ void add_sums(float *o, uint32_t from, float by) {
 #pragma unroll
   for (int c = 0; c < N; c += 32) {
     float v[32];
     tc::load32(from + c, v);
     tc::wait_loads();
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[c + e] += v[e];
+    for (int e = 0; e < 32; ++e) o[c + e] = fmaf(v[e], by, o[c + e]);
   }
 }
 

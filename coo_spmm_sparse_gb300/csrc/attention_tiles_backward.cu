@@ -40,14 +40,49 @@ __device__ __forceinline__ void score_sums(uint32_t d, uint32_t a, uint32_t b, b
 }
 
 // float16 operands hold neither small probabilities nor small gradients of scores:
-// they are taken times powers of two.  bfloat16 has the range of 32 bits.
+// they are taken times powers of two (attention.cuh).  bfloat16 has the range of 32
+// bits.
 template <typename T>
 constexpr bool kScaled = !std::is_same<T, __nv_bfloat16>::value;
 template <typename T>
 constexpr float kUp = kScaled<T> ? kHalfP : 0.f;  // the power of the probabilities
-template <typename T>
-__device__ __forceinline__ float ds_scale(const AttnCall &c) {
-  return kScaled<T> ? half_ds_scale(c) : 1.f;
+
+// The two warps that have a row's 64 columns each tell one another the exponents of
+// their largest gradients of scores.
+struct Tops {
+  uint64_t told[4];  // a pair of warps each
+  uint8_t exponent[2][2][kTile];
+};
+// The row's, of step n; false: the wait has run out.  Whole warps.
+__device__ __forceinline__ bool row_exponent(Tops &tops, const float (&t)[kHalf], int n, uint32_t *exponent,
+                                             volatile int *failed) {
+  const int warp = threadIdx.x >> 5, w = warp >> 2, pair = warp & 3, row = pair * 32 + (threadIdx.x & 31);
+  float top[2] = {};
+#pragma unroll
+  for (int x = 0; x < kHalf; x += 4) {
+    top[0] = tc::max3(top[0], fabsf(t[x]), fabsf(t[x + 1]));
+    top[1] = tc::max3(top[1], fabsf(t[x + 2]), fabsf(t[x + 3]));
+  }
+  *exponent = exponent_bits(fmaxf(top[0], top[1]));
+  tops.exponent[n & 1][w][row] = (uint8_t)*exponent;
+  tc::bar_arrive_warp(&tops.told[pair]);
+  if (!__all_sync(0xffffffffu, tc::bar_wait(&tops.told[pair], n & 1, failed))) return false;
+  *exponent = max(*exponent, (uint32_t)tops.exponent[n & 1][w ^ 1][row]);
+  return true;
+}
+
+// N columns of tensor memory times a factor.  Whole warps.
+template <int N>
+__device__ __forceinline__ void multiply_sums(uint32_t at, float by) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    float v[32];
+    tc::load32(at + c, v);
+    tc::wait_loads();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] *= by;
+    tc::store32(at + c, reinterpret_cast<const uint32_t *>(v));
+  }
 }
 
 // ------------------------------------------------------------------ keys and values
@@ -59,6 +94,7 @@ struct KeyBars {
   int failed;
   alignas(16) float lse[2][kTile];
   alignas(16) float delta[2][kTile];
+  Tops tops;
 };
 
 template <int W>
@@ -88,6 +124,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // barriers, tensor memory and the block's place are made ready side by side
   if (warp == kCopyWarp && lane == 0) {
     tc::bar_init(&bars.kv, 2);
+    for (int i = 0; i < 4; ++i) tc::bar_init(&bars.tops.told[i], 2);
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&bars.q_full[i], 1);
       tc::bar_init(&bars.q_empty[i], 1);
@@ -238,7 +275,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           bars.lse[slot][lane + 32 * x] = up - lse[x];  // as they are added
-          bars.delta[slot][lane + 32 * x] = -delta[x];
+          bars.delta[slot][lane + 32 * x] = -delta[x] * exp2f(-up);
         }
         tc::bar_arrive_warp(&bars.stat_full[slot]);
       }
@@ -248,12 +285,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int w = warp >> 2, j = j0 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
-    const float ds = ds_scale<T>(c);
     const Scales by = scales_of(c);
     const float2 cs2 = make_float2(by.scores, by.scores);
-    const float ds_by_p = ds * exp2f(-kUp<T>);
+    const float dprobs = by.dprobs * exp2f(-kUp<T>);  // (times probabilities that are that power up)
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
-    constexpr int kDpChunk = kSplit ? 32 : kHalf;  // what registers leave room for
+    int power = kSplit ? 0 : kMostPower;  // of the row's dS: split, of the last step's; else of its sums
     const bool alone = nk == 1 || (c.causal && j0 == 0 && (warp & 3) == 0);
     const uint64_t seed = DROP ? c.draws() : 0;
     bool ok = true;
@@ -280,7 +316,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
-        if (w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile);  // dV of the tile before
+        if (w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile, 1.f);  // dV of the tile before
       float p[kHalf];
       tc::load32(s_at, p);
       tc::load32(s_at + 32, p + 32);
@@ -315,41 +351,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
-        if (!w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + DP);  // dK of the tile before
+        if (!w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + DP, power_of_two(-power));  // dK of the tile before
 #pragma unroll
-      for (int c0 = 0; c0 < kHalf; c0 += kDpChunk) {
-        float t[kDpChunk];
-#pragma unroll
-        for (int x = 0; x < kDpChunk; x += 32) tc::load32(dp_at + c0 + x, t + x);
+      for (int c0 = 0; c0 < kHalf; c0 += 32) {  // dS takes the probabilities' place
+        float t[32];
+        tc::load32(dp_at + c0, t);
         tc::wait_loads();
 #pragma unroll
-        for (int x = 0; x < kDpChunk; x += 4) {
+        for (int x = 0; x < 32; x += 4) {
           const float4 d = *reinterpret_cast<const float4 *>(&bars.delta[slot][w * kHalf + c0 + x]);
           float v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            v[y] = t[x + y] * by.dprobs;
+            v[y] = t[x + y] * dprobs;
             if (DROP) v[y] = kept[y] >> (c0 + x) & 1 ? v[y] * c.keep_scale : 0.f;
           }
           const float2 u0 = tc::add2(make_float2(v[0], v[1]), make_float2(d.x, d.y));
           const float2 u1 = tc::add2(make_float2(v[2], v[3]), make_float2(d.z, d.w));
-          float2 r0 = tc::mul2(make_float2(p[c0 + x], p[c0 + x + 1]), u0);
-          float2 r1 = tc::mul2(make_float2(p[c0 + x + 2], p[c0 + x + 3]), u1);
-          r0 = tc::mul2(r0, make_float2(ds_by_p, ds_by_p));
-          r1 = tc::mul2(r1, make_float2(ds_by_p, ds_by_p));
-          t[x] = r0.x;
-          t[x + 1] = r0.y;
-          t[x + 2] = r1.x;
-          t[x + 3] = r1.y;
+          const float2 r0 = tc::mul2(make_float2(p[c0 + x], p[c0 + x + 1]), u0);
+          const float2 r1 = tc::mul2(make_float2(p[c0 + x + 2], p[c0 + x + 3]), u1);
+          p[c0 + x] = r0.x;
+          p[c0 + x + 1] = r0.y;
+          p[c0 + x + 2] = r1.x;
+          p[c0 + x + 3] = r1.y;
         }
-        if (alone) {  // queries that see one key: P = 1 whatever the score, dS is zero
-#pragma unroll
-          for (int x = 0; x < kDpChunk; ++x)
-            if (nk == 1 || (j == 0 && q0 + c0 + x == nq - nk)) t[x] = 0.f;
-        }
-#pragma unroll
-        for (int x = 0; x < kDpChunk; x += 32) store_score32<T>(dp_at, c0 + x, t + x);
       }
+      if (alone) {  // queries that see one key: P = 1 whatever the score, dS is zero
+#pragma unroll
+        for (int x = 0; x < kHalf; ++x)
+          if (nk == 1 || (j == 0 && q0 + x == nq - nk)) p[x] = 0.f;
+      }
+      if constexpr (kScaled<T>) {
+        uint32_t exponent;
+        ok = row_exponent(bars.tops, p, n, &exponent, failed);
+        if (!ok) break;
+        if constexpr (kSplit) {
+          power = row_power(exponent, 14, 0);
+        } else {  // (the sums so far are complete: these dP come after them)
+          const int now = running_power(power, exponent);
+          if (n > 0 && __any_sync(0xffffffffu, now != power))
+            multiply_sums<DP / 2>(tmem + lanes + 2 * kTile + DP + w * (DP / 2), exp2f((float)(now - power)));
+          power = now;
+        }
+        const float up = power_of_two(power);
+#pragma unroll
+        for (int x = 0; x < kHalf; ++x) p[x] *= up;
+      }
+      store_score32<T>(dp_at, 0, p);
+      store_score32<T>(dp_at, 32, p + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores);
@@ -365,11 +414,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j < ks.cover)
         row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
               kh * to.head;
-      const float factor = w ? exp2f(-kUp<T>) * c.keep_scale * by.dout : c.scale / ds * by.q;
+      float factor = w ? exp2f(-kUp<T>) * c.keep_scale * by.dout : c.scale * by.q;
       if constexpr (kSplit) {
-        if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP));
+        if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP), w ? 1.f : power_of_two(-power));
         store_floats<DP>(row, acc, factor, c.d, j >= nk);
       } else {
+        if (kScaled<T> && !w) factor *= power_of_two(-power);
         store_sums<T, DP>(tmem + lanes + 2 * kTile + (w ? 0 : DP), row, factor, c.d, all > 0, j >= nk);
       }
     }
@@ -390,6 +440,7 @@ struct QueryBars {
   uint64_t scores[2], read[2], dprobs[2], dscores[2], done, cut, drain;
   uint32_t tmem;
   int failed;
+  Tops tops;
 };
 
 template <int W>
@@ -414,6 +465,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == kCopyWarp && lane == 0) {
     tc::bar_init(&bars.qd, 2);
+    for (int i = 0; i < 4; ++i) tc::bar_init(&bars.tops.told[i], 2);
     for (int i = 0; i < 3; ++i) {
       tc::bar_init(&bars.k_full[i], 1);
       tc::bar_init(&bars.k_empty[i], 1);
@@ -549,7 +601,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::take_registers<kRowRegisters>();
     const int w = warp >> 2, i = i0 + (warp & 3) * 32 + lane;
     const uint32_t at_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const float ds = ds_scale<T>(c);
     float lse = 0.f, delta = 0.f;
     int lim = 0;
     if (i < nq) {
@@ -564,6 +615,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     const Scales by = scales_of(c);
     float acc[kSplit ? DP / 2 : 1] = {};  // split: the sums of this warpgroup's half of the columns
+    int power = kSplit ? 0 : kMostPower, power_before = 0;  // of the row's dS: split, of the last two steps'; else of its sums
     const float2 cs2 = make_float2(by.scores, by.scores), off2 = make_float2(-lse, -lse);
     const float2 delta2 = make_float2(-delta, -delta);
     const uint64_t draw = DROP ? dropout_row(c.draws(), qs.row + i, c.heads, head) : 0;
@@ -574,7 +626,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
-        if (n > 1) add_sums<DP / 2>(acc, at_lane + 3 * kTile + b * DP + w * (DP / 2));  // of two tiles before
+        if (n > 1)  // of two tiles before
+          add_sums<DP / 2>(acc, at_lane + 3 * kTile + b * DP + w * (DP / 2), power_of_two(-power_before));
       const uint32_t s_at = at_lane + 2 * n % 3 * kTile + w * kHalf, dp_at = at_lane + (2 * n + 1) % 3 * kTile + w * kHalf;
       float p[kHalf];
       tc::load32(s_at, p);
@@ -608,7 +661,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int x = 0; x < kHalf; x += 2) {
         float2 a = tc::fma2(make_float2(t[x], t[x + 1]), make_float2(by.dprobs, by.dprobs), delta2);
-        a = tc::mul2(a, make_float2(ds, ds));
         a = tc::mul2(a, make_float2(p[x], p[x + 1]));
         t[x] = a.x;
         t[x + 1] = a.y;
@@ -616,6 +668,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
+      if constexpr (kScaled<T>) {
+        uint32_t exponent;
+        ok = row_exponent(bars.tops, t, n, &exponent, failed);
+        if (!ok) break;
+        if constexpr (kSplit) {
+          power_before = power;
+          power = row_power(exponent, 14, 0);
+        } else {
+          const int now = running_power(power, exponent);
+          if (n > 0 && __any_sync(0xffffffffu, now != power)) {  // once the sums so far are complete
+            ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[(n - 1) % 3], ((n - 1) / 3) & 1, failed));
+            if (!ok) break;
+            tc::fence_after();
+            multiply_sums<DP / 2>(at_lane + 3 * kTile + w * (DP / 2), exp2f((float)(now - power)));
+          }
+          power = now;
+        }
+        const float up = power_of_two(power);
+#pragma unroll
+        for (int x = 0; x < kHalf; ++x) t[x] *= up;
+      }
       store_score32<T>(dp_at, 0, t);
       store_score32<T>(dp_at, 32, t + 32);
       tc::wait_stores();
@@ -633,10 +706,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         row = static_cast<T *>(c.dq.p) +
               (c.q_offsets ? (qs.row + i) * c.dq.token : qs.seq * c.dq.seq + i * c.dq.token) + head * c.dq.head + from;
       if constexpr (kSplit) {
-        for (int n = max(0, all - 2); n < all; ++n) add_sums<DP / 2>(acc, at_lane + 3 * kTile + (n & 1) * DP + from);
-        store_floats<DP / 2>(row, acc, c.scale / ds * by.k, c.d - from, lim == 0);
+        for (int n = max(0, all - 2); n < all; ++n)
+          add_sums<DP / 2>(acc, at_lane + 3 * kTile + (n & 1) * DP + from,
+                           power_of_two(n == all - 1 ? -power : -power_before));
+        store_floats<DP / 2>(row, acc, c.scale * by.k, c.d - from, lim == 0);
       } else {
-        store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, c.scale / ds * by.k, c.d - from, all > 0, lim == 0);
+        const float factor = kScaled<T> ? c.scale * power_of_two(-power) : c.scale;
+        store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, factor, c.d - from, all > 0, lim == 0);
       }
     }
     tc::fence_before();

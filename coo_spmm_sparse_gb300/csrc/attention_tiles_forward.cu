@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
         if (!ok) break;
         tc::fence_after();
-        if (j > 0) add_sums<DP>(o, o_at);  // of the tile before: complete when these scores are
+        if (j > 0) add_sums<DP>(o, o_at, 1.f);  // of the tile before: complete when these scores are
         const int left = lim - j * kTile;  // keys of this tile that the row sees
         const bool cut = __any_sync(0xffffffffu, left < kTile);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (ok && steps[t]) {
         ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));
         tc::fence_after();
-        if (ok) add_sums<DP>(o, o_at);
+        if (ok) add_sums<DP>(o, o_at, 1.f);
       }
       if (ok && i < qs.cover) {
         float *const row = c.splits > 1 ? c.part + slot * c.d

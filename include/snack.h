@@ -502,12 +502,11 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
  * operands in one type.  32-bit calls of some size (head_size up to 64, see
  * attention.cu) take each operand as two float16 parts of the tensor times a
  * power of two: 22 bits of what lies above 2^-17 of the tensor's largest
- * element, and nothing more than 2^-39 of that off.  Gradients of scores and
- * probabilities are split the same way: in 32-bit calls and in float16 calls of
- * such size a term dS[i][j] is never more than 2^-38 of
- * 2 * head_size * max|dout| * max|v| / (1 - dropout) off by that.  In 16-bit types
- * the gradients of scores are taken in two parts of the type; bfloat16's have no
- * such bound.  An infinite or NaN element inside a sequence may reach results that
+ * element, and nothing more than 2^-39 of that off; probabilities are split the same
+ * way, 2^14 fold.  Gradients of scores are taken in two parts in every type, in
+ * float16 parts times a power of two of their own row (a query's for dq, a key's for
+ * dk): off by 2^-22 of themselves and 2^-36 of the row's largest, whatever other rows
+ * hold.  An infinite or NaN element inside a sequence may reach results that
  * do not depend on it, in bfloat16 those of the same sequence alone.
  * Limits: 1 <= head_size <= 128, heads <= 65536, ragged sides of at most 65536
  * sequences; tokens, and q_tokens * (heads / key_heads), below 2^31 - 4096.
