@@ -35,34 +35,19 @@ __device__ __forceinline__ bool in_sequence(const int32_t *offsets, const int32_
   return !lengths || *token < lengths[*seq];
 }
 
-// One atomic maximum a block, and none where the peak is as large already: an
-// atomic for every warp of a grid on one address took longer than the reads.
-__device__ __forceinline__ void block_peak(float v, uint32_t *peak) {
-  __shared__ uint32_t tops[8];
-  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v));  // magnitudes: their bits order as they do
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t most = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) most = max(most, tops[w]);
-    if (most > *const_cast<volatile uint32_t *>(peak)) atomicMax(peak, most);
-  }
-}
 __device__ __forceinline__ float larger(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(fabsf(b))));
 }
 
-// delta = dout . out for every row and head; with `peak` also the largest
-// |dout|.  A team of lanes takes a row with one 16-byte load of each tensor a
+// delta = dout . out for every row and head.  A team of lanes takes a row with one 16-byte load of each tensor a
 // lane, and kItems rows at a time, whose loads are in flight together.
 constexpr int kItems = 4;
 template <typename T, int TEAM, bool VEC>
-__global__ void __launch_bounds__(256) attention_delta(const AttnCall c, uint32_t *peak) {
+__global__ void __launch_bounds__(256) attention_delta(const AttnCall c) {
   constexpr int E = 16 / sizeof(T), kTeams = 256 / TEAM;
   const int lane = threadIdx.x % TEAM;
   const int64_t first = (int64_t)blockIdx.x * (kTeams * kItems) + threadIdx.x / TEAM;
-  float sum[kItems] = {}, top = 0.f;
+  float sum[kItems] = {};
   int64_t place[kItems];
   uint4 x[kItems], y[kItems];
 #pragma unroll
@@ -83,11 +68,7 @@ __global__ void __launch_bounds__(256) attention_delta(const AttnCall c, uint32_
         y[i] = *reinterpret_cast<const uint4 *>(o + lane * E);
       }
     } else {
-      for (int col = lane; col < c.d; col += TEAM) {
-        const float v = to_float(d[col]);
-        sum[i] += v * to_float(o[col]);
-        top = larger(top, v);
-      }
+      for (int col = lane; col < c.d; col += TEAM) sum[i] += to_float(d[col]) * to_float(o[col]);
     }
   }
 #pragma unroll
@@ -97,16 +78,12 @@ __global__ void __launch_bounds__(256) attention_delta(const AttnCall c, uint32_
       unpack16<T>(x[i], a);
       unpack16<T>(y[i], b);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        sum[i] += a[e] * b[e];
-        top = larger(top, a[e]);
-      }
+      for (int e = 0; e < E; ++e) sum[i] += a[e] * b[e];
     }
 #pragma unroll
     for (int o = TEAM / 2; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
     if (place[i] >= 0 && lane == 0) c.delta[place[i]] = sum[i];
   }
-  if (peak) block_peak(top, peak);
 }
 
 // 16 bytes of elements from v on, of which `left` are there.
@@ -134,11 +111,10 @@ __device__ __forceinline__ uint4 load_vector(const T *v, int left) {
 // and a work of 400000; above it delta is of out: at 8 x 24 tokens 1.3 times.
 constexpr int kFewKeys = 32;
 template <typename T>
-__global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c, uint32_t *peak) {
+__global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c) {
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), row = item / c.heads;
   const int head = (int)(item - row * c.heads), kh = head / c.group;
-  float top = 0.f;
   int seq = 0, token = 0;
   if (row < c.rows && in_sequence(c.q_offsets, c.q_lengths, c.sequences, c.q_tokens, row, &seq, &token)) {
     const T *const q = static_cast<const T *>(c.q.p) + seq * c.q.seq + token * c.q.token + head * c.q.head;
@@ -159,12 +135,6 @@ __global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c
     const int seen = seen_keys(c.causal, i, qs.valid, ks.valid);
     float term = 0.f;
     constexpr int E = 16 / sizeof(T);
-    for (int col = lane * E; col < c.d; col += 32 * E) {
-      float g[E];
-      unpack16<T>(load_vector(d + col, c.d - col), g);
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = larger(top, g[e]);
-    }
     for (int j = lane; j < seen; j += 32) {
       const int64_t at = c.k_offsets ? ks.row + j : j;
       const T *const k = static_cast<const T *>(c.k.p) + ks.seq * c.k.seq + at * c.k.token + kh * c.k.head;
@@ -193,7 +163,6 @@ __global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c
     const float delta = warp_sum(term);
     if (lane == 0) c.delta[place] = delta;
   }
-  if (peak) block_peak(top, peak);
 }
 
 // What that kernel reads, in products.  A causal call's rows before its last
@@ -208,18 +177,17 @@ inline double few_keys_work(const AttnCall &c) {
 }
 
 template <typename T>
-cudaError_t delta_launch(const AttnCall &c, bool vec, uint32_t *peak, cudaStream_t s) {
+cudaError_t delta_launch(const AttnCall &c, bool vec, cudaStream_t s) {
   if (sizeof(T) == 2 && c.k_tokens <= kFewKeys && few_keys_work(c) <= kFewKeysWork)
-    return launch_kernel(attention_delta_few_keys<T>, dim3((unsigned)((c.rows * c.heads + 7) / 8)), 256, 0, false, s, c,
-                         peak);
+    return launch_kernel(attention_delta_few_keys<T>, dim3((unsigned)((c.rows * c.heads + 7) / 8)), 256, 0, false, s, c);
   const int lanes = vec ? (c.d * (int)sizeof(T) + 15) / 16 : 32;
   const int team = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const int64_t each = 256 / team * kItems;
   const dim3 grid((unsigned)((c.rows * c.heads + each - 1) / each));
-  if (!vec) return launch_kernel(attention_delta<T, 32, false>, grid, 256, 0, false, s, c, peak);
-  return team == 8    ? launch_kernel(attention_delta<T, 8, true>, grid, 256, 0, false, s, c, peak)
-         : team == 16 ? launch_kernel(attention_delta<T, 16, true>, grid, 256, 0, false, s, c, peak)
-                      : launch_kernel(attention_delta<T, 32, true>, grid, 256, 0, false, s, c, peak);
+  if (!vec) return launch_kernel(attention_delta<T, 32, false>, grid, 256, 0, false, s, c);
+  return team == 8    ? launch_kernel(attention_delta<T, 8, true>, grid, 256, 0, false, s, c)
+         : team == 16 ? launch_kernel(attention_delta<T, 16, true>, grid, 256, 0, false, s, c)
+                      : launch_kernel(attention_delta<T, 32, true>, grid, 256, 0, false, s, c);
 }
 
 // One tensor of a call and what is made of it.
@@ -228,8 +196,8 @@ struct Source {
   const int32_t *offsets, *lengths;
   int tokens, heads;
   int64_t rows;    // tokens of all sequences
-  uint32_t *peak;  // receives the bits of the largest magnitude
   void *made;      // receives what the tiles read
+  int32_t *power;  // 32 bits: and the powers of two of its tiles
 };
 struct Sources {
   Source t[4];
@@ -245,57 +213,18 @@ __device__ __forceinline__ bool token_of(const Source &t, int sequences, int64_t
   return have;
 }
 
-// The largest magnitude of each tensor, over the sequences' tokens.  Heads that
-// lie end to end are read as one row.  Grid: y = tensor.
-template <typename T>
-__global__ void __launch_bounds__(256) attention_peak(const Sources all, int sequences, int d) {
-  constexpr int E = 16 / sizeof(T), kAhead = 6;
-  const Source &t = all.t[blockIdx.y];
-  const bool flat = t.from.head == d || t.heads == 1;
-  const int lane = threadIdx.x & 31, heads = flat ? 1 : t.heads, width = flat ? t.heads * d : d;
-  float top = 0.f;
-  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
-    int64_t at;
-    if (!token_of(t, sequences, row, &at)) continue;
-    for (int head = 0; head < heads; ++head) {
-      const T *const v = static_cast<const T *>(t.from.p) + at + head * t.from.head;
-      for (int col = lane * E; col < width; col += 32 * E * kAhead) {
-        uint4 u[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int c = col + i * 32 * E;
-          u[i] = c < width ? load_vector(v + c, width - c) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          float x[E];
-          unpack16<T>(u[i], x);
-#pragma unroll
-          for (int e = 0; e < E; ++e) top = larger(top, x[e]);
-        }
-      }
-    }
-  }
-  block_peak(top, t.peak);
-}
-
-// Every tensor as TMA can bring it: rows of W columns of each head (zeros behind the
-// head size and for tokens outside every sequence).  16-bit types as they are.
-// 32-bit floats as two float16 parts, 64 high and 64 low halves, of the elements
-// times the power of two that brings the tensor's largest to [2^14, 2^15).  Grid: y =
-// tensor.
+// 16-bit tensors as TMA can bring them: rows of W columns of each head, zeros behind
+// the head size and for tokens outside every sequence.  Grid: y = tensor.
 template <typename T, int W>
-__global__ void __launch_bounds__(256) tile_operands(const Sources all, int sequences, int d) {
-  constexpr bool kSplit = sizeof(T) == 4;
-  constexpr int E = 16 / sizeof(T), kPlaces = (kSplit ? W / 2 : W) / E, kAhead = 4;
+__global__ void __launch_bounds__(256) copy_operands(const Sources all, int sequences, int d) {
+  constexpr int E = 16 / sizeof(T), kPlaces = W / E, kAhead = 4;
   const Source &t = all.t[blockIdx.y];
   const int lane = threadIdx.x & 31, work = t.heads * kPlaces;
-  const float by = kSplit ? exp2f((float)power_to_half(*t.peak)) : 1.f;
   for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < t.rows; row += (int64_t)gridDim.x * 8) {
     int64_t at;
     const bool have = token_of(t, sequences, row, &at);
     const T *const v = static_cast<const T *>(t.from.p) + at;
-    uint16_t *const made = static_cast<uint16_t *>(t.made) + row * t.heads * W;
+    uint4 *const made = static_cast<uint4 *>(t.made) + row * work;
     for (int i0 = lane; i0 < work; i0 += 32 * kAhead) {
       uint4 u[kAhead];
 #pragma unroll
@@ -304,29 +233,64 @@ __global__ void __launch_bounds__(256) tile_operands(const Sources all, int sequ
         u[n] = have && i < work && col < d ? load_vector(v + head * t.from.head + col, d - col) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int n = 0; n < kAhead; ++n) {
-        const int i = i0 + n * 32, head = i / kPlaces, col = i % kPlaces * E;
-        if (i >= work) break;
-        uint16_t *const to = made + head * W + col;
-        if constexpr (kSplit) {
-          float x[E];
-          unpack16<T>(u[n], x);
-          uint32_t hi[E / 2], lo[E / 2];
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            float a, b;
-            const float l = x[2 * e] * by, r = x[2 * e + 1] * by;
-            hi[e] = pack2<__half>(l, r);
-            unpack2<__half>(hi[e], a, b);
-            lo[e] = pack2<__half>(l - a, r - b);
-          }
-          *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2 *>(to + W / 2) = make_uint2(lo[0], lo[1]);
-        } else {
-          *reinterpret_cast<uint4 *>(to) = u[n];
-        }
-      }
+      for (int n = 0; n < kAhead; ++n)
+        if (i0 + n * 32 < work) made[i0 + n * 32] = u[n];
     }
+  }
+}
+
+// 32-bit tensors as two float16 parts, rows of 64 high and 64 low halves (zeros as
+// above), of the elements times the power of two that brings the largest of their
+// tile to [2^14, 2^15).  A block takes a tile of a head, which stays in registers
+// from the search for its largest on: the memory is read once.  Grid: x = tile * heads +
+// head, y = tensor.
+__global__ void __launch_bounds__(256) split_operands(const Sources all, int sequences, int d) {
+  __shared__ uint32_t tops[8];
+  const Source &t = all.t[blockIdx.y];
+  const int head = blockIdx.x % t.heads;
+  const Place at = find_tile(t.offsets, sequences, t.tokens, 1, kTile, blockIdx.x / t.heads, false);
+  if (at.s < 0) return;
+  const Span sp = own_span(t.offsets, t.lengths, at.s, sequences, t.tokens);
+  constexpr int kRows = kTile / 16;  // of a thread; 16 threads take a row
+  const int col = threadIdx.x % 16 * 4, first = at.tile * kTile + threadIdx.x / 16;
+  const float *const from = static_cast<const float *>(t.from.p) +
+                            (t.offsets ? sp.row * t.from.token : sp.seq * t.from.seq) + head * t.from.head + col;
+  float x[kRows][4], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = first + 16 * i;
+    const uint4 u = row < sp.valid && col < d ? load_vector(from + row * t.from.token, d - col) : make_uint4(0, 0, 0, 0);
+    unpack16<float>(u, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = larger(top, x[i][e]);
+  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // magnitudes: their bits order as they do
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) most = max(most, tops[w]);
+  const int power = power_to_half(most);
+  if (threadIdx.x == 0) t.power[(sp.tile + at.tile) * t.heads + head] = power;
+  const float by = power_of_two(power);
+  uint16_t *const made = static_cast<uint16_t *>(t.made) + head * 128 + col;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = first + 16 * i;
+    if (row >= sp.cover) break;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float a, b;
+      const float l = x[i][2 * e] * by, r = x[i][2 * e + 1] * by;
+      hi[e] = pack2<__half>(l, r);
+      unpack2<__half>(hi[e], a, b);
+      lo[e] = pack2<__half>(l - a, r - b);
+    }
+    uint16_t *const to = made + (sp.row + row) * t.heads * 128;
+    *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2 *>(to + 64) = make_uint2(lo[0], lo[1]);
   }
 }
 
@@ -369,8 +333,6 @@ __global__ void __launch_bounds__(128) join_splits(const AttnCall c) {
 
 int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
-constexpr int64_t kTileRows = 128;  // of the tiles' kernels
-
 bool dense_or_ragged(const int32_t *offsets, const int32_t *lengths) { return !(offsets && lengths); }
 
 snack_status bad(const std::string &m) { return refuse(SNACK_ERR_INVALID_ARG, m); }
@@ -405,7 +367,7 @@ snack_status check_args(const snack_attention_args *a) {
   if (a->sequences > (1 << 16) && (a->q_offsets || a->k_offsets))
     return refuse(SNACK_ERR_UNSUPPORTED, "a ragged side takes at most 2^16 sequences");  // every block looks for its own
   if (tiles(a->q_offsets, a->q_tokens, group) + tiles(a->k_offsets, a->k_tokens, 1) >= lim ||
-      tiles_of(a->q_offsets != nullptr, a->sequences, a->q_tokens, 1, kTileRows) * a->heads >= lim ||
+      tiles_of(a->q_offsets != nullptr, a->sequences, a->q_tokens, 1, kTile) * a->heads >= lim ||
       rows * a->heads >= lim * 4)
     return refuse(SNACK_ERR_UNSUPPORTED, "too many rows for one launch");
   const int64_t strides[] = {a->q_stride[0], a->q_stride[1], a->q_stride[2], a->k_stride[0], a->k_stride[1],
@@ -450,9 +412,8 @@ AttnCall call_of(const snack_attention_args *a) {
 struct Plan {
   bool tiles = false, few = false;  // on tcgen05; in blocks of 16 rows
   int splits = 1, chunk = 0, width = 0;  // width: columns of operands that are made; 0: none are
-  size_t delta = 0, part = 0, parts[4] = {}, bytes = 0;  // offsets; parts: of q, k, v, dout
+  size_t part = 0, parts[4] = {}, powers[4] = {}, bytes = 0;  // offsets (delta is at 0); parts: of q, k, v, dout
 };
-constexpr size_t kPeaks = 256;
 
 // Operands that are made first: those of 32-bit calls, and 16-bit tensors that TMA
 // cannot bring as they lie (odd head sizes, addresses or strides): else mma.sync
@@ -461,12 +422,20 @@ int part_width(const AttnCall &c, int type) {
   if (type == SNACK_F32) return 128;
   return tiles_read(c) ? 0 : c.d <= 64 ? 64 : 128;
 }
-void plan_parts(Plan *p, const AttnCall &c, int width, bool backward) {
+void plan_parts(Plan *p, const AttnCall &c, int type, bool backward) {
   const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
   const int64_t rows[4] = {c.rows * c.heads, keys * c.key_heads, keys * c.key_heads, backward ? c.rows * c.heads : 0};
   for (int i = 0; i < 4; ++i) {
     p->parts[i] = p->bytes;
-    p->bytes += rows[i] * width * 2;
+    p->bytes += rows[i] * p->width * 2;
+  }
+  if (type != SNACK_F32) return;
+  const int64_t q = tile_numbers(c.q_offsets, c.sequences, c.q_tokens) * c.heads;
+  const int64_t k = tile_numbers(c.k_offsets, c.sequences, c.k_tokens) * c.key_heads;
+  const int64_t tiles[4] = {q, k, k, backward ? q : 0};
+  for (int i = 0; i < 4; ++i) {
+    p->powers[i] = p->bytes;
+    p->bytes += round_up(tiles[i] * (int64_t)sizeof(int32_t), 16);
   }
 }
 
@@ -493,10 +462,7 @@ Plan plan_forward(const AttnCall &c, int type) {
   int64_t blocks, least, want;  // least keys of a part: below that it starts and ends more than it reads
   if (p.tiles) {
     p.width = part_width(c, type);
-    if (p.width) {
-      p.bytes = kPeaks;
-      plan_parts(&p, c, p.width, false);
-    }
+    if (p.width) plan_parts(&p, c, type, false);
     blocks = tile_forward_blocks(c);
     least = 1024;
     want = blocks ? sms / blocks : 1;
@@ -521,27 +487,23 @@ Plan plan_forward(const AttnCall &c, int type) {
 
 Plan plan_backward(const AttnCall &c, int type) {
   Plan p;
-  p.bytes = kPeaks;
-  p.delta = p.bytes;
-  p.bytes += round_up(c.rows * c.heads * (int64_t)sizeof(float), 256);
+  p.bytes = round_up(std::max<int64_t>(c.rows * c.heads, 1) * (int64_t)sizeof(float), 256);
   p.tiles = worth_tiles(c, type, true) && tiles_take(c, type);
   p.width = p.tiles ? part_width(c, type) : 0;
-  if (p.width) plan_parts(&p, c, p.width, true);
+  if (p.width) plan_parts(&p, c, type, true);
   return p;
 }
 
-// q, k, v and dout of a call; peaks in the order that AttnCall has them in.
+// q, k, v and dout of a call.
 Sources sources_of(const AttnCall &c, const Plan &p, char *workspace) {
   Sources s;
-  uint32_t *const peak = reinterpret_cast<uint32_t *>(workspace);
   const int64_t keys = c.k_offsets ? c.k_tokens : (int64_t)c.sequences * c.k_tokens;
   const Strided *const from[4] = {&c.q, &c.k, &c.v, &c.dout};
-  const int at[4] = {2, 3, 1, 0};
   for (int i = 0; i < 4; ++i) {
     const bool own = i == 0 || i == 3;
     s.t[i] = Source{*from[i], own ? c.q_offsets : c.k_offsets, own ? c.q_lengths : c.k_lengths,
-                    own ? c.q_tokens : c.k_tokens, own ? c.heads : c.key_heads, own ? c.rows : keys, peak + at[i],
-                    workspace + p.parts[i]};
+                    own ? c.q_tokens : c.k_tokens, own ? c.heads : c.key_heads, own ? c.rows : keys,
+                    workspace + p.parts[i], reinterpret_cast<int32_t *>(workspace + p.powers[i])};
   }
   return s;
 }
@@ -550,26 +512,26 @@ unsigned spread(int64_t rows) {  // a warp for each, or as many as are resident 
   return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows + 7) / 8, 8 * device_sms()));
 }
 
-// Makes a call's operands: q, k, v and, backward, dout, whose peak is there already.
+// Makes a call's operands: q, k, v and, backward, dout.
 template <typename T>
 cudaError_t make_parts(AttnCall *c, const Plan &p, bool backward, char *workspace, SplitParts *parts, cudaStream_t s) {
   const Sources all = sources_of(*c, p, workspace);
-  const unsigned blocks = spread(std::max(all.t[0].rows, all.t[1].rows));
-  cudaError_t e = cudaSuccess;
-  if (sizeof(T) == 4) {
-    e = launch_kernel(attention_peak<T>, dim3(blocks, 3), 256, 0, false, s, all, c->sequences, c->d);
-    c->made = 1;
-  }
-  if (e == cudaSuccess)
-    e = launch_kernel(p.width == 64 ? tile_operands<T, 64> : tile_operands<T, 128>, dim3(blocks, backward ? 4 : 3), 256,
-                      0, false, s, all, c->sequences, c->d);
   *parts = SplitParts{p.width, all.t[0].made, all.t[1].made, all.t[2].made, all.t[3].made};
-  return e;
-}
-
-cudaError_t clear_peaks(AttnCall *c, char *workspace, cudaStream_t s) {
-  c->peak = reinterpret_cast<const uint32_t *>(workspace);
-  return cudaMemsetAsync(workspace, 0, 4 * sizeof(uint32_t), s);
+  const unsigned tensors = backward ? 4 : 3;
+  if constexpr (sizeof(T) == 4) {
+    c->q_power = all.t[0].power;
+    c->k_power = all.t[1].power;
+    c->v_power = all.t[2].power;
+    c->dout_power = all.t[3].power;
+    const int64_t q = tiles_of(c->q_offsets, c->sequences, c->q_tokens, 1, kTile) * c->heads;
+    const int64_t k = tiles_of(c->k_offsets, c->sequences, c->k_tokens, 1, kTile) * c->key_heads;
+    return launch_kernel(split_operands, dim3((unsigned)std::max(q, k), tensors), 256, 0, false, s, all, c->sequences,
+                         c->d);
+  } else {
+    const unsigned blocks = spread(std::max(all.t[0].rows, all.t[1].rows));
+    return launch_kernel(p.width == 64 ? copy_operands<T, 64> : copy_operands<T, 128>, dim3(blocks, tensors), 256, 0,
+                         false, s, all, c->sequences, c->d);
+  }
 }
 
 template <typename T>
@@ -581,10 +543,7 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
   cudaError_t e = cudaSuccess;
   if (p.tiles) {
     SplitParts parts = {};
-    if (p.width) {
-      if (type == SNACK_F32) e = clear_peaks(&c, workspace, s);
-      if (e == cudaSuccess) e = make_parts<T>(&c, p, false, workspace, &parts, s);
-    }
+    if (p.width) e = make_parts<T>(&c, p, false, workspace, &parts, s);
     if (e == cudaSuccess) e = tile_forward_launch(c, type, parts, s);
   } else {
     e = few_forward_launch(c, type, s);
@@ -597,14 +556,12 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
 template <typename T>
 cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  const bool peaks = type == SNACK_F32 && p.width;
-  cudaError_t e = peaks ? clear_peaks(&c, workspace, s) : cudaSuccess;
-  if (e == cudaSuccess && c.rows) {
+  cudaError_t e = cudaSuccess;
+  if (c.rows) {
     const auto even = [](const Strided &t) {
       return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
     };
-    e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out),
-                        peaks ? reinterpret_cast<uint32_t *>(workspace) : nullptr, s);
+    e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out), s);
   }
   if (e != cudaSuccess) return e;
   SplitParts parts = {};
@@ -675,7 +632,7 @@ extern "C" snack_status snack_attention_backward(const snack_attention_args *a, 
   c.dv = strided(g->dv, g->dv_stride);
   c.lse = const_cast<float *>(g->lse);
   char *const ws = static_cast<char *>(workspace);
-  c.delta = reinterpret_cast<float *>(ws + p.delta);
+  c.delta = reinterpret_cast<float *>(ws);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a->type == SNACK_F32    ? backward_typed<float>(c, p, a->type, ws, s)
                         : a->type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, p, a->type, ws, s)

@@ -17,12 +17,13 @@ struct AttnCall {
   float *lse;    // [heads][rows]: log of the sum of exp(scale * q . k), -inf where no key is seen
   float *delta;  // [heads][rows]: dout . out
   float *part;   // partial results of a split call
-  const uint32_t *peak;  // 32-bit operands that are made: bits of the largest |dout|, |v|, |q|, |k|
+  // 32-bit calls on tcgen05: the power of two that the float16 parts of each tile of
+  // 128 tokens of a head are scaled by, [tile][head] (tiles numbered as Span says)
+  const int32_t *q_power, *k_power, *v_power, *dout_power;
   int64_t rows;  // rows of lse for a head: all tokens of q
   int sequences, q_tokens, k_tokens;
   int heads, key_heads, group, d;
   int causal, splits, chunk;
-  int made;  // 32-bit operands: made as two float16 parts, scaled by the powers of two of their peaks
   float scale, scale_log2;  // scale * log2(e)
   const int32_t *q_offsets, *k_offsets, *q_lengths, *k_lengths;
   uint32_t drop;  // 0: no dropout; else a probability is kept where its 16 bits are at least this
@@ -33,14 +34,22 @@ struct AttnCall {
   __device__ __forceinline__ uint64_t draws() const { return seed_at ? *seed_at : seed; }
 };
 
-// The tokens of one sequence on one side.  `base` is the address part that
-// does not depend on the head; rows `valid` .. cover-1 belong to the tensor
-// but not to the sequence (padding): their results are zero.
+constexpr int kTile = 128;  // tokens of a tile on tcgen05
+
+// The tokens of one sequence on one side.  Rows `valid` .. cover-1 belong to the
+// tensor but not to the sequence (padding): their results are zero.
 struct Span {
-  int64_t row;  // number of the first token among all
+  int64_t row;   // number of the first token among all
+  int64_t tile;  // number of the first tile of kTile tokens among all (a ragged side leaves numbers out)
   int valid, cover;
   int seq;  // of a dense side; 0 in a ragged one, whose tokens are numbered through
 };
+
+// Numbers of tiles that a side can have: the tiles of ragged sequence s begin at
+// offset / kTile + s, which is at least where those of sequence s - 1 end.
+inline int64_t tile_numbers(bool ragged, int64_t n, int64_t tokens) {
+  return ragged ? tokens / kTile + n + 3 : n * ((tokens + kTile - 1) / kTile);
+}
 
 // Sequences are numbered 0 .. sequences-1 in a dense side.  A ragged side has
 // two more, without partners on the other side: the tokens before the first
@@ -64,12 +73,14 @@ __device__ __forceinline__ Span own_span(const int32_t *offsets, const int32_t *
   if (offsets) {
     const int a = ragged_begin(offsets, s, tokens), b = ragged_end(offsets, s, n, tokens);
     sp.row = a;
+    sp.tile = a / kTile + s;
     sp.cover = b > a ? b - a : 0;
     sp.valid = s == 0 || s == n + 1 ? 0 : sp.cover;
     sp.seq = 0;
     return sp;
   }
   sp.row = (int64_t)s * tokens;
+  sp.tile = (int64_t)s * ((tokens + kTile - 1) / kTile);
   sp.cover = tokens;
   sp.valid = lengths ? min(max(lengths[s], 0), tokens) : tokens;
   sp.seq = s;
@@ -81,7 +92,7 @@ __device__ __forceinline__ Span own_span(const int32_t *offsets, const int32_t *
 __device__ __forceinline__ Span other_span(const int32_t *offsets, const int32_t *lengths, int s, bool ragged, int n,
                                            int tokens) {
   const int i = ragged ? s - 1 : s;
-  if (i < 0 || i >= n) return Span{0, 0, 0, 0};
+  if (i < 0 || i >= n) return Span{0, 0, 0, 0, 0};
   if (offsets) return own_span(offsets, nullptr, i + 1, n, tokens);
   return own_span(nullptr, lengths, i, n, tokens);
 }

@@ -12,10 +12,12 @@
 // (zero) entries in the second product are set to zero, since what lies there
 // may not be finite.
 //
-// 32-bit floats arrive as two float16 parts of a tensor scaled by a power of two
-// to below 2^15, x = hi + lo (made by tile_operands in attention.cu): 22 bits of
-// everything above 2^-17 of the tensor's largest, and never more than 2^-39 of
-// that off.  A row has its 64 high halves, then its 64 low ones, and a product
+// 32-bit floats arrive as two float16 parts of a tile (128 tokens of a head) scaled
+// by a power of two to below 2^15, x = hi + lo (made by split_operands in
+// attention.cu): 22 bits of everything above 2^-17 of the tile's largest, and never
+// more than 2^-39 of that off.  A power for a tile, not for a tensor, so that nothing
+// depends on other sequences and heads; products with a tile of keys, or of queries,
+// are brought back as they leave tensor memory.  A row has its 64 high halves, then its 64 low ones, and a product
 // is hi*hi + hi*lo + lo*hi; probabilities (2^14 fold) and gradients of scores
 // are split the same way.  Three products at the rate of 16 bits cost half of
 // three tf32 ones.  The sums leave tensor memory after every tile for 32-bit
@@ -30,7 +32,6 @@ namespace snack {
 // Sticky: a wait of one of this file's kernels has run out since the last read.
 static __device__ int g_attention_failed = 0;
 
-constexpr int kTile = 128;
 // Warps 0-7: rows; 8: copies; 9: MMAs; 10: statistics of
 // rows, where they are not a thread's own; 11 only completes the warpgroup.
 // 384 threads are launched with 168 registers each: 3 * 168 = 2 * 224 + 56.
@@ -136,14 +137,9 @@ __device__ __forceinline__ void store_sums(uint32_t from, T *row, float factor, 
   }
 }
 
-// 32-bit operands' parts are scaled by powers of two: what takes them out again.
-struct Scales {
-  float scores, dprobs, q, k, v, dout;
-};
-__device__ __forceinline__ Scales scales_of(const AttnCall &c) {
-  if (!c.made) return Scales{c.scale_log2, 1.f, 1.f, 1.f, 1.f, 1.f};
-  const auto back = [&](int i) { return exp2f((float)-power_to_half(c.peak[i])); };
-  return Scales{c.scale_log2 * back(2) * back(3), back(0) * back(1), back(2), back(3), back(1), back(0)};
+// What takes the power of a tile of 32-bit operands out again.
+__device__ __forceinline__ float power_back(const int32_t *power, int64_t tile, int heads, int head) {
+  return power_of_two(-__ldg(power + tile * heads + head));
 }
 
 // Rows a times rows b, over the head size.

@@ -94,6 +94,9 @@ struct KeyBars {
   int failed;
   alignas(16) float lse[2][kTile];
   alignas(16) float delta[2][kTile];
+  struct {
+    float scores, dprobs, q, dout;
+  } by[2];  // what a tile of queries' products are multiplied by
   Tops tops;
 };
 
@@ -260,10 +263,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
     } else if (warp == kStatWarp) {
       constexpr float up = kUp<T>;
+      float k_back = 1.f, v_back = 1.f;
+      if (kSplit && all > 0) {
+        k_back = power_back(c.k_power, ks.tile + at.tile, c.key_heads, kh);
+        v_back = power_back(c.v_power, ks.tile + at.tile, c.key_heads, kh);
+      }
       for (int n = 0; n < all; ++n) {
         const int slot = n & 1, g = n / tiles, q0 = (tile0 + n - g * tiles) * kTile;
         const int64_t place = (int64_t)(kh * G + g) * c.rows + qs.row;
-        float lse[4], delta[4];
+        float lse[4], delta[4], q_back = 1.f, d_back = 1.f;
+        if (kSplit) {
+          q_back = power_back(c.q_power, qs.tile + q0 / kTile, c.heads, kh * G + g);
+          d_back = power_back(c.dout_power, qs.tile + q0 / kTile, c.heads, kh * G + g);
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int i = q0 + lane + 32 * x;
@@ -275,8 +287,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           bars.lse[slot][lane + 32 * x] = up - lse[x];  // as they are added
-          bars.delta[slot][lane + 32 * x] = -delta[x] * exp2f(-up);
+          bars.delta[slot][lane + 32 * x] = -delta[x] * exp2f(-up);  // (times probabilities that are that power up)
         }
+        if (lane == 0) bars.by[slot] = {c.scale_log2 * k_back * q_back, v_back * d_back * exp2f(-up), q_back, d_back};
         tc::bar_arrive_warp(&bars.stat_full[slot]);
       }
     }
@@ -285,11 +298,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int w = warp >> 2, j = j0 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + w * kHalf, dp_at = s_at + kTile;
-    const Scales by = scales_of(c);
-    const float2 cs2 = make_float2(by.scores, by.scores);
-    const float dprobs = by.dprobs * exp2f(-kUp<T>);  // (times probabilities that are that power up)
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
-    int power = kSplit ? 0 : kMostPower;  // of the row's dS: split, of the last step's; else of its sums
+    float back = 0.f;                 // split: what the last step's are multiplied by
+    int power = kMostPower;           // else of the row's sums
     const bool alone = nk == 1 || (c.causal && j0 == 0 && (warp & 3) == 0);
     const uint64_t seed = DROP ? c.draws() : 0;
     bool ok = true;
@@ -316,7 +327,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
-        if (w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile, 1.f);  // dV of the tile before
+        if (w) {
+          if (n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile, back);  // dV of the tile before
+          back = bars.by[slot].dout;
+        }
+      const float cs = kSplit ? bars.by[slot].scores : c.scale_log2, dprobs = kSplit ? bars.by[slot].dprobs : exp2f(-kUp<T>);
+      const float2 cs2 = make_float2(cs, cs);
       float p[kHalf];
       tc::load32(s_at, p);
       tc::load32(s_at + 32, p + 32);
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
-        if (!w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + DP, power_of_two(-power));  // dK of the tile before
+        if (!w && n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + DP, back);  // dK of the tile before
 #pragma unroll
       for (int c0 = 0; c0 < kHalf; c0 += 32) {  // dS takes the probabilities' place
         float t[32];
@@ -385,15 +401,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t exponent;
         ok = row_exponent(bars.tops, p, n, &exponent, failed);
         if (!ok) break;
+        float up;
         if constexpr (kSplit) {
-          power = row_power(exponent, 14, 0);
+          const int now = row_power(exponent, 14, 0);
+          up = power_of_two(now);
+          if (!w) back = power_of_two(-now) * bars.by[slot].q;
         } else {  // (the sums so far are complete: these dP come after them)
           const int now = running_power(power, exponent);
           if (n > 0 && __any_sync(0xffffffffu, now != power))
             multiply_sums<DP / 2>(tmem + lanes + 2 * kTile + DP + w * (DP / 2), exp2f((float)(now - power)));
           power = now;
+          up = power_of_two(power);
         }
-        const float up = power_of_two(power);
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) p[x] *= up;
       }
@@ -414,9 +433,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j < ks.cover)
         row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
               kh * to.head;
-      float factor = w ? exp2f(-kUp<T>) * c.keep_scale * by.dout : c.scale * by.q;
+      float factor = w ? exp2f(-kUp<T>) * c.keep_scale : c.scale;
       if constexpr (kSplit) {
-        if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP), w ? 1.f : power_of_two(-power));
+        if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP), back);
         store_floats<DP>(row, acc, factor, c.d, j >= nk);
       } else {
         if (kScaled<T> && !w) factor *= power_of_two(-power);
@@ -613,10 +632,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         lim = max(0, seen_keys(c.causal, i, nq, nk));
       if (lim == 1) lim = 0;  // P = 1 whatever the score: dS is zero
     }
-    const Scales by = scales_of(c);
     float acc[kSplit ? DP / 2 : 1] = {};  // split: the sums of this warpgroup's half of the columns
-    int power = kSplit ? 0 : kMostPower, power_before = 0;  // of the row's dS: split, of the last two steps'; else of its sums
-    const float2 cs2 = make_float2(by.scores, by.scores), off2 = make_float2(-lse, -lse);
+    float back = 0.f, back_before = 0.f;  // split: what the last two steps' are multiplied by
+    int power = kMostPower;               // else of the row's sums
+    // powers of two of this tile and, one step ahead, of the keys and values
+    float q_back = 1.f, d_back = 1.f, k_next = 1.f, v_next = 1.f;
+    const auto load_powers = [&](int n) {
+      k_next = power_back(c.k_power, ks.tile + n, c.key_heads, kh);
+      v_next = power_back(c.v_power, ks.tile + n, c.key_heads, kh);
+    };
+    if (kSplit && all > 0) {
+      q_back = power_back(c.q_power, qs.tile + at.tile, c.heads, head);
+      d_back = power_back(c.dout_power, qs.tile + at.tile, c.heads, head);
+      load_powers(0);
+    }
+    const float2 off2 = make_float2(-lse, -lse);
     const float2 delta2 = make_float2(-delta, -delta);
     const uint64_t draw = DROP ? dropout_row(c.draws(), qs.row + i, c.heads, head) : 0;
     bool ok = true;
@@ -627,7 +657,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::fence_after();
       if constexpr (kSplit)
         if (n > 1)  // of two tiles before
-          add_sums<DP / 2>(acc, at_lane + 3 * kTile + b * DP + w * (DP / 2), power_of_two(-power_before));
+          add_sums<DP / 2>(acc, at_lane + 3 * kTile + b * DP + w * (DP / 2), back_before);
+      const float k_back = k_next, cs = c.scale_log2 * q_back * k_back, dprobs = d_back * v_next;
+      const float2 cs2 = make_float2(cs, cs);
+      if (kSplit && n + 1 < all) load_powers(n + 1);
       const uint32_t s_at = at_lane + 2 * n % 3 * kTile + w * kHalf, dp_at = at_lane + (2 * n + 1) % 3 * kTile + w * kHalf;
       float p[kHalf];
       tc::load32(s_at, p);
@@ -660,7 +693,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
 #pragma unroll
       for (int x = 0; x < kHalf; x += 2) {
-        float2 a = tc::fma2(make_float2(t[x], t[x + 1]), make_float2(by.dprobs, by.dprobs), delta2);
+        float2 a = tc::fma2(make_float2(t[x], t[x + 1]), make_float2(dprobs, dprobs), delta2);
         a = tc::mul2(a, make_float2(p[x], p[x + 1]));
         t[x] = a.x;
         t[x + 1] = a.y;
@@ -672,9 +705,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t exponent;
         ok = row_exponent(bars.tops, t, n, &exponent, failed);
         if (!ok) break;
+        float up;
         if constexpr (kSplit) {
-          power_before = power;
-          power = row_power(exponent, 14, 0);
+          const int now = row_power(exponent, 14, 0);
+          up = power_of_two(now);
+          back_before = back;
+          back = power_of_two(-now) * k_back;
         } else {
           const int now = running_power(power, exponent);
           if (n > 0 && __any_sync(0xffffffffu, now != power)) {  // once the sums so far are complete
@@ -684,8 +720,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             multiply_sums<DP / 2>(at_lane + 3 * kTile + w * (DP / 2), exp2f((float)(now - power)));
           }
           power = now;
+          up = power_of_two(power);
         }
-        const float up = power_of_two(power);
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] *= up;
       }
@@ -708,8 +744,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if constexpr (kSplit) {
         for (int n = max(0, all - 2); n < all; ++n)
           add_sums<DP / 2>(acc, at_lane + 3 * kTile + (n & 1) * DP + from,
-                           power_of_two(n == all - 1 ? -power : -power_before));
-        store_floats<DP / 2>(row, acc, c.scale * by.k, c.d - from, lim == 0);
+                           n == all - 1 ? back : back_before);
+        store_floats<DP / 2>(row, acc, c.scale, c.d - from, lim == 0);
       } else {
         const float factor = kScaled<T> ? c.scale * power_of_two(-power) : c.scale;
         store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, factor, c.d - from, all > 0, lim == 0);

@@ -186,8 +186,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int lim = i < nq ? max(0, seen_keys(c.causal, i, nq, nk) - begin * kTile) : 0;
     const int64_t slot = (blockIdx.y * c.rows + qs.row + i) * c.heads + head;
     float *const part_lse = c.part + (int64_t)c.splits * c.rows * c.heads * c.d + slot;
-    const Scales by = scales_of(c);
-    const float cs = by.scores;
     uint64_t draw = 0;
     if (DROP) draw = dropout_row(c.draws(), qs.row + i, c.heads, head);
     float m = -INFINITY, sum = 0.f;
@@ -196,11 +194,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // Two passes over the scores in tensor memory, 64 at a time: a row's sums
       // stay in registers beside them.
       float o[DP] = {};
+      // powers of two of this tile of queries, of the keys' (one tile ahead) and of the values before
+      const float q_back = steps[t] ? power_back(c.q_power, qs.tile + first[t] / kTile, c.heads, head) : 0.f;
+      float k_back = 0.f, v_back = 0.f, v_before = 0.f;
+      const auto load_powers = [&](int j) {
+        k_back = power_back(c.k_power, ks.tile + begin + j, c.key_heads, kh);
+        v_back = power_back(c.v_power, ks.tile + begin + j, c.key_heads, kh);
+      };
+      if (steps[t]) load_powers(0);
       for (int j = 0; j < steps[t]; ++j) {
         ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
         if (!ok) break;
         tc::fence_after();
-        if (j > 0) add_sums<DP>(o, o_at, 1.f);  // of the tile before: complete when these scores are
+        if (j > 0) add_sums<DP>(o, o_at, v_before);  // of the tile before: complete when these scores are
+        const float cs = fmaxf(c.scale_log2 * q_back * k_back, 1e-37f);
+        v_before = v_back;
+        if (j + 1 < steps[t]) load_powers(j + 1);
         const int left = lim - j * kTile;  // keys of this tile that the row sees
         const bool cut = __any_sync(0xffffffffu, left < kTile);
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -218,14 +227,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int y = 0; y < 4; ++y) top[y] = tc::max3(top[y], s[e + y], s[e + 4 + y]);
         }
-        const float grown = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-        const float shrink = grown == -INFINITY ? 1.f : tc::exp2_fast((m - grown) * cs);
+        const float grown = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cs);
+        const float shrink = grown == -INFINITY ? 1.f : tc::exp2_fast(m - grown);
         m = grown;
         sum *= shrink;
         if (__any_sync(0xffffffffu, shrink != 1.f))
 #pragma unroll
           for (int e = 0; e < DP; ++e) o[e] *= shrink;
-        const float off = m == -INFINITY ? kHalfP : kHalfP - m * cs;
+        const float off = m == -INFINITY ? kHalfP : kHalfP - m;
         float part[4] = {};
 #pragma unroll
         for (int x = 0; x < kTile; x += 64) {
@@ -258,18 +267,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (ok && steps[t]) {
         ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));
         tc::fence_after();
-        if (ok) add_sums<DP>(o, o_at, 1.f);
+        if (ok) add_sums<DP>(o, o_at, v_before);
       }
       if (ok && i < qs.cover) {
         float *const row = c.splits > 1 ? c.part + slot * c.d
                                         : static_cast<float *>(c.out.p) + head * c.out.head +
                                               (c.q_offsets ? (qs.row + i) * c.out.token
                                                            : qs.seq * c.out.seq + i * c.out.token);
-        store_floats<DP>(row, o, c.keep_scale / sum * by.v, c.d, sum == 0.f);
+        store_floats<DP>(row, o, c.keep_scale / sum, c.d, sum == 0.f);
         *(c.splits > 1 ? part_lse : c.lse + (int64_t)head * c.rows + qs.row + i) =
-            sum == 0.f ? -INFINITY : m * cs * kLn2 + (logf(sum) - kHalfP * kLn2);
+            sum == 0.f ? -INFINITY : m * kLn2 + (logf(sum) - kHalfP * kLn2);
       }
     } else {
+    const float cs = c.scale_log2;
     for (int j = 0; j < steps[t]; ++j) {
       ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
       if (!ok) break;
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (ok) {
       const bool mine = i < qs.cover;
-      const float factor = c.keep_scale / sum * by.v;
+      const float factor = c.keep_scale / sum;
       if (c.splits > 1) {
 #pragma unroll
         for (int x = 0; x < DP; x += 32) {

@@ -500,14 +500,14 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
  * sequences].  Products are summed in 32 bits.  In 16-bit types P is rounded to
  * the type before the second product, as tensor instructions take both
  * operands in one type.  32-bit calls of some size (head_size up to 64, see
- * attention.cu) take each operand as two float16 parts of the tensor times a
- * power of two: 22 bits of what lies above 2^-17 of the tensor's largest
- * element, and nothing more than 2^-39 of that off; probabilities are split the same
- * way, 2^14 fold.  Gradients of scores are taken in two parts in every type, in
- * float16 parts times a power of two of their own row (a query's for dq, a key's for
- * dk): off by 2^-22 of themselves and 2^-36 of the row's largest, whatever other rows
- * hold.  An infinite or NaN element inside a sequence may reach results that
- * do not depend on it, in bfloat16 those of the same sequence alone.
+ * attention.cu) take each operand as two float16 parts, every 128 tokens of a head
+ * (from its sequence's first on) times a power of two of their own: 22 bits of what
+ * lies above 2^-17 of their largest element, and nothing more than 2^-39 of that
+ * off; probabilities are split the same way, 2^14 fold.  Gradients of scores are taken
+ * in two parts in every type, in float16 parts times a power of two of their own row (a
+ * query's for dq, a key's for dk): off by 2^-22 of themselves and 2^-36 of the row's
+ * largest, whatever other rows hold.  An infinite or NaN element inside a sequence may
+ * reach results of that sequence that do not depend on it, and no other sequence's.
  * Limits: 1 <= head_size <= 128, heads <= 65536, ragged sides of at most 65536
  * sequences; tokens, and q_tokens * (heads / key_heads), below 2^31 - 4096.
  * Workspaces are 16-byte aligned and hold nothing from one call to the next.

@@ -37,8 +37,7 @@ def test_the_longest_cache(dtype):
 
 # ---------------------------------------------------------------- sequences far apart in magnitude
 
-RANGE_TYPES = [BF16, F16]
-GRADIENT_TYPES = [BF16, F16, F32]
+
 
 
 def run(q, k, v, dout, **opts):
@@ -66,7 +65,7 @@ def layouts(d, n, length):
             ((n * length,), dict(q_offsets=ends, k_offsets=ends), [slice(i * length, (i + 1) * length) for i in range(n)])]
 
 
-@pytest.mark.parametrize("dtype", RANGE_TYPES)
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("length,d", [(40, 64), (700, 64), (700, 65), (700, 128), (515, 100)])
 @pytest.mark.parametrize("dropout", [0.0, 0.2])
 def test_a_sequence_does_not_change_with_the_others_magnitudes(dtype, length, d, dropout):
@@ -95,7 +94,7 @@ def test_a_sequence_does_not_change_with_the_others_magnitudes(dtype, length, d,
                     same_but_for_powers(y[s], w[s], p)
 
 
-@pytest.mark.parametrize("dtype", RANGE_TYPES)
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("length,d", [(40, 64), (700, 64), (700, 65), (700, 128)])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
 def test_what_is_not_finite_stays_in_its_sequence(dtype, length, d, value):
@@ -111,7 +110,7 @@ def test_what_is_not_finite_stays_in_its_sequence(dtype, length, d, value):
                 assert torch.equal(y[s], w[s])
 
 
-@pytest.mark.parametrize("dtype", GRADIENT_TYPES)
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("ratio", [2.0 ** -7, 2.0 ** -13, 2.0 ** -17])
 @pytest.mark.parametrize("length,d", [(1100, 64), (1100, 65), (1000, 128), (200, 64)])
 def test_tokens_whose_gradients_lie_far_apart(dtype, ratio, length, d):
@@ -141,3 +140,19 @@ def test_tokens_whose_gradients_lie_far_apart(dtype, ratio, length, d):
     for name, got in (("dk", dk), ("dv", dv)):
         ref, bound = (t[:, first:] * ratio for t in want[name])
         assert bool(((got[:, first:].double() - ref).abs() <= 1.01 * bound + tiny).all()), name
+
+
+@pytest.mark.parametrize("length", [300, 1500])
+def test_heads_whose_values_lie_far_apart(length):
+    """32-bit operands are taken in parts scaled tile by tile and head by head: a head's results are
+    those of the same head among others of its size."""
+    g = gen(length)
+    q, dout = (rnd(g, (2, length, 6, 64), F32) for _ in range(2))
+    k, v = (rnd(g, (2, length, 3, 64), F32) for _ in range(2))
+    want = run(q, k, v, dout)
+    powers = torch.tensor([2.0 ** 30, 1.0, 2.0 ** -30], device="cuda")[:, None]
+    both = powers.repeat_interleave(2, 0)
+    got = run(q * both, k / powers, v * powers, dout * both.flip(0))
+    assert torch.equal(got[1], want[1]) and torch.equal(got[0], want[0] * both)
+    assert torch.equal(got[2], want[2] * both.flip(0)) and torch.equal(got[4], want[4] * powers.flip(0))
+    assert torch.equal(got[3], want[3] * powers * powers * powers.flip(0))
