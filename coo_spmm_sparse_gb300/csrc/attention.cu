@@ -39,14 +39,138 @@ __device__ __forceinline__ float larger(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(fabsf(b))));
 }
 
-// delta = dout . out for every row and head.  A team of lanes takes a row with one 16-byte load of each tensor a
-// lane, and kItems rows at a time, whose loads are in flight together.
+// 16 bytes of elements from v on, of which `left` are there.
+template <typename T>
+__device__ __forceinline__ uint4 load_vector(const T *v, int left) {
+  constexpr int E = 16 / sizeof(T);
+  if (left >= E && (reinterpret_cast<uintptr_t>(v) & 15) == 0) return *reinterpret_cast<const uint4 *>(v);
+  uint4 u = make_uint4(0, 0, 0, 0);
+  T x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = e < left ? v[e] : from_float<T>(0.f);
+  memcpy(&u, x, 16);
+  return u;
+}
+
+// 16-bit types: delta of a row that sees 2 to kFewKeys keys is sum_j M P (dout . v_j),
+// from the tensors themselves.  out is rounded, and with delta from it causal calls'
+// dq and dk were off by this many times what rounding the results alone costs (worst
+// of 5 draws, three shapes): 7.3 at 2 keys, 2.1 at 8, 1.6 at 32 and 1.3 at 64; from
+// here 1.0.  Which rows do depends on the keys that they see and on nothing else of
+// the call.
+constexpr int kFewKeys = 32;
+__device__ __forceinline__ bool few_keys(int seen) { return seen >= 2 && seen <= kFewKeys; }
+
+// The keys that a row of all sequences sees.
+__device__ __forceinline__ int seen_by_row(const AttnCall &c, int64_t row, int seq, int token) {
+  int s = seq;
+  if (c.q_offsets) {  // the last sequence that begins at or before the row
+    int lo = 0, hi = c.sequences;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (clamped(c.q_offsets, mid, c.q_tokens) <= row) lo = mid; else hi = mid;
+    }
+    s = lo;
+  }
+  const Span qs = own_span(c.q_offsets, c.q_lengths, c.q_offsets ? s + 1 : s, c.sequences, c.q_tokens);
+  const Span ks = own_span(c.k_offsets, c.k_lengths, c.k_offsets ? s + 1 : s, c.sequences, c.k_tokens);
+  return seen_keys(c.causal, c.q_offsets ? (int)(row - qs.row) : token, qs.valid, ks.valid);
+}
+
+// Those rows of a sequence are neighbours (the first ones of a causal call): block
+// `part` of `parts` of a sequence gives a warp one row at a time, whose L lanes read a
+// key side by side, four times 32 / L keys at once.  The lanes' parts of the eight
+// products are added up so that each lane is left with one of them.
+template <typename T, int L, bool VEC>
+__device__ __forceinline__ void delta_of_few_keys(const AttnCall &c, int s, int part, int parts) {
+  constexpr int E = 16 / sizeof(T), kAhead = 4, kKeys = 32 / L;
+  const int lane = threadIdx.x & 31, col = lane % L * E;
+  const bool lower = lane & (L / 2), later = lane & (L / 4), odd = lane & (L / 8);  // dprob; of keys 2 and 3; 1 and 3
+  const int own = (later ? 2 * kKeys : 0) + (odd ? kKeys : 0) + lane / L;
+  const bool counts = !lower && (L == 8 || !(lane & 1));
+  const Span qs = own_span(c.q_offsets, c.q_lengths, c.q_offsets ? s + 1 : s, c.sequences, c.q_tokens);
+  const Span ks = own_span(c.k_offsets, c.k_lengths, c.k_offsets ? s + 1 : s, c.sequences, c.k_tokens);
+  const int nq = qs.valid, nk = ks.valid;
+  const int lo = c.causal ? max(0, nq - nk + 1) : 0;
+  const int hi = c.causal ? min((int64_t)nq, (int64_t)nq - nk + kFewKeys) : few_keys(nk) ? nq : 0;
+  const int64_t items = (int64_t)max(0, hi - lo) * c.heads;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  for (int64_t item = (int64_t)part * 8 + (threadIdx.x >> 5); item < items; item += (int64_t)parts * 8) {
+    const int i = lo + (int)(item / c.heads), head = (int)(item % c.heads), kh = head / c.group;
+    const int64_t row = qs.row + i, place = (int64_t)head * c.rows + row;
+    const int64_t q_at = c.q_offsets ? row : i, k_at = c.k_offsets ? ks.row : 0;
+    const int seen = seen_keys(c.causal, i, nq, nk);
+    const float lse = c.lse[place];
+    const bool some = col < c.d;
+    const auto load = [&](const T *at) {
+      return VEC ? *reinterpret_cast<const uint4 *>(at) : load_vector(at, c.d - col);
+    };
+    const auto of_query = [&](const Strided &t) {
+      return some ? load(static_cast<const T *>(t.p) + qs.seq * t.seq + q_at * t.token + head * t.head + col) : none;
+    };
+    const uint4 qu = of_query(c.q), gu = of_query(c.dout);
+    const auto of_key = [&](const Strided &t, int j) {
+      return some && j < seen ? load(static_cast<const T *>(t.p) + ks.seq * t.seq + (k_at + j) * t.token +
+                                     kh * t.head + col) : none;
+    };
+    const uint64_t draws = c.drop ? dropout_row(c.draws(), row, c.heads, head) : 0;
+    float delta = 0.f;
+    for (int j0 = 0; j0 < seen; j0 += kAhead * kKeys) {
+      uint4 ku[kAhead], vu[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        ku[u] = of_key(c.k, j0 + u * kKeys + lane / L);
+        vu[u] = of_key(c.v, j0 + u * kKeys + lane / L);
+      }
+      float q[E], g[E];
+      unpack16<T>(qu, q);
+      unpack16<T>(gu, g);
+      float x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float a[E], b[E], score = 0.f, dprob = 0.f;
+        unpack16<T>(ku[u], a);
+        unpack16<T>(vu[u], b);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          score = fmaf(q[e], a[e], score);
+          dprob = fmaf(g[e], b[e], dprob);
+        }
+        x[u] = (lower ? dprob : score) + __shfl_xor_sync(0xffffffffu, lower ? score : dprob, L / 2);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        x[u] = (later ? x[u + 2] : x[u]) + __shfl_xor_sync(0xffffffffu, later ? x[u] : x[u + 2], L / 4);
+      x[0] = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], L / 8);
+      if (L == 16) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+      const float dprob = __shfl_xor_sync(0xffffffffu, x[0], L / 2);
+      const int j = j0 + own;
+      if (counts && j < seen) {
+        float p = expf(x[0] * c.scale - lse) * dprob;
+        if (c.drop) p = draw_lane(dropout_draw(draws, j), j & 3) >= c.drop ? p * c.keep_scale : 0.f;
+        delta += p;
+      }
+    }
+    delta = warp_sum(delta);
+    if (lane == 0) c.delta[place] = lse == -INFINITY ? 0.f : delta;
+  }
+}
+
+// delta of the other rows, dout . out.  A team of lanes takes a row with one 16-byte
+// load of each tensor a lane, and kItems rows at a time, whose loads are in flight
+// together.  The first `few` blocks, `parts` for each sequence, take the rows of few
+// keys: bf16 backward calls, us, with delta of out alone / with them: 8 x 24 tokens, 24
+// heads over 12 of 128, 27 / 35; 8 x 64 47 / 56; 64 x 33, 12 over 4, 70 / 101 (24576 such
+// rows, bound by their instructions).
 constexpr int kItems = 4;
 template <typename T, int TEAM, bool VEC>
-__global__ void __launch_bounds__(256) attention_delta(const AttnCall c) {
+__global__ void __launch_bounds__(256, 3) attention_delta(const AttnCall c, int few, int parts) {
+  if constexpr (sizeof(T) == 2)
+    if ((int)blockIdx.x < few)
+      return delta_of_few_keys<T, TEAM == 8 ? 8 : 16, VEC>(c, blockIdx.x / parts, blockIdx.x % parts, parts);
   constexpr int E = 16 / sizeof(T), kTeams = 256 / TEAM;
   const int lane = threadIdx.x % TEAM;
-  const int64_t first = (int64_t)blockIdx.x * (kTeams * kItems) + threadIdx.x / TEAM;
+  const int64_t first = (int64_t)(blockIdx.x - few) * (kTeams * kItems) + threadIdx.x / TEAM;
   float sum[kItems] = {};
   int64_t place[kItems];
   uint4 x[kItems], y[kItems];
@@ -70,6 +194,7 @@ __global__ void __launch_bounds__(256) attention_delta(const AttnCall c) {
     } else {
       for (int col = lane; col < c.d; col += TEAM) sum[i] += to_float(d[col]) * to_float(o[col]);
     }
+    if (sizeof(T) == 2 && few && few_keys(seen_by_row(c, row, seq, token))) place[i] = -1;
   }
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
@@ -86,108 +211,33 @@ __global__ void __launch_bounds__(256) attention_delta(const AttnCall c) {
   }
 }
 
-// 16 bytes of elements from v on, of which `left` are there.
 template <typename T>
-__device__ __forceinline__ uint4 load_vector(const T *v, int left) {
+cudaError_t delta_launch(const AttnCall &c, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  if (left >= E && (reinterpret_cast<uintptr_t>(v) & 15) == 0) return *reinterpret_cast<const uint4 *>(v);
-  uint4 u = make_uint4(0, 0, 0, 0);
-  T x[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = e < left ? v[e] : from_float<T>(0.f);
-  memcpy(&u, x, 16);
-  return u;
-}
-
-// delta of 16-bit calls with few keys: sum_j M P (dout . v_j), from the tensors
-// themselves.  out is rounded, and with delta from it causal calls' dq and dk were
-// off by this many times what rounding the results alone costs (worst of 5 draws,
-// three shapes): 7.3 at 2 keys, 2.1 at 8, 1.6 at 32 and 1.3 at 64; from here 1.0.
-// A warp takes a row and head, a lane a key, so a warp's loads of k and v lie in 32
-// rows, and that is what it costs.  Whole backward calls, from out / from here (us,
-// steps of 2): bf16 8 x 16 tokens, 24 heads over 12 of 128 (work 393216) 31 / 37;
-// 24 tokens (589824) 35 / 49; 6 x 32 tokens, 24 over 12 of 64, every key seen
-// (294912) 25 / 37; 8 x 64 tokens, 24 over 12 of 128: 61 / 125.  So up to 32 keys
-// and a work of 400000; above it delta is of out: at 8 x 24 tokens 1.3 times.
-constexpr int kFewKeys = 32;
-template <typename T>
-__global__ void __launch_bounds__(256) attention_delta_few_keys(const AttnCall c) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), row = item / c.heads;
-  const int head = (int)(item - row * c.heads), kh = head / c.group;
-  int seq = 0, token = 0;
-  if (row < c.rows && in_sequence(c.q_offsets, c.q_lengths, c.sequences, c.q_tokens, row, &seq, &token)) {
-    const T *const q = static_cast<const T *>(c.q.p) + seq * c.q.seq + token * c.q.token + head * c.q.head;
-    const T *const d = static_cast<const T *>(c.dout.p) + seq * c.dout.seq + token * c.dout.token + head * c.dout.head;
-    int s = seq;
-    if (c.q_offsets) {  // the last sequence that begins at or before the row
-      int lo = 0, hi = c.sequences;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (clamped(c.q_offsets, mid, c.q_tokens) <= row) lo = mid; else hi = mid;
-      }
-      s = lo;
-    }
-    const Span qs = own_span(c.q_offsets, c.q_lengths, c.q_offsets ? s + 1 : s, c.sequences, c.q_tokens);
-    const Span ks = own_span(c.k_offsets, c.k_lengths, c.k_offsets ? s + 1 : s, c.sequences, c.k_tokens);
-    const int i = c.q_offsets ? (int)(row - qs.row) : token;
-    const int64_t place = (int64_t)head * c.rows + row;
-    const int seen = seen_keys(c.causal, i, qs.valid, ks.valid);
-    float term = 0.f;
-    constexpr int E = 16 / sizeof(T);
-    for (int j = lane; j < seen; j += 32) {
-      const int64_t at = c.k_offsets ? ks.row + j : j;
-      const T *const k = static_cast<const T *>(c.k.p) + ks.seq * c.k.seq + at * c.k.token + kh * c.k.head;
-      const T *const v = static_cast<const T *>(c.v.p) + ks.seq * c.v.seq + at * c.v.token + kh * c.v.head;
-      float score = 0.f, dprob = 0.f;
-#pragma unroll 2
-      for (int col = 0; col < c.d; col += E) {
-        float x[4][E];
-        unpack16<T>(load_vector(q + col, c.d - col), x[0]);
-        unpack16<T>(load_vector(k + col, c.d - col), x[1]);
-        unpack16<T>(load_vector(d + col, c.d - col), x[2]);
-        unpack16<T>(load_vector(v + col, c.d - col), x[3]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          score = fmaf(x[0][e], x[1][e], score);
-          dprob = fmaf(x[2][e], x[3][e], dprob);
-        }
-      }
-      float p = expf(score * c.scale - c.lse[place]) * dprob;
-      if (c.drop) {
-        const uint64_t z = dropout_draw(dropout_row(c.draws(), row, c.heads, head), j);
-        p = draw_lane(z, j & 3) >= c.drop ? p * c.keep_scale : 0.f;
-      }
-      term += p;
-    }
-    const float delta = warp_sum(term);
-    if (lane == 0) c.delta[place] = delta;
-  }
-}
-
-// What that kernel reads, in products.  A causal call's rows before its last
-// k_tokens see no key and are not counted, though each still takes a warp: causal
-// bf16 8 x 1024 queries over 2 keys, 12 heads of 64, 41 / 76 us for dq and dk 2.25
-// times as far off or 1.0; 2 x 2115 over 8, 24 heads of 128, 70 / 104 for 1.6 or 1.0.
-constexpr double kFewKeysWork = 400000.0;
-inline double few_keys_work(const AttnCall &c) {
-  const double keys = c.k_offsets ? (double)c.k_tokens : (double)c.sequences * c.k_tokens;
-  const double rows = (double)c.rows;
-  return (c.causal && keys < rows ? keys : rows) * c.heads * c.d;
-}
-
-template <typename T>
-cudaError_t delta_launch(const AttnCall &c, bool vec, cudaStream_t s) {
-  if (sizeof(T) == 2 && c.k_tokens <= kFewKeys && few_keys_work(c) <= kFewKeysWork)
-    return launch_kernel(attention_delta_few_keys<T>, dim3((unsigned)((c.rows * c.heads + 7) / 8)), 256, 0, false, s, c);
+  const auto even = [](const Strided &t) {
+    return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
+  };
+  const bool vec = c.d % E == 0 && even(c.dout) && even(c.out) &&
+                   (sizeof(T) == 4 || (even(c.q) && even(c.k) && even(c.v)));
   const int lanes = vec ? (c.d * (int)sizeof(T) + 15) / 16 : 32;
   const int team = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const int64_t each = 256 / team * kItems;
-  const dim3 grid((unsigned)((c.rows * c.heads + each - 1) / each));
-  if (!vec) return launch_kernel(attention_delta<T, 32, false>, grid, 256, 0, false, s, c);
-  return team == 8    ? launch_kernel(attention_delta<T, 8, true>, grid, 256, 0, false, s, c)
-         : team == 16 ? launch_kernel(attention_delta<T, 16, true>, grid, 256, 0, false, s, c)
-                      : launch_kernel(attention_delta<T, 32, true>, grid, 256, 0, false, s, c);
+  // blocks for rows of few keys: a warp each, or as many for a sequence as keep the SMs busy
+  int64_t few = 0, parts = 0;
+  const bool all_long = !c.causal && !c.k_offsets && !c.k_lengths && c.k_tokens > kFewKeys;
+  if (sizeof(T) == 2 && c.sequences && !all_long) {
+    const int64_t rows = c.causal ? std::min(c.q_tokens, kFewKeys - 1) : c.q_tokens;
+    parts = std::max<int64_t>(1, std::min<int64_t>((rows * c.heads + 7) / 8, 16 * device_sms() / c.sequences));
+    few = c.sequences * parts;
+  }
+  const dim3 grid((unsigned)((c.rows * c.heads + each - 1) / each + few));
+  const auto launch = [&](auto kern) {
+    return launch_kernel(kern, grid, 256, 0, false, s, c, (int)few, (int)parts);
+  };
+  if (!vec) return launch(attention_delta<T, 32, false>);
+  return team == 8    ? launch(attention_delta<T, 8, true>)
+         : team == 16 ? launch(attention_delta<T, 16, true>)
+                      : launch(attention_delta<T, 32, true>);
 }
 
 // One tensor of a call and what is made of it.
@@ -555,14 +605,7 @@ cudaError_t forward_typed(AttnCall c, const Plan &p, int type, char *workspace, 
 
 template <typename T>
 cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace, cudaStream_t s) {
-  constexpr int E = 16 / sizeof(T);
-  cudaError_t e = cudaSuccess;
-  if (c.rows) {
-    const auto even = [](const Strided &t) {
-      return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
-    };
-    e = delta_launch<T>(c, c.d % E == 0 && even(c.dout) && even(c.out), s);
-  }
+  cudaError_t e = c.rows ? delta_launch<T>(c, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
   SplitParts parts = {};
   if (p.width) e = make_parts<T>(&c, p, true, workspace, &parts, s);

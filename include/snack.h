@@ -537,9 +537,9 @@ snack_status snack_attention_forward(const snack_attention_args *args, void *out
  *   dS[i][j] = P[i][j] * (M[i][j] * (dout[i] . v[j]) - delta[i]),
  *   dq[i] = scale * sum_j dS[i][j] k[j],   dk[j] = scale * sum_i dS[i][j] q[i],
  *   dv[j] = sum_i M[i][j] P[i][j] dout[i],
- * dk and dv summed over the query heads that share them.  16-bit calls of some
- * rows over at most 32 keys (see attention.cu) take delta as the sum over j of
- * M[i][j] P[i][j] (dout[i] . v[j]) instead, without out's rounding.  A query that
+ * dk and dv summed over the query heads that share them.  In 16-bit types the delta
+ * of a query that sees at most 32 keys is the sum over j of M[i][j] P[i][j]
+ * (dout[i] . v[j]) instead, without out's rounding.  A query that
  * sees one key moves no score, so its dS is exactly 0 (with dropout too: delta and
  * the term are one value).  dq, dk and dv are
  * overwritten and must not overlap one another or an input; each may be NULL.

@@ -156,3 +156,62 @@ def test_heads_whose_values_lie_far_apart(length):
     assert torch.equal(got[1], want[1]) and torch.equal(got[0], want[0] * both)
     assert torch.equal(got[2], want[2] * both.flip(0)) and torch.equal(got[4], want[4] * powers.flip(0))
     assert torch.equal(got[3], want[3] * powers * powers * powers.flip(0))
+
+
+# ---------------------------------------------------------------- queries that see few keys
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("form", ["wide", "long", "padded", "all", "ragged", "other", "odd"])
+def test_queries_of_few_keys_do_not_read_out(dtype, form):
+    """delta of a query that sees 2 to 32 keys comes from the tensors, whatever else is in the call:
+    the gradients are the same, bit for bit, with another out in those rows.  The keys of the other
+    queries do matter to it: with another out there dq changes."""
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(21)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    ends = lambda *v: ints(0, *torch.tensor(v).cumsum(0).tolist())  # noqa: E731
+    heads, key_heads, d, causal, opts = 12, 4, 128, True, {}
+    if form == "wide":  # many sequences of few tokens
+        shape, kshape = (64, 33), (64, 33)
+    elif form == "long":  # the first rows of long sequences
+        shape = kshape = (2, 1500)
+    elif form == "padded":
+        shape = kshape = (5, 300)
+        opts = dict(q_lengths=ints(300, 2, 20, 33, 0), k_lengths=ints(300, 2, 20, 33, 0))
+    elif form == "all":  # every key seen
+        shape, kshape, causal = (4, 200), (4, 600), False
+        opts = dict(k_lengths=ints(32, 600, 5, 33))
+    elif form == "ragged":
+        at = ends(2, 0, 500, 31, 33, 1, 7)
+        shape = kshape = (574,)
+        opts = dict(q_offsets=at, k_offsets=at)
+    elif form == "other":
+        shape, kshape = (260,), (340,)
+        opts = dict(q_offsets=ends(20, 200, 40), k_offsets=ends(22, 300, 18))
+    else:
+        shape, kshape, d = (3, 90), (3, 90), 65
+    q, dout = (rnd(g, (*shape, heads, d), dtype) for _ in range(2))
+    k, v = (rnd(g, (*kshape, key_heads, d), dtype) for _ in range(2))
+    opts = dict(opts, causal=causal, dropout=0.2, seed=5)
+    out, lse = sn.snack_attention_forward(q, k, v, **opts)
+    want = sn.snack_attention_backward(dout, q, k, v, out, lse, **opts)
+    few = torch.zeros(shape, dtype=torch.bool, device="cuda")
+    if len(shape) == 1:
+        qo, ko = opts["q_offsets"].tolist(), opts["k_offsets"].tolist()
+        spans = [(slice(a, b), b - a, y - x) for a, b, x, y in zip(qo, qo[1:], ko, ko[1:])]
+    else:
+        ql = opts["q_lengths"].tolist() if "q_lengths" in opts else [shape[1]] * shape[0]
+        kl = opts["k_lengths"].tolist() if "k_lengths" in opts else [kshape[1]] * shape[0]
+        spans = [((n, slice(0, a)), a, b) for n, (a, b) in enumerate(zip(ql, kl))]
+    for at, nq, nk in spans:
+        i = torch.arange(nq, device="cuda")
+        few[at] = (i + nk - nq + 1 if causal else i * 0 + nk) <= 32
+    assert few.any() and not few.all()
+    other = torch.where(few[..., None, None], out * (1 + torch.finfo(dtype).eps), out)
+    got = sn.snack_attention_backward(dout, q, k, v, other, lse, **opts)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    rest = torch.where(few[..., None, None], out, out * 1.5)
+    assert not torch.equal(sn.snack_attention_backward(dout, q, k, v, rest, lse, **opts)[0], want[0])
+    import attention_ref
+    attention_ref.assert_within(dict(zip(("dq", "dk", "dv"), want)),
+                                attention_ref.attention(q, k, v, dout=dout, **opts))
