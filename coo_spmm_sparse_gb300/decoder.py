@@ -8,8 +8,9 @@ Every block's four projections (c_attn 768->2304, attention c_proj
 768->768, c_fc 768->3072, MLP c_proj 3072->768) are ``SnackLinear`` layers
 at the given sparsity: their forward and backward run in the library's
 kernels, and so does the causal attention between them
-(``snack_packed_attention`` on c_attn's output).  Token and position
-embeddings, layer norms, GELU and the tied LM head stay dense PyTorch: the
+(``snack_packed_attention`` on c_attn's output; heads of more than 128
+columns, which it does not take, attend through PyTorch, without dropout).
+Token and position embeddings, layer norms, GELU and the tied LM head stay dense PyTorch: the
 paper makes only the Linear projections sparse.
 
 ``dropout`` (0 by default) is GPT-2's: of the embeddings, of the attention's
@@ -76,11 +77,21 @@ class Block(torch.nn.Module):
         return [self.c_attn, self.attn_c_proj, self.c_fc, self.mlp_c_proj]
 
     def forward(self, x: torch.Tensor, dropout: float = 0.0, seed: int = 0) -> torch.Tensor:
-        a = snack_packed_attention(self.c_attn(self.ln_1(x)), self.heads, dropout=dropout,
-                                   seed=seed)
+        a = attend(self.c_attn(self.ln_1(x)), self.heads, dropout, seed)
         x = join(x, self.attn_c_proj(a), dropout, seed + 1)
         return join(x, self.mlp_c_proj(F.gelu(self.c_fc(self.ln_2(x)), approximate="tanh")),
                     dropout, seed + 2)
+
+
+def attend(qkv: torch.Tensor, heads: int, dropout: float = 0.0, seed=0) -> torch.Tensor:
+    """Causal self-attention of a projection's output [B][T][3 * d]."""
+    B, T, width = qkv.shape
+    if width // (3 * heads) <= 128:
+        return snack_packed_attention(qkv, heads, dropout=dropout, seed=seed)
+    if dropout:
+        raise ValueError("dropout takes heads of at most 128 columns")
+    q, k, v = (t.unflatten(-1, (heads, -1)).transpose(1, 2) for t in qkv.split(width // 3, dim=-1))
+    return F.scaled_dot_product_attention(q, k, v, is_causal=True).transpose(1, 2).flatten(-2)
 
 
 def join(x: torch.Tensor, y: torch.Tensor, dropout: float, seed: int) -> torch.Tensor:

@@ -21,9 +21,8 @@ from __future__ import annotations
 import torch
 import torch.nn.functional as F
 
-from . import (SnackAdapters, SnackResidualNorm, snack_clip_grad_norm, snack_packed_attention,
-               snack_residual_norm)
-from .decoder import DecoderConfig, SparseDecoder
+from . import SnackAdapters, SnackResidualNorm, snack_clip_grad_norm, snack_residual_norm
+from .decoder import DecoderConfig, SparseDecoder, attend
 
 
 class AdaptedBlock(torch.nn.Module):
@@ -46,7 +45,7 @@ class AdaptedBlock(torch.nn.Module):
 
     def attention(self, h, requests):
         b = self.block
-        a = snack_packed_attention(self.project(0, b.c_attn, h, requests), b.heads)
+        a = attend(self.project(0, b.c_attn, h, requests), b.heads)
         return self.project(1, b.attn_c_proj, a, requests)
 
     def mlp(self, h, requests):
