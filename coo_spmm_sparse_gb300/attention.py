@@ -112,11 +112,13 @@ class _PackedAttentionFunction(torch.autograd.Function):
         ragged = opts.get("q_offsets") is not None
         q, k, v = _split(qkv, heads, key_heads, ragged)
         out, lse = snack_attention_forward(q, k, v, **opts)
+        # the same memory as a tensor that is nothing's view: a caller may write to it
+        out = torch.ops.aten._unsafe_view(out, (*qkv.shape[:-1], heads * q.shape[-1]))
         ctx.shape = heads, key_heads, ragged
         ctx.names = [n for n, t in opts.items() if isinstance(t, torch.Tensor)]
         ctx.opts = {n: t for n, t in opts.items() if n not in ctx.names}
         ctx.save_for_backward(qkv, out, lse, *(opts[n] for n in ctx.names))
-        return out.flatten(-2)
+        return out
 
     @staticmethod
     @first_derivative
@@ -125,8 +127,8 @@ class _PackedAttentionFunction(torch.autograd.Function):
         q, k, v = _split(qkv, *ctx.shape)
         grad = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
         dq, dk, dv = _split(grad, *ctx.shape)
-        snack_attention_backward(_rows_contiguous(dout).unflatten(-1, out.shape[-2:]), q, k, v, out,
-                                 lse, dq=dq, dk=dk, dv=dv, **ctx.opts,
+        snack_attention_backward(_rows_contiguous(dout).unflatten(-1, q.shape[-2:]), q, k, v,
+                                 out.unflatten(-1, q.shape[-2:]), lse, dq=dq, dk=dk, dv=dv, **ctx.opts,
                                  **dict(zip(ctx.names, rest)))
         return grad, None, None, None
 

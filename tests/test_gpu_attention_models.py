@@ -30,3 +30,29 @@ def test_heads_of_more_than_128_columns():
     assert torch.isfinite(loss)
     with pytest.raises(ValueError, match="at most 128"):
         small(d=512, heads=2, dropout=0.1)(idx)
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_packed_attention_can_be_written_to(ragged):
+    """The result is no view: it may be written to in grad mode.  As for any function that keeps its
+    result for the gradient, a backward pass through the old value then raises."""
+    import coo_spmm_sparse_gb300 as sn
+    g = torch.Generator(device="cuda").manual_seed(1)
+    shape = (90,) if ragged else (2, 45)
+    offsets = torch.tensor([0, 30, 90], dtype=torch.int32, device="cuda") if ragged else None
+    qkv = torch.randn(*shape, 8 * 32, generator=g, device="cuda", requires_grad=True)
+    out = sn.snack_packed_attention(qkv, 4, 2, offsets=offsets)
+    assert out.shape == (*shape, 128) and out._base is None
+    keep = out.detach().clone()
+    out += 1.0
+    assert torch.equal(out.detach(), keep + 1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    with torch.no_grad():
+        again = sn.snack_packed_attention(qkv, 4, 2, offsets=offsets)
+    again.mul_(2.0)
+    assert torch.equal(again, keep * 2.0)
+    empty = sn.snack_packed_attention(qkv[:0].detach().requires_grad_(), 4, 2,
+                                      offsets=offsets[:1] if ragged else None)
+    assert empty.shape == (0, *shape[1:], 128)
+    empty.sum().backward()
