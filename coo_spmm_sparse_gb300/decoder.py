@@ -16,7 +16,10 @@ paper makes only the Linear projections sparse.
 ``dropout`` (0 by default) is GPT-2's: of the embeddings, of the attention's
 probabilities and of a block's outputs before they join the residual stream,
 while the model is in training mode.  Call n of the model draws its masks
-from seeds 4096 * n + place.
+from seeds 2^40 * mask_seed + 4096 * n + place (place 0: the embeddings;
+4 i + 1 .. 4 i + 3: block i), on the device.  n counts the calls in a buffer
+that is part of the state of a model with dropout, and of a captured step; a
+call that is made again (activation checkpointing) has to name its n.
 
 The training step is plain SGD on every parameter (the sparse values are
 updated in place through their Parameter views) and, every
@@ -54,6 +57,7 @@ class DecoderConfig:
     std: float = 0.02
     seed: int = 0
     dropout: float = 0.0
+    mask_seed: int | None = None  # of dropout's masks, below 2^23; None: seed.  Ranks take unlike ones
 
 
 class Block(torch.nn.Module):
@@ -76,11 +80,11 @@ class Block(torch.nn.Module):
     def sparse_layers(self):
         return [self.c_attn, self.attn_c_proj, self.c_fc, self.mlp_c_proj]
 
-    def forward(self, x: torch.Tensor, dropout: float = 0.0, seed: int = 0) -> torch.Tensor:
-        a = attend(self.c_attn(self.ln_1(x)), self.heads, dropout, seed)
-        x = join(x, self.attn_c_proj(a), dropout, seed + 1)
+    def forward(self, x: torch.Tensor, dropout: float = 0.0, seeds=(0, 0, 0)) -> torch.Tensor:
+        a = attend(self.c_attn(self.ln_1(x)), self.heads, dropout, seeds[0])
+        x = join(x, self.attn_c_proj(a), dropout, seeds[1])
         return join(x, self.mlp_c_proj(F.gelu(self.c_fc(self.ln_2(x)), approximate="tanh")),
-                    dropout, seed + 2)
+                    dropout, seeds[2])
 
 
 def attend(qkv: torch.Tensor, heads: int, dropout: float = 0.0, seed=0) -> torch.Tensor:
@@ -94,7 +98,7 @@ def attend(qkv: torch.Tensor, heads: int, dropout: float = 0.0, seed=0) -> torch
     return F.scaled_dot_product_attention(q, k, v, is_causal=True).transpose(1, 2).flatten(-2)
 
 
-def join(x: torch.Tensor, y: torch.Tensor, dropout: float, seed: int) -> torch.Tensor:
+def join(x: torch.Tensor, y: torch.Tensor, dropout: float, seed) -> torch.Tensor:
     """x + y, with dropout of y."""
     return snack_dropout(y, dropout, seed, residual=x) if dropout else x + y
 
@@ -114,28 +118,61 @@ class SparseDecoder(torch.nn.Module):
             self.wpe.weight.copy_(torch.randn(cfg.ctx, cfg.d, generator=g) * 0.01)
         self.blocks = torch.nn.ModuleList(Block(cfg, i) for i in range(cfg.layers))
         self.ln_f = torch.nn.LayerNorm(cfg.d, device=dev)
-        self.calls = 0  # with dropout; its masks' seeds follow
+        mask_seed = cfg.seed if cfg.mask_seed is None else cfg.mask_seed
+        self.register_buffer("_calls", torch.zeros((), dtype=torch.long), persistent=cfg.dropout > 0)
+        self.register_buffer("_places", torch.arange(4 * cfg.layers + 1) + (mask_seed % 2 ** 23 << 40),
+                             persistent=False)
         self.to(dev)
+
+    @property
+    def calls(self) -> int:
+        """Calls with dropout so far (read from the device)."""
+        return int(self._calls)
+
+    @calls.setter
+    def calls(self, n: int):
+        self._calls.fill_(n)
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        if self.cfg.dropout:  # a state of a model without dropout, or from before the calls were part of it
+            state_dict.setdefault(prefix + "_calls", self._calls)
+        else:
+            state_dict.pop(prefix + "_calls", None)
+        super()._load_from_state_dict(state_dict, prefix, *args)
+
+    def mask_seeds(self, call: int | None = None):
+        """(dropout, seeds of the places) of a call: the next one, which is counted, or number `call`."""
+        p = self.cfg.dropout if self.training else 0.0
+        if not p:
+            return 0.0, [0] * (4 * self.cfg.layers + 1)
+        if 4 * self.cfg.layers >= 4096:
+            raise ValueError("dropout takes at most 1023 blocks")
+        if call is not None:
+            return p, (self._places + 4096 * call).unbind()
+        if torch._C._current_graph_task_id() != -1:
+            raise RuntimeError("a call inside a backward pass (activation checkpointing) would draw other masks "
+                               "than the one it repeats: give both the call's number, model(idx, call=n)")
+        seeds = torch.add(self._places, self._calls, alpha=4096).unbind()
+        self._calls.add_(1)
+        return p, seeds
 
     def sparse_layers(self):
         return [lin for b in self.blocks for lin in b.sparse_layers()]
 
-    def forward(self, idx: torch.Tensor) -> torch.Tensor:
+    def forward(self, idx: torch.Tensor, call: int | None = None) -> torch.Tensor:
         B, T = idx.shape
         pos = torch.arange(T, device=idx.device)
         x = self.wte(idx) + self.wpe(pos)
-        p = self.cfg.dropout if self.training else 0.0
-        seed = 4096 * self.calls
+        p, seeds = self.mask_seeds(call)
         if p:
-            self.calls += 1
-            x = snack_dropout(x, p, seed)
+            x = snack_dropout(x, p, seeds[0])
         for i, b in enumerate(self.blocks):
-            x = b(x, p, seed + 4 * i + 1)
+            x = b(x, p, seeds[4 * i + 1: 4 * i + 4])
         return F.linear(self.ln_f(x), self.wte.weight)  # tied LM head
 
-    def loss(self, idx: torch.Tensor) -> torch.Tensor:
+    def loss(self, idx: torch.Tensor, call: int | None = None) -> torch.Tensor:
         """Next-token cross-entropy of a [B][T] token batch."""
-        logits = self.forward(idx)
+        logits = self.forward(idx, call)
         return F.cross_entropy(logits[:, :-1].reshape(-1, logits.shape[-1]),
                                idx[:, 1:].reshape(-1))
 

@@ -56,3 +56,75 @@ def test_packed_attention_can_be_written_to(ragged):
                                       offsets=offsets[:1] if ragged else None)
     assert empty.shape == (0, *shape[1:], 128)
     empty.sum().backward()
+
+
+def test_masks_are_part_of_the_models_state():
+    a, idx = small(dropout=0.2), tokens()
+    first = [a(idx).detach() for _ in range(3)]
+    assert a.calls == 3 and not torch.equal(first[0], first[1])
+    b = small(dropout=0.2)
+    b.load_state_dict(a.state_dict())
+    assert b.calls == 3
+    assert torch.equal(a(idx), b(idx))
+    for n in range(3):
+        assert torch.equal(b(idx, call=n), first[n])
+    assert b.calls == 4
+    b.eval()
+    b(idx)
+    assert b.calls == 4
+    plain = small()
+    assert not [k for k in plain.state_dict() if "_calls" in k or "_places" in k]
+    older = {k: v for k, v in a.state_dict().items() if k != "_calls"}
+    small(dropout=0.2).load_state_dict(older)
+    plain.load_state_dict(older)
+    plain.load_state_dict(a.state_dict())
+
+
+def test_masks_follow_the_models_seed():
+    from coo_spmm_sparse_gb300.decoder import DecoderConfig, SparseDecoder
+    import attention_ref
+    idx = tokens()
+    base = dict(vocab=128, ctx=64, d=192, heads=4, layers=1, mlp=384, sparsity=80.0, std=0.1, dropout=0.2)
+    a = SparseDecoder(DecoderConfig(**base))
+    others = [SparseDecoder(DecoderConfig(**base, mask_seed=m)) for m in (0, 1, 2)]
+    got = [m(idx) for m in (a, *others)]
+    assert torch.equal(got[0], got[1])
+    assert not torch.equal(got[1], got[2]) and not torch.equal(got[2], got[3])
+    assert [int(s) for s in others[2].mask_seeds()[1][:2]] == [2 * 2 ** 40 + 4096, 2 * 2 ** 40 + 4097]
+    # the embeddings' mask is that of the documented seed
+    x = torch.ones(300, device="cuda")
+    import coo_spmm_sparse_gb300 as sn
+    M = attention_ref.mask_of(2 ** 40 + 4096 * 5, torch.zeros(1, dtype=torch.long, device="cuda"), 300, 0.2)
+    assert torch.equal(sn.snack_dropout_forward(x, 0.2, others[1].mask_seeds(call=5)[1][0]) != 0, M.flatten() != 0)
+
+
+def test_a_captured_call_draws_new_masks_at_every_replay():
+    model, idx = small(dropout=0.2), tokens()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.no_grad(), torch.cuda.stream(side):
+        model(idx)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(graph):
+        logits = model(idx)
+    start = model.calls
+    for n in range(3):
+        graph.replay()
+        got = logits.clone()
+        with torch.no_grad():
+            assert torch.equal(got, model(idx, call=start + n))
+    assert model.calls == start + 3
+
+
+def test_a_call_that_is_made_again_draws_its_own_masks():
+    from torch.utils.checkpoint import checkpoint
+    model, idx = small(dropout=0.2), tokens()
+    model(idx, call=7).sum().backward()
+    want = {n: p.grad.clone() for n, p in model.named_parameters()}
+    model.zero_grad()
+    checkpoint(lambda i: model(i, call=7), idx, use_reentrant=False).sum().backward()
+    for n, p in model.named_parameters():
+        assert torch.allclose(p.grad, want[n], rtol=1e-4, atol=1e-5 * float(want[n].abs().max())), n
+    with pytest.raises(RuntimeError, match="call=n"):
+        checkpoint(lambda i: model(i), idx, use_reentrant=False).sum().backward()
