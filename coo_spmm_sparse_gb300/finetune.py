@@ -8,7 +8,8 @@ adapters.  Its blocks run through ``snack_residual_norm``: the add of a
 block's output and the layer norm that follows are one call, optionally with
 a norm of the output itself and a learned gate per channel.  With new
 adapters (B = 0), gates of 1 and no output norm it computes what the decoder
-it wraps computes.
+it wraps computes, its dropout included: in training mode the base's
+probability and masks apply (``call`` as in the decoder).
 
 ``FineTuner`` trains the adapters and gates: plain SGD on gradients clipped
 to a global norm (``snack_clip_grad_norm`` over all of them).
@@ -21,7 +22,8 @@ from __future__ import annotations
 import torch
 import torch.nn.functional as F
 
-from . import SnackAdapters, SnackResidualNorm, snack_clip_grad_norm, snack_residual_norm
+from . import (SnackAdapters, SnackResidualNorm, snack_clip_grad_norm, snack_dropout,
+               snack_residual_norm)
 from .decoder import DecoderConfig, SparseDecoder, attend
 
 
@@ -43,9 +45,9 @@ class AdaptedBlock(torch.nn.Module):
     def project(self, k: int, lin, x, requests):
         return self.adapters[k](x, lin(x), *requests)
 
-    def attention(self, h, requests):
+    def attention(self, h, requests, dropout: float = 0.0, seed=0):
         b = self.block
-        a = attend(self.project(0, b.c_attn, h, requests), b.heads)
+        a = attend(self.project(0, b.c_attn, h, requests), b.heads, dropout, seed)
         return self.project(1, b.attn_c_proj, a, requests)
 
     def mlp(self, h, requests):
@@ -53,6 +55,10 @@ class AdaptedBlock(torch.nn.Module):
         return self.project(3, b.mlp_c_proj,
                             F.gelu(self.project(2, b.c_fc, h, requests), approximate="tanh"),
                             requests)
+
+
+def _drop(y, dropout: float, seed):
+    return snack_dropout(y, dropout, seed) if dropout else y
 
 
 def _join(norm: SnackResidualNorm, x, y, following: torch.nn.LayerNorm):
@@ -83,22 +89,24 @@ class AdaptedDecoder(torch.nn.Module):
         """The parameters that fine-tuning changes."""
         return [p for p in self.parameters() if p.requires_grad]
 
-    def forward(self, idx: torch.Tensor, requests) -> torch.Tensor:
+    def forward(self, idx: torch.Tensor, requests, call: int | None = None) -> torch.Tensor:
         base = self.base
         pos = torch.arange(idx.shape[1], device=idx.device)
-        x = base.wte(idx) + base.wpe(pos)
+        p, seeds = base.mask_seeds(call)
+        x = _drop(base.wte(idx) + base.wpe(pos), p, seeds[0])
         first = base.blocks[0].ln_1
         x, h = snack_residual_norm(x, next_weight=first.weight, next_bias=first.bias,
                                    eps=first.eps)
         for i, b in enumerate(self.blocks):
-            x, h = _join(b.joins[0], x, b.attention(h, requests), b.block.ln_2)
+            s = seeds[4 * i + 1: 4 * i + 4]
+            x, h = _join(b.joins[0], x, _drop(b.attention(h, requests, p, s[0]), p, s[1]), b.block.ln_2)
             after = base.blocks[i + 1].ln_1 if i + 1 < len(self.blocks) else base.ln_f
-            x, h = _join(b.joins[1], x, b.mlp(h, requests), after)
+            x, h = _join(b.joins[1], x, _drop(b.mlp(h, requests), p, s[2]), after)
         return F.linear(h, base.wte.weight)
 
-    def loss(self, idx: torch.Tensor, requests) -> torch.Tensor:
+    def loss(self, idx: torch.Tensor, requests, call: int | None = None) -> torch.Tensor:
         """Next-token cross-entropy of a [B][T] token batch."""
-        logits = self.forward(idx, requests)
+        logits = self.forward(idx, requests, call)
         return F.cross_entropy(logits[:, :-1].reshape(-1, logits.shape[-1]),
                                idx[:, 1:].reshape(-1))
 

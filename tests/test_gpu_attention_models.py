@@ -128,3 +128,24 @@ def test_a_call_that_is_made_again_draws_its_own_masks():
         assert torch.allclose(p.grad, want[n], rtol=1e-4, atol=1e-5 * float(want[n].abs().max())), n
     with pytest.raises(RuntimeError, match="call=n"):
         checkpoint(lambda i: model(i), idx, use_reentrant=False).sum().backward()
+
+
+def test_adapted_decoder_drops_what_its_base_drops():
+    """New adapters add nothing: the logits of a call are the base's of the same call, in training
+    mode with its masks (two orders of 32-bit sums: 1e-4 of the largest), outside it without."""
+    from coo_spmm_sparse_gb300.finetune import AdaptedDecoder, FineTuner, sequences
+    base, idx = small(dropout=0.3), tokens()
+    model = AdaptedDecoder(base, adapters=2, rank=4)
+    requests = sequences(2, 64, [0, 1])
+    with torch.no_grad():
+        want, got = base(idx, call=3), model(idx, requests, call=3)
+        assert float((got - want).abs().max()) <= 1e-4 * float(want.abs().max())
+        other = model(idx, requests, call=4)
+        assert float((other - want).abs().max()) > 1e-2 * float(want.abs().max())
+        model.eval()
+        want = base(idx)
+        assert float((model(idx, requests) - want).abs().max()) <= 1e-4 * float(want.abs().max())
+        model.train()
+    assert base.calls == 0
+    loss, _ = FineTuner(model).step(idx, requests)
+    assert torch.isfinite(loss) and base.calls == 1
