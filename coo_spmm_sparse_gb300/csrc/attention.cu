@@ -496,15 +496,26 @@ void plan_parts(Plan *p, const AttnCall &c, int type, bool backward) {
 // fp32, where the operands are made first: forward 4 x 256 x 256 28, 29; 8 x 256
 // x 256 (6e6) 32, 55; backward, 8 x 256 x 256, 66, 132.
 // Few rows over many keys are too few for the forward tiles even with the keys
-// in parts.
+// in parts.  A ragged side's lengths are not known here, only their mean; a tile holds
+// one sequence's tokens.  Forward, bf16, 24 heads over 8 of 128, tiles / without, us:
+// 128 x 1 over 500 keys each 228 / 56; 256 x 8 tokens 291 / 86; 128 x 16 139 / 56; but 1 x
+// 2000 and 127 x 1 162 / 176, 1 x 4000 and 255 x 4 376 / 591 (mean 20; fp32, 12 heads of
+// 64, 295 / 659): without below a mean of 16.  Backward, where the keys' side counts too,
+// 128 x 1 over 500 619 / 720, 256 x 8 496 / 285, 1 x 2000 and 127 x 1 315 / 771: tiles.
 bool worth_tiles(const AttnCall &c, int type, bool backward) {
   if (c.q_tokens < 64 || c.k_tokens < 64) return false;
+  if (c.q_offsets && !backward && c.q_tokens < (int64_t)16 * c.sequences) return false;
   const double rows = (double)c.rows * c.heads, x = rows * c.k_tokens;
   return x >= (type == SNACK_F32 && !backward ? 4e6 : 2e6) && (backward || rows >= 1024);
 }
 
-// Off the tiles, few rows (16 to a block) where blocks of 128 would leave SMs
-// idle; and the keys in parts where the blocks still do.
+// Off the tiles, 16 rows to a block where blocks of 128 would leave SMs idle, and
+// where a sequence has few rows for its key head (tokens * group; the mean on a ragged
+// side), so that most of a block of 128 would be empty.  bf16, 128 rows / 16, us:
+// decoding 128 requests over 500 keys, 24 heads over 8 of 128 (3 rows) 187 / 53; 512 over
+// 1024 1358 / 307; fp32 12 heads of 64 537 / 113; 8 tokens of a group of 3 (24 rows) 167 /
+// 123, of 4 (32) 39 / 45; 16 of 3 (48) 29 / 35.  The keys in parts where the blocks
+// still leave SMs idle.
 Plan plan_forward(const AttnCall &c, int type) {
   Plan p;
   const int64_t sms = device_sms();
@@ -518,7 +529,8 @@ Plan plan_forward(const AttnCall &c, int type) {
     want = blocks ? sms / blocks : 1;
   } else {
     const bool ragged = c.q_offsets != nullptr;
-    p.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms;
+    p.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms ||
+            (int64_t)c.q_tokens * c.group <= (int64_t)24 * (ragged ? c.sequences : 1);
     if (!p.few) return p;
     blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
     least = 512;

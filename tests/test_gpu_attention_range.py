@@ -215,3 +215,26 @@ def test_queries_of_few_keys_do_not_read_out(dtype, form):
     import attention_ref
     attention_ref.assert_within(dict(zip(("dq", "dk", "dv"), want)),
                                 attention_ref.attention(q, k, v, dout=dout, **opts))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group,d", [(1, 64), (3, 128), (8, 80)])
+def test_many_sequences_of_few_queries(dtype, group, d):
+    """On both sides of the rules that go by the rows of a sequence: decoding large batches, packed
+    requests of 1 to 20 new tokens, one long sequence among many short ones."""
+    import attention_ref
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(group)
+    for n, nq, nk in ((200, 1, 100), (150, 24 // group, 70), (150, 24 // group + 1, 70)):
+        q, k, v = (rnd(g, (n, t, h, d), dtype) for t, h in ((nq, 2 * group), (nk, 2), (nk, 2)))
+        fill = torch.randint(nq, nk + 1, (n,), generator=g, device="cuda").to(torch.int32)
+        opts = dict(k_lengths=fill, dropout=0.2, seed=1)
+        got = sn.snack_attention_forward(q, k, v, **opts)
+        attention_ref.assert_within(dict(zip(("out", "lse"), got)), attention_ref.attention(q, k, v, **opts))
+    for lq, lk in (([1] * 128, [90] * 128), ([15] * 150, [20] * 150), ([16] * 150, [16] * 150),
+                   ([1500] + [1] * 100, [1500] + [3] * 100), ([0, 20, 1] * 40, [5, 40, 0] * 40)):
+        ends = [torch.tensor([0, *l], device="cuda").cumsum(0).to(torch.int32) for l in (lq, lk)]
+        q, k, v = (rnd(g, (t, h, d), dtype) for t, h in ((sum(lq), 2 * group), (sum(lk), 2), (sum(lk), 2)))
+        opts = dict(q_offsets=ends[0], k_offsets=ends[1])
+        got = sn.snack_attention_forward(q, k, v, **opts)
+        attention_ref.assert_within(dict(zip(("out", "lse"), got)), attention_ref.attention(q, k, v, **opts))
