@@ -50,7 +50,7 @@ __all__ = [
     "snack_adapter_forward", "snack_adapter_backward", "SnackAdapters",
     "SnackTensorList", "snack_tensor_list", "snack_grad_norm", "snack_clip_grad_norm",
     "snack_attention_forward", "snack_attention_backward", "snack_attention", "snack_packed_attention",
-    "snack_attention_error",
+    "snack_attention_error", "snack_debug_attention_polls",
     "snack_dropout_forward", "snack_dropout_backward", "snack_dropout",
 ]
 
@@ -493,7 +493,8 @@ class SnackLinear(torch.nn.Module):
 
 from .adapters import SnackAdapters, snack_adapter_backward, snack_adapter_forward  # noqa: E402
 from .attention import (snack_attention, snack_attention_backward,  # noqa: E402
-                        snack_attention_error, snack_attention_forward, snack_packed_attention)
+                        snack_attention_error, snack_attention_forward,
+                        snack_debug_attention_polls, snack_packed_attention)
 from .dropout import snack_dropout, snack_dropout_backward, snack_dropout_forward  # noqa: E402
 from .grad_clip import (SnackTensorList, snack_clip_grad_norm, snack_grad_norm,  # noqa: E402
                         snack_tensor_list)

@@ -55,6 +55,7 @@ SIGNATURES = {
     "snack_attention_backward_workspace": (sz, [vp]),
     "snack_attention_backward": (ctypes.c_int, [vp, vp, vp, vp]),
     "snack_attention_error": (ctypes.c_int, [P(ctypes.c_int), vp]),
+    "snack_debug_attention_polls": (None, [ctypes.c_int]),
     "snack_dropout": (ctypes.c_int, [i64, vp, ctypes.c_int, vp, vp, ctypes.c_int, f32, u64, vp,
                                      vp]),
     "snack_launch_count": (u64, []),

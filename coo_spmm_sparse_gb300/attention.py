@@ -58,10 +58,16 @@ def snack_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
 
 def snack_attention_error(stream=None) -> bool:
     """Read and clear the current device's flag: True if a kernel of an attention call gave
-    up a bounded wait since the last read (its results are then wrong).  Synchronises."""
+    up a bounded wait since the last read (its block's results are then NaN).  Synchronises."""
     flag = ctypes.c_int()
     _check(_lib.snack_attention_error(ctypes.byref(flag), _stream(stream)))
     return bool(flag.value)
+
+
+def snack_debug_attention_polls(polls: int) -> None:
+    """Test hook: waits of attention kernels launched from now on give up after so many polls
+    (negative: the usual limit)."""
+    _lib.snack_debug_attention_polls(int(polls))
 
 
 def _rows_contiguous(t):

@@ -1,14 +1,17 @@
 // Attention: argument checks, the choice of kernels, and what runs around
 // them (delta, the joining of split calls).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
 #include "attention.cuh"
+#include "tcgen05.cuh"
 
 namespace snack {
 namespace {
 
+std::atomic<int> g_polls{tc::kPolls};
 
 template <typename T>
 __device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[16 / sizeof(T)]) {
@@ -455,6 +458,7 @@ AttnCall call_of(const snack_attention_args *a) {
   c.keep_scale = c.drop ? 65536.f / (float)(65536 - c.drop) : 1.f;
   c.seed = a->seed;
   c.seed_at = a->seed_at;
+  c.polls = g_polls.load(std::memory_order_relaxed);
   return c;
 }
 
@@ -664,6 +668,10 @@ extern "C" snack_status snack_attention_error(int *flag, void *stream) {
   cudaError_t e = tile_forward_failed(flag, s);
   if (e == cudaSuccess) e = tile_backward_failed(flag, s);
   return e == cudaSuccess ? SNACK_OK : cuda_status(e, "attention error flag");
+}
+
+extern "C" void snack_debug_attention_polls(int polls) {
+  g_polls.store(polls < 0 ? tc::kPolls : polls, std::memory_order_relaxed);
 }
 
 extern "C" size_t snack_attention_backward_workspace(const snack_attention_args *a) {

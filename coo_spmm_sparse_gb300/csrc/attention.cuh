@@ -30,6 +30,7 @@ struct AttnCall {
   float keep_scale;  // 1 without dropout
   uint64_t seed;
   const uint64_t *seed_at;
+  int polls;  // of a wait on tcgen05, before it gives up
 
   __device__ __forceinline__ uint64_t draws() const { return seed_at ? *seed_at : seed; }
 };

@@ -82,24 +82,30 @@ __device__ __forceinline__ void copy_tile(unsigned char *to, const CUtensorMap *
 }
 
 // The whole warp copies a tile and sets the rows from `rows` on to zero;
-// `full` is then arrived at by one plain arrival.
+// `full` is then arrived at by one plain arrival, also where the wait gives up.
 template <int DP>
 __device__ __forceinline__ bool copy_tile_cut(unsigned char *to, const CUtensorMap *map, uint64_t *full, uint64_t *cut,
                                               int *cut_phase, int head, int token, int seq, int rows,
-                                              volatile int *failed) {
+                                              volatile int *failed, int polls) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) copy_tile<DP>(to, map, cut, head, token, seq);
   __syncwarp();
-  const bool ok = __all_sync(0xffffffffu, tc::bar_wait(cut, *cut_phase, failed));
+  const bool ok = __all_sync(0xffffffffu, tc::bar_wait(cut, *cut_phase, failed, polls));
+  if (!ok) tc::bar_drain(cut, *cut_phase);
   *cut_phase ^= 1;
-  if (!ok) return false;
   for (int x = 0; x < DP; x += 64)
     for (int i = rows * 8 + lane; i < kTile * 8; i += 32)
       *reinterpret_cast<uint4 *>(to + x / 64 * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
   tc::fence_async_proxy();
   __syncwarp();
   if (lane == 0) tc::bar_arrive(full);
-  return true;
+  return ok;
+}
+
+// What a block whose wait has given up leaves in a row of results.
+template <typename T>
+__device__ __forceinline__ void poison_row(T *row, int d) {
+  for (int e = 0; e < d; ++e) row[e] = from_float<T>(__uint_as_float(0x7fc00000u));
 }
 
 // Stores columns [0, d) of a thread's row of sums (DP of them from column

@@ -55,7 +55,7 @@ struct Tops {
 };
 // The row's, of step n; false: the wait has run out.  Whole warps.
 __device__ __forceinline__ bool row_exponent(Tops &tops, const float (&t)[kHalf], int n, uint32_t *exponent,
-                                             volatile int *failed) {
+                                             volatile int *failed, int polls) {
   const int warp = threadIdx.x >> 5, w = warp >> 2, pair = warp & 3, row = pair * 32 + (threadIdx.x & 31);
   float top[2] = {};
 #pragma unroll
@@ -66,7 +66,7 @@ __device__ __forceinline__ bool row_exponent(Tops &tops, const float (&t)[kHalf]
   *exponent = exponent_bits(fmaxf(top[0], top[1]));
   tops.exponent[n & 1][w][row] = (uint8_t)*exponent;
   tc::bar_arrive_warp(&tops.told[pair]);
-  if (!__all_sync(0xffffffffu, tc::bar_wait(&tops.told[pair], n & 1, failed))) return false;
+  if (!__all_sync(0xffffffffu, tc::bar_wait(&tops.told[pair], n & 1, failed, polls))) return false;
   *exponent = max(*exponent, (uint32_t)tops.exponent[n & 1][w ^ 1][row]);
   return true;
 }
@@ -91,7 +91,7 @@ struct KeyBars {
   uint64_t kv, q_full[2], q_empty[2], d_full[2], d_empty[2], stat_full[2], stat_empty[2];
   uint64_t scores, probs, dprobs, dscores, done, cut, drain;
   uint32_t tmem;
-  int failed;
+  int failed, copied;  // copied: tiles of queries and dout whose copies were started
   alignas(16) float lse[2][kTile];
   alignas(16) float delta[2][kTile];
   struct {
@@ -103,6 +103,25 @@ struct KeyBars {
 template <int W>
 constexpr size_t keys_smem() { return 1024 + (size_t)6 * tile_bytes<W>(); }
 
+// A block whose wait has given up (as in the forward call).
+__device__ __forceinline__ void drain_copies(KeyBars &bars) {
+  tc::bar_drain(&bars.kv, 0);
+  for (int i = max(0, bars.copied - 4); i < bars.copied; ++i)
+    tc::bar_drain(i & 1 ? &bars.d_full[i / 2 & 1] : &bars.q_full[i / 2 & 1], (i / 4) & 1);
+}
+template <typename T>
+__device__ __noinline__ void poison_keys(const AttnCall &c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kh = blockIdx.x % c.key_heads;
+  if (threadIdx.x == 0) g_attention_failed = 1;
+  const Place at = find_tile(c.k_offsets, c.sequences, c.k_tokens, 1, kTile, blockIdx.x / c.key_heads, false);
+  const Span ks = own_span(c.k_offsets, c.k_lengths, at.s, c.sequences, c.k_tokens);
+  const Strided &to = warp >> 2 ? c.dv : c.dk;
+  const int j = at.tile * kTile + (warp & 3) * 32 + lane;
+  if (j < ks.cover && to.p)
+    poison_row(static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
+                   kh * to.head, c.d);
+}
+
 // A tile of 128 keys (rows of every product: a thread has a key), past which
 // the query tiles of all heads that share it stream:
 //   S^T = K Q^T,  P^T = exp2(S^T - lse),  dP^T = V dO^T,  dS^T = P^T (dP^T - delta),
@@ -112,7 +131,7 @@ constexpr size_t keys_smem() { return 1024 + (size_t)6 * tile_bytes<W>(); }
 // does.  Scores, dP and both sums fill the 512 columns of tensor memory.
 template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    tile_backward_keys(const AttnCall c, const __grid_constant__ TileMaps maps) {
+    tile_backward_keys(const __grid_constant__ AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
   constexpr bool kSplit = Operand<T>::kSplit;
   extern __shared__ unsigned char raw[];
@@ -184,24 +203,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           uint64_t *const full = side ? &bars.d_full[slot] : &bars.q_full[slot];
           if (n >= 2)
             ok = __all_sync(0xffffffffu, tc::bar_wait(side ? &bars.d_empty[slot] : &bars.q_empty[slot],
-                                                      (n / 2 - 1) & 1, failed));
+                                                      (n / 2 - 1) & 1, failed, c.polls));
           if (!ok) break;
           unsigned char *const to = (side ? sd : sq) + slot * tile_bytes<W>();
           const CUtensorMap *const map = side ? &maps.dout : &maps.q;
           if (q0 + kTile > nq)
-            ok = copy_tile_cut<W>(to, map, full, &bars.cut, &cut_phase, head, q_token + q0, qs.seq, nq - q0, failed);
+            ok = copy_tile_cut<W>(to, map, full, &bars.cut, &cut_phase, head, q_token + q0, qs.seq, nq - q0, failed,
+                                   c.polls);
           else if (lane == 0)
             copy_tile<W>(to, map, full, head, q_token + q0, qs.seq);
           __syncwarp();
-          if (ok) ++parts;
+          ++parts;
         }
       }
-      if (*failed) {
-        int unseen = 0;
-        tc::bar_wait(&bars.kv, 0, &unseen);
-        for (int i = max(0, parts - 4); i < parts; ++i)
-          tc::bar_wait(i & 1 ? &bars.d_full[i / 2 & 1] : &bars.q_full[i / 2 & 1], (i / 4) & 1, &unseen);
-      }
+      if (lane == 0) bars.copied = parts;
     } else if (warp == kMmaWarp) {
       // the whole warp goes along, so that descriptors stay in uniform registers
       if (all > 0) {
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t q0c = tc::desc_columns(tc::smem_addr(sq), kBlock), d0c = tc::desc_columns(tc::smem_addr(sd), kBlock);
         const uint32_t t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = t_dv + DP;
         const auto wait = [&](uint64_t *bar, int phase) {
-          const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
+          const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed, c.polls));
           tc::fence_after();
           return done;
         };
@@ -257,8 +272,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tc::commit(&bars.done);
           tc::commit(&bars.drain);
         }
-        int unseen = 0;
-        tc::bar_wait(&bars.drain, 0, &unseen);
+        tc::bar_drain(&bars.drain, 0);
       }
       __syncwarp();
     } else if (warp == kStatWarp) {
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (lse[x] == -INFINITY) lse[x] = INFINITY;  // a row that sees nothing: its probabilities are zero
           delta[x] = i < nq ? c.delta[place + i] : 0.f;
         }
-        if (n >= 2 && !__all_sync(0xffffffffu, tc::bar_wait(&bars.stat_empty[slot], (n / 2 - 1) & 1, failed))) break;
+        if (n >= 2 && !__all_sync(0xffffffffu, tc::bar_wait(&bars.stat_empty[slot], (n / 2 - 1) & 1, failed, c.polls))) break;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           bars.lse[slot][lane + 32 * x] = up - lse[x];  // as they are added
@@ -322,8 +336,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int y = 0; y < 4; ++y) kept[y] = __shfl_sync(0xffffffffu, own, (lane & ~3) + y) >> (lane & 3);
       }
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.stat_full[slot], (n / 2) & 1, failed) &&
-                                       tc::bar_wait(&bars.scores, n & 1, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.stat_full[slot], (n / 2) & 1, failed, c.polls) &&
+                                       tc::bar_wait(&bars.scores, n & 1, failed, c.polls));
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
@@ -363,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.probs);
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs, n & 1, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs, n & 1, failed, c.polls));
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
@@ -399,7 +413,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if constexpr (kScaled<T>) {
         uint32_t exponent;
-        ok = row_exponent(bars.tops, p, n, &exponent, failed);
+        ok = row_exponent(bars.tops, p, n, &exponent, failed, c.polls);
         if (!ok) break;
         float up;
         if constexpr (kSplit) {
@@ -424,7 +438,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) tc::bar_arrive(&bars.stat_empty[slot]);
     }
     if (ok && all > 0) {
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed, c.polls));
       tc::fence_after();
     }
     const Strided &to = w ? c.dv : c.dk;  // a warpgroup each
@@ -445,10 +459,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::fence_before();
   }
   __syncthreads();
-  if (threadIdx.x == 0 && bars.failed) g_attention_failed = 1;
   if (warp == kMmaWarp) {
     tc::fence_after();
     tc::tmem_free(tmem, 512);
+  }
+  if (bars.failed) {
+    if (warp == kCopyWarp) drain_copies(bars);
+    if (warp < kCopyWarp) poison_keys<T>(c);
   }
 }
 
@@ -458,12 +475,29 @@ struct QueryBars {
   uint64_t qd, k_full[3], k_empty[3], v_full[2], v_empty[2];
   uint64_t scores[2], read[2], dprobs[2], dscores[2], done, cut, drain;
   uint32_t tmem;
-  int failed;
+  int failed, copied_k, copied_v;  // copied: tiles whose copies were started
   Tops tops;
 };
 
 template <int W>
 constexpr size_t queries_smem() { return 1024 + (size_t)7 * tile_bytes<W>(); }
+
+__device__ __forceinline__ void drain_copies(QueryBars &bars) {
+  tc::bar_drain(&bars.qd, 0);
+  for (int i = max(0, bars.copied_k - 3); i < bars.copied_k; ++i) tc::bar_drain(&bars.k_full[i % 3], (i / 3) & 1);
+  for (int i = max(0, bars.copied_v - 2); i < bars.copied_v; ++i) tc::bar_drain(&bars.v_full[i & 1], (i / 2) & 1);
+}
+template <typename T>
+__device__ __noinline__ void poison_queries(const AttnCall &c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.x % c.heads;
+  if (threadIdx.x == 0) g_attention_failed = 1;
+  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, kTile, blockIdx.x / c.heads, c.causal);
+  const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
+  const int i = at.tile * kTile + (warp & 3) * 32 + lane;
+  if (warp < 4 && i < qs.cover)
+    poison_row(static_cast<T *>(c.dq.p) +
+                   (c.q_offsets ? (qs.row + i) * c.dq.token : qs.seq * c.dq.seq + i * c.dq.token) + head * c.dq.head, c.d);
+}
 
 // A tile of 128 queries of one head, past which the keys stream:
 //   S = Q K^T,  P = exp2(S - lse),  dP = dO V^T,  dS = P (dP - delta),  dQ += dS K.
@@ -472,7 +506,7 @@ constexpr size_t queries_smem() { return 1024 + (size_t)7 * tile_bytes<W>(); }
 // Order of the products: dP(n+1), dQ(n), S(n+2).
 template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    tile_backward_queries(const AttnCall c, const __grid_constant__ TileMaps maps) {
+    tile_backward_queries(const __grid_constant__ AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
   constexpr bool kSplit = Operand<T>::kSplit;
   extern __shared__ unsigned char raw[];
@@ -538,29 +572,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int cut_phase = 0, ks_done = 0, vs_done = 0;
       bool ok = true;
       for (int n = 0; n < all && ok; ++n) {
-        if (n >= 3) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[n % 3], (n / 3 - 1) & 1, failed));
+        if (n >= 3) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[n % 3], (n / 3 - 1) & 1, failed, c.polls));
         if (!ok) break;
         unsigned char *const to = sk + n % 3 * tile_bytes<W>();
         if ((n + 1) * kTile > nk)
           ok = copy_tile_cut<W>(to, &maps.k, &bars.k_full[n % 3], &bars.cut, &cut_phase, kh, k_token + n * kTile,
-                                 ks.seq, nk - n * kTile, failed);
+                                 ks.seq, nk - n * kTile, failed, c.polls);
         else if (lane == 0)
           copy_tile<W>(to, &maps.k, &bars.k_full[n % 3], kh, k_token + n * kTile, ks.seq);
         __syncwarp();
-        if (!ok) break;
         ++ks_done;
-        if (n >= 2) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.v_empty[n & 1], (n / 2 - 1) & 1, failed));
+        if (!ok) break;
+        if (n >= 2) ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.v_empty[n & 1], (n / 2 - 1) & 1, failed, c.polls));
         if (!ok) break;
         if (lane == 0)
           copy_tile<W>(sv + (n & 1) * tile_bytes<W>(), &maps.v, &bars.v_full[n & 1], kh, k_token + n * kTile, ks.seq);
         __syncwarp();
         ++vs_done;
       }
-      if (*failed) {
-        int unseen = 0;
-        tc::bar_wait(&bars.qd, 0, &unseen);
-        for (int i = max(0, ks_done - 3); i < ks_done; ++i) tc::bar_wait(&bars.k_full[i % 3], (i / 3) & 1, &unseen);
-        for (int i = max(0, vs_done - 2); i < vs_done; ++i) tc::bar_wait(&bars.v_full[i & 1], (i / 2) & 1, &unseen);
+      if (lane == 0) {
+        bars.copied_k = ks_done;
+        bars.copied_v = vs_done;
       }
     } else if (warp == kMmaWarp) {
       if (all > 0) {
@@ -570,7 +602,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t k0 = tc::desc_rows(tc::smem_addr(sk)), v0 = tc::desc_rows(tc::smem_addr(sv));
         const uint32_t k0c = tc::desc_columns(tc::smem_addr(sk), kBlock);
         const auto wait = [&](uint64_t *bar, int phase) {
-          const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
+          const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed, c.polls));
           tc::fence_after();
           return done;
         };
@@ -611,8 +643,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tc::commit(&bars.done);
           tc::commit(&bars.drain);
         }
-        int unseen = 0;
-        tc::bar_wait(&bars.drain, 0, &unseen);
+        tc::bar_drain(&bars.drain, 0);
       }
       __syncwarp();
     }
@@ -652,7 +683,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int n = 0; n < all; ++n) {
       const int b = n & 1, phase = (n / 2) & 1, key0 = n * kTile + w * kHalf;
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[b], phase, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[b], phase, failed, c.polls));
       if (!ok) break;
       tc::fence_after();
       if constexpr (kSplit)
@@ -676,7 +707,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const int left = lim - key0;
       const bool cut = __any_sync(0xffffffffu, left < kHalf);
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs[b], phase, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.dprobs[b], phase, failed, c.polls));
       if (!ok) break;
       tc::fence_after();
       float t[kHalf];
@@ -703,7 +734,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
       if constexpr (kScaled<T>) {
         uint32_t exponent;
-        ok = row_exponent(bars.tops, t, n, &exponent, failed);
+        ok = row_exponent(bars.tops, t, n, &exponent, failed, c.polls);
         if (!ok) break;
         float up;
         if constexpr (kSplit) {
@@ -714,7 +745,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         } else {
           const int now = running_power(power, exponent);
           if (n > 0 && __any_sync(0xffffffffu, now != power)) {  // once the sums so far are complete
-            ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[(n - 1) % 3], ((n - 1) / 3) & 1, failed));
+            ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.k_empty[(n - 1) % 3], ((n - 1) / 3) & 1, failed, c.polls));
             if (!ok) break;
             tc::fence_after();
             multiply_sums<DP / 2>(at_lane + 3 * kTile + w * (DP / 2), exp2f((float)(now - power)));
@@ -732,7 +763,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::bar_arrive_warp(&bars.dscores[b]);
     }
     if (ok && all > 0) {
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done, 0, failed, c.polls));
       tc::fence_after();
     }
     if (ok) {
@@ -754,10 +785,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::fence_before();
   }
   __syncthreads();
-  if (threadIdx.x == 0 && bars.failed) g_attention_failed = 1;
   if (warp == kMmaWarp) {
     tc::fence_after();
     tc::tmem_free(tmem, 512);
+  }
+  if (bars.failed) {
+    if (warp == kCopyWarp) drain_copies(bars);
+    if (warp < kCopyWarp) poison_queries<T>(c);
   }
   // what follows in the stream waits for this kernel only: its last block waits for the keys'
   if (blockIdx.x == gridDim.x - 1) dependency_wait();

@@ -13,8 +13,55 @@ constexpr size_t tile_forward_smem() { return 1024 + (size_t)(2 + kForwardSlots)
 struct ForwardBars {
   uint64_t q[2], full[kForwardSlots], empty[kForwardSlots], scores[2], probs[2][2], done[2], cut, drain;
   uint32_t tmem;
-  int failed;
+  int failed, copied, copied_q;  // tiles of keys and values whose copies were started; a bit for each of queries
 };
+
+// A block's part of the queries: two tiles of 128 rows.
+struct ForwardPlace {
+  Place at;
+  Span qs;
+  int head0, first[2];
+};
+__device__ __forceinline__ ForwardPlace forward_place(const AttnCall &c) {
+  const bool by_heads = c.group % 2 == 0;
+  const int units = by_heads ? c.heads / 2 : c.heads, u = blockIdx.x % units, rows = by_heads ? kTile : 2 * kTile;
+  ForwardPlace p;
+  p.at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, rows, blockIdx.x / units, c.causal);
+  p.head0 = by_heads ? 2 * u : u;
+  if (p.at.s < 0) return p;
+  p.qs = own_span(c.q_offsets, c.q_lengths, p.at.s, c.sequences, c.q_tokens);
+  p.first[0] = p.at.tile * rows;
+  p.first[1] = p.first[0] + (by_heads ? 0 : kTile);
+  return p;
+}
+
+// The copies of a block whose wait has given up end before it does.
+__device__ __forceinline__ void drain_copies(ForwardBars &bars) {
+  for (int t = 0; t < 2; ++t)
+    if (bars.copied_q >> t & 1) tc::bar_drain(&bars.q[t], 0);
+  for (int i = max(0, bars.copied - kForwardSlots); i < bars.copied; ++i)
+    tc::bar_drain(&bars.full[i % kForwardSlots], (i / kForwardSlots) & 1);
+}
+// The flag, and NaN for its results, by the warps that have rows.  (A call of its own,
+// and what it needs made again, so that the kernel keeps no registers for it: they
+// cost the long prompt 3 %.)
+template <typename T>
+__device__ __noinline__ void poison_forward(const AttnCall &c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) g_attention_failed = 1;
+  const ForwardPlace p = forward_place(c);
+  const int t = warp >> 2, i = p.first[t] + (warp & 3) * 32 + lane, head = p.head0 + (c.group % 2 == 0 ? t : 0);
+  if (i >= p.qs.cover) return;
+  const int64_t slot = (blockIdx.y * c.rows + p.qs.row + i) * c.heads + head;
+  if (c.splits > 1) {
+    poison_row(c.part + slot * c.d, c.d);
+    poison_row(c.part + (int64_t)c.splits * c.rows * c.heads * c.d + slot, 1);
+  } else {
+    poison_row(static_cast<T *>(c.out.p) + head * c.out.head +
+                   (c.q_offsets ? (p.qs.row + i) * c.out.token : p.qs.seq * c.out.seq + i * c.out.token), c.d);
+    poison_row(c.lse + (int64_t)head * c.rows + p.qs.row + i, 1);
+  }
+}
 
 // Two tiles of 128 query rows share the keys: two heads of a group over the
 // same tokens where the group is even, else neighbouring tokens of one head.
@@ -25,7 +72,7 @@ struct ForwardBars {
 // fold, which the 32-bit sums hold as well.
 template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    tile_forward(const AttnCall c, const __grid_constant__ TileMaps maps) {
+    tile_forward(const __grid_constant__ AttnCall c, const __grid_constant__ TileMaps maps) {
   constexpr int W = wide<T, DP>();
   constexpr bool kSplit = Operand<T>::kSplit;
   extern __shared__ unsigned char raw[];
@@ -59,26 +106,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::tmem_alloc(&bars.tmem, 512);
     tc::fence_before();
   }
-  const bool by_heads = c.group % 2 == 0;
-  const int units = by_heads ? c.heads / 2 : c.heads, u = blockIdx.x % units;
-  const int rows = by_heads ? kTile : 2 * kTile;
-  const Place at = find_tile(c.q_offsets, c.sequences, c.q_tokens, 1, rows, blockIdx.x / units, c.causal);
+  const ForwardPlace place = forward_place(c);
+  const Place at = place.at;
   if (at.s < 0) return leave_block(warp, &bars.tmem);
-  const Span qs = own_span(c.q_offsets, c.q_lengths, at.s, c.sequences, c.q_tokens);
+  const Span qs = place.qs;
+  const bool by_heads = c.group % 2 == 0;
   const Span ks = other_span(c.k_offsets, c.k_lengths, at.s, c.q_offsets != nullptr, c.sequences, c.k_tokens);
   const int nq = qs.valid, nk = ks.valid;
-  int first[2], steps[2];
+  const int first[2] = {place.first[0], place.first[1]}, head0 = place.head0, kh = head0 / c.group;
+  int steps[2];
   const int begin = c.splits > 1 ? (int)blockIdx.y * (c.chunk / kTile) : 0;  // the first tile of keys
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    first[t] = at.tile * rows + (by_heads ? 0 : t * kTile);
     const int last = min(first[t] + kTile, nq) - 1;
     int end = first[t] < nq ? (max(0, seen_keys(c.causal, last, nq, nk)) + kTile - 1) / kTile : 0;
     if (c.splits > 1) end = min(end, begin + c.chunk / kTile);
     steps[t] = max(0, end - begin);
   }
   const int all = max(steps[0], steps[1]);
-  const int head0 = by_heads ? 2 * u : u, kh = head0 / c.group;
 
   const int q_token = c.q_offsets ? (int)qs.row : 0, k_token = (c.k_offsets ? (int)ks.row : 0) + begin * kTile;
   if (warp == kCopyWarp && lane == 0 && all > 0) {
@@ -102,22 +147,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int slot = item % kForwardSlots;
         if (item >= kForwardSlots)
           ok = __all_sync(0xffffffffu,
-                          tc::bar_wait(&bars.empty[slot], (item / kForwardSlots - 1) & 1, failed));
+                          tc::bar_wait(&bars.empty[slot], (item / kForwardSlots - 1) & 1, failed, c.polls));
         if (!ok) break;
         unsigned char *const to = ring + slot * tile_bytes<W>();
         const int token = k_token + j * kTile;
         const int left = nk - (begin + j) * kTile;
         if (kv && left < kTile)
-          ok = copy_tile_cut<W>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq, left, failed);
+          ok = copy_tile_cut<W>(to, &maps.v, &bars.full[slot], &bars.cut, &cut_phase, kh, token, ks.seq, left, failed,
+                                 c.polls);
         else if (lane == 0)
           copy_tile<W>(to, kv ? &maps.v : &maps.k, &bars.full[slot], kh, token, ks.seq);
         __syncwarp();
       }
     }
-    // copies in flight end before the block does, also where a wait has given up
-    for (int i = max(0, item - kForwardSlots); i < item && *failed; ++i) {
-      int unseen = 0;
-      tc::bar_wait(&bars.full[i % kForwardSlots], (i / kForwardSlots) & 1, &unseen);
+    if (lane == 0) {
+      bars.copied = item;
+      bars.copied_q = (steps[0] > 0) + 2 * (steps[1] > 0);
     }
   } else if (warp == kMmaWarp) {
     // the whole warp goes along, so that descriptors stay in uniform registers
@@ -127,7 +172,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t v0 = tc::desc_columns(tc::smem_addr(ring), kBlock);
       constexpr uint32_t kStep = tile_bytes<W>() / 16;
       const auto wait = [&](uint64_t *bar, int phase) {
-        const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed));
+        const bool done = __all_sync(0xffffffffu, tc::bar_wait(bar, phase, failed, c.polls));
         tc::fence_after();
         return done;
       };
@@ -171,8 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
       }
       if (leader) tc::commit(&bars.drain);
-      int unseen = 0;
-      tc::bar_wait(&bars.drain, 0, &unseen);
+      tc::bar_drain(&bars.drain, 0);
     }
     __syncwarp();
   }
@@ -203,7 +247,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       if (steps[t]) load_powers(0);
       for (int j = 0; j < steps[t]; ++j) {
-        ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed, c.polls));
         if (!ok) break;
         tc::fence_after();
         if (j > 0) add_sums<DP>(o, o_at, v_before);  // of the tile before: complete when these scores are
@@ -265,7 +309,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         sum += (part[0] + part[1]) + (part[2] + part[3]);
       }
       if (ok && steps[t]) {
-        ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed, c.polls));
         tc::fence_after();
         if (ok) add_sums<DP>(o, o_at, v_before);
       }
@@ -281,7 +325,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     } else {
     const float cs = c.scale_log2;
     for (int j = 0; j < steps[t]; ++j) {
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.scores[t], j & 1, failed, c.polls));
       if (!ok) break;
       tc::fence_after();
       float s[kTile];
@@ -355,7 +399,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
     }
     if (ok && steps[t]) {
-      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed));
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&bars.done[t], 0, failed, c.polls));
       tc::fence_after();
     }
     if (ok) {
@@ -387,10 +431,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::fence_before();
   }
   __syncthreads();
-  if (threadIdx.x == 0 && bars.failed) g_attention_failed = 1;
   if (warp == kMmaWarp) {
     tc::fence_after();
     tc::tmem_free(tmem, 512);
+  }
+  if (bars.failed) {
+    if (warp == kCopyWarp) drain_copies(bars);
+    if (warp < kCopyWarp) poison_forward<T>(c);
   }
 }
 

@@ -32,22 +32,30 @@ __device__ __forceinline__ void bar_arrive_warp(uint64_t *b) {
   if ((threadIdx.x & 31) == 0) bar_arrive(b);
 }
 
-// Waits for the phase of that parity, for 2^22 polls at most, or until another
+constexpr int kPolls = 1 << 22;  // of a wait, at most
+__device__ __forceinline__ bool bar_done(uint64_t *b, int parity) {
+  uint32_t done;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(done)
+               : "r"(smem_addr(b)), "r"(parity)
+               : "memory");
+  return done;
+}
+// Waits for the phase of that parity, for so many polls at most, or until another
 // wait of the block has given up; false: the caller leaves its loop.
-constexpr int kPolls = 1 << 22;
-__device__ __forceinline__ bool bar_wait(uint64_t *b, int parity, volatile int *failed) {
-  for (int i = 0; i < kPolls; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(smem_addr(b)), "r"(parity)
-        : "memory");
-    if (done) return true;
+__device__ __forceinline__ bool bar_wait(uint64_t *b, int parity, volatile int *failed, int polls) {
+  for (int i = 0; i < polls; ++i) {
+    if (bar_done(b, parity)) return true;
     if ((i & 63) == 63 && *failed) return false;
   }
   *failed = 1;
   return false;
+}
+// Waits for copies or products that are in flight after a wait has given up: a block
+// does not end before they have.
+__device__ __forceinline__ void bar_drain(uint64_t *b, int parity) {
+  for (int i = 0; i < kPolls && !bar_done(b, parity); ++i) {
+  }
 }
 
 // Shared memory written by ordinary stores, seen by the copies and MMAs that follow.

@@ -560,10 +560,16 @@ snack_status snack_attention_backward(const snack_attention_args *args,
 /*
  * Read and clear the current device's flag of the attention calls: *flag = 1
  * if, since the last read, a kernel gave up a bounded wait on its own copies
- * or products (the results of that call are then not to be trusted).
- * Synchronises `stream`.
+ * or products.  The block's results of that call are NaN.  Synchronises `stream`.
  */
 snack_status snack_attention_error(int *flag, void *stream);
+
+/*
+ * Test hook for that path: the waits of attention kernels that are launched from now
+ * on give up after `polls` polls (0: at once); a negative value restores the limit.
+ * Process-wide.  Copies and products in flight are waited for all the same.
+ */
+void snack_debug_attention_polls(int polls);
 
 /*
  * Dropout of n contiguous elements: y = residual + M * x (residual NULL: M * x),

@@ -238,3 +238,46 @@ def test_many_sequences_of_few_queries(dtype, group, d):
         opts = dict(q_offsets=ends[0], k_offsets=ends[1])
         got = sn.snack_attention_forward(q, k, v, **opts)
         attention_ref.assert_within(dict(zip(("out", "lse"), got)), attention_ref.attention(q, k, v, **opts))
+
+
+# ---------------------------------------------------------------- waits that give up
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("length", [300, 1024])
+def test_waits_that_give_up_leave_nan_and_the_flag(dtype, d, length):
+    """Every wait of the tiles gives up at once: all results are NaN, the flag is set and is cleared by
+    reading it, and the calls that follow are right.  (32 bits at 128 columns: no tiles, no waits.)"""
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(22)
+    q, k, v, dout = (rnd(g, (8, length, h, d), dtype) for h in (8, 4, 4, 8))
+    want = run(q, k, v, dout)
+    torch.cuda.synchronize()
+    assert not sn.snack_attention_error()
+    try:
+        sn.snack_debug_attention_polls(0)
+        out, lse = sn.snack_attention_forward(q, k, v)
+        grads = sn.snack_attention_backward(dout, q, k, v, want[0], want[1])
+        torch.cuda.synchronize()
+        tiles = dtype != F32 or d == 64
+        assert sn.snack_attention_error() == tiles and not sn.snack_attention_error()
+        for t in (out, lse, *grads) if tiles else ():
+            assert t.isnan().all()
+    finally:
+        sn.snack_debug_attention_polls(-1)
+    assert all(torch.equal(a, b) for a, b in zip(run(q, k, v, dout), want))
+    assert not sn.snack_attention_error()
+
+
+def test_waits_that_give_up_with_keys_in_parts():
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(23)
+    q, k, v = (rnd(g, (1, n, 8, 64), BF16) for n in (130, 9000, 9000))
+    want = sn.snack_attention_forward(q, k, v)
+    try:
+        sn.snack_debug_attention_polls(0)
+        out, lse = sn.snack_attention_forward(q, k, v)
+        assert sn.snack_attention_error() and out.isnan().all() and lse.isnan().all()
+    finally:
+        sn.snack_debug_attention_polls(-1)
+    assert all(torch.equal(a, b) for a, b in zip(sn.snack_attention_forward(q, k, v), want))
