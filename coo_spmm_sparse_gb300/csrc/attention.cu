@@ -494,11 +494,14 @@ void plan_parts(Plan *p, const AttnCall &c, int type, bool backward) {
 }
 
 // The tiles take calls from 64 query tokens on, where there is work for them:
-// X = query rows (tokens * heads) * keys.  Measured with 12 heads of 64, bf16,
-// tiles and mma.sync, us: forward 1 x 256 x 256 (X = 8e5) 11, 9; 4 x 256 x 256
-// (3e6) 11, 17; 1 x 1024 x 1024 (1.3e7) 19, 41; backward 35, 23; 37, 45; 50, 92.
-// fp32, where the operands are made first: forward 4 x 256 x 256 28, 29; 8 x 256
-// x 256 (6e6) 32, 55; backward, 8 x 256 x 256, 66, 132.
+// X = query rows (tokens * heads) * keys.  12 heads of 64 (16 over 4 where it says so),
+// tiles / mma.sync, us:
+//   forward, bf16: 1 x 128 (X = 2e5) 8 / 7; 1 x 256 (8e5) 10 / 10, 16 over 4 10 / 10; 2 x 256
+//   (1.6e6) 10 / 11; 4 x 256 (3e6) 10 / 17; 1 x 1024 (1.3e7) 18 / 41: from 1e6;
+//   forward, fp32, where the operands are made first: 1 x 256 19 / 15; 2 x 256 19 / 19, 16
+//   over 4 (2.1e6) 19 / 23; 4 x 256 21 / 31; 1 x 1024 37 / 82: from 2e6;
+//   backward: 1 x 128 bf16 17 / 17, float16 18 / 17, fp32 24 / 22; 1 x 256 19 / 23, 19 / 25, 26 /
+//   34; 4 x 128 (8e5) 17 / 29, 19 / 29, 28 / 41; 1 x 1024 28 / 97, 31 / 103, 45 / 236: from 5e5.
 // Few rows over many keys are too few for the forward tiles even with the keys
 // in parts.  A ragged side's lengths are not known here, only their mean; a tile holds
 // one sequence's tokens.  Forward, bf16, 24 heads over 8 of 128, tiles / without, us:
@@ -510,7 +513,8 @@ bool worth_tiles(const AttnCall &c, int type, bool backward) {
   if (c.q_tokens < 64 || c.k_tokens < 64) return false;
   if (c.q_offsets && !backward && c.q_tokens < (int64_t)16 * c.sequences) return false;
   const double rows = (double)c.rows * c.heads, x = rows * c.k_tokens;
-  return x >= (type == SNACK_F32 && !backward ? 4e6 : 2e6) && (backward || rows >= 1024);
+  if (backward) return x >= 5e5;
+  return x >= (type == SNACK_F32 ? 2e6 : 1e6) && rows >= 1024;
 }
 
 // Off the tiles, 16 rows to a block where blocks of 128 would leave SMs idle, and
