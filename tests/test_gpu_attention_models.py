@@ -149,3 +149,35 @@ def test_adapted_decoder_drops_what_its_base_drops():
     assert base.calls == 0
     loss, _ = FineTuner(model).step(idx, requests)
     assert torch.isfinite(loss) and base.calls == 1
+
+
+def test_the_decoders_attention_within_its_own_bounds():
+    """What every block of a training call passes to the attention and gets back, forward and backward,
+    held to the operator's own bounds (products in one tf32 part would miss them)."""
+    import attention_ref
+    from coo_spmm_sparse_gb300 import decoder
+    model, idx = small(d=256, heads=4), tokens(n=12)
+    calls, plain = [], decoder.attend
+
+    def attend(qkv, heads, dropout=0.0, seed=0):
+        a = plain(qkv, heads, dropout, seed)
+        qkv.retain_grad()
+        a.retain_grad()
+        calls.append((qkv, a))
+        return a
+
+    decoder.attend = attend
+    try:
+        (model(idx) * torch.randn(12, 64, 128, device="cuda")).sum().backward()
+    finally:
+        decoder.attend = plain
+    assert len(calls) == 2
+    for qkv, a in calls:
+        q, k, v = (t.unflatten(-1, (4, 64)) for t in qkv.detach().split(256, -1))
+        want = attention_ref.attention(q, k, v, dout=a.grad.unflatten(-1, (4, 64)))
+        grads = qkv.grad.unflatten(-1, (3, 4, 64)).unbind(-3)
+        attention_ref.assert_within(dict(zip(("out", "dq", "dk", "dv"), (a.detach().unflatten(-1, (4, 64)), *grads))),
+                                    want)
+        rough = [t.to(torch.float32).view(torch.int32).bitwise_and(-8192).view(torch.float32) for t in (q, k, v)]
+        other = attention_ref.attention(*rough)["out"][0]  # operands cut to tf32 are outside them
+        assert bool(((other - want["out"][0]).abs() > want["out"][1]).any())
