@@ -185,9 +185,8 @@ __device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint32_t b, bool ad
   }
 }
 
-// Gradients of scores in two parts of 16-bit type T (laid out as above) times rows b
-// in one: where the operands' type holds the results no better than it holds them,
-// rounding them once more would make the results 1.5 times as far off.
+// Probabilities or gradients of scores in two parts of 16-bit type T (laid out as
+// above) times rows b in one.
 template <typename T, int DP>
 __device__ __forceinline__ void fine_sums(uint32_t d, uint32_t a, uint32_t b, bool add) {
   constexpr uint32_t kind = tc::mma_kind<T>(DP, true);

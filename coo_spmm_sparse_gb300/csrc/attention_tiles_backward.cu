@@ -11,12 +11,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = kTile / 2;  // columns of a tile that a warpgroup takes
 constexpr int kStatWarp = 10;
 
-// 32 probabilities of a row, columns [x, x + 32) of a warpgroup's 64 that begin at
-// `at`, as the left operand of a product.
+// Left operands of the second products, in one part of the type or in two; 32 values
+// of a row, columns [x, x + 32) of a warpgroup's 64 that begin at `at`.
+//
+// Gradients of scores are always in two: in 16-bit types rounding them to one made dq
+// and dk 1.5 times as far off as the rounding of the results alone.  Probabilities are
+// in two but in float16: in one, bfloat16's dv was 1.4 times as far off (two cost 9
+// packed sequences at 64 columns 322 -> 334 us, 8192 tokens at 128 1902 -> 2012, forward
+// included); float16's is 1.4 times, in a type of eight times the precision.
 template <typename T>
+constexpr bool kFineProbs = !std::is_same<T, __half>::value;
+template <typename T, bool FINE>
 __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) {
-  if constexpr (Operand<T>::kSplit) {
-    store_parts<__half>(at + x, v);
+  if constexpr (FINE) {
+    store_parts<typename Operand<T>::type>(at + x, v);
   } else {
     uint32_t out[16];
 #pragma unroll
@@ -24,19 +32,12 @@ __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) 
     tc::store16(at + x / 2, out);
   }
 }
-
-// The gradients of the scores, always in two parts: in 16-bit types rounding them to
-// one made dq and dk 1.5 times as far off as the rounding of the results alone.
-template <typename T>
-__device__ __forceinline__ void store_score32(uint32_t at, int x, const float *v) {
-  store_parts<typename Operand<T>::type>(at + x, v);
-}
-template <typename T, int DP>
-__device__ __forceinline__ void score_sums(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  if constexpr (Operand<T>::kSplit)
-    sums<T, DP, kTile>(d, a, b, add);
-  else
+template <typename T, int DP, bool FINE>
+__device__ __forceinline__ void row_sums(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  if constexpr (FINE && !Operand<T>::kSplit)
     fine_sums<T, DP>(d, a, b, add);
+  else
+    sums<T, DP, kTile>(d, a, b, add);
 }
 
 // float16 operands hold neither small probabilities nor small gradients of scores:
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = wait(&bars.probs, n & 1);
           if (!ok) break;
           if (leader) {
-            sums<T, DP, kTile>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
+            row_sums<T, DP, kFineProbs<T>>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.d_empty[n & 1]);
           }
           __syncwarp();
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
           if (leader) {
-            score_sums<T, DP>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
+            row_sums<T, DP, true>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.q_empty[n & 1]);
           }
           __syncwarp();
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = !DROP || (kept[e & 3] >> ((x + e) & ~3) & 1) ? p[x + e] : 0.f;
-        store_row32<T>(s_at, x, v);
+        store_row32<T, kFineProbs<T>>(s_at, x, v);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) p[x] *= up;
       }
-      store_score32<T>(dp_at, 0, p);
-      store_score32<T>(dp_at, 32, p + 32);
+      store_row32<T, true>(dp_at, 0, p);
+      store_row32<T, true>(dp_at, 32, p + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores);
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (leader) {
             // split: two buffers in turn, each added to the rows' own sums two tiles later
             const uint32_t to = tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), ds_at = tmem + (2 * n + 1) % 3 * kTile;
-            score_sums<T, DP>(to, ds_at, k0c + n % 3 * kStep, n > 0);
+            row_sums<T, DP, true>(to, ds_at, k0c + n % 3 * kStep, n > 0);
             tc::commit(&bars.k_empty[n % 3]);
           }
           __syncwarp();
@@ -756,8 +757,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] *= up;
       }
-      store_score32<T>(dp_at, 0, t);
-      store_score32<T>(dp_at, 32, t + 32);
+      store_row32<T, true>(dp_at, 0, t);
+      store_row32<T, true>(dp_at, 32, t + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores[b]);

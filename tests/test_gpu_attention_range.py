@@ -281,3 +281,49 @@ def test_waits_that_give_up_with_keys_in_parts():
     finally:
         sn.snack_debug_attention_polls(-1)
     assert all(torch.equal(a, b) for a, b in zip(sn.snack_attention_forward(q, k, v), want))
+
+
+# ---------------------------------------------------------------- how far off 16-bit gradients are
+
+@pytest.mark.parametrize("n,length,heads,key_heads,d", [(2, 1024, 8, 4, 64), (1, 2048, 8, 2, 128), (4, 300, 12, 12, 64)])
+def test_bfloat16_gradients_are_as_exact_as_their_rounding(n, length, heads, key_heads, d):
+    """Probabilities and gradients of scores in two parts leave dq, dk and dv where rounding them to
+    bfloat16 alone does: with errors that add up like independent ones, delta of a rounded out
+    (2^-9 of a sum that cancels to about 2 of its size) may add a tenth; one part of either adds half."""
+    import attention_ref
+    g = gen(24)
+    q, k, v, dout = (rnd(g, (n, length, h, d), BF16) for h in (heads, key_heads, key_heads, heads))
+    got = run(q, k, v, dout)
+    want = attention_ref.attention(q, k, v, dout=dout)
+    for name, t in zip(("dq", "dk", "dv"), got[2:]):
+        ref = want[name][0]
+        off, least = ((x.double() - ref).norm() for x in (t, ref.to(BF16)))
+        assert float(off) <= 1.1 * float(least), (name, float(off / least))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("side", ["keys", "queries"])
+def test_gradients_of_scores_that_grow_along_a_row(dtype, d, side):
+    """Values, or dout, 16 times as large every 128 tokens: a row's power falls from step to step, and
+    sums that stay in tensor memory are multiplied down with it."""
+    import attention_ref
+    g = gen(25)
+    n = 640
+    q, k, v, dout = (rnd(g, (2, n, h, d), torch.float64) for h in (4, 2, 2, 4))
+    growth = (16.0 ** (torch.arange(n, device="cuda") // 128) / 256.0)[None, :, None, None]
+    if side == "keys":
+        v = v * growth
+    else:
+        dout = dout * growth
+    q, k, v, dout = (t.to(dtype) for t in (q, k, v, dout))
+    for causal in (True, False):
+        got = run(q, k, v, dout, causal=causal)
+        want = attention_ref.attention(q, k, v, dout=dout, causal=causal)
+        attention_ref.assert_within(dict(zip(("out", "lse", "dq", "dk", "dv"), got)), want)
+        # and by the norm of each block of 128 tokens, which the largest does not cover
+        u = {F32: 2.0 ** -16, BF16: 2.0 ** -7, F16: 2.0 ** -9}[dtype]
+        for name, t in zip(("dq", "dk", "dv"), got[2:]):
+            for at in range(0, n, 128):
+                ref = want[name][0][:, at: at + 128]
+                assert float((t[:, at: at + 128].double() - ref).norm()) <= u * float(ref.norm()), (name, at)
