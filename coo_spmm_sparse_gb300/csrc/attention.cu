@@ -250,7 +250,7 @@ struct Source {
   int tokens, heads;
   int64_t rows;    // tokens of all sequences
   void *made;      // receives what the tiles read
-  int32_t *power;  // 32 bits: and the powers of two of its tiles
+  int32_t *power;  // made in float16: and the powers of two of its tiles, or peaks of its sequences
 };
 struct Sources {
   Source t[4];
@@ -344,6 +344,64 @@ __global__ void __launch_bounds__(256) split_operands(const Sources all, int seq
     uint16_t *const to = made + (sp.row + row) * t.heads * 128;
     *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2 *>(to + 64) = make_uint2(lo[0], lo[1]);
+  }
+}
+
+// bfloat16 tensors in float16, rows of 128 columns: of the elements times the power of
+// two that brings the largest of their sequence and key head to [2^14, 2^15), so that
+// nothing depends on other sequences and key heads; the eight bits lose nothing down
+// to 2^-28 of it.  Two launches of the same blocks, each a tile of a head: the first finds
+// the largest, the second writes.  Grid as above.
+template <bool WRITE>
+__global__ void __launch_bounds__(256) half_operands(const Sources all, int sequences, int key_heads, int d) {
+  using T = __nv_bfloat16;
+  __shared__ uint32_t tops[8];
+  const Source &t = all.t[blockIdx.y];
+  const int head = blockIdx.x % t.heads, kh = head / (t.heads / key_heads);
+  const Place at = find_tile(t.offsets, sequences, t.tokens, 1, kTile, blockIdx.x / t.heads, false);
+  if (at.s < 0) return;
+  const Span sp = own_span(t.offsets, t.lengths, at.s, sequences, t.tokens);
+  constexpr int kRows = kTile / 16;  // of a thread; 16 threads take a row
+  const int col = threadIdx.x % 16 * 8, first = at.tile * kTile + threadIdx.x / 16;
+  const T *const from = static_cast<const T *>(t.from.p) +
+                        (t.offsets ? sp.row * t.from.token : sp.seq * t.from.seq) + head * t.from.head + col;
+  uint32_t *const peak = reinterpret_cast<uint32_t *>(t.power) + (int64_t)at.s * key_heads + kh;
+  uint4 u[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = first + 16 * i;
+    u[i] = row < sp.valid && col < d ? load_vector(from + row * t.from.token, d - col) : make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (!WRITE) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float x[8];
+      unpack16<T>(u[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = larger(top, x[e]);
+    }
+    uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int w = 0; w < 8; ++w) most = max(most, tops[w]);
+      atomicMax(peak, most);  // (a maximum does not depend on the order)
+    }
+  } else {
+    const float by = power_of_two(power_to_half(*peak));
+    uint16_t *const made = static_cast<uint16_t *>(t.made) + head * 128 + col;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int row = first + 16 * i;
+      if (row >= sp.cover) break;
+      float x[8];
+      unpack16<T>(u[i], x);
+      *reinterpret_cast<uint4 *>(made + (sp.row + row) * t.heads * 128) =
+          make_uint4(pack2<__half>(x[0] * by, x[1] * by), pack2<__half>(x[2] * by, x[3] * by),
+                     pack2<__half>(x[4] * by, x[5] * by), pack2<__half>(x[6] * by, x[7] * by));
+    }
   }
 }
 
@@ -466,6 +524,7 @@ AttnCall call_of(const snack_attention_args *a) {
 struct Plan {
   bool tiles = false, few = false;  // on tcgen05; in blocks of 16 rows
   int splits = 1, chunk = 0, width = 0;  // width: columns of operands that are made; 0: none are
+  bool halves = false;                   // bfloat16's, in float16
   size_t part = 0, parts[4] = {}, powers[4] = {}, bytes = 0;  // offsets (delta is at 0); parts: of q, k, v, dout
 };
 
@@ -483,9 +542,10 @@ void plan_parts(Plan *p, const AttnCall &c, int type, bool backward) {
     p->parts[i] = p->bytes;
     p->bytes += rows[i] * p->width * 2;
   }
-  if (type != SNACK_F32) return;
-  const int64_t q = tile_numbers(c.q_offsets, c.sequences, c.q_tokens) * c.heads;
-  const int64_t k = tile_numbers(c.k_offsets, c.sequences, c.k_tokens) * c.key_heads;
+  if (type != SNACK_F32 && !p->halves) return;
+  int64_t q = tile_numbers(c.q_offsets, c.sequences, c.q_tokens) * c.heads;
+  int64_t k = tile_numbers(c.k_offsets, c.sequences, c.k_tokens) * c.key_heads;
+  if (p->halves) q = k = ((int64_t)c.sequences + 2) * c.key_heads;
   const int64_t tiles[4] = {q, k, k, backward ? q : 0};
   for (int i = 0; i < 4; ++i) {
     p->powers[i] = p->bytes;
@@ -555,11 +615,19 @@ Plan plan_forward(const AttnCall &c, int type) {
   return p;
 }
 
+// bfloat16 backward calls whose operands are made in float16 (attention_tiles_backward.cu):
+// seven products instead of ten, for passes that make them.  X as above; heads of 128,
+// made / as they lie, us: 2 x 2048 tokens, 16 over 4 heads (X = 1.3e8) 171 / 150; 1 x 4096
+// (2.7e8) 284 / 271; 1 x 8192 (1.1e9) 691 / 750; 32 over 8 (2.1e9) 1375 / 1550; 4 x 4096 (2.1e9)
+// 1618 / 1722.  At 64 columns exponentials bind, not products.
+bool halves_take(const AttnCall &c) { return c.d > 64 && (double)c.rows * c.heads * c.k_tokens >= 6e8; }
+
 Plan plan_backward(const AttnCall &c, int type) {
   Plan p;
   p.bytes = round_up(std::max<int64_t>(c.rows * c.heads, 1) * (int64_t)sizeof(float), 256);
   p.tiles = worth_tiles(c, type, true) && tiles_take(c, type);
-  p.width = p.tiles ? part_width(c, type) : 0;
+  p.halves = p.tiles && type == SNACK_BF16 && halves_take(c);
+  p.width = !p.tiles ? 0 : p.halves ? 128 : part_width(c, type);
   if (p.width) plan_parts(&p, c, type, true);
   return p;
 }
@@ -586,18 +654,26 @@ unsigned spread(int64_t rows) {  // a warp for each, or as many as are resident 
 template <typename T>
 cudaError_t make_parts(AttnCall *c, const Plan &p, bool backward, char *workspace, SplitParts *parts, cudaStream_t s) {
   const Sources all = sources_of(*c, p, workspace);
-  *parts = SplitParts{p.width, all.t[0].made, all.t[1].made, all.t[2].made, all.t[3].made};
+  *parts = SplitParts{p.width, p.halves, all.t[0].made, all.t[1].made, all.t[2].made, all.t[3].made};
   const unsigned tensors = backward ? 4 : 3;
+  c->q_power = all.t[0].power;
+  c->k_power = all.t[1].power;
+  c->v_power = all.t[2].power;
+  c->dout_power = all.t[3].power;
+  const int64_t q = tiles_of(c->q_offsets, c->sequences, c->q_tokens, 1, kTile) * c->heads;
+  const int64_t k = tiles_of(c->k_offsets, c->sequences, c->k_tokens, 1, kTile) * c->key_heads;
+  const dim3 tiles((unsigned)std::max(q, k), tensors);
   if constexpr (sizeof(T) == 4) {
-    c->q_power = all.t[0].power;
-    c->k_power = all.t[1].power;
-    c->v_power = all.t[2].power;
-    c->dout_power = all.t[3].power;
-    const int64_t q = tiles_of(c->q_offsets, c->sequences, c->q_tokens, 1, kTile) * c->heads;
-    const int64_t k = tiles_of(c->k_offsets, c->sequences, c->k_tokens, 1, kTile) * c->key_heads;
-    return launch_kernel(split_operands, dim3((unsigned)std::max(q, k), tensors), 256, 0, false, s, all, c->sequences,
-                         c->d);
+    return launch_kernel(split_operands, tiles, 256, 0, false, s, all, c->sequences, c->d);
   } else {
+    if (p.halves) {
+      cudaError_t e = cudaMemsetAsync(all.t[0].power, 0, p.bytes - p.powers[0], s);
+      if (e == cudaSuccess)
+        e = launch_kernel(half_operands<false>, tiles, 256, 0, false, s, all, c->sequences, c->key_heads, c->d);
+      if (e == cudaSuccess)
+        e = launch_kernel(half_operands<true>, tiles, 256, 0, false, s, all, c->sequences, c->key_heads, c->d);
+      return e;
+    }
     const unsigned blocks = spread(std::max(all.t[0].rows, all.t[1].rows));
     return launch_kernel(p.width == 64 ? copy_operands<T, 64> : copy_operands<T, 128>, dim3(blocks, tensors), 256, 0,
                          false, s, all, c->sequences, c->d);

@@ -17,8 +17,10 @@ struct AttnCall {
   float *lse;    // [heads][rows]: log of the sum of exp(scale * q . k), -inf where no key is seen
   float *delta;  // [heads][rows]: dout . out
   float *part;   // partial results of a split call
-  // 32-bit calls on tcgen05: the power of two that the float16 parts of each tile of
-  // 128 tokens of a head are scaled by, [tile][head] (tiles numbered as Span says)
+  // Operands made in float16.  32-bit calls: the power of two that the parts of each
+  // tile of 128 tokens of a head are scaled by, [tile][head] (tiles numbered as Span
+  // says).  bfloat16 calls: bits of the largest magnitude of each sequence and key head,
+  // [sequence][key head], from which the power follows
   const int32_t *q_power, *k_power, *v_power, *dout_power;
   int64_t rows;  // rows of lse for a head: all tokens of q
   int sequences, q_tokens, k_tokens;
@@ -151,6 +153,7 @@ cudaError_t few_forward_launch(const AttnCall &c, int type, cudaStream_t s);
 // Where operands that were made are: [tokens][heads][width]; width 0: none are.
 struct SplitParts {
   int width;
+  bool halves;  // bfloat16's made in float16
   void *q, *k, *v, *dout;
 };
 

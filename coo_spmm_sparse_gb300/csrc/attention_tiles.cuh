@@ -290,7 +290,7 @@ static inline bool maps_of(TileMaps *m, const AttnCall &c, int type, const Split
   const int64_t qn = c.q_offsets ? 1 : c.sequences, kn = c.k_offsets ? 1 : c.sequences;
   const auto map = [&](CUtensorMap *to, const Strided &t, void *part, int64_t heads, int64_t tokens, int64_t seqs) {
     const int64_t row = parts.width;
-    return row ? map_of(to, type == SNACK_F32 ? SNACK_F16 : type, Strided{part, tokens * heads * row, heads * row, row}, row, heads, tokens, seqs)
+    return row ? map_of(to, type == SNACK_F32 || parts.halves ? SNACK_F16 : type, Strided{part, tokens * heads * row, heads * row, row}, row, heads, tokens, seqs)
                  : map_of(to, type, t, c.d, heads, tokens, seqs);
   };
   return map(&m->q, c.q, parts.q, c.heads, c.q_tokens, qn) && map(&m->k, c.k, parts.k, c.key_heads, c.k_tokens, kn) &&

@@ -11,16 +11,36 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHalf = kTile / 2;  // columns of a tile that a warpgroup takes
 constexpr int kStatWarp = 10;
 
-// Left operands of the second products, in one part of the type or in two; 32 values
-// of a row, columns [x, x + 32) of a warpgroup's 64 that begin at `at`.
+// T is the type of the call's tensors and Op that of the operands: T's own, or float16
+// for bfloat16 calls of more than 64 columns and some work (halves_take), whose
+// tensors are made in it first, times a power of two for each sequence and key head.
+// Float16 has 11 bits, so that probabilities and gradients of scores in one part
+// leave bfloat16's results as their rounding does, in seven products for both kernels
+// where two parts of both take ten.
 //
-// Gradients of scores are always in two: in 16-bit types rounding them to one made dq
-// and dk 1.5 times as far off as the rounding of the results alone.  Probabilities are
-// in two but in float16: in one, bfloat16's dv was 1.4 times as far off (two cost 9
+// Else left operands of the second products are in two parts where rounding them
+// to one shows in the results.  Gradients of scores: dq and dk would be 1.5 times as far
+// off as rounding them alone.  Bfloat16's probabilities: dv 1.4 times (two parts cost 9
 // packed sequences at 64 columns 322 -> 334 us, 8192 tokens at 128 1902 -> 2012, forward
-// included); float16's is 1.4 times, in a type of eight times the precision.
-template <typename T>
-constexpr bool kFineProbs = !std::is_same<T, __half>::value;
+// included).  Float16's are in one: 1.4 times, in a type of eight times the precision.
+template <typename T, typename Op>
+constexpr bool kHalves = std::is_same<T, __nv_bfloat16>::value && std::is_same<Op, __half>::value;
+template <typename T, typename Op>
+constexpr bool kFineScores = !kHalves<T, Op>;
+template <typename Op>
+constexpr bool kFineProbs = !std::is_same<Op, __half>::value;
+
+// What brings back a product with a tensor that was made in float16; `sequence`
+// numbers the tensor's side as find_tile does.
+__device__ __forceinline__ float halves_back(const int32_t *peak, int sequence, int key_heads, int kh) {
+  return power_of_two(-power_to_half((uint32_t)__ldg(peak + (int64_t)sequence * key_heads + kh)));
+}
+__device__ __forceinline__ int other_sequence(int s, bool ragged, bool other_ragged) {
+  return s - (ragged ? 1 : 0) + (other_ragged ? 1 : 0);
+}
+
+// 32 values of a row, columns [x, x + 32) of a warpgroup's 64 that begin at `at`, as
+// the left operand of a product.
 template <typename T, bool FINE>
 __device__ __forceinline__ void store_row32(uint32_t at, int x, const float *v) {
   if constexpr (FINE) {
@@ -130,11 +150,11 @@ __device__ __noinline__ void poison_keys(const AttnCall &c) {
 // Order of the products: dV(n), S(n+1), dK(n), dP(n+1), so that the
 // exponentials of n+1 run while dK(n) and dP(n+1) do, and dS(n+1) while dV(n+1)
 // does.  Scores, dP and both sums fill the 512 columns of tensor memory.
-template <typename T, int DP, bool DROP>
+template <typename T, typename Op, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_keys(const __grid_constant__ AttnCall c, const __grid_constant__ TileMaps maps) {
-  constexpr int W = wide<T, DP>();
-  constexpr bool kSplit = Operand<T>::kSplit;
+  constexpr int W = wide<Op, DP>();
+  constexpr bool kSplit = Operand<Op>::kSplit;
   extern __shared__ unsigned char raw[];
   __shared__ KeyBars bars;
   unsigned char *const sk = align1024(raw), *const sv = sk + tile_bytes<W>();
@@ -235,7 +255,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.q_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<T, DP>(t_s, k0, q0 + (n & 1) * kStep);
+            products<Op, DP>(t_s, k0, q0 + (n & 1) * kStep);
             tc::commit(&bars.scores);
           }
           __syncwarp();
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.d_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<T, DP>(t_dp, v0, d0 + (n & 1) * kStep);
+            products<Op, DP>(t_dp, v0, d0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs);
           }
           __syncwarp();
@@ -255,7 +275,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = wait(&bars.probs, n & 1);
           if (!ok) break;
           if (leader) {
-            row_sums<T, DP, kFineProbs<T>>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
+            row_sums<Op, DP, kFineProbs<Op>>(t_dv, t_s, d0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.d_empty[n & 1]);
           }
           __syncwarp();
@@ -263,7 +283,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = ok && wait(&bars.dscores, n & 1);
           if (!ok) break;
           if (leader) {
-            row_sums<T, DP, true>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
+            row_sums<Op, DP, kFineScores<T, Op>>(t_dk, t_dp, q0c + (n & 1) * kStep, n > 0);
             tc::commit(&bars.q_empty[n & 1]);
           }
           __syncwarp();
@@ -277,7 +297,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     } else if (warp == kStatWarp) {
-      constexpr float up = kUp<T>;
+      constexpr float up = kUp<Op>;
       float k_back = 1.f, v_back = 1.f;
       if (kSplit && all > 0) {
         k_back = power_back(c.k_power, ks.tile + at.tile, c.key_heads, kh);
@@ -316,6 +336,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float acc[kSplit ? DP : 1] = {};  // split: the sums of dK (first warpgroup) or dV
     float back = 0.f;                 // split: what the last step's are multiplied by
     int power = kMostPower;           // else of the row's sums
+    float scores_by = c.scale_log2, dprobs_by = exp2f(-kUp<Op>);
+    if (kHalves<T, Op> && all > 0) {
+      const int q_at = other_sequence(at.s, c.k_offsets != nullptr, c.q_offsets != nullptr);
+      scores_by *= halves_back(c.k_power, at.s, c.key_heads, kh) * halves_back(c.q_power, q_at, c.key_heads, kh);
+      dprobs_by *= halves_back(c.v_power, at.s, c.key_heads, kh) * halves_back(c.dout_power, q_at, c.key_heads, kh);
+    }
     const bool alone = nk == 1 || (c.causal && j0 == 0 && (warp & 3) == 0);
     const uint64_t seed = DROP ? c.draws() : 0;
     bool ok = true;
@@ -346,7 +372,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (n > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile, back);  // dV of the tile before
           back = bars.by[slot].dout;
         }
-      const float cs = kSplit ? bars.by[slot].scores : c.scale_log2, dprobs = kSplit ? bars.by[slot].dprobs : exp2f(-kUp<T>);
+      const float cs = kSplit ? bars.by[slot].scores : scores_by, dprobs = kSplit ? bars.by[slot].dprobs : dprobs_by;
       const float2 cs2 = make_float2(cs, cs);
       float p[kHalf];
       tc::load32(s_at, p);
@@ -373,7 +399,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = !DROP || (kept[e & 3] >> ((x + e) & ~3) & 1) ? p[x + e] : 0.f;
-        store_row32<T, kFineProbs<T>>(s_at, x, v);
+        store_row32<Op, kFineProbs<Op>>(s_at, x, v);
       }
       tc::wait_stores();
       tc::fence_before();
@@ -412,7 +438,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int x = 0; x < kHalf; ++x)
           if (nk == 1 || (j == 0 && q0 + x == nq - nk)) p[x] = 0.f;
       }
-      if constexpr (kScaled<T>) {
+      if constexpr (kScaled<Op>) {
         uint32_t exponent;
         ok = row_exponent(bars.tops, p, n, &exponent, failed, c.polls);
         if (!ok) break;
@@ -431,8 +457,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) p[x] *= up;
       }
-      store_row32<T, true>(dp_at, 0, p);
-      store_row32<T, true>(dp_at, 32, p + 32);
+      store_row32<Op, kFineScores<T, Op>>(dp_at, 0, p);
+      store_row32<Op, kFineScores<T, Op>>(dp_at, 32, p + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores);
@@ -448,12 +474,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (j < ks.cover)
         row = static_cast<T *>(to.p) + (c.k_offsets ? (ks.row + j) * to.token : ks.seq * to.seq + j * to.token) +
               kh * to.head;
-      float factor = w ? exp2f(-kUp<T>) * c.keep_scale : c.scale;
+      float factor = w ? exp2f(-kUp<Op>) * c.keep_scale : c.scale;
+      if (kHalves<T, Op> && all > 0)
+        factor *= halves_back(w ? c.dout_power : c.q_power,
+                              other_sequence(at.s, c.k_offsets != nullptr, c.q_offsets != nullptr), c.key_heads, kh);
       if constexpr (kSplit) {
         if (all > 0) add_sums<DP>(acc, tmem + lanes + 2 * kTile + (w ? 0 : DP), back);
         store_floats<DP>(row, acc, factor, c.d, j >= nk);
       } else {
-        if (kScaled<T> && !w) factor *= power_of_two(-power);
+        if (kScaled<Op> && !w) factor *= power_of_two(-power);
         store_sums<T, DP>(tmem + lanes + 2 * kTile + (w ? 0 : DP), row, factor, c.d, all > 0, j >= nk);
       }
     }
@@ -505,11 +534,11 @@ __device__ __noinline__ void poison_queries(const AttnCall &c) {
 // Scores and dP take turns in three buffers of tensor memory (S(n) in 2n mod 3,
 // dP(n) in 2n+1 mod 3), so that S(n+1) is there before the rows are done with n.
 // Order of the products: dP(n+1), dQ(n), S(n+2).
-template <typename T, int DP, bool DROP>
+template <typename T, typename Op, int DP, bool DROP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_backward_queries(const __grid_constant__ AttnCall c, const __grid_constant__ TileMaps maps) {
-  constexpr int W = wide<T, DP>();
-  constexpr bool kSplit = Operand<T>::kSplit;
+  constexpr int W = wide<Op, DP>();
+  constexpr bool kSplit = Operand<Op>::kSplit;
   extern __shared__ unsigned char raw[];
   __shared__ QueryBars bars;
   unsigned char *const sq = align1024(raw), *const sd = sq + tile_bytes<W>();
@@ -610,7 +639,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto scores = [&](int n) {
           const bool done = wait(&bars.k_full[n % 3], (n / 3) & 1);
           if (done && leader) {
-            products<T, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
+            products<Op, DP>(tmem + 2 * n % 3 * kTile, q0, k0 + n % 3 * kStep);
             tc::commit(&bars.scores[n & 1]);
           }
           __syncwarp();
@@ -619,7 +648,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const auto dprobs = [&](int n) {
           const bool done = wait(&bars.v_full[n & 1], (n / 2) & 1);
           if (done && leader) {
-            products<T, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
+            products<Op, DP>(tmem + (2 * n + 1) % 3 * kTile, d0, v0 + (n & 1) * kStep);
             tc::commit(&bars.dprobs[n & 1]);
             tc::commit(&bars.v_empty[n & 1]);
           }
@@ -634,7 +663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (leader) {
             // split: two buffers in turn, each added to the rows' own sums two tiles later
             const uint32_t to = tmem + 3 * kTile + (kSplit ? (n & 1) * DP : 0), ds_at = tmem + (2 * n + 1) % 3 * kTile;
-            row_sums<T, DP, true>(to, ds_at, k0c + n % 3 * kStep, n > 0);
+            row_sums<Op, DP, kFineScores<T, Op>>(to, ds_at, k0c + n % 3 * kStep, n > 0);
             tc::commit(&bars.k_empty[n % 3]);
           }
           __syncwarp();
@@ -677,6 +706,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       q_back = power_back(c.q_power, qs.tile + at.tile, c.heads, head);
       d_back = power_back(c.dout_power, qs.tile + at.tile, c.heads, head);
       load_powers(0);
+    }
+    if (kHalves<T, Op> && all > 0) {
+      const int k_at = other_sequence(at.s, c.q_offsets != nullptr, c.k_offsets != nullptr);
+      q_back = halves_back(c.q_power, at.s, c.key_heads, kh);
+      d_back = halves_back(c.dout_power, at.s, c.key_heads, kh);
+      k_next = halves_back(c.k_power, k_at, c.key_heads, kh);
+      v_next = halves_back(c.v_power, k_at, c.key_heads, kh);
     }
     const float2 off2 = make_float2(-lse, -lse);
     const float2 delta2 = make_float2(-delta, -delta);
@@ -733,7 +769,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (cut)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] = x < left ? t[x] : 0.f;
-      if constexpr (kScaled<T>) {
+      if constexpr (kScaled<Op>) {
         uint32_t exponent;
         ok = row_exponent(bars.tops, t, n, &exponent, failed, c.polls);
         if (!ok) break;
@@ -757,8 +793,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int x = 0; x < kHalf; ++x) t[x] *= up;
       }
-      store_row32<T, true>(dp_at, 0, t);
-      store_row32<T, true>(dp_at, 32, t + 32);
+      store_row32<Op, kFineScores<T, Op>>(dp_at, 0, t);
+      store_row32<Op, kFineScores<T, Op>>(dp_at, 32, t + 32);
       tc::wait_stores();
       tc::fence_before();
       tc::bar_arrive_warp(&bars.dscores[b]);
@@ -779,7 +815,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                            n == all - 1 ? back : back_before);
         store_floats<DP / 2>(row, acc, c.scale, c.d - from, lim == 0);
       } else {
-        const float factor = kScaled<T> ? c.scale * power_of_two(-power) : c.scale;
+        const float factor = (kScaled<Op> ? c.scale * power_of_two(-power) : c.scale) * k_next;
         store_sums<T, DP / 2>(at_lane + 3 * kTile + from, row, factor, c.d - from, all > 0, lim == 0);
       }
     }
@@ -798,11 +834,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (blockIdx.x == gridDim.x - 1) dependency_wait();
 }
 
-template <typename T, int DP, bool DROP>
+template <typename T, typename Op, int DP, bool DROP>
 cudaError_t backward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
-  constexpr int W = wide<T, DP>();
+  constexpr int W = wide<Op, DP>();
   if (c.dk.p || c.dv.p) {
-    const auto kern = tile_backward_keys<T, DP, DROP>;
+    const auto kern = tile_backward_keys<T, Op, DP, DROP>;
     cudaError_t e = allow_smem(kern, keys_smem<W>());
     if (e != cudaSuccess) return e;
     const int64_t blocks = tiles_of(c.k_offsets != nullptr, c.sequences, c.k_tokens, 1, kTile) * c.key_heads;
@@ -810,28 +846,29 @@ cudaError_t backward_launch(const AttnCall &c, const TileMaps &m, cudaStream_t s
     if (e != cudaSuccess) return e;
   }
   if (!c.dq.p) return cudaSuccess;
-  const auto kern = tile_backward_queries<T, DP, DROP>;
+  const auto kern = tile_backward_queries<T, Op, DP, DROP>;
   const cudaError_t e = allow_smem(kern, queries_smem<W>());
   if (e != cudaSuccess) return e;
   const int64_t blocks = tiles_of(c.q_offsets != nullptr, c.sequences, c.q_tokens, 1, kTile) * c.heads;
   return launch_kernel(kern, dim3((unsigned)blocks), kTileThreads, queries_smem<W>(), c.dk.p || c.dv.p, s, c, m);
 }
 
-template <typename T>
+template <typename T, typename Op, int DP>
 cudaError_t backward_typed(const AttnCall &c, const TileMaps &m, cudaStream_t s) {
-  if constexpr (!Operand<T>::kSplit)
-    if (c.d > 64) return c.drop ? backward_launch<T, 128, true>(c, m, s) : backward_launch<T, 128, false>(c, m, s);
-  return c.drop ? backward_launch<T, 64, true>(c, m, s) : backward_launch<T, 64, false>(c, m, s);
+  return c.drop ? backward_launch<T, Op, DP, true>(c, m, s) : backward_launch<T, Op, DP, false>(c, m, s);
 }
 
 }  // namespace
 
 cudaError_t tile_backward_launch(const AttnCall &c, int type, const SplitParts &parts, cudaStream_t s) {
+  using Bf16 = __nv_bfloat16;
   TileMaps m = {};
   if (!maps_of(&m, c, type, parts, true)) return cudaErrorInvalidValue;
-  return type == SNACK_F32    ? backward_typed<float>(c, m, s)
-         : type == SNACK_BF16 ? backward_typed<__nv_bfloat16>(c, m, s)
-                              : backward_typed<__half>(c, m, s);
+  if (type == SNACK_F32) return backward_typed<float, float, 64>(c, m, s);
+  if (type == SNACK_F16)
+    return c.d > 64 ? backward_typed<__half, __half, 128>(c, m, s) : backward_typed<__half, __half, 64>(c, m, s);
+  if (parts.halves) return backward_typed<Bf16, __half, 128>(c, m, s);
+  return c.d > 64 ? backward_typed<Bf16, Bf16, 128>(c, m, s) : backward_typed<Bf16, Bf16, 64>(c, m, s);
 }
 
 cudaError_t tile_backward_failed(int *flag, cudaStream_t s) { return read_flag(g_attention_failed, flag, s); }

@@ -327,3 +327,75 @@ def test_gradients_of_scores_that_grow_along_a_row(dtype, d, side):
             for at in range(0, n, 128):
                 ref = want[name][0][:, at: at + 128]
                 assert float((t[:, at: at + 128].double() - ref).norm()) <= u * float(ref.norm()), (name, at)
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("d", [72, 128])
+def test_long_bfloat16_sequences_do_not_change_with_the_others(ragged, d):
+    """The sizes whose operands are made in float16: powers of two and what is not finite, as above."""
+    n, length = (3, 2400) if ragged else (3, 4200)
+    shape, opts, at = layouts(d, n, length)[2 if ragged else 0]
+    g = gen(d)
+    x = [rnd(g, (*shape, h, d), BF16) for h in (12, 4, 4, 12)]
+    opts = dict(opts, dropout=0.1, seed=3)
+    want = run(*x, **opts)
+    powers = ((0, 0, 0), (24, -24, 12), (-24, 0, -24))
+    y = [t.clone() for t in x]
+    for s, (a, b, c) in zip(at, powers):
+        for t, p in zip(y, (a, -a, b, c)):
+            t[s] *= 2.0 ** p
+    got = run(*y, **opts)
+    assert torch.equal(got[1], want[1])
+    for s, (a, b, c) in zip(at, powers):
+        for u, w, p in zip((got[0], *got[2:]), (want[0], *want[2:]), (b, b + c - a, b + c + a, c)):
+            same_but_for_powers(u[s], w[s], p)
+    for t in x:
+        t[at[1]][20, 1, 3] = math.nan
+    got = run(*x, **opts)
+    for s in (at[0], at[2]):
+        for u, w in zip((got[0], *got[2:]), (want[0], *want[2:])):
+            assert torch.equal(u[s], w[s])
+
+
+@pytest.mark.parametrize("d,causal,dropout", [(128, True, 0.0), (80, False, 0.0), (128, True, 0.2), (65, True, 0.0)])
+def test_long_bfloat16_gradients(d, causal, dropout):
+    """Against 64 bits, and, as long sequences' bounds are wide, as exact as their rounding (a tenth
+    for delta of the rounded out); then with dout of every other token 2^-17 of the rest."""
+    import attention_ref
+    g = gen(d)
+    n, heads = 7200, 12
+    q, k, v, dout = (rnd(g, (1, n, h, d), BF16) for h in (heads, 4, 4, heads))
+    opts = dict(causal=causal, dropout=dropout, seed=2)
+    size = torch.ones(n, device="cuda", dtype=torch.float64)
+    size[1::2] = 2.0 ** -17
+    size = size[None, :, None, None]
+    for scale in (torch.ones_like(size), size):
+        x = (dout.double() * scale).to(BF16)
+        got = run(q, k, v, x, **opts)
+        for h in range(4):  # a key head at a time: the reference holds its probabilities
+            at = slice(3 * h, 3 * h + 3)
+            if dropout:  # (the mask goes by all heads; the heads' own reference needs it all)
+                break
+            want = attention_ref.attention(q[:, :, at], k[:, :, h: h + 1], v[:, :, h: h + 1], dout=x[:, :, at], causal=causal)
+            attention_ref.assert_within({"out": got[0][:, :, at], "dv": got[4][:, :, h: h + 1],
+                                         "dk": got[3][:, :, h: h + 1], "dq": got[2][:, :, at]}, want)
+            ref = want["dq"][0] / scale
+            off, least = (((t.double() / scale) - ref).norm() for t in (got[2][:, :, at], want["dq"][0].to(BF16)))
+            assert float(off) <= 1.1 * float(least), float(off / least)
+            for name, t in (("dk", got[3]), ("dv", got[4])):
+                ref = want[name][0]
+                off, least = ((y.double() - ref).norm() for y in (t[:, :, h: h + 1], ref.to(BF16)))
+                assert float(off) <= 1.1 * float(least), (name, float(off / least))
+            del want
+    if dropout:  # dv by its linearity in dout: a single row's
+        x = torch.zeros_like(dout)
+        x[:, 5000] = dout[:, 5000]
+        out, lse, _, _, dv = run(q, k, v, x, **opts)
+        M = attention_ref.mask_of(2, (torch.tensor([5000 * heads], device="cuda") + torch.arange(heads, device="cuda")) << 30,
+                                  n, dropout)
+        s = torch.einsum("hd,jhd->hj", q[0, 5000].double(), k[0].double().repeat_interleave(3, 1)) * d ** -0.5
+        P = torch.softmax(s[:, :5001], -1) * M[:, :5001]
+        want = torch.einsum("hj,hd->jhd", P, dout[0, 5000].double()).view(5001, 4, 3, d).sum(2)
+        terms = torch.einsum("hj,hd->jhd", P, dout[0, 5000].double().abs()).view(5001, 4, 3, d).sum(2)
+        assert bool(((dv[0, :5001].double() - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + 2.0 ** -9 * terms + 1e-12).all())
+        assert not dv[0, 5001:].any()
