@@ -706,7 +706,7 @@ cudaError_t backward_typed(AttnCall c, const Plan &p, int type, char *workspace,
   SplitParts parts = {};
   if (p.width) e = make_parts<T>(&c, p, true, workspace, &parts, s);
   if (e != cudaSuccess) return e;
-  // (a float16 call whose dout alone lies badly was not planned for)
+  // (a 16-bit call whose dout alone lies badly was not planned for)
   if (p.tiles && (p.width || tiles_read(c))) return tile_backward_launch(c, type, parts, s);
   return rows_backward_launch<T>(c, s);
 }

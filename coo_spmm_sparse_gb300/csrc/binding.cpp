@@ -702,6 +702,19 @@ struct Attention {
     s[2] = t.stride(n - 2);
   }
 
+  // Whether the rows of a 16-bit tensor of t's shape begin on 16 bytes and repeat no memory.  A
+  // gradient whose do not is copied: it is the only operand that the plan does not know, and without
+  // room for it in the workspace its call would leave the tensor cores' fast path.  (Of head sizes
+  // that do not fill 16 bytes every tensor is copied in the call.)
+  static bool even(const at::Tensor &t, const void *p, const int64_t (&s)[3]) {
+    if (t.element_size() != 2 || t.size(-1) % 8 || t.numel() == 0) return true;
+    for (int64_t i = 0; i < t.dim() - 1; ++i) {
+      const int64_t stride = s[3 - (t.dim() - 1) + i];
+      if (t.size(i) > 1 && (stride == 0 || stride % 8)) return false;
+    }
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  }
+
   const at::Tensor &like_q(PyObject *o, const char *name, int64_t (&s)[3]) { return like(o, *q, name, "q", s); }
   const at::Tensor &like(PyObject *o, const at::Tensor &other, const char *name, const char *of, int64_t (&s)[3]) {
     const at::Tensor &t = dense(o, name);
@@ -813,6 +826,12 @@ PyObject *attention_backward(PyObject *, PyObject *const *o, Py_ssize_t n) {
     g.lse = static_cast<const float *>(lse.data_ptr());
     const bool need_dq = truth(r[3]), need_dkv = truth(r[4]);
     const Stream s(r[5], m.dev.dev);
+    at::Tensor even_dout;
+    if (!Attention::even(*m.q, g.dout, g.dout_stride)) {
+      even_dout = THPVariable_Unpack(o[0]).detach().clone(at::MemoryFormat::Contiguous);
+      g.dout = even_dout.data_ptr();
+      Attention::strides(even_dout, g.dout_stride, "dout");
+    }
     at::Tensor fresh[3];
     PyObject *res[3] = {Py_None, Py_None, Py_None};
     const auto result = [&](int i, const at::Tensor &like, const char *name, const char *of, int64_t (&st)[3],

@@ -399,3 +399,22 @@ def test_long_bfloat16_gradients(d, causal, dropout):
         terms = torch.einsum("hj,hd->jhd", P, dout[0, 5000].double().abs()).view(5001, 4, 3, d).sum(2)
         assert bool(((dv[0, :5001].double() - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + 2.0 ** -9 * terms + 1e-12).all())
         assert not dv[0, 5001:].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("form", ["offset", "repeated", "odd strides"])
+def test_a_gradient_that_lies_badly_takes_the_same_path(dtype, form):
+    """The same bits as from a copy of it (mma.sync would differ in some)."""
+    import coo_spmm_sparse_gb300 as sn
+    g = gen(26)
+    q, k, v = (rnd(g, (2, 500, h, 64), dtype) for h in (8, 4, 4))
+    if form == "offset":
+        dout = rnd(g, (2 * 500 * 8 * 64 + 4,), dtype)[4:].view(2, 500, 8, 64)
+    elif form == "repeated":
+        dout = rnd(g, (2, 500, 1, 64), dtype).expand(2, 500, 8, 64)
+    else:
+        dout = rnd(g, (2, 500, 8, 65), dtype)[..., :64]
+    out, lse = sn.snack_attention_forward(q, k, v)
+    got = sn.snack_attention_backward(dout, q, k, v, out, lse)
+    want = sn.snack_attention_backward(dout.contiguous().clone(), q, k, v, out, lse)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
