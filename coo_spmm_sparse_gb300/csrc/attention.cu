@@ -292,16 +292,35 @@ __global__ void __launch_bounds__(256) copy_operands(const Sources all, int sequ
   }
 }
 
+// Sequence and tile of a tile's number (as Span counts them): by bisection, where
+// find_tile, whose order is the products', goes through the sequences.  s < 0: the
+// number is left out.
+__device__ __forceinline__ Place numbered_tile(const Source &t, int n, int64_t number) {
+  if (!t.offsets) {
+    const int per = (t.tokens + kTile - 1) / kTile;
+    const int s = (int)(number / per);
+    return s < n ? Place{s, (int)(number - (int64_t)s * per)} : Place{-1, 0};
+  }
+  int lo = 0, hi = n + 2;  // the last sequence whose tiles begin at or before the number
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (ragged_begin(t.offsets, mid, t.tokens) / kTile + mid <= number) lo = mid; else hi = mid;
+  }
+  const int a = ragged_begin(t.offsets, lo, t.tokens), b = ragged_end(t.offsets, lo, n, t.tokens);
+  const int64_t tile = number - (a / kTile + lo);
+  return tile >= 0 && tile * kTile < b - a ? Place{lo, (int)tile} : Place{-1, 0};
+}
+
 // 32-bit tensors as two float16 parts, rows of 64 high and 64 low halves (zeros as
 // above), of the elements times the power of two that brings the largest of their
 // tile to [2^14, 2^15).  A block takes a tile of a head, which stays in registers
-// from the search for its largest on: the memory is read once.  Grid: x = tile * heads +
-// head, y = tensor.
+// from the search for its largest on: the memory is read once.  Grid: x = the tile's
+// number * heads + head, y = tensor.
 __global__ void __launch_bounds__(256) split_operands(const Sources all, int sequences, int d) {
   __shared__ uint32_t tops[8];
   const Source &t = all.t[blockIdx.y];
   const int head = blockIdx.x % t.heads;
-  const Place at = find_tile(t.offsets, sequences, t.tokens, 1, kTile, blockIdx.x / t.heads, false);
+  const Place at = numbered_tile(t, sequences, blockIdx.x / t.heads);
   if (at.s < 0) return;
   const Span sp = own_span(t.offsets, t.lengths, at.s, sequences, t.tokens);
   constexpr int kRows = kTile / 16;  // of a thread; 16 threads take a row
@@ -325,7 +344,7 @@ __global__ void __launch_bounds__(256) split_operands(const Sources all, int seq
 #pragma unroll
   for (int w = 0; w < 8; ++w) most = max(most, tops[w]);
   const int power = power_to_half(most);
-  if (threadIdx.x == 0) t.power[(sp.tile + at.tile) * t.heads + head] = power;
+  if (threadIdx.x == 0) t.power[blockIdx.x] = power;
   const float by = power_of_two(power);
   uint16_t *const made = static_cast<uint16_t *>(t.made) + head * 128 + col;
 #pragma unroll
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(256) half_operands(const Sources all, int sequ
   __shared__ uint32_t tops[8];
   const Source &t = all.t[blockIdx.y];
   const int head = blockIdx.x % t.heads, kh = head / (t.heads / key_heads);
-  const Place at = find_tile(t.offsets, sequences, t.tokens, 1, kTile, blockIdx.x / t.heads, false);
+  const Place at = numbered_tile(t, sequences, blockIdx.x / t.heads);
   if (at.s < 0) return;
   const Span sp = own_span(t.offsets, t.lengths, at.s, sequences, t.tokens);
   constexpr int kRows = kTile / 16;  // of a thread; 16 threads take a row
@@ -619,8 +638,12 @@ Plan plan_forward(const AttnCall &c, int type) {
 // seven products instead of ten, for passes that make them.  X as above; heads of 128,
 // made / as they lie, us: 2 x 2048 tokens, 16 over 4 heads (X = 1.3e8) 171 / 150; 1 x 4096
 // (2.7e8) 284 / 271; 1 x 8192 (1.1e9) 691 / 750; 32 over 8 (2.1e9) 1375 / 1550; 4 x 4096 (2.1e9)
-// 1618 / 1722.  At 64 columns exponentials bind, not products.
-bool halves_take(const AttnCall &c) { return c.d > 64 && (double)c.rows * c.heads * c.k_tokens >= 6e8; }
+// 1618 / 1722.  At 64 columns exponentials bind, not products.  On a ragged side the mean of
+// the keys counts: 500 x 40 tokens have few products however many tokens there are.
+bool halves_take(const AttnCall &c) {
+  const double keys = c.k_offsets ? (double)c.k_tokens / std::max(c.sequences, 1) : c.k_tokens;
+  return c.d > 64 && (double)c.rows * c.heads * keys >= 6e8;
+}
 
 Plan plan_backward(const AttnCall &c, int type) {
   Plan p;
@@ -660,8 +683,8 @@ cudaError_t make_parts(AttnCall *c, const Plan &p, bool backward, char *workspac
   c->k_power = all.t[1].power;
   c->v_power = all.t[2].power;
   c->dout_power = all.t[3].power;
-  const int64_t q = tiles_of(c->q_offsets, c->sequences, c->q_tokens, 1, kTile) * c->heads;
-  const int64_t k = tiles_of(c->k_offsets, c->sequences, c->k_tokens, 1, kTile) * c->key_heads;
+  const int64_t q = tile_numbers(c->q_offsets, c->sequences, c->q_tokens) * c->heads;
+  const int64_t k = tile_numbers(c->k_offsets, c->sequences, c->k_tokens) * c->key_heads;
   const dim3 tiles((unsigned)std::max(q, k), tensors);
   if constexpr (sizeof(T) == 4) {
     return launch_kernel(split_operands, tiles, 256, 0, false, s, all, c->sequences, c->d);

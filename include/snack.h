@@ -500,7 +500,7 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
  * sequences].  Products are summed in 32 bits.  In 16-bit types P is rounded to
  * the type before the second product, as tensor instructions take both
  * operands in one type (bfloat16's dv of calls of some size: in two parts; above
- * 64 columns and 6e8 query rows * keys, backward, all its operands in float16, times a power
+ * 64 columns and 6e8 query rows * keys of a sequence, backward, all its operands in float16, times a power
  * of two for each sequence and key head: nothing lost above 2^-28 of the largest).  32-bit calls of some size (head_size up to 64, see
  * attention.cu) take each operand as two float16 parts, every 128 tokens of a head
  * (from its sequence's first on) times a power of two of their own: 22 bits of what
