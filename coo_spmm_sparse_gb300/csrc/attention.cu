@@ -5,7 +5,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "attention.cuh"
+#include "attention_rows.cuh"
 #include "tcgen05.cuh"
 
 namespace snack {
@@ -80,97 +80,89 @@ __device__ __forceinline__ int seen_by_row(const AttnCall &c, int64_t row, int s
   return seen_keys(c.causal, c.q_offsets ? (int)(row - qs.row) : token, qs.valid, ks.valid);
 }
 
-// Those rows of a sequence are neighbours (the first ones of a causal call): block
-// `part` of `parts` of a sequence gives a warp one row at a time, whose L lanes read a
-// key side by side, four times 32 / L keys at once.  The lanes' parts of the eight
-// products are added up so that each lane is left with one of them.
-template <typename T, int L, bool VEC>
-__device__ __forceinline__ void delta_of_few_keys(const AttnCall &c, int s, int part, int parts) {
-  constexpr int E = 16 / sizeof(T), kAhead = 4, kKeys = 32 / L;
-  const int lane = threadIdx.x & 31, col = lane % L * E;
-  const bool lower = lane & (L / 2), later = lane & (L / 4), odd = lane & (L / 8);  // dprob; of keys 2 and 3; 1 and 3
-  const int own = (later ? 2 * kKeys : 0) + (odd ? kKeys : 0) + lane / L;
-  const bool counts = !lower && (L == 8 || !(lane & 1));
+// Those rows of a sequence are neighbours (the first ones of a causal call).  A block
+// takes 32 of them and one head at a time, every `parts`-th of its sequence and head;
+// both products on mma.sync, a warp 16 rows and 16 keys of them.  (A warp a row, its lanes
+// side by side along keys, took 170 us of a call of 500 x 40 tokens.)
+template <int DP>
+constexpr size_t few_keys_smem() { return 4 * kFewKeys * (DP + 8) * 2; }
+template <typename T, int DP>
+__device__ __forceinline__ void delta_of_few_keys(const AttnCall &c, int64_t block, int parts) {
+  using Ops = Tile<T, DP>;
+  constexpr int kLd = Ops::kLd, kRows = 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float sums[2][kRows];
+  T *const sq = reinterpret_cast<T *>(smem), *const sd = sq + kRows * kLd, *const sk = sd + kRows * kLd,
+           *const sv = sk + kFewKeys * kLd;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = (int)(block % parts);
+  const int head = (int)(block / parts % c.heads), s = (int)(block / parts / c.heads), kh = head / c.group;
   const Span qs = own_span(c.q_offsets, c.q_lengths, c.q_offsets ? s + 1 : s, c.sequences, c.q_tokens);
   const Span ks = own_span(c.k_offsets, c.k_lengths, c.k_offsets ? s + 1 : s, c.sequences, c.k_tokens);
   const int nq = qs.valid, nk = ks.valid;
   const int lo = c.causal ? max(0, nq - nk + 1) : 0;
   const int hi = c.causal ? min((int64_t)nq, (int64_t)nq - nk + kFewKeys) : few_keys(nk) ? nq : 0;
-  const int64_t items = (int64_t)max(0, hi - lo) * c.heads;
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  for (int64_t item = (int64_t)part * 8 + (threadIdx.x >> 5); item < items; item += (int64_t)parts * 8) {
-    const int i = lo + (int)(item / c.heads), head = (int)(item % c.heads), kh = head / c.group;
-    const int64_t row = qs.row + i, place = (int64_t)head * c.rows + row;
-    const int64_t q_at = c.q_offsets ? row : i, k_at = c.k_offsets ? ks.row : 0;
-    const int seen = seen_keys(c.causal, i, nq, nk);
-    const float lse = c.lse[place];
-    const bool some = col < c.d;
-    const auto load = [&](const T *at) {
-      return VEC ? *reinterpret_cast<const uint4 *>(at) : load_vector(at, c.d - col);
-    };
-    const auto of_query = [&](const Strided &t) {
-      return some ? load(static_cast<const T *>(t.p) + qs.seq * t.seq + q_at * t.token + head * t.head + col) : none;
-    };
-    const uint4 qu = of_query(c.q), gu = of_query(c.dout);
-    const auto of_key = [&](const Strided &t, int j) {
-      return some && j < seen ? load(static_cast<const T *>(t.p) + ks.seq * t.seq + (k_at + j) * t.token +
-                                     kh * t.head + col) : none;
-    };
-    const uint64_t draws = c.drop ? dropout_row(c.draws(), row, c.heads, head) : 0;
-    float delta = 0.f;
-    for (int j0 = 0; j0 < seen; j0 += kAhead * kKeys) {
-      uint4 ku[kAhead], vu[kAhead];
+  int64_t i0 = lo + (int64_t)part * kRows;
+  if (i0 >= hi) return;
+  const Rows<T> kr(c.k, ks, c.k_offsets != nullptr, kh, 1, c.d), vr(c.v, ks, c.k_offsets != nullptr, kh, 1, c.d);
+  const Rows<T> qr(c.q, qs, c.q_offsets != nullptr, head, 1, c.d), dr(c.dout, qs, c.q_offsets != nullptr, head, 1, c.d);
+  copy_rows<T, DP>(sk, kr, 0, kFewKeys, min(nk, kFewKeys));
+  copy_rows<T, DP>(sv, vr, 0, kFewKeys, min(nk, kFewKeys));
+  const int row0 = (warp & 1) * 16, key0 = (warp >> 1) * 16;
+  for (; i0 < hi; i0 += (int64_t)parts * kRows) {
+    copy_rows<T, DP>(sq, qr, (int)i0, kRows, hi);
+    copy_rows<T, DP>(sd, dr, (int)i0, kRows, hi);
+    copies_commit();
+    copies_wait<0>();
+    __syncthreads();
+    if (warp < 4) {
+      float score[2][4] = {}, dprob[2][4] = {};
+      Ops::template rows_by_rows<2>(score, sq + row0 * kLd, sk + key0 * kLd, lane);
+      Ops::template rows_by_rows<2>(dprob, sd + row0 * kLd, sv + key0 * kLd, lane);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        ku[u] = of_key(c.k, j0 + u * kKeys + lane / L);
-        vu[u] = of_key(c.v, j0 + u * kKeys + lane / L);
-      }
-      float q[E], g[E];
-      unpack16<T>(qu, q);
-      unpack16<T>(gu, g);
-      float x[kAhead];
+      for (int h = 0; h < 2; ++h) {
+        const int r = row0 + (lane >> 2) + 8 * h, i = (int)i0 + r;
+        const int seen = i < hi ? seen_keys(c.causal, i, nq, nk) : 0;
+        const int64_t row = qs.row + i;
+        const float lse = seen > 0 ? c.lse[(int64_t)head * c.rows + row] : 0.f;
+        const uint64_t draws = c.drop ? dropout_row(c.draws(), row, c.heads, head) : 0;
+        float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        float a[E], b[E], score = 0.f, dprob = 0.f;
-        unpack16<T>(ku[u], a);
-        unpack16<T>(vu[u], b);
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          score = fmaf(q[e], a[e], score);
-          dprob = fmaf(g[e], b[e], dprob);
-        }
-        x[u] = (lower ? dprob : score) + __shfl_xor_sync(0xffffffffu, lower ? score : dprob, L / 2);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        x[u] = (later ? x[u + 2] : x[u]) + __shfl_xor_sync(0xffffffffu, later ? x[u] : x[u + 2], L / 4);
-      x[0] = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], L / 8);
-      if (L == 16) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-      const float dprob = __shfl_xor_sync(0xffffffffu, x[0], L / 2);
-      const int j = j0 + own;
-      if (counts && j < seen) {
-        float p = expf(x[0] * c.scale - lse) * dprob;
-        if (c.drop) p = draw_lane(dropout_draw(draws, j), j & 3) >= c.drop ? p * c.keep_scale : 0.f;
-        delta += p;
+          for (int e = 0; e < 2; ++e) {
+            const int j = key0 + Ops::column(n, lane, e), x = 2 * h + e;
+            float p = j < seen ? expf(score[n][x] * c.scale - lse) * dprob[n][x] : 0.f;
+            if (c.drop) p = draw_lane(dropout_draw(draws, j), j & 3) >= c.drop ? p * c.keep_scale : 0.f;
+            sum += p;
+          }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if ((lane & 3) == 0) sums[warp >> 1][r] = lse == -INFINITY ? 0.f : sum;
       }
     }
-    delta = warp_sum(delta);
-    if (lane == 0) c.delta[place] = lse == -INFINITY ? 0.f : delta;
+    __syncthreads();
+    if (threadIdx.x < kRows && i0 + threadIdx.x < hi)
+      c.delta[(int64_t)head * c.rows + qs.row + i0 + threadIdx.x] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
   }
 }
 
 // delta of the other rows, dout . out.  A team of lanes takes a row with one 16-byte
 // load of each tensor a lane, and kItems rows at a time, whose loads are in flight
-// together.  The first `few` blocks, `parts` for each sequence, take the rows of few
-// keys: bf16 backward calls, us, with delta of out alone / with them: 8 x 24 tokens, 24
-// heads over 12 of 128, 27 / 35; 8 x 64 47 / 56; 64 x 33, 12 over 4, 70 / 101 (24576 such
-// rows, bound by their instructions).
+// together.  The first `few` blocks take the rows of few keys: bf16 backward calls, us,
+// with delta of out alone / with them (the rest of the call as it was): 8 x 24 tokens, 24
+// heads over 12 of 128, 27 / 31; 64 x 33, 12 over 4, 70 / 79; 300 x 2, 24 over 12, 303 / 357 (two
+// rows to a block); 500 x 40 at 128 columns 698 / 736.
 constexpr int kItems = 4;
 template <typename T, int TEAM, bool VEC>
 __global__ void __launch_bounds__(256, 3) attention_delta(const AttnCall c, int few, int parts) {
   if constexpr (sizeof(T) == 2)
-    if ((int)blockIdx.x < few)
-      return delta_of_few_keys<T, TEAM == 8 ? 8 : 16, VEC>(c, blockIdx.x / parts, blockIdx.x % parts, parts);
+    if ((int)blockIdx.x < few) {
+      for (int64_t b = blockIdx.x; b < (int64_t)c.sequences * c.heads * parts; b += few) {
+        delta_of_few_keys<T, TEAM == 8 ? 64 : 128>(c, b, parts);
+        __syncthreads();
+      }
+      return;
+    }
   constexpr int E = 16 / sizeof(T), kTeams = 256 / TEAM;
   const int lane = threadIdx.x % TEAM;
   const int64_t first = (int64_t)(blockIdx.x - few) * (kTeams * kItems) + threadIdx.x / TEAM;
@@ -220,22 +212,23 @@ cudaError_t delta_launch(const AttnCall &c, cudaStream_t s) {
   const auto even = [](const Strided &t) {
     return aligned_to(t.p, 16) && t.seq % E == 0 && t.token % E == 0 && t.head % E == 0;
   };
-  const bool vec = c.d % E == 0 && even(c.dout) && even(c.out) &&
-                   (sizeof(T) == 4 || (even(c.q) && even(c.k) && even(c.v)));
+  const bool vec = c.d % E == 0 && even(c.dout) && even(c.out);
   const int lanes = vec ? (c.d * (int)sizeof(T) + 15) / 16 : 32;
   const int team = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const int64_t each = 256 / team * kItems;
-  // blocks for rows of few keys: a warp each, or as many for a sequence as keep the SMs busy
+  // blocks for rows of few keys: one for 32 of a sequence and head, or as many as keep the SMs busy
   int64_t few = 0, parts = 0;
   const bool all_long = !c.causal && !c.k_offsets && !c.k_lengths && c.k_tokens > kFewKeys;
   if (sizeof(T) == 2 && c.sequences && !all_long) {
     const int64_t rows = c.causal ? std::min(c.q_tokens, kFewKeys - 1) : c.q_tokens;
-    parts = std::max<int64_t>(1, std::min<int64_t>((rows * c.heads + 7) / 8, 16 * device_sms() / c.sequences));
-    few = c.sequences * parts;
+    const int64_t units = (int64_t)c.sequences * c.heads;
+    parts = std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, 16 * device_sms() / units));
+    few = std::min<int64_t>(units * parts, 1 << 24);
   }
   const dim3 grid((unsigned)((c.rows * c.heads + each - 1) / each + few));
   const auto launch = [&](auto kern) {
-    return launch_kernel(kern, grid, 256, 0, false, s, c, (int)few, (int)parts);
+    return launch_kernel(kern, grid, 256, !few ? 0 : team == 8 ? few_keys_smem<64>() : few_keys_smem<128>(), false, s, c,
+                         (int)few, (int)parts);
   };
   if (!vec) return launch(attention_delta<T, 32, false>);
   return team == 8    ? launch(attention_delta<T, 8, true>)
