@@ -110,6 +110,9 @@ def _split(qkv, heads, key_heads, ragged):
     return tuple(t.unflatten(-1, (-1, d)) for t in parts)
 
 
+_unsafe_view = torch.ops.aten._unsafe_view.default
+
+
 class _PackedAttentionFunction(torch.autograd.Function):
     """The same on parts of one tensor, whose gradient is written in one piece."""
 
@@ -119,7 +122,7 @@ class _PackedAttentionFunction(torch.autograd.Function):
         q, k, v = _split(qkv, heads, key_heads, ragged)
         out, lse = snack_attention_forward(q, k, v, **opts)
         # the same memory as a tensor that is nothing's view: a caller may write to it
-        out = torch.ops.aten._unsafe_view(out, (*qkv.shape[:-1], heads * q.shape[-1]))
+        out = _unsafe_view(out, (*qkv.shape[:-1], heads * q.shape[-1]))
         ctx.shape = heads, key_heads, ragged
         ctx.names = [n for n, t in opts.items() if isinstance(t, torch.Tensor)]
         ctx.opts = {n: t for n, t in opts.items() if n not in ctx.names}
@@ -133,9 +136,8 @@ class _PackedAttentionFunction(torch.autograd.Function):
         q, k, v = _split(qkv, *ctx.shape)
         grad = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
         dq, dk, dv = _split(grad, *ctx.shape)
-        snack_attention_backward(_rows_contiguous(dout).unflatten(-1, q.shape[-2:]), q, k, v,
-                                 out.unflatten(-1, q.shape[-2:]), lse, dq=dq, dk=dk, dv=dv, **ctx.opts,
-                                 **dict(zip(ctx.names, rest)))
+        snack_attention_backward(_rows_contiguous(dout).view(q.shape), q, k, v, out.view(q.shape), lse,
+                                 dq=dq, dk=dk, dv=dv, **ctx.opts, **dict(zip(ctx.names, rest)))
         return grad, None, None, None
 
 
