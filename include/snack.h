@@ -499,17 +499,20 @@ snack_status snack_clip_grad_norm(int64_t count, const void *const *grads, void 
  * All tensors are of `type`; lse is fp32 [heads][query tokens of all
  * sequences].  Products are summed in 32 bits.  In 16-bit types P is rounded to
  * the type before the second product, as tensor instructions take both
- * operands in one type (bfloat16's dv of calls of some size: in two parts; above
- * 64 columns and 6e8 query rows * keys of a sequence, backward, all its operands in float16, times a power
- * of two for each sequence and key head: nothing lost above 2^-28 of the largest).  32-bit calls of some size (head_size up to 64, see
- * attention.cu) take each operand as two float16 parts, every 128 tokens of a head
- * (from its sequence's first on) times a power of two of their own: 22 bits of what
- * lies above 2^-17 of their largest element, and nothing more than 2^-39 of that
- * off; probabilities are split the same way, 2^14 fold.  Gradients of scores are taken
- * in two parts in every type, in float16 parts times a power of two of their own row (a
- * query's for dq, a key's for dk): off by 2^-22 of themselves and 2^-36 of the row's
- * largest, whatever other rows hold.  An infinite or NaN element inside a sequence may
- * reach results of that sequence that do not depend on it, and no other sequence's.
+ * operands in one type (bfloat16's dv of calls of some size: in two parts).
+ *
+ * Operands of calls of some size (see attention.cu and attention_tiles_backward.cu):
+ * 32-bit calls with head_size up to 64 take each as two float16 parts, every 128 tokens
+ * of a head (from its sequence's first on) times a power of two of their own: 22 bits of
+ * what lies above 2^-17 of their largest element, and nothing more than 2^-39 of that
+ * off; probabilities are split the same way, 2^14 fold.  bfloat16's backward calls with
+ * head_size above 64 and at least 6e8 query rows * keys of a sequence take each in float16,
+ * times a power of two for each sequence and key head: all bits of what lies above 2^-28
+ * of its largest element.  Gradients of scores are taken in two parts (in one where
+ * bfloat16's operands are float16), in float16 times a power of two of their own row (a
+ * query's for dq, a key's for dk): off by 2^-22 (2^-11) of themselves and 2^-36 of the
+ * row's largest, whatever other rows hold.  An infinite or NaN element inside a sequence
+ * may reach results of that sequence that do not depend on it, and no other sequence's.
  * Limits: 1 <= head_size <= 128, heads <= 65536, ragged sides of at most 65536
  * sequences; tokens, and q_tokens * (heads / key_heads), below 2^31 - 4096.
  * Workspaces are 16-byte aligned and hold nothing from one call to the next.

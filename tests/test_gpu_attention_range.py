@@ -418,3 +418,50 @@ def test_a_gradient_that_lies_badly_takes_the_same_path(dtype, form):
     got = sn.snack_attention_backward(dout, q, k, v, out, lse)
     want = sn.snack_attention_backward(dout.contiguous().clone(), q, k, v, out, lse)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype,length,d", [(F32, 700, 64), (F32, 515, 40), (F16, 700, 128), (BF16, 700, 64),
+                                            (BF16, 4200, 128)])
+def test_dense_and_ragged_sides_in_any_mix(dtype, length, d):
+    """The same sequences dense, padded or packed on either side: the same bits (tiles, and the powers
+    of two of their operands, are found by unlike numberings)."""
+    g = gen(27)
+    n, heads, key_heads = 3, 12, 4
+    q, k, v, dout = (rnd(g, (n, length, h, d), dtype) for h in (heads, key_heads, key_heads, heads))
+    q[1] *= 16.0
+    v[2] *= 2.0 ** -10 if dtype != F16 else 0.25
+    ends = (torch.arange(n + 1, device="cuda") * length).to(torch.int32)
+    full = torch.full((n,), length, dtype=torch.int32, device="cuda")
+    opts = dict(dropout=0.1, seed=4)
+    want = run(q, k, v, dout, **opts)
+    flat = lambda t: t.flatten(0, 1)  # noqa: E731
+    for q_form in ("dense", "padded", "ragged"):
+        for k_form in ("dense", "padded", "ragged"):
+            o = dict(opts)
+            x = [flat(t) if form == "ragged" else t for t, form in zip((q, k, v, dout), (q_form, k_form, k_form, q_form))]
+            for side, form in (("q", q_form), ("k", k_form)):
+                if form != "dense":
+                    o[f"{side}_offsets" if form == "ragged" else f"{side}_lengths"] = ends if form == "ragged" else full
+            got = run(*x, **o)
+            for a, b in zip(got, want):
+                assert torch.equal(a.reshape(-1), b.reshape(-1)), (q_form, k_form)
+
+
+@pytest.mark.parametrize("dtype,length,d", [(F32, 700, 64), (F16, 700, 64), (BF16, 700, 128), (BF16, 7300, 128)])
+def test_replays_take_their_powers_from_their_own_inputs(dtype, length, d):
+    """A captured call whose inputs are replaced by ones 2^12 times smaller, and back: each replay's
+    results are those of an eager call on the same inputs (no largest magnitude stays behind)."""
+    g = gen(28)
+    x = [rnd(g, (1, length, h, d), dtype) for h in (12, 4, 4, 12)]
+    room = [t.clone() for t in x]
+    run(*room)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(*room)
+    by = 2.0 ** -12 if dtype != F16 else 2.0 ** -3
+    for scale in (1.0, by, 1.0):
+        for r, t in zip(room, x):
+            r.copy_(t * scale)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, run(*room)))
