@@ -593,9 +593,10 @@ bool worth_tiles(const AttnCall &c, int type, bool backward) {
 // where a sequence has few rows for its key head (tokens * group; the mean on a ragged
 // side), so that most of a block of 128 would be empty.  bf16, 128 rows / 16, us:
 // decoding 128 requests over 500 keys, 24 heads over 8 of 128 (3 rows) 187 / 53; 512 over
-// 1024 1358 / 307; fp32 12 heads of 64 537 / 113; 8 tokens of a group of 3 (24 rows) 167 /
-// 123, of 4 (32) 39 / 45; 16 of 3 (48) 29 / 35.  The keys in parts where the blocks
-// still leave SMs idle.
+// 1024 1358 / 307; 512 over 2048, 32 over 1 (32 rows) 396 / 186; fp32 256 over 4096, 64 over 2
+// (32) 3341 / 1021; 256 x 32 tokens over 512, 12 heads of 64 (32) 259 / 162, but over 32 keys 37 / 44;
+// 256 x 48 over 300 (48) 173 / 179; 16 tokens of a group of 3 over 64 keys (48) 29 / 35.  The
+// keys in parts where the blocks still leave SMs idle.
 Plan plan_forward(const AttnCall &c, int type) {
   Plan p;
   const int64_t sms = device_sms();
@@ -610,7 +611,7 @@ Plan plan_forward(const AttnCall &c, int type) {
   } else {
     const bool ragged = c.q_offsets != nullptr;
     p.few = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 128) * c.key_heads < sms ||
-            (int64_t)c.q_tokens * c.group <= (int64_t)24 * (ragged ? c.sequences : 1);
+            (int64_t)c.q_tokens * c.group <= (int64_t)32 * (ragged ? c.sequences : 1);
     if (!p.few) return p;
     blocks = tiles_of(ragged, c.sequences, c.q_tokens, c.group, 16) * c.key_heads;
     least = 512;

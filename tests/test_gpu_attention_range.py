@@ -225,7 +225,7 @@ def test_many_sequences_of_few_queries(dtype, group, d):
     import attention_ref
     import coo_spmm_sparse_gb300 as sn
     g = gen(group)
-    for n, nq, nk in ((200, 1, 100), (150, 24 // group, 70), (150, 24 // group + 1, 70)):
+    for n, nq, nk in ((200, 1, 100), (150, 32 // group, 70), (150, 32 // group + 1, 70)):
         q, k, v = (rnd(g, (n, t, h, d), dtype) for t, h in ((nq, 2 * group), (nk, 2), (nk, 2)))
         fill = torch.randint(nq, nk + 1, (n,), generator=g, device="cuda").to(torch.int32)
         opts = dict(k_lengths=fill, dropout=0.2, seed=1)
