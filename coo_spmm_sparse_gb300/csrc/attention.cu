@@ -570,10 +570,13 @@ void plan_parts(Plan *p, const AttnCall &c, int type, bool backward) {
 // tiles / mma.sync, us:
 //   forward, bf16: 1 x 128 (X = 2e5) 8 / 7; 1 x 256 (8e5) 10 / 10, 16 over 4 10 / 10; 2 x 256
 //   (1.6e6) 10 / 11; 4 x 256 (3e6) 10 / 17; 1 x 1024 (1.3e7) 18 / 41: from 1e6;
-//   forward, fp32, where the operands are made first: 1 x 256 19 / 15; 2 x 256 19 / 19, 16
-//   over 4 (2.1e6) 19 / 23; 4 x 256 21 / 31; 1 x 1024 37 / 82: from 2e6;
-//   backward: 1 x 128 bf16 17 / 17, float16 18 / 17, fp32 24 / 22; 1 x 256 19 / 23, 19 / 25, 26 /
-//   34; 4 x 128 (8e5) 17 / 29, 19 / 29, 28 / 41; 1 x 1024 28 / 97, 31 / 103, 45 / 236: from 5e5.
+//   backward, bf16 and float16: 1 x 128 17 / 17, 18 / 17; 1 x 256 19 / 23, 19 / 25; 4 x 128
+//   (8e5) 17 / 29, 19 / 29; 1 x 1024 28 / 97, 31 / 103: from 5e5;
+//   fp32, where the operands are made first, forward: 1 x 256 19 / 15; 2 x 256 19 / 19; 4 x 256
+//   21 / 31; 8 x 256 (6e6) 23 / 58; backward 1 x 256 26 / 34; 2 x 256 31 / 51; 4 x 256 33 / 99.  The
+//   float16 parts leave gradients 1.5 times as far from 64 bits as the tf32 parts do
+//   (6.2e-7, 4.2e-7 at 1 x 256), so: where they take less than about half the time, from 4e6
+//   forward and 2e6 backward.
 // Few rows over many keys are too few for the forward tiles even with the keys
 // in parts.  A ragged side's lengths are not known here, only their mean; a tile holds
 // one sequence's tokens.  Forward, bf16, 24 heads over 8 of 128, tiles / without, us:
@@ -585,8 +588,8 @@ bool worth_tiles(const AttnCall &c, int type, bool backward) {
   if (c.q_tokens < 64 || c.k_tokens < 64) return false;
   if (c.q_offsets && !backward && c.q_tokens < (int64_t)16 * c.sequences) return false;
   const double rows = (double)c.rows * c.heads, x = rows * c.k_tokens;
-  if (backward) return x >= 5e5;
-  return x >= (type == SNACK_F32 ? 2e6 : 1e6) && rows >= 1024;
+  if (backward) return x >= (type == SNACK_F32 ? 2e6 : 5e5);
+  return x >= (type == SNACK_F32 ? 4e6 : 1e6) && rows >= 1024;
 }
 
 // Off the tiles, 16 rows to a block where blocks of 128 would leave SMs idle, and
